@@ -292,11 +292,174 @@ attn_status attn_fwd_decode_paged(const void* q, const void* kv_cache,
                                   cudaStream_t stream);
 
 /*
+ * Rotary positions.  A pair (a, b) of a head at position t turns by t * f_i,
+ * f_i the frequency of pair i:
+ *
+ *     (a, b) -> magnitude * (a cos(t f_i) - b sin(t f_i), b cos(t f_i) + a sin(t f_i))
+ *
+ * The first rot_dim elements of a head turn, the others pass through.  Pair i
+ * is (x[i], x[i + rot_dim/2]) (interleaved = 0) or (x[2i], x[2i + 1])
+ * (interleaved = 1).  turns[i] is f_i / (2 pi) modulo 1, the fraction of a
+ * turn a step of one position makes, in units of 2^-64: t * f_i is then exact
+ * modulo whole turns for any 32-bit t, negative ones among them (the rotation
+ * by -t undoes the one by t, and carries a gradient back through it).
+ */
+typedef struct {
+    const unsigned long long* turns; /* device, [rot_dim / 2], 8-byte aligned */
+    int rot_dim;                     /* even, 0 .. D; 0: nothing turns (turns may be NULL) */
+    int interleaved;
+    float magnitude;                 /* 2^-6 .. 64; 1 but for scaled contexts */
+} attn_rotation;
+
+/* Frequencies for contexts longer than the model was trained on: f_i starts as
+ * base^(-2i/rot_dim); `factor` is how much longer the context is. */
+typedef enum {
+    ATTN_ROPE_PLAIN = 0,      /* f_i */
+    ATTN_ROPE_LINEAR = 1,     /* f_i / factor */
+    ATTN_ROPE_BASE = 2,       /* base * factor^(rot_dim / (rot_dim - 2)) in base's place */
+    ATTN_ROPE_WAVELENGTH = 3, /* a pair that makes r = original_length * f_i / (2 pi) turns over the
+                                 trained context keeps f_i from r >= high on, has f_i / factor up to
+                                 r <= low, and in between their mean weighted linearly in r */
+    ATTN_ROPE_YARN = 4        /* the same two ends, weighted linearly in the pair's index between
+                                 floor(i(high)) and ceil(i(low)), i(r) = rot_dim ln(original_length /
+                                 (2 pi r)) / (2 ln base), both clamped to 0 .. rot_dim - 1;
+                                 magnitude 0.1 ln(factor) + 1 (1 for factor <= 1) */
+} attn_rope_scaling;
+
+/*
+ * attn_rope_turns -- fills turns[rot_dim / 2] (HOST memory) and *magnitude for
+ * an attn_rotation, in double precision.  rot_dim even and >= 2, base > 1,
+ * factor > 0; original_length, low, high (0 < low < high) are read by the last
+ * two scalings only; ATTN_ROPE_BASE needs rot_dim > 2.  Needs no GPU.
+ */
+attn_status attn_rope_turns(unsigned long long* turns, float* magnitude, int rot_dim,
+                            double base, attn_rope_scaling scaling, double factor,
+                            double original_length, double low, double high);
+
+/*
+ * Rows of D contiguous elements, one for each (batch, head, token), at
+ * x + batch * x_batch + head * x_head + token * x_token, and results at y
+ * likewise (strides in elements, >= 0): any slice of a fused projection, in
+ * any order of its dimensions.  x and y are 16-byte aligned and every stride is
+ * a multiple of 16 bytes.  y == x with equal strides works in place; otherwise
+ * the two may not share memory, and no two rows of y may.  Nothing else that a
+ * call reads or writes may overlap y.
+ */
+typedef struct {
+    const void* x;
+    void* y;
+    int heads;
+    long long x_batch, x_head, x_token;
+    long long y_batch, y_head, y_token;
+} attn_rows;
+
+/*
+ * attn_rope -- rotary positions of the query heads (and, k not NULL, of the key
+ * heads) of B x T tokens in one launch.  positions: [B, T] int32, device.  D 64
+ * or 128; x and y in dtype (ATTN_F32, ATTN_BF16 or ATTN_F16), the arithmetic in
+ * fp32, one rounding at the end.  B * T = 0 launches nothing.
+ */
+attn_status attn_rope(const attn_rows* q, const attn_rows* k, const int* positions, int B,
+                      int T, int D, const attn_rotation* rotation, attn_dtype dtype,
+                      cudaStream_t stream);
+
+/*
+ * attn_qk_norm_rope -- every head of q and k normalised, then rotated, in one
+ * pass:  y = rotation(x / sqrt(mean(x^2) + eps) * weight), the mean over the
+ * head's D elements.  q_weight, k_weight: [D] in dtype, 16-byte aligned, or
+ * NULL for all ones.  eps >= 0.  The sum of squares is fp32 (|x| up to about
+ * 1e18); one rounding at the end.  k may be NULL.  Otherwise as attn_rope.
+ */
+attn_status attn_qk_norm_rope(const attn_rows* q, const attn_rows* k, const void* q_weight,
+                              const void* k_weight, float eps, const int* positions, int B,
+                              int T, int D, const attn_rotation* rotation, attn_dtype dtype,
+                              cudaStream_t stream);
+
+/*
+ * attn_append_paged -- the new tokens of B requests into the paged cache of
+ * attn_fwd_decode_paged, keys rotated on the way.
+ *   q, k, v:     rows of `total` packed tokens (the head and token strides of
+ *                attn_rows; batch strides are not used).  Request b's new tokens
+ *                are cu_seqlens[b] .. cu_seqlens[b+1]-1.  k and v have the
+ *                cache's Hkv heads.  q may be NULL; otherwise its heads are
+ *                rotated into q->y in the same launch.  k->y may be NULL;
+ *                otherwise the rotated keys are written there too (for the
+ *                attention over the prompt).  v->y must be NULL.
+ *   cu_seqlens:  [B + 1] int32, device.
+ *   seq_lens:    [B] int32, device: the keys of each request, its new ones among
+ *                them (what attn_fwd_decode_paged takes afterwards).  With n new
+ *                tokens, they go to slots seq_lens[b] - n .. seq_lens[b] - 1.
+ *   positions:   [total] int32, device, or NULL: a token's position is its slot.
+ *   block_table: [B, max_pages_per_seq] int32, device, as in
+ *                attn_fwd_decode_paged.  The blocks that the call writes belong
+ *                to one request each.
+ *   kv_cache:    [num_blocks, 2, Hkv, page_size, D]; other slots stay as they are.
+ *   rotation:    NULL: keys (and queries) are copied.
+ *   dtype:       ATTN_BF16 or ATTN_F16, of q, k, v and the cache.
+ * Tokens outside every request (cu_seqlens[B] < total) are left out, their rows
+ * of y unwritten.  Device-side checks: a request whose offsets decrease or leave
+ * 0 .. total, or whose length is under its new tokens or over the table's, is
+ * left out, and so is a page whose block id is outside the pool; both are
+ * reported by attn_get_device_status as ATTN_ERR_BAD_INPUT.  No workspace.
+ */
+attn_status attn_append_paged(const attn_rows* q, const attn_rows* k, const attn_rows* v,
+                              const int* cu_seqlens, const int* seq_lens,
+                              const int* positions, const int* block_table, void* kv_cache,
+                              int B, int total, int D, int page_size, int max_pages_per_seq,
+                              int num_blocks, const attn_rotation* rotation,
+                              attn_dtype dtype, cudaStream_t stream);
+
+/*
+ * attn_append_paged_e4m3 -- attn_append_paged into an 8-bit cache: kv_cache
+ * [num_blocks, 2, Hkv, page_size, D] of e4m3 codes (4 exponent, 3 mantissa
+ * bits, largest value 448) and scales [num_blocks, 2, Hkv] float32, one for each
+ * block, K or V, and head; a code stands for code * scale.
+ *   The scale of a block that gets its first rows is the smallest power of two
+ *   s >= 2^-100 with b * max|x| <= 448 s over the finite elements of the rows
+ *   before their rotation; b = sqrt(2) * magnitude for keys of a call with
+ *   rot_dim > 0 (no rotation raises an element more), else 1.  A block that
+ *   holds rows of its request already (from earlier slots) keeps the larger of
+ *   that and its present scale; if the scale grows, the older rows are divided
+ *   by the ratio and rounded again (exact but for values under 2^-6 * scale).
+ *   The present scales must be positive and finite.
+ *   Elements are rounded once, from fp32, to the nearest code (ties to even);
+ *   infinities become +-448, NaN stays NaN.
+ * q, k, v, q->y and k->y are in dtype (ATTN_BF16 or ATTN_F16).
+ */
+attn_status attn_append_paged_e4m3(const attn_rows* q, const attn_rows* k, const attn_rows* v,
+                                   const int* cu_seqlens, const int* seq_lens,
+                                   const int* positions, const int* block_table,
+                                   void* kv_cache, float* scales, int B, int total, int D,
+                                   int page_size, int max_pages_per_seq, int num_blocks,
+                                   const attn_rotation* rotation, attn_dtype dtype,
+                                   cudaStream_t stream);
+
+/*
+ * attn_fwd_decode_paged_e4m3 -- attn_fwd_decode_paged over the 8-bit cache of
+ * attn_append_paged_e4m3:
+ *
+ *     O = sum_j p_j vs_j v_j / sum_j p_j,   p_j = exp(scale * ks_j q . k_j),
+ *
+ * k_j, v_j the codes of key j and ks_j, vs_j the scales of its block (any finite
+ * values >= 0).  q and o are [B, Hq, 1, D] in dtype (ATTN_BF16 or ATTN_F16), lse
+ * [B, Hq] float32 or NULL.  The products run on the tensor cores in fp16 with
+ * fp32 sums: codes are exact in fp16; a query head is multiplied by a power of
+ * two that keeps it in range; a key's weight p_j vs_j is rounded to fp16
+ * relative to the largest one so far.  Any group Hq / Hkv.  The other arguments,
+ * checks, errors and the workspace are those of attn_fwd_decode_paged.
+ */
+attn_status attn_fwd_decode_paged_e4m3(const void* q, const void* kv_cache, const float* scales,
+                                       const int* block_table, const int* seq_lens, void* o,
+                                       float* lse, int B, int Hq, int Hkv, int D, int page_size,
+                                       int max_pages_per_seq, int num_blocks, float scale,
+                                       attn_dtype dtype, cudaStream_t stream);
+
+/*
  * attn_get_device_status -- synchronise `stream`, then read and clear the
  * device status word of the current device.  Returns ATTN_ERR_TIMEOUT when a
  * kernel gave up on a pipeline wait since the last call (its outputs are
  * then undefined), ATTN_ERR_BAD_INPUT when a kernel met a device-side index
- * outside its declared range (attn_fwd_decode_paged), ATTN_ERR_CUDA when
+ * outside its declared range (the packed and paged calls), ATTN_ERR_CUDA when
  * synchronising failed, else ATTN_OK.
  */
 attn_status attn_get_device_status(cudaStream_t stream);

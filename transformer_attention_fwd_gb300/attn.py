@@ -42,12 +42,25 @@ class AttnError(RuntimeError):
         self.status = status
 
 
+class _Rows(ctypes.Structure):
+    """attn_rows."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int)] + [
+        (n, ctypes.c_longlong) for n in ("x_batch", "x_head", "x_token", "y_batch", "y_head", "y_token")]
+
+
+class _Rotation(ctypes.Structure):
+    """attn_rotation."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("magnitude", ctypes.c_float)]
+
+
 def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise RuntimeError(
             f"{path} is missing: build it with transformer_attention_fwd_gb300.build.build()")
     lib = ctypes.CDLL(path)
     P, I, F, LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
+    DB, R, N = ctypes.c_double, ctypes.POINTER(_Rows), ctypes.POINTER(_Rotation)
     sig = {
         "attn_fwd": [P, P, P, P, P, I, I, I, I, I, I, I, F, I, P],
         "attn_fwd_prefill": [P, P, P, P, P, I, I, I, I, I, I, I, F, P],
@@ -56,6 +69,12 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "attn_fwd_window": [P, P, P, P, P, I, I, I, I, I, I, I, F, I, P],
         "attn_fwd_host": [P, P, P, P, P, I, I, I, I, I, I, I, F, I, P],
         "attn_fwd_varlen": [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P],
+        "attn_rope_turns": [P, P, I, DB, I, DB, DB, DB, DB],
+        "attn_rope": [R, R, P, I, I, I, N, I, P],
+        "attn_qk_norm_rope": [R, R, P, P, F, P, I, I, I, N, I, P],
+        "attn_append_paged": [R, R, R, P, P, P, P, P, I, I, I, I, I, I, N, I, P],
+        "attn_append_paged_e4m3": [R, R, R, P, P, P, P, P, P, I, I, I, I, I, I, N, I, P],
+        "attn_fwd_decode_paged_e4m3": [P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P],
         "attn_get_device_status": [P],
         "attn_diag_mma_tile": [P, P, P, P, P, I, P],
         "attn_diag_wait_timeout": [LL, P],
@@ -335,6 +354,268 @@ def attn_fwd_decode_paged(q, kv_cache, block_table, seq_lens, scale: float | Non
                                      block_table.shape[1], nblk, scale,
                                      ATTN_F16 if q.dtype == torch.float16 else ATTN_BF16,
                                      _stream_handle(stream)))
+    return o, lse
+
+
+_DTYPES = {torch.float32: ATTN_F32, torch.bfloat16: ATTN_BF16, torch.float16: ATTN_F16}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "wavelength": 3, "yarn": 4}
+
+
+class Rotation:
+    """A rotation of head elements by position (``attn_rotation``): ``turns``
+    [rot_dim / 2] int64, a CUDA tensor of each pair's fraction of a turn per
+    position in units of 2^-64 turn (kept alive by this object); pairs are
+    (i, i + rot_dim/2), or (2i, 2i + 1) with ``interleaved``."""
+
+    def __init__(self, turns, interleaved: bool = False, magnitude: float = 1.0):
+        if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+            raise ValueError("turns must be a contiguous int64 tensor [rot_dim / 2]")
+        if not turns.is_cuda:
+            raise ValueError("turns must be a CUDA tensor")
+        self.turns, self.interleaved, self.magnitude = turns, bool(interleaved), float(magnitude)
+        self.device_index = turns.get_device()
+        self._struct = _Rotation(turns.data_ptr(), 2 * turns.shape[0], int(self.interleaved), self.magnitude)
+
+    @classmethod
+    def make(cls, rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+             original_length: float = 0.0, low: float = 1.0, high: float | None = None,
+             interleaved: bool = False, device="cuda"):
+        """The table of ``rope_turns`` on ``device``."""
+        turns, magnitude = rope_turns(rot_dim, base, scaling, factor, original_length, low, high)
+        return cls(turns.to(device), interleaved, magnitude)
+
+
+def rope_turns(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               original_length: float = 0.0, low: float = 1.0, high: float | None = None):
+    """Frequencies base^(-2i/rot_dim), scaled for a ``factor`` times longer
+    context (``attn_rope_turns``): "linear", "base", "wavelength" (``high``
+    defaults to 4) or "yarn" (32).  Returns ``(turns, magnitude)``: a CPU int64
+    tensor in units of 2^-64 turn per position, and the factor of cos and sin."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"unknown scaling {scaling!r} (one of {', '.join(ROPE_SCALINGS)})")
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
+    turns = torch.empty(max(0, rot_dim // 2), dtype=torch.int64)
+    magnitude = ctypes.c_float()
+    _check(lib.attn_rope_turns(_ptr(turns), ctypes.addressof(magnitude), rot_dim, base,
+                               ROPE_SCALINGS[scaling], factor, original_length, low, high))
+    return turns, magnitude.value
+
+
+def _heads(name, t, like, device, packed_only=False):
+    """A tensor of rows: [T, H, D], or [B, H, T, D], D innermost and contiguous."""
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
+    if t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype} (got {t.dtype})")
+    if t.dim() != like.dim() or (packed_only and t.dim() != 3) or t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [T, H, D]" + ("" if packed_only else " or [B, H, T, D]"))
+    if t.shape[-1] != like.shape[-1] or t.shape[0] != like.shape[0] or (
+            t.dim() == 4 and t.shape[2] != like.shape[2]):
+        raise ValueError(f"{name} must have the same tokens and head dim as the others")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+
+
+def _rows(x, y):
+    """attn_rows from x to y (None: no output)."""
+    xs = x.stride()
+    if x.dim() == 3:
+        n, xb, xh, xt = x.shape[1], 0, xs[1], xs[0]
+        if y is None:
+            return _Rows(x.data_ptr(), None, n, xb, xh, xt, 0, 0, 0)
+        ys = y.stride()
+        return _Rows(x.data_ptr(), y.data_ptr(), n, xb, xh, xt, 0, ys[1], ys[0])
+    ys = y.stride()
+    return _Rows(x.data_ptr(), y.data_ptr(), x.shape[1], xs[0], xs[1], xs[2], ys[0], ys[1], ys[2])
+
+
+def _rows_out(name, x, out):
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.shape != x.shape or out.dtype != x.dtype or out.get_device() != x.get_device():
+        raise ValueError(f"{name} must be {tuple(x.shape)} {x.dtype} on {x.device}")
+    if out.stride(-1) != 1 and x.shape[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return out
+
+
+def _current(device: int):
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{device} but the current device is "
+                         f"cuda:{torch.cuda.current_device()}; call under torch.cuda.device({device})")
+
+
+def _ints(name, t, shape, device):
+    """An int32 device tensor of exactly this shape."""
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} (got {tuple(t.shape)} {t.dtype})")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
+
+
+def _rope_call(q, k, positions, rotation, out_q, out_k):
+    device = q.get_device()
+    dt = _DTYPES.get(q.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    _heads("q", q, q, device)
+    if k is not None:
+        _heads("k", k, q, device)
+    elif out_k is not None:
+        raise ValueError("out_k without k")
+    B, T = (1, q.shape[0]) if q.dim() == 3 else (q.shape[0], q.shape[2])
+    _ints("positions", positions, (T,) if q.dim() == 3 else (B, T), device)
+    if rotation.device_index != device:
+        raise ValueError("the rotation's table must be on the device of the tensors")
+    _current(device)
+    yq = _rows_out("out_q", q, out_q)
+    yk = None if k is None else _rows_out("out_k", k, out_k)
+    return B, T, dt, yq, yk
+
+
+def attn_rope(q, k, positions, rotation: Rotation, out_q=None, out_k=None, stream=None):
+    """Rotary positions of query and key heads (``attn_rope``).
+
+    q: [T, Hq, D] with positions [T], or [B, Hq, T, D] with positions [B, T]
+    (int32); k: the same with Hkv heads, or None; fp32, bf16 or fp16 CUDA
+    tensors of any strides whose rows are contiguous and 16-byte aligned.
+    Returns ``(out_q, out_k)``; ``out_q=q`` works in place.  The gradient of
+    the inputs is this call on the outputs' gradients with -positions.
+    """
+    B, T, dt, yq, yk = _rope_call(q, k, positions, rotation, out_q, out_k)
+    _check(lib.attn_rope(_rows(q, yq), None if k is None else _rows(k, yk), positions.data_ptr(), B, T,
+                         q.shape[-1], rotation._struct, dt, _stream_handle(stream)))
+    return yq, yk
+
+
+def attn_qk_norm_rope(q, k, q_weight, k_weight, positions, rotation: Rotation, eps: float = 1e-6,
+                      out_q=None, out_k=None, stream=None):
+    """``attn_rope`` of x / sqrt(mean(x^2) + eps) * weight for every head x of q
+    and k (``attn_qk_norm_rope``); weights [D] in q's dtype, or None for ones."""
+    B, T, dt, yq, yk = _rope_call(q, k, positions, rotation, out_q, out_k)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and (w.shape != q.shape[-1:] or w.dtype != q.dtype or not w.is_contiguous()
+                              or w.get_device() != q.get_device()):
+            raise ValueError(f"{name} must be a contiguous {q.dtype} tensor [{q.shape[-1]}] on {q.device}")
+    _check(lib.attn_qk_norm_rope(_rows(q, yq), None if k is None else _rows(k, yk), _ptr(q_weight),
+                                 _ptr(k_weight), eps, positions.data_ptr(), B, T, q.shape[-1],
+                                 rotation._struct, dt, _stream_handle(stream)))
+    return yq, yk
+
+
+def _append(name, k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens, rotation, positions, q,
+            out_q, out_k, stream):
+    device = k.get_device()
+    dt = _DTYPES.get(k.dtype)
+    if dt is None or dt == ATTN_F32:
+        raise ValueError(f"{name} takes bf16 or fp16 tensors")
+    _heads("k", k, k, device, packed_only=True)
+    _heads("v", v, k, device, packed_only=True)
+    if q is not None:
+        _heads("q", q, k, device, packed_only=True)
+    elif out_q is not None:
+        raise ValueError("out_q without q")
+    total, Hkv, D = k.shape
+    if v.shape[1] != Hkv:
+        raise ValueError("k and v must have the same heads")
+    want = k.dtype if scales is None else torch.float8_e4m3fn
+    if (kv_cache.dim() != 5 or kv_cache.dtype != want or not kv_cache.is_contiguous()
+            or kv_cache.get_device() != device):
+        raise ValueError(f"kv_cache must be a contiguous {want} tensor [num_blocks, 2, Hkv, page_size, D] on {k.device}")
+    blocks, two, heads, page, Dc = kv_cache.shape
+    if two != 2 or heads != Hkv or Dc != D:
+        raise ValueError("kv_cache must be [num_blocks, 2, Hkv, page_size, D] with k's Hkv and D")
+    if scales is not None and (scales.dtype != torch.float32 or scales.shape != (blocks, 2, Hkv)
+                               or not scales.is_contiguous() or scales.get_device() != device):
+        raise ValueError("scales must be a contiguous float32 tensor [num_blocks, 2, Hkv]")
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    _ints("seq_lens", seq_lens, (B,), device)
+    _ints("cu_seqlens", cu_seqlens, (B + 1,), device)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    _ints("block_table", block_table, (B, block_table.shape[1]), device)
+    if positions is not None:
+        _ints("positions", positions, (total,), device)
+    if rotation is not None and rotation.device_index != device:
+        raise ValueError("the rotation's table must be on the device of the tensors")
+    _current(device)
+    if q is not None:
+        out_q = _rows_out("out_q", q, out_q)
+    if out_k is not None:
+        out_k = _rows_out("out_k", k, out_k)
+    args = [None if q is None else _rows(q, out_q), _rows(k, out_k), _rows(v, None), cu_seqlens.data_ptr(),
+            seq_lens.data_ptr(), _ptr(positions), block_table.data_ptr(), kv_cache.data_ptr()]
+    if scales is not None:
+        args.append(scales.data_ptr())
+    _check(getattr(lib, name)(*args, B, total, D, page, block_table.shape[1], blocks,
+                              None if rotation is None else rotation._struct, dt, _stream_handle(stream)))
+    return out_q, out_k
+
+
+def attn_append_paged(k, v, kv_cache, block_table, cu_seqlens, seq_lens, rotation: Rotation | None = None,
+                      positions=None, q=None, out_q=None, out_k=None, stream=None):
+    """New tokens of B requests into the paged cache (``attn_append_paged``).
+
+    k, v: [total, Hkv, D] packed tokens (bf16 or fp16, any strides whose rows
+    are contiguous and 16-byte aligned), request b's at cu_seqlens[b] ..
+    cu_seqlens[b+1]-1; they go to the last slots of its seq_lens[b] (the new
+    tokens counted in).  With ``rotation`` keys are rotated by ``positions``
+    [total] (default: their slots), and so are q's heads [total, Hq, D] if
+    given.  Returns ``(out_q, out_k)``: the rotated q (None without q), and
+    ``out_k`` as passed, filled with the rotated keys (None if not passed).
+    """
+    return _append("attn_append_paged", k, v, kv_cache, None, block_table, cu_seqlens, seq_lens, rotation,
+                   positions, q, out_q, out_k, stream)
+
+
+def attn_append_paged_e4m3(k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens,
+                           rotation: Rotation | None = None, positions=None, q=None, out_q=None, out_k=None,
+                           stream=None):
+    """``attn_append_paged`` into an 8-bit cache (``attn_append_paged_e4m3``):
+    kv_cache float8_e4m3fn, scales float32 [num_blocks, 2, Hkv]; a code stands
+    for code * scale of its block, K or V, and head."""
+    return _append("attn_append_paged_e4m3", k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens,
+                   rotation, positions, q, out_q, out_k, stream)
+
+
+def attn_fwd_decode_paged_e4m3(q, kv_cache, scales, block_table, seq_lens, scale: float | None = None,
+                               out=None, lse=None, want_lse: bool = True, stream=None):
+    """Decode against the paged 8-bit cache (``attn_fwd_decode_paged_e4m3``).
+
+    q: [B, Hq, 1, D] bf16 or fp16; kv_cache: [num_blocks, 2, Hkv, page_size, D]
+    float8_e4m3fn; scales: [num_blocks, 2, Hkv] float32; block_table: [B,
+    max_pages] and seq_lens: [B] int32; all contiguous CUDA tensors.  Returns
+    ``(o [B, Hq, 1, D], lse [B, Hq] or None)``.
+    """
+    device = q.get_device()
+    if device < 0 or q.dim() != 4 or q.shape[2] != 1 or not q.is_contiguous() or q.dtype not in (
+            torch.bfloat16, torch.float16):
+        raise ValueError("q must be a contiguous bf16 or fp16 CUDA tensor [B, Hq, 1, D]")
+    B, Hq, _, D = q.shape
+    if (kv_cache.dim() != 5 or kv_cache.dtype != torch.float8_e4m3fn or not kv_cache.is_contiguous()
+            or kv_cache.shape[1] != 2 or kv_cache.shape[4] != D or kv_cache.get_device() != device):
+        raise ValueError("kv_cache must be a contiguous float8_e4m3fn tensor [num_blocks, 2, Hkv, page_size, D]")
+    blocks, _, Hkv, page, _ = kv_cache.shape
+    if (scales.dtype != torch.float32 or scales.shape != (blocks, 2, Hkv) or not scales.is_contiguous()
+            or scales.get_device() != device):
+        raise ValueError("scales must be a contiguous float32 tensor [num_blocks, 2, Hkv]")
+    _ints("seq_lens", seq_lens, (B,), device)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    _ints("block_table", block_table, (B, block_table.shape[1]), device)
+    _current(device)
+    _check_buffer("out", out, q.shape, q.dtype, q.device)
+    _check_buffer("lse", lse, (B, Hq), torch.float32, q.device)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    o = torch.empty_like(q) if out is None else out
+    if lse is None and want_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    _check(lib.attn_fwd_decode_paged_e4m3(q.data_ptr(), kv_cache.data_ptr(), scales.data_ptr(),
+                                          block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+                                          _ptr(lse), B, Hq, Hkv, D, page, block_table.shape[1], blocks, scale,
+                                          ATTN_F16 if q.dtype == torch.float16 else ATTN_BF16,
+                                          _stream_handle(stream)))
     return o, lse
 
 

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdint>
@@ -11,6 +12,7 @@
 #include <cstring>
 #include <mutex>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "../../include/attn.h"
@@ -119,6 +121,34 @@ attn_status validate(const void* q, const void* k, const void* v, const void* o,
         return fail(ATTN_ERR_INVALID_ARG, "B*Hq and B*Hkv must fit in 31 bits");
     if (Tq > 0x7fffffffLL - 1024 || Tk > 0x7fffffffLL - 1024)
         return fail(ATTN_ERR_INVALID_ARG, "Tq and Tk must be below 2^31 - 1024");
+    return ATTN_OK;
+}
+
+// Arguments of a decode over a paged cache (16-bit I/O).
+attn_status validate_paged(const void* q, const void* kv_cache, const int* block_table, const int* seq_lens,
+                           const void* o, const float* lse, int B, int Hq, int Hkv, int D, int page_size,
+                           int max_pages_per_seq, int num_blocks, float scale, attn_dtype dtype) {
+    if (dtype != ATTN_BF16 && dtype != ATTN_F16)
+        return fail(ATTN_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
+    if (!q || !kv_cache || !block_table || !seq_lens || !o)
+        return fail(ATTN_ERR_INVALID_ARG, "q, kv_cache, block_table, seq_lens and o must be non-null");
+    if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(o, 16))
+        return fail(ATTN_ERR_INVALID_ARG, "q, kv_cache and o must be 16-byte aligned");
+    if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || (lse && !aligned(lse, 4)))
+        return fail(ATTN_ERR_INVALID_ARG, "block_table, seq_lens and lse must be 4-byte aligned");
+    if (B < 1 || Hq < 1 || Hkv < 1 || D < 1 || page_size < 1 || max_pages_per_seq < 1 ||
+        num_blocks < 1)
+        return fail(ATTN_ERR_INVALID_ARG,
+                    "B, Hq, Hkv, D, page_size, max_pages_per_seq and num_blocks must be >= 1");
+    if (D != 64 && D != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim D=%d not supported (64 or 128)", D);
+    if (Hq % Hkv != 0) return fail(ATTN_ERR_INVALID_ARG, "Hq=%d is not a multiple of Hkv=%d", Hq, Hkv);
+    if (!std::isfinite(scale) || !(scale > 0.0f))
+        return fail(ATTN_ERR_INVALID_ARG, "scale must be finite and positive (got %g)", (double)scale);
+    if (static_cast<long long>(B) * Hq > 0x7fffffffLL ||
+        static_cast<long long>(B) * max_pages_per_seq > 0x7fffffffLL)
+        return fail(ATTN_ERR_INVALID_ARG, "B*Hq and B*max_pages_per_seq must fit in 31 bits");
+    if (static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 1024)
+        return fail(ATTN_ERR_INVALID_ARG, "max_pages_per_seq*page_size must be below 2^31 - 1024");
     return ATTN_OK;
 }
 
@@ -713,29 +743,11 @@ attn_status attn_fwd_decode_paged(const void* q, const void* kv_cache, const int
                                   float scale, attn_dtype dtype, cudaStream_t stream) {
     if (dtype == ATTN_F32)
         return fail(ATTN_ERR_UNSUPPORTED, "the paged decode is implemented for 16-bit I/O only");
-    if (dtype != ATTN_BF16 && dtype != ATTN_F16)
-        return fail(ATTN_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
-    if (!q || !kv_cache || !block_table || !seq_lens || !o)
-        return fail(ATTN_ERR_INVALID_ARG, "q, kv_cache, block_table, seq_lens and o must be non-null");
-    if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(o, 16))
-        return fail(ATTN_ERR_INVALID_ARG, "q, kv_cache and o must be 16-byte aligned");
-    if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || (lse && !aligned(lse, 4)))
-        return fail(ATTN_ERR_INVALID_ARG, "block_table, seq_lens and lse must be 4-byte aligned");
-    if (B < 1 || Hq < 1 || Hkv < 1 || D < 1 || page_size < 1 || max_pages_per_seq < 1 ||
-        num_blocks < 1)
-        return fail(ATTN_ERR_INVALID_ARG,
-                    "B, Hq, Hkv, D, page_size, max_pages_per_seq and num_blocks must be >= 1");
-    if (D != 64 && D != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim D=%d not supported (64 or 128)", D);
-    if (Hq % Hkv != 0) return fail(ATTN_ERR_INVALID_ARG, "Hq=%d is not a multiple of Hkv=%d", Hq, Hkv);
-    if (!std::isfinite(scale) || !(scale > 0.0f))
-        return fail(ATTN_ERR_INVALID_ARG, "scale must be finite and positive (got %g)", (double)scale);
-    if (static_cast<long long>(B) * Hq > 0x7fffffffLL ||
-        static_cast<long long>(B) * max_pages_per_seq > 0x7fffffffLL)
-        return fail(ATTN_ERR_INVALID_ARG, "B*Hq and B*max_pages_per_seq must fit in 31 bits");
-    if (static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 1024)
-        return fail(ATTN_ERR_INVALID_ARG, "max_pages_per_seq*page_size must be below 2^31 - 1024");
+    attn_status st = validate_paged(q, kv_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, D, page_size,
+                                    max_pages_per_seq, num_blocks, scale, dtype);
+    if (st != ATTN_OK) return st;
     LaunchEnv env;
-    attn_status st = device_env(stream, &env);
+    st = device_env(stream, &env);
     if (st != ATTN_OK) return st;
     PagedShape s{B, Hq, Hkv, D, page_size, max_pages_per_seq, num_blocks, scale};
     s.f16 = dtype == ATTN_F16 ? 1 : 0;
@@ -943,3 +955,295 @@ extern "C" attn_status attn_fwd_decode_noalloc(const void* q, const void* k, con
     record_launch(B * Hkv, splits, kernels);
     return ok();
 }
+
+// ---------------------------------------------------------------------------
+// Rotary positions, the paged appends and the decode over the 8-bit cache.
+// ---------------------------------------------------------------------------
+namespace attn {
+namespace {
+
+int dtype_bytes(attn_dtype t) { return t == ATTN_F32 ? 4 : 2; }
+
+attn_status validate_rotation(const attn_rotation* r, int D) {
+    if (r->rot_dim < 0 || r->rot_dim > D || r->rot_dim % 2 != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "rot_dim must be even and in 0..D (got %d, D=%d)", r->rot_dim, D);
+    if (r->rot_dim > 0 && (!r->turns || !aligned(r->turns, 8)))
+        return fail(ATTN_ERR_INVALID_ARG, "turns must be a non-null, 8-byte aligned device pointer");
+    if (!(r->magnitude >= 0.015625f && r->magnitude <= 64.0f))
+        return fail(ATTN_ERR_INVALID_ARG, "magnitude must be in 2^-6..64 (got %g)", (double)r->magnitude);
+    return ATTN_OK;
+}
+
+// Elements from the first to the last of rows at the given strides, D included;
+// -1 if that overflows.
+long long rows_span(const long long (&stride)[3], const long long (&extent)[3], int D) {
+    __int128 n = D;
+    for (int i = 0; i < 3; ++i) n += static_cast<__int128>(stride[i]) * (extent[i] - 1);
+    return n > (static_cast<__int128>(1) << 61) ? -1 : static_cast<long long>(n);
+}
+
+// One tensor of rows: [B, heads, T] of D elements.  want_y: 1 needed, 0
+// optional, -1 must be null.
+attn_status validate_rows(const char* name, const attn_rows* r, long long B, long long T, int D, int bytes,
+                          int want_y) {
+    if (r->heads < 1) return fail(ATTN_ERR_INVALID_ARG, "%s: heads must be >= 1 (got %d)", name, r->heads);
+    if (!r->x || (want_y > 0 && !r->y)) return fail(ATTN_ERR_INVALID_ARG, "%s: x and y must be non-null", name);
+    if (want_y < 0 && r->y) return fail(ATTN_ERR_INVALID_ARG, "%s: y must be null", name);
+    const long long extent[3] = {B, r->heads, T};
+    const long long xs[3] = {r->x_batch, r->x_head, r->x_token}, ys[3] = {r->y_batch, r->y_head, r->y_token};
+    const bool has_y = r->y != nullptr;
+    const int unit = 16 / bytes;
+    for (int i = 0; i < 3; ++i) {
+        if (extent[i] < 2) continue;
+        if (xs[i] < 0 || xs[i] % unit != 0 || (has_y && (ys[i] < 0 || ys[i] % unit != 0)))
+            return fail(ATTN_ERR_INVALID_ARG, "%s: strides must be >= 0 and multiples of 16 bytes", name);
+    }
+    if (!aligned(r->x, 16) || !aligned(r->y, 16))
+        return fail(ATTN_ERR_INVALID_ARG, "%s: x and y must be 16-byte aligned", name);
+    // Strides of dimensions with one entry are not used.
+    long long sx[3], sy[3];
+    for (int i = 0; i < 3; ++i) {
+        sx[i] = extent[i] < 2 ? 0 : xs[i];
+        sy[i] = extent[i] < 2 ? 0 : ys[i];
+    }
+    const long long span_x = rows_span(sx, extent, D), span_y = has_y ? rows_span(sy, extent, D) : D;
+    if (span_x < 0 || span_y < 0) return fail(ATTN_ERR_INVALID_ARG, "%s: strides too large", name);
+    if (!has_y) return ATTN_OK;
+    // No two rows of y may meet: from the smallest stride on, each dimension
+    // steps over all that the ones before it cover.
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (sy[order[j]] < sy[order[i]]) std::swap(order[i], order[j]);
+    long long covered = D;
+    for (int i = 0; i < 3; ++i) {
+        const int d = order[i];
+        if (extent[d] < 2) continue;
+        if (sy[d] < covered) return fail(ATTN_ERR_INVALID_ARG, "%s: rows of y overlap", name);
+        covered += sy[d] * (extent[d] - 1);
+    }
+    const bool in_place = r->x == r->y && sx[0] == sy[0] && sx[1] == sy[1] && sx[2] == sy[2];
+    if (!in_place) {
+        const uintptr_t x0 = reinterpret_cast<uintptr_t>(r->x), y0 = reinterpret_cast<uintptr_t>(r->y);
+        if (x0 < y0 + static_cast<uintptr_t>(span_y) * bytes && y0 < x0 + static_cast<uintptr_t>(span_x) * bytes)
+            return fail(ATTN_ERR_INVALID_ARG, "%s: x and y share memory without being the same rows", name);
+    }
+    return ATTN_OK;
+}
+
+// The rows as the kernels read them: strides of one-entry dimensions are 0.
+attn_rows plain_rows(const attn_rows& r, long long B, long long T) {
+    attn_rows o = r;
+    if (B < 2) o.x_batch = o.y_batch = 0;
+    if (r.heads < 2) o.x_head = o.y_head = 0;
+    if (T < 2) o.x_token = o.y_token = 0;
+    return o;
+}
+
+attn_status run_rope(const attn_rows* q, const attn_rows* k, const void* qw, const void* kw, bool norm, float eps,
+                     const int* positions, int B, int T, int D, const attn_rotation* rotation, attn_dtype dtype,
+                     cudaStream_t stream) {
+    if (dtype != ATTN_F32 && dtype != ATTN_BF16 && dtype != ATTN_F16)
+        return fail(ATTN_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
+    if (!q || !rotation) return fail(ATTN_ERR_INVALID_ARG, "q and rotation must be non-null");
+    if (B < 0 || T < 0) return fail(ATTN_ERR_INVALID_ARG, "B and T must be >= 0 (got %d, %d)", B, T);
+    if (D != 64 && D != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim D=%d not supported (64 or 128)", D);
+    attn_status st = validate_rotation(rotation, D);
+    if (st != ATTN_OK) return st;
+    if (norm && !(std::isfinite(eps) && eps >= 0.0f))
+        return fail(ATTN_ERR_INVALID_ARG, "eps must be finite and >= 0 (got %g)", (double)eps);
+    if (!aligned(qw, 16) || !aligned(kw, 16))
+        return fail(ATTN_ERR_INVALID_ARG, "q_weight and k_weight must be 16-byte aligned");
+    const long long tokens = static_cast<long long>(B) * T;
+    if (tokens == 0) {
+        record_launch(0, 0, 0);
+        return ok();
+    }
+    if (!positions || !aligned(positions, 4))
+        return fail(ATTN_ERR_INVALID_ARG, "positions must be a non-null, 4-byte aligned device pointer");
+    const int bytes = dtype_bytes(dtype);
+    if ((st = validate_rows("q", q, B, T, D, bytes, 1)) != ATTN_OK) return st;
+    if (k && (st = validate_rows("k", k, B, T, D, bytes, 1)) != ATTN_OK) return st;
+    LaunchEnv env;
+    if ((st = device_env(stream, &env)) != ATTN_OK) return st;
+    const RopeShape s{B, T, D, rotation->turns, rotation->rot_dim, rotation->interleaved ? 1 : 0,
+                      rotation->magnitude, dtype};
+    attn_rows none{};
+    int grid = 0, kernels = 0;
+    cudaError_t e = launch_rope(s, plain_rows(*q, B, T), k ? plain_rows(*k, B, T) : none, qw, kw, norm, eps,
+                                positions, env, &grid, &kernels);
+    if (e == cudaErrorInvalidConfiguration) return fail(ATTN_ERR_UNSUPPORTED, "too many rows for one launch");
+    if (e != cudaSuccess) return cuda_fail(e, "rope launch");
+    record_launch(grid, 0, kernels);
+    return ok();
+}
+
+attn_status run_append(bool e4m3, const attn_rows* q, const attn_rows* k, const attn_rows* v,
+                       const int* cu_seqlens, const int* seq_lens, const int* positions, const int* block_table,
+                       void* kv_cache, float* scales, int B, int total, int D, int page_size,
+                       int max_pages_per_seq, int num_blocks, const attn_rotation* rotation, attn_dtype dtype,
+                       cudaStream_t stream) {
+    if (dtype == ATTN_F32)
+        return fail(ATTN_ERR_UNSUPPORTED, "the paged append is implemented for 16-bit I/O only");
+    if (dtype != ATTN_BF16 && dtype != ATTN_F16)
+        return fail(ATTN_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
+    if (B < 1 || total < 0 || page_size < 1 || max_pages_per_seq < 1 || num_blocks < 1)
+        return fail(ATTN_ERR_INVALID_ARG,
+                    "B, page_size, max_pages_per_seq and num_blocks must be >= 1 and total >= 0");
+    if (D != 64 && D != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim D=%d not supported (64 or 128)", D);
+    if (!k || !v) return fail(ATTN_ERR_INVALID_ARG, "k and v must be non-null");
+    if (static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 1024)
+        return fail(ATTN_ERR_INVALID_ARG, "max_pages_per_seq*page_size must be below 2^31 - 1024");
+    if (static_cast<long long>(B) * max_pages_per_seq > 0x7fffffffLL)
+        return fail(ATTN_ERR_INVALID_ARG, "B*max_pages_per_seq must fit in 31 bits");
+    const attn_rotation plain{nullptr, 0, 0, 1.0f};
+    const attn_rotation& rot = rotation ? *rotation : plain;
+    attn_status st = validate_rotation(&rot, D);
+    if (st != ATTN_OK) return st;
+    if (k->heads != v->heads)
+        return fail(ATTN_ERR_INVALID_ARG, "k and v must have the same heads (got %d, %d)", k->heads, v->heads);
+    if (total == 0) {
+        record_launch(0, 0, 0);
+        return ok();
+    }
+    if ((st = validate_rows("k", k, 1, total, D, 2, 0)) != ATTN_OK) return st;
+    if ((st = validate_rows("v", v, 1, total, D, 2, -1)) != ATTN_OK) return st;
+    if (q && (st = validate_rows("q", q, 1, total, D, 2, 1)) != ATTN_OK) return st;
+    if (!cu_seqlens || !seq_lens || !block_table || !kv_cache || (e4m3 && !scales))
+        return fail(ATTN_ERR_INVALID_ARG, "cu_seqlens, seq_lens, block_table, kv_cache%s must be non-null",
+                    e4m3 ? " and scales" : "");
+    if (!aligned(cu_seqlens, 4) || !aligned(seq_lens, 4) || !aligned(positions, 4) || !aligned(block_table, 4) ||
+        !aligned(scales, 4))
+        return fail(ATTN_ERR_INVALID_ARG, "cu_seqlens, seq_lens, positions, block_table and scales must be 4-byte aligned");
+    if (!aligned(kv_cache, 16)) return fail(ATTN_ERR_INVALID_ARG, "kv_cache must be 16-byte aligned");
+    LaunchEnv env;
+    if ((st = device_env(stream, &env)) != ATTN_OK) return st;
+    const RopeShape r{1, total, D, rot.turns, rot.rot_dim, rot.interleaved ? 1 : 0, rot.magnitude, dtype};
+    const AppendShape s{cu_seqlens, seq_lens, positions, block_table, kv_cache, scales,
+                        B, total, page_size, max_pages_per_seq, num_blocks};
+    attn_rows qr{};
+    if (q) qr = plain_rows(*q, 1, total);
+    const attn_rows kr = plain_rows(*k, 1, total), vr = plain_rows(*v, 1, total);
+    int grid = 0, kernels = 0;
+    cudaError_t e = e4m3 ? launch_append_paged_e4m3(s, r, q ? &qr : nullptr, kr, vr, env, &grid, &kernels)
+                         : launch_append_paged(s, r, q ? &qr : nullptr, kr, vr, env, &grid, &kernels);
+    if (e == cudaErrorInvalidConfiguration) return fail(ATTN_ERR_UNSUPPORTED, "too many rows for one launch");
+    if (e != cudaSuccess) return cuda_fail(e, "paged append launch");
+    record_launch(grid, 0, kernels);
+    return ok();
+}
+
+}  // namespace
+}  // namespace attn
+
+extern "C" {
+
+attn_status attn_rope_turns(unsigned long long* turns, float* magnitude, int rot_dim, double base,
+                            attn_rope_scaling scaling, double factor, double original_length, double low,
+                            double high) {
+    using namespace attn;
+    if (rot_dim < 2 || rot_dim % 2 != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "rot_dim must be even and >= 2 (got %d)", rot_dim);
+    if (!turns || !magnitude) return fail(ATTN_ERR_INVALID_ARG, "turns and magnitude must be non-null");
+    if (scaling < ATTN_ROPE_PLAIN || scaling > ATTN_ROPE_YARN)
+        return fail(ATTN_ERR_INVALID_ARG, "unknown scaling %d", static_cast<int>(scaling));
+    if (!(std::isfinite(base) && base > 1.0)) return fail(ATTN_ERR_INVALID_ARG, "base must be > 1 (got %g)", base);
+    if (scaling != ATTN_ROPE_PLAIN && !(std::isfinite(factor) && factor > 0.0))
+        return fail(ATTN_ERR_INVALID_ARG, "factor must be > 0 (got %g)", factor);
+    if (scaling == ATTN_ROPE_BASE && rot_dim < 4)
+        return fail(ATTN_ERR_INVALID_ARG, "this scaling needs rot_dim > 2");
+    const bool mixed = scaling == ATTN_ROPE_WAVELENGTH || scaling == ATTN_ROPE_YARN;
+    if (mixed && !(std::isfinite(original_length) && original_length > 0.0 && low > 0.0 && low < high && std::isfinite(high)))
+        return fail(ATTN_ERR_INVALID_ARG, "original_length must be > 0 and 0 < low < high");
+    const double kTwoPi = 6.283185307179586476925;
+    if (scaling == ATTN_ROPE_BASE) base *= std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+    if (!(std::isfinite(base) && base > 1.0))
+        return fail(ATTN_ERR_INVALID_ARG, "base * factor^(rot_dim/(rot_dim-2)) must be > 1 (got %g)", base);
+    double first = 0.0, last = 1.0;
+    if (scaling == ATTN_ROPE_YARN) {
+        auto index = [&](double r) {
+            return rot_dim * std::log(original_length / (r * kTwoPi)) / (2.0 * std::log(base));
+        };
+        first = std::min(std::max(std::floor(index(high)), 0.0), rot_dim - 1.0);
+        last = std::min(std::max(std::ceil(index(low)), 0.0), rot_dim - 1.0);
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot_dim);
+        double keep = 1.0;  // weight of f against f / factor
+        if (scaling == ATTN_ROPE_LINEAR) keep = 0.0;
+        if (scaling == ATTN_ROPE_WAVELENGTH) keep = (original_length * f / kTwoPi - low) / (high - low);
+        if (scaling == ATTN_ROPE_YARN) keep = 1.0 - (i - first) / std::max(last - first, 1e-3);
+        keep = std::min(1.0, std::max(0.0, keep));
+        const double g = (scaling == ATTN_ROPE_PLAIN || scaling == ATTN_ROPE_BASE) ? f : keep * f + (1.0 - keep) * f / factor;
+        const double turn = std::fmod(g / kTwoPi, 1.0);  // < 1, so the product below fits
+        turns[i] = static_cast<unsigned long long>(std::ldexp(turn, 64));
+    }
+    *magnitude = scaling == ATTN_ROPE_YARN && factor > 1.0 ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return ok();
+}
+
+attn_status attn_rope(const attn_rows* q, const attn_rows* k, const int* positions, int B, int T, int D,
+                      const attn_rotation* rotation, attn_dtype dtype, cudaStream_t stream) {
+    return attn::run_rope(q, k, nullptr, nullptr, false, 0.0f, positions, B, T, D, rotation, dtype, stream);
+}
+
+attn_status attn_qk_norm_rope(const attn_rows* q, const attn_rows* k, const void* q_weight, const void* k_weight,
+                              float eps, const int* positions, int B, int T, int D,
+                              const attn_rotation* rotation, attn_dtype dtype, cudaStream_t stream) {
+    return attn::run_rope(q, k, q_weight, k_weight, true, eps, positions, B, T, D, rotation, dtype, stream);
+}
+
+attn_status attn_append_paged(const attn_rows* q, const attn_rows* k, const attn_rows* v, const int* cu_seqlens,
+                              const int* seq_lens, const int* positions, const int* block_table, void* kv_cache,
+                              int B, int total, int D, int page_size, int max_pages_per_seq, int num_blocks,
+                              const attn_rotation* rotation, attn_dtype dtype, cudaStream_t stream) {
+    return attn::run_append(false, q, k, v, cu_seqlens, seq_lens, positions, block_table, kv_cache, nullptr, B,
+                            total, D, page_size, max_pages_per_seq, num_blocks, rotation, dtype, stream);
+}
+
+attn_status attn_append_paged_e4m3(const attn_rows* q, const attn_rows* k, const attn_rows* v,
+                                   const int* cu_seqlens, const int* seq_lens, const int* positions,
+                                   const int* block_table, void* kv_cache, float* scales, int B, int total, int D,
+                                   int page_size, int max_pages_per_seq, int num_blocks,
+                                   const attn_rotation* rotation, attn_dtype dtype, cudaStream_t stream) {
+    return attn::run_append(true, q, k, v, cu_seqlens, seq_lens, positions, block_table, kv_cache, scales, B,
+                            total, D, page_size, max_pages_per_seq, num_blocks, rotation, dtype, stream);
+}
+
+attn_status attn_fwd_decode_paged_e4m3(const void* q, const void* kv_cache, const float* scales,
+                                       const int* block_table, const int* seq_lens, void* o, float* lse, int B,
+                                       int Hq, int Hkv, int D, int page_size, int max_pages_per_seq,
+                                       int num_blocks, float scale, attn_dtype dtype, cudaStream_t stream) {
+    using namespace attn;
+    if (dtype == ATTN_F32)
+        return fail(ATTN_ERR_UNSUPPORTED, "the paged decode is implemented for 16-bit I/O only");
+    if (!scales || !aligned(scales, 4))
+        return fail(ATTN_ERR_INVALID_ARG, "scales must be a non-null, 4-byte aligned device pointer");
+    attn_status st = validate_paged(q, kv_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, D, page_size,
+                                    max_pages_per_seq, num_blocks, scale, dtype);
+    if (st != ATTN_OK) return st;
+    LaunchEnv env;
+    st = device_env(stream, &env);
+    if (st != ATTN_OK) return st;
+    PagedShape s{B, Hq, Hkv, D, page_size, max_pages_per_seq, num_blocks, scale};
+    s.f16 = dtype == ATTN_F16 ? 1 : 0;
+    const size_t bytes = decode_e4m3_workspace_bytes(s, env.num_sms);
+    void* ws = nullptr;
+    cudaError_t e = cudaMallocAsync(&ws, bytes, env.stream);
+    if (e != cudaSuccess || ws == nullptr) {
+        cudaGetLastError();
+        return fail(ATTN_ERR_NO_MEMORY, "paged decode workspace of %zu bytes: %s", bytes, cudaGetErrorString(e));
+    }
+    int grid = 0, kernels = 0;
+    e = launch_decode_paged_e4m3(static_cast<const uint16_t*>(q), static_cast<const uint8_t*>(kv_cache), scales,
+                                 reinterpret_cast<const int32_t*>(block_table),
+                                 reinterpret_cast<const int32_t*>(seq_lens), static_cast<uint16_t*>(o), lse, ws,
+                                 s, env, &grid, &kernels);
+    cudaError_t f = cudaFreeAsync(ws, env.stream);
+    if (e == cudaSuccess && f != cudaSuccess) e = f;
+    if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
+    record_launch(grid, 0, kernels);
+    return ok();
+}
+
+}  // extern "C"

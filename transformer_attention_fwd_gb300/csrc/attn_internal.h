@@ -123,6 +123,75 @@ cudaError_t launch_decode_paged_bf16(const uint16_t* q, const uint16_t* kv,
                                      uint16_t* o, float* lse, void* ws, const PagedShape& s,
                                      const LaunchEnv& env, int* grid_out, int* kernels_launched);
 
+// A division by the page size: q = n / size for 0 <= n < 2^31 as one widening
+// product, multiplier ceil(2^(31 + shift) / size) with shift = ceil(log2 size)
+// (the rounding of the multiplier adds less than 2^shift / size to the product
+// in units of the last place, which never reaches the next integer).
+struct PageDivider {
+    int size = 1;
+    uint32_t multiplier = 0x80000000u;
+    int shift = 31;
+    PageDivider() = default;
+    explicit PageDivider(int n) : size(n) {
+        int l = 0;
+        while ((1ll << l) < n) ++l;
+        shift = 31 + l;
+        multiplier = static_cast<uint32_t>(((1ull << shift) + n - 1) / n);
+    }
+    __host__ __device__ int quotient(int n) const {
+        return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(n)) * multiplier) >> shift);
+    }
+    __host__ __device__ int split(int n, int* rest) const {
+        const int q = quotient(n);
+        *rest = n - q * size;
+        return q;
+    }
+};
+
+// Rotary positions.  Rows as in the public ABI (strides in elements).
+using RopeRows = attn_rows;
+struct RopeShape {
+    int B, T, D;  // the append uses D only
+    const unsigned long long* turns;
+    int rot_dim, interleaved;
+    float magnitude;
+    attn_dtype dtype;
+};
+int rope_layout(int rot_dim, int interleaved);  // RopeLayout of rope.cuh
+// qw, kw: the norm's weights (null: all ones), used when norm is set.
+cudaError_t launch_rope(const RopeShape& s, const RopeRows& q, const RopeRows& k, const void* qw,
+                        const void* kw, bool norm, float eps, const int* positions,
+                        const LaunchEnv& env, int* grid_out, int* kernels_launched);
+
+// New tokens of B requests into the paged cache.
+struct AppendShape {
+    const int* cu_seqlens;
+    const int* seq_lens;
+    const int* positions;  // or null
+    const int* block_table;
+    void* cache;
+    float* scales;  // 8-bit cache only
+    int B, total, page, max_pages, num_blocks;
+};
+struct AppendParams;
+AppendParams append_params(const AppendShape& s, const RopeShape& r, const RopeRows* q,
+                           const RopeRows& k, const RopeRows& v, const LaunchEnv& env);
+// q may be null; k.y may be null (no copy of the rotated keys).
+cudaError_t launch_append_paged(const AppendShape& s, const RopeShape& r, const RopeRows* q,
+                                const RopeRows& k, const RopeRows& v, const LaunchEnv& env,
+                                int* grid_out, int* kernels_launched);
+cudaError_t launch_append_paged_e4m3(const AppendShape& s, const RopeShape& r, const RopeRows* q,
+                                     const RopeRows& k, const RopeRows& v, const LaunchEnv& env,
+                                     int* grid_out, int* kernels_launched);
+
+// Decode over the paged 8-bit cache: kv [num_blocks, 2, Hkv, page, D] codes,
+// scales [num_blocks, 2, Hkv].
+size_t decode_e4m3_workspace_bytes(const PagedShape& s, int num_sms);
+cudaError_t launch_decode_paged_e4m3(const uint16_t* q, const uint8_t* kv, const float* scales,
+                                     const int32_t* block_table, const int32_t* seq_lens,
+                                     uint16_t* o, float* lse, void* ws, const PagedShape& s,
+                                     const LaunchEnv& env, int* grid_out, int* kernels_launched);
+
 // Diagnostics.
 cudaError_t launch_diag_mma_tile(const CUtensorMap& a, const CUtensorMap& b,
                                  const CUtensorMap& v, float* s_out, float* o_out, int D,

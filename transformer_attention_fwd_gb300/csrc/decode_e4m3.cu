@@ -1,0 +1,771 @@
+// decode_e4m3.cu -- decode (one query row per (request, head)) over the paged
+// 8-bit cache with one scale for each block, K or V, and head
+// (attn_fwd_decode_paged_e4m3).
+//
+//   O = sum_j p_j vs_j v_j / sum_j p_j,  p_j = 2^x_j,
+//   x_j = log2(e) * scale * ks_j * (q . k_j)
+//
+// with k_j, v_j the codes and ks_j, vs_j the scales of key j's block.  HBM bound:
+// 2 * D bytes per key and KV head are read once.  Half the bytes of the 16-bit
+// cache leave half the time per key, so the products go to the tensor cores
+// (mma.sync m16n8k16 in fp16, fp32 sums; the codes convert exactly): S = Q K^T
+// with the query heads of a KV head as rows and 8 keys as columns, and O^T =
+// V^T P^T with 16 columns of V as rows.  In that orientation the scores a lane
+// holds are the P^T operand it needs, and since the order of a product's inner
+// index is free, K's columns and V's rows are dealt to lanes so that each reads
+// 16 contiguous bytes.
+//
+// Two running references.  The sum of the p_j is taken relative to 2^m, m a
+// maximum over x_j, in fp32.  What multiplies a code is w_j = p_j vs_j, taken
+// relative to 2^mv, mv a maximum over x_j + log2 vs_j, in fp16: the weights that
+// matter keep 11 bits and none overflows, however far apart the scales are.  The
+// result is (sum w_j v_j) / (sum p_j) * 2^(mv - m).  A reference moves only when
+// a key exceeds it by 2^kSlack.
+//
+// Work: all 16-key tiles of all (request, KV head, head chunk) units are laid
+// end to end, cut into one equal slice per CTA and that into one per warp.  A
+// warp streams its tiles through a ring of its own with 16-byte asynchronous
+// copies; nothing in the loop waits for another warp.  Units inside one warp's
+// range are written at once; the pieces of the others are merged in the CTA at
+// its end, and those that a CTA boundary cuts by the combine kernel.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "attn_internal.h"
+#include "e4m3.cuh"
+#include "sm100.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kTile = 16;          // keys of a tile
+constexpr int kMaxPrefixB = 1024;  // requests whose tile counts a CTA sums itself
+constexpr float kSlack = 6.0f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+struct E4m3Params {
+    const uint16_t* q;
+    const uint8_t* kv;
+    const float* scales;
+    const int* block_table;
+    const int* seq_lens;
+    uint16_t* o;
+    float* lse;
+    long long* cum;  // [B + 1] tiles before each request (global: more than kMaxPrefixB requests)
+    int4* first;     // [grid] {request, unit, tile, tiles} a CTA's slice starts in
+    float* ws_o;     // [2 * grid, HC, D] pieces of cut units, not normalised
+    float4* ws_ml;   // [2 * grid, HC] their {m, sum, mv}
+    unsigned* status;
+    PageDivider page;
+    int B, Hq, Hkv, group, chunks, max_pages, num_blocks;
+    float scale_log2;
+};
+
+template <int D, int HC>
+struct E4m3Layout {
+    static constexpr int kStage = 2 * kTile * D + 2 * kTile * 4;  // K rows, V rows, scales
+    static constexpr int kPiece = HC * D * 4;
+    static constexpr int kStages = D == 128 ? (HC == 8 ? 5 : 4) : 8;
+    static constexpr int kPieceOff = kWarps * kStages * kStage;
+    static constexpr int kMlOff = kPieceOff + kWarps * kPiece;  // [warp][2][HC] float4
+    static constexpr int kMetaOff = kMlOff + kWarps * 2 * HC * 16;
+    static constexpr int kCumOff = kMetaOff + kWarps * 2 * 16;
+    static constexpr int kBytes = kCumOff + (kMaxPrefixB + 1) * 8 + 40 * 8;
+    static_assert(kStages * kStage >= kPiece, "a warp's ring holds its second piece");
+    static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
+};
+
+// One place in the sequence of tiles.
+struct Cursor {
+    int b, unit, tile, tiles, len;
+};
+
+__device__ __forceinline__ int clamped_len(const E4m3Params& p, int b) {
+    const int L = p.seq_lens[b], most = p.max_pages * p.page.size;
+    return L < 0 ? 0 : (L > most ? most : L);
+}
+
+__device__ __forceinline__ Cursor cursor_at(const E4m3Params& p, const long long* cum, long long v) {
+    const long long U = static_cast<long long>(p.Hkv) * p.chunks;
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] * U <= v) lo = mid; else hi = mid - 1;
+    }
+    Cursor c;
+    c.b = lo;
+    c.tiles = static_cast<int>(cum[lo + 1] - cum[lo]);
+    const long long r = v - cum[lo] * U;
+    c.unit = static_cast<int>(r / c.tiles);
+    c.tile = static_cast<int>(r - static_cast<long long>(c.unit) * c.tiles);
+    c.len = clamped_len(p, lo);
+    return c;
+}
+
+// The next tile; there has to be one.
+__device__ __forceinline__ void cursor_next(const E4m3Params& p, const long long* cum, Cursor& c) {
+    if (++c.tile < c.tiles) return;
+    c.tile = 0;
+    if (++c.unit < p.Hkv * p.chunks) return;
+    c.unit = 0;
+    do {
+        ++c.b;
+        c.tiles = static_cast<int>(cum[c.b + 1] - cum[c.b]);
+    } while (c.tiles == 0);
+    c.len = clamped_len(p, c.b);
+}
+
+// cum[b] = tiles of requests 0 .. b - 1, by the whole block.
+__device__ void tile_prefix(const E4m3Params& p, long long* cum, long long* scan, bool report) {
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.B + nt - 1) / nt;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int L = clamped_len(p, b);
+        if (report && L != p.seq_lens[b]) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
+        mine += (static_cast<long long>(L) + kTile - 1) / kTile;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long run = incl - mine;
+    for (int i = 0; i < warp; ++i) run += scan[i];
+    for (int b = b0; b < b1; ++b) {
+        cum[b] = run;
+        run += (static_cast<long long>(clamped_len(p, b)) + kTile - 1) / kTile;
+    }
+    if (tid == nt - 1) cum[p.B] = run;  // the last thread's range ends at B
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(1024) e4m3_prefix_kernel(const E4m3Params p) {
+    __shared__ long long scan[32];
+    tile_prefix(p, p.cum, scan, true);
+}
+
+__device__ __forceinline__ long long slice_tiles(long long total, int grid) {
+    const long long per = (total + grid - 1) / grid;
+    return per < kWarps ? kWarps : per;  // at least one tile a warp
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 (4) bytes into shared memory; bytes = 0 writes zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Place of a row's 16-byte chunk: rows of eight chunks rotate theirs by the row,
+// rows of four by the row pair, so that both products' reads spread over the banks.
+template <int D>
+__device__ __forceinline__ int chunk_at(int row, int chunk) {
+    return D == 128 ? (chunk ^ (row & 7)) : (chunk ^ ((row >> 1) & 3));
+}
+
+// The 2 or 4 words of a lane's D/8 columns of a V row.
+template <int D>
+__device__ __forceinline__ void load_v(const uint8_t* rows, int row, int g, uint32_t (&w)[D / 32]) {
+    if (D == 128) {
+        const uint4 u = *reinterpret_cast<const uint4*>(rows + row * D + chunk_at<D>(row, g) * 16);
+        w[0] = u.x; w[1] = u.y; w[D / 32 - 2] = u.z; w[D / 32 - 1] = u.w;
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(rows + row * D + chunk_at<D>(row, g >> 1) * 16 + (g & 1) * 8);
+        w[0] = u.x; w[1] = u.y;
+    }
+}
+
+template <bool kF16>
+__device__ __forceinline__ float elem_f32(uint16_t x) {
+    return kF16 ? f16_lo_to_f32(x) : bf16_lo_to_f32(x);
+}
+
+// The state of the unit a warp is in.
+template <int D, int HC>
+struct UnitState {
+    static constexpr int kR = HC / 8;       // 8-head halves
+    uint32_t qa[D / 16][2 * kR];            // Q operand: row g (and g + 8), two halves of 16 columns
+    float qs[kR];                           // what a product with it is multiplied by
+    float m[kR], l[kR], mv[kR];             // head g (g + 8): reference, this lane's sum; O's reference
+    float o[kR][D / 16][4];                 // O^T: columns 2t, 2t + 1 of the heads
+};
+
+// Q fragments of heads hq0 .. hq0 + heads - 1, each times a power of two that
+// takes its largest element to [512, 1024).
+template <int D, int HC, bool kF16>
+__device__ __forceinline__ void unit_begin(const E4m3Params& p, const Cursor& c, int lane,
+                                           UnitState<D, HC>& s) {
+    const int g = lane >> 2, t = lane & 3;
+    const int hkv = c.unit / p.chunks, chunk = c.unit - hkv * p.chunks;
+    const int heads = min(HC, p.group - chunk * HC);
+    const int hq0 = hkv * p.group + chunk * HC;
+#pragma unroll
+    for (int r = 0; r < HC / 8; ++r) {
+        const int h = r * 8 + g;
+        uint32_t w[D / 8];  // the lane's D/4 columns, t * D/4 on
+        float most = 0.0f;
+        if (h < heads) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                p.q + (static_cast<int64_t>(c.b) * p.Hq + hq0 + h) * D + t * (D / 4));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 u = src[i];
+                w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) w[i] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            most = fmaxf(most, fmaxf(fabsf(elem_f32<kF16>(w[i] & 0xffffu)), fabsf(elem_f32<kF16>(w[i] >> 16))));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        // up = 2^(9 - floor(log2 most)), 1 for zero, subnormal or non-finite rows.
+        const int e = static_cast<int>(__float_as_uint(most) >> 23);
+        const int k = (e == 0 || e == 255) ? 0 : max(-126, min(126, 9 - (e - 127)));
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+        s.qs[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+        // Product step j takes columns 4 j .. 4 j + 3 of the lane's: the first two as
+        // inner indices 2t, 2t + 1, the others as 2t + 8, 2t + 9.
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            s.qa[i / 2][(i & 1) * (HC / 8) + r] =
+                pack_f16x2(elem_f32<kF16>(w[i] & 0xffffu) * up, elem_f32<kF16>(w[i] >> 16) * up);
+        s.m[r] = -INFINITY;
+        s.mv[r] = -INFINITY;
+        s.l[r] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s.o[r][j][i] = 0.0f;
+    }
+}
+
+// Maximum of a head's scores in one tile: a lane's four, over its lane quad.
+__device__ __forceinline__ float row_max(const float (&x)[4]) {
+    float m = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+
+// Factor from sum w v to O: 2^(mv - m) / l.
+__device__ __forceinline__ float out_factor(float m, float l, float mv) { return ex2_approx(mv - m) / l; }
+
+// {m, sum, mv} of pieces folded into one: returns what O's terms of the new
+// piece are multiplied by, and in *keep what the old ones are.
+__device__ __forceinline__ float fold(float4& a, const float4& e, float* keep) {
+    const float m = fmaxf(a.x, e.x), mv = fmaxf(a.z, e.z);
+    a.y = (a.x == -INFINITY ? 0.0f : a.y * ex2_approx(a.x - m)) + (e.x == -INFINITY ? 0.0f : e.y * ex2_approx(e.x - m));
+    *keep = a.z == -INFINITY ? 0.0f : ex2_approx(a.z - mv);
+    const float w = e.z == -INFINITY ? 0.0f : ex2_approx(e.z - mv);
+    a.x = m;
+    a.z = mv;
+    return w;
+}
+
+// One tile of a warp's ring: scores, weights, and the weighted V rows.
+template <int D, int HC>
+__device__ __forceinline__ void unit_tile(const uint8_t* stage, int valid, int lane, UnitState<D, HC>& s) {
+    constexpr int kR = HC / 8;
+    const int g = lane >> 2, t = lane & 3;
+    const uint8_t* vrows = stage + kTile * D;
+    const float* ks = reinterpret_cast<const float*>(stage + 2 * kTile * D);
+    const float* vs = ks + kTile;
+    float sc[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[n][i] = 0.0f;
+        const int row = n * 8 + g;
+        uint32_t w[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            const int chunk = D == 128 ? 2 * t + i : t;
+            const uint4 u = *reinterpret_cast<const uint4*>(stage + row * D + chunk_at<D>(row, chunk) * 16);
+            w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+            mma_f16(sc[n], s.qa[j][0], kR == 2 ? s.qa[j][1] : 0u, s.qa[j][kR], kR == 2 ? s.qa[j][kR + 1] : 0u,
+                    e4m3_to_f16x2(w[j] & 0xffffu), e4m3_to_f16x2(w[j] >> 16));
+    }
+    const float2 k2[2] = {*reinterpret_cast<const float2*>(ks + 2 * t),
+                          *reinterpret_cast<const float2*>(ks + 8 + 2 * t)};
+    const float2 v2[2] = {*reinterpret_cast<const float2*>(vs + 2 * t),
+                          *reinterpret_cast<const float2*>(vs + 8 + 2 * t)};
+    float x[kR][4], y[kR][4];  // exponents of p and of w
+    bool need = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float kk = (i & 1) ? k2[i >> 1].y : k2[i >> 1].x;
+        const float lift = __log2f((i & 1) ? v2[i >> 1].y : v2[i >> 1].x);
+        const bool seen = (i >> 1) * 8 + 2 * t + (i & 1) < valid;
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            x[r][i] = seen ? sc[i >> 1][2 * r + (i & 1)] * kk * s.qs[r] : -INFINITY;
+            y[r][i] = x[r][i] + lift;
+            need |= x[r][i] > s.m[r] + kSlack || y[r][i] > s.mv[r] + kSlack;
+        }
+    }
+    if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            const float m = fmaxf(s.m[r], row_max(x[r])), mv = fmaxf(s.mv[r], row_max(y[r]));
+            s.l[r] *= s.m[r] == -INFINITY ? 0.0f : ex2_approx(s.m[r] - m);
+            const float alpha = s.mv[r] == -INFINITY ? 0.0f : ex2_approx(s.mv[r] - mv);
+            s.m[r] = m;
+            s.mv[r] = mv;
+            const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t), a1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                s.o[r][j][0] *= a0; s.o[r][j][1] *= a1; s.o[r][j][2] *= a0; s.o[r][j][3] *= a1;
+            }
+        }
+    }
+    uint32_t pb[kR][2];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const float m = s.m[r] == -INFINITY ? 0.0f : s.m[r], mv = s.mv[r] == -INFINITY ? 0.0f : s.mv[r];
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s.l[r] += ex2_approx(x[r][i] - m);
+            w[i] = ex2_approx(y[r][i] - mv);
+        }
+        pb[r][0] = pack_f16x2(w[0], w[1]);
+        pb[r][1] = pack_f16x2(w[2], w[3]);
+    }
+    uint32_t vw[4][D / 32];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_v<D>(vrows, 2 * t + (j & 1) + 8 * (j >> 1), g, vw[j]);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            // Bytes 2 half, 2 half + 1 of two keys' words: (k0, k1) of one column, then of the next.
+            const uint32_t sel = half ? 0x7362u : 0x5140u;
+            const uint32_t lo = __byte_perm(vw[0][i], vw[1][i], sel), hi = __byte_perm(vw[2][i], vw[3][i], sel);
+            const uint32_t a0 = e4m3_to_f16x2(lo & 0xffffu), a1 = e4m3_to_f16x2(lo >> 16);
+            const uint32_t a2 = e4m3_to_f16x2(hi & 0xffffu), a3 = e4m3_to_f16x2(hi >> 16);
+#pragma unroll
+            for (int r = 0; r < kR; ++r) mma_f16(s.o[r][2 * i + half], a0, a1, a2, a3, pb[r][0], pb[r][1]);
+        }
+    }
+}
+
+template <bool kF16, int N>
+__device__ __forceinline__ void store_row(uint16_t* dst, const float (&v)[N]) {
+    using E = Elem16<kF16>;
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+        *reinterpret_cast<uint4*>(dst + i) = make_uint4(E::pack(v[i], v[i + 1]), E::pack(v[i + 2], v[i + 3]),
+                                                        E::pack(v[i + 4], v[i + 5]), E::pack(v[i + 6], v[i + 7]));
+}
+
+// What a warp leaves of a unit it has not covered alone.
+struct PieceMeta {
+    long long unit;  // request * units + unit, -1: none
+    int begins, ends;  // the piece holds the unit's first (last) tile; begins = 2: not at the slice's start
+};
+
+template <int D, int HC, bool kF16, bool kWholePages>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
+    using L = E4m3Layout<D, HC>;
+    constexpr int kR = HC / 8, kCols = D / 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    uint8_t* ring = smem + warp * L::kStages * L::kStage;
+    float4* ml = reinterpret_cast<float4*>(smem + L::kMlOff);
+    PieceMeta* meta = reinterpret_cast<PieceMeta*>(smem + L::kMetaOff);
+    long long* s_cum = reinterpret_cast<long long*>(smem + L::kCumOff);
+    const long long* cum = p.cum;
+    if (prefix_in_kernel) {
+        tile_prefix(p, s_cum, s_cum + kMaxPrefixB + 1, blockIdx.x == 0);
+        cum = s_cum;
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int grid = static_cast<int>(gridDim.x);
+    const int U = p.Hkv * p.chunks;
+
+    // Requests without keys.
+    for (int b = blockIdx.x; b < p.B; b += grid) {
+        if (cum[b + 1] != cum[b]) continue;
+        const int64_t row0 = static_cast<int64_t>(b) * p.Hq;
+        for (int i = threadIdx.x; i < p.Hq * (D / 8); i += kWarps * 32)
+            reinterpret_cast<uint4*>(p.o + row0 * D)[i] = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+            for (int i = threadIdx.x; i < p.Hq; i += kWarps * 32) p.lse[row0 + i] = -INFINITY;
+    }
+
+    const long long total = cum[p.B] * U;
+    const long long per = slice_tiles(total, grid);
+    const long long v0 = per * blockIdx.x, v1 = v0 + per < total ? v0 + per : total;
+    if (v0 >= total) return;
+    if (threadIdx.x == 0) {
+        const Cursor c = cursor_at(p, cum, v0);
+        p.first[blockIdx.x] = make_int4(c.b, c.unit, c.tile, c.tiles);
+    }
+    const int wper = static_cast<int>((v1 - v0 + kWarps - 1) / kWarps);
+    const long long va = v0 + static_cast<long long>(warp) * wper;
+    const int count = va >= v1 ? 0 : static_cast<int>(va + wper < v1 ? wper : v1 - va);
+    if (lane < 2) meta[2 * warp + lane].unit = -1;
+    __syncwarp();
+
+    if (count > 0) {
+        Cursor lc = cursor_at(p, cum, va), cc = lc;
+        int loaded = 0;  // tiles whose copies have been issued
+        // The next tile to copy: its block ids are loaded one step ahead.
+        int id = 0, row = 0;
+        auto look_up = [&]() {
+            if (kWholePages) {  // the tile lies in one page
+                const int pg = p.page.split(lc.tile * kTile, &row);
+                id = p.block_table[static_cast<int64_t>(lc.b) * p.max_pages + pg];
+            } else {
+                const int key = lc.tile * kTile + (lane & 15);
+                const int pg = p.page.split(key < lc.len ? key : lc.len - 1, &row);
+                id = p.block_table[static_cast<int64_t>(lc.b) * p.max_pages + pg];
+            }
+        };
+        look_up();
+        auto issue = [&]() {
+            if (loaded < count) {
+                const uint32_t dst = smem_u32(ring + (loaded % L::kStages) * L::kStage);
+                if (id < 0 || id >= p.num_blocks) {
+                    atomicOr(p.status, ATTN_DEV_BAD_INPUT);
+                    id = 0;
+                }
+                const int hkv = lc.unit / p.chunks;
+                const int valid = min(kTile, lc.len - lc.tile * kTile);
+                constexpr int kPerRow = D / 16, kRowsPer = 32 / kPerRow;
+                const int r0 = lane / kPerRow, col = lane % kPerRow;
+                const int64_t to_v = static_cast<int64_t>(p.Hkv) * p.page.size * D;
+                // Lanes 0 .. 15: K's scales, 16 .. 31: V's.
+                copy4(dst + 2 * kTile * D + lane * 4,
+                      p.scales + (static_cast<int64_t>(id) * 2 + (lane >> 4)) * p.Hkv + hkv,
+                      (lane & 15) < valid ? 4 : 0);
+#pragma unroll
+                for (int i = 0; i < kTile / kRowsPer; ++i) {
+                    const int r = i * kRowsPer + r0;
+                    const int rid = kWholePages ? id : __shfl_sync(0xffffffffu, id, r);
+                    const int rrow = kWholePages ? row + (r < valid ? r : 0) : __shfl_sync(0xffffffffu, row, r);
+                    const uint8_t* src =
+                        p.kv + ((static_cast<int64_t>(rid) * 2 * p.Hkv + hkv) * p.page.size + rrow) * D + col * 16;
+                    const int bytes = r < valid ? 16 : 0;
+                    const uint32_t at = dst + r * D + chunk_at<D>(r, col) * 16;
+                    copy16(at, src, bytes);
+                    copy16(at + kTile * D, src + to_v, bytes);
+                }
+                if (++loaded < count) {
+                    cursor_next(p, cum, lc);
+                    look_up();
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int i = 0; i < L::kStages - 1; ++i) issue();
+
+        UnitState<D, HC> s;
+        int pieces = 0;
+        int from = cc.tile;  // the unit's first tile of this warp
+        unit_begin<D, HC, kF16>(p, cc, lane, s);
+        for (int n = 0; n < count; ++n) {
+            asm volatile("cp.async.wait_group %0;" :: "n"(L::kStages - 2) : "memory");
+            __syncwarp();  // the tile is there, and the stage filled next has been read
+            issue();
+            unit_tile<D, HC>(ring + (n % L::kStages) * L::kStage, min(kTile, cc.len - cc.tile * kTile), lane, s);
+            const bool unit_done = cc.tile + 1 == cc.tiles;
+            if (!unit_done && n + 1 < count) {
+                ++cc.tile;
+                continue;
+            }
+            // The unit, or this warp's part of it, is done.
+            const int hkv = cc.unit / p.chunks, chunk = cc.unit - hkv * p.chunks;
+            const int heads = min(HC, p.group - chunk * HC);
+            const int64_t row0 = static_cast<int64_t>(cc.b) * p.Hq + hkv * p.group + chunk * HC;
+            const bool whole = unit_done && from == 0;
+            float* piece = reinterpret_cast<float*>(pieces == 0 ? smem + L::kPieceOff + warp * L::kPiece : ring);
+            if (!whole && pieces == 1) {  // the warp's last: no copy is in flight into its ring
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncwarp();
+            }
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                float l = s.l[r];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                const int h0 = r * 8 + 2 * t;
+                float c0[kCols], c1[kCols];
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    c0[2 * j] = s.o[r][j][0]; c0[2 * j + 1] = s.o[r][j][2];
+                    c1[2 * j] = s.o[r][j][1]; c1[2 * j + 1] = s.o[r][j][3];
+                }
+                if (whole) {
+                    const float f = out_factor(s.m[r], l, s.mv[r]);
+                    const float i0 = __shfl_sync(0xffffffffu, f, 8 * t), i1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i) {
+                        c0[i] *= i0;
+                        c1[i] *= i1;
+                    }
+                    if (h0 < heads) store_row<kF16>(p.o + (row0 + h0) * D + g * kCols, c0);
+                    if (h0 + 1 < heads) store_row<kF16>(p.o + (row0 + h0 + 1) * D + g * kCols, c1);
+                    if (p.lse && t == 0 && r * 8 + g < heads) p.lse[row0 + r * 8 + g] = (s.m[r] + __log2f(l)) * kLn2;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kCols; i += 4) {
+                        *reinterpret_cast<float4*>(piece + h0 * D + g * kCols + i) =
+                            make_float4(c0[i], c0[i + 1], c0[i + 2], c0[i + 3]);
+                        *reinterpret_cast<float4*>(piece + (h0 + 1) * D + g * kCols + i) =
+                            make_float4(c1[i], c1[i + 1], c1[i + 2], c1[i + 3]);
+                    }
+                    if (t == 0) ml[(2 * warp + pieces) * HC + r * 8 + g] = make_float4(s.m[r], l, s.mv[r], 0.0f);
+                }
+            }
+            if (!whole) {
+                if (lane == 0) {
+                    const long long at = va + n - (cc.tile - from);  // the piece's first tile in the sequence
+                    meta[2 * warp + pieces] = PieceMeta{static_cast<long long>(cc.b) * U + cc.unit,
+                                                        from == 0 ? (at > v0 ? 2 : 1) : 0, unit_done ? 1 : 0};
+                }
+                ++pieces;
+            }
+            if (n + 1 < count) {
+                cursor_next(p, cum, cc);
+                from = 0;
+                unit_begin<D, HC, kF16>(p, cc, lane, s);
+            }
+        }
+    }
+    __syncthreads();
+
+    // Merge the pieces of one unit: by the warp that has its first one.
+    for (int slot = 0; slot < 2; ++slot) {
+        const PieceMeta mine = meta[2 * warp + slot];
+        if (mine.unit < 0) continue;
+        if (slot == 0 && warp > 0) {
+            const PieceMeta* before = &meta[2 * (warp - 1)];
+            if ((before[1].unit >= 0 ? before[1].unit : before[0].unit) == mine.unit) continue;
+        }
+        int last = warp;  // last warp that has a piece of it
+        while (last + 1 < kWarps && meta[2 * (last + 1)].unit == mine.unit) ++last;
+        const bool ends = last == warp ? mine.ends : meta[2 * last].ends;
+        const int b = static_cast<int>(mine.unit / U), unit = static_cast<int>(mine.unit - static_cast<long long>(b) * U);
+        const int hkv = unit / p.chunks, chunk = unit - hkv * p.chunks;
+        const int heads = min(HC, p.group - chunk * HC);
+        const int64_t row0 = static_cast<int64_t>(b) * p.Hq + hkv * p.group + chunk * HC;
+        const bool whole = mine.begins && ends;
+        const int64_t ws = 2ll * blockIdx.x + (mine.begins == 2 ? 1 : 0);
+        for (int h = 0; h < heads; ++h) {
+            float4 sum = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+            float acc[D / 32];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
+            for (int w = warp; w <= last; ++w) {
+                const int sl = w == warp ? slot : 0;
+                float keep;
+                const float wt = fold(sum, ml[(2 * w + sl) * HC + h], &keep);
+                const float* piece = reinterpret_cast<const float*>(
+                    sl == 0 ? smem + L::kPieceOff + w * L::kPiece : smem + w * L::kStages * L::kStage);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(piece[h * D + i * 32 + lane], wt, acc[i] * keep);
+            }
+            if (whole) {
+                const float f = out_factor(sum.x, sum.y, sum.z);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+                    p.o[(row0 + h) * D + i * 32 + lane] =
+                        static_cast<uint16_t>(Elem16<kF16>::pack(acc[i] * f, 0.0f) & 0xffffu);
+                if (p.lse && lane == 0) p.lse[row0 + h] = (sum.x + __log2f(sum.y)) * kLn2;
+            } else {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) p.ws_o[(ws * HC + h) * D + i * 32 + lane] = acc[i];
+                if (lane == 0) p.ws_ml[ws * HC + h] = sum;
+            }
+        }
+    }
+}
+
+// Merge the pieces of the units that CTA boundaries cut: block j takes the
+// boundary between the slices of CTAs j and j + 1, if it is the unit's first
+// one; one thread per head and column.  Launched with programmatic stream
+// serialisation: it waits for the kernel before it reads.
+template <int D, int HC, bool kF16>
+__global__ void __launch_bounds__(1024) decode_e4m3_combine_kernel(const E4m3Params p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int grid = static_cast<int>(gridDim.x) + 1;
+    // The tile total: from the prefix, or summed here.
+    __shared__ long long s_total;
+    if (p.cum == nullptr) {
+        if (threadIdx.x < 32) {
+            long long n = 0;
+            for (int b = threadIdx.x; b < p.B; b += 32) n += (static_cast<long long>(clamped_len(p, b)) + kTile - 1) / kTile;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            if (threadIdx.x == 0) s_total = n;
+        }
+        __syncthreads();
+    }
+    const int U = p.Hkv * p.chunks;
+    const long long total = (p.cum == nullptr ? s_total : p.cum[p.B]) * U;
+    const long long per = slice_tiles(total, grid);
+    const long long at = per * (blockIdx.x + 1ll);
+    if (at >= total) return;
+    const int4 f = p.first[blockIdx.x + 1];
+    if (f.z == 0 || f.z > per) return;  // not cut here, or cut at an earlier boundary
+    const long long start = at - f.z;
+    const long long c0 = start / per, c1 = (start + f.w - 1) / per;
+    const int in_first = start != c0 * per ? 1 : 0;
+    const int hkv = f.y / p.chunks, chunk = f.y - hkv * p.chunks;
+    const int heads = min(HC, p.group - chunk * HC);
+    const int64_t row0 = static_cast<int64_t>(f.x) * p.Hq + hkv * p.group + chunk * HC;
+    for (int i = threadIdx.x; i < heads * D; i += blockDim.x) {
+        const int h = i / D, d = i - h * D;
+        float4 sum = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+        float acc = 0.0f;
+        for (long long c = c0; c <= c1; ++c) {
+            const long long slot = (2 * c + (c == c0 ? in_first : 0)) * HC + h;
+            float keep;
+            const float wt = fold(sum, p.ws_ml[slot], &keep);
+            acc = fmaf(p.ws_o[slot * D + d], wt, acc * keep);
+        }
+        p.o[(row0 + h) * D + d] =
+            static_cast<uint16_t>(Elem16<kF16>::pack(acc * out_factor(sum.x, sum.y, sum.z), 0.0f) & 0xffffu);
+        if (d == 0 && p.lse) p.lse[row0 + h] = (sum.x + __log2f(sum.y)) * kLn2;
+    }
+}
+
+// Query heads a CTA serves at a time: one or two 8-row halves of the product.
+int heads_at_once(int group) { return group <= 8 ? 8 : 16; }
+
+// Workspace: cum (long long [B + 1]), first (int4 [grid]), the pieces of the
+// cut units and their references and sums.
+struct WsLayout {
+    size_t first, ws_o, ws_ml, bytes;
+    WsLayout(const PagedShape& s, int grid) {
+        const size_t rows = 2ull * grid * heads_at_once(s.Hq / s.Hkv);
+        auto up16 = [](size_t x) { return (x + 15) / 16 * 16; };
+        first = up16(8ull * (s.B + 1));
+        ws_o = first + 16ull * grid;
+        ws_ml = ws_o + rows * s.D * sizeof(float);
+        bytes = ws_ml + rows * sizeof(float4);
+    }
+};
+
+template <int D, int HC, bool kF16, bool kWholePages>
+cudaError_t launch_main(const E4m3Params& p, int grid, int prefix, int device, cudaStream_t st) {
+    using L = E4m3Layout<D, HC>;
+    auto* kern = decode_e4m3_kernel<D, HC, kF16, kWholePages>;
+    static bool attr_set[64] = {};  // device < 64 (device_env)
+    cudaError_t e = cudaSuccess;
+    if (!attr_set[device]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+        if (e != cudaSuccess) return e;
+        attr_set[device] = true;
+    }
+    kern<<<grid, kWarps * 32, L::kBytes, st>>>(p, prefix);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || grid < 2) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid - 1);
+    cfg.blockDim = dim3(std::min(1024, HC * D));
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_e4m3_combine_kernel<D, HC, kF16>, p);
+}
+
+template <int D, int HC>
+cudaError_t launch_types(const E4m3Params& p, bool f16, bool whole, int grid, int prefix,
+                         const LaunchEnv& env) {
+    const int dev = env.device;
+    cudaStream_t st = env.stream;
+    if (f16)
+        return whole ? launch_main<D, HC, true, true>(p, grid, prefix, dev, st)
+                     : launch_main<D, HC, true, false>(p, grid, prefix, dev, st);
+    return whole ? launch_main<D, HC, false, true>(p, grid, prefix, dev, st)
+                 : launch_main<D, HC, false, false>(p, grid, prefix, dev, st);
+}
+
+}  // namespace
+
+size_t decode_e4m3_workspace_bytes(const PagedShape& s, int num_sms) { return WsLayout(s, num_sms).bytes; }
+
+cudaError_t launch_decode_paged_e4m3(const uint16_t* q, const uint8_t* kv, const float* scales,
+                                     const int32_t* block_table, const int32_t* seq_lens,
+                                     uint16_t* o, float* lse, void* ws, const PagedShape& s,
+                                     const LaunchEnv& env, int* grid_out, int* kernels_launched) {
+    const int grid = env.num_sms;
+    const WsLayout lay(s, grid);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    const bool prefix = s.B <= kMaxPrefixB;
+    E4m3Params p{};
+    p.q = q;
+    p.kv = kv;
+    p.scales = scales;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.o = o;
+    p.lse = lse;
+    p.cum = prefix ? nullptr : reinterpret_cast<long long*>(base);
+    p.first = reinterpret_cast<int4*>(base + lay.first);
+    p.ws_o = reinterpret_cast<float*>(base + lay.ws_o);
+    p.ws_ml = reinterpret_cast<float4*>(base + lay.ws_ml);
+    p.status = env.status;
+    p.page = PageDivider(s.page);
+    p.B = s.B;
+    p.Hq = s.Hq;
+    p.Hkv = s.Hkv;
+    p.group = s.Hq / s.Hkv;
+    const int hc = heads_at_once(p.group);
+    p.chunks = (p.group + hc - 1) / hc;
+    p.max_pages = s.max_pages;
+    p.num_blocks = s.num_blocks;
+    p.scale_log2 = s.scale * 1.4426950408889634f;
+
+    cudaError_t e = cudaSuccess;
+    if (!prefix) {
+        e4m3_prefix_kernel<<<1, 1024, 0, env.stream>>>(p);
+        e = cudaGetLastError();
+    }
+    const bool f16 = s.f16 != 0, whole = s.page % kTile == 0;
+    if (e == cudaSuccess) {
+        if (s.D == 64)
+            e = hc == 8 ? launch_types<64, 8>(p, f16, whole, grid, prefix, env)
+                        : launch_types<64, 16>(p, f16, whole, grid, prefix, env);
+        else
+            e = hc == 8 ? launch_types<128, 8>(p, f16, whole, grid, prefix, env)
+                        : launch_types<128, 16>(p, f16, whole, grid, prefix, env);
+    }
+    if (grid_out) *grid_out = grid;
+    if (kernels_launched) *kernels_launched = (prefix ? 1 : 2) + (grid > 1 ? 1 : 0);
+    return e;
+}
+
+}  // namespace attn
