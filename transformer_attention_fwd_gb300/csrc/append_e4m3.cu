@@ -11,12 +11,12 @@
 // scale that grows by an exact division.
 //
 // Work: an item is one page of one request, in which the call's new tokens fill
-// some rows.  A CTA takes one item and eight of its 2 * Hkv (K or V, head)
-// tasks, a warp each: it loads up to 16 rows, takes their largest magnitude
-// from the raw bits, fixes the scale, rotates from registers with the sines and
-// cosines the CTA shares, rounds and stores.  Longer pages run in groups of 16
-// rows and read their rows a second time (out of L2).  Query rows are taken by
-// further CTAs of the same launch, as in append.cu.
+// some rows.  A CTA takes one item and up to eight heads, a warp each: it loads
+// up to 16 rows of K and of V, takes their largest magnitudes from the raw bits,
+// fixes the scales, rotates K from registers with the sines and cosines the CTA
+// shares, rounds and stores.  Longer pages run in groups of 16 rows and read
+// their rows a second time (out of L2).  Query rows are taken by further CTAs of
+// the same launch, as in append.cu.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -29,6 +29,7 @@
 namespace attn {
 namespace {
 
+constexpr int kPageWarps = 8;
 constexpr int kGroup = 16;  // rows in registers at a time
 
 // The smallest power of two s >= 2^-100 with amax <= limit * s.
@@ -40,64 +41,121 @@ __device__ __forceinline__ float block_scale(float amax, float limit) {
 }
 
 // Largest finite magnitude of the two 16-bit elements of each word.
-template <typename Row>
+template <typename E>
 __device__ __forceinline__ uint32_t finite_magnitude(uint32_t w) {
-    constexpr uint32_t kInf = Row::kInfinity;
+    constexpr uint32_t kInf = E::kInfinity;
     const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
     return max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u);
 }
 
 struct BlockBf16 : RopeBf16 {
     static constexpr uint32_t kInfinity = 0x7f80u;
-    static __device__ __forceinline__ float value(uint32_t bits) { return bf16_lo_to_f32(bits); }
 };
 struct BlockF16 : RopeF16 {
     static constexpr uint32_t kInfinity = 0x7c00u;
-    static __device__ __forceinline__ float value(uint32_t bits) { return f16_lo_to_f32(bits); }
 };
 
-template <typename Row, int D, int kLayout>
-__global__ void __launch_bounds__(kAppendWarps * 32)
+// The rows of one (page, K or V, head) as a warp holds them.
+template <typename E, int D, int kLayout>
+struct PageRows {
+    using R = Rope<E, D, kLayout>;
+    static constexpr int kSteps = kGroup / R::kRows;
+    typename R::Raw raw[kSteps];
+
+    // Rows 16 g .. of `rows` at x (the warp's token 0 and head), zeros beyond.
+    __device__ __forceinline__ void load(const uint8_t* x, long long row_bytes, int g, int rows, int grp,
+                                         long long at0, long long at1) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = g * kGroup + i * R::kRows + grp;
+            const uint8_t* at = x + r * row_bytes;
+            raw[i] = r < rows ? R::load(at + at0, at + at1) : R::zero();
+        }
+    }
+    // Largest magnitude's bits, both halves of a word apart; infinities and NaN count.
+    __device__ __forceinline__ uint32_t magnitude() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            m = __vmaxu2(__vmaxu2(m, raw[i].c0.x & 0x7fff7fffu), raw[i].c1.x & 0x7fff7fffu);
+            m = __vmaxu2(__vmaxu2(m, raw[i].c0.y & 0x7fff7fffu), raw[i].c1.y & 0x7fff7fffu);
+            m = __vmaxu2(__vmaxu2(m, raw[i].c0.z & 0x7fff7fffu), raw[i].c1.z & 0x7fff7fffu);
+            m = __vmaxu2(__vmaxu2(m, raw[i].c0.w & 0x7fff7fffu), raw[i].c1.w & 0x7fff7fffu);
+        }
+        return m;
+    }
+    __device__ __forceinline__ uint32_t finite() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            m = max(m, max(finite_magnitude<E>(raw[i].c0.x), finite_magnitude<E>(raw[i].c1.x)));
+            m = max(m, max(finite_magnitude<E>(raw[i].c0.y), finite_magnitude<E>(raw[i].c1.y)));
+            m = max(m, max(finite_magnitude<E>(raw[i].c0.z), finite_magnitude<E>(raw[i].c1.z)));
+            m = max(m, max(finite_magnitude<E>(raw[i].c0.w), finite_magnitude<E>(raw[i].c1.w)));
+        }
+        return m;
+    }
+};
+
+// The block's scale for new rows of magnitude amax; the `held` rows it has
+// already follow a scale that grows.
+template <int D>
+__device__ __forceinline__ float settle_scale(float amax, float limit, int held, float* scale_at, uint8_t* block,
+                                              int lane) {
+    float scale = block_scale(amax, limit);
+    if (held > 0) {
+        const float old = *scale_at;
+        if (scale > old) {
+            const float ratio = old / scale;
+            for (int c = lane; c < held * (D / 16); c += 32) {
+                uint4* at = reinterpret_cast<uint4*>(block) + c;
+                uint4 w = *at;
+                w.x = e4m3_rescale(w.x, ratio);
+                w.y = e4m3_rescale(w.y, ratio);
+                w.z = e4m3_rescale(w.z, ratio);
+                w.w = e4m3_rescale(w.w, ratio);
+                *at = w;
+            }
+        }
+        scale = fmaxf(scale, old);
+    }
+    __syncwarp();  // every lane has read the old scale
+    if (lane == 0) *scale_at = scale;
+    return scale;
+}
+
+template <typename R>
+__device__ __forceinline__ void store_codes(uint8_t* row, int e0, int e1, typename R::Pairs& v, float inv) {
+    R::scale(v, inv);
+    float x[8], y[8];
+    R::elements(v, x, y);
+    *reinterpret_cast<uint2*>(row + e0) =
+        make_uint2(e4m3_pack4(x[0], x[1], x[2], x[3]), e4m3_pack4(x[4], x[5], x[6], x[7]));
+    *reinterpret_cast<uint2*>(row + e1) =
+        make_uint2(e4m3_pack4(y[0], y[1], y[2], y[3]), e4m3_pack4(y[4], y[5], y[6], y[7]));
+}
+
+template <typename E, int D, int kLayout>
+__global__ void __launch_bounds__(kPageWarps * 32, 2)
 append_e4m3_kernel(const AppendParams p) {
-    constexpr int kLanes = D / kRopeChunk, kRowsPerStep = 32 / kLanes;
-    constexpr int kSteps = kGroup / kRowsPerStep;
-    __shared__ float s_row[kLayout == kRopeHalvesOdd ? kAppendWarps * kRowsPerStep * D : 1];
-    __shared__ float2 s_cs[kGroup][D / 2];  // cos, sin of a row's pairs
+    using R = Rope<E, D, kLayout>;
+    using Rows = PageRows<E, D, kLayout>;
+    __shared__ __align__(16) float s_table[kGroup][D];  // a row's cosines and sines
+    __shared__ float s_scratch[R::kScratch ? kPageWarps * R::kScratch : 1];
+    static_assert(kGroup >= kPageWarps, "query CTAs take a table row for each warp");
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int sub = lane % kLanes, grp = lane / kLanes;
-    float* row = s_row + (kLayout == kRopeHalvesOdd ? (warp * kRowsPerStep + grp) * D : 0);
+    float* scratch = s_scratch + (R::kScratch ? warp * R::kScratch : 0);
     const unsigned kv_blocks = p.items * p.splits;
     if (blockIdx.x == gridDim.x - 1) append_report(p);
-
-    if (blockIdx.x >= kv_blocks) {  // query rows
-        const long long w = static_cast<long long>(blockIdx.x - kv_blocks) * kAppendWarps + warp;
-        if (w >= p.warps) return;
-        const int token = static_cast<int>(w / p.q_segs);
-        const int seg = static_cast<int>(w - static_cast<long long>(token) * p.q_segs);
-        int b, slot;
-        if (!append_slot(p, token, lane, &b, &slot)) return;
-        RopeCoef coef;
-        rope_coefficients<Row, kLayout>(p.table, sub * kRopeChunk,
-                                        p.positions ? p.positions[token] : slot, nullptr, coef);
-        const uint8_t* x = static_cast<const uint8_t*>(p.q.x) +
-                           (token * p.q.x_token + sub * kRopeChunk) * Row::kBytes;
-        uint8_t* y = static_cast<uint8_t*>(p.q.y) +
-                     (token * p.q.y_token + sub * kRopeChunk) * Row::kBytes;
-        const int h0 = seg * p.steps * kRowsPerStep;
-        const int h1 = min(p.q.heads, h0 + p.steps * kRowsPerStep);
-        for (int h = h0; h < h1; h += kRowsPerStep) {
-            const int head = h + grp;
-            const typename Row::Raw raw =
-                head < h1 ? Row::load(x + head * p.q.x_head * Row::kBytes) : Row::zero();
-            float v[8], vp[8];
-            Row::unpack(raw, v);
-            rope_exchange<Row, kLayout, D>(raw, v, p.table.half, lane, row, vp);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], coef.own[e], vp[e] * coef.other[e]);
-            if (head < h1) Row::store(y + head * p.q.y_head * Row::kBytes, v);
-        }
+    if (blockIdx.x >= kv_blocks) {
+        append_rows<E, D, kLayout>(p, static_cast<long long>(blockIdx.x - kv_blocks) * kPageWarps + warp,
+                                   s_table[warp], scratch);
         return;
     }
+    const int j = lane % R::kLanes, grp = lane / R::kLanes;
+    if (R::kScratch) scratch += grp * D;
+    const int half = p.table.half;
+    const unsigned on = R::turning(half, j);
 
     // The item's request, page and rows: the same in every warp.
     const int item = static_cast<int>(blockIdx.x / p.splits);
@@ -118,135 +176,100 @@ append_e4m3_kernel(const AppendParams p) {
     const int groups = (rows + kGroup - 1) / kGroup;
 
     const int Hkv = p.k.heads;
-    const int first_task = static_cast<int>(blockIdx.x % p.splits) * kAppendWarps;
-    const int task = first_task + warp;
-    const bool active = task < 2 * Hkv, is_v = task >= Hkv, cta_has_k = first_task < Hkv;
-    const int head = is_v ? task - Hkv : task;
-    const RopeRows& src = is_v ? p.v : p.k;
-    const uint8_t* x = static_cast<const uint8_t*>(src.x) +
-                       (token0 * src.x_token + head * src.x_head + sub * kRopeChunk) * Row::kBytes;
+    const int head = static_cast<int>(blockIdx.x % p.splits) * kPageWarps + warp;
+    const bool active = head < Hkv;
+    const long long at0 = R::first(j, half) * E::kBytes, at1 = R::second(j, half) * E::kBytes;
+    const uint8_t* xk = static_cast<const uint8_t*>(p.k.x) + (token0 * p.k.x_token + head * p.k.x_head) * E::kBytes;
+    const uint8_t* xv = static_cast<const uint8_t*>(p.v.x) + (token0 * p.v.x_token + head * p.v.x_head) * E::kBytes;
+    const long long k_row = p.k.x_token * E::kBytes, v_row = p.v.x_token * E::kBytes;
+    const int mine = active ? rows : 0;  // rows this warp loads
     const int id = append_block(p, b, p.page.quotient(static_cast<int>(page0)));
-
-    typename Row::Raw raw[kSteps];
-    auto load = [&](int g) {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int rr = g * kGroup + i * kRowsPerStep + grp;
-            raw[i] = active && rr < rows ? Row::load(x + rr * src.x_token * Row::kBytes) : Row::zero();
-        }
-    };
-    load(0);
-    uint32_t packed = 0;
-    for (int g = 0;;) {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            packed = __vmaxu2(packed, raw[i].x & 0x7fff7fffu);
-            packed = __vmaxu2(packed, raw[i].y & 0x7fff7fffu);
-            packed = __vmaxu2(packed, raw[i].z & 0x7fff7fffu);
-            packed = __vmaxu2(packed, raw[i].w & 0x7fff7fffu);
-        }
-        if (++g == groups) break;
-        load(g);
-    }
-    uint32_t most = __reduce_max_sync(0xffffffffu, max(packed & 0xffffu, packed >> 16));
-    if (most >= Row::kInfinity) {  // infinities or NaN among them: the finite ones alone
-        most = 0;
-        for (int g = 0; g < groups; ++g) {
-            if (groups > 1) load(g);
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                most = max(most, max(finite_magnitude<Row>(raw[i].x), finite_magnitude<Row>(raw[i].y)));
-                most = max(most, max(finite_magnitude<Row>(raw[i].z), finite_magnitude<Row>(raw[i].w)));
-            }
-        }
-        most = __reduce_max_sync(0xffffffffu, most);
-    }
     const bool write = active && id >= 0;
-    float scale = block_scale(Row::value(most), is_v ? kE4m3Max : p.k_limit);
-    uint8_t* block = p.cache + ((static_cast<int64_t>(id) * 2 + (is_v ? 1 : 0)) * Hkv + head) * p.page.size * D;
-    if (write) {
-        float* scale_at = p.scales + (static_cast<int64_t>(id) * 2 + (is_v ? 1 : 0)) * Hkv + head;
-        if (r0 > 0) {
-            const float old = *scale_at;
-            if (scale > old) {  // the older rows follow
-                const float ratio = old / scale;
-                for (int c = lane; c < r0 * (D / 16); c += 32) {
-                    uint4* at = reinterpret_cast<uint4*>(block) + c;
-                    uint4 w = *at;
-                    w.x = e4m3_rescale(w.x, ratio);
-                    w.y = e4m3_rescale(w.y, ratio);
-                    w.z = e4m3_rescale(w.z, ratio);
-                    w.w = e4m3_rescale(w.w, ratio);
-                    *at = w;
-                }
-            }
-            scale = fmaxf(scale, old);
-        }
-        __syncwarp();  // every lane has read the old scale
-        if (lane == 0) *scale_at = scale;
+
+    Rows k, v;
+    k.load(xk, k_row, 0, mine, grp, at0, at1);
+    v.load(xv, v_row, 0, mine, grp, at0, at1);
+    uint32_t mk = k.magnitude(), mv = v.magnitude();
+    for (int g = 1; g < groups; ++g) {
+        k.load(xk, k_row, g, mine, grp, at0, at1);
+        v.load(xv, v_row, g, mine, grp, at0, at1);
+        mk = __vmaxu2(mk, k.magnitude());
+        mv = __vmaxu2(mv, v.magnitude());
     }
-    const float inv = 1.0f / scale;
+    mk = __reduce_max_sync(0xffffffffu, max(mk & 0xffffu, mk >> 16));
+    mv = __reduce_max_sync(0xffffffffu, max(mv & 0xffffu, mv >> 16));
+    if (max(mk, mv) >= E::kInfinity) {  // infinities or NaN among them: the finite ones alone
+        mk = mv = 0;
+        for (int g = 0; g < groups; ++g) {
+            if (groups > 1) {
+                k.load(xk, k_row, g, mine, grp, at0, at1);
+                v.load(xv, v_row, g, mine, grp, at0, at1);
+            }
+            mk = max(mk, k.finite());
+            mv = max(mv, v.finite());
+        }
+        mk = __reduce_max_sync(0xffffffffu, mk);
+        mv = __reduce_max_sync(0xffffffffu, mv);
+    }
+    const int64_t slot = static_cast<int64_t>(id) * 2 * Hkv + head;  // of K; V's is Hkv further
+    uint8_t* kb = p.cache + slot * p.page.size * D;
+    uint8_t* vb = kb + static_cast<int64_t>(Hkv) * p.page.size * D;
+    float ik = 0.0f, iv = 0.0f;
+    if (write) {
+        ik = 1.0f / settle_scale<D>(E::lo(mk), p.k_limit, r0, p.scales + slot, kb, lane);
+        iv = 1.0f / settle_scale<D>(E::lo(mv), kE4m3Max, r0, p.scales + slot + Hkv, vb, lane);
+    }
 
     // From the last group, which is in registers, to the first.
     for (int g = groups - 1; g >= 0; --g) {
-        if (cta_has_k && p.table.half > 0) {
-            __syncthreads();
-            const int here = min(kGroup, rows - g * kGroup);
-            for (int i = threadIdx.x; i < here * p.table.half; i += kAppendWarps * 32) {
-                const int rr = i / p.table.half, pair = i - rr * p.table.half;
-                const int at = g * kGroup + rr;
-                float s, c;
-                rope_sincos(p.table, pair, p.positions ? p.positions[token0 + at] : start + (token0 - rq.begin) + at,
-                            &s, &c);
-                s_cs[rr][pair] = make_float2(c * p.table.magnitude, s * p.table.magnitude);
-            }
-            __syncthreads();
+        if (g != groups - 1) __syncthreads();  // the table of the group before has been read
+        const int here = min(kGroup, rows - g * kGroup);
+        for (int i = threadIdx.x; i < here * (D / 2); i += kPageWarps * 32) {
+            const int rr = i / (D / 2), token = token0 + g * kGroup + rr;
+            rope_entry<D>(p.table, i % (D / 2), p.positions ? p.positions[token] : start + (token - rq.begin),
+                          s_table[rr]);
         }
+        __syncthreads();
         if (!active) continue;
-        if (g != groups - 1) load(g);
+        if (g != groups - 1) {
+            k.load(xk, k_row, g, mine, grp, at0, at1);
+            v.load(xv, v_row, g, mine, grp, at0, at1);
+        }
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int in_group = i * kRowsPerStep + grp, rr = g * kGroup + in_group;
-            if (g * kGroup + i * kRowsPerStep >= rows) break;  // the same for the whole warp
-            float v[8];
-            Row::unpack(raw[i], v);
-            if (!is_v) {
-                float vp[8];
-                rope_exchange<Row, kLayout, D>(raw[i], v, p.table.half, lane, row, vp);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    bool first = true;
-                    const int pair = rope_pair<kLayout>(sub * kRopeChunk + e, p.table.half, &first);
-                    if (pair < 0) continue;
-                    const float2 cs = s_cs[in_group][pair];
-                    v[e] = fmaf(v[e], cs.x, vp[e] * (first ? -cs.y : cs.y));
-                }
-                if (rr < rows && p.k.y != nullptr)
-                    Row::store(static_cast<uint8_t*>(p.k.y) +
-                                   ((token0 + rr) * p.k.y_token + head * p.k.y_head + sub * kRopeChunk) * Row::kBytes,
-                               v);
+        for (int i = 0; i < Rows::kSteps; ++i) {
+            if (i * R::kRows >= here) break;  // the same for the whole warp
+            const int in_group = i * R::kRows + grp, rr = g * kGroup + in_group;
+            typename R::Pairs x = R::unpack(k.raw[i]);
+            typename R::Coef coef;
+            R::coefficients(s_table[in_group], j, coef);
+            R::turn(x, coef, on, half, j, s_table[in_group], scratch);
+            if (rr >= rows) continue;
+            if (p.k.y != nullptr) {
+                uint8_t* y = static_cast<uint8_t*>(p.k.y) +
+                             ((token0 + rr) * p.k.y_token + head * p.k.y_head) * E::kBytes;
+                R::store(y + at0, y + at1, x);
             }
-            if (rr < rows && write) {
-                uint2 out;
-                out.x = e4m3_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-                out.y = e4m3_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
-                *reinterpret_cast<uint2*>(block + static_cast<int64_t>(r0 + rr) * D + sub * kRopeChunk) = out;
-            }
+            if (!write) continue;
+            const int64_t at = static_cast<int64_t>(r0 + rr) * D;
+            const int e0 = static_cast<int>(at0) / E::kBytes, e1 = static_cast<int>(at1) / E::kBytes;
+            store_codes<R>(kb + at, e0, e1, x, ik);
+            x = R::unpack(v.raw[i]);
+            store_codes<R>(vb + at, e0, e1, x, iv);
         }
     }
 }
 
-template <typename Row, int D>
+template <typename E, int D>
 cudaError_t launch_layout(const AppendParams& p, int layout, unsigned blocks, cudaStream_t st) {
     switch (layout) {
         case kRopeAdjacent:
-            append_e4m3_kernel<Row, D, kRopeAdjacent><<<blocks, kAppendWarps * 32, 0, st>>>(p);
+            append_e4m3_kernel<E, D, kRopeAdjacent><<<blocks, kPageWarps * 32, 0, st>>>(p);
             break;
         case kRopeHalves:
-            append_e4m3_kernel<Row, D, kRopeHalves><<<blocks, kAppendWarps * 32, 0, st>>>(p);
+            append_e4m3_kernel<E, D, kRopeHalves><<<blocks, kPageWarps * 32, 0, st>>>(p);
             break;
         default:
-            append_e4m3_kernel<Row, D, kRopeHalvesOdd><<<blocks, kAppendWarps * 32, 0, st>>>(p);
+            append_e4m3_kernel<E, D, kRopeHalvesOdd><<<blocks, kPageWarps * 32, 0, st>>>(p);
             break;
     }
     return cudaGetLastError();
@@ -263,19 +286,23 @@ cudaError_t launch_append_paged_e4m3(const AppendShape& s, const RopeShape& r, c
                     : kE4m3Max;
     // Request b's pages are items cu[b] / page + 2 b and on: it touches at most
     // n / page + 2 of them, so the ranges do not meet.
-    p.splits = static_cast<unsigned>((2 * k.heads + kAppendWarps - 1) / kAppendWarps);
+    p.splits = static_cast<unsigned>((k.heads + kPageWarps - 1) / kPageWarps);
     const long long items = s.total / s.page + 2ll * s.B;
-    const int rows = 32 / (r.D / kRopeChunk);
-    const int q_steps = (p.q.heads + rows - 1) / rows;
-    const long long per = static_cast<long long>(s.total) * q_steps / (static_cast<long long>(env.num_sms) * 32);
-    p.steps = static_cast<int>(std::max<long long>(1, std::min<long long>(per, q_steps)));
-    p.q_segs = (q_steps + p.steps - 1) / p.steps;
-    p.warps = static_cast<long long>(s.total) * p.q_segs;
-    const long long blocks = items * p.splits + (p.warps + kAppendWarps - 1) / kAppendWarps;
+    // The query heads' steps as in append.cu.
+    const int step_rows = 32 * 16 / r.D;
+    p.q_steps = p.steps = (p.q.heads + step_rows - 1) / step_rows;
+    if (p.steps > 0) {
+        const long long want = static_cast<long long>(env.num_sms) * 32;
+        p.segs = static_cast<int>(std::max<long long>(1, std::min<long long>(p.steps, want / s.total)));
+        p.per_seg = (p.steps + p.segs - 1) / p.segs;
+        p.segs = (p.steps + p.per_seg - 1) / p.per_seg;
+        p.warps = static_cast<long long>(s.total) * p.segs;
+    }
+    const long long blocks = items * p.splits + (p.warps + kPageWarps - 1) / kPageWarps;
     if (items > 0x7fffffffLL || blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     p.items = static_cast<unsigned>(items);
     const unsigned g = static_cast<unsigned>(blocks);
-    const int layout = rope_layout(r.rot_dim, r.interleaved);
+    const int layout = rope_layout(r.rot_dim, r.interleaved, 2);
     cudaError_t e;
     if (r.dtype == ATTN_F16)
         e = r.D == 64 ? launch_layout<BlockF16, 64>(p, layout, g, env.stream)

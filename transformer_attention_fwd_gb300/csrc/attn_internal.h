@@ -157,7 +157,7 @@ struct RopeShape {
     float magnitude;
     attn_dtype dtype;
 };
-int rope_layout(int rot_dim, int interleaved);  // RopeLayout of rope.cuh
+int rope_layout(int rot_dim, int interleaved, int bytes);  // RopeLayout of rope.cuh
 // qw, kw: the norm's weights (null: all ones), used when norm is set.
 cudaError_t launch_rope(const RopeShape& s, const RopeRows& q, const RopeRows& k, const void* qw,
                         const void* kw, bool norm, float eps, const int* positions,

@@ -5,14 +5,11 @@
 //   y = R(t) (x * w / sqrt(mean(x^2) + eps)),  R(t): the rotation of rope.cuh
 //
 // Memory bound: every element is read once and written once, 3 to 7 flops
-// between.  One warp takes one token and a run of its heads; D/8 lanes share a
-// row, 16 bytes (fp32: 32) each, so a warp access covers 32/(D/8) whole rows.
-// The sines and cosines belong to the token, not to the head: a lane computes
-// those of its eight elements once and applies them to every head of the run,
-// which is as long as the grid stays large enough to fill the GPU.  Halves
-// trade whole 8-element chunks between lanes (four shuffles a row); only a
-// rotated half that is no multiple of eight elements goes through shared
-// memory.
+// between.  One warp takes one token and a run of its heads, kRows of them a
+// step; D/16 lanes (fp32: D/8) share a row, two 16-byte chunks each, so a
+// warp's accesses cover whole rows.  The sines and cosines belong to the token,
+// not to the head: the warp computes each once, into shared memory, and every
+// lane keeps those of its pairs in registers for all its heads.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -24,8 +21,8 @@
 namespace attn {
 namespace {
 
-constexpr int kRopeWarps = 8;
-constexpr int kRopeUnroll = 4;  // rows a lane has in flight
+constexpr int kRopeWarps = 4;
+constexpr int kRopeUnroll = 2;  // steps a lane has in flight
 
 struct RopeParams {
     RopeRows q, k;
@@ -33,88 +30,118 @@ struct RopeParams {
     const void* kw;
     const int* positions;
     RopeTable table;
-    long long warps;  // tokens * (q segments + k segments)
+    long long warps;  // tokens * segments
     int T;
-    int q_segs, segs, steps;  // segments of the query heads, of all heads; steps a segment
+    int q_steps, steps, segs, per_seg;  // a token's steps, cut into segments
     float eps;
-    int norm;
 };
 
-template <typename Row, int D, int kLayout>
-__global__ void __launch_bounds__(kRopeWarps * 32)
+template <typename E, int D, int kLayout, bool kNorm>
+__global__ void __launch_bounds__(kRopeWarps * 32, kNorm ? 5 : 6)
 rope_kernel(const RopeParams p) {
-    constexpr int kLanes = D / kRopeChunk, kRowsPerStep = 32 / kLanes;
-    __shared__ float s_row[kLayout == kRopeHalvesOdd ? kRopeWarps * kRowsPerStep * D : 1];
+    using R = Rope<E, D, kLayout, kNorm>;
+    __shared__ __align__(16) float s_table[kRopeWarps][D];
+    __shared__ float s_scratch[R::kScratch ? kRopeWarps * R::kScratch : 1];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int sub = lane % kLanes, grp = lane / kLanes;
+    const int j = lane % R::kLanes, grp = lane / R::kLanes;
     const long long w = static_cast<long long>(blockIdx.x) * kRopeWarps + warp;
     if (w >= p.warps) return;
     const long long token = w / p.segs;
-    int seg = static_cast<int>(w - token * p.segs);
-    const bool is_k = seg >= p.q_segs;
-    if (is_k) seg -= p.q_segs;
-    const RopeRows& r = is_k ? p.k : p.q;
+    const int seg = static_cast<int>(w - token * p.segs);
     const long long b = token / p.T, t = token - b * p.T;
-    const uint8_t* x = static_cast<const uint8_t*>(r.x) +
-                       (b * r.x_batch + t * r.x_token + sub * kRopeChunk) * Row::kBytes;
-    uint8_t* y = static_cast<uint8_t*>(r.y) +
-                 (b * r.y_batch + t * r.y_token + sub * kRopeChunk) * Row::kBytes;
-    const long long xh = r.x_head * Row::kBytes, yh = r.y_head * Row::kBytes;
-    const int h0 = seg * p.steps * kRowsPerStep;
-    const int h1 = min(r.heads, h0 + p.steps * kRowsPerStep);
-    float* row = s_row + (kLayout == kRopeHalvesOdd ? (warp * kRowsPerStep + grp) * D : 0);
+    const int half = p.table.half;
+    const unsigned on = R::turning(half, j);
+    const long long at0 = R::first(j, half) * E::kBytes, at1 = R::second(j, half) * E::kBytes;
+    const uint8_t* xq = static_cast<const uint8_t*>(p.q.x) + (b * p.q.x_batch + t * p.q.x_token) * E::kBytes;
+    const uint8_t* xk = static_cast<const uint8_t*>(p.k.x) + (b * p.k.x_batch + t * p.k.x_token) * E::kBytes;
+    uint8_t* yq = static_cast<uint8_t*>(p.q.y) + (b * p.q.y_batch + t * p.q.y_token) * E::kBytes;
+    uint8_t* yk = static_cast<uint8_t*>(p.k.y) + (b * p.k.y_batch + t * p.k.y_token) * E::kBytes;
+    float* table = s_table[warp];
+    float* scratch = s_scratch + (R::kScratch ? warp * R::kScratch + grp * D : 0);
 
-    RopeCoef coef;
-    bool have = false;
-    for (int h = h0; h < h1; h += kRopeUnroll * kRowsPerStep) {
-        typename Row::Raw raw[kRopeUnroll];
+    const int s0 = seg * p.per_seg, s1 = min(p.steps, s0 + p.per_seg);
+    typename R::Coef coef;
+    typename R::Pairs weight;  // the odd layout multiplies by it; the others have it in coef
+    int coef_of = -1;          // 0: query heads, 1: key heads
+    for (int s = s0; s < s1; s += kRopeUnroll) {
+        typename R::Raw raw[kRopeUnroll];
 #pragma unroll
         for (int u = 0; u < kRopeUnroll; ++u) {
-            const int head = h + u * kRowsPerStep + grp;
-            raw[u] = head < h1 ? Row::load(x + head * xh) : Row::zero();
+            const bool is_k = s + u >= p.q_steps;
+            const int head = (is_k ? s + u - p.q_steps : s + u) * R::kRows + grp;
+            const uint8_t* x = is_k ? xk + head * p.k.x_head * E::kBytes : xq + head * p.q.x_head * E::kBytes;
+            raw[u] = s + u < s1 && head < (is_k ? p.k.heads : p.q.heads) ? R::load(x + at0, x + at1) : R::zero();
         }
-        if (!have) {  // behind the first loads
-            rope_coefficients<Row, kLayout>(p.table, sub * kRopeChunk, p.positions[token],
-                                            p.norm ? (is_k ? p.kw : p.qw) : nullptr, coef);
-            have = true;
+        if (s == s0) {  // behind the first loads
+            rope_fill<D>(p.table, p.positions[token], lane, table);
+            if (!kNorm) R::coefficients(table, j, coef);
         }
 #pragma unroll
         for (int u = 0; u < kRopeUnroll; ++u) {
-            if (h + u * kRowsPerStep >= h1) break;  // the same for the whole warp
-            const int head = h + u * kRowsPerStep + grp;
-            float v[8], vp[8];
-            Row::unpack(raw[u], v);
-            rope_exchange<Row, kLayout, D>(raw[u], v, p.table.half, lane, row, vp);
-            const float scale = p.norm ? rope_rms_scale<D>(v, p.eps) : 1.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = fmaf(v[e], coef.own[e], vp[e] * coef.other[e]) * scale;
-            if (head < h1) Row::store(y + head * yh, v);
+            if (s + u >= s1) break;  // the same for the whole warp
+            const bool is_k = s + u >= p.q_steps;
+            const int head = (is_k ? s + u - p.q_steps : s + u) * R::kRows + grp;
+            typename R::Pairs v = R::unpack(raw[u]);
+            float scale = 1.0f;
+            if (kNorm) {
+                if (coef_of != (is_k ? 1 : 0)) {
+                    coef_of = is_k ? 1 : 0;
+                    const uint8_t* wrow = static_cast<const uint8_t*>(is_k ? p.kw : p.qw);
+                    weight = wrow ? R::unpack(R::load(wrow + at0, wrow + at1)) : R::ones();
+                    R::coefficients(table, j, coef, &weight);
+                }
+                scale = R::rms_scale(v, p.eps);
+                if (kLayout == kRopeHalvesOdd) R::multiply(v, weight);
+            }
+            R::turn(v, coef, on, half, j, table, scratch);
+            if (kNorm) R::scale(v, scale);
+            uint8_t* y = is_k ? yk + head * p.k.y_head * E::kBytes : yq + head * p.q.y_head * E::kBytes;
+            if (head < (is_k ? p.k.heads : p.q.heads)) R::store(y + at0, y + at1, v);
         }
     }
 }
 
-template <typename Row, int D>
-cudaError_t launch_layout(const RopeParams& p, int layout, unsigned blocks, cudaStream_t st) {
-    switch (layout) {
-        case kRopeAdjacent: rope_kernel<Row, D, kRopeAdjacent><<<blocks, kRopeWarps * 32, 0, st>>>(p); break;
-        case kRopeHalves: rope_kernel<Row, D, kRopeHalves><<<blocks, kRopeWarps * 32, 0, st>>>(p); break;
-        default: rope_kernel<Row, D, kRopeHalvesOdd><<<blocks, kRopeWarps * 32, 0, st>>>(p); break;
-    }
+template <typename E, int D, int kLayout>
+cudaError_t launch_norm(const RopeParams& p, bool norm, unsigned blocks, cudaStream_t st) {
+    if (norm) rope_kernel<E, D, kLayout, true><<<blocks, kRopeWarps * 32, 0, st>>>(p);
+    else rope_kernel<E, D, kLayout, false><<<blocks, kRopeWarps * 32, 0, st>>>(p);
     return cudaGetLastError();
 }
 
-template <typename Row>
-cudaError_t launch_dim(const RopeParams& p, int D, int layout, unsigned blocks, cudaStream_t st) {
-    return D == 64 ? launch_layout<Row, 64>(p, layout, blocks, st)
-                   : launch_layout<Row, 128>(p, layout, blocks, st);
+template <typename E>
+cudaError_t launch_type(RopeParams p, int D, int layout, bool norm, const LaunchEnv& env, int* grid) {
+    const int rows = 32 * 2 * (16 / E::kBytes) / D;  // Rope<...>::kRows
+    p.q_steps = (p.q.heads + rows - 1) / rows;
+    p.steps = p.q_steps + (p.k.heads + rows - 1) / rows;
+    // A token's steps stay in one warp once 32 warps per SM are there without
+    // cutting; fewer tokens cut them (a decode step is all latency).
+    const long long tokens = p.warps, want = static_cast<long long>(env.num_sms) * 32;
+    p.segs = static_cast<int>(std::max<long long>(1, std::min<long long>(p.steps, want / tokens)));
+    p.per_seg = (p.steps + p.segs - 1) / p.segs;
+    p.segs = (p.steps + p.per_seg - 1) / p.per_seg;
+    p.warps = tokens * p.segs;
+    const long long blocks = (p.warps + kRopeWarps - 1) / kRopeWarps;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const unsigned g = static_cast<unsigned>(blocks);
+    *grid = static_cast<int>(g);
+    if (D == 64)
+        switch (layout) {
+            case kRopeAdjacent: return launch_norm<E, 64, kRopeAdjacent>(p, norm, g, env.stream);
+            case kRopeHalves: return launch_norm<E, 64, kRopeHalves>(p, norm, g, env.stream);
+            default: return launch_norm<E, 64, kRopeHalvesOdd>(p, norm, g, env.stream);
+        }
+    switch (layout) {
+        case kRopeAdjacent: return launch_norm<E, 128, kRopeAdjacent>(p, norm, g, env.stream);
+        case kRopeHalves: return launch_norm<E, 128, kRopeHalves>(p, norm, g, env.stream);
+        default: return launch_norm<E, 128, kRopeHalvesOdd>(p, norm, g, env.stream);
+    }
 }
 
 }  // namespace
 
-int rope_layout(int rot_dim, int interleaved) {
+int rope_layout(int rot_dim, int interleaved, int bytes) {
     if (interleaved || rot_dim == 0) return kRopeAdjacent;
-    return (rot_dim / 2) % 8 == 0 ? kRopeHalves : kRopeHalvesOdd;
+    return (rot_dim / 2) % (16 / bytes) == 0 ? kRopeHalves : kRopeHalvesOdd;
 }
 
 cudaError_t launch_rope(const RopeShape& s, const RopeRows& q, const RopeRows& k, const void* qw,
@@ -129,26 +156,14 @@ cudaError_t launch_rope(const RopeShape& s, const RopeRows& q, const RopeRows& k
     p.table = RopeTable{s.turns, s.rot_dim / 2, s.magnitude};
     p.T = s.T;
     p.eps = eps;
-    p.norm = norm ? 1 : 0;
-    const int rows = 32 / (s.D / kRopeChunk);
-    const long long tokens = static_cast<long long>(s.B) * s.T;
-    const int q_steps = (q.heads + rows - 1) / rows, k_steps = (k.heads + rows - 1) / rows;
-    // Steps a warp takes: one while 32 warps per SM are not reached (a decode
-    // step is all latency), then as many as keep that many warps.
-    const long long per = tokens * (q_steps + k_steps) / (static_cast<long long>(env.num_sms) * 32);
-    p.steps = static_cast<int>(std::max<long long>(1, std::min<long long>(per, std::max(q_steps, k_steps))));
-    p.q_segs = (q_steps + p.steps - 1) / p.steps;
-    p.segs = p.q_segs + (k_steps + p.steps - 1) / p.steps;
-    p.warps = tokens * p.segs;
-    const long long blocks = (p.warps + kRopeWarps - 1) / kRopeWarps;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const unsigned g = static_cast<unsigned>(blocks);
+    p.warps = static_cast<long long>(s.B) * s.T;
+    const int layout = rope_layout(s.rot_dim, s.interleaved, s.dtype == ATTN_F32 ? 4 : 2);
+    int grid = 0;
     cudaError_t e;
-    const int layout = rope_layout(s.rot_dim, s.interleaved);
-    if (s.dtype == ATTN_F32) e = launch_dim<RopeF32>(p, s.D, layout, g, env.stream);
-    else if (s.dtype == ATTN_F16) e = launch_dim<RopeF16>(p, s.D, layout, g, env.stream);
-    else e = launch_dim<RopeBf16>(p, s.D, layout, g, env.stream);
-    if (grid_out) *grid_out = static_cast<int>(g);
+    if (s.dtype == ATTN_F32) e = launch_type<RopeF32>(p, s.D, layout, norm, env, &grid);
+    else if (s.dtype == ATTN_F16) e = launch_type<RopeF16>(p, s.D, layout, norm, env, &grid);
+    else e = launch_type<RopeBf16>(p, s.D, layout, norm, env, &grid);
+    if (grid_out) *grid_out = grid;
     if (kernels_launched) *kernels_launched = 1;
     return e;
 }

@@ -1,6 +1,6 @@
-// rope.cuh -- rotary positions on rows of D elements held by lane groups of a
-// warp, shared by the rotation kernels (rope.cu) and the paged append
-// (append.cu, append_e4m3.cu).
+// rope.cuh -- rotary positions on rows of D elements held by groups of lanes,
+// shared by the rotation kernels (rope.cu) and the paged appends (append.cu,
+// append_e4m3.cu).
 //
 // A pair (a, b) of one head at position t turns by the angle t * f of its
 // frequency f:  (a cos - b sin, b cos + a sin), times the rotation's
@@ -9,6 +9,13 @@
 // product: exact, whatever the position.  The angle's error is the table's
 // rounding, |t| * 2^-65 turns, and the 2^-25 half turns of the float the top
 // 32 bits are rounded to.
+//
+// A lane holds two 16-byte chunks of a row, chosen so that both elements of
+// each of its pairs are its own: chunks j and j + half for the halves layout,
+// any two for adjacent pairs.  Then nothing is exchanged between lanes, and
+// pairs are worked on two at a time as packed fp32 (first elements A, second
+// elements B).  Only halves that are no whole number of chunks go through
+// shared memory.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -18,96 +25,27 @@
 
 namespace attn {
 
-constexpr int kRopeChunk = 8;  // elements of a row one lane holds
-
-// How the pairs of a head are laid out, as far as the exchange between lanes
-// goes.
 enum RopeLayout {
-    kRopeAdjacent = 0,  // (2i, 2i+1): inside one lane
-    kRopeHalves = 1,    // (i, i + rot/2), rot/2 a multiple of 8: whole chunks trade lanes
-    kRopeHalvesOdd = 2  // (i, i + rot/2), any even rot: elements traded through shared memory
+    kRopeAdjacent = 0,  // pairs (2i, 2i+1)
+    kRopeHalves = 1,    // pairs (i, i + half), half a whole number of 16-byte chunks
+    kRopeHalvesOdd = 2  // pairs (i, i + half), any half
 };
 
-// Element types: eight elements of a row as loaded (Raw), and as fp32.
+// Element types: words of a chunk to and from fp32.
 struct RopeBf16 {
-    using Raw = uint4;
     static constexpr int kBytes = 2;
-    static __device__ __forceinline__ Raw load(const void* p) { return *static_cast<const uint4*>(p); }
-    static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
-    static __device__ __forceinline__ void unpack(const Raw& u, float (&f)[8]) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = bf16_lo_to_f32(w[i]);
-            f[2 * i + 1] = bf16_hi_to_f32(w[i]);
-        }
-    }
-    static __device__ __forceinline__ void store(void* p, const float (&f)[8]) {
-        *static_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-    }
-    static __device__ __forceinline__ void store_raw(void* p, const Raw& u) { *static_cast<uint4*>(p) = u; }
-    static __device__ __forceinline__ Raw shuffle(const Raw& u, int lane) {
-        return make_uint4(__shfl_sync(0xffffffffu, u.x, lane), __shfl_sync(0xffffffffu, u.y, lane),
-                          __shfl_sync(0xffffffffu, u.z, lane), __shfl_sync(0xffffffffu, u.w, lane));
-    }
+    static __device__ __forceinline__ float lo(uint32_t w) { return bf16_lo_to_f32(w); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return bf16_hi_to_f32(w); }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_bf16x2(a, b); }
 };
-
 struct RopeF16 {
-    using Raw = uint4;
     static constexpr int kBytes = 2;
-    static __device__ __forceinline__ Raw load(const void* p) { return *static_cast<const uint4*>(p); }
-    static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
-    static __device__ __forceinline__ void unpack(const Raw& u, float (&f)[8]) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = f16_lo_to_f32(w[i]);
-            f[2 * i + 1] = f16_hi_to_f32(w[i]);
-        }
-    }
-    static __device__ __forceinline__ void store(void* p, const float (&f)[8]) {
-        *static_cast<uint4*>(p) = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]),
-                                             pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
-    }
-    static __device__ __forceinline__ void store_raw(void* p, const Raw& u) { *static_cast<uint4*>(p) = u; }
-    static __device__ __forceinline__ Raw shuffle(const Raw& u, int lane) { return RopeBf16::shuffle(u, lane); }
+    static __device__ __forceinline__ float lo(uint32_t w) { return f16_lo_to_f32(w); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return f16_hi_to_f32(w); }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_f16x2(a, b); }
 };
-
 struct RopeF32 {
-    struct Raw {
-        float4 a, b;
-    };
     static constexpr int kBytes = 4;
-    static __device__ __forceinline__ Raw load(const void* p) {
-        const float4* q = static_cast<const float4*>(p);
-        return Raw{q[0], q[1]};
-    }
-    static __device__ __forceinline__ Raw zero() {
-        return Raw{make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
-    }
-    static __device__ __forceinline__ void unpack(const Raw& u, float (&f)[8]) {
-        f[0] = u.a.x; f[1] = u.a.y; f[2] = u.a.z; f[3] = u.a.w;
-        f[4] = u.b.x; f[5] = u.b.y; f[6] = u.b.z; f[7] = u.b.w;
-    }
-    static __device__ __forceinline__ void store(void* p, const float (&f)[8]) {
-        float4* q = static_cast<float4*>(p);
-        q[0] = make_float4(f[0], f[1], f[2], f[3]);
-        q[1] = make_float4(f[4], f[5], f[6], f[7]);
-    }
-    static __device__ __forceinline__ void store_raw(void* p, const Raw& u) {
-        float4* q = static_cast<float4*>(p);
-        q[0] = u.a;
-        q[1] = u.b;
-    }
-    static __device__ __forceinline__ Raw shuffle(const Raw& u, int lane) {
-        Raw r;
-        r.a.x = __shfl_sync(0xffffffffu, u.a.x, lane); r.a.y = __shfl_sync(0xffffffffu, u.a.y, lane);
-        r.a.z = __shfl_sync(0xffffffffu, u.a.z, lane); r.a.w = __shfl_sync(0xffffffffu, u.a.w, lane);
-        r.b.x = __shfl_sync(0xffffffffu, u.b.x, lane); r.b.y = __shfl_sync(0xffffffffu, u.b.y, lane);
-        r.b.z = __shfl_sync(0xffffffffu, u.b.z, lane); r.b.w = __shfl_sync(0xffffffffu, u.b.w, lane);
-        return r;
-    }
 };
 
 // The rotation of one call.
@@ -117,130 +55,273 @@ struct RopeTable {
     float magnitude;
 };
 
-__device__ __forceinline__ void rope_sincos(const RopeTable& t, int pair, int position, float* s,
-                                            float* c) {
+// magnitude * (cos, sin) of a pair's angle.
+__device__ __forceinline__ float2 rope_cos_sin(const RopeTable& t, int pair, int position) {
     const unsigned long long phase =
         static_cast<unsigned long long>(static_cast<long long>(position)) * t.turns[pair];
-    const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f;
-    sincospif(half_turns, s, c);
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &s, &c);
+    return make_float2(c * t.magnitude, s * t.magnitude);
 }
 
-// What a lane multiplies its eight elements and their partners by:
-// y[e] = x[e] * own[e] + partner[e] * other[e].
-struct RopeCoef {
-    float own[8], other[8];
-};
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 
-// Pair and sign of element i of a head: the pair it belongs to (-1 outside the
-// rotated part) and whether it is the pair's first element.
-template <int kLayout>
-__device__ __forceinline__ int rope_pair(int i, int half, bool* first) {
-    if (i >= 2 * half) return -1;
-    if (kLayout == kRopeAdjacent) {
-        *first = (i & 1) == 0;
-        return i >> 1;
+// kWeights: elements are multiplied by weights (the norm's) on the way.
+template <typename E, int D, int kLayout, bool kWeights = false>
+struct Rope {
+    static constexpr int kChunk = 16 / E::kBytes;       // elements of a 16-byte chunk; pairs of a lane
+    static constexpr int kLanes = D / (2 * kChunk);     // lanes of a row
+    static constexpr int kRows = 32 / kLanes;           // rows of a warp step
+    static constexpr int kP2 = kChunk / 2;              // pairs of pairs of a lane
+    static constexpr int kScratch = kLayout == kRopeHalvesOdd ? kRows * D : 0;  // floats a warp needs
+
+    struct Raw {
+        uint4 c0, c1;
+    };
+    struct Pairs {  // pairs 2k, 2k + 1: first elements, second elements
+        uint64_t a[kP2], b[kP2];
+    };
+    // A row's result from its pairs: a' = a * aa + b * ab, b' = b * bb + a * ba.
+    // Without weights aa = bb = cos and ab = -ba = -sin, of which one each is
+    // kept.
+    struct Coef {
+        uint64_t aa[kP2], ab[kP2], bb[kWeights ? kP2 : 1], ba[kWeights ? kP2 : 1];
+    };
+
+    // First elements of lane j's chunks.
+    static __device__ __forceinline__ int first(int j, int half) {
+        if (kLayout != kRopeHalves) return j * kChunk;
+        const int hc = half / kChunk;
+        return (j < hc ? j : 2 * hc + 2 * (j - hc)) * kChunk;
     }
-    *first = i < half;
-    return *first ? i : i - half;
-}
+    static __device__ __forceinline__ int second(int j, int half) {
+        if (kLayout != kRopeHalves) return (j + kLanes) * kChunk;
+        const int hc = half / kChunk;
+        return (j < hc ? j + hc : 2 * hc + 2 * (j - hc) + 1) * kChunk;
+    }
+    // Pair i of lane j.
+    static __device__ __forceinline__ int pair(int j, int i) {
+        if (kLayout == kRopeAdjacent)
+            return i < kP2 ? j * kP2 + i : (j + kLanes) * kP2 + i - kP2;
+        return j * kChunk + i;
+    }
 
-// Element a lane's element i trades with (itself outside the rotated part).
-template <int kLayout>
-__device__ __forceinline__ int rope_partner(int i, int half) {
-    if (i >= 2 * half) return i;
-    if (kLayout == kRopeAdjacent) return i ^ 1;
-    return i < half ? i + half : i - half;
-}
+    static __device__ __forceinline__ Raw load(const void* first_chunk, const void* second_chunk) {
+        return Raw{*static_cast<const uint4*>(first_chunk), *static_cast<const uint4*>(second_chunk)};
+    }
+    static __device__ __forceinline__ Raw zero() { return Raw{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}; }
 
-// weight: nullptr, or the norm's weight row (fp32 values come from Row::unpack
-// of its chunks); the partner's element carries the partner's weight.
-template <typename Row, int kLayout>
-__device__ __forceinline__ void rope_coefficients(const RopeTable& t, int chunk0, int position,
-                                                  const void* weight, RopeCoef& k) {
+    static __device__ __forceinline__ Pairs ones() {
+        Pairs p;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        bool first = true;
-        const int pair = rope_pair<kLayout>(chunk0 + e, t.half, &first);
-        float s = 0.0f, c = 1.0f;
-        if (pair >= 0) {
-            if (kLayout == kRopeAdjacent && (e & 1)) {  // the pair's even element has them already
-                k.own[e] = k.own[e - 1];
-                k.other[e] = -k.other[e - 1];
-                continue;
+        for (int i = 0; i < kP2; ++i) p.a[i] = p.b[i] = f2_pack(1.0f, 1.0f);
+        return p;
+    }
+    static __device__ __forceinline__ Pairs unpack(const Raw& r) {
+        Pairs p;
+        if constexpr (E::kBytes == 4) {
+            const float x[4] = {__uint_as_float(r.c0.x), __uint_as_float(r.c0.y), __uint_as_float(r.c0.z), __uint_as_float(r.c0.w)};
+            const float y[4] = {__uint_as_float(r.c1.x), __uint_as_float(r.c1.y), __uint_as_float(r.c1.z), __uint_as_float(r.c1.w)};
+            if (kLayout == kRopeAdjacent) {
+                p.a[0] = f2_pack(x[0], x[2]); p.b[0] = f2_pack(x[1], x[3]);
+                p.a[1] = f2_pack(y[0], y[2]); p.b[1] = f2_pack(y[1], y[3]);
+            } else {
+                p.a[0] = f2_pack(x[0], x[1]); p.a[1] = f2_pack(x[2], x[3]);
+                p.b[0] = f2_pack(y[0], y[1]); p.b[1] = f2_pack(y[2], y[3]);
             }
-            rope_sincos(t, pair, position, &s, &c);
-            s *= t.magnitude;
-            c *= t.magnitude;
-        }
-        k.own[e] = c;
-        k.other[e] = first ? -s : s;
-    }
-    if (weight != nullptr) {
-        float w[8];
-        const uint8_t* base = static_cast<const uint8_t*>(weight);
-        Row::unpack(Row::load(base + static_cast<int64_t>(chunk0) * Row::kBytes), w);
+        } else {
+            const uint32_t x[4] = {r.c0.x, r.c0.y, r.c0.z, r.c0.w}, y[4] = {r.c1.x, r.c1.y, r.c1.z, r.c1.w};
+            if (kLayout == kRopeAdjacent) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) k.own[e] *= w[e];
+                for (int k = 0; k < 2; ++k) {
+                    p.a[k] = f2_pack(E::lo(x[2 * k]), E::lo(x[2 * k + 1]));
+                    p.b[k] = f2_pack(E::hi(x[2 * k]), E::hi(x[2 * k + 1]));
+                    p.a[kP2 - 2 + k] = f2_pack(E::lo(y[2 * k]), E::lo(y[2 * k + 1]));
+                    p.b[kP2 - 2 + k] = f2_pack(E::hi(y[2 * k]), E::hi(y[2 * k + 1]));
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kP2; ++k) {
+                    p.a[k] = f2_pack(E::lo(x[k]), E::hi(x[k]));
+                    p.b[k] = f2_pack(E::lo(y[k]), E::hi(y[k]));
+                }
+            }
+        }
+        return p;
+    }
+
+    // The elements in the chunks' order.
+    static __device__ __forceinline__ void elements(const Pairs& p, float (&x)[kChunk], float (&y)[kChunk]) {
         if (kLayout == kRopeAdjacent) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) k.other[e] *= w[e ^ 1];
-        } else if (kLayout == kRopeHalves) {
-            const int p0 = rope_partner<kLayout>(chunk0, t.half);
-            Row::unpack(Row::load(base + static_cast<int64_t>(p0) * Row::kBytes), w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) k.other[e] *= w[e];
+            for (int k = 0; k < kP2 / 2; ++k) {
+                f2_unpack(p.a[k], x[4 * k], x[4 * k + 2]);
+                f2_unpack(p.b[k], x[4 * k + 1], x[4 * k + 3]);
+                f2_unpack(p.a[kP2 / 2 + k], y[4 * k], y[4 * k + 2]);
+                f2_unpack(p.b[kP2 / 2 + k], y[4 * k + 1], y[4 * k + 3]);
+            }
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int p = rope_partner<kLayout>(chunk0 + e, t.half);
-                float wp[8];
-                Row::unpack(Row::load(base + static_cast<int64_t>(p & ~7) * Row::kBytes), wp);
-                float v = wp[0];
-#pragma unroll
-                for (int j = 1; j < 8; ++j) v = (p & 7) == j ? wp[j] : v;
-                k.other[e] *= v;
+            for (int k = 0; k < kP2; ++k) {
+                f2_unpack(p.a[k], x[2 * k], x[2 * k + 1]);
+                f2_unpack(p.b[k], y[2 * k], y[2 * k + 1]);
             }
         }
     }
-}
 
-// The partners of a lane's eight elements.  All 32 lanes call it; `row` is the
-// lane group's D floats of shared memory (kRopeHalvesOdd only).  Elements
-// outside the rotated part get 0, so that 0 * infinity does not reach them.
-template <typename Row, int kLayout, int D>
-__device__ __forceinline__ void rope_exchange(const typename Row::Raw& raw, const float (&x)[8],
-                                              int half, int lane, float* row, float (&xp)[8]) {
-    const int sub = lane % (D / 8);
-    if (kLayout == kRopeAdjacent) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xp[e] = x[e ^ 1];
-    } else if (kLayout == kRopeHalves) {
-        const int hc = half / 8;
-        const int to = sub >= 2 * hc ? lane : (sub < hc ? lane + hc : lane - hc);
-        Row::unpack(Row::shuffle(raw, to), xp);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) row[sub * 8 + e] = x[e];
-        __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xp[e] = row[rope_partner<kLayout>(sub * 8 + e, half)];
-        __syncwarp();
+    static __device__ __forceinline__ uint4 pack(const float (&x)[kChunk]) {
+        if constexpr (E::kBytes == 4)
+            return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        else
+            return make_uint4(E::pack(x[0], x[1]), E::pack(x[2], x[3]), E::pack(x[4], x[5]), E::pack(x[6], x[7]));
     }
-    if (2 * half < D) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xp[e] = sub * 8 + e < 2 * half ? xp[e] : 0.0f;
+    static __device__ __forceinline__ void store(void* first_chunk, void* second_chunk, const Pairs& p) {
+        float x[kChunk], y[kChunk];
+        elements(p, x, y);
+        *static_cast<uint4*>(first_chunk) = pack(x);
+        *static_cast<uint4*>(second_chunk) = pack(y);
     }
-}
 
-// 1 / sqrt(mean(x^2) + eps) over a row held by D/8 neighbouring lanes.
+    // Which of lane j's pairs turn.
+    static __device__ __forceinline__ unsigned turning(int half, int j) {
+        unsigned on = 0;
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) on |= pair(j, i) < half ? 1u << i : 0u;
+        return on;
+    }
+    // Lane j's coefficients from a token's table, and from its weights.
+    static __device__ __forceinline__ void coefficients(const float* table, int j, Coef& k,
+                                                        const Pairs* w = nullptr) {
+        if constexpr (kLayout != kRopeHalvesOdd) {  // the odd layout reads them where they are used
+#pragma unroll
+            for (int i = 0; i < kP2; i += 2) {  // four pairs next to one another (fp32 adjacent: two)
+                k.aa[i] = *reinterpret_cast<const uint64_t*>(table + pair(j, 2 * i));
+                k.ab[i] = *reinterpret_cast<const uint64_t*>(table + D / 2 + pair(j, 2 * i));
+                k.aa[i + 1] = *reinterpret_cast<const uint64_t*>(table + pair(j, 2 * i + 2));
+                k.ab[i + 1] = *reinterpret_cast<const uint64_t*>(table + D / 2 + pair(j, 2 * i + 2));
+            }
+            if constexpr (kWeights) {
+#pragma unroll
+                for (int i = 0; i < kP2; ++i) {
+                    k.bb[i] = f2_mul(k.aa[i], w->b[i]);
+                    k.ba[i] = f2_mul(f2_mul(k.ab[i], f2_pack(-1.0f, -1.0f)), w->a[i]);
+                    k.aa[i] = f2_mul(k.aa[i], w->a[i]);
+                    k.ab[i] = f2_mul(k.ab[i], w->b[i]);
+                }
+            }
+        }
+    }
+
+    // Turns a row; on: turning().  All 32 lanes call it; table and scratch (the
+    // lane group's D floats) are used in the HalvesOdd layout only.
+    static __device__ __forceinline__ void turn(Pairs& p, const Coef& k, unsigned on, int half, int j,
+                                                const float* table, float* scratch) {
+        if constexpr (kLayout == kRopeHalvesOdd) {
+            float x[kChunk], y[kChunk];
+            elements(p, x, y);
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                scratch[j * kChunk + i] = x[i];
+                scratch[(j + kLanes) * kChunk + i] = y[i];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                x[i] = turned(scratch, table, half, j * kChunk + i);
+                y[i] = turned(scratch, table, half, (j + kLanes) * kChunk + i);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kP2; ++i) {
+                p.a[i] = f2_pack(x[2 * i], x[2 * i + 1]);
+                p.b[i] = f2_pack(y[2 * i], y[2 * i + 1]);
+            }
+        } else {
+            const bool whole = 2 * half == D;
+#pragma unroll
+            for (int i = 0; i < kP2; ++i) {
+                // What does not turn takes nothing of its partner (0 * infinity would).
+                const uint64_t pa = whole ? p.a[i] : masked(p.a[i], on >> (2 * i));
+                const uint64_t pb = whole ? p.b[i] : masked(p.b[i], on >> (2 * i));
+                if constexpr (kWeights) {
+                    p.a[i] = f2_fma(pb, k.ab[i], f2_mul(p.a[i], k.aa[i]));
+                    p.b[i] = f2_fma(pa, k.ba[i], f2_mul(p.b[i], k.bb[i]));
+                } else {
+                    p.a[i] = f2_fma(pb, k.ab[i], f2_mul(p.a[i], k.aa[i]));
+                    p.b[i] = f2_sub(f2_mul(p.b[i], k.aa[i]), f2_mul(pa, k.ab[i]));
+                }
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void scale(Pairs& p, float f) {
+        const uint64_t ff = f2_pack(f, f);
+#pragma unroll
+        for (int i = 0; i < kP2; ++i) {
+            p.a[i] = f2_mul(p.a[i], ff);
+            p.b[i] = f2_mul(p.b[i], ff);
+        }
+    }
+    static __device__ __forceinline__ void multiply(Pairs& p, const Pairs& w) {
+#pragma unroll
+        for (int i = 0; i < kP2; ++i) {
+            p.a[i] = f2_mul(p.a[i], w.a[i]);
+            p.b[i] = f2_mul(p.b[i], w.b[i]);
+        }
+    }
+    // 1 / sqrt(mean(x^2) + eps) of a row.
+    static __device__ __forceinline__ float rms_scale(const Pairs& p, float eps) {
+        uint64_t ss = f2_mul(p.a[0], p.a[0]);
+        ss = f2_fma(p.b[0], p.b[0], ss);
+#pragma unroll
+        for (int i = 1; i < kP2; ++i) {
+            ss = f2_fma(p.a[i], p.a[i], ss);
+            ss = f2_fma(p.b[i], p.b[i], ss);
+        }
+        float u, v;
+        f2_unpack(ss, u, v);
+        u += v;
+#pragma unroll
+        for (int m = kLanes / 2; m > 0; m >>= 1) u += __shfl_xor_sync(0xffffffffu, u, m);
+        return rsqrtf(u * (1.0f / D) + eps);
+    }
+
+  private:
+    // The two floats, each 0 unless its bit of `on` is set.
+    static __device__ __forceinline__ uint64_t masked(uint64_t v, unsigned on) {
+        float lo, hi;
+        f2_unpack(v, lo, hi);
+        return f2_pack((on & 1u) ? lo : 0.0f, (on & 2u) ? hi : 0.0f);
+    }
+    static __device__ __forceinline__ float turned(const float* row, const float* table, int half, int i) {
+        if (i >= 2 * half) return row[i];
+        const int q = i < half ? i : i - half;
+        const float c = table[q], n = table[D / 2 + q];
+        return i < half ? fmaf(row[i + half], n, row[i] * c) : fmaf(row[i - half], -n, row[i] * c);
+    }
+};
+
+// A token's table: cos of every pair (1 for those that do not turn), then the
+// negated sines; entry i of D/2.
 template <int D>
-__device__ __forceinline__ float rope_rms_scale(const float (&x)[8], float eps) {
-    float ss = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-    for (int m = D / 16; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-    return rsqrtf(ss * (1.0f / D) + eps);
+__device__ __forceinline__ void rope_entry(const RopeTable& t, int i, int position, float* table) {
+    const float2 cs = i < t.half ? rope_cos_sin(t, i, position) : make_float2(1.0f, 0.0f);
+    table[i] = cs.x;
+    table[D / 2 + i] = -cs.y;
+}
+template <int D>
+__device__ __forceinline__ void rope_fill(const RopeTable& t, int position, int lane, float* table) {
+    for (int i = lane; i < D / 2; i += 32) rope_entry<D>(t, i, position, table);
+    __syncwarp();
 }
 
 }  // namespace attn
