@@ -284,7 +284,7 @@ __device__ __forceinline__ float fold(float4& a, const float4& e, float* keep) {
 }
 
 // One tile of a warp's ring: scores, weights, and the weighted V rows.
-template <int D, int HC>
+template <int D, int HC, bool kWholePages>
 __device__ __forceinline__ void unit_tile(const uint8_t* stage, int valid, int lane, UnitState<D, HC>& s) {
     constexpr int kR = HC / 8;
     const int g = lane >> 2, t = lane & 3;
@@ -305,32 +305,59 @@ __device__ __forceinline__ void unit_tile(const uint8_t* stage, int valid, int l
             w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
         }
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-            mma_f16(sc[n], s.qa[j][0], kR == 2 ? s.qa[j][1] : 0u, s.qa[j][kR], kR == 2 ? s.qa[j][kR + 1] : 0u,
-                    e4m3_to_f16x2(w[j] & 0xffffu), e4m3_to_f16x2(w[j] >> 16));
-    }
-    const float2 k2[2] = {*reinterpret_cast<const float2*>(ks + 2 * t),
-                          *reinterpret_cast<const float2*>(ks + 8 + 2 * t)};
-    const float2 v2[2] = {*reinterpret_cast<const float2*>(vs + 2 * t),
-                          *reinterpret_cast<const float2*>(vs + 8 + 2 * t)};
-    float x[kR][4], y[kR][4];  // exponents of p and of w
-    bool need = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float kk = (i & 1) ? k2[i >> 1].y : k2[i >> 1].x;
-        const float lift = __log2f((i & 1) ? v2[i >> 1].y : v2[i >> 1].x);
-        const bool seen = (i >> 1) * 8 + 2 * t + (i & 1) < valid;
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            x[r][i] = seen ? sc[i >> 1][2 * r + (i & 1)] * kk * s.qs[r] : -INFINITY;
-            y[r][i] = x[r][i] + lift;
-            need |= x[r][i] > s.m[r] + kSlack || y[r][i] > s.mv[r] + kSlack;
+        for (int j = 0; j < D / 16; ++j) {
+            uint32_t b0, b1;
+            e4m3_to_f16x4(w[j], b0, b1);
+            mma_f16(sc[n], s.qa[j][0], kR == 2 ? s.qa[j][1] : 0u, s.qa[j][kR], kR == 2 ? s.qa[j][kR + 1] : 0u, b0,
+                    b1);
         }
     }
+    // Factors and lifts (log2 of V's scales) of the lane's keys: one pair for a
+    // tile inside one page, else one for each key.
+    constexpr int kF = kWholePages ? 1 : 4;
+    float kk[kF], lift[kF];
+    if (kWholePages) {
+        kk[0] = ks[0];
+        lift[0] = __log2f(vs[0]);
+    } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const float2 k2 = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * t);
+            const float2 v2 = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * t);
+            kk[2 * n % kF] = k2.x;
+            kk[(2 * n + 1) % kF] = k2.y;
+            lift[2 * n % kF] = __log2f(v2.x);
+            lift[(2 * n + 1) % kF] = __log2f(v2.y);
+        }
+    }
+    float x[kR][4];  // exponents of p; those of w are x + lift
+    bool need = false;
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const float f = kk[0] * s.qs[r];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[r][i] = sc[i >> 1][2 * r + (i & 1)] * (kWholePages ? f : kk[i % kF] * s.qs[r]);
+    }
+    if (valid < kTile) {  // the unit's last tile
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if ((i >> 1) * 8 + 2 * t + (i & 1) >= valid) x[r][i] = -INFINITY;
+    }
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            need |= x[r][i] > fminf(s.m[r], s.mv[r] - lift[i % kF]) + kSlack;
     if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
-            const float m = fmaxf(s.m[r], row_max(x[r])), mv = fmaxf(s.mv[r], row_max(y[r]));
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = x[r][i] + lift[i % kF];
+            const float m = fmaxf(s.m[r], row_max(x[r])), mv = fmaxf(s.mv[r], row_max(y));
             s.l[r] *= s.m[r] == -INFINITY ? 0.0f : ex2_approx(s.m[r] - m);
             const float alpha = s.mv[r] == -INFINITY ? 0.0f : ex2_approx(s.mv[r] - mv);
             s.m[r] = m;
@@ -350,7 +377,7 @@ __device__ __forceinline__ void unit_tile(const uint8_t* stage, int valid, int l
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             s.l[r] += ex2_approx(x[r][i] - m);
-            w[i] = ex2_approx(y[r][i] - mv);
+            w[i] = ex2_approx(x[r][i] + (lift[i % kF] - mv));
         }
         pb[r][0] = pack_f16x2(w[0], w[1]);
         pb[r][1] = pack_f16x2(w[2], w[3]);
@@ -365,8 +392,9 @@ __device__ __forceinline__ void unit_tile(const uint8_t* stage, int valid, int l
             // Bytes 2 half, 2 half + 1 of two keys' words: (k0, k1) of one column, then of the next.
             const uint32_t sel = half ? 0x7362u : 0x5140u;
             const uint32_t lo = __byte_perm(vw[0][i], vw[1][i], sel), hi = __byte_perm(vw[2][i], vw[3][i], sel);
-            const uint32_t a0 = e4m3_to_f16x2(lo & 0xffffu), a1 = e4m3_to_f16x2(lo >> 16);
-            const uint32_t a2 = e4m3_to_f16x2(hi & 0xffffu), a3 = e4m3_to_f16x2(hi >> 16);
+            uint32_t a0, a1, a2, a3;
+            e4m3_to_f16x4(lo, a0, a1);
+            e4m3_to_f16x4(hi, a2, a3);
 #pragma unroll
             for (int r = 0; r < kR; ++r) mma_f16(s.o[r][2 * i + half], a0, a1, a2, a3, pb[r][0], pb[r][1]);
         }
@@ -449,34 +477,59 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
             }
         };
         look_up();
+        // Where a lane's copies go in a stage: row r0 + i * kRowsPer, chunk col.
+        constexpr int kPerRow = D / 16, kRowsPer = 32 / kPerRow;
+        const int r0 = lane / kPerRow, col = lane % kPerRow;
+        int put[kTile / kRowsPer];
+#pragma unroll
+        for (int i = 0; i < kTile / kRowsPer; ++i)
+            put[i] = (r0 + i * kRowsPer) * D + chunk_at<D>(r0 + i * kRowsPer, col) * 16;
+        const int64_t to_v = static_cast<int64_t>(p.Hkv) * p.page.size * D;
+        const uint32_t ring32 = smem_u32(ring);
+        uint32_t fill = ring32;  // the stage copied into next
         auto issue = [&]() {
             if (loaded < count) {
-                const uint32_t dst = smem_u32(ring + (loaded % L::kStages) * L::kStage);
                 if (id < 0 || id >= p.num_blocks) {
                     atomicOr(p.status, ATTN_DEV_BAD_INPUT);
                     id = 0;
                 }
-                const int hkv = lc.unit / p.chunks;
+                const int hkv = p.chunks == 1 ? lc.unit : lc.unit / p.chunks;
                 const int valid = min(kTile, lc.len - lc.tile * kTile);
-                constexpr int kPerRow = D / 16, kRowsPer = 32 / kPerRow;
-                const int r0 = lane / kPerRow, col = lane % kPerRow;
-                const int64_t to_v = static_cast<int64_t>(p.Hkv) * p.page.size * D;
-                // Lanes 0 .. 15: K's scales, 16 .. 31: V's.
-                copy4(dst + 2 * kTile * D + lane * 4,
-                      p.scales + (static_cast<int64_t>(id) * 2 + (lane >> 4)) * p.Hkv + hkv,
-                      (lane & 15) < valid ? 4 : 0);
+                const int64_t block = static_cast<int64_t>(id) * 2 * p.Hkv + hkv;  // of K; V's is Hkv further
+                // Lanes 0 .. 15: K's scales, 16 .. 31: V's (a tile in one page: lanes 0 and 16).
+                if (kWholePages ? (lane & 15) == 0 : true)
+                    copy4(fill + 2 * kTile * D + lane * 4, p.scales + block + (lane >> 4) * p.Hkv,
+                          (lane & 15) < valid ? 4 : 0);
+                if (kWholePages) {  // one run of rows
+                    const uint8_t* src = p.kv + (block * p.page.size + row) * D + lane * 16;
+                    if (valid == kTile) {
 #pragma unroll
-                for (int i = 0; i < kTile / kRowsPer; ++i) {
-                    const int r = i * kRowsPer + r0;
-                    const int rid = kWholePages ? id : __shfl_sync(0xffffffffu, id, r);
-                    const int rrow = kWholePages ? row + (r < valid ? r : 0) : __shfl_sync(0xffffffffu, row, r);
-                    const uint8_t* src =
-                        p.kv + ((static_cast<int64_t>(rid) * 2 * p.Hkv + hkv) * p.page.size + rrow) * D + col * 16;
-                    const int bytes = r < valid ? 16 : 0;
-                    const uint32_t at = dst + r * D + chunk_at<D>(r, col) * 16;
-                    copy16(at, src, bytes);
-                    copy16(at + kTile * D, src + to_v, bytes);
+                        for (int i = 0; i < kTile / kRowsPer; ++i) {
+                            copy16(fill + put[i], src + i * 512, 16);
+                            copy16(fill + kTile * D + put[i], src + to_v + i * 512, 16);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kTile / kRowsPer; ++i) {
+                            const bool in = r0 + i * kRowsPer < valid;
+                            const uint8_t* at = in ? src + i * 512 : p.kv;
+                            copy16(fill + put[i], at, in ? 16 : 0);
+                            copy16(fill + kTile * D + put[i], in ? at + to_v : p.kv, in ? 16 : 0);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kTile / kRowsPer; ++i) {
+                        const int r = r0 + i * kRowsPer;
+                        const int rid = __shfl_sync(0xffffffffu, id, r), rrow = __shfl_sync(0xffffffffu, row, r);
+                        const uint8_t* src = p.kv +
+                            ((static_cast<int64_t>(rid) * 2 * p.Hkv + hkv) * p.page.size + rrow) * D + col * 16;
+                        copy16(fill + put[i], src, r < valid ? 16 : 0);
+                        copy16(fill + kTile * D + put[i], src + to_v, r < valid ? 16 : 0);
+                    }
                 }
+                fill += L::kStage;
+                if (fill == ring32 + L::kStages * L::kStage) fill = ring32;
                 if (++loaded < count) {
                     cursor_next(p, cum, lc);
                     look_up();
@@ -488,6 +541,7 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
         for (int i = 0; i < L::kStages - 1; ++i) issue();
 
         UnitState<D, HC> s;
+        const uint8_t* stage = ring;
         int pieces = 0;
         int from = cc.tile;  // the unit's first tile of this warp
         unit_begin<D, HC, kF16>(p, cc, lane, s);
@@ -495,7 +549,9 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
             asm volatile("cp.async.wait_group %0;" :: "n"(L::kStages - 2) : "memory");
             __syncwarp();  // the tile is there, and the stage filled next has been read
             issue();
-            unit_tile<D, HC>(ring + (n % L::kStages) * L::kStage, min(kTile, cc.len - cc.tile * kTile), lane, s);
+            unit_tile<D, HC, kWholePages>(stage, min(kTile, cc.len - cc.tile * kTile), lane, s);
+            stage += L::kStage;
+            if (stage == ring + L::kStages * L::kStage) stage = ring;
             const bool unit_done = cc.tile + 1 == cc.tiles;
             if (!unit_done && n + 1 < count) {
                 ++cc.tile;

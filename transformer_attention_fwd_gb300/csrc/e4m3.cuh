@@ -23,18 +23,18 @@ __device__ __forceinline__ uint32_t e4m3_pack2(float a, float b) {
 __device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float d) {
     return e4m3_pack2(a, b) | (e4m3_pack2(c, d) << 16);
 }
-// Two codes (the low 16 bits) to two fp16 values: exact.
-__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t codes) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-        : "=r"(r) : "r"(codes));
-    return r;
+// Four codes to two pairs of fp16 values (lower two codes, upper two): exact.
+__device__ __forceinline__ void e4m3_to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(codes));
 }
 
 // Four codes times a ratio, rounded to codes again (exact for a power of two,
 // but for results under 2^-6).
 __device__ __forceinline__ uint32_t e4m3_rescale(uint32_t codes, float ratio) {
-    const uint32_t lo = e4m3_to_f16x2(codes & 0xffffu), hi = e4m3_to_f16x2(codes >> 16);
+    uint32_t lo, hi;
+    e4m3_to_f16x4(codes, lo, hi);
     return e4m3_pack4(f16_lo_to_f32(lo) * ratio, f16_hi_to_f32(lo) * ratio,
                       f16_lo_to_f32(hi) * ratio, f16_hi_to_f32(hi) * ratio);
 }
