@@ -357,7 +357,8 @@ typedef struct {
  * attn_rope -- rotary positions of the query heads (and, k not NULL, of the key
  * heads) of B x T tokens in one launch.  positions: [B, T] int32, device.  D 64
  * or 128; x and y in dtype (ATTN_F32, ATTN_BF16 or ATTN_F16), the arithmetic in
- * fp32, one rounding at the end.  B * T = 0 launches nothing.
+ * fp32, one rounding at the end.  B * T = 0 launches nothing; it must fit in 31
+ * bits.
  */
 attn_status attn_rope(const attn_rows* q, const attn_rows* k, const int* positions, int B,
                       int T, int D, const attn_rotation* rotation, attn_dtype dtype,

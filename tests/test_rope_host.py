@@ -120,6 +120,7 @@ def _rope(a, q=None, k=None, positions=FAKE, B=1, T=3, D=64, rot=None, dtype=1, 
     (dict(dtype=3), 1, "dtype"),
     (dict(D=96), 2, "D=96"),
     (dict(B=-1), 1, ">= 0"),
+    (dict(B=1 << 16, T=1 << 15), 1, "31 bits"),
     (dict(positions=None), 1, "positions"),
     (dict(positions=FAKE + 2), 1, "positions"),
     (dict(rot=dict(rot=65)), 1, "rot_dim"),
@@ -177,6 +178,7 @@ def _append(a, e4m3, q=None, k="k", v="v", cu=FAKE, lens=FAKE, positions=None, t
     (dict(dtype=7), 1, "dtype"),
     (dict(B=0), 1, ">= 1"),
     (dict(total=-1), 1, ">= 0"),
+    (dict(total=2 ** 31 - 1), 1, "total"),
     (dict(page=0), 1, ">= 1"),
     (dict(blocks=0), 1, ">= 1"),
     (dict(D=80), 2, "D=80"),

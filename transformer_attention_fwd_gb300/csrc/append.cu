@@ -22,14 +22,14 @@ append_kernel(const AppendParams p) {
     using R = Rope<E, D, kLayout>;
     __shared__ __align__(16) float s_table[kAppendWarps][D];
     __shared__ float s_scratch[R::kScratch ? kAppendWarps * R::kScratch : 1];
-    if (blockIdx.x == gridDim.x - 1) append_report(p);
-    append_rows<E, D, kLayout>(p, static_cast<long long>(blockIdx.x) * kAppendWarps + threadIdx.x / 32,
-                               s_table[threadIdx.x / 32],
-                               s_scratch + (R::kScratch ? threadIdx.x / 32 * R::kScratch : 0));
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0) append_report(p);
+    const int warp = threadIdx.x / 32;
+    append_rows<E, D, kLayout>(p, static_cast<int>(blockIdx.x) * kAppendWarps + warp, blockIdx.y, s_table[warp],
+                               s_scratch + warp * R::kScratch);
 }
 
 template <typename E, int D>
-cudaError_t launch_layout(const AppendParams& p, int layout, unsigned blocks, cudaStream_t st) {
+cudaError_t launch_layout(const AppendParams& p, int layout, dim3 blocks, cudaStream_t st) {
     switch (layout) {
         case kRopeAdjacent: append_kernel<E, D, kRopeAdjacent><<<blocks, kAppendWarps * 32, 0, st>>>(p); break;
         case kRopeHalves: append_kernel<E, D, kRopeHalves><<<blocks, kAppendWarps * 32, 0, st>>>(p); break;
@@ -39,6 +39,13 @@ cudaError_t launch_layout(const AppendParams& p, int layout, unsigned blocks, cu
 }
 
 }  // namespace
+
+// As in rope.cu: a token's steps are cut while 32 warps per SM are not there.
+int append_segments(AppendParams& p, int num_sms) {
+    const int segs = std::max(1, std::min(p.steps, num_sms * 32 / p.total));
+    p.per_seg = (p.steps + segs - 1) / segs;
+    return (p.steps + p.per_seg - 1) / p.per_seg;
+}
 
 AppendParams append_params(const AppendShape& s, const RopeShape& r, const RopeRows* q,
                            const RopeRows& k, const RopeRows& v, const LaunchEnv& env) {
@@ -70,15 +77,9 @@ cudaError_t launch_append_paged(const AppendShape& s, const RopeShape& r, const 
     p.q_steps = (p.q.heads + rows - 1) / rows;
     p.kv_steps = (k.heads + rows - 1) / rows;
     p.steps = p.q_steps + 2 * p.kv_steps;
-    // As in rope.cu: a token's steps are cut while 32 warps per SM are not there.
-    const long long want = static_cast<long long>(env.num_sms) * 32;
-    p.segs = static_cast<int>(std::max<long long>(1, std::min<long long>(p.steps, want / s.total)));
-    p.per_seg = (p.steps + p.segs - 1) / p.segs;
-    p.segs = (p.steps + p.per_seg - 1) / p.per_seg;
-    p.warps = static_cast<long long>(s.total) * p.segs;
-    const long long blocks = (p.warps + kAppendWarps - 1) / kAppendWarps;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const unsigned g = static_cast<unsigned>(blocks);
+    const int segs = append_segments(p, env.num_sms);
+    if (segs > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 g((s.total + kAppendWarps - 1) / kAppendWarps, segs);
     const int layout = rope_layout(r.rot_dim, r.interleaved, 2);
     cudaError_t e;
     if (r.dtype == ATTN_F16)
@@ -87,7 +88,7 @@ cudaError_t launch_append_paged(const AppendShape& s, const RopeShape& r, const 
     else
         e = r.D == 64 ? launch_layout<RopeBf16, 64>(p, layout, g, env.stream)
                       : launch_layout<RopeBf16, 128>(p, layout, g, env.stream);
-    if (grid_out) *grid_out = static_cast<int>(g);
+    if (grid_out) *grid_out = static_cast<int>(g.x * g.y);
     if (kernels_launched) *kernels_launched = 1;
     return e;
 }

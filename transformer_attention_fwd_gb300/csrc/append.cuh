@@ -11,6 +11,11 @@
 
 namespace attn {
 
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
 constexpr int kAppendWarps = 4;
 constexpr int kAppendUnroll = 2;  // steps a lane has in flight
 
@@ -26,10 +31,9 @@ struct AppendParams {
     RopeTable table;
     PageDivider page;
     int B, total, max_pages, num_blocks;
-    long long warps;  // tokens * segs; 8-bit cache: of the query rows
-    int q_steps, kv_steps, steps, segs, per_seg;  // a token's steps, cut into segments
+    int q_steps, kv_steps, steps, per_seg;  // a token's steps; segments of per_seg
     float k_limit;  // 8-bit: largest |K| element a scale of 1 takes
-    unsigned items, splits;  // 8-bit: blocks of the K and V pages (see append_e4m3.cu)
+    unsigned items, splits, segs;  // 8-bit: blocks of the K and V pages, segments (see append_e4m3.cu)
 };
 
 // The last i in 0 .. n - 1 with value(i) <= target, for non-decreasing values
@@ -90,84 +94,88 @@ __device__ __forceinline__ int append_block(const AppendParams& p, int b, int pa
     return -1;
 }
 
-// A warp's segment w of the steps of a token: its query heads into q.y, its
-// key heads into the cache and k.y, its values into the cache.  With kv_steps =
-// 0 the query heads alone.  table: D floats of shared memory, scratch:
+// Segment `seg` of a token's steps, by one warp: its query heads into q.y, its key
+// heads into the cache and k.y, its values into the cache.  With kv_steps = 0 the
+// query heads alone.  table: D floats of shared memory, scratch:
 // Rope<...>::kScratch.
 template <typename E, int D, int kLayout>
-__device__ __forceinline__ void append_rows(const AppendParams& p, long long w, float* table, float* scratch) {
+__device__ __forceinline__ void append_rows(const AppendParams& p, int token, int seg, float* table, float* scratch) {
     using R = Rope<E, D, kLayout>;
+    if (token >= p.total) return;
     const int lane = threadIdx.x % 32;
     const int j = lane % R::kLanes, grp = lane / R::kLanes;
-    if (w >= p.warps) return;
-    const int token = static_cast<int>(w / p.segs);
-    const int seg = static_cast<int>(w - static_cast<long long>(token) * p.segs);
     const int half = p.table.half;
     const unsigned on = R::turning(half, j);
-    const long long at0 = R::first(j, half) * E::kBytes, at1 = R::second(j, half) * E::kBytes;
-    const uint8_t* xq = static_cast<const uint8_t*>(p.q.x) + token * p.q.x_token * E::kBytes;
-    const uint8_t* xk = static_cast<const uint8_t*>(p.k.x) + token * p.k.x_token * E::kBytes;
-    const uint8_t* xv = static_cast<const uint8_t*>(p.v.x) + token * p.v.x_token * E::kBytes;
+    const int at0 = R::first(j, half) * E::kBytes, to1 = R::second(j, half) * E::kBytes - at0;
     if (R::kScratch) scratch += grp * D;
 
-    // Steps of a token: its query heads, then its key heads, then its values.
     const int s0 = seg * p.per_seg, s1 = min(p.steps, s0 + p.per_seg);
     const int k_end = p.q_steps + p.kv_steps;
     typename R::Coef coef;
     uint8_t* cache = nullptr;  // the slot's K row of head 0; null: the page is left out
-    const long long ch = static_cast<long long>(p.page.size) * D * E::kBytes, to_v = p.k.heads * ch;
-    for (int s = s0; s < s1; s += kAppendUnroll) {
-        typename R::Raw raw[kAppendUnroll];
-#pragma unroll
-        for (int u = 0; u < kAppendUnroll; ++u) {
-            const int st = s + u;
-            const int kind = st < p.q_steps ? 0 : (st < k_end ? 1 : 2);
-            const int head = (st - (kind == 0 ? 0 : (kind == 1 ? p.q_steps : k_end))) * R::kRows + grp;
-            const uint8_t* x = kind == 0 ? xq + head * p.q.x_head * E::kBytes
-                                         : (kind == 1 ? xk + head * p.k.x_head * E::kBytes
-                                                      : xv + head * p.v.x_head * E::kBytes);
-            raw[u] = st < s1 && head < (kind == 0 ? p.q.heads : p.k.heads) ? R::load(x + at0, x + at1) : R::zero();
+    const long long head_bytes = static_cast<long long>(p.page.size) * D * E::kBytes;
+    bool found = false, mine = true;
+    // The token's request, coefficients and place in the cache, behind the first
+    // loads; false if no request has it.
+    auto find = [&]() {
+        found = true;
+        int b, slot;
+        mine = append_slot(p, token, lane, &b, &slot);
+        if (!mine) return;
+        if (s0 < k_end) {
+            rope_fill<D>(p.table, p.positions ? p.positions[token] : slot, lane, table);
+            R::coefficients(table, j, coef);
         }
-        if (s == s0) {  // behind the first loads
-            int b, slot;
-            if (!append_slot(p, token, lane, &b, &slot)) return;  // the whole warp
-            if (s0 < k_end) {
-                rope_fill<D>(p.table, p.positions ? p.positions[token] : slot, lane, table);
-                R::coefficients(table, j, coef);
-            }
-            if (s1 > p.q_steps) {
-                int in_page;
-                const int id = append_block(p, b, p.page.split(slot, &in_page));
-                if (id >= 0)
-                    cache = p.cache +
-                            (static_cast<int64_t>(id) * 2 * p.k.heads * p.page.size + in_page) * D * E::kBytes;
-            }
+        if (s1 > p.q_steps) {
+            int in_page;
+            const int id = append_block(p, b, p.page.split(slot, &in_page));
+            if (id >= 0)
+                cache = p.cache + (static_cast<int64_t>(id) * 2 * p.k.heads * p.page.size + in_page) * D * E::kBytes;
         }
+    };
+    // Heads h0 + grp, h0 + grp + kRows, .. below h1: of q (kind 0), k (1), v (2).
+    auto run = [&](auto kind_tag, const RopeRows& r, int h0, int h1) {
+        constexpr int kKind = decltype(kind_tag)::value;
+        const long long xs = R::kRows * r.x_head * E::kBytes, ys = R::kRows * r.y_head * E::kBytes;
+        const long long cs = R::kRows * head_bytes;
+        const uint8_t* x = static_cast<const uint8_t*>(r.x) + at0 + (token * r.x_token + (h0 + grp) * r.x_head) * E::kBytes;
+        uint8_t* y = static_cast<uint8_t*>(r.y) + at0 + (token * r.y_token + (h0 + grp) * r.y_head) * E::kBytes;
+        long long c = at0 + (h0 + grp + (kKind == 2 ? p.k.heads : 0)) * head_bytes;
+        for (int h = h0 + grp; h - grp < h1; h += kAppendUnroll * R::kRows) {
+            typename R::Raw raw[kAppendUnroll];
 #pragma unroll
-        for (int u = 0; u < kAppendUnroll; ++u) {
-            const int st = s + u;
-            if (st >= s1) break;  // the same for the whole warp
-            const int kind = st < p.q_steps ? 0 : (st < k_end ? 1 : 2);
-            const int head = (st - (kind == 0 ? 0 : (kind == 1 ? p.q_steps : k_end))) * R::kRows + grp;
-            const bool in = head < (kind == 0 ? p.q.heads : p.k.heads);
-            uint8_t* row = cache + head * ch;
-            if (kind == 2) {
-                if (in && cache) {
-                    *reinterpret_cast<uint4*>(row + to_v + at0) = raw[u].c0;
-                    *reinterpret_cast<uint4*>(row + to_v + at1) = raw[u].c1;
+            for (int u = 0; u < kAppendUnroll; ++u) {
+                raw[u] = h + u * R::kRows < h1 ? R::load(x, x + to1) : R::zero();
+                x += xs;
+            }
+            if (!found) find();
+            if (!mine) return;
+#pragma unroll
+            for (int u = 0; u < kAppendUnroll; ++u) {
+                if (u > 0 && h - grp + u * R::kRows >= h1) break;  // the same for the whole warp
+                const bool in = h + u * R::kRows < h1;
+                if constexpr (kKind == 2) {
+                    if (in && cache) {
+                        *reinterpret_cast<uint4*>(cache + c) = raw[u].c0;
+                        *reinterpret_cast<uint4*>(cache + c + to1) = raw[u].c1;
+                    }
+                } else {
+                    typename R::Pairs v = R::unpack(raw[u]);
+                    R::turn(v, coef, on, half, j, table, scratch);
+                    if (in && r.y) R::store(y, y + to1, v);
+                    if (kKind == 1 && in && cache) R::store(cache + c, cache + c + to1, v);
                 }
-                continue;
+                y += ys;
+                c += cs;
             }
-            typename R::Pairs v = R::unpack(raw[u]);
-            R::turn(v, coef, on, half, j, table, scratch);
-            const RopeRows& r = kind == 0 ? p.q : p.k;
-            if (in && r.y) {
-                uint8_t* y = static_cast<uint8_t*>(r.y) + (token * r.y_token + head * r.y_head) * E::kBytes;
-                R::store(y + at0, y + at1, v);
-            }
-            if (in && kind == 1 && cache) R::store(row + at0, row + at1, v);
         }
-    }
+    };
+    if (s0 < p.q_steps) run(Int<0>{}, p.q, s0 * R::kRows, min(p.q.heads, s1 * R::kRows));
+    if (p.kv_steps == 0) return;
+    if (mine && s0 < k_end && s1 > p.q_steps)
+        run(Int<1>{}, p.k, max(0, s0 - p.q_steps) * R::kRows, min(p.k.heads, (s1 - p.q_steps) * R::kRows));
+    if (mine && s1 > k_end)
+        run(Int<2>{}, p.v, max(0, s0 - k_end) * R::kRows, min(p.v.heads, (s1 - k_end) * R::kRows));
 }
 
 }  // namespace attn

@@ -148,7 +148,8 @@ append_e4m3_kernel(const AppendParams p) {
     const unsigned kv_blocks = p.items * p.splits;
     if (blockIdx.x == gridDim.x - 1) append_report(p);
     if (blockIdx.x >= kv_blocks) {
-        append_rows<E, D, kLayout>(p, static_cast<long long>(blockIdx.x - kv_blocks) * kPageWarps + warp,
+        const unsigned qb = blockIdx.x - kv_blocks;
+        append_rows<E, D, kLayout>(p, static_cast<int>(qb / p.segs) * kPageWarps + warp, static_cast<int>(qb % p.segs),
                                    s_table[warp], scratch);
         return;
     }
@@ -291,14 +292,9 @@ cudaError_t launch_append_paged_e4m3(const AppendShape& s, const RopeShape& r, c
     // The query heads' steps as in append.cu.
     const int step_rows = 32 * 16 / r.D;
     p.q_steps = p.steps = (p.q.heads + step_rows - 1) / step_rows;
-    if (p.steps > 0) {
-        const long long want = static_cast<long long>(env.num_sms) * 32;
-        p.segs = static_cast<int>(std::max<long long>(1, std::min<long long>(p.steps, want / s.total)));
-        p.per_seg = (p.steps + p.segs - 1) / p.segs;
-        p.segs = (p.steps + p.per_seg - 1) / p.per_seg;
-        p.warps = static_cast<long long>(s.total) * p.segs;
-    }
-    const long long blocks = items * p.splits + (p.warps + kPageWarps - 1) / kPageWarps;
+    p.segs = p.steps > 0 ? append_segments(p, env.num_sms) : 0;
+    const long long blocks =
+        items * p.splits + static_cast<long long>((s.total + kPageWarps - 1) / kPageWarps) * p.segs;
     if (items > 0x7fffffffLL || blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     p.items = static_cast<unsigned>(items);
     const unsigned g = static_cast<unsigned>(blocks);

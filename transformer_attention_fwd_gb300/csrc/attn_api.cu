@@ -1055,6 +1055,7 @@ attn_status run_rope(const attn_rows* q, const attn_rows* k, const void* qw, con
     if (!aligned(qw, 16) || !aligned(kw, 16))
         return fail(ATTN_ERR_INVALID_ARG, "q_weight and k_weight must be 16-byte aligned");
     const long long tokens = static_cast<long long>(B) * T;
+    if (tokens > 0x7fffffffLL) return fail(ATTN_ERR_INVALID_ARG, "B*T must fit in 31 bits");
     if (tokens == 0) {
         record_launch(0, 0, 0);
         return ok();
@@ -1096,6 +1097,7 @@ attn_status run_append(bool e4m3, const attn_rows* q, const attn_rows* k, const 
         return fail(ATTN_ERR_INVALID_ARG, "max_pages_per_seq*page_size must be below 2^31 - 1024");
     if (static_cast<long long>(B) * max_pages_per_seq > 0x7fffffffLL)
         return fail(ATTN_ERR_INVALID_ARG, "B*max_pages_per_seq must fit in 31 bits");
+    if (total > 0x7fffffff - 1024) return fail(ATTN_ERR_INVALID_ARG, "total must be below 2^31 - 1024");
     const attn_rotation plain{nullptr, 0, 0, 1.0f};
     const attn_rotation& rot = rotation ? *rotation : plain;
     attn_status st = validate_rotation(&rot, D);

@@ -176,6 +176,7 @@ struct AppendShape {
 struct AppendParams;
 AppendParams append_params(const AppendShape& s, const RopeShape& r, const RopeRows* q,
                            const RopeRows& k, const RopeRows& v, const LaunchEnv& env);
+int append_segments(AppendParams& p, int num_sms);  // sets p.per_seg from p.steps and p.total
 // q may be null; k.y may be null (no copy of the rotated keys).
 cudaError_t launch_append_paged(const AppendShape& s, const RopeShape& r, const RopeRows* q,
                                 const RopeRows& k, const RopeRows& v, const LaunchEnv& env,

@@ -41,7 +41,6 @@
 namespace attn {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kTile = 16;          // keys of a tile
 constexpr int kMaxPrefixB = 1024;  // requests whose tile counts a CTA sums itself
 constexpr float kSlack = 6.0f;
@@ -67,9 +66,10 @@ struct E4m3Params {
 
 template <int D, int HC>
 struct E4m3Layout {
+    static constexpr int kWarps = HC == 8 ? 12 : 8;
     static constexpr int kStage = 2 * kTile * D + 2 * kTile * 4;  // K rows, V rows, scales
     static constexpr int kPiece = HC * D * 4;
-    static constexpr int kStages = D == 128 ? (HC == 8 ? 5 : 4) : 8;
+    static constexpr int kStages = D == 128 ? (HC == 8 ? 3 : 4) : (HC == 8 ? 6 : 8);
     static constexpr int kPieceOff = kWarps * kStages * kStage;
     static constexpr int kMlOff = kPieceOff + kWarps * kPiece;  // [warp][2][HC] float4
     static constexpr int kMetaOff = kMlOff + kWarps * 2 * HC * 16;
@@ -153,9 +153,9 @@ __global__ void __launch_bounds__(1024) e4m3_prefix_kernel(const E4m3Params p) {
     tile_prefix(p, p.cum, scan, true);
 }
 
-__device__ __forceinline__ long long slice_tiles(long long total, int grid) {
+__device__ __forceinline__ long long slice_tiles(long long total, int grid, int warps) {
     const long long per = (total + grid - 1) / grid;
-    return per < kWarps ? kWarps : per;  // at least one tile a warp
+    return per < warps ? warps : per;  // at least one tile a warp
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -271,16 +271,20 @@ __device__ __forceinline__ float row_max(const float (&x)[4]) {
 // Factor from sum w v to O: 2^(mv - m) / l.
 __device__ __forceinline__ float out_factor(float m, float l, float mv) { return ex2_approx(mv - m) / l; }
 
-// {m, sum, mv} of pieces folded into one: returns what O's terms of the new
-// piece are multiplied by, and in *keep what the old ones are.
-__device__ __forceinline__ float fold(float4& a, const float4& e, float* keep) {
-    const float m = fmaxf(a.x, e.x), mv = fmaxf(a.z, e.z);
-    a.y = (a.x == -INFINITY ? 0.0f : a.y * ex2_approx(a.x - m)) + (e.x == -INFINITY ? 0.0f : e.y * ex2_approx(e.x - m));
-    *keep = a.z == -INFINITY ? 0.0f : ex2_approx(a.z - mv);
-    const float w = e.z == -INFINITY ? 0.0f : ex2_approx(e.z - mv);
-    a.x = m;
-    a.z = mv;
-    return w;
+// {m, sum, mv} of a warp's 32 pieces (m = mv = -infinity, sum = 0 where there is
+// none): the common references {m, mv}, and the sum relative to m.
+__device__ __forceinline__ float2 merge_weights(const float4& e, float* sum) {
+    float m = e.x, mv = e.z;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+    }
+    float l = e.x == -INFINITY ? 0.0f : e.y * ex2_approx(e.x - m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    *sum = l;
+    return make_float2(m, mv);
 }
 
 // One tile of a warp's ring: scores, weights, and the weighted V rows.
@@ -417,9 +421,10 @@ struct PieceMeta {
 };
 
 template <int D, int HC, bool kF16, bool kWholePages>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(E4m3Layout<D, HC>::kWarps * 32, 1)
 decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
     using L = E4m3Layout<D, HC>;
+    constexpr int kWarps = L::kWarps;
     constexpr int kR = HC / 8, kCols = D / 8;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -448,7 +453,7 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
     }
 
     const long long total = cum[p.B] * U;
-    const long long per = slice_tiles(total, grid);
+    const long long per = slice_tiles(total, grid, kWarps);
     const long long v0 = per * blockIdx.x, v1 = v0 + per < total ? v0 + per : total;
     if (v0 >= total) return;
     if (threadIdx.x == 0) {
@@ -618,63 +623,73 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
     }
     __syncthreads();
 
-    // Merge the pieces of one unit: by the warp that has its first one.
-    for (int slot = 0; slot < 2; ++slot) {
-        const PieceMeta mine = meta[2 * warp + slot];
-        if (mine.unit < 0) continue;
-        if (slot == 0 && warp > 0) {
-            const PieceMeta* before = &meta[2 * (warp - 1)];
-            if ((before[1].unit >= 0 ? before[1].unit : before[0].unit) == mine.unit) continue;
+    // Merge the pieces of each unit that is not one warp's: every warp takes some
+    // of its heads.
+    for (int from = 0; from < 2 * kWarps; ++from) {
+        const PieceMeta head_piece = meta[from];
+        const int w0 = from >> 1;
+        if (head_piece.unit < 0) continue;
+        if ((from & 1) == 0 && w0 > 0) {  // the unit's first piece here?
+            const PieceMeta* before = &meta[2 * (w0 - 1)];
+            if ((before[1].unit >= 0 ? before[1].unit : before[0].unit) == head_piece.unit) continue;
         }
-        int last = warp;  // last warp that has a piece of it
-        while (last + 1 < kWarps && meta[2 * (last + 1)].unit == mine.unit) ++last;
-        const bool ends = last == warp ? mine.ends : meta[2 * last].ends;
-        const int b = static_cast<int>(mine.unit / U), unit = static_cast<int>(mine.unit - static_cast<long long>(b) * U);
+        int w1 = w0;  // last warp that has a piece of it, in its first slot unless it is w0
+        while (w1 + 1 < kWarps && meta[2 * (w1 + 1)].unit == head_piece.unit) ++w1;
+        const bool ends = w1 == w0 ? head_piece.ends : meta[2 * w1].ends;
+        const int n = w1 - w0 + 1;
+        const int b = static_cast<int>(head_piece.unit / U);
+        const int unit = static_cast<int>(head_piece.unit - static_cast<long long>(b) * U);
         const int hkv = unit / p.chunks, chunk = unit - hkv * p.chunks;
         const int heads = min(HC, p.group - chunk * HC);
         const int64_t row0 = static_cast<int64_t>(b) * p.Hq + hkv * p.group + chunk * HC;
-        const bool whole = mine.begins && ends;
-        const int64_t ws = 2ll * blockIdx.x + (mine.begins == 2 ? 1 : 0);
-        for (int h = 0; h < heads; ++h) {
-            float4 sum = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+        const bool whole = head_piece.begins && ends;
+        const int64_t ws = 2ll * blockIdx.x + (head_piece.begins == 2 ? 1 : 0);
+        for (int h = warp; h < heads; h += kWarps) {
+            // Lane i: the i-th piece's references, sum and weight.
+            const float4 e = lane < n ? ml[(lane == 0 ? from : 2 * (w0 + lane)) * HC + h]
+                                      : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+            float l;
+            const float2 m = merge_weights(e, &l);
+            float weight = e.z == -INFINITY ? 0.0f : ex2_approx(e.z - m.y);
             float acc[D / 32];
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
-            for (int w = warp; w <= last; ++w) {
-                const int sl = w == warp ? slot : 0;
-                float keep;
-                const float wt = fold(sum, ml[(2 * w + sl) * HC + h], &keep);
+            for (int k = 0; k < n; ++k) {
+                const float wt = __shfl_sync(0xffffffffu, weight, k);
                 const float* piece = reinterpret_cast<const float*>(
-                    sl == 0 ? smem + L::kPieceOff + w * L::kPiece : smem + w * L::kStages * L::kStage);
+                    k == 0 && (from & 1) ? smem + w0 * L::kStages * L::kStage : smem + L::kPieceOff + (w0 + k) * L::kPiece);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(piece[h * D + i * 32 + lane], wt, acc[i] * keep);
+                for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(piece[h * D + i * 32 + lane], wt, acc[i]);
             }
             if (whole) {
-                const float f = out_factor(sum.x, sum.y, sum.z);
+                const float f = out_factor(m.x, l, m.y);
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i)
                     p.o[(row0 + h) * D + i * 32 + lane] =
                         static_cast<uint16_t>(Elem16<kF16>::pack(acc[i] * f, 0.0f) & 0xffffu);
-                if (p.lse && lane == 0) p.lse[row0 + h] = (sum.x + __log2f(sum.y)) * kLn2;
+                if (p.lse && lane == 0) p.lse[row0 + h] = (m.x + __log2f(l)) * kLn2;
             } else {
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) p.ws_o[(ws * HC + h) * D + i * 32 + lane] = acc[i];
-                if (lane == 0) p.ws_ml[ws * HC + h] = sum;
+                if (lane == 0) p.ws_ml[ws * HC + h] = make_float4(m.x, l, m.y, 0.0f);
             }
         }
     }
 }
 
-// Merge the pieces of the units that CTA boundaries cut: block j takes the
-// boundary between the slices of CTAs j and j + 1, if it is the unit's first
-// one; one thread per head and column.  Launched with programmatic stream
-// serialisation: it waits for the kernel before it reads.
+// Merge the pieces of the units that CTA boundaries cut: block (j, h) takes head
+// h of the unit that the boundary between the slices of CTAs j and j + 1 cuts,
+// if it is the unit's first one.  A unit over many CTAs has that many pieces:
+// kCombineRows of them are added up side by side.  Launched with programmatic
+// stream serialisation: it waits for the kernel before it reads.
+constexpr int kCombineRows = 4;
+
 template <int D, int HC, bool kF16>
-__global__ void __launch_bounds__(1024) decode_e4m3_combine_kernel(const E4m3Params p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int grid = static_cast<int>(gridDim.x) + 1;
-    // The tile total: from the prefix, or summed here.
+__global__ void __launch_bounds__(D * kCombineRows) decode_e4m3_combine_kernel(const E4m3Params p, int grid) {
     __shared__ long long s_total;
+    __shared__ float s_acc[kCombineRows][D];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The tile total: from the prefix, or summed here.
     if (p.cum == nullptr) {
         if (threadIdx.x < 32) {
             long long n = 0;
@@ -687,31 +702,55 @@ __global__ void __launch_bounds__(1024) decode_e4m3_combine_kernel(const E4m3Par
     }
     const int U = p.Hkv * p.chunks;
     const long long total = (p.cum == nullptr ? s_total : p.cum[p.B]) * U;
-    const long long per = slice_tiles(total, grid);
+    const long long per = slice_tiles(total, grid, E4m3Layout<D, HC>::kWarps);
     const long long at = per * (blockIdx.x + 1ll);
     if (at >= total) return;
     const int4 f = p.first[blockIdx.x + 1];
     if (f.z == 0 || f.z > per) return;  // not cut here, or cut at an earlier boundary
-    const long long start = at - f.z;
-    const long long c0 = start / per, c1 = (start + f.w - 1) / per;
-    const int in_first = start != c0 * per ? 1 : 0;
     const int hkv = f.y / p.chunks, chunk = f.y - hkv * p.chunks;
-    const int heads = min(HC, p.group - chunk * HC);
-    const int64_t row0 = static_cast<int64_t>(f.x) * p.Hq + hkv * p.group + chunk * HC;
-    for (int i = threadIdx.x; i < heads * D; i += blockDim.x) {
-        const int h = i / D, d = i - h * D;
-        float4 sum = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
-        float acc = 0.0f;
-        for (long long c = c0; c <= c1; ++c) {
-            const long long slot = (2 * c + (c == c0 ? in_first : 0)) * HC + h;
-            float keep;
-            const float wt = fold(sum, p.ws_ml[slot], &keep);
-            acc = fmaf(p.ws_o[slot * D + d], wt, acc * keep);
-        }
-        p.o[(row0 + h) * D + d] =
-            static_cast<uint16_t>(Elem16<kF16>::pack(acc * out_factor(sum.x, sum.y, sum.z), 0.0f) & 0xffffu);
-        if (d == 0 && p.lse) p.lse[row0 + h] = (sum.x + __log2f(sum.y)) * kLn2;
+    const int h = blockIdx.y, heads = min(HC, p.group - chunk * HC);
+    if (h >= heads) return;
+    const long long start = at - f.z;
+    const long long c0 = start / per;
+    const int n = static_cast<int>((start + f.w - 1) / per - c0) + 1;  // pieces: of CTAs c0 on
+    const long long slot0 = 2 * c0 + (start != c0 * per ? 1 : 0);
+    auto slot = [&](int i) { return (i == 0 ? slot0 : 2 * (c0 + i)) * HC + h; };
+    const int lane = threadIdx.x % 32;
+    // Every warp: the references and the sum over all pieces.
+    float m = -INFINITY, mv = -INFINITY;
+    for (int i = lane; i < n; i += 32) {
+        const float4 e = p.ws_ml[slot(i)];
+        m = fmaxf(m, e.x);
+        mv = fmaxf(mv, e.z);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+    }
+    float l = 0.0f;
+    for (int i = lane; i < n; i += 32) {
+        const float4 e = p.ws_ml[slot(i)];
+        l += e.x == -INFINITY ? 0.0f : e.y * ex2_approx(e.x - m);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const int d = threadIdx.x % D, row = threadIdx.x / D;
+    float acc = 0.0f;
+#pragma unroll 4
+    for (int i = row; i < n; i += kCombineRows) {
+        const float z = p.ws_ml[slot(i)].z;
+        acc = fmaf(p.ws_o[slot(i) * D + d], z == -INFINITY ? 0.0f : ex2_approx(z - mv), acc);
+    }
+    s_acc[row][d] = acc;
+    __syncthreads();
+    if (row > 0) return;
+#pragma unroll
+    for (int i = 1; i < kCombineRows; ++i) acc += s_acc[i][d];
+    const int64_t out = static_cast<int64_t>(f.x) * p.Hq + hkv * p.group + chunk * HC + h;
+    p.o[out * D + d] =
+        static_cast<uint16_t>(Elem16<kF16>::pack(acc * out_factor(m, l, mv), 0.0f) & 0xffffu);
+    if (d == 0 && p.lse) p.lse[out] = (m + __log2f(l)) * kLn2;
 }
 
 // Query heads a CTA serves at a time: one or two 8-row halves of the product.
@@ -742,19 +781,19 @@ cudaError_t launch_main(const E4m3Params& p, int grid, int prefix, int device, c
         if (e != cudaSuccess) return e;
         attr_set[device] = true;
     }
-    kern<<<grid, kWarps * 32, L::kBytes, st>>>(p, prefix);
+    kern<<<grid, L::kWarps * 32, L::kBytes, st>>>(p, prefix);
     e = cudaGetLastError();
     if (e != cudaSuccess || grid < 2) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid - 1);
-    cfg.blockDim = dim3(std::min(1024, HC * D));
+    cfg.gridDim = dim3(grid - 1, std::min(HC, p.group));
+    cfg.blockDim = dim3(D * kCombineRows);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_e4m3_combine_kernel<D, HC, kF16>, p);
+    return cudaLaunchKernelEx(&cfg, decode_e4m3_combine_kernel<D, HC, kF16>, p, grid);
 }
 
 template <int D, int HC>

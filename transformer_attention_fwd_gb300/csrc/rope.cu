@@ -30,9 +30,8 @@ struct RopeParams {
     const void* kw;
     const int* positions;
     RopeTable table;
-    long long warps;  // tokens * segments
-    int T;
-    int q_steps, steps, segs, per_seg;  // a token's steps, cut into segments
+    unsigned tokens, T;
+    int q_steps, steps, per_seg;  // a token's steps; grid.y segments of per_seg
     float eps;
 };
 
@@ -44,65 +43,68 @@ rope_kernel(const RopeParams p) {
     __shared__ float s_scratch[R::kScratch ? kRopeWarps * R::kScratch : 1];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int j = lane % R::kLanes, grp = lane / R::kLanes;
-    const long long w = static_cast<long long>(blockIdx.x) * kRopeWarps + warp;
-    if (w >= p.warps) return;
-    const long long token = w / p.segs;
-    const int seg = static_cast<int>(w - token * p.segs);
-    const long long b = token / p.T, t = token - b * p.T;
+    const unsigned token = blockIdx.x * kRopeWarps + warp;
+    if (token >= p.tokens) return;
+    const unsigned b = p.tokens == p.T ? 0u : token / p.T, t = token - b * p.T;
     const int half = p.table.half;
     const unsigned on = R::turning(half, j);
-    const long long at0 = R::first(j, half) * E::kBytes, at1 = R::second(j, half) * E::kBytes;
-    const uint8_t* xq = static_cast<const uint8_t*>(p.q.x) + (b * p.q.x_batch + t * p.q.x_token) * E::kBytes;
-    const uint8_t* xk = static_cast<const uint8_t*>(p.k.x) + (b * p.k.x_batch + t * p.k.x_token) * E::kBytes;
-    uint8_t* yq = static_cast<uint8_t*>(p.q.y) + (b * p.q.y_batch + t * p.q.y_token) * E::kBytes;
-    uint8_t* yk = static_cast<uint8_t*>(p.k.y) + (b * p.k.y_batch + t * p.k.y_token) * E::kBytes;
+    const int at0 = R::first(j, half) * E::kBytes, to1 = R::second(j, half) * E::kBytes - at0;
     float* table = s_table[warp];
     float* scratch = s_scratch + (R::kScratch ? warp * R::kScratch + grp * D : 0);
 
-    const int s0 = seg * p.per_seg, s1 = min(p.steps, s0 + p.per_seg);
+    const int s0 = blockIdx.y * p.per_seg, s1 = min(p.steps, s0 + p.per_seg);
     typename R::Coef coef;
     typename R::Pairs weight;  // the odd layout multiplies by it; the others have it in coef
-    int coef_of = -1;          // 0: query heads, 1: key heads
-    for (int s = s0; s < s1; s += kRopeUnroll) {
-        typename R::Raw raw[kRopeUnroll];
+    bool filled = false;
+    // Heads h0 + grp, h0 + grp + kRows, .. below h1 of one tensor.
+    auto run = [&](const RopeRows& r, const void* w, int h0, int h1) {
+        const long long xs = R::kRows * r.x_head * E::kBytes, ys = R::kRows * r.y_head * E::kBytes;
+        const uint8_t* x = static_cast<const uint8_t*>(r.x) + at0 +
+                           (b * r.x_batch + t * r.x_token + (h0 + grp) * r.x_head) * E::kBytes;
+        uint8_t* y = static_cast<uint8_t*>(r.y) + at0 +
+                     (b * r.y_batch + t * r.y_token + (h0 + grp) * r.y_head) * E::kBytes;
+        bool weighted = false;
+        for (int h = h0 + grp; h - grp < h1; h += kRopeUnroll * R::kRows) {
+            typename R::Raw raw[kRopeUnroll];
 #pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u) {
-            const bool is_k = s + u >= p.q_steps;
-            const int head = (is_k ? s + u - p.q_steps : s + u) * R::kRows + grp;
-            const uint8_t* x = is_k ? xk + head * p.k.x_head * E::kBytes : xq + head * p.q.x_head * E::kBytes;
-            raw[u] = s + u < s1 && head < (is_k ? p.k.heads : p.q.heads) ? R::load(x + at0, x + at1) : R::zero();
-        }
-        if (s == s0) {  // behind the first loads
-            rope_fill<D>(p.table, p.positions[token], lane, table);
-            if (!kNorm) R::coefficients(table, j, coef);
-        }
-#pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u) {
-            if (s + u >= s1) break;  // the same for the whole warp
-            const bool is_k = s + u >= p.q_steps;
-            const int head = (is_k ? s + u - p.q_steps : s + u) * R::kRows + grp;
-            typename R::Pairs v = R::unpack(raw[u]);
-            float scale = 1.0f;
-            if (kNorm) {
-                if (coef_of != (is_k ? 1 : 0)) {
-                    coef_of = is_k ? 1 : 0;
-                    const uint8_t* wrow = static_cast<const uint8_t*>(is_k ? p.kw : p.qw);
-                    weight = wrow ? R::unpack(R::load(wrow + at0, wrow + at1)) : R::ones();
-                    R::coefficients(table, j, coef, &weight);
-                }
-                scale = R::rms_scale(v, p.eps);
-                if (kLayout == kRopeHalvesOdd) R::multiply(v, weight);
+            for (int u = 0; u < kRopeUnroll; ++u) {
+                raw[u] = h + u * R::kRows < h1 ? R::load(x, x + to1) : R::zero();
+                x += xs;
             }
-            R::turn(v, coef, on, half, j, table, scratch);
-            if (kNorm) R::scale(v, scale);
-            uint8_t* y = is_k ? yk + head * p.k.y_head * E::kBytes : yq + head * p.q.y_head * E::kBytes;
-            if (head < (is_k ? p.k.heads : p.q.heads)) R::store(y + at0, y + at1, v);
+            if (!filled) {  // behind the first loads
+                rope_fill<D>(p.table, p.positions[token], lane, table);
+                filled = true;
+                if (!kNorm) R::coefficients(table, j, coef);
+            }
+            if (kNorm && !weighted) {
+                const uint8_t* row = static_cast<const uint8_t*>(w) + at0;
+                weight = w ? R::unpack(R::load(row, row + to1)) : R::ones();
+                R::coefficients(table, j, coef, &weight);
+                weighted = true;
+            }
+#pragma unroll
+            for (int u = 0; u < kRopeUnroll; ++u) {
+                if (u > 0 && h - grp + u * R::kRows >= h1) break;  // the same for the whole warp
+                typename R::Pairs v = R::unpack(raw[u]);
+                float scale = 1.0f;
+                if (kNorm) {
+                    scale = R::rms_scale(v, p.eps);
+                    if (kLayout == kRopeHalvesOdd) R::multiply(v, weight);
+                }
+                R::turn(v, coef, on, half, j, table, scratch);
+                if (kNorm) R::scale(v, scale);
+                if (h + u * R::kRows < h1) R::store(y, y + to1, v);
+                y += ys;
+            }
         }
-    }
+    };
+    if (s0 < p.q_steps) run(p.q, p.qw, s0 * R::kRows, min(p.q.heads, s1 * R::kRows));
+    if (s1 > p.q_steps)
+        run(p.k, p.kw, max(0, s0 - p.q_steps) * R::kRows, min(p.k.heads, (s1 - p.q_steps) * R::kRows));
 }
 
 template <typename E, int D, int kLayout>
-cudaError_t launch_norm(const RopeParams& p, bool norm, unsigned blocks, cudaStream_t st) {
+cudaError_t launch_norm(const RopeParams& p, bool norm, dim3 blocks, cudaStream_t st) {
     if (norm) rope_kernel<E, D, kLayout, true><<<blocks, kRopeWarps * 32, 0, st>>>(p);
     else rope_kernel<E, D, kLayout, false><<<blocks, kRopeWarps * 32, 0, st>>>(p);
     return cudaGetLastError();
@@ -115,15 +117,13 @@ cudaError_t launch_type(RopeParams p, int D, int layout, bool norm, const Launch
     p.steps = p.q_steps + (p.k.heads + rows - 1) / rows;
     // A token's steps stay in one warp once 32 warps per SM are there without
     // cutting; fewer tokens cut them (a decode step is all latency).
-    const long long tokens = p.warps, want = static_cast<long long>(env.num_sms) * 32;
-    p.segs = static_cast<int>(std::max<long long>(1, std::min<long long>(p.steps, want / tokens)));
-    p.per_seg = (p.steps + p.segs - 1) / p.segs;
-    p.segs = (p.steps + p.per_seg - 1) / p.per_seg;
-    p.warps = tokens * p.segs;
-    const long long blocks = (p.warps + kRopeWarps - 1) / kRopeWarps;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const unsigned g = static_cast<unsigned>(blocks);
-    *grid = static_cast<int>(g);
+    const int want = env.num_sms * 32;
+    int segs = std::max(1, static_cast<int>(std::min<unsigned>(p.steps, want / p.tokens)));
+    p.per_seg = (p.steps + segs - 1) / segs;
+    segs = (p.steps + p.per_seg - 1) / p.per_seg;
+    if (segs > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 g((p.tokens + kRopeWarps - 1) / kRopeWarps, segs);
+    *grid = static_cast<int>(g.x * g.y);
     if (D == 64)
         switch (layout) {
             case kRopeAdjacent: return launch_norm<E, 64, kRopeAdjacent>(p, norm, g, env.stream);
@@ -156,7 +156,7 @@ cudaError_t launch_rope(const RopeShape& s, const RopeRows& q, const RopeRows& k
     p.table = RopeTable{s.turns, s.rot_dim / 2, s.magnitude};
     p.T = s.T;
     p.eps = eps;
-    p.warps = static_cast<long long>(s.B) * s.T;
+    p.tokens = static_cast<unsigned>(s.B) * static_cast<unsigned>(s.T);
     const int layout = rope_layout(s.rot_dim, s.interleaved, s.dtype == ATTN_F32 ? 4 : 2);
     int grid = 0;
     cudaError_t e;
