@@ -55,6 +55,7 @@ struct E4m3Params {
     uint16_t* o;
     float* lse;
     long long* cum;  // [B + 1] tiles before each request (global: more than kMaxPrefixB requests)
+    longlong2* geom;  // {all tiles, tiles of a CTA's slice}
     int4* first;     // [grid] {request, unit, tile, tiles} a CTA's slice starts in
     float* ws_o;     // [2 * grid, HC, D] pieces of cut units, not normalised
     float4* ws_ml;   // [2 * grid, HC] their {m, sum, mv}
@@ -66,10 +67,10 @@ struct E4m3Params {
 
 template <int D, int HC>
 struct E4m3Layout {
-    static constexpr int kWarps = HC == 8 ? 12 : 8;
+    static constexpr int kWarps = 8;
     static constexpr int kStage = 2 * kTile * D + 2 * kTile * 4;  // K rows, V rows, scales
     static constexpr int kPiece = HC * D * 4;
-    static constexpr int kStages = D == 128 ? (HC == 8 ? 3 : 4) : (HC == 8 ? 6 : 8);
+    static constexpr int kStages = D == 128 ? 4 : 6;
     static constexpr int kPieceOff = kWarps * kStages * kStage;
     static constexpr int kMlOff = kPieceOff + kWarps * kPiece;  // [warp][2][HC] float4
     static constexpr int kMetaOff = kMlOff + kWarps * 2 * HC * 16;
@@ -84,10 +85,12 @@ struct Cursor {
     int b, unit, tile, tiles, len;
 };
 
-__device__ __forceinline__ int clamped_len(const E4m3Params& p, int b) {
-    const int L = p.seq_lens[b], most = p.max_pages * p.page.size;
+// A length inside the block table (bad ones are reported by tile_prefix).
+__device__ __forceinline__ int clamped(const E4m3Params& p, int L) {
+    const int most = p.max_pages * p.page.size;
     return L < 0 ? 0 : (L > most ? most : L);
 }
+__device__ __forceinline__ int clamped_len(const E4m3Params& p, int b) { return clamped(p, p.seq_lens[b]); }
 
 __device__ __forceinline__ Cursor cursor_at(const E4m3Params& p, const long long* cum, long long v) {
     const long long U = static_cast<long long>(p.Hkv) * p.chunks;
@@ -126,9 +129,9 @@ __device__ void tile_prefix(const E4m3Params& p, long long* cum, long long* scan
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
-        const int L = clamped_len(p, b);
-        if (report && L != p.seq_lens[b]) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
-        mine += (static_cast<long long>(L) + kTile - 1) / kTile;
+        const int n = p.seq_lens[b], L = clamped(p, n);
+        if (report && L != n) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
+        mine += (L + kTile - 1) / kTile;
     }
     long long incl = mine;
 #pragma unroll
@@ -140,11 +143,12 @@ __device__ void tile_prefix(const E4m3Params& p, long long* cum, long long* scan
     __syncthreads();
     long long run = incl - mine;
     for (int i = 0; i < warp; ++i) run += scan[i];
-    for (int b = b0; b < b1; ++b) {
-        cum[b] = run;
-        run += (static_cast<long long>(clamped_len(p, b)) + kTile - 1) / kTile;
+    const long long end = run + mine;
+    for (int b = b0; b < b1; ++b) {  // one request: nothing to read again
+        run = b + 1 == b1 ? end : run + (clamped_len(p, b) + kTile - 1) / kTile;
+        cum[b + 1] = run;
     }
-    if (tid == nt - 1) cum[p.B] = run;  // the last thread's range ends at B
+    if (tid == 0) cum[0] = 0;
     __syncthreads();
 }
 
@@ -271,18 +275,20 @@ __device__ __forceinline__ float row_max(const float (&x)[4]) {
 // Factor from sum w v to O: 2^(mv - m) / l.
 __device__ __forceinline__ float out_factor(float m, float l, float mv) { return ex2_approx(mv - m) / l; }
 
-// {m, sum, mv} of a warp's 32 pieces (m = mv = -infinity, sum = 0 where there is
-// none): the common references {m, mv}, and the sum relative to m.
+// {m, sum, mv} of pieces, one in each of the first 2 * kHalf lanes (m = mv =
+// -infinity, sum = 0 where there is none): the common references {m, mv}, and the
+// sum relative to m, in those lanes.
+template <int kHalf>
 __device__ __forceinline__ float2 merge_weights(const float4& e, float* sum) {
     float m = e.x, mv = e.z;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = kHalf; o > 0; o >>= 1) {
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
     }
     float l = e.x == -INFINITY ? 0.0f : e.y * ex2_approx(e.x - m);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    for (int o = kHalf; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     *sum = l;
     return make_float2(m, mv);
 }
@@ -455,11 +461,8 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
     const long long total = cum[p.B] * U;
     const long long per = slice_tiles(total, grid, kWarps);
     const long long v0 = per * blockIdx.x, v1 = v0 + per < total ? v0 + per : total;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.geom = make_longlong2(total, per);
     if (v0 >= total) return;
-    if (threadIdx.x == 0) {
-        const Cursor c = cursor_at(p, cum, v0);
-        p.first[blockIdx.x] = make_int4(c.b, c.unit, c.tile, c.tiles);
-    }
     const int wper = static_cast<int>((v1 - v0 + kWarps - 1) / kWarps);
     const long long va = v0 + static_cast<long long>(warp) * wper;
     const int count = va >= v1 ? 0 : static_cast<int>(va + wper < v1 ? wper : v1 - va);
@@ -468,6 +471,7 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
 
     if (count > 0) {
         Cursor lc = cursor_at(p, cum, va), cc = lc;
+        if (threadIdx.x == 0) p.first[blockIdx.x] = make_int4(lc.b, lc.unit, lc.tile, lc.tiles);  // va = v0
         int loaded = 0;  // tiles whose copies have been issued
         // The next tile to copy: its block ids are loaded one step ahead.
         int id = 0, row = 0;
@@ -623,20 +627,21 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
     }
     __syncthreads();
 
-    // Merge the pieces of each unit that is not one warp's: every warp takes some
-    // of its heads.
-    for (int from = 0; from < 2 * kWarps; ++from) {
+    // Merge the pieces of each unit that is not one warp's, its heads dealt to the
+    // warps.  Lane i holds place i of the pieces' list (two places a warp, in the
+    // order of the sequence); a unit's pieces after its first are in first places.
+    static_assert(2 * kWarps <= 32, "a lane for each place");
+    const long long place = lane < 2 * kWarps ? meta[lane].unit : -1;
+    const long long back1 = __shfl_up_sync(0xffffffffu, place, 1), back2 = __shfl_up_sync(0xffffffffu, place, 2);
+    const bool is_first = place >= 0 && ((lane & 1) || lane == 0 || (back1 >= 0 ? back1 : back2) != place);
+    int dealt = 0;
+    for (unsigned left = __ballot_sync(0xffffffffu, is_first); left != 0; left &= left - 1) {
+        const int from = __ffs(left) - 1, w0 = from >> 1;
         const PieceMeta head_piece = meta[from];
-        const int w0 = from >> 1;
-        if (head_piece.unit < 0) continue;
-        if ((from & 1) == 0 && w0 > 0) {  // the unit's first piece here?
-            const PieceMeta* before = &meta[2 * (w0 - 1)];
-            if ((before[1].unit >= 0 ? before[1].unit : before[0].unit) == head_piece.unit) continue;
-        }
-        int w1 = w0;  // last warp that has a piece of it, in its first slot unless it is w0
-        while (w1 + 1 < kWarps && meta[2 * (w1 + 1)].unit == head_piece.unit) ++w1;
-        const bool ends = w1 == w0 ? head_piece.ends : meta[2 * w1].ends;
-        const int n = w1 - w0 + 1;
+        const unsigned others =
+            __ballot_sync(0xffffffffu, place == head_piece.unit && lane > from && (lane & 1) == 0);
+        const int n = 1 + __popc(others);
+        const bool ends = n == 1 ? head_piece.ends : meta[2 * (w0 + n - 1)].ends;
         const int b = static_cast<int>(head_piece.unit / U);
         const int unit = static_cast<int>(head_piece.unit - static_cast<long long>(b) * U);
         const int hkv = unit / p.chunks, chunk = unit - hkv * p.chunks;
@@ -644,13 +649,17 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
         const int64_t row0 = static_cast<int64_t>(b) * p.Hq + hkv * p.group + chunk * HC;
         const bool whole = head_piece.begins && ends;
         const int64_t ws = 2ll * blockIdx.x + (head_piece.begins == 2 ? 1 : 0);
-        for (int h = warp; h < heads; h += kWarps) {
+        for (int h = 0; h < heads; ++h, ++dealt) {
+            if (dealt % kWarps != warp) continue;
             // Lane i: the i-th piece's references, sum and weight.
             const float4 e = lane < n ? ml[(lane == 0 ? from : 2 * (w0 + lane)) * HC + h]
                                       : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
             float l;
-            const float2 m = merge_weights(e, &l);
-            float weight = e.z == -INFINITY ? 0.0f : ex2_approx(e.z - m.y);
+            float2 m = merge_weights<8>(e, &l);
+            m.x = __shfl_sync(0xffffffffu, m.x, 0);
+            m.y = __shfl_sync(0xffffffffu, m.y, 0);
+            l = __shfl_sync(0xffffffffu, l, 0);
+            const float weight = e.z == -INFINITY ? 0.0f : ex2_approx(e.z - m.y);
             float acc[D / 32];
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
@@ -677,93 +686,81 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
     }
 }
 
-// Merge the pieces of the units that CTA boundaries cut: block (j, h) takes head
-// h of the unit that the boundary between the slices of CTAs j and j + 1 cuts,
-// if it is the unit's first one.  A unit over many CTAs has that many pieces:
-// kCombineRows of them are added up side by side.  Launched with programmatic
+// Merge the pieces of the units that CTA boundaries cut: block j takes the unit
+// that the boundary between the slices of CTAs j and j + 1 cuts, if it is the
+// unit's first one; grid.y blocks share its heads.  A block is kRows rows of D
+// threads: with few pieces the rows take a head each, with many (a long request
+// over many CTAs) they share one head's pieces.  Launched with programmatic
 // stream serialisation: it waits for the kernel before it reads.
-constexpr int kCombineRows = 4;
+constexpr int kCombineThreads = 512;
 
 template <int D, int HC, bool kF16>
-__global__ void __launch_bounds__(D * kCombineRows) decode_e4m3_combine_kernel(const E4m3Params p, int grid) {
-    __shared__ long long s_total;
-    __shared__ float s_acc[kCombineRows][D];
+__global__ void __launch_bounds__(kCombineThreads) decode_e4m3_combine_kernel(const E4m3Params p) {
+    constexpr int kRows = kCombineThreads / D;
+    __shared__ float s_acc[kRows][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // The tile total: from the prefix, or summed here.
-    if (p.cum == nullptr) {
-        if (threadIdx.x < 32) {
-            long long n = 0;
-            for (int b = threadIdx.x; b < p.B; b += 32) n += (static_cast<long long>(clamped_len(p, b)) + kTile - 1) / kTile;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-            if (threadIdx.x == 0) s_total = n;
-        }
-        __syncthreads();
-    }
-    const int U = p.Hkv * p.chunks;
-    const long long total = (p.cum == nullptr ? s_total : p.cum[p.B]) * U;
-    const long long per = slice_tiles(total, grid, E4m3Layout<D, HC>::kWarps);
-    const long long at = per * (blockIdx.x + 1ll);
-    if (at >= total) return;
-    const int4 f = p.first[blockIdx.x + 1];
-    if (f.z == 0 || f.z > per) return;  // not cut here, or cut at an earlier boundary
+    const longlong2 geom = *p.geom;  // {tiles, tiles of a slice}
+    const int4 f = p.first[blockIdx.x + 1];  // not written past the last slice
+    const long long at = geom.y * (blockIdx.x + 1ll);
+    if (at >= geom.x) return;
+    if (f.z == 0 || f.z > geom.y) return;  // not cut here, or cut at an earlier boundary
     const int hkv = f.y / p.chunks, chunk = f.y - hkv * p.chunks;
-    const int h = blockIdx.y, heads = min(HC, p.group - chunk * HC);
-    if (h >= heads) return;
+    const int heads = min(HC, p.group - chunk * HC);
     const long long start = at - f.z;
-    const long long c0 = start / per;
-    const int n = static_cast<int>((start + f.w - 1) / per - c0) + 1;  // pieces: of CTAs c0 on
-    const long long slot0 = 2 * c0 + (start != c0 * per ? 1 : 0);
-    auto slot = [&](int i) { return (i == 0 ? slot0 : 2 * (c0 + i)) * HC + h; };
-    const int lane = threadIdx.x % 32;
-    // Every warp: the references and the sum over all pieces.
-    float m = -INFINITY, mv = -INFINITY;
-    for (int i = lane; i < n; i += 32) {
-        const float4 e = p.ws_ml[slot(i)];
-        m = fmaxf(m, e.x);
-        mv = fmaxf(mv, e.z);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-    }
-    float l = 0.0f;
-    for (int i = lane; i < n; i += 32) {
-        const float4 e = p.ws_ml[slot(i)];
-        l += e.x == -INFINITY ? 0.0f : e.y * ex2_approx(e.x - m);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const int d = threadIdx.x % D, row = threadIdx.x / D;
-    float acc = 0.0f;
+    const long long c0 = start / geom.y;
+    const int n = static_cast<int>((start + f.w - 1) / geom.y - c0) + 1;  // pieces: of CTAs c0 on
+    const long long slot0 = 2 * c0 + (start != c0 * geom.y ? 1 : 0);
+    const int64_t row0 = static_cast<int64_t>(f.x) * p.Hq + hkv * p.group + chunk * HC;
+    const int lane = threadIdx.x % 32, d = threadIdx.x % D, row = threadIdx.x / D;
+    const int abreast = n <= 8 ? kRows : 1;  // heads at a time
+    const int sharers = kRows / abreast, sharer = row / abreast;
+    for (int h0 = blockIdx.y * abreast; h0 < heads; h0 += gridDim.y * abreast) {
+        const int h = min(heads - 1, h0 + row % abreast);
+        // References and sum over all pieces, by every warp.
+        float4 e = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+        for (int i = lane; i < n; i += 32) {
+            const float4 x = p.ws_ml[(i == 0 ? slot0 : 2 * (c0 + i)) * HC + h];
+            const float m = fmaxf(e.x, x.x);
+            e.y = (e.x == -INFINITY ? 0.0f : e.y * ex2_approx(e.x - m)) + (x.x == -INFINITY ? 0.0f : x.y * ex2_approx(x.x - m));
+            e.x = m;
+            e.z = fmaxf(e.z, x.z);
+        }
+        float l;
+        const float2 m = merge_weights<16>(e, &l);
+        float acc = 0.0f;
 #pragma unroll 4
-    for (int i = row; i < n; i += kCombineRows) {
-        const float z = p.ws_ml[slot(i)].z;
-        acc = fmaf(p.ws_o[slot(i) * D + d], z == -INFINITY ? 0.0f : ex2_approx(z - mv), acc);
+        for (int i = sharer; i < n; i += sharers) {
+            const long long slot = (i == 0 ? slot0 : 2 * (c0 + i)) * HC + h;
+            const float z = p.ws_ml[slot].z;
+            acc = fmaf(p.ws_o[slot * D + d], z == -INFINITY ? 0.0f : ex2_approx(z - m.y), acc);
+        }
+        if (sharers > 1) {
+            s_acc[row][d] = acc;
+            __syncthreads();
+            acc = 0.0f;
+            for (int i = 0; i < kRows; ++i) acc += s_acc[i][d];
+            __syncthreads();
+        }
+        if (sharer == 0 && h0 + row % abreast < heads) {
+            p.o[(row0 + h) * D + d] =
+                static_cast<uint16_t>(Elem16<kF16>::pack(acc * out_factor(m.x, l, m.y), 0.0f) & 0xffffu);
+            if (d == 0 && p.lse) p.lse[row0 + h] = (m.x + __log2f(l)) * kLn2;
+        }
     }
-    s_acc[row][d] = acc;
-    __syncthreads();
-    if (row > 0) return;
-#pragma unroll
-    for (int i = 1; i < kCombineRows; ++i) acc += s_acc[i][d];
-    const int64_t out = static_cast<int64_t>(f.x) * p.Hq + hkv * p.group + chunk * HC + h;
-    p.o[out * D + d] =
-        static_cast<uint16_t>(Elem16<kF16>::pack(acc * out_factor(m, l, mv), 0.0f) & 0xffffu);
-    if (d == 0 && p.lse) p.lse[out] = (m + __log2f(l)) * kLn2;
 }
 
 // Query heads a CTA serves at a time: one or two 8-row halves of the product.
 int heads_at_once(int group) { return group <= 8 ? 8 : 16; }
 
-// Workspace: cum (long long [B + 1]), first (int4 [grid]), the pieces of the
-// cut units and their references and sums.
+// Workspace: cum (long long [B + 1]), geom (longlong2), first (int4 [grid]), the
+// pieces of the cut units and their references and sums.
 struct WsLayout {
-    size_t first, ws_o, ws_ml, bytes;
+    size_t geom, first, ws_o, ws_ml, bytes;
     WsLayout(const PagedShape& s, int grid) {
         const size_t rows = 2ull * grid * heads_at_once(s.Hq / s.Hkv);
         auto up16 = [](size_t x) { return (x + 15) / 16 * 16; };
-        first = up16(8ull * (s.B + 1));
+        geom = up16(8ull * (s.B + 1));
+        first = geom + sizeof(longlong2);
         ws_o = first + 16ull * grid;
         ws_ml = ws_o + rows * s.D * sizeof(float);
         bytes = ws_ml + rows * sizeof(float4);
@@ -785,15 +782,17 @@ cudaError_t launch_main(const E4m3Params& p, int grid, int prefix, int device, c
     e = cudaGetLastError();
     if (e != cudaSuccess || grid < 2) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid - 1, std::min(HC, p.group));
-    cfg.blockDim = dim3(D * kCombineRows);
+    // Few units: each has many pieces, and its heads are shared out to more blocks.
+    const bool few = static_cast<long long>(p.B) * p.Hkv * p.chunks * 4 < grid;
+    cfg.gridDim = dim3(grid - 1, few ? std::min(HC, p.group) : 1);
+    cfg.blockDim = dim3(kCombineThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_e4m3_combine_kernel<D, HC, kF16>, p, grid);
+    return cudaLaunchKernelEx(&cfg, decode_e4m3_combine_kernel<D, HC, kF16>, p);
 }
 
 template <int D, int HC>
@@ -829,6 +828,7 @@ cudaError_t launch_decode_paged_e4m3(const uint16_t* q, const uint8_t* kv, const
     p.o = o;
     p.lse = lse;
     p.cum = prefix ? nullptr : reinterpret_cast<long long*>(base);
+    p.geom = reinterpret_cast<longlong2*>(base + lay.geom);
     p.first = reinterpret_cast<int4*>(base + lay.first);
     p.ws_o = reinterpret_cast<float*>(base + lay.ws_o);
     p.ws_ml = reinterpret_cast<float4*>(base + lay.ws_ml);
