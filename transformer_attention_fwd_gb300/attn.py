@@ -402,76 +402,76 @@ def rope_turns(rot_dim: int, base: float = 10000.0, scaling: str = "none", facto
     return turns, magnitude.value
 
 
-def _heads(name, t, like, device, packed_only=False):
-    """A tensor of rows: [T, H, D], or [B, H, T, D], D innermost and contiguous."""
-    if t.get_device() != device or device < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
-    if t.dtype != like.dtype:
-        raise ValueError(f"{name} must be {like.dtype} (got {t.dtype})")
-    if t.dim() != like.dim() or (packed_only and t.dim() != 3) or t.dim() not in (3, 4):
-        raise ValueError(f"{name} must be [T, H, D]" + ("" if packed_only else " or [B, H, T, D]"))
-    if t.shape[-1] != like.shape[-1] or t.shape[0] != like.shape[0] or (
-            t.dim() == 4 and t.shape[2] != like.shape[2]):
-        raise ValueError(f"{name} must have the same tokens and head dim as the others")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-
-
-def _rows(x, y):
-    """attn_rows from x to y (None: no output)."""
-    xs = x.stride()
-    if x.dim() == 3:
-        n, xb, xh, xt = x.shape[1], 0, xs[1], xs[0]
-        if y is None:
-            return _Rows(x.data_ptr(), None, n, xb, xh, xt, 0, 0, 0)
-        ys = y.stride()
-        return _Rows(x.data_ptr(), y.data_ptr(), n, xb, xh, xt, 0, ys[1], ys[0])
-    ys = y.stride()
-    return _Rows(x.data_ptr(), y.data_ptr(), x.shape[1], xs[0], xs[1], xs[2], ys[0], ys[1], ys[2])
-
-
-def _rows_out(name, x, out):
-    if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if out.shape != x.shape or out.dtype != x.dtype or out.get_device() != x.get_device():
-        raise ValueError(f"{name} must be {tuple(x.shape)} {x.dtype} on {x.device}")
-    if out.stride(-1) != 1 and x.shape[-1] > 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return out
+def _raw_stream(stream, device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else int(stream.cuda_stream)
 
 
 def _current(device: int):
-    if device != torch.cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{device} but the current device is "
-                         f"cuda:{torch.cuda.current_device()}; call under torch.cuda.device({device})")
+    now = torch._C._cuda_getDevice()
+    if device != now:
+        raise ValueError(f"tensors are on cuda:{device} but the current device is cuda:{now}; "
+                         f"call under torch.cuda.device({device})")
+
+
+def _rows(name, x, out, like, device, write=True):
+    """attn_rows of x, [T, H, D] or [B, H, T, D] with the tokens, head dim and type
+    of ``like``, and its output: ``out``, or a new one (``write`` False: none)."""
+    shape, dtype = x.shape, x.dtype
+    n, want = len(shape), like.shape
+    if x.get_device() != device or device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
+    if dtype is not like.dtype:
+        raise ValueError(f"{name} must be {like.dtype} (got {dtype})")
+    if n != len(want) or shape[0] != want[0] or shape[-1] != want[-1] or (n == 4 and shape[2] != want[2]):
+        raise ValueError(f"{name} must have the tokens and head dim of the others (got {tuple(shape)})")
+    xs = x.stride()
+    if xs[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    if not write:
+        return _Rows(x.data_ptr(), None, shape[1], 0, xs[1], xs[0], 0, 0, 0), None
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    elif out.shape != shape or out.dtype is not dtype or out.get_device() != device:
+        raise ValueError(f"out_{name} must be {tuple(shape)} {dtype} on {x.device}")
+    ys = out.stride()
+    if ys[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"out_{name}'s last dimension must be contiguous")
+    if n == 3:
+        return _Rows(x.data_ptr(), out.data_ptr(), shape[1], 0, xs[1], xs[0], 0, ys[1], ys[0]), out
+    return _Rows(x.data_ptr(), out.data_ptr(), shape[1], xs[0], xs[1], xs[2], ys[0], ys[1], ys[2]), out
 
 
 def _ints(name, t, shape, device):
     """An int32 device tensor of exactly this shape."""
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} (got {tuple(t.shape)} {t.dtype})")
     if t.get_device() != device:
         raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
 
 
 def _rope_call(q, k, positions, rotation, out_q, out_k):
-    device = q.get_device()
+    device, shape = q.get_device(), q.shape
     dt = _DTYPES.get(q.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {q.dtype}")
-    _heads("q", q, q, device)
-    if k is not None:
-        _heads("k", k, q, device)
-    elif out_k is not None:
+    if len(shape) == 3:
+        B, T = 1, shape[0]
+        pos_shape = (T,)
+    elif len(shape) == 4:
+        B, T = pos_shape = shape[0], shape[2]
+    else:
+        raise ValueError("q must be [T, H, D] or [B, H, T, D]")
+    if k is None and out_k is not None:
         raise ValueError("out_k without k")
-    B, T = (1, q.shape[0]) if q.dim() == 3 else (q.shape[0], q.shape[2])
-    _ints("positions", positions, (T,) if q.dim() == 3 else (B, T), device)
+    rq, out_q = _rows("q", q, out_q, q, device)
+    rk = None
+    if k is not None:
+        rk, out_k = _rows("k", k, out_k, q, device)
+    _ints("positions", positions, pos_shape, device)
     if rotation.device_index != device:
         raise ValueError("the rotation's table must be on the device of the tensors")
     _current(device)
-    yq = _rows_out("out_q", q, out_q)
-    yk = None if k is None else _rows_out("out_k", k, out_k)
-    return B, T, dt, yq, yk
+    return device, B, T, shape[-1], dt, rq, out_q, rk, out_k
 
 
 def attn_rope(q, k, positions, rotation: Rotation, out_q=None, out_k=None, stream=None):
@@ -483,73 +483,77 @@ def attn_rope(q, k, positions, rotation: Rotation, out_q=None, out_k=None, strea
     Returns ``(out_q, out_k)``; ``out_q=q`` works in place.  The gradient of
     the inputs is this call on the outputs' gradients with -positions.
     """
-    B, T, dt, yq, yk = _rope_call(q, k, positions, rotation, out_q, out_k)
-    _check(lib.attn_rope(_rows(q, yq), None if k is None else _rows(k, yk), positions.data_ptr(), B, T,
-                         q.shape[-1], rotation._struct, dt, _stream_handle(stream)))
-    return yq, yk
+    device, B, T, D, dt, rq, out_q, rk, out_k = _rope_call(q, k, positions, rotation, out_q, out_k)
+    _check(lib.attn_rope(rq, rk, positions.data_ptr(), B, T, D, rotation._struct, dt,
+                         _raw_stream(stream, device)))
+    return out_q, out_k
 
 
 def attn_qk_norm_rope(q, k, q_weight, k_weight, positions, rotation: Rotation, eps: float = 1e-6,
                       out_q=None, out_k=None, stream=None):
     """``attn_rope`` of x / sqrt(mean(x^2) + eps) * weight for every head x of q
     and k (``attn_qk_norm_rope``); weights [D] in q's dtype, or None for ones."""
-    B, T, dt, yq, yk = _rope_call(q, k, positions, rotation, out_q, out_k)
+    device, B, T, D, dt, rq, out_q, rk, out_k = _rope_call(q, k, positions, rotation, out_q, out_k)
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.shape != q.shape[-1:] or w.dtype != q.dtype or not w.is_contiguous()
-                              or w.get_device() != q.get_device()):
-            raise ValueError(f"{name} must be a contiguous {q.dtype} tensor [{q.shape[-1]}] on {q.device}")
-    _check(lib.attn_qk_norm_rope(_rows(q, yq), None if k is None else _rows(k, yk), _ptr(q_weight),
-                                 _ptr(k_weight), eps, positions.data_ptr(), B, T, q.shape[-1],
-                                 rotation._struct, dt, _stream_handle(stream)))
-    return yq, yk
+        if w is not None and (w.shape != (D,) or w.dtype is not q.dtype or not w.is_contiguous()
+                              or w.get_device() != device):
+            raise ValueError(f"{name} must be a contiguous {q.dtype} tensor [{D}] on {q.device}")
+    _check(lib.attn_qk_norm_rope(rq, rk, _ptr(q_weight), _ptr(k_weight), eps, positions.data_ptr(), B, T, D,
+                                 rotation._struct, dt, _raw_stream(stream, device)))
+    return out_q, out_k
 
 
-def _append(name, k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens, rotation, positions, q,
+def _append(call, k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens, rotation, positions, q,
             out_q, out_k, stream):
-    device = k.get_device()
-    dt = _DTYPES.get(k.dtype)
-    if dt is None or dt == ATTN_F32:
-        raise ValueError(f"{name} takes bf16 or fp16 tensors")
-    _heads("k", k, k, device, packed_only=True)
-    _heads("v", v, k, device, packed_only=True)
-    if q is not None:
-        _heads("q", q, k, device, packed_only=True)
-    elif out_q is not None:
-        raise ValueError("out_q without q")
+    device, dtype = k.get_device(), k.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError("the paged append takes bf16 or fp16 tensors")
+    if len(k.shape) != 3:
+        raise ValueError("k must be [total, Hkv, D]")
     total, Hkv, D = k.shape
+    rk, out_k = _rows("k", k, out_k, k, device, out_k is not None)
+    rv, _ = _rows("v", v, None, k, device, False)
     if v.shape[1] != Hkv:
         raise ValueError("k and v must have the same heads")
-    want = k.dtype if scales is None else torch.float8_e4m3fn
-    if (kv_cache.dim() != 5 or kv_cache.dtype != want or not kv_cache.is_contiguous()
-            or kv_cache.get_device() != device):
-        raise ValueError(f"kv_cache must be a contiguous {want} tensor [num_blocks, 2, Hkv, page_size, D] on {k.device}")
-    blocks, two, heads, page, Dc = kv_cache.shape
-    if two != 2 or heads != Hkv or Dc != D:
-        raise ValueError("kv_cache must be [num_blocks, 2, Hkv, page_size, D] with k's Hkv and D")
-    if scales is not None and (scales.dtype != torch.float32 or scales.shape != (blocks, 2, Hkv)
+    rq = None
+    if q is not None:
+        rq, out_q = _rows("q", q, out_q, k, device)
+    elif out_q is not None:
+        raise ValueError("out_q without q")
+    want = dtype if scales is None else torch.float8_e4m3fn
+    held = kv_cache.shape
+    if (len(held) != 5 or held[1] != 2 or held[2] != Hkv or held[4] != D or kv_cache.dtype is not want
+            or not kv_cache.is_contiguous() or kv_cache.get_device() != device):
+        raise ValueError(f"kv_cache must be a contiguous {want} tensor [num_blocks, 2, {Hkv}, page_size, {D}] on {k.device}")
+    blocks, page = held[0], held[3]
+    if scales is not None and (scales.dtype is not torch.float32 or scales.shape != (blocks, 2, Hkv)
                                or not scales.is_contiguous() or scales.get_device() != device):
         raise ValueError("scales must be a contiguous float32 tensor [num_blocks, 2, Hkv]")
-    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    table = block_table.shape
+    if len(table) != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    B = table[0]
+    _ints("block_table", block_table, table, device)
     _ints("seq_lens", seq_lens, (B,), device)
     _ints("cu_seqlens", cu_seqlens, (B + 1,), device)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    _ints("block_table", block_table, (B, block_table.shape[1]), device)
     if positions is not None:
         _ints("positions", positions, (total,), device)
-    if rotation is not None and rotation.device_index != device:
-        raise ValueError("the rotation's table must be on the device of the tensors")
+    struct = None
+    if rotation is not None:
+        if rotation.device_index != device:
+            raise ValueError("the rotation's table must be on the device of the tensors")
+        struct = rotation._struct
     _current(device)
-    if q is not None:
-        out_q = _rows_out("out_q", q, out_q)
-    if out_k is not None:
-        out_k = _rows_out("out_k", k, out_k)
-    args = [None if q is None else _rows(q, out_q), _rows(k, out_k), _rows(v, None), cu_seqlens.data_ptr(),
-            seq_lens.data_ptr(), _ptr(positions), block_table.data_ptr(), kv_cache.data_ptr()]
-    if scales is not None:
-        args.append(scales.data_ptr())
-    _check(getattr(lib, name)(*args, B, total, D, page, block_table.shape[1], blocks,
-                              None if rotation is None else rotation._struct, dt, _stream_handle(stream)))
+    dt, stream = _DTYPES[dtype], _raw_stream(stream, device)
+    if scales is None:
+        status = call(rq, rk, rv, cu_seqlens.data_ptr(), seq_lens.data_ptr(), _ptr(positions),
+                      block_table.data_ptr(), kv_cache.data_ptr(), B, total, D, page, table[1], blocks, struct,
+                      dt, stream)
+    else:
+        status = call(rq, rk, rv, cu_seqlens.data_ptr(), seq_lens.data_ptr(), _ptr(positions),
+                      block_table.data_ptr(), kv_cache.data_ptr(), scales.data_ptr(), B, total, D, page,
+                      table[1], blocks, struct, dt, stream)
+    _check(status)
     return out_q, out_k
 
 
@@ -565,7 +569,7 @@ def attn_append_paged(k, v, kv_cache, block_table, cu_seqlens, seq_lens, rotatio
     given.  Returns ``(out_q, out_k)``: the rotated q (None without q), and
     ``out_k`` as passed, filled with the rotated keys (None if not passed).
     """
-    return _append("attn_append_paged", k, v, kv_cache, None, block_table, cu_seqlens, seq_lens, rotation,
+    return _append(lib.attn_append_paged, k, v, kv_cache, None, block_table, cu_seqlens, seq_lens, rotation,
                    positions, q, out_q, out_k, stream)
 
 
@@ -575,7 +579,7 @@ def attn_append_paged_e4m3(k, v, kv_cache, scales, block_table, cu_seqlens, seq_
     """``attn_append_paged`` into an 8-bit cache (``attn_append_paged_e4m3``):
     kv_cache float8_e4m3fn, scales float32 [num_blocks, 2, Hkv]; a code stands
     for code * scale of its block, K or V, and head."""
-    return _append("attn_append_paged_e4m3", k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens,
+    return _append(lib.attn_append_paged_e4m3, k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens,
                    rotation, positions, q, out_q, out_k, stream)
 
 
@@ -588,35 +592,39 @@ def attn_fwd_decode_paged_e4m3(q, kv_cache, scales, block_table, seq_lens, scale
     max_pages] and seq_lens: [B] int32; all contiguous CUDA tensors.  Returns
     ``(o [B, Hq, 1, D], lse [B, Hq] or None)``.
     """
-    device = q.get_device()
-    if device < 0 or q.dim() != 4 or q.shape[2] != 1 or not q.is_contiguous() or q.dtype not in (
-            torch.bfloat16, torch.float16):
+    device, dtype, shape = q.get_device(), q.dtype, q.shape
+    if (device < 0 or len(shape) != 4 or shape[2] != 1 or not q.is_contiguous()
+            or (dtype is not torch.bfloat16 and dtype is not torch.float16)):
         raise ValueError("q must be a contiguous bf16 or fp16 CUDA tensor [B, Hq, 1, D]")
-    B, Hq, _, D = q.shape
-    if (kv_cache.dim() != 5 or kv_cache.dtype != torch.float8_e4m3fn or not kv_cache.is_contiguous()
-            or kv_cache.shape[1] != 2 or kv_cache.shape[4] != D or kv_cache.get_device() != device):
+    B, Hq, _, D = shape
+    held = kv_cache.shape
+    if (len(held) != 5 or held[1] != 2 or held[4] != D or kv_cache.dtype is not torch.float8_e4m3fn
+            or not kv_cache.is_contiguous() or kv_cache.get_device() != device):
         raise ValueError("kv_cache must be a contiguous float8_e4m3fn tensor [num_blocks, 2, Hkv, page_size, D]")
-    blocks, _, Hkv, page, _ = kv_cache.shape
-    if (scales.dtype != torch.float32 or scales.shape != (blocks, 2, Hkv) or not scales.is_contiguous()
+    blocks, _, Hkv, page, _ = held
+    if (scales.dtype is not torch.float32 or scales.shape != (blocks, 2, Hkv) or not scales.is_contiguous()
             or scales.get_device() != device):
         raise ValueError("scales must be a contiguous float32 tensor [num_blocks, 2, Hkv]")
-    _ints("seq_lens", seq_lens, (B,), device)
-    if block_table.dim() != 2:
+    table = block_table.shape
+    if len(table) != 2 or table[0] != B:
         raise ValueError("block_table must be [B, max_pages]")
-    _ints("block_table", block_table, (B, block_table.shape[1]), device)
+    _ints("block_table", block_table, table, device)
+    _ints("seq_lens", seq_lens, (B,), device)
     _current(device)
-    _check_buffer("out", out, q.shape, q.dtype, q.device)
-    _check_buffer("lse", lse, (B, Hq), torch.float32, q.device)
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    o = torch.empty_like(q) if out is None else out
-    if lse is None and want_lse:
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+    else:
+        _check_buffer("out", out, shape, dtype, q.device)
+    if lse is not None:
+        _check_buffer("lse", lse, (B, Hq), torch.float32, q.device)
+    elif want_lse:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     _check(lib.attn_fwd_decode_paged_e4m3(q.data_ptr(), kv_cache.data_ptr(), scales.data_ptr(),
-                                          block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
-                                          _ptr(lse), B, Hq, Hkv, D, page, block_table.shape[1], blocks, scale,
-                                          ATTN_F16 if q.dtype == torch.float16 else ATTN_BF16,
-                                          _stream_handle(stream)))
-    return o, lse
+                                          block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+                                          _ptr(lse), B, Hq, Hkv, D, page, table[1], blocks, scale,
+                                          _DTYPES[dtype], _raw_stream(stream, device)))
+    return out, lse
 
 
 def device_status(stream=None) -> int:

@@ -17,7 +17,7 @@ struct Int {
 };
 
 constexpr int kAppendWarps = 4;
-constexpr int kAppendUnroll = 2;  // steps a lane has in flight
+constexpr int kAppendUnroll = 2;  // steps a lane has in flight (as in rope.cu)
 
 struct AppendParams {
     RopeRows q, k, v;  // packed tokens: the token and head strides only; q.heads = 0 without q
@@ -141,15 +141,16 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int token, in
         const uint8_t* x = static_cast<const uint8_t*>(r.x) + at0 + (token * r.x_token + (h0 + grp) * r.x_head) * E::kBytes;
         uint8_t* y = static_cast<uint8_t*>(r.y) + at0 + (token * r.y_token + (h0 + grp) * r.y_head) * E::kBytes;
         long long c = at0 + (h0 + grp + (kKind == 2 ? p.k.heads : 0)) * head_bytes;
-        for (int h = h0 + grp; h - grp < h1; h += kAppendUnroll * R::kRows) {
-            typename R::Raw raw[kAppendUnroll];
+        typename R::Raw raw[kAppendUnroll];
+        auto load = [&](int u, int h) {
+            raw[u] = h < h1 ? R::load(x, x + to1) : R::zero();
+            x += xs;
+        };
 #pragma unroll
-            for (int u = 0; u < kAppendUnroll; ++u) {
-                raw[u] = h + u * R::kRows < h1 ? R::load(x, x + to1) : R::zero();
-                x += xs;
-            }
-            if (!found) find();
-            if (!mine) return;
+        for (int u = 0; u < kAppendUnroll; ++u) load(u, h0 + grp + u * R::kRows);
+        if (!found) find();
+        if (!mine) return;
+        for (int h = h0 + grp; h - grp < h1; h += kAppendUnroll * R::kRows) {
 #pragma unroll
             for (int u = 0; u < kAppendUnroll; ++u) {
                 if (u > 0 && h - grp + u * R::kRows >= h1) break;  // the same for the whole warp
@@ -159,8 +160,10 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int token, in
                         *reinterpret_cast<uint4*>(cache + c) = raw[u].c0;
                         *reinterpret_cast<uint4*>(cache + c + to1) = raw[u].c1;
                     }
+                    load(u, h + (kAppendUnroll + u) * R::kRows);
                 } else {
                     typename R::Pairs v = R::unpack(raw[u]);
+                    load(u, h + (kAppendUnroll + u) * R::kRows);
                     R::turn(v, coef, on, half, j, table, scratch);
                     if (in && r.y) R::store(y, y + to1, v);
                     if (kKind == 1 && in && cache) R::store(cache + c, cache + c + to1, v);

@@ -11,10 +11,10 @@
 // scale that grows by an exact division.
 //
 // Work: an item is one page of one request, in which the call's new tokens fill
-// some rows.  A CTA takes one item and up to eight heads, a warp each: it loads
-// up to 16 rows of K and of V, takes their largest magnitudes from the raw bits,
-// fixes the scales, rotates K from registers with the sines and cosines the CTA
-// shares, rounds and stores.  Longer pages run in groups of 16 rows and read
+// some rows.  A CTA takes one item and eight of its 2 * Hkv tasks (K or V, head), a
+// warp each: it loads up to 16 rows, takes their largest magnitude from the raw
+// bits, fixes the scale, rotates K from registers with the sines and cosines the
+// CTA shares, rounds and stores.  Longer pages run in groups of 16 rows and read
 // their rows a second time (out of L2).  Query rows are taken by further CTAs of
 // the same launch, as in append.cu.
 #include <cuda_runtime.h>
@@ -64,7 +64,7 @@ struct PageRows {
 
     // Rows 16 g .. of `rows` at x (the warp's token 0 and head), zeros beyond.
     __device__ __forceinline__ void load(const uint8_t* x, long long row_bytes, int g, int rows, int grp,
-                                         long long at0, long long at1) {
+                                         int at0, int at1) {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int r = g * kGroup + i * R::kRows + grp;
@@ -136,7 +136,7 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int e0, int e1, typena
 }
 
 template <typename E, int D, int kLayout>
-__global__ void __launch_bounds__(kPageWarps * 32, 2)
+__global__ void __launch_bounds__(kPageWarps * 32, 3)
 append_e4m3_kernel(const AppendParams p) {
     using R = Rope<E, D, kLayout>;
     using Rows = PageRows<E, D, kLayout>;
@@ -177,85 +177,70 @@ append_e4m3_kernel(const AppendParams p) {
     const int groups = (rows + kGroup - 1) / kGroup;
 
     const int Hkv = p.k.heads;
-    const int head = static_cast<int>(blockIdx.x % p.splits) * kPageWarps + warp;
-    const bool active = head < Hkv;
-    const long long at0 = R::first(j, half) * E::kBytes, at1 = R::second(j, half) * E::kBytes;
-    const uint8_t* xk = static_cast<const uint8_t*>(p.k.x) + (token0 * p.k.x_token + head * p.k.x_head) * E::kBytes;
-    const uint8_t* xv = static_cast<const uint8_t*>(p.v.x) + (token0 * p.v.x_token + head * p.v.x_head) * E::kBytes;
-    const long long k_row = p.k.x_token * E::kBytes, v_row = p.v.x_token * E::kBytes;
+    const int first_task = static_cast<int>(blockIdx.x % p.splits) * kPageWarps, task = first_task + warp;
+    const bool active = task < 2 * Hkv, is_v = task >= Hkv, cta_turns = first_task < Hkv && half > 0;
+    const int head = is_v ? task - Hkv : task;
+    const RopeRows& src = is_v ? p.v : p.k;
+    const int at0 = R::first(j, half), at1 = R::second(j, half);  // elements
+    const uint8_t* x = static_cast<const uint8_t*>(src.x) + (token0 * src.x_token + head * src.x_head) * E::kBytes;
+    const long long row_bytes = src.x_token * E::kBytes;
     const int mine = active ? rows : 0;  // rows this warp loads
+    Rows r;
+    r.load(x, row_bytes, 0, mine, grp, at0 * E::kBytes, at1 * E::kBytes);
     const int id = append_block(p, b, p.page.quotient(static_cast<int>(page0)));
     const bool write = active && id >= 0;
 
-    Rows k, v;
-    k.load(xk, k_row, 0, mine, grp, at0, at1);
-    v.load(xv, v_row, 0, mine, grp, at0, at1);
-    uint32_t mk = k.magnitude(), mv = v.magnitude();
+    uint32_t most = r.magnitude();
     for (int g = 1; g < groups; ++g) {
-        k.load(xk, k_row, g, mine, grp, at0, at1);
-        v.load(xv, v_row, g, mine, grp, at0, at1);
-        mk = __vmaxu2(mk, k.magnitude());
-        mv = __vmaxu2(mv, v.magnitude());
+        r.load(x, row_bytes, g, mine, grp, at0 * E::kBytes, at1 * E::kBytes);
+        most = __vmaxu2(most, r.magnitude());
     }
-    mk = __reduce_max_sync(0xffffffffu, max(mk & 0xffffu, mk >> 16));
-    mv = __reduce_max_sync(0xffffffffu, max(mv & 0xffffu, mv >> 16));
-    if (max(mk, mv) >= E::kInfinity) {  // infinities or NaN among them: the finite ones alone
-        mk = mv = 0;
+    most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+    if (most >= E::kInfinity) {  // infinities or NaN among them: the finite ones alone
+        most = 0;
         for (int g = 0; g < groups; ++g) {
-            if (groups > 1) {
-                k.load(xk, k_row, g, mine, grp, at0, at1);
-                v.load(xv, v_row, g, mine, grp, at0, at1);
-            }
-            mk = max(mk, k.finite());
-            mv = max(mv, v.finite());
+            if (groups > 1) r.load(x, row_bytes, g, mine, grp, at0 * E::kBytes, at1 * E::kBytes);
+            most = max(most, r.finite());
         }
-        mk = __reduce_max_sync(0xffffffffu, mk);
-        mv = __reduce_max_sync(0xffffffffu, mv);
+        most = __reduce_max_sync(0xffffffffu, most);
     }
-    const int64_t slot = static_cast<int64_t>(id) * 2 * Hkv + head;  // of K; V's is Hkv further
-    uint8_t* kb = p.cache + slot * p.page.size * D;
-    uint8_t* vb = kb + static_cast<int64_t>(Hkv) * p.page.size * D;
-    float ik = 0.0f, iv = 0.0f;
-    if (write) {
-        ik = 1.0f / settle_scale<D>(E::lo(mk), p.k_limit, r0, p.scales + slot, kb, lane);
-        iv = 1.0f / settle_scale<D>(E::lo(mv), kE4m3Max, r0, p.scales + slot + Hkv, vb, lane);
-    }
+    const int64_t slot = (static_cast<int64_t>(id) * 2 + (is_v ? 1 : 0)) * Hkv + head;
+    uint8_t* block = p.cache + slot * p.page.size * D;
+    float inv = 0.0f;
+    if (write)
+        inv = 1.0f / settle_scale<D>(E::lo(most), is_v ? kE4m3Max : p.k_limit, r0, p.scales + slot, block, lane);
 
     // From the last group, which is in registers, to the first.
     for (int g = groups - 1; g >= 0; --g) {
-        if (g != groups - 1) __syncthreads();  // the table of the group before has been read
         const int here = min(kGroup, rows - g * kGroup);
-        for (int i = threadIdx.x; i < here * (D / 2); i += kPageWarps * 32) {
-            const int rr = i / (D / 2), token = token0 + g * kGroup + rr;
-            rope_entry<D>(p.table, i % (D / 2), p.positions ? p.positions[token] : start + (token - rq.begin),
-                          s_table[rr]);
+        if (cta_turns) {
+            if (g != groups - 1) __syncthreads();  // the table of the group before has been read
+            for (int i = threadIdx.x; i < here * (D / 2); i += kPageWarps * 32) {
+                const int rr = i / (D / 2), token = token0 + g * kGroup + rr;
+                rope_entry<D>(p.table, i % (D / 2), p.positions ? p.positions[token] : start + (token - rq.begin),
+                              s_table[rr]);
+            }
+            __syncthreads();
         }
-        __syncthreads();
         if (!active) continue;
-        if (g != groups - 1) {
-            k.load(xk, k_row, g, mine, grp, at0, at1);
-            v.load(xv, v_row, g, mine, grp, at0, at1);
-        }
+        if (g != groups - 1) r.load(x, row_bytes, g, mine, grp, at0 * E::kBytes, at1 * E::kBytes);
 #pragma unroll
         for (int i = 0; i < Rows::kSteps; ++i) {
             if (i * R::kRows >= here) break;  // the same for the whole warp
             const int in_group = i * R::kRows + grp, rr = g * kGroup + in_group;
-            typename R::Pairs x = R::unpack(k.raw[i]);
-            typename R::Coef coef;
-            R::coefficients(s_table[in_group], j, coef);
-            R::turn(x, coef, on, half, j, s_table[in_group], scratch);
+            typename R::Pairs v = R::unpack(r.raw[i]);
+            if (!is_v && cta_turns) {
+                typename R::Coef coef;
+                R::coefficients(s_table[in_group], j, coef);
+                R::turn(v, coef, on, half, j, s_table[in_group], scratch);
+            }
             if (rr >= rows) continue;
-            if (p.k.y != nullptr) {
+            if (!is_v && p.k.y != nullptr) {
                 uint8_t* y = static_cast<uint8_t*>(p.k.y) +
                              ((token0 + rr) * p.k.y_token + head * p.k.y_head) * E::kBytes;
-                R::store(y + at0, y + at1, x);
+                R::store(y + at0 * E::kBytes, y + at1 * E::kBytes, v);
             }
-            if (!write) continue;
-            const int64_t at = static_cast<int64_t>(r0 + rr) * D;
-            const int e0 = static_cast<int>(at0) / E::kBytes, e1 = static_cast<int>(at1) / E::kBytes;
-            store_codes<R>(kb + at, e0, e1, x, ik);
-            x = R::unpack(v.raw[i]);
-            store_codes<R>(vb + at, e0, e1, x, iv);
+            if (write) store_codes<R>(block + static_cast<int64_t>(r0 + rr) * D, at0, at1, v, inv);
         }
     }
 }
@@ -287,7 +272,7 @@ cudaError_t launch_append_paged_e4m3(const AppendShape& s, const RopeShape& r, c
                     : kE4m3Max;
     // Request b's pages are items cu[b] / page + 2 b and on: it touches at most
     // n / page + 2 of them, so the ranges do not meet.
-    p.splits = static_cast<unsigned>((k.heads + kPageWarps - 1) / kPageWarps);
+    p.splits = static_cast<unsigned>((2 * k.heads + kPageWarps - 1) / kPageWarps);
     const long long items = s.total / s.page + 2ll * s.B;
     // The query heads' steps as in append.cu.
     const int step_rows = 32 * 16 / r.D;

@@ -22,7 +22,7 @@ namespace attn {
 namespace {
 
 constexpr int kRopeWarps = 4;
-constexpr int kRopeUnroll = 2;  // steps a lane has in flight
+constexpr int kRopeUnroll = 2;  // steps a lane has in flight: a step's registers are loaded again once unpacked
 
 struct RopeParams {
     RopeRows q, k;
@@ -63,29 +63,29 @@ rope_kernel(const RopeParams p) {
                            (b * r.x_batch + t * r.x_token + (h0 + grp) * r.x_head) * E::kBytes;
         uint8_t* y = static_cast<uint8_t*>(r.y) + at0 +
                      (b * r.y_batch + t * r.y_token + (h0 + grp) * r.y_head) * E::kBytes;
-        bool weighted = false;
-        for (int h = h0 + grp; h - grp < h1; h += kRopeUnroll * R::kRows) {
-            typename R::Raw raw[kRopeUnroll];
+        typename R::Raw raw[kRopeUnroll];
+        auto load = [&](int u, int h) {
+            raw[u] = h < h1 ? R::load(x, x + to1) : R::zero();
+            x += xs;
+        };
 #pragma unroll
-            for (int u = 0; u < kRopeUnroll; ++u) {
-                raw[u] = h + u * R::kRows < h1 ? R::load(x, x + to1) : R::zero();
-                x += xs;
-            }
-            if (!filled) {  // behind the first loads
-                rope_fill<D>(p.table, p.positions[token], lane, table);
-                filled = true;
-                if (!kNorm) R::coefficients(table, j, coef);
-            }
-            if (kNorm && !weighted) {
-                const uint8_t* row = static_cast<const uint8_t*>(w) + at0;
-                weight = w ? R::unpack(R::load(row, row + to1)) : R::ones();
-                R::coefficients(table, j, coef, &weight);
-                weighted = true;
-            }
+        for (int u = 0; u < kRopeUnroll; ++u) load(u, h0 + grp + u * R::kRows);
+        if (!filled) {  // behind the first loads
+            rope_fill<D>(p.table, p.positions[token], lane, table);
+            filled = true;
+            if (!kNorm) R::coefficients(table, j, coef);
+        }
+        if (kNorm) {
+            const uint8_t* row = static_cast<const uint8_t*>(w) + at0;
+            weight = w ? R::unpack(R::load(row, row + to1)) : R::ones();
+            R::coefficients(table, j, coef, &weight);
+        }
+        for (int h = h0 + grp; h - grp < h1; h += kRopeUnroll * R::kRows) {
 #pragma unroll
             for (int u = 0; u < kRopeUnroll; ++u) {
                 if (u > 0 && h - grp + u * R::kRows >= h1) break;  // the same for the whole warp
                 typename R::Pairs v = R::unpack(raw[u]);
+                load(u, h + (kRopeUnroll + u) * R::kRows);
                 float scale = 1.0f;
                 if (kNorm) {
                     scale = R::rms_scale(v, p.eps);
