@@ -8,12 +8,12 @@
 // with k_j, v_j the codes and ks_j, vs_j the scales of key j's block.  HBM bound:
 // 2 * D bytes per key and KV head are read once.  Half the bytes of the 16-bit
 // cache leave half the time per key, so the products go to the tensor cores
-// (mma.sync m16n8k16 in fp16, fp32 sums; the codes convert exactly): S = Q K^T
-// with the query heads of a KV head as rows and 8 keys as columns, and O^T =
-// V^T P^T with 16 columns of V as rows.  In that orientation the scores a lane
-// holds are the P^T operand it needs, and since the order of a product's inner
-// index is free, K's columns and V's rows are dealt to lanes so that each reads
-// 16 contiguous bytes.
+// (mma.sync m16n8k16 in fp16, fp32 sums; the codes convert exactly): S^T = K Q^T
+// with 16 keys as rows and eight query heads of their KV head as columns, and
+// O^T = V^T P^T with 16 columns of V as rows.  P^T's operand is S^T's result with
+// each 8 x 8 block transposed (movmatrix).  The order of a product's inner index
+// is free, so K's columns and V's rows are dealt to lanes so that each reads 16
+// contiguous bytes.
 //
 // Two running references.  The sum of the p_j is taken relative to 2^m, m a
 // maximum over x_j, in fp32.  What multiplies a code is w_j = p_j vs_j, taken
@@ -44,6 +44,9 @@ namespace {
 constexpr int kTile = 16;          // keys of a tile
 constexpr int kMaxPrefixB = 1024;  // requests whose tile counts a CTA sums itself
 constexpr float kSlack = 6.0f;
+// References start here: below any score, and finite, so that no difference of
+// two of them is NaN.
+constexpr float kLowest = -3.0e38f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct E4m3Params {
@@ -171,9 +174,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 (4) bytes into shared memory; bytes = 0 writes zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+// 16 (4) bytes into shared memory; 0 bytes of them: zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -203,14 +209,15 @@ __device__ __forceinline__ float elem_f32(uint16_t x) {
     return kF16 ? f16_lo_to_f32(x) : bf16_lo_to_f32(x);
 }
 
-// The state of the unit a warp is in.
+// The state of the unit a warp is in.  Lane (g, t) = (lane / 4, lane % 4) works
+// on heads 2t and 2t + 1 (of each half of eight).
 template <int D, int HC>
 struct UnitState {
-    static constexpr int kR = HC / 8;       // 8-head halves
-    uint32_t qa[D / 16][2 * kR];            // Q operand: row g (and g + 8), two halves of 16 columns
-    float qs[kR];                           // what a product with it is multiplied by
-    float m[kR], l[kR], mv[kR];             // head g (g + 8): reference, this lane's sum; O's reference
-    float o[kR][D / 16][4];                 // O^T: columns 2t, 2t + 1 of the heads
+    static constexpr int kR = HC / 8;       // halves of eight heads
+    uint32_t qb[D / 16][kR][2];             // Q^T operand: head g, two runs of inner indices
+    float qs[kR][2];                        // what a product with it is multiplied by
+    float m[kR][2], l[kR][2], mv[kR][2];    // reference and this lane's sum of the p; O's reference
+    float o[kR][D / 16][4];                 // O^T: two columns of V, two heads
 };
 
 // Q fragments of heads hq0 .. hq0 + heads - 1, each times a power of two that
@@ -248,16 +255,20 @@ __device__ __forceinline__ void unit_begin(const E4m3Params& p, const Cursor& c,
         const int e = static_cast<int>(__float_as_uint(most) >> 23);
         const int k = (e == 0 || e == 255) ? 0 : max(-126, min(126, 9 - (e - 127)));
         const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-        s.qs[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+        const float back = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+        s.qs[r][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+        s.qs[r][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
         // Product step j takes columns 4 j .. 4 j + 3 of the lane's: the first two as
         // inner indices 2t, 2t + 1, the others as 2t + 8, 2t + 9.
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
-            s.qa[i / 2][(i & 1) * (HC / 8) + r] =
+            s.qb[i / 2][r][i & 1] =
                 pack_f16x2(elem_f32<kF16>(w[i] & 0xffffu) * up, elem_f32<kF16>(w[i] >> 16) * up);
-        s.m[r] = -INFINITY;
-        s.mv[r] = -INFINITY;
-        s.l[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            s.m[r][i] = s.mv[r][i] = kLowest;
+            s.l[r][i] = 0.0f;
+        }
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -265,19 +276,30 @@ __device__ __forceinline__ void unit_begin(const E4m3Params& p, const Cursor& c,
     }
 }
 
-// Maximum of a head's scores in one tile: a lane's four, over its lane quad.
-__device__ __forceinline__ float row_max(const float (&x)[4]) {
-    float m = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+// Maximum over the lanes that hold the same heads.
+__device__ __forceinline__ float heads_max(float m) {
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+    return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+}
+__device__ __forceinline__ float heads_sum(float l) {
+    l += __shfl_xor_sync(0xffffffffu, l, 4);
+    l += __shfl_xor_sync(0xffffffffu, l, 8);
+    return l + __shfl_xor_sync(0xffffffffu, l, 16);
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 // Factor from sum w v to O: 2^(mv - m) / l.
 __device__ __forceinline__ float out_factor(float m, float l, float mv) { return ex2_approx(mv - m) / l; }
 
-// {m, sum, mv} of pieces, one in each of the first 2 * kHalf lanes (m = mv =
-// -infinity, sum = 0 where there is none): the common references {m, mv}, and the
-// sum relative to m, in those lanes.
+// {m, sum, mv} of pieces, one in each of the first 2 * kHalf lanes (kLowest, 0,
+// kLowest where there is none): the common references {m, mv}, and the sum
+// relative to m, in those lanes.
 template <int kHalf>
 __device__ __forceinline__ float2 merge_weights(const float4& e, float* sum) {
     float m = e.x, mv = e.z;
@@ -286,7 +308,7 @@ __device__ __forceinline__ float2 merge_weights(const float4& e, float* sum) {
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
     }
-    float l = e.x == -INFINITY ? 0.0f : e.y * ex2_approx(e.x - m);
+    float l = e.y * ex2_approx(e.x - m);
 #pragma unroll
     for (int o = kHalf; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     *sum = l;
@@ -296,118 +318,105 @@ __device__ __forceinline__ float2 merge_weights(const float4& e, float* sum) {
 // One tile of a warp's ring: scores, weights, and the weighted V rows.
 template <int D, int HC, bool kWholePages>
 __device__ __forceinline__ void unit_tile(const uint8_t* stage, int valid, int lane, UnitState<D, HC>& s) {
-    constexpr int kR = HC / 8;
+    constexpr int kR = HC / 8, kS = D / 16;
     const int g = lane >> 2, t = lane & 3;
     const uint8_t* vrows = stage + kTile * D;
     const float* ks = reinterpret_cast<const float*>(stage + 2 * kTile * D);
     const float* vs = ks + kTile;
-    float sc[2][4];
+    // Key g's and key g + 8's columns of this lane, four to a product step.
+    uint32_t kw[2][kS];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[n][i] = 0.0f;
         const int row = n * 8 + g;
-        uint32_t w[D / 16];
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
             const int chunk = D == 128 ? 2 * t + i : t;
             const uint4 u = *reinterpret_cast<const uint4*>(stage + row * D + chunk_at<D>(row, chunk) * 16);
-            w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
-        }
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            uint32_t b0, b1;
-            e4m3_to_f16x4(w[j], b0, b1);
-            mma_f16(sc[n], s.qa[j][0], kR == 2 ? s.qa[j][1] : 0u, s.qa[j][kR], kR == 2 ? s.qa[j][kR + 1] : 0u, b0,
-                    b1);
+            kw[n][4 * i] = u.x; kw[n][4 * i + 1] = u.y; kw[n][4 * i + 2] = u.z; kw[n][4 * i + 3] = u.w;
         }
     }
-    // Factors and lifts (log2 of V's scales) of the lane's keys: one pair for a
-    // tile inside one page, else one for each key.
-    constexpr int kF = kWholePages ? 1 : 4;
-    float kk[kF], lift[kF];
-    if (kWholePages) {
-        kk[0] = ks[0];
-        lift[0] = __log2f(vs[0]);
-    } else {
+    uint32_t vw[4][D / 32];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const float2 k2 = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * t);
-            const float2 v2 = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * t);
-            kk[2 * n % kF] = k2.x;
-            kk[(2 * n + 1) % kF] = k2.y;
-            lift[2 * n % kF] = __log2f(v2.x);
-            lift[(2 * n + 1) % kF] = __log2f(v2.y);
-        }
+    for (int j = 0; j < 4; ++j) load_v<D>(vrows, 2 * t + (j & 1) + 8 * (j >> 1), g, vw[j]);
+    float sc[kR][4], sd[kR][4];  // two chains of products
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[r][i] = sd[r][i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kS; ++j) {
+        uint32_t a0, a1, a2, a3;
+        e4m3_to_f16x4(kw[0][j], a0, a2);
+        e4m3_to_f16x4(kw[1][j], a1, a3);
+#pragma unroll
+        for (int r = 0; r < kR; ++r) mma_f16((j & 1) ? sd[r] : sc[r], a0, a1, a2, a3, s.qb[j][r][0], s.qb[j][r][1]);
+    }
+    // V^T's operand, while the products run: bytes 2i, 2i + 1 of two keys' words are
+    // (k0, k1) of one column, then of the next.
+    uint32_t va[kS][4];
+#pragma unroll
+    for (int i = 0; i < kS; ++i) {
+        const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+        e4m3_to_f16x4(__byte_perm(vw[0][i / 2], vw[1][i / 2], sel), va[i][0], va[i][1]);
+        e4m3_to_f16x4(__byte_perm(vw[2][i / 2], vw[3][i / 2], sel), va[i][2], va[i][3]);
+    }
+    // Factors and lifts (log2 of V's scales) of keys g and g + 8: one pair for a tile
+    // inside one page.
+    constexpr int kF = kWholePages ? 1 : 2;
+    float kk[kF], lift[kF];
+#pragma unroll
+    for (int n = 0; n < kF; ++n) {
+        kk[n] = ks[kWholePages ? 0 : n * 8 + g];
+        lift[n] = __log2f(vs[kWholePages ? 0 : n * 8 + g]);
     }
     float x[kR][4];  // exponents of p; those of w are x + lift
-    bool need = false;
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        const float f = kk[0] * s.qs[r];
+    for (int r = 0; r < kR; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            x[r][i] = sc[i >> 1][2 * r + (i & 1)] * (kWholePages ? f : kk[i % kF] * s.qs[r]);
-    }
+        for (int i = 0; i < 4; ++i) x[r][i] = (sc[r][i] + sd[r][i]) * (kk[(i >> 1) % kF] * s.qs[r][i & 1]);
     if (valid < kTile) {  // the unit's last tile
 #pragma unroll
         for (int r = 0; r < kR; ++r)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if ((i >> 1) * 8 + 2 * t + (i & 1) >= valid) x[r][i] = -INFINITY;
+                if ((i >> 1) * 8 + g >= valid) x[r][i] = -INFINITY;
     }
+    bool need = false;
 #pragma unroll
     for (int r = 0; r < kR; ++r)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            need |= x[r][i] > fminf(s.m[r], s.mv[r] - lift[i % kF]) + kSlack;
+            need |= x[r][i] > fminf(s.m[r][i & 1], s.mv[r][i & 1] - lift[(i >> 1) % kF]) + kSlack;
     if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
-            float y[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = x[r][i] + lift[i % kF];
-            const float m = fmaxf(s.m[r], row_max(x[r])), mv = fmaxf(s.mv[r], row_max(y));
-            s.l[r] *= s.m[r] == -INFINITY ? 0.0f : ex2_approx(s.m[r] - m);
-            const float alpha = s.mv[r] == -INFINITY ? 0.0f : ex2_approx(s.mv[r] - mv);
-            s.m[r] = m;
-            s.mv[r] = mv;
-            const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t), a1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
+            for (int i = 0; i < 2; ++i) {
+                const float m = fmaxf(s.m[r][i], heads_max(fmaxf(x[r][i], x[r][i + 2])));
+                const float mv = fmaxf(s.mv[r][i], heads_max(fmaxf(x[r][i] + lift[0], x[r][i + 2] + lift[kF - 1])));
+                const float alpha = ex2_approx(s.mv[r][i] - mv);
+                s.l[r][i] *= ex2_approx(s.m[r][i] - m);
+                s.m[r][i] = m;
+                s.mv[r][i] = mv;
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                s.o[r][j][0] *= a0; s.o[r][j][1] *= a1; s.o[r][j][2] *= a0; s.o[r][j][3] *= a1;
+                for (int j = 0; j < kS; ++j) {
+                    s.o[r][j][i] *= alpha;
+                    s.o[r][j][i + 2] *= alpha;
+                }
             }
         }
     }
-    uint32_t pb[kR][2];
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-        const float m = s.m[r] == -INFINITY ? 0.0f : s.m[r], mv = s.mv[r] == -INFINITY ? 0.0f : s.mv[r];
         float w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            s.l[r] += ex2_approx(x[r][i] - m);
-            w[i] = ex2_approx(x[r][i] + (lift[i % kF] - mv));
+            s.l[r][i & 1] += ex2_approx(x[r][i] - s.m[r][i & 1]);
+            w[i] = ex2_approx(x[r][i] + (lift[(i >> 1) % kF] - s.mv[r][i & 1]));
         }
-        pb[r][0] = pack_f16x2(w[0], w[1]);
-        pb[r][1] = pack_f16x2(w[2], w[3]);
-    }
-    uint32_t vw[4][D / 32];
+        const uint32_t b0 = transpose8x8(pack_f16x2(w[0], w[1])), b1 = transpose8x8(pack_f16x2(w[2], w[3]));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load_v<D>(vrows, 2 * t + (j & 1) + 8 * (j >> 1), g, vw[j]);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            // Bytes 2 half, 2 half + 1 of two keys' words: (k0, k1) of one column, then of the next.
-            const uint32_t sel = half ? 0x7362u : 0x5140u;
-            const uint32_t lo = __byte_perm(vw[0][i], vw[1][i], sel), hi = __byte_perm(vw[2][i], vw[3][i], sel);
-            uint32_t a0, a1, a2, a3;
-            e4m3_to_f16x4(lo, a0, a1);
-            e4m3_to_f16x4(hi, a2, a3);
-#pragma unroll
-            for (int r = 0; r < kR; ++r) mma_f16(s.o[r][2 * i + half], a0, a1, a2, a3, pb[r][0], pb[r][1]);
-        }
+        for (int i = 0; i < kS; ++i) mma_f16(s.o[r][i], va[i][0], va[i][1], va[i][2], va[i][3], b0, b1);
     }
 }
 
@@ -434,7 +443,7 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
     constexpr int kR = HC / 8, kCols = D / 8;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = lane >> 2, t = lane & 3;
+    const int g = lane >> 2, t = lane & 3;  // as in UnitState
     uint8_t* ring = smem + warp * L::kStages * L::kStage;
     float4* ml = reinterpret_cast<float4*>(smem + L::kMlOff);
     PieceMeta* meta = reinterpret_cast<PieceMeta*>(smem + L::kMetaOff);
@@ -474,74 +483,71 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
         if (threadIdx.x == 0) p.first[blockIdx.x] = make_int4(lc.b, lc.unit, lc.tile, lc.tiles);  // va = v0
         int loaded = 0;  // tiles whose copies have been issued
         // The next tile to copy: its block ids are loaded one step ahead.
-        int id = 0, row = 0;
+        int id = 0, row = 0, page = 0;
         auto look_up = [&]() {
-            if (kWholePages) {  // the tile lies in one page
-                const int pg = p.page.split(lc.tile * kTile, &row);
-                id = p.block_table[static_cast<int64_t>(lc.b) * p.max_pages + pg];
-            } else {
-                const int key = lc.tile * kTile + (lane & 15);
-                const int pg = p.page.split(key < lc.len ? key : lc.len - 1, &row);
-                id = p.block_table[static_cast<int64_t>(lc.b) * p.max_pages + pg];
-            }
+            const int key = lc.tile * kTile + (kWholePages ? 0 : lane & 15);
+            page = p.page.split(kWholePages || key < lc.len ? key : lc.len - 1, &row);
+            id = p.block_table[static_cast<int64_t>(lc.b) * p.max_pages + page];
         };
         look_up();
-        // Where a lane's copies go in a stage: row r0 + i * kRowsPer, chunk col.
-        constexpr int kPerRow = D / 16, kRowsPer = 32 / kPerRow;
+        // Where a lane's copies go in a stage: row r0 + i * kRowsPer, chunk col.  The
+        // chunks' order repeats every eight rows.
+        constexpr int kPerRow = D / 16, kRowsPer = 32 / kPerRow, kCopies = kTile / kRowsPer;
         const int r0 = lane / kPerRow, col = lane % kPerRow;
-        int put[kTile / kRowsPer];
-#pragma unroll
-        for (int i = 0; i < kTile / kRowsPer; ++i)
-            put[i] = (r0 + i * kRowsPer) * D + chunk_at<D>(r0 + i * kRowsPer, col) * 16;
-        const int64_t to_v = static_cast<int64_t>(p.Hkv) * p.page.size * D;
+        const int put0 = r0 * D + chunk_at<D>(r0, col) * 16;
+        const int put1 = (r0 + kRowsPer) * D + chunk_at<D>(r0 + kRowsPer, col) * 16;
+        auto put = [&](int i) { return ((i & 1) ? put1 : put0) + (i / 2) * 2 * kRowsPer * D; };
+        const int64_t page_bytes = static_cast<int64_t>(p.page.size) * D, to_v = p.Hkv * page_bytes;
         const uint32_t ring32 = smem_u32(ring);
         uint32_t fill = ring32;  // the stage copied into next
         auto issue = [&]() {
             if (loaded < count) {
-                if (id < 0 || id >= p.num_blocks) {
+                if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) {
                     atomicOr(p.status, ATTN_DEV_BAD_INPUT);
                     id = 0;
                 }
                 const int hkv = p.chunks == 1 ? lc.unit : lc.unit / p.chunks;
-                const int valid = min(kTile, lc.len - lc.tile * kTile);
-                const int64_t block = static_cast<int64_t>(id) * 2 * p.Hkv + hkv;  // of K; V's is Hkv further
+                const int valid = lc.len - lc.tile * kTile;  // 16 and more: the whole tile
+                const int64_t block = static_cast<int64_t>(id) * (2 * p.Hkv) + hkv;  // of K; V's is Hkv further
                 // Lanes 0 .. 15: K's scales, 16 .. 31: V's (a tile in one page: lanes 0 and 16).
                 if (kWholePages ? (lane & 15) == 0 : true)
                     copy4(fill + 2 * kTile * D + lane * 4, p.scales + block + (lane >> 4) * p.Hkv,
                           (lane & 15) < valid ? 4 : 0);
                 if (kWholePages) {  // one run of rows
-                    const uint8_t* src = p.kv + (block * p.page.size + row) * D + lane * 16;
-                    if (valid == kTile) {
+                    const uint8_t* src = p.kv + block * page_bytes + (row * D + lane * 16);
+                    if (valid >= kTile) {
 #pragma unroll
-                        for (int i = 0; i < kTile / kRowsPer; ++i) {
-                            copy16(fill + put[i], src + i * 512, 16);
-                            copy16(fill + kTile * D + put[i], src + to_v + i * 512, 16);
+                        for (int i = 0; i < kCopies; ++i) {
+                            copy16(fill + put(i), src + i * 512);
+                            copy16(fill + kTile * D + put(i), src + to_v + i * 512);
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < kTile / kRowsPer; ++i) {
+                        for (int i = 0; i < kCopies; ++i) {
                             const bool in = r0 + i * kRowsPer < valid;
                             const uint8_t* at = in ? src + i * 512 : p.kv;
-                            copy16(fill + put[i], at, in ? 16 : 0);
-                            copy16(fill + kTile * D + put[i], in ? at + to_v : p.kv, in ? 16 : 0);
+                            copy16_or_zero(fill + put(i), at, in);
+                            copy16_or_zero(fill + kTile * D + put(i), in ? at + to_v : p.kv, in);
                         }
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < kTile / kRowsPer; ++i) {
+                    for (int i = 0; i < kCopies; ++i) {
                         const int r = r0 + i * kRowsPer;
                         const int rid = __shfl_sync(0xffffffffu, id, r), rrow = __shfl_sync(0xffffffffu, row, r);
                         const uint8_t* src = p.kv +
-                            ((static_cast<int64_t>(rid) * 2 * p.Hkv + hkv) * p.page.size + rrow) * D + col * 16;
-                        copy16(fill + put[i], src, r < valid ? 16 : 0);
-                        copy16(fill + kTile * D + put[i], src + to_v, r < valid ? 16 : 0);
+                            (static_cast<int64_t>(rid) * (2 * p.Hkv) + hkv) * page_bytes + (rrow * D + col * 16);
+                        copy16_or_zero(fill + put(i), src, r < valid);
+                        copy16_or_zero(fill + kTile * D + put(i), src + to_v, r < valid);
                     }
                 }
                 fill += L::kStage;
                 if (fill == ring32 + L::kStages * L::kStage) fill = ring32;
                 if (++loaded < count) {
+                    const int tile = lc.tile;
                     cursor_next(p, cum, lc);
-                    look_up();
+                    if (kWholePages && lc.tile == tile + 1 && row + kTile < p.page.size) row += kTile;  // the same page
+                    else look_up();
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -578,36 +584,30 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
             }
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
-                float l = s.l[r];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
                 const int h0 = r * 8 + 2 * t;
-                float c0[kCols], c1[kCols];
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    c0[2 * j] = s.o[r][j][0]; c0[2 * j + 1] = s.o[r][j][2];
-                    c1[2 * j] = s.o[r][j][1]; c1[2 * j + 1] = s.o[r][j][3];
-                }
-                if (whole) {
-                    const float f = out_factor(s.m[r], l, s.mv[r]);
-                    const float i0 = __shfl_sync(0xffffffffu, f, 8 * t), i1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+                for (int i = 0; i < 2; ++i) {
+                    const int h = h0 + i;
+                    const float l = heads_sum(s.l[r][i]);
+                    float c[kCols];
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i) {
-                        c0[i] *= i0;
-                        c1[i] *= i1;
+                    for (int j = 0; j < D / 16; ++j) {
+                        c[2 * j] = s.o[r][j][i];
+                        c[2 * j + 1] = s.o[r][j][i + 2];
                     }
-                    if (h0 < heads) store_row<kF16>(p.o + (row0 + h0) * D + g * kCols, c0);
-                    if (h0 + 1 < heads) store_row<kF16>(p.o + (row0 + h0 + 1) * D + g * kCols, c1);
-                    if (p.lse && t == 0 && r * 8 + g < heads) p.lse[row0 + r * 8 + g] = (s.m[r] + __log2f(l)) * kLn2;
-                } else {
+                    if (whole) {
+                        const float f = out_factor(s.m[r][i], l, s.mv[r][i]);
 #pragma unroll
-                    for (int i = 0; i < kCols; i += 4) {
-                        *reinterpret_cast<float4*>(piece + h0 * D + g * kCols + i) =
-                            make_float4(c0[i], c0[i + 1], c0[i + 2], c0[i + 3]);
-                        *reinterpret_cast<float4*>(piece + (h0 + 1) * D + g * kCols + i) =
-                            make_float4(c1[i], c1[i + 1], c1[i + 2], c1[i + 3]);
+                        for (int k = 0; k < kCols; ++k) c[k] *= f;
+                        if (h < heads) store_row<kF16>(p.o + (row0 + h) * D + g * kCols, c);
+                        if (p.lse && g == 0 && h < heads) p.lse[row0 + h] = (s.m[r][i] + __log2f(l)) * kLn2;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < kCols; k += 4)
+                            *reinterpret_cast<float4*>(piece + h * D + g * kCols + k) =
+                                make_float4(c[k], c[k + 1], c[k + 2], c[k + 3]);
+                        if (g == 0) ml[(2 * warp + pieces) * HC + h] = make_float4(s.m[r][i], l, s.mv[r][i], 0.0f);
                     }
-                    if (t == 0) ml[(2 * warp + pieces) * HC + r * 8 + g] = make_float4(s.m[r], l, s.mv[r], 0.0f);
                 }
             }
             if (!whole) {
@@ -653,13 +653,13 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
             if (dealt % kWarps != warp) continue;
             // Lane i: the i-th piece's references, sum and weight.
             const float4 e = lane < n ? ml[(lane == 0 ? from : 2 * (w0 + lane)) * HC + h]
-                                      : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+                                      : make_float4(kLowest, 0.0f, kLowest, 0.0f);
             float l;
             float2 m = merge_weights<8>(e, &l);
             m.x = __shfl_sync(0xffffffffu, m.x, 0);
             m.y = __shfl_sync(0xffffffffu, m.y, 0);
             l = __shfl_sync(0xffffffffu, l, 0);
-            const float weight = e.z == -INFINITY ? 0.0f : ex2_approx(e.z - m.y);
+            const float weight = ex2_approx(e.z - m.y);
             float acc[D / 32];
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
@@ -717,11 +717,11 @@ __global__ void __launch_bounds__(kCombineThreads) decode_e4m3_combine_kernel(co
     for (int h0 = blockIdx.y * abreast; h0 < heads; h0 += gridDim.y * abreast) {
         const int h = min(heads - 1, h0 + row % abreast);
         // References and sum over all pieces, by every warp.
-        float4 e = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+        float4 e = make_float4(kLowest, 0.0f, kLowest, 0.0f);
         for (int i = lane; i < n; i += 32) {
             const float4 x = p.ws_ml[(i == 0 ? slot0 : 2 * (c0 + i)) * HC + h];
             const float m = fmaxf(e.x, x.x);
-            e.y = (e.x == -INFINITY ? 0.0f : e.y * ex2_approx(e.x - m)) + (x.x == -INFINITY ? 0.0f : x.y * ex2_approx(x.x - m));
+            e.y = e.y * ex2_approx(e.x - m) + x.y * ex2_approx(x.x - m);
             e.x = m;
             e.z = fmaxf(e.z, x.z);
         }
@@ -731,8 +731,7 @@ __global__ void __launch_bounds__(kCombineThreads) decode_e4m3_combine_kernel(co
 #pragma unroll 4
         for (int i = sharer; i < n; i += sharers) {
             const long long slot = (i == 0 ? slot0 : 2 * (c0 + i)) * HC + h;
-            const float z = p.ws_ml[slot].z;
-            acc = fmaf(p.ws_o[slot * D + d], z == -INFINITY ? 0.0f : ex2_approx(z - m.y), acc);
+            acc = fmaf(p.ws_o[slot * D + d], ex2_approx(p.ws_ml[slot].z - m.y), acc);
         }
         if (sharers > 1) {
             s_acc[row][d] = acc;
