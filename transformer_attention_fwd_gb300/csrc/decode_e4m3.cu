@@ -27,7 +27,10 @@
 // warp streams its tiles through a ring of its own with 16-byte asynchronous
 // copies; nothing in the loop waits for another warp.  Units inside one warp's
 // range are written at once; the pieces of the others are merged in the CTA at
-// its end, and those that a CTA boundary cuts by the combine kernel.
+// its end, and those that a CTA boundary cuts by the combine kernel.  Two
+// small CTAs share an SM, so that one's start and end pass under the other's
+// streaming.  (More of them than fit at once, to even out the SMs, lost 5 us for
+// each further wave: a start costs that much.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -43,6 +46,7 @@ namespace {
 
 constexpr int kTile = 16;          // keys of a tile
 constexpr int kMaxPrefixB = 1024;  // requests whose tile counts a CTA sums itself
+constexpr int kPerSm = 2;  // CTAs
 constexpr float kSlack = 6.0f;
 // References start here: below any score, and finite, so that no difference of
 // two of them is NaN.
@@ -70,18 +74,23 @@ struct E4m3Params {
 
 template <int D, int HC>
 struct E4m3Layout {
-    static constexpr int kWarps = 8;
+    static constexpr int kWarps = 4;
     static constexpr int kStage = 2 * kTile * D + 2 * kTile * 4;  // K rows, V rows, scales
     static constexpr int kPiece = HC * D * 4;
-    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kStages = D == 128 ? 4 : 8;
     static constexpr int kPieceOff = kWarps * kStages * kStage;
     static constexpr int kMlOff = kPieceOff + kWarps * kPiece;  // [warp][2][HC] float4
     static constexpr int kMetaOff = kMlOff + kWarps * 2 * HC * 16;
     static constexpr int kCumOff = kMetaOff + kWarps * 2 * 16;
     static constexpr int kBytes = kCumOff + (kMaxPrefixB + 1) * 8 + 40 * 8;
     static_assert(kStages * kStage >= kPiece, "a warp's ring holds its second piece");
-    static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
+    static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "CTAs to an SM");
 };
+
+// n / d for n, d >= 0: most fit in 32 bits, whose division is several times shorter.
+__device__ __forceinline__ long long divide(long long n, int d) {
+    return (n >> 32) == 0 ? static_cast<long long>(static_cast<unsigned>(n) / static_cast<unsigned>(d)) : n / d;
+}
 
 // One place in the sequence of tiles.
 struct Cursor {
@@ -106,7 +115,7 @@ __device__ __forceinline__ Cursor cursor_at(const E4m3Params& p, const long long
     c.b = lo;
     c.tiles = static_cast<int>(cum[lo + 1] - cum[lo]);
     const long long r = v - cum[lo] * U;
-    c.unit = static_cast<int>(r / c.tiles);
+    c.unit = static_cast<int>(divide(r, c.tiles));
     c.tile = static_cast<int>(r - static_cast<long long>(c.unit) * c.tiles);
     c.len = clamped_len(p, lo);
     return c;
@@ -160,9 +169,10 @@ __global__ void __launch_bounds__(1024) e4m3_prefix_kernel(const E4m3Params p) {
     tile_prefix(p, p.cum, scan, true);
 }
 
+// Tiles of a CTA's slice: at least one a warp.
 __device__ __forceinline__ long long slice_tiles(long long total, int grid, int warps) {
-    const long long per = (total + grid - 1) / grid;
-    return per < warps ? warps : per;  // at least one tile a warp
+    const long long per = divide(total + grid - 1, grid);
+    return per < warps ? warps : per;
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -226,7 +236,7 @@ template <int D, int HC, bool kF16>
 __device__ __forceinline__ void unit_begin(const E4m3Params& p, const Cursor& c, int lane,
                                            UnitState<D, HC>& s) {
     const int g = lane >> 2, t = lane & 3;
-    const int hkv = c.unit / p.chunks, chunk = c.unit - hkv * p.chunks;
+    const int hkv = p.chunks == 1 ? c.unit : c.unit / p.chunks, chunk = c.unit - hkv * p.chunks;
     const int heads = min(HC, p.group - chunk * HC);
     const int hq0 = hkv * p.group + chunk * HC;
 #pragma unroll
@@ -297,23 +307,57 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // Factor from sum w v to O: 2^(mv - m) / l.
 __device__ __forceinline__ float out_factor(float m, float l, float mv) { return ex2_approx(mv - m) / l; }
 
-// {m, sum, mv} of pieces, one in each of the first 2 * kHalf lanes (kLowest, 0,
-// kLowest where there is none): the common references {m, mv}, and the sum
-// relative to m, in those lanes.
-template <int kHalf>
-__device__ __forceinline__ float2 merge_weights(const float4& e, float* sum) {
-    float m = e.x, mv = e.z;
-#pragma unroll
-    for (int o = kHalf; o > 0; o >>= 1) {
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-    }
-    float l = e.y * ex2_approx(e.x - m);
-#pragma unroll
-    for (int o = kHalf; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    *sum = l;
-    return make_float2(m, mv);
+// Folds {m, sum, mv} of a piece into e.
+__device__ __forceinline__ void fold(float4& e, const float4& x) {
+    const float m = fmaxf(e.x, x.x);
+    e.y = e.y * ex2_approx(e.x - m) + x.y * ex2_approx(x.x - m);
+    e.x = m;
+    e.z = fmaxf(e.z, x.z);
 }
+// The same over lanes kFrom, 2 kFrom, .. 16 apart; every lane gets the result.
+template <int kFrom>
+__device__ __forceinline__ void fold_lanes(float4& e) {
+    float m = e.x;
+#pragma unroll
+    for (int o = kFrom; o < 32; o <<= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        e.z = fmaxf(e.z, __shfl_xor_sync(0xffffffffu, e.z, o));
+    }
+    e.y *= ex2_approx(e.x - m);
+    e.x = m;
+#pragma unroll
+    for (int o = kFrom; o < 32; o <<= 1) e.y += __shfl_xor_sync(0xffffffffu, e.y, o);
+}
+
+// A lane's D/32 neighbouring columns.
+template <int D>
+struct Columns {
+    float c[D / 32];
+    __device__ __forceinline__ void load(const float* row, int lane) {
+        if constexpr (D == 128) {
+            const float4 v = reinterpret_cast<const float4*>(row)[lane];
+            c[0] = v.x; c[1] = v.y; c[2] = v.z; c[3] = v.w;
+        } else {
+            const float2 v = reinterpret_cast<const float2*>(row)[lane];
+            c[0] = v.x; c[1] = v.y;
+        }
+    }
+    __device__ __forceinline__ void store(float* row, int lane) const {
+        if constexpr (D == 128) reinterpret_cast<float4*>(row)[lane] = make_float4(c[0], c[1], c[2], c[3]);
+        else reinterpret_cast<float2*>(row)[lane] = make_float2(c[0], c[1]);
+    }
+    __device__ __forceinline__ void add(const Columns& x, float w) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) c[i] = fmaf(x.c[i], w, c[i]);
+    }
+    template <bool kF16>
+    __device__ __forceinline__ void store16(uint16_t* row, int lane, float f) const {
+        using E = Elem16<kF16>;
+        if constexpr (D == 128)
+            reinterpret_cast<uint2*>(row)[lane] = make_uint2(E::pack(c[0] * f, c[1] * f), E::pack(c[2] * f, c[3] * f));
+        else reinterpret_cast<uint32_t*>(row)[lane] = E::pack(c[0] * f, c[1] * f);
+    }
+};
 
 // One tile of a warp's ring: scores, weights, and the weighted V rows.
 template <int D, int HC, bool kWholePages>
@@ -431,12 +475,12 @@ __device__ __forceinline__ void store_row(uint16_t* dst, const float (&v)[N]) {
 
 // What a warp leaves of a unit it has not covered alone.
 struct PieceMeta {
-    long long unit;  // request * units + unit, -1: none
+    long long unit;  // request << 32 | unit, -1: none
     int begins, ends;  // the piece holds the unit's first (last) tile; begins = 2: not at the slice's start
 };
 
 template <int D, int HC, bool kF16, bool kWholePages>
-__global__ void __launch_bounds__(E4m3Layout<D, HC>::kWarps * 32, 1)
+__global__ void __launch_bounds__(E4m3Layout<D, HC>::kWarps * 32, kPerSm)
 decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
     using L = E4m3Layout<D, HC>;
     constexpr int kWarps = L::kWarps;
@@ -573,7 +617,7 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
                 continue;
             }
             // The unit, or this warp's part of it, is done.
-            const int hkv = cc.unit / p.chunks, chunk = cc.unit - hkv * p.chunks;
+            const int hkv = p.chunks == 1 ? cc.unit : cc.unit / p.chunks, chunk = cc.unit - hkv * p.chunks;
             const int heads = min(HC, p.group - chunk * HC);
             const int64_t row0 = static_cast<int64_t>(cc.b) * p.Hq + hkv * p.group + chunk * HC;
             const bool whole = unit_done && from == 0;
@@ -613,7 +657,7 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
             if (!whole) {
                 if (lane == 0) {
                     const long long at = va + n - (cc.tile - from);  // the piece's first tile in the sequence
-                    meta[2 * warp + pieces] = PieceMeta{static_cast<long long>(cc.b) * U + cc.unit,
+                    meta[2 * warp + pieces] = PieceMeta{(static_cast<long long>(cc.b) << 32) | cc.unit,
                                                         from == 0 ? (at > v0 ? 2 : 1) : 0, unit_done ? 1 : 0};
                 }
                 ++pieces;
@@ -634,7 +678,6 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
     const long long place = lane < 2 * kWarps ? meta[lane].unit : -1;
     const long long back1 = __shfl_up_sync(0xffffffffu, place, 1), back2 = __shfl_up_sync(0xffffffffu, place, 2);
     const bool is_first = place >= 0 && ((lane & 1) || lane == 0 || (back1 >= 0 ? back1 : back2) != place);
-    int dealt = 0;
     for (unsigned left = __ballot_sync(0xffffffffu, is_first); left != 0; left &= left - 1) {
         const int from = __ffs(left) - 1, w0 = from >> 1;
         const PieceMeta head_piece = meta[from];
@@ -642,45 +685,48 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
             __ballot_sync(0xffffffffu, place == head_piece.unit && lane > from && (lane & 1) == 0);
         const int n = 1 + __popc(others);
         const bool ends = n == 1 ? head_piece.ends : meta[2 * (w0 + n - 1)].ends;
-        const int b = static_cast<int>(head_piece.unit / U);
-        const int unit = static_cast<int>(head_piece.unit - static_cast<long long>(b) * U);
-        const int hkv = unit / p.chunks, chunk = unit - hkv * p.chunks;
+        const int b = static_cast<int>(head_piece.unit >> 32), unit = static_cast<int>(head_piece.unit & 0x7fffffff);
+        const int hkv = p.chunks == 1 ? unit : unit / p.chunks, chunk = unit - hkv * p.chunks;
         const int heads = min(HC, p.group - chunk * HC);
         const int64_t row0 = static_cast<int64_t>(b) * p.Hq + hkv * p.group + chunk * HC;
         const bool whole = head_piece.begins && ends;
         const int64_t ws = 2ll * blockIdx.x + (head_piece.begins == 2 ? 1 : 0);
-        for (int h = 0; h < heads; ++h, ++dealt) {
-            if (dealt % kWarps != warp) continue;
-            // Lane i: the i-th piece's references, sum and weight.
-            const float4 e = lane < n ? ml[(lane == 0 ? from : 2 * (w0 + lane)) * HC + h]
-                                      : make_float4(kLowest, 0.0f, kLowest, 0.0f);
-            float l;
-            float2 m = merge_weights<8>(e, &l);
-            m.x = __shfl_sync(0xffffffffu, m.x, 0);
-            m.y = __shfl_sync(0xffffffffu, m.y, 0);
-            l = __shfl_sync(0xffffffffu, l, 0);
-            const float weight = ex2_approx(e.z - m.y);
-            float acc[D / 32];
+        // Lane h + HC * k: the references, sums and weights of head h's pieces k, k + 32 / HC, ..
+        constexpr int kApart = 32 / HC, kHeld = (kWarps + kApart - 1) / kApart;
+        float4 e[kHeld], all = make_float4(kLowest, 0.0f, kLowest, 0.0f);
+        float weight[kHeld];
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
-            for (int k = 0; k < n; ++k) {
-                const float wt = __shfl_sync(0xffffffffu, weight, k);
-                const float* piece = reinterpret_cast<const float*>(
-                    k == 0 && (from & 1) ? smem + w0 * L::kStages * L::kStage : smem + L::kPieceOff + (w0 + k) * L::kPiece);
+        for (int i = 0; i < kHeld; ++i) {
+            const int k = lane / HC + i * kApart;
+            e[i] = k < n ? ml[(k == 0 ? from : 2 * (w0 + k)) * HC + lane % HC] : make_float4(kLowest, 0.0f, kLowest, 0.0f);
+            fold(all, e[i]);
+        }
+        fold_lanes<HC>(all);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(piece[h * D + i * 32 + lane], wt, acc[i]);
+        for (int i = 0; i < kHeld; ++i) weight[i] = ex2_approx(e[i].z - all.z);
+#pragma unroll
+        for (int i = 0; i < HC / kWarps; ++i) {
+            const int h = warp + i * kWarps;
+            Columns<D> acc{};
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float wt = __shfl_sync(0xffffffffu, weight[k / kApart], h + HC * (k % kApart));
+                if (k >= n) continue;
+                Columns<D> x;
+                x.load(reinterpret_cast<const float*>(k == 0 && (from & 1) ? smem + w0 * L::kStages * L::kStage
+                                                                           : smem + L::kPieceOff + (w0 + k) * L::kPiece) + h * D,
+                       lane);
+                acc.add(x, wt);
             }
+            const float m = __shfl_sync(0xffffffffu, all.x, h), l = __shfl_sync(0xffffffffu, all.y, h);
+            const float mv = __shfl_sync(0xffffffffu, all.z, h);
+            if (h >= heads) continue;
             if (whole) {
-                const float f = out_factor(m.x, l, m.y);
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i)
-                    p.o[(row0 + h) * D + i * 32 + lane] =
-                        static_cast<uint16_t>(Elem16<kF16>::pack(acc[i] * f, 0.0f) & 0xffffu);
-                if (p.lse && lane == 0) p.lse[row0 + h] = (m.x + __log2f(l)) * kLn2;
+                acc.template store16<kF16>(p.o + (row0 + h) * D, lane, out_factor(m, l, mv));
+                if (p.lse && lane == 0) p.lse[row0 + h] = (m + __log2f(l)) * kLn2;
             } else {
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) p.ws_o[(ws * HC + h) * D + i * 32 + lane] = acc[i];
-                if (lane == 0) p.ws_ml[ws * HC + h] = make_float4(m.x, l, m.y, 0.0f);
+                acc.store(p.ws_o + (ws * HC + h) * D, lane);
+                if (lane == 0) p.ws_ml[ws * HC + h] = make_float4(m, l, mv, 0.0f);
             }
         }
     }
@@ -688,62 +734,63 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
 
 // Merge the pieces of the units that CTA boundaries cut: block j takes the unit
 // that the boundary between the slices of CTAs j and j + 1 cuts, if it is the
-// unit's first one; grid.y blocks share its heads.  A block is kRows rows of D
-// threads: with few pieces the rows take a head each, with many (a long request
-// over many CTAs) they share one head's pieces.  Launched with programmatic
-// stream serialisation: it waits for the kernel before it reads.
-constexpr int kCombineThreads = 512;
+// unit's first one.  Its warps share out the heads, and a head's pieces where there
+// are more warps than heads; of few units, with many pieces each, the heads go to
+// grid.y blocks.
+// Launched with programmatic stream serialisation: it waits for the kernel before
+// it reads.
+constexpr int kCombineWarps = 8;
 
 template <int D, int HC, bool kF16>
-__global__ void __launch_bounds__(kCombineThreads) decode_e4m3_combine_kernel(const E4m3Params p) {
-    constexpr int kRows = kCombineThreads / D;
-    __shared__ float s_acc[kRows][D];
+__global__ void __launch_bounds__(kCombineWarps * 32) decode_e4m3_combine_kernel(const E4m3Params p) {
+    __shared__ __align__(16) float s_acc[kCombineWarps][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const longlong2 geom = *p.geom;  // {tiles, tiles of a slice}
     const int4 f = p.first[blockIdx.x + 1];  // not written past the last slice
     const long long at = geom.y * (blockIdx.x + 1ll);
     if (at >= geom.x) return;
     if (f.z == 0 || f.z > geom.y) return;  // not cut here, or cut at an earlier boundary
-    const int hkv = f.y / p.chunks, chunk = f.y - hkv * p.chunks;
+    const int hkv = p.chunks == 1 ? f.y : f.y / p.chunks, chunk = f.y - hkv * p.chunks;
     const int heads = min(HC, p.group - chunk * HC);
-    const long long start = at - f.z;
-    const long long c0 = start / geom.y;
-    const int n = static_cast<int>((start + f.w - 1) / geom.y - c0) + 1;  // pieces: of CTAs c0 on
-    const long long slot0 = 2 * c0 + (start != c0 * geom.y ? 1 : 0);
+    // The unit starts in the slice before the boundary; its pieces: of CTA blockIdx.x,
+    // in its second place unless its slice starts with the unit, and on.
+    const int n = 2 + static_cast<int>(divide(f.w - f.z - 1, static_cast<int>(min(geom.y, 0x7fffffffll))));
+    const long long slot0 = 2ll * blockIdx.x + (f.z != geom.y ? 1 : 0);
     const int64_t row0 = static_cast<int64_t>(f.x) * p.Hq + hkv * p.group + chunk * HC;
-    const int lane = threadIdx.x % 32, d = threadIdx.x % D, row = threadIdx.x / D;
-    const int abreast = n <= 8 ? kRows : 1;  // heads at a time
-    const int sharers = kRows / abreast, sharer = row / abreast;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    auto slot = [&](int i, int h) {
+        return (i == 0 ? slot0 : 2 * (blockIdx.x + static_cast<long long>(i))) * HC + h;
+    };
+    // Heads at a time, and the warps that share a head's pieces.
+    int abreast = 1;
+    while (gridDim.y == 1 && abreast < heads && abreast < kCombineWarps) abreast *= 2;
+    const int sharers = kCombineWarps / abreast, sharer = warp % sharers;
     for (int h0 = blockIdx.y * abreast; h0 < heads; h0 += gridDim.y * abreast) {
-        const int h = min(heads - 1, h0 + row % abreast);
-        // References and sum over all pieces, by every warp.
-        float4 e = make_float4(kLowest, 0.0f, kLowest, 0.0f);
-        for (int i = lane; i < n; i += 32) {
-            const float4 x = p.ws_ml[(i == 0 ? slot0 : 2 * (c0 + i)) * HC + h];
-            const float m = fmaxf(e.x, x.x);
-            e.y = e.y * ex2_approx(e.x - m) + x.y * ex2_approx(x.x - m);
-            e.x = m;
-            e.z = fmaxf(e.z, x.z);
-        }
-        float l;
-        const float2 m = merge_weights<16>(e, &l);
-        float acc = 0.0f;
+        const int h = min(heads - 1, h0 + warp / sharers);
+        float4 all = make_float4(kLowest, 0.0f, kLowest, 0.0f);
+        for (int i = lane; i < n; i += 32) fold(all, p.ws_ml[slot(i, h)]);
+        fold_lanes<1>(all);
+        Columns<D> acc{};
 #pragma unroll 4
         for (int i = sharer; i < n; i += sharers) {
-            const long long slot = (i == 0 ? slot0 : 2 * (c0 + i)) * HC + h;
-            acc = fmaf(p.ws_o[slot * D + d], ex2_approx(p.ws_ml[slot].z - m.y), acc);
+            Columns<D> x;
+            x.load(p.ws_o + slot(i, h) * D, lane);
+            acc.add(x, ex2_approx(p.ws_ml[slot(i, h)].z - all.z));
         }
         if (sharers > 1) {
-            s_acc[row][d] = acc;
+            acc.store(s_acc[warp], lane);
             __syncthreads();
-            acc = 0.0f;
-            for (int i = 0; i < kRows; ++i) acc += s_acc[i][d];
+            if (sharer == 0)
+                for (int i = 1; i < sharers; ++i) {
+                    Columns<D> x;
+                    x.load(s_acc[warp + i], lane);
+                    acc.add(x, 1.0f);
+                }
             __syncthreads();
         }
-        if (sharer == 0 && h0 + row % abreast < heads) {
-            p.o[(row0 + h) * D + d] =
-                static_cast<uint16_t>(Elem16<kF16>::pack(acc * out_factor(m.x, l, m.y), 0.0f) & 0xffffu);
-            if (d == 0 && p.lse) p.lse[row0 + h] = (m.x + __log2f(l)) * kLn2;
+        if (sharer == 0 && h0 + warp / sharers < heads) {
+            acc.template store16<kF16>(p.o + (row0 + h) * D, lane, out_factor(all.x, all.y, all.z));
+            if (lane == 0 && p.lse) p.lse[row0 + h] = (all.x + __log2f(all.y)) * kLn2;
         }
     }
 }
@@ -784,7 +831,7 @@ cudaError_t launch_main(const E4m3Params& p, int grid, int prefix, int device, c
     // Few units: each has many pieces, and its heads are shared out to more blocks.
     const bool few = static_cast<long long>(p.B) * p.Hkv * p.chunks * 4 < grid;
     cfg.gridDim = dim3(grid - 1, few ? std::min(HC, p.group) : 1);
-    cfg.blockDim = dim3(kCombineThreads);
+    cfg.blockDim = dim3(kCombineWarps * 32);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -808,13 +855,15 @@ cudaError_t launch_types(const E4m3Params& p, bool f16, bool whole, int grid, in
 
 }  // namespace
 
-size_t decode_e4m3_workspace_bytes(const PagedShape& s, int num_sms) { return WsLayout(s, num_sms).bytes; }
+size_t decode_e4m3_workspace_bytes(const PagedShape& s, int num_sms) {
+    return WsLayout(s, kPerSm * num_sms).bytes;
+}
 
 cudaError_t launch_decode_paged_e4m3(const uint16_t* q, const uint8_t* kv, const float* scales,
                                      const int32_t* block_table, const int32_t* seq_lens,
                                      uint16_t* o, float* lse, void* ws, const PagedShape& s,
                                      const LaunchEnv& env, int* grid_out, int* kernels_launched) {
-    const int grid = env.num_sms;
+    const int grid = kPerSm * env.num_sms;
     const WsLayout lay(s, grid);
     uint8_t* base = static_cast<uint8_t*>(ws);
     const bool prefix = s.B <= kMaxPrefixB;
