@@ -46,7 +46,6 @@ namespace {
 
 constexpr int kTile = 16;          // keys of a tile
 constexpr int kMaxPrefixB = 1024;  // requests whose tile counts a CTA sums itself
-constexpr int kPerSm = 2;  // CTAs
 constexpr float kSlack = 6.0f;
 // References start here: below any score, and finite, so that no difference of
 // two of them is NaN.
@@ -75,9 +74,10 @@ struct E4m3Params {
 template <int D, int HC>
 struct E4m3Layout {
     static constexpr int kWarps = 4;
+    static constexpr int kPerSm = D == 128 ? 2 : (HC == 8 ? 4 : 3);  // CTAs, as registers allow
     static constexpr int kStage = 2 * kTile * D + 2 * kTile * 4;  // K rows, V rows, scales
     static constexpr int kPiece = HC * D * 4;
-    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kStages = D == 128 ? 4 : (HC == 8 ? 4 : 5);
     static constexpr int kPieceOff = kWarps * kStages * kStage;
     static constexpr int kMlOff = kPieceOff + kWarps * kPiece;  // [warp][2][HC] float4
     static constexpr int kMetaOff = kMlOff + kWarps * 2 * HC * 16;
@@ -480,7 +480,7 @@ struct PieceMeta {
 };
 
 template <int D, int HC, bool kF16, bool kWholePages>
-__global__ void __launch_bounds__(E4m3Layout<D, HC>::kWarps * 32, kPerSm)
+__global__ void __launch_bounds__(E4m3Layout<D, HC>::kWarps * 32, E4m3Layout<D, HC>::kPerSm)
 decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
     using L = E4m3Layout<D, HC>;
     constexpr int kWarps = L::kWarps;
@@ -798,6 +798,11 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode_e4m3_combine_kernel
 // Query heads a CTA serves at a time: one or two 8-row halves of the product.
 int heads_at_once(int group) { return group <= 8 ? 8 : 16; }
 
+int ctas_per_sm(const PagedShape& s) {
+    if (heads_at_once(s.Hq / s.Hkv) == 8) return s.D == 64 ? E4m3Layout<64, 8>::kPerSm : E4m3Layout<128, 8>::kPerSm;
+    return s.D == 64 ? E4m3Layout<64, 16>::kPerSm : E4m3Layout<128, 16>::kPerSm;
+}
+
 // Workspace: cum (long long [B + 1]), geom (longlong2), first (int4 [grid]), the
 // pieces of the cut units and their references and sums.
 struct WsLayout {
@@ -856,14 +861,14 @@ cudaError_t launch_types(const E4m3Params& p, bool f16, bool whole, int grid, in
 }  // namespace
 
 size_t decode_e4m3_workspace_bytes(const PagedShape& s, int num_sms) {
-    return WsLayout(s, kPerSm * num_sms).bytes;
+    return WsLayout(s, ctas_per_sm(s) * num_sms).bytes;
 }
 
 cudaError_t launch_decode_paged_e4m3(const uint16_t* q, const uint8_t* kv, const float* scales,
                                      const int32_t* block_table, const int32_t* seq_lens,
                                      uint16_t* o, float* lse, void* ws, const PagedShape& s,
                                      const LaunchEnv& env, int* grid_out, int* kernels_launched) {
-    const int grid = kPerSm * env.num_sms;
+    const int grid = ctas_per_sm(s) * env.num_sms;
     const WsLayout lay(s, grid);
     uint8_t* base = static_cast<uint8_t*>(ws);
     const bool prefix = s.B <= kMaxPrefixB;
