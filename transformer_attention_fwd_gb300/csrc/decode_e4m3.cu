@@ -395,15 +395,17 @@ __device__ __forceinline__ void unit_tile(const uint8_t* stage, int valid, int l
 #pragma unroll
         for (int r = 0; r < kR; ++r) mma_f16((j & 1) ? sd[r] : sc[r], a0, a1, a2, a3, s.qb[j][r][0], s.qb[j][r][1]);
     }
-    // V^T's operand, while the products run: bytes 2i, 2i + 1 of two keys' words are
+    // V^T's operand (with eight heads all of it now, while the products run): bytes 2i, 2i + 1 of two keys' words are
     // (k0, k1) of one column, then of the next.
     uint32_t va[kS][4];
-#pragma unroll
-    for (int i = 0; i < kS; ++i) {
+    auto convert = [&](int i) {
         const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
         e4m3_to_f16x4(__byte_perm(vw[0][i / 2], vw[1][i / 2], sel), va[i][0], va[i][1]);
         e4m3_to_f16x4(__byte_perm(vw[2][i / 2], vw[3][i / 2], sel), va[i][2], va[i][3]);
-    }
+    };
+    if (HC == 8)
+#pragma unroll
+        for (int i = 0; i < kS; ++i) convert(i);
     // Factors and lifts (log2 of V's scales) of keys g and g + 8: one pair for a tile
     // inside one page.
     constexpr int kF = kWholePages ? 1 : 2;
@@ -450,6 +452,7 @@ __device__ __forceinline__ void unit_tile(const uint8_t* stage, int valid, int l
             }
         }
     }
+    uint32_t pb[kR][2];
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
         float w[4];
@@ -458,9 +461,14 @@ __device__ __forceinline__ void unit_tile(const uint8_t* stage, int valid, int l
             s.l[r][i & 1] += ex2_approx(x[r][i] - s.m[r][i & 1]);
             w[i] = ex2_approx(x[r][i] + (lift[(i >> 1) % kF] - s.mv[r][i & 1]));
         }
-        const uint32_t b0 = transpose8x8(pack_f16x2(w[0], w[1])), b1 = transpose8x8(pack_f16x2(w[2], w[3]));
+        pb[r][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+        pb[r][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+    }
 #pragma unroll
-        for (int i = 0; i < kS; ++i) mma_f16(s.o[r][i], va[i][0], va[i][1], va[i][2], va[i][3], b0, b1);
+    for (int i = 0; i < kS; ++i) {
+        if (HC != 8) convert(i);
+#pragma unroll
+        for (int r = 0; r < kR; ++r) mma_f16(s.o[r][i], va[i][0], va[i][1], va[i][2], va[i][3], pb[r][0], pb[r][1]);
     }
 }
 
