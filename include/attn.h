@@ -20,8 +20,9 @@
  * ---------------------------------------
  * Memory: q, k, v, o and lse are DEVICE pointers owned by the caller; the
  *   library keeps none of them after the call returns.
- * Layout: q and o are [B, Hq, Tq, D], k and v are [B, Hkv, Tk, D], row-major
- *   and contiguous, D innermost.  lse is float32 [B, Hq, Tq], or NULL when not
+ * Layout (the attention calls; the rotary and append calls take rows of any
+ *   strides, attn_rows): q and o are [B, Hq, Tq, D], k and v are [B, Hkv, Tk, D],
+ *   row-major and contiguous, D innermost.  lse is float32 [B, Hq, Tq], or NULL when not
  *   wanted.  q, k, v, o must be 16-byte aligned; lse 4-byte aligned.
  * Element type: q, k, v and o share one type (attn_dtype); accumulation is
  *   always float32 ("Attention 入门" §11.8.5: 16-bit I/O, fp32 accumulation).
@@ -339,7 +340,7 @@ attn_status attn_rope_turns(unsigned long long* turns, float* magnitude, int rot
 /*
  * Rows of D contiguous elements, one for each (batch, head, token), at
  * x + batch * x_batch + head * x_head + token * x_token, and results at y
- * likewise (strides in elements, >= 0): any slice of a fused projection, in
+ * likewise (strides in elements, >= 0; heads up to 2^20): any slice of a fused projection, in
  * any order of its dimensions.  x and y are 16-byte aligned and every stride is
  * a multiple of 16 bytes.  y == x with equal strides works in place; otherwise
  * the two may not share memory, and no two rows of y may.  Nothing else that a
@@ -392,8 +393,8 @@ attn_status attn_qk_norm_rope(const attn_rows* q, const attn_rows* k, const void
  *                tokens, they go to slots seq_lens[b] - n .. seq_lens[b] - 1.
  *   positions:   [total] int32, device, or NULL: a token's position is its slot.
  *   block_table: [B, max_pages_per_seq] int32, device, as in
- *                attn_fwd_decode_paged.  The blocks that the call writes belong
- *                to one request each.
+ *                attn_fwd_decode_paged.  No block is written twice in a call: the
+ *                pages that get new tokens have blocks of their own.
  *   kv_cache:    [num_blocks, 2, Hkv, page_size, D]; other slots stay as they are.
  *   rotation:    NULL: keys (and queries) are copied.
  *   dtype:       ATTN_BF16 or ATTN_F16, of q, k, v and the cache.

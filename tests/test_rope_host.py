@@ -179,6 +179,8 @@ def _append(a, e4m3, q=None, k="k", v="v", cu=FAKE, lens=FAKE, positions=None, t
     (dict(B=0), 1, ">= 1"),
     (dict(total=-1), 1, ">= 0"),
     (dict(total=2 ** 31 - 1), 1, "total"),
+    (dict(B=2 ** 31 - 1, pages=1), 1, "B and total"),
+    (dict(k=dict(heads=2 ** 20 + 1, y=None), v=dict(heads=2 ** 20 + 1, y=None)), 1, "2^20"),
     (dict(page=0), 1, ">= 1"),
     (dict(blocks=0), 1, ">= 1"),
     (dict(D=80), 2, "D=80"),
@@ -215,6 +217,7 @@ def test_append_e4m3_needs_scales(a):
 @pytest.mark.parametrize("kw,code,msg", [
     (dict(q=None), 1, "non-null"), (dict(scales=None), 1, "scales"), (dict(scales=FAKE + 1), 1, "scales"),
     (dict(kv=FAKE + 8), 1, "aligned"), (dict(dtype=0), 2, "16-bit"), (dict(dtype=9), 1, "dtype"),
+    (dict(B=2 ** 31 - 1, Hq=1, Hkv=1, pages=1), 1, "B must be"),
     (dict(D=32), 2, "D=32"), (dict(Hq=5), 1, "multiple"), (dict(scale=0.0), 1, "scale"), (dict(B=0), 1, ">= 1"),
     (dict(pages=1 << 28), 1, "max_pages_per_seq*page_size"),
 ])

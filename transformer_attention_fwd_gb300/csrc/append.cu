@@ -22,7 +22,10 @@ append_kernel(const AppendParams p) {
     using R = Rope<E, D, kLayout>;
     __shared__ __align__(16) float s_table[kAppendWarps][D];
     __shared__ float s_scratch[R::kScratch ? kAppendWarps * R::kScratch : 1];
-    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0) append_report(p);
+    if (blockIdx.x >= p.token_blocks) {
+        if (blockIdx.y == 0) append_report(p, blockIdx.x - p.token_blocks);
+        return;
+    }
     const int warp = threadIdx.x / 32;
     append_rows<E, D, kLayout>(p, static_cast<int>(blockIdx.x) * kAppendWarps + warp, blockIdx.y, s_table[warp],
                                s_scratch + warp * R::kScratch);
@@ -79,7 +82,8 @@ cudaError_t launch_append_paged(const AppendShape& s, const RopeShape& r, const 
     p.steps = p.q_steps + 2 * p.kv_steps;
     const int segs = append_segments(p, env.num_sms);
     if (segs > 65535) return cudaErrorInvalidConfiguration;
-    const dim3 g((s.total + kAppendWarps - 1) / kAppendWarps, segs);
+    p.token_blocks = static_cast<unsigned>((s.total + kAppendWarps - 1) / kAppendWarps);
+    const dim3 g(p.token_blocks + (s.B + kAppendWarps * 32 - 1) / (kAppendWarps * 32), segs);
     const int layout = rope_layout(r.rot_dim, r.interleaved, 2);
     cudaError_t e;
     if (r.dtype == ATTN_F16)

@@ -33,7 +33,8 @@ struct AppendParams {
     int B, total, max_pages, num_blocks;
     int q_steps, kv_steps, steps, per_seg;  // a token's steps; segments of per_seg
     float k_limit;  // 8-bit: largest |K| element a scale of 1 takes
-    unsigned items, splits, segs;  // 8-bit: blocks of the K and V pages, segments (see append_e4m3.cu)
+    unsigned items, splits, segs, q_blocks;  // 8-bit cache: see append_e4m3.cu
+    unsigned token_blocks;                   // 16-bit cache: those behind them report bad requests
 };
 
 // The last i in 0 .. n - 1 with value(i) <= target, for non-decreasing values
@@ -70,10 +71,11 @@ __device__ __forceinline__ AppendRequest append_request(const AppendParams& p, i
     return r;
 }
 
-// One CTA reports requests that append_request() drops.
-__device__ __forceinline__ void append_report(const AppendParams& p) {
-    for (int b = threadIdx.x; b < p.B; b += blockDim.x)
-        if (!append_request(p, b).ok) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
+// Reporting block `block`: the requests of its threads that append_request() drops.
+__device__ __forceinline__ void append_report(const AppendParams& p, unsigned block) {
+    const unsigned b = block * blockDim.x + threadIdx.x;
+    if (b < static_cast<unsigned>(p.B) && !append_request(p, static_cast<int>(b)).ok)
+        atomicOr(p.status, ATTN_DEV_BAD_INPUT);
 }
 
 // The request and slot of a new token (by the whole warp); false if no valid

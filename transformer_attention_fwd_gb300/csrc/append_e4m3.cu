@@ -107,7 +107,7 @@ __device__ __forceinline__ float settle_scale(float amax, float limit, int held,
         const float old = *scale_at;
         if (scale > old) {
             const float ratio = old / scale;
-            for (int c = lane; c < held * (D / 16); c += 32) {
+            for (long long c = lane; c < held * (D / 16ll); c += 32) {
                 uint4* at = reinterpret_cast<uint4*>(block) + c;
                 uint4 w = *at;
                 w.x = e4m3_rescale(w.x, ratio);
@@ -146,9 +146,12 @@ append_e4m3_kernel(const AppendParams p) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     float* scratch = s_scratch + (R::kScratch ? warp * R::kScratch : 0);
     const unsigned kv_blocks = p.items * p.splits;
-    if (blockIdx.x == gridDim.x - 1) append_report(p);
     if (blockIdx.x >= kv_blocks) {
         const unsigned qb = blockIdx.x - kv_blocks;
+        if (qb >= p.q_blocks) {
+            append_report(p, qb - p.q_blocks);
+            return;
+        }
         append_rows<E, D, kLayout>(p, static_cast<int>(qb / p.segs) * kPageWarps + warp, static_cast<int>(qb % p.segs),
                                    s_table[warp], scratch);
         return;
@@ -278,8 +281,9 @@ cudaError_t launch_append_paged_e4m3(const AppendShape& s, const RopeShape& r, c
     const int step_rows = 32 * 16 / r.D;
     p.q_steps = p.steps = (p.q.heads + step_rows - 1) / step_rows;
     p.segs = p.steps > 0 ? append_segments(p, env.num_sms) : 0;
-    const long long blocks =
-        items * p.splits + static_cast<long long>((s.total + kPageWarps - 1) / kPageWarps) * p.segs;
+    const long long q_blocks = static_cast<long long>((s.total + kPageWarps - 1) / kPageWarps) * p.segs;
+    const long long blocks = items * p.splits + q_blocks + (s.B + kPageWarps * 32 - 1) / (kPageWarps * 32);
+    p.q_blocks = static_cast<unsigned>(q_blocks);
     if (items > 0x7fffffffLL || blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     p.items = static_cast<unsigned>(items);
     const unsigned g = static_cast<unsigned>(blocks);

@@ -986,7 +986,8 @@ long long rows_span(const long long (&stride)[3], const long long (&extent)[3], 
 // optional, -1 must be null.
 attn_status validate_rows(const char* name, const attn_rows* r, long long B, long long T, int D, int bytes,
                           int want_y) {
-    if (r->heads < 1) return fail(ATTN_ERR_INVALID_ARG, "%s: heads must be >= 1 (got %d)", name, r->heads);
+    if (r->heads < 1 || r->heads > (1 << 20))
+        return fail(ATTN_ERR_INVALID_ARG, "%s: heads must be in 1..2^20 (got %d)", name, r->heads);
     if (!r->x || (want_y > 0 && !r->y)) return fail(ATTN_ERR_INVALID_ARG, "%s: x and y must be non-null", name);
     if (want_y < 0 && r->y) return fail(ATTN_ERR_INVALID_ARG, "%s: y must be null", name);
     const long long extent[3] = {B, r->heads, T};
@@ -1097,7 +1098,8 @@ attn_status run_append(bool e4m3, const attn_rows* q, const attn_rows* k, const 
         return fail(ATTN_ERR_INVALID_ARG, "max_pages_per_seq*page_size must be below 2^31 - 1024");
     if (static_cast<long long>(B) * max_pages_per_seq > 0x7fffffffLL)
         return fail(ATTN_ERR_INVALID_ARG, "B*max_pages_per_seq must fit in 31 bits");
-    if (total > 0x7fffffff - 1024) return fail(ATTN_ERR_INVALID_ARG, "total must be below 2^31 - 1024");
+    if (total > 0x7fffffff - 1024 || B > 0x7fffffff - 1024)
+        return fail(ATTN_ERR_INVALID_ARG, "B and total must be below 2^31 - 1024");
     const attn_rotation plain{nullptr, 0, 0, 1.0f};
     const attn_rotation& rot = rotation ? *rotation : plain;
     attn_status st = validate_rotation(&rot, D);
@@ -1224,6 +1226,7 @@ attn_status attn_fwd_decode_paged_e4m3(const void* q, const void* kv_cache, cons
     attn_status st = validate_paged(q, kv_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, D, page_size,
                                     max_pages_per_seq, num_blocks, scale, dtype);
     if (st != ATTN_OK) return st;
+    if (B > 0x7fffffff - 1024) return fail(ATTN_ERR_INVALID_ARG, "B must be below 2^31 - 1024");
     LaunchEnv env;
     st = device_env(stream, &env);
     if (st != ATTN_OK) return st;

@@ -560,13 +560,13 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
                 }
                 const int hkv = p.chunks == 1 ? lc.unit : lc.unit / p.chunks;
                 const int valid = lc.len - lc.tile * kTile;  // 16 and more: the whole tile
-                const int64_t block = static_cast<int64_t>(id) * (2 * p.Hkv) + hkv;  // of K; V's is Hkv further
+                const int64_t block = static_cast<int64_t>(id) * 2 * p.Hkv + hkv;  // of K; V's is Hkv further
                 // Lanes 0 .. 15: K's scales, 16 .. 31: V's (a tile in one page: lanes 0 and 16).
                 if (kWholePages ? (lane & 15) == 0 : true)
                     copy4(fill + 2 * kTile * D + lane * 4, p.scales + block + (lane >> 4) * p.Hkv,
                           (lane & 15) < valid ? 4 : 0);
                 if (kWholePages) {  // one run of rows
-                    const uint8_t* src = p.kv + block * page_bytes + (row * D + lane * 16);
+                    const uint8_t* src = p.kv + block * page_bytes + static_cast<int64_t>(row) * D + lane * 16;
                     if (valid >= kTile) {
 #pragma unroll
                         for (int i = 0; i < kCopies; ++i) {
@@ -588,7 +588,7 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
                         const int r = r0 + i * kRowsPer;
                         const int rid = __shfl_sync(0xffffffffu, id, r), rrow = __shfl_sync(0xffffffffu, row, r);
                         const uint8_t* src = p.kv +
-                            (static_cast<int64_t>(rid) * (2 * p.Hkv) + hkv) * page_bytes + (rrow * D + col * 16);
+                            (static_cast<int64_t>(rid) * 2 * p.Hkv + hkv) * page_bytes + static_cast<int64_t>(rrow) * D + col * 16;
                         copy16_or_zero(fill + put(i), src, r < valid);
                         copy16_or_zero(fill + kTile * D + put(i), src + to_v, r < valid);
                     }
