@@ -430,7 +430,7 @@ def _rows(name, x, out, like, device, write=True):
     if not write:
         return _Rows(x.data_ptr(), None, shape[1], 0, xs[1], xs[0], 0, 0, 0), None
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.shape != shape or out.dtype is not dtype or out.get_device() != device:
         raise ValueError(f"out_{name} must be {tuple(shape)} {dtype} on {x.device}")
     ys = out.stride()
@@ -612,7 +612,7 @@ def attn_fwd_decode_paged_e4m3(q, kv_cache, scales, block_table, seq_lens, scale
     _ints("seq_lens", seq_lens, (B,), device)
     _current(device)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = torch.empty_like(q)
     else:
         _check_buffer("out", out, shape, dtype, q.device)
     if lse is not None:
