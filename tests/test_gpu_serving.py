@@ -111,3 +111,77 @@ def test_prompt_then_decode(e4m3, with_norm):
             w = refs[b][0][prompts[b] + i]
             size = w.abs() + w.roll(D // 2, dims=-1).abs()
             kv_ref.check_rows(q[b, :, 0], w, 1.5 * size, kv_ref.ROTATION_ERROR + kv_ref.norm_error(D), "query")
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["16bit", "e4m3"])
+def test_decode_step_in_one_graph(e4m3):
+    """A whole step captured, with copies and a clearing between the launches and a second stream
+    that forks off and joins; replays on new inputs give an eager step's bits, also back to back."""
+    a = attn()
+    g = torch.Generator().manual_seed(62)
+    B, steps = 3, 20
+    lens0 = torch.tensor([5, 30, 17], dtype=torch.int32)
+    table, blocks = kv_ref.random_table(lens0 + steps, PAGE, g)
+    table = table.cuda()
+    turns, _ = a.rope_turns(D)
+    rotation = a.Rotation(turns.cuda())
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    inputs = [torch.randn(B, Hq + 2 * Hkv, D, generator=g).to(torch.bfloat16).cuda() for _ in range(steps)]
+    kind = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+
+    def state():
+        return {"x": torch.zeros_like(inputs[0]), "in": torch.zeros_like(inputs[0]), "lens": lens0.cuda(),
+                "cache": torch.zeros(blocks, 2, Hkv, PAGE, D, device="cuda").to(kind),
+                "scales": torch.ones(blocks, 2, Hkv, device="cuda"),
+                "q": torch.empty(B, Hq, 1, D, dtype=torch.bfloat16, device="cuda"),
+                "o": torch.empty(B, Hq, 1, D, dtype=torch.bfloat16, device="cuda"),
+                "side": torch.empty(B, Hkv, D, dtype=torch.bfloat16, device="cuda")}
+
+    def step(s, other):
+        s["x"].copy_(s["in"])
+        s["lens"].add_(1)
+        s["o"].zero_()
+        here = torch.cuda.current_stream()
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            # The same keys rotated apart, at the step's positions.
+            a.attn_rope(s["x"][:, Hq:Hq + Hkv], None, s["lens"] - 1, rotation, out_q=s["side"])
+        k, v = s["x"][:, Hq:Hq + Hkv], s["x"][:, Hq + Hkv:]
+        kw = dict(rotation=rotation, q=s["x"][:, :Hq], out_q=s["q"][:, :, 0])
+        if e4m3:
+            a.attn_append_paged_e4m3(k, v, s["cache"], s["scales"], table, cu, s["lens"], **kw)
+            a.attn_fwd_decode_paged_e4m3(s["q"], s["cache"], s["scales"], table, s["lens"], out=s["o"])
+        else:
+            a.attn_append_paged(k, v, s["cache"], table, cu, s["lens"], **kw)
+            a.attn_fwd_decode_paged(s["q"], s["cache"], table, s["lens"], out=s["o"])
+        here.wait_stream(other)
+        # In place, after the join.
+        a.attn_qk_norm_rope(s["o"][:, :, 0], s["side"], None, None, s["lens"], rotation, out_q=s["o"][:, :, 0],
+                            out_k=s["side"])
+
+    eager, captured, other = state(), state(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        step(captured, torch.cuda.Stream())
+    for x in inputs:
+        eager["in"].copy_(x)
+        captured["in"].copy_(x)
+        step(eager, other)
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in ("o", "side", "q", "scales"):
+            assert torch.equal(eager[name], captured[name]), name
+        assert torch.equal(eager["cache"].view(torch.uint8), captured["cache"].view(torch.uint8))
+    check_status(a)
+    # Back to back, nothing waiting between.
+    for s in (eager, captured):
+        s["lens"].copy_(lens0)
+    for _ in range(10):
+        step(eager, other)
+    for _ in range(10):
+        graph.replay()
+    torch.cuda.synchronize()
+    for name in ("o", "side", "q", "scales"):
+        assert torch.equal(eager[name], captured[name]), name
+    check_status(a)

@@ -12,6 +12,7 @@
 #include <cstdint>
 
 #include "append.cuh"
+#include "pdl.cuh"
 
 namespace attn {
 namespace {
@@ -22,6 +23,8 @@ append_kernel(const AppendParams p) {
     using R = Rope<E, D, kLayout>;
     __shared__ __align__(16) float s_table[kAppendWarps][D];
     __shared__ float s_scratch[R::kScratch ? kAppendWarps * R::kScratch : 1];
+    grid_wait();
+    grid_launch_next();
     if (blockIdx.x >= p.token_blocks) {
         if (blockIdx.y == 0) append_report(p, blockIdx.x - p.token_blocks);
         return;
@@ -34,11 +37,10 @@ append_kernel(const AppendParams p) {
 template <typename E, int D>
 cudaError_t launch_layout(const AppendParams& p, int layout, dim3 blocks, cudaStream_t st) {
     switch (layout) {
-        case kRopeAdjacent: append_kernel<E, D, kRopeAdjacent><<<blocks, kAppendWarps * 32, 0, st>>>(p); break;
-        case kRopeHalves: append_kernel<E, D, kRopeHalves><<<blocks, kAppendWarps * 32, 0, st>>>(p); break;
-        default: append_kernel<E, D, kRopeHalvesOdd><<<blocks, kAppendWarps * 32, 0, st>>>(p); break;
+        case kRopeAdjacent: return launch_serial(append_kernel<E, D, kRopeAdjacent>, blocks, kAppendWarps * 32, 0, st, p);
+        case kRopeHalves: return launch_serial(append_kernel<E, D, kRopeHalves>, blocks, kAppendWarps * 32, 0, st, p);
+        default: return launch_serial(append_kernel<E, D, kRopeHalvesOdd>, blocks, kAppendWarps * 32, 0, st, p);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace

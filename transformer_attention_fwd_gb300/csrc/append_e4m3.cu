@@ -25,6 +25,7 @@
 
 #include "append.cuh"
 #include "e4m3.cuh"
+#include "pdl.cuh"
 
 namespace attn {
 namespace {
@@ -143,6 +144,8 @@ append_e4m3_kernel(const AppendParams p) {
     __shared__ __align__(16) float s_table[kGroup][D];  // a row's cosines and sines
     __shared__ float s_scratch[R::kScratch ? kPageWarps * R::kScratch : 1];
     static_assert(kGroup >= kPageWarps, "query CTAs take a table row for each warp");
+    grid_wait();
+    grid_launch_next();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     float* scratch = s_scratch + (R::kScratch ? warp * R::kScratch : 0);
     const unsigned kv_blocks = p.items * p.splits;
@@ -252,16 +255,12 @@ template <typename E, int D>
 cudaError_t launch_layout(const AppendParams& p, int layout, unsigned blocks, cudaStream_t st) {
     switch (layout) {
         case kRopeAdjacent:
-            append_e4m3_kernel<E, D, kRopeAdjacent><<<blocks, kPageWarps * 32, 0, st>>>(p);
-            break;
+            return launch_serial(append_e4m3_kernel<E, D, kRopeAdjacent>, blocks, kPageWarps * 32, 0, st, p);
         case kRopeHalves:
-            append_e4m3_kernel<E, D, kRopeHalves><<<blocks, kPageWarps * 32, 0, st>>>(p);
-            break;
+            return launch_serial(append_e4m3_kernel<E, D, kRopeHalves>, blocks, kPageWarps * 32, 0, st, p);
         default:
-            append_e4m3_kernel<E, D, kRopeHalvesOdd><<<blocks, kPageWarps * 32, 0, st>>>(p);
-            break;
+            return launch_serial(append_e4m3_kernel<E, D, kRopeHalvesOdd>, blocks, kPageWarps * 32, 0, st, p);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace

@@ -39,6 +39,7 @@
 
 #include "attn_internal.h"
 #include "e4m3.cuh"
+#include "pdl.cuh"
 #include "sm100.cuh"
 
 namespace attn {
@@ -501,11 +502,11 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
     PieceMeta* meta = reinterpret_cast<PieceMeta*>(smem + L::kMetaOff);
     long long* s_cum = reinterpret_cast<long long*>(smem + L::kCumOff);
     const long long* cum = p.cum;
+    grid_launch_next();
     if (prefix_in_kernel) {
         tile_prefix(p, s_cum, s_cum + kMaxPrefixB + 1, blockIdx.x == 0);
         cum = s_cum;
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int grid = static_cast<int>(gridDim.x);
     const int U = p.Hkv * p.chunks;
 
@@ -752,7 +753,7 @@ constexpr int kCombineWarps = 8;
 template <int D, int HC, bool kF16>
 __global__ void __launch_bounds__(kCombineWarps * 32) decode_e4m3_combine_kernel(const E4m3Params p) {
     __shared__ __align__(16) float s_acc[kCombineWarps][D];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
     const longlong2 geom = *p.geom;  // {tiles, tiles of a slice}
     const int4 f = p.first[blockIdx.x + 1];  // not written past the last slice
     const long long at = geom.y * (blockIdx.x + 1ll);
@@ -837,21 +838,15 @@ cudaError_t launch_main(const E4m3Params& p, int grid, int prefix, int device, c
         if (e != cudaSuccess) return e;
         attr_set[device] = true;
     }
+    // Not overlapped with what runs before: CTAs that start one by one as it drains
+    // cost the stream its even start (91.7 -> 92.3 us at 64 x 4096 keys).
     kern<<<grid, L::kWarps * 32, L::kBytes, st>>>(p, prefix);
     e = cudaGetLastError();
     if (e != cudaSuccess || grid < 2) return e;
-    cudaLaunchConfig_t cfg{};
     // Few units: each has many pieces, and its heads are shared out to more blocks.
     const bool few = static_cast<long long>(p.B) * p.Hkv * p.chunks * 4 < grid;
-    cfg.gridDim = dim3(grid - 1, few ? std::min(HC, p.group) : 1);
-    cfg.blockDim = dim3(kCombineWarps * 32);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_e4m3_combine_kernel<D, HC, kF16>, p);
+    return launch_serial(decode_e4m3_combine_kernel<D, HC, kF16>, dim3(grid - 1, few ? std::min(HC, p.group) : 1),
+                         kCombineWarps * 32, 0, st, p);
 }
 
 template <int D, int HC>

@@ -1,0 +1,36 @@
+// pdl.cuh -- launches with programmatic stream serialisation.
+//
+// A kernel launched so may have its blocks scheduled while the kernel before it
+// in the stream drains; every thread of it starts with grid_wait(), which returns
+// once that kernel is complete and its writes are visible, so nothing is read or
+// written early.  grid_launch_next() lets the next kernel launched so be scheduled
+// once all blocks have called it.  (A kernel launched without the attribute waits
+// for the one before it as a whole, and grid_wait() in it returns at once.)
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <utility>
+
+namespace attn {
+
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... Params, typename... Args>
+cudaError_t launch_serial(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                          Args&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+}  // namespace attn

@@ -16,6 +16,7 @@
 #include <cstdint>
 
 #include "attn_internal.h"
+#include "pdl.cuh"
 #include "rope.cuh"
 
 namespace attn {
@@ -44,6 +45,8 @@ rope_kernel(const RopeParams p) {
     constexpr int kRopeUnroll = kNorm ? 3 : 2;
     __shared__ __align__(16) float s_table[kRopeWarps][D];
     __shared__ float s_scratch[R::kScratch ? kRopeWarps * R::kScratch : 1];
+    grid_wait();
+    grid_launch_next();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int j = lane % R::kLanes, grp = lane / R::kLanes;
     const unsigned token = blockIdx.x * kRopeWarps + warp;
@@ -108,9 +111,8 @@ rope_kernel(const RopeParams p) {
 
 template <typename E, int D, int kLayout>
 cudaError_t launch_norm(const RopeParams& p, bool norm, dim3 blocks, cudaStream_t st) {
-    if (norm) rope_kernel<E, D, kLayout, true><<<blocks, kRopeWarps * 32, 0, st>>>(p);
-    else rope_kernel<E, D, kLayout, false><<<blocks, kRopeWarps * 32, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_serial(norm ? rope_kernel<E, D, kLayout, true> : rope_kernel<E, D, kLayout, false>, blocks,
+                         kRopeWarps * 32, 0, st, p);
 }
 
 template <typename E>
