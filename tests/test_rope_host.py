@@ -261,3 +261,14 @@ def test_page_division_is_exact(a):
             if 0 <= n < 2 ** 31:
                 assert (n * m) >> shift == n // d, (n, d)
     assert ctypes.sizeof(a._Rows) == 72 and ctypes.sizeof(a._Rotation) == 24
+
+
+def test_library_errors_come_as_the_bindings(a):
+    """A status of the library, through the native calls, is the binding's exception."""
+    with pytest.raises(a.AttnError) as e:
+        a.rope_turns(7)
+    assert e.value.status == a.ATTN_ERR_INVALID_ARG
+    with pytest.raises(ValueError, match="arguments"):
+        a._native.rope(1)
+    with pytest.raises(ValueError, match="q must be a tensor"):
+        a.attn_rope([1.0], None, torch.zeros(1, dtype=torch.int32), None)

@@ -1,14 +1,17 @@
-"""ctypes binding over libattn.so (include/attn.h, include/attn_diag.h).
+"""Binding over libattn.so (include/attn.h, include/attn_diag.h): ctypes, and
+csrc/binding.cpp for the calls of a decode step that take microseconds.
 
 Argument marshalling only: the functions check tensor placement, dtype and
 contiguity, allocate outputs with torch, and pass raw device pointers plus the
 current CUDA stream to the C ABI.  Every step of the computation runs in the
-library's CUDA kernels; there is no fallback.  If the library is missing the
+library's CUDA kernels; there is no fallback.  If a library is missing the
 import-time load raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 
@@ -16,6 +19,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libattn.so")
+BINDING_PATH = os.path.join(_PKG, "_build", "_attn_binding.so")
 
 ATTN_OK = 0
 ATTN_ERR_INVALID_ARG = 1
@@ -91,6 +95,20 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 lib = _load()
+
+
+def _load_binding(path: str = BINDING_PATH):
+    if not os.path.exists(path):
+        raise RuntimeError(
+            f"{path} is missing: build it with transformer_attention_fwd_gb300.build.build()")
+    loader = importlib.machinery.ExtensionFileLoader("_attn_binding", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_attn_binding", loader, origin=path))
+    loader.exec_module(module)
+    module.set_error(AttnError)
+    return module
+
+
+_native = _load_binding()
 
 
 def last_error() -> str:
@@ -357,7 +375,6 @@ def attn_fwd_decode_paged(q, kv_cache, block_table, seq_lens, scale: float | Non
     return o, lse
 
 
-_DTYPES = {torch.float32: ATTN_F32, torch.bfloat16: ATTN_BF16, torch.float16: ATTN_F16}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "wavelength": 3, "yarn": 4}
 
 
@@ -368,13 +385,8 @@ class Rotation:
     (i, i + rot_dim/2), or (2i, 2i + 1) with ``interleaved``."""
 
     def __init__(self, turns, interleaved: bool = False, magnitude: float = 1.0):
-        if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
-            raise ValueError("turns must be a contiguous int64 tensor [rot_dim / 2]")
-        if not turns.is_cuda:
-            raise ValueError("turns must be a CUDA tensor")
         self.turns, self.interleaved, self.magnitude = turns, bool(interleaved), float(magnitude)
-        self.device_index = turns.get_device()
-        self._struct = _Rotation(turns.data_ptr(), 2 * turns.shape[0], int(self.interleaved), self.magnitude)
+        self._held = _native.rotation(turns, self.interleaved, self.magnitude)
 
     @classmethod
     def make(cls, rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -402,78 +414,6 @@ def rope_turns(rot_dim: int, base: float = 10000.0, scaling: str = "none", facto
     return turns, magnitude.value
 
 
-def _raw_stream(stream, device: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else int(stream.cuda_stream)
-
-
-def _current(device: int):
-    now = torch._C._cuda_getDevice()
-    if device != now:
-        raise ValueError(f"tensors are on cuda:{device} but the current device is cuda:{now}; "
-                         f"call under torch.cuda.device({device})")
-
-
-def _rows(name, x, out, like, device, write=True):
-    """attn_rows of x, [T, H, D] or [B, H, T, D] with the tokens, head dim and type
-    of ``like``, and its output: ``out``, or a new one (``write`` False: none)."""
-    shape, dtype = x.shape, x.dtype
-    n, want = len(shape), like.shape
-    if x.get_device() != device or device < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
-    if dtype is not like.dtype:
-        raise ValueError(f"{name} must be {like.dtype} (got {dtype})")
-    if n != len(want) or shape[0] != want[0] or shape[-1] != want[-1] or (n == 4 and shape[2] != want[2]):
-        raise ValueError(f"{name} must have the tokens and head dim of the others (got {tuple(shape)})")
-    xs = x.stride()
-    if xs[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    if not write:
-        return _Rows(x.data_ptr(), None, shape[1], 0, xs[1], xs[0], 0, 0, 0), None
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    elif out.shape != shape or out.dtype is not dtype or out.get_device() != device:
-        raise ValueError(f"out_{name} must be {tuple(shape)} {dtype} on {x.device}")
-    ys = out.stride()
-    if ys[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"out_{name}'s last dimension must be contiguous")
-    if n == 3:
-        return _Rows(x.data_ptr(), out.data_ptr(), shape[1], 0, xs[1], xs[0], 0, ys[1], ys[0]), out
-    return _Rows(x.data_ptr(), out.data_ptr(), shape[1], xs[0], xs[1], xs[2], ys[0], ys[1], ys[2]), out
-
-
-def _ints(name, t, shape, device):
-    """An int32 device tensor of exactly this shape."""
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} (got {tuple(t.shape)} {t.dtype})")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
-
-
-def _rope_call(q, k, positions, rotation, out_q, out_k):
-    device, shape = q.get_device(), q.shape
-    dt = _DTYPES.get(q.dtype)
-    if dt is None:
-        raise ValueError(f"unsupported dtype {q.dtype}")
-    if len(shape) == 3:
-        B, T = 1, shape[0]
-        pos_shape = (T,)
-    elif len(shape) == 4:
-        B, T = pos_shape = shape[0], shape[2]
-    else:
-        raise ValueError("q must be [T, H, D] or [B, H, T, D]")
-    if k is None and out_k is not None:
-        raise ValueError("out_k without k")
-    rq, out_q = _rows("q", q, out_q, q, device)
-    rk = None
-    if k is not None:
-        rk, out_k = _rows("k", k, out_k, q, device)
-    _ints("positions", positions, pos_shape, device)
-    if rotation.device_index != device:
-        raise ValueError("the rotation's table must be on the device of the tensors")
-    _current(device)
-    return device, B, T, shape[-1], dt, rq, out_q, rk, out_k
-
-
 def attn_rope(q, k, positions, rotation: Rotation, out_q=None, out_k=None, stream=None):
     """Rotary positions of query and key heads (``attn_rope``).
 
@@ -483,78 +423,16 @@ def attn_rope(q, k, positions, rotation: Rotation, out_q=None, out_k=None, strea
     Returns ``(out_q, out_k)``; ``out_q=q`` works in place.  The gradient of
     the inputs is this call on the outputs' gradients with -positions.
     """
-    device, B, T, D, dt, rq, out_q, rk, out_k = _rope_call(q, k, positions, rotation, out_q, out_k)
-    _check(lib.attn_rope(rq, rk, positions.data_ptr(), B, T, D, rotation._struct, dt,
-                         _raw_stream(stream, device)))
-    return out_q, out_k
+    return _native.rope(q, k, positions, None if rotation is None else rotation._held, out_q, out_k,
+                        None if stream is None else stream.cuda_stream, False, None, None, 0.0)
 
 
 def attn_qk_norm_rope(q, k, q_weight, k_weight, positions, rotation: Rotation, eps: float = 1e-6,
                       out_q=None, out_k=None, stream=None):
     """``attn_rope`` of x / sqrt(mean(x^2) + eps) * weight for every head x of q
     and k (``attn_qk_norm_rope``); weights [D] in q's dtype, or None for ones."""
-    device, B, T, D, dt, rq, out_q, rk, out_k = _rope_call(q, k, positions, rotation, out_q, out_k)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.shape != (D,) or w.dtype is not q.dtype or not w.is_contiguous()
-                              or w.get_device() != device):
-            raise ValueError(f"{name} must be a contiguous {q.dtype} tensor [{D}] on {q.device}")
-    _check(lib.attn_qk_norm_rope(rq, rk, _ptr(q_weight), _ptr(k_weight), eps, positions.data_ptr(), B, T, D,
-                                 rotation._struct, dt, _raw_stream(stream, device)))
-    return out_q, out_k
-
-
-def _append(call, k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens, rotation, positions, q,
-            out_q, out_k, stream):
-    device, dtype = k.get_device(), k.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise ValueError("the paged append takes bf16 or fp16 tensors")
-    if len(k.shape) != 3:
-        raise ValueError("k must be [total, Hkv, D]")
-    total, Hkv, D = k.shape
-    rk, out_k = _rows("k", k, out_k, k, device, out_k is not None)
-    rv, _ = _rows("v", v, None, k, device, False)
-    if v.shape[1] != Hkv:
-        raise ValueError("k and v must have the same heads")
-    rq = None
-    if q is not None:
-        rq, out_q = _rows("q", q, out_q, k, device)
-    elif out_q is not None:
-        raise ValueError("out_q without q")
-    want = dtype if scales is None else torch.float8_e4m3fn
-    held = kv_cache.shape
-    if (len(held) != 5 or held[1] != 2 or held[2] != Hkv or held[4] != D or kv_cache.dtype is not want
-            or not kv_cache.is_contiguous() or kv_cache.get_device() != device):
-        raise ValueError(f"kv_cache must be a contiguous {want} tensor [num_blocks, 2, {Hkv}, page_size, {D}] on {k.device}")
-    blocks, page = held[0], held[3]
-    if scales is not None and (scales.dtype is not torch.float32 or scales.shape != (blocks, 2, Hkv)
-                               or not scales.is_contiguous() or scales.get_device() != device):
-        raise ValueError("scales must be a contiguous float32 tensor [num_blocks, 2, Hkv]")
-    table = block_table.shape
-    if len(table) != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    B = table[0]
-    _ints("block_table", block_table, table, device)
-    _ints("seq_lens", seq_lens, (B,), device)
-    _ints("cu_seqlens", cu_seqlens, (B + 1,), device)
-    if positions is not None:
-        _ints("positions", positions, (total,), device)
-    struct = None
-    if rotation is not None:
-        if rotation.device_index != device:
-            raise ValueError("the rotation's table must be on the device of the tensors")
-        struct = rotation._struct
-    _current(device)
-    dt, stream = _DTYPES[dtype], _raw_stream(stream, device)
-    if scales is None:
-        status = call(rq, rk, rv, cu_seqlens.data_ptr(), seq_lens.data_ptr(), _ptr(positions),
-                      block_table.data_ptr(), kv_cache.data_ptr(), B, total, D, page, table[1], blocks, struct,
-                      dt, stream)
-    else:
-        status = call(rq, rk, rv, cu_seqlens.data_ptr(), seq_lens.data_ptr(), _ptr(positions),
-                      block_table.data_ptr(), kv_cache.data_ptr(), scales.data_ptr(), B, total, D, page,
-                      table[1], blocks, struct, dt, stream)
-    _check(status)
-    return out_q, out_k
+    return _native.rope(q, k, positions, None if rotation is None else rotation._held, out_q, out_k,
+                        None if stream is None else stream.cuda_stream, True, q_weight, k_weight, eps)
 
 
 def attn_append_paged(k, v, kv_cache, block_table, cu_seqlens, seq_lens, rotation: Rotation | None = None,
@@ -569,8 +447,9 @@ def attn_append_paged(k, v, kv_cache, block_table, cu_seqlens, seq_lens, rotatio
     given.  Returns ``(out_q, out_k)``: the rotated q (None without q), and
     ``out_k`` as passed, filled with the rotated keys (None if not passed).
     """
-    return _append(lib.attn_append_paged, k, v, kv_cache, None, block_table, cu_seqlens, seq_lens, rotation,
-                   positions, q, out_q, out_k, stream)
+    return _native.append(k, v, kv_cache, None, block_table, cu_seqlens, seq_lens,
+                          None if rotation is None else rotation._held, positions, q, out_q, out_k,
+                          None if stream is None else stream.cuda_stream)
 
 
 def attn_append_paged_e4m3(k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens,
@@ -579,8 +458,11 @@ def attn_append_paged_e4m3(k, v, kv_cache, scales, block_table, cu_seqlens, seq_
     """``attn_append_paged`` into an 8-bit cache (``attn_append_paged_e4m3``):
     kv_cache float8_e4m3fn, scales float32 [num_blocks, 2, Hkv]; a code stands
     for code * scale of its block, K or V, and head."""
-    return _append(lib.attn_append_paged_e4m3, k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens,
-                   rotation, positions, q, out_q, out_k, stream)
+    if scales is None:
+        raise ValueError("scales must be a tensor")
+    return _native.append(k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens,
+                          None if rotation is None else rotation._held, positions, q, out_q, out_k,
+                          None if stream is None else stream.cuda_stream)
 
 
 def attn_fwd_decode_paged_e4m3(q, kv_cache, scales, block_table, seq_lens, scale: float | None = None,
@@ -592,39 +474,8 @@ def attn_fwd_decode_paged_e4m3(q, kv_cache, scales, block_table, seq_lens, scale
     max_pages] and seq_lens: [B] int32; all contiguous CUDA tensors.  Returns
     ``(o [B, Hq, 1, D], lse [B, Hq] or None)``.
     """
-    device, dtype, shape = q.get_device(), q.dtype, q.shape
-    if (device < 0 or len(shape) != 4 or shape[2] != 1 or not q.is_contiguous()
-            or (dtype is not torch.bfloat16 and dtype is not torch.float16)):
-        raise ValueError("q must be a contiguous bf16 or fp16 CUDA tensor [B, Hq, 1, D]")
-    B, Hq, _, D = shape
-    held = kv_cache.shape
-    if (len(held) != 5 or held[1] != 2 or held[4] != D or kv_cache.dtype is not torch.float8_e4m3fn
-            or not kv_cache.is_contiguous() or kv_cache.get_device() != device):
-        raise ValueError("kv_cache must be a contiguous float8_e4m3fn tensor [num_blocks, 2, Hkv, page_size, D]")
-    blocks, _, Hkv, page, _ = held
-    if (scales.dtype is not torch.float32 or scales.shape != (blocks, 2, Hkv) or not scales.is_contiguous()
-            or scales.get_device() != device):
-        raise ValueError("scales must be a contiguous float32 tensor [num_blocks, 2, Hkv]")
-    table = block_table.shape
-    if len(table) != 2 or table[0] != B:
-        raise ValueError("block_table must be [B, max_pages]")
-    _ints("block_table", block_table, table, device)
-    _ints("seq_lens", seq_lens, (B,), device)
-    _current(device)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _check_buffer("out", out, shape, dtype, q.device)
-    if lse is not None:
-        _check_buffer("lse", lse, (B, Hq), torch.float32, q.device)
-    elif want_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    _check(lib.attn_fwd_decode_paged_e4m3(q.data_ptr(), kv_cache.data_ptr(), scales.data_ptr(),
-                                          block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
-                                          _ptr(lse), B, Hq, Hkv, D, page, table[1], blocks, scale,
-                                          _DTYPES[dtype], _raw_stream(stream, device)))
-    return out, lse
+    return _native.decode_e4m3(q, kv_cache, scales, block_table, seq_lens, scale, out, lse, want_lse,
+                               None if stream is None else stream.cuda_stream)
 
 
 def device_status(stream=None) -> int:
