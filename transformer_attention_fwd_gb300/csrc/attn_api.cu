@@ -962,6 +962,40 @@ extern "C" attn_status attn_fwd_decode_noalloc(const void* q, const void* k, con
 namespace attn {
 namespace {
 
+// Stream-ordered workspace out of a pool of this library's.  The device's default
+// pool gives its memory back at every synchronisation, and a step that waits for
+// its result then pays 200 us for mapping it again; this pool keeps what the
+// largest calls at one time needed.  A captured call allocates in its graph.
+cudaMemPool_t g_pool[64] = {};
+
+cudaError_t workspace_alloc(void** out, size_t bytes, const LaunchEnv& env) {
+    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(env.stream, &capturing);
+    if (e != cudaSuccess) return e;
+    if (capturing != cudaStreamCaptureStatusNone) return cudaMallocAsync(out, bytes, env.stream);
+    cudaMemPool_t pool;
+    {
+        std::lock_guard<std::mutex> lock(g_dev_mutex);
+        if (g_pool[env.device] == nullptr) {
+            cudaMemPoolProps props{};
+            props.allocType = cudaMemAllocationTypePinned;
+            props.location.type = cudaMemLocationTypeDevice;
+            props.location.id = env.device;
+            cudaMemPool_t made = nullptr;
+            e = cudaMemPoolCreate(&made, &props);
+            uint64_t keep = UINT64_MAX;
+            if (e == cudaSuccess) e = cudaMemPoolSetAttribute(made, cudaMemPoolAttrReleaseThreshold, &keep);
+            if (e != cudaSuccess) {
+                if (made) cudaMemPoolDestroy(made);
+                return e;
+            }
+            g_pool[env.device] = made;
+        }
+        pool = g_pool[env.device];
+    }
+    return cudaMallocFromPoolAsync(out, bytes, pool, env.stream);
+}
+
 int dtype_bytes(attn_dtype t) { return t == ATTN_F32 ? 4 : 2; }
 
 attn_status validate_rotation(const attn_rotation* r, int D) {
@@ -1234,7 +1268,7 @@ attn_status attn_fwd_decode_paged_e4m3(const void* q, const void* kv_cache, cons
     s.f16 = dtype == ATTN_F16 ? 1 : 0;
     const size_t bytes = decode_e4m3_workspace_bytes(s, env.num_sms);
     void* ws = nullptr;
-    cudaError_t e = cudaMallocAsync(&ws, bytes, env.stream);
+    cudaError_t e = workspace_alloc(&ws, bytes, env);
     if (e != cudaSuccess || ws == nullptr) {
         cudaGetLastError();
         return fail(ATTN_ERR_NO_MEMORY, "paged decode workspace of %zu bytes: %s", bytes, cudaGetErrorString(e));
