@@ -502,6 +502,7 @@ decode_e4m3_kernel(const E4m3Params p, int prefix_in_kernel) {
     PieceMeta* meta = reinterpret_cast<PieceMeta*>(smem + L::kMetaOff);
     long long* s_cum = reinterpret_cast<long long*>(smem + L::kCumOff);
     const long long* cum = p.cum;
+    grid_wait();
     grid_launch_next();
     if (prefix_in_kernel) {
         tile_prefix(p, s_cum, s_cum + kMaxPrefixB + 1, blockIdx.x == 0);
@@ -838,10 +839,7 @@ cudaError_t launch_main(const E4m3Params& p, int grid, int prefix, int device, c
         if (e != cudaSuccess) return e;
         attr_set[device] = true;
     }
-    // Not overlapped with what runs before: CTAs that start one by one as it drains
-    // cost the stream its even start (91.7 -> 92.3 us at 64 x 4096 keys).
-    kern<<<grid, L::kWarps * 32, L::kBytes, st>>>(p, prefix);
-    e = cudaGetLastError();
+    e = launch_serial(kern, dim3(grid), L::kWarps * 32, L::kBytes, st, p, prefix);
     if (e != cudaSuccess || grid < 2) return e;
     // Few units: each has many pieces, and its heads are shared out to more blocks.
     const bool few = static_cast<long long>(p.B) * p.Hkv * p.chunks * 4 < grid;
