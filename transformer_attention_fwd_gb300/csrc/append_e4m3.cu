@@ -17,6 +17,11 @@
 // CTA shares, rounds and stores.  Longer pages run in groups of 16 rows and read
 // their rows a second time (out of L2).  Query rows are taken by further CTAs of
 // the same launch, as in append.cu.
+//
+// 17100 tokens of 9 requests, 32 query and 8 KV heads, D 128 (385 MB, 280 of them
+// the queries): 64 us, 6.0 TB/s.  K and V of a head in one warp (128 registers, 16
+// warps per SM, for the query rows too) took 73 us.  One token for each of 64
+// requests: 4.4 us, a chain of dependent reads (offsets, length, block id, scale).
 #include <cuda_runtime.h>
 
 #include <algorithm>
