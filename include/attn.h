@@ -419,7 +419,8 @@ attn_status attn_append_paged(const attn_rows* q, const attn_rows* k, const attn
  *   The scale of a block that gets its first rows is the smallest power of two
  *   s >= 2^-100 with b * max|x| <= 448 s over the finite elements of the rows
  *   before their rotation; b = sqrt(2) * magnitude for keys of a call with
- *   rot_dim > 0 (no rotation raises an element more), else 1.  A block that
+ *   rot_dim > 0 (no rotation raises an element more), but at least 1 for
+ *   rot_dim < D (elements pass through), else 1.  A block that
  *   holds rows of its request already (from earlier slots) keeps the larger of
  *   that and its present scale; if the scale grows, the older rows are divided
  *   by the ratio and rounded again (exact but for values under 2^-6 * scale).

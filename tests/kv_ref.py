@@ -84,9 +84,12 @@ def pow2_scale(amax: float, limit: float) -> float:
     return s
 
 
-def k_limit(magnitude: float, rotated: bool) -> float:
-    m = float(torch.tensor(magnitude, dtype=torch.float32))
-    return float(torch.tensor(E4M3_MAX / (math.sqrt(2.0) * m), dtype=torch.float32)) if rotated else E4M3_MAX
+def k_limit(magnitude: float, rot: int, D: int) -> float:
+    """448 / b of rotated keys: b = sqrt(2) * magnitude, at least 1 if part of the head passes."""
+    if rot == 0:
+        return E4M3_MAX
+    b = math.sqrt(2.0) * float(torch.tensor(magnitude, dtype=torch.float32))
+    return float(torch.tensor(E4M3_MAX / (max(b, 1.0) if rot < D else b), dtype=torch.float32))
 
 
 def gather(cache, table, b, n):

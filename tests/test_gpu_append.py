@@ -115,7 +115,7 @@ class Problem:
 
     def check_scales(self, cache, skip, rotate):
         """Scales are exact; older rows of a grown block are its codes divided and rounded."""
-        now, limits = self.dev_scales.cpu(), (kv_ref.k_limit(self.magnitude, rotate and len(self.freq) > 0), 448.0)
+        now, limits = self.dev_scales.cpu(), (kv_ref.k_limit(self.magnitude, 2 * len(self.freq) if rotate else 0, self.D), 448.0)
         want, old_rows = self.scales.clone(), torch.zeros(self.cache.shape[0], self.page, dtype=torch.bool)
         cu, lens = self.cu.tolist(), self.lens.tolist()
         for b in range(len(lens)):
@@ -156,6 +156,8 @@ CASES = [
     dict(new=[19, 64], past=[0, 33], dtype="f16", inter=True, rot=64),
     dict(new=[19, 20], past=[0, 33], dtype="f16", rot=20, D=64),
     dict(new=[9, 14], past=[2, 3], rot=36, magnitude=1.25, Hkv=5),
+    dict(new=[9, 14], past=[2, 3], rot=6, magnitude=0.5),           # what passes is larger than what turns
+    dict(new=[9, 14], past=[2, 3], magnitude=0.5),
     dict(new=[9, 14], past=[2, 3], rot=0),
     dict(new=[700, 400], past=[0, 100], Hq=32, Hkv=8),
     dict(new=[4, 5], past=[20, 30], tail=6),                      # rows behind the last request

@@ -3,8 +3,9 @@
 //
 // A block's scale is the smallest power of two s with b * max|x| <= 448 s over
 // its finite elements (448: the largest e4m3 value), b = sqrt(2) * magnitude
-// for rotated keys, else 1.  A rotation raises no component above sqrt(2) times
-// the pair's larger one, so the scale needs the elements before the rotation
+// for rotated keys (at least 1 if part of the head passes through), else 1.  A
+// rotation raises no component above sqrt(2) times the pair's larger one, so the
+// scale needs the elements before the rotation
 // only: it is an exact comparison of input values, the same whatever the
 // rounding of the rotation.  A power of two costs e4m3 no precision (only the
 // subnormal end moves), and the rows a partly filled block holds follow a
@@ -274,9 +275,9 @@ cudaError_t launch_append_paged_e4m3(const AppendShape& s, const RopeShape& r, c
                                      const RopeRows& k, const RopeRows& v, const LaunchEnv& env,
                                      int* grid_out, int* kernels_launched) {
     AppendParams p = append_params(s, r, q, k, v, env);
-    p.k_limit = r.rot_dim > 0
-                    ? static_cast<float>(448.0 / (1.4142135623730951 * static_cast<double>(r.magnitude)))
-                    : kE4m3Max;
+    // What a rotation may raise a key's element by; elements that pass through stay.
+    const double raise = r.rot_dim > 0 ? 1.4142135623730951 * static_cast<double>(r.magnitude) : 1.0;
+    p.k_limit = static_cast<float>(448.0 / (r.rot_dim < r.D ? std::max(raise, 1.0) : raise));
     // Request b's pages are items cu[b] / page + 2 b and on: it touches at most
     // n / page + 2 of them, so the ranges do not meet.
     p.splits = static_cast<unsigned>((2 * k.heads + kPageWarps - 1) / kPageWarps);
