@@ -57,7 +57,7 @@ def _binding_compile(obj: str) -> list[str]:
 def _binding_link(obj: str, out: str) -> list[str]:
     lib = os.path.join(_torch(), "lib")
     return ["g++", "-shared", "-o", out, obj, "-L", BUILD, "-l:libattn.so", "-L", lib, "-lc10", "-lc10_cuda",
-            "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+            "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
 
 
 def _inputs():

@@ -11,7 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -136,6 +136,12 @@ attn_rows rows_in(const char* name, const Tensor& x, const Tensor& like, int dev
     return r;
 }
 
+// A new contiguous tensor from torch's CUDA allocator (at::empty without the
+// dispatcher: these calls are not traced).
+Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
+    return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+}
+
 // The output of x: the caller's, or a new tensor.
 Tensor rows_out(const char* name, const Tensor& x, const Tensor* given, attn_rows& r) {
     Tensor out;
@@ -145,7 +151,7 @@ Tensor rows_out(const char* name, const Tensor& x, const Tensor* given, attn_row
             refuse("out_", name, " must be ", x.sizes(), " ", x.scalar_type(), " on ", x.device());
         last_dim(out, name);
     } else {
-        out = at::empty(x.sizes(), x.options());
+        out = fresh(x.sizes(), x.scalar_type(), x);
     }
     const auto n = out.dim();
     r.y = out.data_ptr();
@@ -358,10 +364,10 @@ PyObject* decode_e4m3(PyObject* const* a, Py_ssize_t n) {
             refuse("lse must hold [", B, ", ", Hq, "] = ", B * Hq, " contiguous float32 elements");
         on_device(*given_lse, "lse", device);
     }
-    const Tensor out = given ? *given : at::empty(q.sizes(), q.options());
+    const Tensor out = given ? *given : fresh(q.sizes(), q.scalar_type(), q);
     std::optional<Tensor> lse;
     if (given_lse) lse = *given_lse;
-    else if (a[8] == Py_True) lse = at::empty({B, Hq}, q.options().dtype(at::kFloat));
+    else if (a[8] == Py_True) lse = fresh({B, Hq}, at::kFloat, q);
     const int b = as_int(B, "B"), hq = as_int(Hq, "Hq"), hkv = as_int(Hkv, "Hkv"), d = as_int(D, "D");
     const int p = as_int(page, "page_size"), w = as_int(pages, "max_pages"), nb = as_int(blocks, "num_blocks");
     const attn_dtype type = type_of(q);
