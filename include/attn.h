@@ -449,9 +449,13 @@ attn_status attn_append_paged_e4m3(const attn_rows* q, const attn_rows* k, const
  * fp32 sums: codes are exact in fp16; a query head is multiplied by a power of
  * two that keeps it in range; a key's weight p_j vs_j is rounded to fp16
  * relative to the largest one so far.  Any group Hq / Hkv.  The other arguments,
- * checks and errors are those of attn_fwd_decode_paged.  The workspace (slice
- * geometry, pieces of what slice boundaries cut) is allocated and freed on
- * `stream`, from a memory pool of the library's that keeps it from call to call.
+ * checks and errors are those of attn_fwd_decode_paged.  The table's width says
+ * how long a context may be: up to 1024 to 8192 keys, the more the fewer
+ * (request, KV head) pairs there are, a call is one launch without a workspace,
+ * so a table no wider than the longest request needs is the faster one.  Beyond,
+ * and for thousands of such pairs, the workspace (slice geometry, pieces of
+ * what slice boundaries cut) is allocated and freed on `stream`, from a memory
+ * pool of the library's that keeps it from call to call.
  */
 attn_status attn_fwd_decode_paged_e4m3(const void* q, const void* kv_cache, const float* scales,
                                        const int* block_table, const int* seq_lens, void* o,

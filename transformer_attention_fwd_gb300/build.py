@@ -24,7 +24,8 @@ LIB = os.path.join(BUILD, "libattn.so")
 BINDING = os.path.join(BUILD, "_attn_binding.so")
 
 SOURCES = ["attn_api.cu", "prefill_bf16.cu", "prefill_d64.cu", "decode_bf16.cu", "simt_f32.cu",
-           "varlen_sched.cu", "rope.cu", "append.cu", "append_e4m3.cu", "decode_e4m3.cu"]
+           "varlen_sched.cu", "rope.cu", "append.cu", "append_e4m3.cu", "decode_e4m3.cu",
+           "decode_e4m3_short.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
               "--expt-relaxed-constexpr", "-I", INCLUDE]

@@ -1268,8 +1268,8 @@ attn_status attn_fwd_decode_paged_e4m3(const void* q, const void* kv_cache, cons
     s.f16 = dtype == ATTN_F16 ? 1 : 0;
     const size_t bytes = decode_e4m3_workspace_bytes(s, env.num_sms);
     void* ws = nullptr;
-    cudaError_t e = workspace_alloc(&ws, bytes, env);
-    if (e != cudaSuccess || ws == nullptr) {
+    cudaError_t e = bytes > 0 ? workspace_alloc(&ws, bytes, env) : cudaSuccess;
+    if (e != cudaSuccess || (bytes > 0 && ws == nullptr)) {
         cudaGetLastError();
         return fail(ATTN_ERR_NO_MEMORY, "paged decode workspace of %zu bytes: %s", bytes, cudaGetErrorString(e));
     }
@@ -1278,8 +1278,10 @@ attn_status attn_fwd_decode_paged_e4m3(const void* q, const void* kv_cache, cons
                                  reinterpret_cast<const int32_t*>(block_table),
                                  reinterpret_cast<const int32_t*>(seq_lens), static_cast<uint16_t*>(o), lse, ws,
                                  s, env, &grid, &kernels);
-    cudaError_t f = cudaFreeAsync(ws, env.stream);
-    if (e == cudaSuccess && f != cudaSuccess) e = f;
+    if (ws) {
+        cudaError_t f = cudaFreeAsync(ws, env.stream);
+        if (e == cudaSuccess && f != cudaSuccess) e = f;
+    }
     if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
     record_launch(grid, 0, kernels);
     return ok();

@@ -187,6 +187,12 @@ cudaError_t launch_append_paged_e4m3(const AppendShape& s, const RopeShape& r, c
 
 // Decode over the paged 8-bit cache: kv [num_blocks, 2, Hkv, page, D] codes,
 // scales [num_blocks, 2, Hkv].
+// The workspace is 0 bytes where a cluster takes each unit (decode_e4m3_short.cu):
+// decode_e4m3_short_ranks() CTAs, 0 otherwise.
+int decode_e4m3_short_ranks(const PagedShape& s, int num_sms);
+struct E4m3Params;
+cudaError_t launch_decode_e4m3_short(const E4m3Params& p, const PagedShape& s, int ranks, const LaunchEnv& env,
+                                     int* grid_out);
 size_t decode_e4m3_workspace_bytes(const PagedShape& s, int num_sms);
 cudaError_t launch_decode_paged_e4m3(const uint16_t* q, const uint8_t* kv, const float* scales,
                                      const int32_t* block_table, const int32_t* seq_lens,
