@@ -27,19 +27,21 @@
 // warp streams its tiles through a ring of its own with 16-byte asynchronous
 // copies; nothing in the loop waits for another warp.  Units inside one warp's
 // range are written at once; the pieces of the others are merged in the CTA at
-// its end, and those that a CTA boundary cuts by the combine kernel.  Two
-// small CTAs share an SM, so that one's start and end pass under the other's
-// streaming.  (More of them than fit at once, to even out the SMs, lost 5 us for
-// each further wave: a start costs that much.)
+// its end, and those that a CTA boundary cuts by the combine kernel.  Two to four
+// small CTAs share an SM, as registers allow, so that one's start and end pass
+// under the others' streaming (three instead of two, with rings of three tiles
+// instead of four: 92.0 -> 88.6 us below; 44.7 -> 43.6).  More of them than fit at
+// once, to even out the SMs, lost 5 us for each further wave: a start costs that
+// much.
 //
-// 64 requests of 4096 keys, Hq 32, Hkv 8, D 128, 16-token blocks (539 MB): 91 us,
-// 5.9 TB/s.  Every CTA sums the lengths and finds its place in 2.8 us, the first
-// tiles are there after 5.9, the SMs run dry between 78 and 88 us (together they
-// stream at 7 TB/s), merging takes 1 to 2 us and the combine kernel 3.  With 8
-// query heads per KV head and ragged lengths (231 MB) 44 us, by the same fixed
+// 64 requests of 4096 keys, Hq 32, Hkv 8, D 128, 16-token blocks (539 MB): 88.6 us,
+// 6.1 TB/s.  Every CTA sums the lengths and finds its place in 2.8 us, the first
+// tiles are there after 5.6, the SMs run dry between 75 and 81 us (together they
+// stream at 7.2 TB/s), merging takes 1 to 2 us and the combine kernel 3.  With 8
+// query heads per KV head and ragged lengths (231 MB) 43.6 us, by the same fixed
 // costs (short contexts, for which they are all of the time, are in
-// decode_e4m3_short.cu); at D = 64 94 us for 540 MB.  With 16 heads per KV head instruction issue
-// bounds it: 105 us (D = 128), 123 us (D = 64).
+// decode_e4m3_short.cu); at D = 64 94 us for 540 MB.  With 16 heads per KV head
+// instruction issue bounds it: 105 us (D = 128), 123 us (D = 64).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -56,10 +58,10 @@ namespace {
 template <int D, int HC>
 struct E4m3Layout {
     static constexpr int kWarps = 4;
-    static constexpr int kPerSm = D == 128 ? 2 : (HC == 8 ? 4 : 3);  // CTAs, as registers allow
+    static constexpr int kPerSm = D == 128 ? (HC == 8 ? 3 : 2) : (HC == 8 ? 4 : 3);  // CTAs, as registers allow
     static constexpr int kStage = kStageBytes<D>;
     static constexpr int kPiece = HC * D * 4;
-    static constexpr int kStages = D == 128 ? 4 : (HC == 8 ? 4 : 5);
+    static constexpr int kStages = D == 128 ? (HC == 8 ? 3 : 4) : (HC == 8 ? 4 : 5);
     static constexpr int kPieceOff = kWarps * kStages * kStage;
     static constexpr int kMlOff = kPieceOff + kWarps * kPiece;  // [warp][2][HC] float4
     static constexpr int kMetaOff = kMlOff + kWarps * 2 * HC * 16;
