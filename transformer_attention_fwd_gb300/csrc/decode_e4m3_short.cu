@@ -50,8 +50,22 @@ struct ShortLayout {
     static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "CTAs to an SM");
 };
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The end of a CTA that has nothing to add up: it takes part in both barriers all
+// the same.  So no CTA reads the shared memory of one that is gone, even if the
+// lengths change under the kernel and its CTAs do not see the same.
+__device__ __forceinline__ void leave(int ranks) {
+    if (ranks == 1) return;
+    cluster_arrive();
+    cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+}
 
 // Shared memory of another CTA of the cluster, at this CTA's address.
 __device__ __forceinline__ uint32_t of_rank(const void* p, int rank) {
@@ -95,12 +109,12 @@ decode_e4m3_short_kernel(const E4m3Params p, int ranks) {
     const int heads = min(HC, p.group - chunk * HC);
     const int64_t row0 = static_cast<int64_t>(cc.b) * p.Hq + hkv * p.group + chunk * HC;
     if (asked != cc.len && cc.unit == 0 && rank == 0 && threadIdx.x == 0) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
-    if (cc.tiles == 0) {  // no keys: the same for the whole cluster
-        if (rank > 0) return;
+    if (cc.tiles == 0) {  // no keys
+        if (rank > 0) return leave(ranks);
         for (int i = threadIdx.x; i < heads * (D / 8); i += kWarps * 32)
             reinterpret_cast<uint4*>(p.o + row0 * D)[i] = make_uint4(0, 0, 0, 0);
         if (p.lse && threadIdx.x < heads) p.lse[row0 + threadIdx.x] = -INFINITY;
-        return;
+        return leave(ranks);
     }
 
     // Tiles of a warp, and the CTAs and this CTA's warps that have any.
@@ -151,7 +165,7 @@ decode_e4m3_short_kernel(const E4m3Params p, int ranks) {
             }
         }
     }
-    if (parts == 1) return;  // the same for the whole cluster
+    if (parts == 1) return leave(ranks);
     cluster_arrive();
     cluster_wait();
     // Heads rank, rank + ranks, ..: a warp each.
