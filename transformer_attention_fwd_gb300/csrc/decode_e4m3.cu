@@ -41,7 +41,7 @@
 // query heads per KV head and ragged lengths (231 MB) 43.6 us, by the same fixed
 // costs (short contexts, for which they are all of the time, are in
 // decode_e4m3_short.cu); at D = 64 94 us for 540 MB.  With 16 heads per KV head
-// instruction issue bounds it: 105 us (D = 128), 123 us (D = 64).
+// instruction issue bounds it: 103 us (D = 128), 121 us (D = 64).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -61,7 +61,7 @@ struct E4m3Layout {
     static constexpr int kPerSm = D == 128 ? (HC == 8 ? 3 : 2) : (HC == 8 ? 4 : 3);  // CTAs, as registers allow
     static constexpr int kStage = kStageBytes<D>;
     static constexpr int kPiece = HC * D * 4;
-    static constexpr int kStages = D == 128 ? (HC == 8 ? 3 : 4) : (HC == 8 ? 4 : 5);
+    static constexpr int kStages = HC == 8 ? 3 : 4;
     static constexpr int kPieceOff = kWarps * kStages * kStage;
     static constexpr int kMlOff = kPieceOff + kWarps * kPiece;  // [warp][2][HC] float4
     static constexpr int kMetaOff = kMlOff + kWarps * 2 * HC * 16;
