@@ -447,9 +447,11 @@ attn_status attn_append_paged_e4m3(const attn_rows* q, const attn_rows* k, const
  * values >= 0).  q and o are [B, Hq, 1, D] in dtype (ATTN_BF16 or ATTN_F16), lse
  * [B, Hq] float32 or NULL.  The products run on the tensor cores in fp16 with
  * fp32 sums: codes are exact in fp16; a query head is multiplied by a power of
- * two that keeps it in range; a key's weight p_j vs_j is rounded to fp16
- * relative to the largest one so far.  Any group Hq / Hkv.  The other arguments,
- * checks and errors are those of attn_fwd_decode_paged.  The table's width says
+ * two that keeps it in range (elements under 2^-24 of its largest are off by up
+ * to 2^-34 of that); a key's weight p_j vs_j is held in two fp16 terms, within
+ * 2^-24 of it down to 2^-10 of the largest so far, within 2^-14 under that (and 0
+ * under 2^-125).  Any group Hq / Hkv.  The other arguments, checks and errors are
+ * those of attn_fwd_decode_paged.  The table's width says
  * how long a context may be: up to 1024 to 8192 keys, the more the fewer
  * (request, KV head) pairs there are, a call is one launch without a workspace,
  * so a table no wider than the longest request needs is the faster one.  Beyond,

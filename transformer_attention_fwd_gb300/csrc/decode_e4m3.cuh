@@ -17,6 +17,16 @@ namespace attn {
 constexpr int kTile = 16;          // keys of a tile
 constexpr int kMaxPrefixB = 1024;  // requests whose tile counts a CTA sums itself
 constexpr float kSlack = 6.0f;
+// A weight is held as two fp16 terms, what the first leaves out in the second, relative
+// to 2^mv, mv lying kLift under the maximum it follows: the largest weights are 2^kLift to
+// 2^(kLift + kSlack), inside fp16.  The two terms are within 2^-24 of a weight from 1/2 on
+// and within 2^-25 of the smaller ones: from 2^-kLow on (kLift + kLow binades under the
+// reference) within 2^-14 of itself.  Still smaller ones get products of their own,
+// relative to the largest of them (unit_tile).
+constexpr float kLift = 9.0f;
+constexpr float kLow = 11.0f;
+// A weight this many binades under 2^mv, 2^-125 of the reference, is 0.
+constexpr float kGone = 116.0f;
 // References start here: below any score, and finite, so that no difference of
 // two of them is NaN.
 constexpr float kLowest = -3.0e38f;
@@ -131,7 +141,9 @@ struct UnitState {
 };
 
 // Q fragments of heads hq0 .. hq0 + heads - 1, each times a power of two that
-// takes its largest element to [512, 1024).
+// takes its largest element to [512, 1024).  Elements down to 2^-24 of the largest are
+// then exact in fp16 (bf16's 8 bits, fp16's 11), smaller ones off by at most 2^-34 of the
+// largest: a thousandth of the rounding of the largest's product in an fp32 sum.
 template <int D, int HC, bool kF16>
 __device__ __forceinline__ void unit_begin(const E4m3Params& p, const Cursor& c, int lane,
                                            UnitState<D, HC>& s) {
@@ -300,6 +312,29 @@ struct MergedHeads {
     }
 };
 
+// Two weights as two terms each, P^T's operand.
+struct Weights {
+    uint32_t hi, lo;
+    __device__ __forceinline__ void set(float a, float b) {
+        const uint32_t h = pack_f16x2(a, b);
+        hi = transpose8x8(h);
+        lo = transpose8x8(pack_f16x2(a - f16_lo_to_f32(h), b - f16_hi_to_f32(h)));
+    }
+};
+
+// A head's heaviest weights out of the exponents left, and what the products with them are
+// multiplied by; a lane's two keys.  Those taken are -inf from then on.
+__device__ __forceinline__ float heaviest(float& e0, float& e1, float& w0, float& w1) {
+    const float top = heads_max(fmaxf(e0, e1));
+    const float down = top < 0.0f && top > -kGone ? floorf(top - kLift) : 0.0f;
+    const bool later0 = e0 - down < -kLow, later1 = e1 - down < -kLow;  // false for NaN
+    w0 = later0 ? 0.0f : ex2_approx(e0 - down);
+    w1 = later1 ? 0.0f : ex2_approx(e1 - down);
+    e0 = later0 ? e0 : -INFINITY;
+    e1 = later1 ? e1 : -INFINITY;
+    return ex2_approx(down);
+}
+
 // One tile of a warp's ring: scores, weights, and the weighted V rows.
 template <int D, int HC, bool kWholePages>
 __device__ __forceinline__ void unit_tile(const uint8_t* stage, int valid, int lane, UnitState<D, HC>& s) {
@@ -373,14 +408,15 @@ __device__ __forceinline__ void unit_tile(const uint8_t* stage, int valid, int l
     for (int r = 0; r < kR; ++r)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            need |= x[r][i] > fminf(s.m[r][i & 1], s.mv[r][i & 1] - lift[(i >> 1) % kF]) + kSlack;
+            need |= x[r][i] > fminf(s.m[r][i & 1], (s.mv[r][i & 1] + kLift) - lift[(i >> 1) % kF]) + kSlack;
     if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float m = fmaxf(s.m[r][i], heads_max(fmaxf(x[r][i], x[r][i + 2])));
-                const float mv = fmaxf(s.mv[r][i], heads_max(fmaxf(x[r][i] + lift[0], x[r][i + 2] + lift[kF - 1])));
+                const float mv =
+                    fmaxf(s.mv[r][i], heads_max(fmaxf(x[r][i] + lift[0], x[r][i + 2] + lift[kF - 1])) - kLift);
                 const float alpha = ex2_approx(s.mv[r][i] - mv);
                 s.l[r][i] *= ex2_approx(s.m[r][i] - m);
                 s.m[r][i] = m;
@@ -393,23 +429,65 @@ __device__ __forceinline__ void unit_tile(const uint8_t* stage, int valid, int l
             }
         }
     }
-    uint32_t pb[kR][2];
+    float e[kR][4], w[kR][4], least = INFINITY;  // the weights' exponents, the weights
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        float w[4];
+    for (int r = 0; r < kR; ++r)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             s.l[r][i & 1] += ex2_approx(x[r][i] - s.m[r][i & 1]);
-            w[i] = ex2_approx(x[r][i] + (lift[(i >> 1) % kF] - s.mv[r][i & 1]));
+            e[r][i] = x[r][i] + (lift[(i >> 1) % kF] - s.mv[r][i & 1]);
+            w[r][i] = ex2_approx(e[r][i]);
+            least = fminf(least, e[r][i]);
         }
-        pb[r][0] = transpose8x8(pack_f16x2(w[0], w[1]));
-        pb[r][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+    if (__all_sync(0xffffffffu, least >= -kLow)) {
+        Weights pb[kR][2];
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            pb[r][0].set(w[r][0], w[r][1]);
+            pb[r][1].set(w[r][2], w[r][3]);
+        }
+#pragma unroll
+        for (int i = 0; i < kS; ++i) {
+            if (HC != 8) convert(i);
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                mma_f16(s.o[r][i], va[i][0], va[i][1], va[i][2], va[i][3], pb[r][0].hi, pb[r][1].hi);
+                mma_f16(s.o[r][i], va[i][0], va[i][1], va[i][2], va[i][3], pb[r][0].lo, pb[r][1].lo);
+            }
+        }
+        return;
     }
+    // Some keys are far below their head's reference (or past the unit's end).  The
+    // weights go in groups of kLift + kLow binades, from the largest down, each with
+    // products of its own relative to 2^(mv + down): so a head whose reference is one
+    // heavy key with an empty value still has the others'.
+    bool more = true;
+    while (more) {
+        Weights pb[kR][2];
+        float back[kR][2];
+        float most = -INFINITY;
+        auto half = [&](int r) {
+            back[r][0] = heaviest(e[r][0], e[r][2], w[r][0], w[r][2]);
+            back[r][1] = heaviest(e[r][1], e[r][3], w[r][1], w[r][3]);
+            most = fmaxf(most, fmaxf(fmaxf(e[r][0], e[r][1]), fmaxf(e[r][2], e[r][3])));
+            pb[r][0].set(w[r][0], w[r][1]);
+            pb[r][1].set(w[r][2], w[r][3]);
+        };
+        half(0);  // (a loop here is not unrolled, and puts the arrays in memory)
+        if (kR == 2) half(kR - 1);
+        more = __any_sync(0xffffffffu, most > -kGone);
 #pragma unroll
-    for (int i = 0; i < kS; ++i) {
-        if (HC != 8) convert(i);
+        for (int i = 0; i < kS; ++i) {
+            if (HC != 8) convert(i);
 #pragma unroll
-        for (int r = 0; r < kR; ++r) mma_f16(s.o[r][i], va[i][0], va[i][1], va[i][2], va[i][3], pb[r][0], pb[r][1]);
+            for (int r = 0; r < kR; ++r) {
+                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma_f16(part, va[i][0], va[i][1], va[i][2], va[i][3], pb[r][0].hi, pb[r][1].hi);
+                mma_f16(part, va[i][0], va[i][1], va[i][2], va[i][3], pb[r][0].lo, pb[r][1].lo);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) s.o[r][i][n] = fmaf(part[n], back[r][n & 1], s.o[r][i][n]);
+            }
+        }
     }
 }
 
