@@ -6,9 +6,13 @@ contiguity, allocate outputs with torch, and pass raw device pointers plus the
 current CUDA stream to the C ABI.  Every step of the computation runs in the
 library's CUDA kernels; there is no fallback.  If a library is missing the
 import-time load raises.
+
+``stream``: the torch stream a call runs on (default: the current one).  The
+outputs it allocates belong to that stream, as if it were the current one.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -126,6 +130,17 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _allocating_for(stream, device):
+    """A context in which torch allocates for the stream a call runs on: a block that the
+    current stream has freed may still be in use there."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream.cuda_stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -182,13 +197,14 @@ def _shapes(q, k, v):
     return B, Hq, Hkv, Tq, Tk, D
 
 
-def _outputs(q, out, lse, want_lse):
+def _outputs(q, out, lse, want_lse, stream):
     B, Hq, Tq, D = q.shape
     _check_buffer("out", out, q.shape, q.dtype, q.device)
     _check_buffer("lse", lse, (B, Hq, Tq), torch.float32, q.device)
-    o = torch.empty_like(q) if out is None else out
-    if lse is None and want_lse:
-        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=q.device)
+    with _allocating_for(stream, q.device):
+        o = torch.empty_like(q) if out is None else out
+        if lse is None and want_lse:
+            lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=q.device)
     return o, lse
 
 
@@ -211,7 +227,7 @@ def attn_fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None
     else:
         raise ValueError(f"unsupported dtype {q.dtype}")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    o, lse = _outputs(q, out, lse, want_lse)
+    o, lse = _outputs(q, out, lse, want_lse, stream)
     _check(lib.attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Tq, Tk, D,
                         1 if causal else 0, scale, dt, _stream_handle(stream)))
     return o, lse
@@ -256,7 +272,7 @@ def attn_fwd_prefill(q, k, v, causal: bool = False, scale: float | None = None, 
     if q.dtype != torch.bfloat16:
         raise ValueError("attn_fwd_prefill takes bf16 tensors")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    o, lse = _outputs(q, out, lse, want_lse)
+    o, lse = _outputs(q, out, lse, want_lse, stream)
     _check(lib.attn_fwd_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Tq,
                                 Tk, D, 1 if causal else 0, scale, _stream_handle(stream)))
     return o, lse
@@ -272,7 +288,7 @@ def attn_fwd_decode(q, k, v, scale: float | None = None, num_splits: int = 0, ou
     if q.dtype != torch.bfloat16:
         raise ValueError("attn_fwd_decode takes bf16 tensors")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    o, lse = _outputs(q, out, lse, want_lse)
+    o, lse = _outputs(q, out, lse, want_lse, stream)
     _check(lib.attn_fwd_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Tk, D,
                                scale, int(num_splits), _stream_handle(stream)))
     return o, lse
@@ -286,7 +302,7 @@ def attn_fwd_window(q, k, v, window: int, scale: float | None = None, out=None, 
     if q.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("attn_fwd_window takes bf16 or fp16 tensors")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    o, lse = _outputs(q, out, lse, want_lse)
+    o, lse = _outputs(q, out, lse, want_lse, stream)
     _check(lib.attn_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Tq, Tk,
                                D, int(window), scale,
                                ATTN_F16 if q.dtype == torch.float16 else ATTN_BF16,
@@ -325,9 +341,10 @@ def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, causal: bool, window: i
     _check_buffer("out", out, q.shape, q.dtype, q.device)
     _check_buffer("lse", lse, (Hq, total_q), torch.float32, q.device)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    o = torch.empty_like(q) if out is None else out
-    if lse is None and want_lse:
-        lse = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device)
+    with _allocating_for(stream, q.device):
+        o = torch.empty_like(q) if out is None else out
+        if lse is None and want_lse:
+            lse = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device)
     _check(lib.attn_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens_q),
                                _ptr(cu_seqlens_k), B, Hq, Hkv, total_q, total_k, D,
                                1 if causal else 0, int(window), scale,
@@ -364,9 +381,10 @@ def attn_fwd_decode_paged(q, kv_cache, block_table, seq_lens, scale: float | Non
     _check_buffer("out", out, q.shape, q.dtype, q.device)
     _check_buffer("lse", lse, (B, Hq), torch.float32, q.device)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    o = torch.empty_like(q) if out is None else out
-    if lse is None and want_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    with _allocating_for(stream, q.device):
+        o = torch.empty_like(q) if out is None else out
+        if lse is None and want_lse:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     _check(lib.attn_fwd_decode_paged(_ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens),
                                      _ptr(o), _ptr(lse), B, Hq, Hkv, D, page,
                                      block_table.shape[1], nblk, scale,

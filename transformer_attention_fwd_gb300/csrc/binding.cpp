@@ -13,6 +13,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -91,12 +92,25 @@ void current(int device) {
                "; call under torch.cuda.device(", device, ")");
 }
 
-cudaStream_t stream_of(PyObject* o, int device) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
-    void* p = PyLong_AsVoidPtr(o);
-    if (PyErr_Occurred()) throw PythonError{};
-    return static_cast<cudaStream_t>(p);
-}
+// The stream a call runs on: the given handle, or torch's current one.  While this
+// lives it is torch's current stream, so that new outputs come out of its own memory:
+// torch's allocator orders the reuse of a block by the stream it was asked for on, and
+// one freed by the caller's current stream may still be in use there.
+struct OnStream {
+    cudaStream_t stream;
+    std::optional<c10::cuda::CUDAStreamGuard> guard;
+    OnStream(PyObject* o, int device) {
+        const auto index = static_cast<c10::DeviceIndex>(device);
+        if (o == Py_None) {
+            stream = c10::cuda::getCurrentCUDAStream(index).stream();
+            return;
+        }
+        void* p = PyLong_AsVoidPtr(o);
+        if (PyErr_Occurred()) throw PythonError{};
+        stream = static_cast<cudaStream_t>(p);
+        guard.emplace(p ? c10::cuda::getStreamFromExternal(stream, index) : c10::cuda::getDefaultCUDAStream(index));
+    }
+};
 
 // A contiguous tensor of this type and shape on the device.
 void exact(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape, int device) {
@@ -257,7 +271,7 @@ PyObject* rope(PyObject* const* a, Py_ssize_t n) {
         if (PyErr_Occurred()) throw PythonError{};
     }
     current(device);
-    const cudaStream_t stream = stream_of(a[6], device);
+    const OnStream on(a[6], device);
     const Tensor yq = rows_out("q", q, given_q, rq);
     std::optional<Tensor> yk;
     if (k) yk = rows_out("k", *k, given_k, rk);
@@ -265,8 +279,8 @@ PyObject* rope(PyObject* const* a, Py_ssize_t n) {
     attn_status st;
     Py_BEGIN_ALLOW_THREADS
     st = norm ? attn_qk_norm_rope(&rq, k ? &rk : nullptr, weight[0], weight[1], static_cast<float>(eps), pos, b, t, d,
-                                  rotation.r, type, stream)
-              : attn_rope(&rq, k ? &rk : nullptr, pos, b, t, d, rotation.r, type, stream);
+                                  rotation.r, type, on.stream)
+              : attn_rope(&rq, k ? &rk : nullptr, pos, b, t, d, rotation.r, type, on.stream);
     Py_END_ALLOW_THREADS
     return st == ATTN_OK ? two(yq, yk) : failed(st);
 }
@@ -305,7 +319,7 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
     const int* pos_p = positions ? ints(*positions, "positions", {total}, device) : nullptr;
     const RotationArg rotation(a[7], device);
     current(device);
-    const cudaStream_t stream = stream_of(a[12], device);
+    const OnStream on(a[12], device);
     std::optional<Tensor> yq, yk;
     if (q) yq = rows_out("q", *q, given_q, rq);
     if (given_k) yk = rows_out("k", k, given_k, rk);
@@ -317,9 +331,9 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
     attn_status st;
     Py_BEGIN_ALLOW_THREADS
     st = scales ? attn_append_paged_e4m3(q ? &rq : nullptr, &rk, &rv, cu_p, lens_p, pos_p, table_p, cache_p, scales_p, b,
-                                         t, d, p, w, nb, rotation.r, type, stream)
+                                         t, d, p, w, nb, rotation.r, type, on.stream)
                 : attn_append_paged(q ? &rq : nullptr, &rk, &rv, cu_p, lens_p, pos_p, table_p, cache_p, b, t, d, p, w, nb,
-                                    rotation.r, type, stream);
+                                    rotation.r, type, on.stream);
     Py_END_ALLOW_THREADS
     return st == ATTN_OK ? two(yq, yk) : failed(st);
 }
@@ -352,7 +366,7 @@ PyObject* decode_e4m3(PyObject* const* a, Py_ssize_t n) {
         if (PyErr_Occurred()) throw PythonError{};
     }
     current(device);
-    const cudaStream_t stream = stream_of(a[9], device);
+    const OnStream on(a[9], device);
     // The caller's buffers hold exactly what is written: [B, Hq, 1] serves [B, Hq].
     if (given) {
         if (given->scalar_type() != q.scalar_type() || given->numel() != q.numel() || !given->is_contiguous())
@@ -378,7 +392,7 @@ PyObject* decode_e4m3(PyObject* const* a, Py_ssize_t n) {
     attn_status st;
     Py_BEGIN_ALLOW_THREADS
     st = attn_fwd_decode_paged_e4m3(q_p, cache_p, scales_p, table_p, lens_p, out_p, lse_p, b, hq, hkv, d, p, w, nb,
-                                    static_cast<float>(scale), type, stream);
+                                    static_cast<float>(scale), type, on.stream);
     Py_END_ALLOW_THREADS
     return st == ATTN_OK ? two(out, lse) : failed(st);
 }
