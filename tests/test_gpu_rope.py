@@ -228,3 +228,28 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         _check(src, out, pos.cpu()[:, None], freq, False, 1.0, "replay")
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_the_angle_is_not_rounded_to_a_float(inter):
+    """fp32 rows (1, 0) return cos and sin themselves.  sincospif is within 1 ulp, 2^-23 of a
+    value, the turn by the rest of the phase rounds once more, and the phase's 32 bits leave
+    2^-32 half turns: next to a half turn, where the sine is small, a phase rounded to a float
+    is off by up to 2^-25 half turns, thirty times that."""
+    a = attn()
+    near_half = [2 ** 63 + s * ((64 + 128 * i) << 32) + (i << 20) for i in range(1, 1500, 47) for s in (-1, 1)]
+    for seed in range(20):
+        phases = near_half[:64] if seed == 0 else torch.randint(
+            -2 ** 63, 2 ** 63 - 1, (64,), generator=torch.Generator().manual_seed(seed)).tolist()
+        turns = torch.tensor([p - 2 ** 64 if p >= 2 ** 63 else p for p in phases], dtype=torch.int64)
+        assert len(turns) == 64
+        x = torch.zeros(1, 1, 128)
+        first = slice(0, 128, 2) if inter else slice(0, 64)
+        second = slice(1, 128, 2) if inter else slice(64, 128)
+        x[..., first] = 1.0
+        y, _ = a.attn_rope(x.cuda(), None, torch.ones(1, dtype=torch.int32, device="cuda"),
+                           a.Rotation(turns.cuda(), inter))
+        y = y.cpu().double()[0, 0]
+        angle = torch.tensor([(p % 2 ** 64) / 2.0 ** 64 * 2 * math.pi for p in phases], dtype=torch.float64)
+        for got, want in ((y[first], angle.cos()), (y[second], angle.sin())):
+            assert ((got - want).abs() <= 2.0 ** -22 * want.abs() + math.pi * 2.0 ** -32 + 2.0 ** -46).all()

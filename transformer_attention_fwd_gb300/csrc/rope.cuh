@@ -7,8 +7,7 @@
 // magnitude.  f arrives as a fraction of a turn per position in units of
 // 2^-64 turn, so t * f modulo one turn is the low 64 bits of one integer
 // product: exact, whatever the position.  The angle's error is the table's
-// rounding, |t| * 2^-65 turns, and the 2^-25 half turns of the float the top
-// 32 bits are rounded to.
+// rounding, |t| * 2^-65 turns, and the 2^-33 turns of its top 32 bits.
 //
 // A lane holds two 16-byte chunks of a row, chosen so that both elements of
 // each of its pairs are its own: chunks j and j + half for the halves layout,
@@ -55,13 +54,19 @@ struct RopeTable {
     float magnitude;
 };
 
-// magnitude * (cos, sin) of a pair's angle.
+// magnitude * (cos, sin) of a pair's angle.  Of the phase's top 32 bits (half turns of
+// 2^-31), the multiple of 128 next to them is exact as a float; its sine and cosine are
+// turned by the rest, at most 2^-25 half turns, to first order (the second is under 2^-47).
+// The float nearest to all 32 bits instead would leave an error of that size, more than
+// sincospif's own.
 __device__ __forceinline__ float2 rope_cos_sin(const RopeTable& t, int pair, int position) {
     const unsigned long long phase =
         static_cast<unsigned long long>(static_cast<long long>(position)) * t.turns[pair];
+    const unsigned near = static_cast<unsigned>((phase + 0x80000000u) >> 32) + 64u;  // wraps by whole turns
+    const float rest = static_cast<float>(static_cast<int>(near & 127u) - 64) * (0x1p-31f * 3.14159265f);
     float s, c;
-    sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &s, &c);
-    return make_float2(c * t.magnitude, s * t.magnitude);
+    sincospif(static_cast<float>(static_cast<int>(near & ~127u)) * 0x1p-31f, &s, &c);
+    return make_float2(fmaf(-s, rest, c) * t.magnitude, fmaf(c, rest, s) * t.magnitude);
 }
 
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
