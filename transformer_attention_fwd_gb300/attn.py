@@ -4,8 +4,8 @@ csrc/binding.cpp for the calls of a decode step that take microseconds.
 Argument marshalling only: the functions check tensor placement, dtype and
 contiguity, allocate outputs with torch, and pass raw device pointers plus the
 current CUDA stream to the C ABI.  Every step of the computation runs in the
-library's CUDA kernels; there is no fallback.  If a library is missing the
-import-time load raises.
+library's CUDA kernels; there is no fallback.  If libattn.so is missing the
+import raises; if the binding's native part is, the first call that needs it.
 
 ``stream``: the torch stream a call runs on (default: the current one).  The
 outputs it allocates belong to that stream, as if it were the current one.
@@ -18,6 +18,7 @@ import importlib.machinery
 import importlib.util
 import math
 import os
+import threading
 
 import torch
 
@@ -112,7 +113,22 @@ def _load_binding(path: str = BINDING_PATH):
     return module
 
 
-_native = _load_binding()
+class _Native:
+    """The native part's functions, loaded with the first of them."""
+    _lock = threading.Lock()
+
+    def __getattr__(self, name):
+        if name.startswith("_"):
+            raise AttributeError(name)
+        with self._lock:
+            if not self.__dict__:
+                self.__dict__.update((n, f) for n, f in vars(_load_binding()).items() if callable(f))
+        if name not in self.__dict__:
+            raise AttributeError(name)
+        return self.__dict__[name]
+
+
+_native = _Native()
 
 
 def last_error() -> str:

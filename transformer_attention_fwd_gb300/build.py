@@ -3,12 +3,13 @@ the Python binding with g++.
 
 Every translation unit is compiled in parallel, then linked into
 ``transformer_attention_fwd_gb300/_build/libattn.so`` and, against it and the
-installed torch, ``_build/_attn_binding.so``.  ptxas statistics (registers,
-spills, shared memory) are written to ``_build/ptxas.log``.
+installed torch (where there is one), ``_build/_attn_binding.so``.  ptxas
+statistics (registers, spills, shared memory) are written to ``_build/ptxas.log``.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -38,12 +39,13 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _torch() -> str:
-    import importlib.util
+def _torch() -> str | None:
+    """The installed torch's folder; None without one for CUDA."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("torch not found")
-    return os.path.dirname(spec.origin)
+    if spec is None or not spec.origin:
+        return None
+    folder = os.path.dirname(spec.origin)
+    return folder if os.path.exists(os.path.join(folder, "lib", "libtorch_cuda.so")) else None
 
 
 def _binding_compile(obj: str) -> list[str]:
@@ -65,54 +67,72 @@ def _inputs():
     return glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
 
 
-def is_stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _older(target: str) -> bool:
+    """The target is missing, or older than an input."""
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = os.path.getmtime(target)
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
+def _binding_stale() -> bool:
+    return _torch() is not None and (_older(BINDING) or not os.path.exists(LIB))
+
+
+def is_stale() -> bool:
+    return _older(LIB) or _binding_stale()
+
+
+def _start(cmd: list[str]) -> subprocess.Popen:
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _link(cmd, target: str) -> None:
+    """Runs the link command cmd(output) and puts its output in the target's place."""
+    tmp = target + f".tmp{os.getpid()}"
+    r = subprocess.run(cmd(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout)
+        raise RuntimeError(f"link of {os.path.basename(target)} failed")
+    os.replace(tmp, target)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libattn.so if any source changed (or ``force``); return its path."""
-    if not force and not is_stale():
+    """Compile libattn.so, and the binding where torch with CUDA is installed, if any source
+    changed (or ``force``); return libattn.so's path.  The library needs neither torch nor
+    Python's headers, and is there even if the binding fails."""
+    lib, binding = force or _older(LIB), _torch() is not None and (force or _binding_stale())
+    if not lib and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    cc = nvcc()
+    procs, logs, objs, failed = [], [], [], []
     binding_obj = os.path.join(BUILD, "binding.o")
-    binding_cmd = _binding_compile(binding_obj)
-    procs = [("binding.cpp", None, binding_cmd,
-              subprocess.Popen(binding_cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))]
-    for src in SOURCES:
-        obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-        cmd = [cc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-        procs.append((src, obj, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE,
-                                                        stderr=subprocess.STDOUT, text=True)))
-    logs, objs, failed = [], [], []
-    for src, obj, cmd, p in procs:
+    if binding:
+        procs.append(("binding.cpp", None, _start(_binding_compile(binding_obj))))
+    if lib:
+        cc = nvcc()
+        for src in SOURCES:
+            obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+            objs.append(obj)
+            procs.append((src, obj, _start([cc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])))
+    for src, _, p in procs:
         out, _ = p.communicate()
         logs.append(f"== {src}\n{out}")
         if p.returncode != 0:
             failed.append(src)
-        if obj is not None:
-            objs.append(obj)
-    with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
-        f.write("\n".join(logs))
+    if lib:
+        with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
+            f.write("\n".join(logs))
     if failed:
         sys.stderr.write("\n".join(logs))
+    if set(failed) - {"binding.cpp"}:
         raise RuntimeError(f"nvcc failed for {failed}")
-    tmp = LIB + f".tmp{os.getpid()}"
-    link = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout)
-        raise RuntimeError("link of libattn.so failed")
-    os.replace(tmp, LIB)
-    tmp = BINDING + f".tmp{os.getpid()}"
-    r = subprocess.run(_binding_link(binding_obj, tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout)
-        raise RuntimeError("link of _attn_binding.so failed")
-    os.replace(tmp, BINDING)
+    if lib:
+        _link(lambda out: [cc, *ARCH, "-shared", "-o", out, *objs], LIB)
+    if failed:
+        raise RuntimeError("g++ failed for binding.cpp")
+    if binding:
+        _link(lambda out: _binding_link(binding_obj, out), BINDING)
     if verbose:
         print("\n".join(logs))
     return LIB
