@@ -80,3 +80,22 @@ except RuntimeError as e:
                        env={**os.environ, "PYTHONPATH": str(tmp_path)})
     assert r.returncode == 0, r.stderr
     assert "_attn_binding.so is missing" in r.stdout
+
+
+def test_a_binding_of_another_torch_is_stale_and_refused(b, monkeypatch):
+    import torch
+    from transformer_attention_fwd_gb300 import attn, build
+    build.build()
+    assert build.installed_torch() == torch.__version__ and not build.is_stale()
+    for name in ("_binding_compile", "_binding_link"):
+        monkeypatch.setattr(b, name, lambda *a: [b.nvcc(), "-o", a[-1]])
+    b.build()
+    assert not b.is_stale()
+    first = os.stat(b.BINDING).st_ino
+    monkeypatch.setattr(b, "installed_torch", lambda: "0.1")
+    assert b.is_stale()
+    b.build()
+    assert not b.is_stale() and os.stat(b.BINDING).st_ino != first
+    monkeypatch.setattr(build, "binding_built_for", lambda: "torch 0.1, other")
+    with pytest.raises(RuntimeError, match="built for torch 0.1"):
+        attn._load_binding()

@@ -102,10 +102,16 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
 lib = _load()
 
 
-def _load_binding(path: str = BINDING_PATH):
+def _load_binding():
+    path = BINDING_PATH
     if not os.path.exists(path):
         raise RuntimeError(
             f"{path} is missing: build it with transformer_attention_fwd_gb300.build.build()")
+    from transformer_attention_fwd_gb300 import build
+    here, there = build.binding_for(torch.__version__), build.binding_built_for()
+    if there != here:
+        raise RuntimeError(f"{path} was built for {there or 'an unknown torch'}, not for {here}: build it "
+                           "again with transformer_attention_fwd_gb300.build.build()")
     loader = importlib.machinery.ExtensionFileLoader("_attn_binding", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_attn_binding", loader, origin=path))
     loader.exec_module(module)

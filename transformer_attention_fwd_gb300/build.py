@@ -3,14 +3,16 @@ the Python binding with g++.
 
 Every translation unit is compiled in parallel, then linked into
 ``transformer_attention_fwd_gb300/_build/libattn.so`` and, against it and the
-installed torch (where there is one), ``_build/_attn_binding.so``.  ptxas
-statistics (registers, spills, shared memory) are written to ``_build/ptxas.log``.
+installed torch (where there is one), ``_build/_attn_binding.so``, which is built
+again for another torch or Python.  ptxas statistics (registers, spills, shared
+memory) are written to ``_build/ptxas.log``.
 """
 from __future__ import annotations
 
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -75,8 +77,34 @@ def _older(target: str) -> bool:
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
+def installed_torch() -> str:
+    """The version in the installed torch's version.py ("" if it says none)."""
+    try:
+        with open(os.path.join(_torch() or "", "version.py")) as f:
+            found = re.search(r"^__version__\s*=\s*['\"]([^'\"]+)", f.read(), re.M)
+    except OSError:
+        return ""
+    return found.group(1) if found else ""
+
+
+def binding_for(torch_version: str) -> str:
+    """What a binding is good for: it holds the layouts of one torch's C++ classes, and of
+    one Python's."""
+    return f"torch {torch_version}, {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_built_for() -> str:
+    """The same of the binding that is there ("" if it does not say)."""
+    try:
+        with open(BINDING + ".for") as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def _binding_stale() -> bool:
-    return _torch() is not None and (_older(BINDING) or not os.path.exists(LIB))
+    return _torch() is not None and (_older(BINDING) or not os.path.exists(LIB) or
+                                     binding_built_for() != binding_for(installed_torch()))
 
 
 def is_stale() -> bool:
@@ -132,7 +160,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if failed:
         raise RuntimeError("g++ failed for binding.cpp")
     if binding:
+        if os.path.exists(BINDING + ".for"):  # until the new one is in place
+            os.remove(BINDING + ".for")
         _link(lambda out: _binding_link(binding_obj, out), BINDING)
+        with open(BINDING + ".for", "w") as f:
+            f.write(binding_for(installed_torch()))
     if verbose:
         print("\n".join(logs))
     return LIB
