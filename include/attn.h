@@ -298,7 +298,8 @@ attn_status attn_fwd_decode_paged(const void* q, const void* kv_cache,
  *
  *     (a, b) -> magnitude * (a cos(t f_i) - b sin(t f_i), b cos(t f_i) + a sin(t f_i))
  *
- * The first rot_dim elements of a head turn, the others pass through.  Pair i
+ * The first rot_dim elements of a head turn, the others pass through (zeros with
+ * their sign; a NaN stays a NaN).  Pair i
  * is (x[i], x[i + rot_dim/2]) (interleaved = 0) or (x[2i], x[2i + 1])
  * (interleaved = 1).  turns[i] is f_i / (2 pi) modulo 1, the fraction of a
  * turn a step of one position makes, in units of 2^-64: t * f_i is then exact
@@ -396,7 +397,7 @@ attn_status attn_qk_norm_rope(const attn_rows* q, const attn_rows* k, const void
  *                attn_fwd_decode_paged.  No block is written twice in a call: the
  *                pages that get new tokens have blocks of their own.
  *   kv_cache:    [num_blocks, 2, Hkv, page_size, D]; other slots stay as they are.
- *   rotation:    NULL: keys (and queries) are copied.
+ *   rotation:    NULL: keys (and queries) are copied, bit for bit.
  *   dtype:       ATTN_BF16 or ATTN_F16, of q, k, v and the cache.
  * Tokens outside every request (cu_seqlens[B] < total) are left out, their rows
  * of y unwritten.  Device-side checks: a request whose offsets decrease or leave

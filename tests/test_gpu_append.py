@@ -347,3 +347,26 @@ def test_graph_replay_and_other_stream(e4m3):
             assert torch.equal(g_scales, e_scales)
             lens += 1
     check_status(a)
+
+
+@pytest.mark.parametrize("D,page,dtype,e4m3", [(128, 16, "bf16", False), (64, 5, "f16", False), (64, 16, "bf16", True),
+                                               (128, 24, "f16", True)])
+def test_without_a_rotation_rows_are_copied_bit_for_bit(D, page, dtype, e4m3):
+    """Every 16-bit pattern, zeros of both signs and NaN of any payload among them."""
+    a = attn()
+    pr = Problem(a, [90, 3], [7, 0], Hq=5, Hkv=3, D=D, page=page, dtype=dtype, rot=0, e4m3=e4m3, seed=71)
+    g = torch.Generator().manual_seed(72)
+    pr.qkv = torch.randint(-2 ** 15, 2 ** 15, pr.qkv.shape, generator=g).to(torch.int16).view(pr.dtype)
+    pr.qkv[::3, ::2] = -0.0
+    for rotate in (False, True):  # no rotation, and one of no elements
+        oq, ok = pr.run(rotate=rotate)
+        check_status(a)
+        assert torch.equal(oq.view(torch.int16), pr.q.view(torch.int16))
+        assert torch.equal(ok.view(torch.int16), pr.k.view(torch.int16))
+        if e4m3:
+            continue
+        cache = pr.dev_cache.cpu().view(torch.int16)
+        for j, b, slot in kv_ref.slots(pr.cu.tolist(), pr.lens):
+            blk, row = int(pr.table[b, slot // page]), slot % page
+            assert torch.equal(cache[blk, 0, :, row], pr.k[j].view(torch.int16))
+            assert torch.equal(cache[blk, 1, :, row], pr.v[j].view(torch.int16))

@@ -253,3 +253,22 @@ def test_the_angle_is_not_rounded_to_a_float(inter):
         angle = torch.tensor([(p % 2 ** 64) / 2.0 ** 64 * 2 * math.pi for p in phases], dtype=torch.float64)
         for got, want in ((y[first], angle.cos()), (y[second], angle.sin())):
             assert ((got - want).abs() <= 2.0 ** -22 * want.abs() + math.pi * 2.0 ** -32 + 2.0 ** -46).all()
+
+
+def _bits(t):
+    return t.view(torch.int32 if t.dtype == torch.float32 else torch.int16)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rot,inter", [(0, False), (2, True), (16, False), (20, False), (36, True), (48, False)])
+def test_what_does_not_turn_keeps_its_bits(dtype, D, rot, inter):
+    """Zeros of both signs, infinities and subnormals beyond rot_dim, compared as integers."""
+    a = attn()
+    x = _randn((33, 6, D), DTYPES[dtype], 22)
+    x[::2, :, 1::3], x[1::2, :, 1::3], x[:, ::2, 2::5], x[..., -1] = -0.0, 0.0, -1e-7, -math.inf
+    x[:, 3] = -0.0
+    r, _ = _rotation(a, rot, inter, magnitude=1.25)
+    y, _ = a.attn_rope(x.cuda(), None, torch.arange(33, dtype=torch.int32).cuda(), r)
+    check_status(a)
+    assert torch.equal(_bits(y.cpu())[..., rot:], _bits(x)[..., rot:])

@@ -157,11 +157,9 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int token, in
             for (int u = 0; u < kAppendUnroll; ++u) {
                 if (u > 0 && h - grp + u * R::kRows >= h1) break;  // the same for the whole warp
                 const bool in = h + u * R::kRows < h1;
-                if constexpr (kKind == 2) {
-                    if (in && cache) {
-                        *reinterpret_cast<uint4*>(cache + c) = raw[u].c0;
-                        *reinterpret_cast<uint4*>(cache + c + to1) = raw[u].c1;
-                    }
+                if (kKind == 2 || half == 0) {  // copied as they are
+                    if (kKind != 2 && in && r.y) R::store(y, y + to1, raw[u]);
+                    if (kKind != 0 && in && cache) R::store(cache + c, cache + c + to1, raw[u]);
                     load(u, h + (kAppendUnroll + u) * R::kRows);
                 } else {
                     typename R::Pairs v = R::unpack(raw[u]);

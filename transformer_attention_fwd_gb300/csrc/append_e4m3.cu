@@ -250,7 +250,8 @@ append_e4m3_kernel(const AppendParams p) {
             if (!is_v && p.k.y != nullptr) {
                 uint8_t* y = static_cast<uint8_t*>(p.k.y) +
                              ((token0 + rr) * p.k.y_token + head * p.k.y_head) * E::kBytes;
-                R::store(y + at0 * E::kBytes, y + at1 * E::kBytes, v);
+                if (cta_turns) R::store(y + at0 * E::kBytes, y + at1 * E::kBytes, v);
+                else R::store(y + at0 * E::kBytes, y + at1 * E::kBytes, r.raw[i]);
             }
             if (write) store_codes<R>(block + static_cast<int64_t>(r0 + rr) * D, at0, at1, v, inv);
         }

@@ -196,6 +196,11 @@ struct Rope {
         *static_cast<uint4*>(second_chunk) = pack(y);
     }
 
+    static __device__ __forceinline__ void store(void* first_chunk, void* second_chunk, const Raw& r) {
+        *static_cast<uint4*>(first_chunk) = r.c0;
+        *static_cast<uint4*>(second_chunk) = r.c1;
+    }
+
     // Which of lane j's pairs turn.
     static __device__ __forceinline__ unsigned turning(int half, int j) {
         unsigned on = 0;
@@ -254,9 +259,11 @@ struct Rope {
             const bool whole = 2 * half == D;
 #pragma unroll
             for (int i = 0; i < kP2; ++i) {
-                // What does not turn takes nothing of its partner (0 * infinity would).
-                const uint64_t pa = whole ? p.a[i] : masked(p.a[i], on >> (2 * i));
-                const uint64_t pb = whole ? p.b[i] : masked(p.b[i], on >> (2 * i));
+                // What does not turn takes nothing of its partner (0 * infinity would): its
+                // coefficients are 1 and -0, and the zeros below are signed so that a is
+                // added -0 and b is subtracted +0, which change no value, not -0 either.
+                const uint64_t pa = whole ? p.a[i] : masked(p.a[i], on >> (2 * i), -0.0f);
+                const uint64_t pb = whole ? p.b[i] : masked(p.b[i], on >> (2 * i), 0.0f);
                 if constexpr (kWeights) {
                     p.a[i] = f2_fma(pb, k.ab[i], f2_mul(p.a[i], k.aa[i]));
                     p.b[i] = f2_fma(pa, k.ba[i], f2_mul(p.b[i], k.bb[i]));
@@ -301,11 +308,11 @@ struct Rope {
     }
 
   private:
-    // The two floats, each 0 unless its bit of `on` is set.
-    static __device__ __forceinline__ uint64_t masked(uint64_t v, unsigned on) {
+    // The two floats, each `none` unless its bit of `on` is set.
+    static __device__ __forceinline__ uint64_t masked(uint64_t v, unsigned on, float none) {
         float lo, hi;
         f2_unpack(v, lo, hi);
-        return f2_pack((on & 1u) ? lo : 0.0f, (on & 2u) ? hi : 0.0f);
+        return f2_pack((on & 1u) ? lo : none, (on & 2u) ? hi : none);
     }
     static __device__ __forceinline__ float turned(const float* row, const float* table, int half, int i) {
         if (i >= 2 * half) return row[i];
