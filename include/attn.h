@@ -400,10 +400,13 @@ attn_status attn_qk_norm_rope(const attn_rows* q, const attn_rows* k, const void
  *   rotation:    NULL: keys (and queries) are copied, bit for bit.
  *   dtype:       ATTN_BF16 or ATTN_F16, of q, k, v and the cache.
  * Tokens outside every request (cu_seqlens[B] < total) are left out, their rows
- * of y unwritten.  Device-side checks: a request whose offsets decrease or leave
- * 0 .. total, or whose length is under its new tokens or over the table's, is
- * left out, and so is a page whose block id is outside the pool; both are
- * reported by attn_get_device_status as ATTN_ERR_BAD_INPUT.  No workspace.
+ * of y unwritten.  Device-side checks, all reported by attn_get_device_status as
+ * ATTN_ERR_BAD_INPUT: a request whose length is under its new tokens or over the
+ * table's is left out, and so is a page whose block id is outside the pool.  A
+ * request between offsets that decrease or leave 0 .. total is left out too; since
+ * tokens find their request by the offsets' order, any other request of that call
+ * may then miss tokens or hold some that are not its own, in its own pages.  No
+ * workspace.
  */
 attn_status attn_append_paged(const attn_rows* q, const attn_rows* k, const attn_rows* v,
                               const int* cu_seqlens, const int* seq_lens,

@@ -370,3 +370,27 @@ def test_without_a_rotation_rows_are_copied_bit_for_bit(D, page, dtype, e4m3):
             blk, row = int(pr.table[b, slot // page]), slot % page
             assert torch.equal(cache[blk, 0, :, row], pr.k[j].view(torch.int16))
             assert torch.equal(cache[blk, 1, :, row], pr.v[j].view(torch.int16))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("bad", [[0, 20, 1000, 29, 35], [0, 20, 5, 29, 35], [0, 20, -7, 29, 35], [35, 29, 20, 5, 0],
+                                 [0, 2 ** 31 - 1, -2 ** 31, 29, 35]])
+def test_offsets_out_of_order_are_reported_and_stay_in_their_pages(bad, e4m3):
+    """Any request of the call may miss tokens; blocks of no request, and every slot before a
+    token that a valid request could have, stay as they were, and the next call is whole."""
+    a = attn()
+    pr = Problem(a, new=[20, 3, 6, 6], past=[16, 48, 160, 160], e4m3=e4m3, seed=73)
+    oq, ok = pr.run(cu=torch.tensor(bad, dtype=torch.int32))
+    assert a.device_status() == a.ATTN_ERR_BAD_INPUT
+    kept = torch.ones(pr.cache.shape[0], dtype=torch.bool)
+    for b, n in enumerate(pr.lens.tolist()):
+        if 0 <= bad[b] <= bad[b + 1] <= pr.total and bad[b + 1] - bad[b] <= n:
+            first = (n - (bad[b + 1] - bad[b])) // pr.page
+            kept[pr.table[b, first:-(-n // pr.page)].long()] = False
+    now, before = pr.dev_cache.cpu().view(torch.uint8), pr.cache.view(torch.uint8)
+    assert torch.equal(now[kept], before[kept]) and int(kept.sum()) > 3
+    if e4m3:
+        assert torch.equal(pr.dev_scales.cpu()[kept], pr.scales[kept])
+    oq, ok = pr.run()
+    check_status(a)
+    pr.check(oq, ok)

@@ -79,7 +79,7 @@ __device__ __forceinline__ void append_report(const AppendParams& p, unsigned bl
 }
 
 // The request and slot of a new token (by the whole warp); false if no valid
-// request has it.
+// request has it.  (Offsets out of order may hide a valid one; that is reported.)
 __device__ __forceinline__ bool append_slot(const AppendParams& p, int token, int lane, int* b,
                                             int* slot) {
     *b = warp_last_at_most(p.B, token, lane, [&](int i) { return static_cast<long long>(p.cu[i]); });
