@@ -272,3 +272,19 @@ def test_library_errors_come_as_the_bindings(a):
         a._native.rope(1)
     with pytest.raises(ValueError, match="q must be a tensor"):
         a.attn_rope([1.0], None, torch.zeros(1, dtype=torch.int32), None)
+
+
+@pytest.mark.parametrize("rot", [2, 64, 128])
+@pytest.mark.parametrize("base", [10000, 500000, 10 ** 15, 10 ** 19])
+def test_tables_against_forty_digits(a, rot, base):
+    """Within 2^-53 turns of base^(-2i/rot) / 2 pi: a double's pow (its exponent's rounding times
+    ln base, at most 0.37 * 2^-53 of 1; an ulp, 2^-52), 2 pi and the division, 2^-52 * 1.93 / 2 pi;
+    and where an entry is so small that this is less, within half a unit of 2^-64 of it."""
+    import decimal
+    with decimal.localcontext() as ctx:
+        ctx.prec = 40
+        two_pi = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510")
+        for i, got in enumerate(a.rope_turns(rot, base=float(base))[0].tolist()):
+            want = decimal.Decimal(base) ** (decimal.Decimal(-2 * i) / rot) / two_pi * 2 ** 64
+            double = min(decimal.Decimal(2) ** 11, want * decimal.Decimal(2) ** -46)
+            assert abs(got % 2 ** 64 - want) <= decimal.Decimal("0.5") + double, (i, got, want)

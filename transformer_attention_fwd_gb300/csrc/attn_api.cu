@@ -1214,7 +1214,7 @@ attn_status attn_rope_turns(unsigned long long* turns, float* magnitude, int rot
         keep = std::min(1.0, std::max(0.0, keep));
         const double g = (scaling == ATTN_ROPE_PLAIN || scaling == ATTN_ROPE_BASE) ? f : keep * f + (1.0 - keep) * f / factor;
         const double turn = std::fmod(g / kTwoPi, 1.0);  // < 1, so the product below fits
-        turns[i] = static_cast<unsigned long long>(std::ldexp(turn, 64));
+        turns[i] = static_cast<unsigned long long>(std::nearbyint(std::ldexp(turn, 64)));
     }
     *magnitude = scaling == ATTN_ROPE_YARN && factor > 1.0 ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
     return ok();

@@ -6,8 +6,9 @@
 // frequency f:  (a cos - b sin, b cos + a sin), times the rotation's
 // magnitude.  f arrives as a fraction of a turn per position in units of
 // 2^-64 turn, so t * f modulo one turn is the low 64 bits of one integer
-// product: exact, whatever the position.  The angle's error is the table's
-// rounding, |t| * 2^-65 turns, and the 2^-33 turns of its top 32 bits.
+// product: exact, whatever the position.  The angle's error is |t| times the
+// table's (2^-65 turns where it was rounded to nearest once; attn_rope_turns
+// computes in double, 2^-53 turns) and the 2^-33 turns of its top 32 bits.
 //
 // A lane holds two 16-byte chunks of a row, chosen so that both elements of
 // each of its pairs are its own: chunks j and j + half for the halves layout,
