@@ -112,3 +112,17 @@ def test_weights_far_apart_in_one_tile(Hq, Hkv, D, page):
     pr[0][:, ::3, 0, :2] = 0.5
     pr[2][:, 1] = torch.exp2(-torch.randint(0, 13, pr[2][:, 1].shape, generator=g).float())
     _check(a, _codes(pr), 1.0, 2.0 ** -14, n, "levels")
+
+
+@pytest.mark.parametrize("exponent", [-118, -100, 100, 118])
+def test_values_at_the_ends_of_the_scales(exponent):
+    """V scales at which the factor from the weighted sum to the result is hardly a normal float."""
+    a = attn()
+    for Hq, D, n in ((8, 128, 500), (16, 64, 77), (3, 128, 3000)):
+        pr = _empty(n, Hq, 1, D, 16, torch.bfloat16)
+        g = torch.Generator().manual_seed(81)
+        q, codes, scales, table, lens = _codes(pr)
+        q.copy_(torch.randn(q.shape, generator=g))
+        codes = kv_ref.random_codes(codes.shape, g)
+        scales[:, 0], scales[:, 1] = 2.0 ** -7, 2.0 ** exponent
+        _check(a, (q, codes, scales, table, lens), 1.0 / math.sqrt(D), 2.0 ** -14, n, f"2^{exponent}")

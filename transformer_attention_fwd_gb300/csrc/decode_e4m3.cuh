@@ -216,8 +216,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
-// Factor from sum w v to O: 2^(mv - m) / l.
-__device__ __forceinline__ float out_factor(float m, float l, float mv) { return ex2_approx(mv - m) / l; }
+// Factor from sum w v to O, 2^(mv - m) / l, but for the 2^-kLift that the sum is multiplied
+// by first (out_of): V's scales reach down to where the whole factor would be no normal number.
+__device__ __forceinline__ float out_factor(float m, float l, float mv) { return ex2_approx(mv - m + kLift) / l; }
+__device__ __forceinline__ float out_of(float sum, float factor) { return sum * 0x1p-9f * factor; }
+static_assert(kLift == 9.0f, "out_of");
 
 // Folds {m, sum, mv} of a piece into e.
 __device__ __forceinline__ void fold(float4& e, const float4& x) {
@@ -266,8 +269,9 @@ struct Columns {
     __device__ __forceinline__ void store16(uint16_t* row, int lane, float f) const {
         using E = Elem16<kF16>;
         if constexpr (D == 128)
-            reinterpret_cast<uint2*>(row)[lane] = make_uint2(E::pack(c[0] * f, c[1] * f), E::pack(c[2] * f, c[3] * f));
-        else reinterpret_cast<uint32_t*>(row)[lane] = E::pack(c[0] * f, c[1] * f);
+            reinterpret_cast<uint2*>(row)[lane] =
+                make_uint2(E::pack(out_of(c[0], f), out_of(c[1], f)), E::pack(out_of(c[2], f), out_of(c[3], f)));
+        else reinterpret_cast<uint32_t*>(row)[lane] = E::pack(out_of(c[0], f), out_of(c[1], f));
     }
 };
 
@@ -601,8 +605,8 @@ __device__ __forceinline__ void unit_out(const UnitState<D, HC>& s, const E4m3Pa
             float c[D / 8];
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
-                c[2 * j] = s.o[r][j][i] * f;
-                c[2 * j + 1] = s.o[r][j][i + 2] * f;
+                c[2 * j] = out_of(s.o[r][j][i], f);
+                c[2 * j + 1] = out_of(s.o[r][j][i + 2], f);
             }
             if (h < heads) store_row<kF16>(p.o + (row0 + h) * D + g * (D / 8), c);
             if (p.lse && g == 0 && h < heads) p.lse[row0 + h] = (s.m[r][i] + __log2f(l)) * kLn2;
