@@ -347,8 +347,9 @@ attn_status attn_rope_turns(unsigned long long* turns, float* magnitude, int rot
  * likewise (strides in elements, >= 0; heads up to 2^20): any slice of a fused projection, in
  * any order of its dimensions.  x and y are 16-byte aligned and every stride is
  * a multiple of 16 bytes.  y == x with equal strides works in place; otherwise
- * the two may not share memory, and no two rows of y may.  Nothing else that a
- * call reads or writes may overlap y.
+ * what lies between the first and the last row of x and of y may not meet (so two
+ * slices of one tensor, their rows in turn, are refused), and no two rows of y may.
+ * Nothing else that a call reads or writes may overlap y.
  */
 typedef struct {
     const void* x;

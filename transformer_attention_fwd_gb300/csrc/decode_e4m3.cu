@@ -21,9 +21,10 @@
 // with a product each: one alone, 11 bits, made results that are small differences of
 // large sums wrong by their own size.  A tile with keys 2^20 or more under the reference
 // takes its weights in groups, each relative to its largest, so what light keys add up
-// to behind a heavy one with no value is there too.  (The second term costs 0.5 us at
-// 64 x 4096 keys with up to 8 heads per KV head, 15 % with 16, which instruction issue
-// bounds.)  The result is (sum w_j v_j) / (sum p_j) * 2^(mv - m).  A reference moves
+// to behind a heavy one with no value is there too.  (The second term costs 1 % at
+// 64 x 4096 keys with up to 8 heads per KV head of 128, 8 % of 64, and 15 % with 16
+// heads; products in another order, both checks in one vote and the second term made
+// behind the first one's products change nothing.)  The result is (sum w_j v_j) / (sum p_j) * 2^(mv - m).  A reference moves
 // only when a key exceeds it by 2^kSlack.
 //
 // Work: all 16-key tiles of all (request, KV head, head chunk) units are laid
@@ -34,18 +35,20 @@
 // its end, and those that a CTA boundary cuts by the combine kernel.  Two to four
 // small CTAs share an SM, as registers allow, so that one's start and end pass
 // under the others' streaming (three instead of two, with rings of three tiles
-// instead of four: 92.0 -> 88.6 us below; 44.7 -> 43.6).  More of them than fit at
-// once, to even out the SMs, lost 5 us for each further wave: a start costs that
-// much.
+// instead of four, took 3.4 us off below, and 1.1 off the ragged one).  More of them
+// than fit at once, to even out the SMs, lost 5 us for each further wave: a start
+// costs that much.
 //
-// 64 requests of 4096 keys, Hq 32, Hkv 8, D 128, 16-token blocks (539 MB): 88.6 us,
-// 6.1 TB/s.  Every CTA sums the lengths and finds its place in 2.8 us, the first
+// 64 requests of 4096 keys, Hq 32, Hkv 8, D 128, 16-token blocks (539 MB): 89.6 us,
+// 6.0 TB/s.  Every CTA sums the lengths and finds its place in 2.8 us, the first
 // tiles are there after 5.6, the SMs run dry between 75 and 81 us (together they
-// stream at 7.2 TB/s), merging takes 1 to 2 us and the combine kernel 3.  With 8
-// query heads per KV head and ragged lengths (231 MB) 43.6 us, by the same fixed
-// costs (short contexts, for which they are all of the time, are in
-// decode_e4m3_short.cu); at D = 64 94 us for 540 MB.  With 16 heads per KV head
-// instruction issue bounds it: 103 us (D = 128), 121 us (D = 64).
+// stream at 7.2 TB/s; these before the weights' second terms, at 88.6 us), merging
+// takes 1 to 2 us and the combine kernel 3.  With 8 query heads per KV head and ragged
+// lengths (231 MB) 44.6 us, by the same fixed costs (short contexts, for which they
+// are all of the time, are in decode_e4m3_short.cu); at D = 64 101 us for 540 MB.
+// With 16 heads per KV head 118 us (D = 128) and 139 us (D = 64): two and three warps
+// to a scheduler, each waiting out the latencies of its own instructions (issue active
+// 43 and 58 %, tensor pipe 38 and 32 %).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -9,7 +9,7 @@
 // barrier, after which each CTA adds up some heads out of the others' shared
 // memory.  Latency bounds it: length, block ids, tiles, two merges.
 //
-// 3 requests of up to 1476 keys (12 heads, D 64): 5.2 us against 8.9 for the
+// 3 requests of up to 1476 keys (12 heads, D 64): 5.4 us against 8.9 for the
 // two launches of decode_e4m3.cu, and 5 us of host time against 9.
 #include <cuda_runtime.h>
 
@@ -29,14 +29,14 @@ constexpr int kMaxRanks = 8;  // CTAs of a cluster
 // When a cluster takes each unit, with both kernels' times at head dim 128, Hkv 8,
 // Hq 32, page 16:
 //  - a warp has at most 16 tiles by the table's width (one request of 1024, 4096
-//    and 8192 keys: 5.1, 7.9 and 12.0 us against 9.1, 11.3 and 12.6; of 32768, 64
-//    tiles a warp: 35.7 against 19.2);
-//  - the units fill the GPU at most twice (64 and 96 requests of 200 keys: 9.5 and
-//    11.7 us against 14.1 and 16.5; 256 requests of one key, 4.5 times: 13.6
-//    against 8.8, and 1024 of 200 keys, 18 times: 100 against 79).
+//    and 8192 keys: 6.4, 8.9 and 13.5 us against 9.1, 11.9 and 13.8; of 32768, 64
+//    tiles a warp: 41.1 against 19.8);
+//  - the units fill the GPU at most twice (64 and 96 requests of 200 keys: 10.1 and
+//    12.6 us against 14.6 and 16.6; 256 requests of one key, 4.5 times: 15.3
+//    against 9.8, and 1024 of 200 keys, 18 times: 109 against 77).
 constexpr int kMaxTiles = 16, kMaxFills = 2;
-// A rank more only for over 16 tiles of the unit (8 requests of 200 keys: 4.5, 5.0
-// and 9.5 us with 1, 2 and 8 CTAs; of 1024: 10.6, 8.1 and 7.9 with 1, 2 and 4).
+// A rank more only for over 16 tiles of the unit (8 requests of 200 keys: 4.8, 5.2
+// and 6.0 us with 1, 2 and 8 CTAs; of 1024: 12.0, 8.9 and 8.5 with 1, 2 and 4).
 constexpr int kRankTiles = 16;
 
 template <int D, int HC>

@@ -15,7 +15,8 @@
 // fp32 without it (4099 tokens, 168 MB) 27 us; [8, 12 + 12, 1024, 64] fp16 (50 MB)
 // 9.1 us, the launch and the last blocks' tail being 1.5 of them.  A token's sines
 // once for each lane and tensor instead of once for each token, and partners
-// fetched by shuffles, took 62, 35 and 15 us.  One token: 1.8 us, a launch.
+// fetched by shuffles, took 62, 35 and 15 us.  One token: 1.9 us, a launch.
+// (At 96 registers the norm's instances for any half spill 8 to 16 bytes.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
