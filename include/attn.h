@@ -330,9 +330,9 @@ typedef enum {
 
 /*
  * attn_rope_turns -- fills turns[rot_dim / 2] (HOST memory) and *magnitude for
- * an attn_rotation, in double precision: an entry is within 2^-53 turns (those of
- * mixed frequencies and of factors under 1, 2^-46 of itself), and rounded to the
- * nearest 2^-64.  Position t multiplies that: the fastest pairs' angles are within
+ * an attn_rotation, in double precision: an entry is within 2^-53 turns (of mixed
+ * frequencies 2^-46 of itself, and a factor under 1 divides either), and rounded to
+ * the nearest 2^-64.  Position t multiplies that: the fastest pairs' angles are within
  * 2^-30 turns up to t = 2^23, and within 2^-22 everywhere.  rot_dim even and >= 2,
  * base > 1, factor > 0; original_length, low, high (0 < low < high) are read by the last
  * two scalings only; ATTN_ROPE_BASE needs rot_dim > 2.  Needs no GPU.

@@ -99,3 +99,20 @@ def test_a_binding_of_another_torch_is_stale_and_refused(b, monkeypatch):
     monkeypatch.setattr(build, "binding_built_for", lambda: "torch 0.1, other")
     with pytest.raises(RuntimeError, match="built for torch 0.1"):
         attn._load_binding()
+
+
+def test_a_rebuild_never_leaves_the_binding_without_its_mark(b, monkeypatch):
+    """Another process may load the binding while this one builds it again."""
+    for name in ("_binding_compile", "_binding_link"):
+        monkeypatch.setattr(b, name, lambda *a: [b.nvcc(), "-o", a[-1]])
+    b.build()
+    seen, link = [], b._link
+
+    def watched(cmd, target):
+        seen.append(b.binding_built_for())
+        link(cmd, target)
+        seen.append(b.binding_built_for())
+
+    monkeypatch.setattr(b, "_link", watched)
+    b.build(force=True)
+    assert len(seen) == 4 and set(seen) == {b.binding_for(b.installed_torch())}

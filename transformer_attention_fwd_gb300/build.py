@@ -160,11 +160,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if failed:
         raise RuntimeError("g++ failed for binding.cpp")
     if binding:
-        if os.path.exists(BINDING + ".for"):  # until the new one is in place
-            os.remove(BINDING + ".for")
         _link(lambda out: _binding_link(binding_obj, out), BINDING)
-        with open(BINDING + ".for", "w") as f:
+        # In place at once, and after the binding: other processes may load it meanwhile.
+        tmp = BINDING + f".for.tmp{os.getpid()}"
+        with open(tmp, "w") as f:
             f.write(binding_for(installed_torch()))
+        os.replace(tmp, BINDING + ".for")
     if verbose:
         print("\n".join(logs))
     return LIB
