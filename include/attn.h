@@ -474,6 +474,126 @@ attn_status attn_fwd_decode_paged_e4m3(const void* q, const void* kv_cache, cons
                                        attn_dtype dtype, cudaStream_t stream);
 
 /*
+ * attn_append_paged_e2m1 -- attn_append_paged into a 4-bit cache.  An element is
+ * code * scale * factor:
+ *   kv_cache: [num_blocks, 2, Hkv, page_size, D / 2] bytes of two e2m1 codes (sign, 2
+ *             exponent and 1 mantissa bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6), the even
+ *             element in the low half;
+ *   scales:   [num_blocks, 2, Hkv, page_size, D / 16] e4m3, one for each 16 elements
+ *             of a row, 16-byte aligned;
+ *   factors:  [2, Hkv] float32, of every head of K and of V, between 2^-100 and 2^100
+ *             (not checked), or NULL: all 1.  They keep the scales, which e4m3 holds
+ *             with full precision from 2^-6 to 448, in range: amax / (6 * factor).
+ * A group of 16 elements x (of keys after their rotation, in fp32) gets
+ *   scale = e4m3(max|x| / (6 * factor)) over its finite elements, to nearest (ties to
+ *           even), then at least 2^-9 and at most 448,
+ *   code  = e2m1(x * r), to nearest (ties to even), beyond 6 to +-6, with
+ *           r = 1 / (scale * factor);
+ * each operation rounded to fp32.  Infinities become +-6; a NaN makes its group's scale
+ * NaN, so that all 16 read as NaN (their codes are undefined).  Rows depend on nothing
+ * else in their block.  A power-of-two factor changes no code.
+ */
+attn_status attn_append_paged_e2m1(const attn_rows* q, const attn_rows* k, const attn_rows* v,
+                                   const int* cu_seqlens, const int* seq_lens,
+                                   const int* positions, const int* block_table,
+                                   void* kv_cache, void* scales, const float* factors, int B,
+                                   int total, int D, int page_size, int max_pages_per_seq,
+                                   int num_blocks, const attn_rotation* rotation,
+                                   attn_dtype dtype, cudaStream_t stream);
+
+/*
+ * attn_fwd_decode_paged_e2m1 -- attn_fwd_decode_paged over the 4-bit cache of
+ * attn_append_paged_e2m1 (any e4m3 scales, any finite factors; factors may be NULL).
+ * q and o are [B, Hq, 1, D] in dtype, lse [B, Hq] float32 or NULL.  The products run
+ * on the tensor cores in fp16 with fp32 sums: codes times scales are exact in fp16;
+ * queries and weights are held as attn_fwd_decode_paged_e4m3 holds them.
+ *   weights: [num_blocks, Hkv, page_size] float32, or NULL.  Otherwise every key's
+ *            attention weight is added to its place, summed over the query heads of the
+ *            KV head:  weights[block, hkv, row] += sum_h exp(x_h - lse_h), x_h the scaled
+ *            score and lse_h the result's log-sum-exp.  Places of other slots stay as
+ *            they are.  A block that two requests of the call share gets undefined
+ *            weights.  The scores pass through a workspace of
+ *            4 * B * Hq * max_pages_per_seq * page_size bytes.
+ * The other arguments, checks, errors and the workspace are those of
+ * attn_fwd_decode_paged_e4m3.
+ */
+attn_status attn_fwd_decode_paged_e2m1(const void* q, const void* kv_cache, const void* scales,
+                                       const float* factors, const int* block_table,
+                                       const int* seq_lens, void* o, float* lse, float* weights,
+                                       int B, int Hq, int Hkv, int D, int page_size,
+                                       int max_pages_per_seq, int num_blocks, float scale,
+                                       attn_dtype dtype, cudaStream_t stream);
+
+/*
+ * attn_weights_paged -- the attention weights of packed queries, added up over the keys
+ * of the paged cache of attn_fwd_decode_paged: what an eviction goes by.
+ *
+ *     weights[key j] += sum over i, h of exp(scale * q_ih . k_j - lse_ih)
+ *
+ * over the request's queries i that see key j and the query heads h of the KV head.
+ *   q:          rows of `total` packed queries, Hq = q->heads (a multiple of Hkv); q->y
+ *               must be NULL.  Request b's are cu_seqlens[b] .. cu_seqlens[b+1]-1: its
+ *               last tokens, n of them, query i of which sees keys 0 .. seq_lens[b]-n+i.
+ *               One query a request is a decode step.
+ *   lse:        float32, the log-sum-exp of every query row, at lse + h * lse_head +
+ *               token * lse_token (strides in elements, >= 0): what the attention over
+ *               these keys returned (attn_fwd_varlen: [Hq, total]).  A row whose lse is
+ *               -inf adds nothing.
+ *   seq_lens:   [B] int32, the keys of each request, its queries' own among them.
+ *   weights:    [num_blocks, Hkv, page_size] float32; places of other slots stay as
+ *               they are.  The blocks of the requests that have queries are theirs alone.
+ *   scale:      finite, > 0.
+ * dtype (ATTN_BF16 or ATTN_F16) is q's and the cache's type.  The sums are fp32 in a
+ * fixed order.  Device-side checks, reported as ATTN_ERR_BAD_INPUT: a request whose
+ * offsets or length are out of range is left out, and so is a slot whose block id is.
+ * No workspace.  B and Hkv up to 65535 (ATTN_ERR_UNSUPPORTED beyond).
+ */
+attn_status attn_weights_paged(const attn_rows* q, const float* lse, long long lse_head,
+                               long long lse_token, const void* kv_cache, const int* block_table,
+                               const int* cu_seqlens, const int* seq_lens, float* weights, int B,
+                               int total, int Hkv, int D, int page_size, int max_pages_per_seq,
+                               int num_blocks, float scale, attn_dtype dtype,
+                               cudaStream_t stream);
+
+/* The same over the 4-bit cache of attn_append_paged_e2m1; dtype is q's. */
+attn_status attn_weights_paged_e2m1(const attn_rows* q, const float* lse, long long lse_head,
+                                    long long lse_token, const void* kv_cache, const void* scales,
+                                    const float* factors, const int* block_table,
+                                    const int* cu_seqlens, const int* seq_lens, float* weights,
+                                    int B, int total, int Hkv, int D, int page_size,
+                                    int max_pages_per_seq, int num_blocks, float scale,
+                                    attn_dtype dtype, cudaStream_t stream);
+
+/*
+ * attn_evict_paged -- cuts every request with more than `keep` keys back to `keep`, for
+ * each KV head by itself: its last `recent` slots (0 .. keep) stay, and of the others
+ * the keep - recent with the largest weights; of equal ones the lower slots, and a NaN
+ * counts as the least.  The kept rows of K and V move to slots 0 .. keep-1 in their
+ * order and their weights with them; the weights of slots keep and up become 0, their
+ * rows stay as they are (a shorter table may follow: the pages past slot keep-1 are
+ * free).  Keys keep the rotation they have, so tokens appended later need positions.
+ *   weights:  [num_blocks, Hkv, page_size] float32 (attn_weights_paged).
+ *   new_lens: [B] int32: min(seq_lens[b], keep).  May not be seq_lens.
+ *   kept:     [B, Hkv, keep] int32 or NULL: the slot each kept row had before, -1
+ *             past the request's new length.
+ * A block belongs to one request of the call.  dtype: ATTN_BF16 or ATTN_F16.  Device-side
+ * checks as for attn_weights_paged; a row whose old or new block id is out of range does
+ * not move.  Without `kept` it is a workspace.  (No such call over the 8-bit cache:
+ * rows of its blocks share a scale, and moving one would round it again.)
+ */
+attn_status attn_evict_paged(void* kv_cache, float* weights, const int* block_table,
+                             const int* seq_lens, int* new_lens, int* kept, int B, int Hkv,
+                             int D, int page_size, int max_pages_per_seq, int num_blocks,
+                             int keep, int recent, attn_dtype dtype, cudaStream_t stream);
+
+/* The same over the 4-bit cache of attn_append_paged_e2m1: codes and scales move. */
+attn_status attn_evict_paged_e2m1(void* kv_cache, void* scales, float* weights,
+                                  const int* block_table, const int* seq_lens, int* new_lens,
+                                  int* kept, int B, int Hkv, int D, int page_size,
+                                  int max_pages_per_seq, int num_blocks, int keep, int recent,
+                                  cudaStream_t stream);
+
+/*
  * attn_get_device_status -- synchronise `stream`, then read and clear the
  * device status word of the current device.  Returns ATTN_ERR_TIMEOUT when a
  * kernel gave up on a pipeline wait since the last call (its outputs are

@@ -84,6 +84,12 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "attn_append_paged": [R, R, R, P, P, P, P, P, I, I, I, I, I, I, N, I, P],
         "attn_append_paged_e4m3": [R, R, R, P, P, P, P, P, P, I, I, I, I, I, I, N, I, P],
         "attn_fwd_decode_paged_e4m3": [P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P],
+        "attn_append_paged_e2m1": [R, R, R, P, P, P, P, P, P, P, I, I, I, I, I, I, N, I, P],
+        "attn_fwd_decode_paged_e2m1": [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P],
+        "attn_weights_paged": [R, P, LL, LL, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P],
+        "attn_weights_paged_e2m1": [R, P, LL, LL, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P],
+        "attn_evict_paged": [P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P],
+        "attn_evict_paged_e2m1": [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P],
         "attn_get_device_status": [P],
         "attn_diag_mma_tile": [P, P, P, P, P, I, P],
         "attn_diag_wait_timeout": [LL, P],
@@ -489,7 +495,7 @@ def attn_append_paged(k, v, kv_cache, block_table, cu_seqlens, seq_lens, rotatio
     """
     return _native.append(k, v, kv_cache, None, block_table, cu_seqlens, seq_lens,
                           None if rotation is None else rotation._held, positions, q, out_q, out_k,
-                          None if stream is None else stream.cuda_stream)
+                          None if stream is None else stream.cuda_stream, None, False)
 
 
 def attn_append_paged_e4m3(k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens,
@@ -502,7 +508,7 @@ def attn_append_paged_e4m3(k, v, kv_cache, scales, block_table, cu_seqlens, seq_
         raise ValueError("scales must be a tensor")
     return _native.append(k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens,
                           None if rotation is None else rotation._held, positions, q, out_q, out_k,
-                          None if stream is None else stream.cuda_stream)
+                          None if stream is None else stream.cuda_stream, None, False)
 
 
 def attn_fwd_decode_paged_e4m3(q, kv_cache, scales, block_table, seq_lens, scale: float | None = None,
@@ -514,8 +520,86 @@ def attn_fwd_decode_paged_e4m3(q, kv_cache, scales, block_table, seq_lens, scale
     max_pages] and seq_lens: [B] int32; all contiguous CUDA tensors.  Returns
     ``(o [B, Hq, 1, D], lse [B, Hq] or None)``.
     """
-    return _native.decode_e4m3(q, kv_cache, scales, block_table, seq_lens, scale, out, lse, want_lse,
+    return _native.decode(q, kv_cache, scales, block_table, seq_lens, scale, out, lse, want_lse,
+                          None if stream is None else stream.cuda_stream, None, None, False)
+
+
+def attn_append_paged_e2m1(k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens,
+                           rotation: Rotation | None = None, positions=None, q=None, out_q=None, out_k=None,
+                           factors=None, stream=None):
+    """``attn_append_paged`` into a 4-bit cache (``attn_append_paged_e2m1``):
+    kv_cache uint8 [num_blocks, 2, Hkv, page_size, D/2], two e2m1 codes to a byte;
+    scales float8_e4m3fn [num_blocks, 2, Hkv, page_size, D/16]; factors float32
+    [2, Hkv], or None for ones.  An element is code * scale * factor.
+    """
+    if scales is None:
+        raise ValueError("scales must be a tensor")
+    return _native.append(k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens,
+                          None if rotation is None else rotation._held, positions, q, out_q, out_k,
+                          None if stream is None else stream.cuda_stream, factors, True)
+
+
+def attn_fwd_decode_paged_e2m1(q, kv_cache, scales, block_table, seq_lens, scale: float | None = None,
+                               factors=None, weights=None, out=None, lse=None, want_lse: bool = True,
+                               stream=None):
+    """Decode against the paged 4-bit cache of ``attn_append_paged_e2m1``
+    (``attn_fwd_decode_paged_e2m1``): q [B, Hq, 1, D] bf16 or fp16, block_table
+    [B, max_pages] and seq_lens [B] int32, all contiguous CUDA tensors.  With
+    ``weights`` (float32 [num_blocks, Hkv, page_size]) every key's attention weight,
+    summed over its KV head's query heads, is added to its place there.  Returns
+    ``(o [B, Hq, 1, D], lse [B, Hq] or None)``.
+    """
+    return _native.decode(q, kv_cache, scales, block_table, seq_lens, scale, out, lse, want_lse,
+                          None if stream is None else stream.cuda_stream, factors, weights, True)
+
+
+def attn_weights_paged(q, lse, kv_cache, block_table, cu_seqlens, seq_lens, weights,
+                       scale: float | None = None, stream=None):
+    """Adds to ``weights`` (float32 [num_blocks, Hkv, page_size]) what attention weight
+    the queries give every key of the paged cache (``attn_weights_paged``).
+
+    q: [total, Hq, D] packed queries (bf16 or fp16, any strides whose rows are
+    contiguous and 16-byte aligned), request b's at cu_seqlens[b] ..
+    cu_seqlens[b+1]-1: the last tokens of its seq_lens[b], each of which sees the keys
+    up to its own; lse: [Hq, total] float32 of any strides, as ``attn_fwd_varlen``
+    returns it (after a decode step: q[:, :, 0], lse.t() and one query a request).
+    Returns ``weights``.
+    """
+    return _native.add_weights(q, lse, kv_cache, None, block_table, cu_seqlens, seq_lens, weights, scale, None,
                                None if stream is None else stream.cuda_stream)
+
+
+def attn_weights_paged_e2m1(q, lse, kv_cache, scales, block_table, cu_seqlens, seq_lens, weights,
+                            scale: float | None = None, factors=None, stream=None):
+    """``attn_weights_paged`` over the 4-bit cache of ``attn_append_paged_e2m1``
+    (``attn_weights_paged_e2m1``)."""
+    if scales is None:
+        raise ValueError("scales must be a tensor")
+    return _native.add_weights(q, lse, kv_cache, scales, block_table, cu_seqlens, seq_lens, weights, scale, factors,
+                               None if stream is None else stream.cuda_stream)
+
+
+def attn_evict_paged(kv_cache, weights, block_table, seq_lens, keep: int, recent: int, new_lens=None, kept=None,
+                     want_kept: bool = True, stream=None):
+    """Cuts every request longer than ``keep`` back to ``keep`` keys, for each KV head its
+    last ``recent`` and the heaviest of the others by ``weights`` (float32 [num_blocks,
+    Hkv, page_size]); rows and weights move to the first slots in place
+    (``attn_evict_paged``).  Returns ``(new_lens [B], kept [B, Hkv, keep] or None)``:
+    the new lengths, and the slot each kept key had before (-1 past the length), both
+    int32.  Keys keep their rotation: appending later tokens takes ``positions``.
+    """
+    return _native.evict(kv_cache, None, weights, block_table, seq_lens, keep, recent, new_lens, kept, want_kept,
+                         None if stream is None else stream.cuda_stream)
+
+
+def attn_evict_paged_e2m1(kv_cache, scales, weights, block_table, seq_lens, keep: int, recent: int, new_lens=None,
+                          kept=None, want_kept: bool = True, stream=None):
+    """``attn_evict_paged`` over the 4-bit cache of ``attn_append_paged_e2m1``
+    (``attn_evict_paged_e2m1``)."""
+    if scales is None:
+        raise ValueError("scales must be a tensor")
+    return _native.evict(kv_cache, scales, weights, block_table, seq_lens, keep, recent, new_lens, kept, want_kept,
+                         None if stream is None else stream.cuda_stream)
 
 
 def device_status(stream=None) -> int:

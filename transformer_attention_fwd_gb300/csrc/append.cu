@@ -68,6 +68,8 @@ AppendParams append_params(const AppendShape& s, const RopeShape& r, const RopeR
     p.block_table = s.block_table;
     p.cache = static_cast<uint8_t*>(s.cache);
     p.scales = s.scales;
+    p.row_scales = s.row_scales;
+    p.factors = s.factors;
     p.status = env.status;
     p.table = RopeTable{r.turns, r.rot_dim / 2, r.magnitude};
     p.page = PageDivider(s.page);

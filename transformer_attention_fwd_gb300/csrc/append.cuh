@@ -27,6 +27,8 @@ struct AppendParams {
     const int* block_table;
     uint8_t* cache;
     float* scales;  // 8-bit cache only
+    uint8_t* row_scales;   // 4-bit cache only, and
+    const float* factors;  // [2, heads] or null
     unsigned* status;
     RopeTable table;
     PageDivider page;
@@ -96,11 +98,17 @@ __device__ __forceinline__ int append_block(const AppendParams& p, int b, int pa
     return -1;
 }
 
+// Where append_rows() puts a token's K and V rows: into the 16-bit cache, as its own rows are
+// stored.  (append_e2m1.cu has the 4-bit cache, whose rows take more.)
+struct PlainRows {
+    static constexpr bool kPlain = true;
+};
+
 // Segment `seg` of a token's steps, by one warp: its query heads into q.y, its key
 // heads into the cache and k.y, its values into the cache.  With kv_steps = 0 the
 // query heads alone.  table: D floats of shared memory, scratch:
 // Rope<...>::kScratch.
-template <typename E, int D, int kLayout>
+template <typename E, int D, int kLayout, class Sink = PlainRows>
 __device__ __forceinline__ void append_rows(const AppendParams& p, int token, int seg, float* table, float* scratch) {
     using R = Rope<E, D, kLayout>;
     if (token >= p.total) return;
@@ -116,6 +124,8 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int token, in
     typename R::Coef coef;
     uint8_t* cache = nullptr;  // the slot's K row of head 0; null: the page is left out
     const long long head_bytes = static_cast<long long>(p.page.size) * D * E::kBytes;
+    Sink sink{};
+    if constexpr (!Sink::kPlain) sink.begin(j, half);
     bool found = false, mine = true;
     // The token's request, coefficients and place in the cache, behind the first
     // loads; false if no request has it.
@@ -131,7 +141,8 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int token, in
         if (s1 > p.q_steps) {
             int in_page;
             const int id = append_block(p, b, p.page.split(slot, &in_page));
-            if (id >= 0)
+            if constexpr (!Sink::kPlain) sink.place(p, id, in_page);
+            else if (id >= 0)
                 cache = p.cache + (static_cast<int64_t>(id) * 2 * p.k.heads * p.page.size + in_page) * D * E::kBytes;
         }
     };
@@ -159,14 +170,22 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int token, in
                 const bool in = h + u * R::kRows < h1;
                 if (kKind == 2 || half == 0) {  // copied as they are
                     if (kKind != 2 && in && r.y) R::store(y, y + to1, raw[u]);
-                    if (kKind != 0 && in && cache) R::store(cache + c, cache + c + to1, raw[u]);
+                    if constexpr (!Sink::kPlain) {
+                        if (kKind != 0) sink.store(p, h + u * R::kRows + (kKind == 2 ? p.k.heads : 0), in, R::unpack(raw[u]));
+                    } else {
+                        if (kKind != 0 && in && cache) R::store(cache + c, cache + c + to1, raw[u]);
+                    }
                     load(u, h + (kAppendUnroll + u) * R::kRows);
                 } else {
                     typename R::Pairs v = R::unpack(raw[u]);
                     load(u, h + (kAppendUnroll + u) * R::kRows);
                     R::turn(v, coef, on, half, j, table, scratch);
                     if (in && r.y) R::store(y, y + to1, v);
-                    if (kKind == 1 && in && cache) R::store(cache + c, cache + c + to1, v);
+                    if constexpr (!Sink::kPlain) {
+                        if (kKind == 1) sink.store(p, h + u * R::kRows, in, v);
+                    } else {
+                        if (kKind == 1 && in && cache) R::store(cache + c, cache + c + to1, v);
+                    }
                 }
                 y += ys;
                 c += cs;

@@ -1114,9 +1114,13 @@ attn_status run_rope(const attn_rows* q, const attn_rows* k, const void* qw, con
     return ok();
 }
 
-attn_status run_append(bool e4m3, const attn_rows* q, const attn_rows* k, const attn_rows* v,
+// The cache of an append: 16-bit rows, e4m3 codes with block scales, or e2m1 codes with row
+// scales.
+enum class CacheFormat { k16, kE4m3, kE2m1 };
+
+attn_status run_append(CacheFormat format, const attn_rows* q, const attn_rows* k, const attn_rows* v,
                        const int* cu_seqlens, const int* seq_lens, const int* positions, const int* block_table,
-                       void* kv_cache, float* scales, int B, int total, int D, int page_size,
+                       void* kv_cache, void* scales, const float* factors, int B, int total, int D, int page_size,
                        int max_pages_per_seq, int num_blocks, const attn_rotation* rotation, attn_dtype dtype,
                        cudaStream_t stream) {
     if (dtype == ATTN_F32)
@@ -1147,9 +1151,11 @@ attn_status run_append(bool e4m3, const attn_rows* q, const attn_rows* k, const 
     if ((st = validate_rows("k", k, 1, total, D, 2, 0)) != ATTN_OK) return st;
     if ((st = validate_rows("v", v, 1, total, D, 2, -1)) != ATTN_OK) return st;
     if (q && (st = validate_rows("q", q, 1, total, D, 2, 1)) != ATTN_OK) return st;
-    if (!cu_seqlens || !seq_lens || !block_table || !kv_cache || (e4m3 && !scales))
+    if (!cu_seqlens || !seq_lens || !block_table || !kv_cache || (format != CacheFormat::k16 && !scales))
         return fail(ATTN_ERR_INVALID_ARG, "cu_seqlens, seq_lens, block_table, kv_cache%s must be non-null",
-                    e4m3 ? " and scales" : "");
+                    format != CacheFormat::k16 ? " and scales" : "");
+    if (format == CacheFormat::kE2m1 && (!aligned(scales, 16) || !aligned(factors, 4)))
+        return fail(ATTN_ERR_INVALID_ARG, "scales must be 16-byte aligned and factors 4-byte aligned");
     if (!aligned(cu_seqlens, 4) || !aligned(seq_lens, 4) || !aligned(positions, 4) || !aligned(block_table, 4) ||
         !aligned(scales, 4))
         return fail(ATTN_ERR_INVALID_ARG, "cu_seqlens, seq_lens, positions, block_table and scales must be 4-byte aligned");
@@ -1157,16 +1163,150 @@ attn_status run_append(bool e4m3, const attn_rows* q, const attn_rows* k, const 
     LaunchEnv env;
     if ((st = device_env(stream, &env)) != ATTN_OK) return st;
     const RopeShape r{1, total, D, rot.turns, rot.rot_dim, rot.interleaved ? 1 : 0, rot.magnitude, dtype};
-    const AppendShape s{cu_seqlens, seq_lens, positions, block_table, kv_cache, scales,
-                        B, total, page_size, max_pages_per_seq, num_blocks};
+    const bool rows = format == CacheFormat::kE2m1;
+    const AppendShape s{cu_seqlens, seq_lens, positions, block_table, kv_cache,
+                        rows ? nullptr : static_cast<float*>(scales), rows ? static_cast<uint8_t*>(scales) : nullptr,
+                        factors, B, total, page_size, max_pages_per_seq, num_blocks};
     attn_rows qr{};
     if (q) qr = plain_rows(*q, 1, total);
     const attn_rows kr = plain_rows(*k, 1, total), vr = plain_rows(*v, 1, total);
     int grid = 0, kernels = 0;
-    cudaError_t e = e4m3 ? launch_append_paged_e4m3(s, r, q ? &qr : nullptr, kr, vr, env, &grid, &kernels)
-                         : launch_append_paged(s, r, q ? &qr : nullptr, kr, vr, env, &grid, &kernels);
+    const auto launch = format == CacheFormat::k16     ? launch_append_paged
+                        : format == CacheFormat::kE4m3 ? launch_append_paged_e4m3
+                                                       : launch_append_paged_e2m1;
+    cudaError_t e = launch(s, r, q ? &qr : nullptr, kr, vr, env, &grid, &kernels);
     if (e == cudaErrorInvalidConfiguration) return fail(ATTN_ERR_UNSUPPORTED, "too many rows for one launch");
     if (e != cudaSuccess) return cuda_fail(e, "paged append launch");
+    record_launch(grid, 0, kernels);
+    return ok();
+}
+
+// What the calls over a paged cache without an output tensor check of it.
+attn_status validate_pool(const void* kv_cache, const void* scales, bool four, const float* weights,
+                          const int* block_table, const int* seq_lens, int B, int Hkv, int D, int page_size,
+                          int max_pages_per_seq, int num_blocks) {
+    if (B < 1 || Hkv < 1 || page_size < 1 || max_pages_per_seq < 1 || num_blocks < 1)
+        return fail(ATTN_ERR_INVALID_ARG, "B, Hkv, page_size, max_pages_per_seq and num_blocks must be >= 1");
+    if (D != 64 && D != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim D=%d not supported (64 or 128)", D);
+    if (!kv_cache || !weights || !block_table || !seq_lens || (four && !scales))
+        return fail(ATTN_ERR_INVALID_ARG, "kv_cache, weights, block_table, seq_lens%s must be non-null",
+                    four ? " and scales" : "");
+    if (!aligned(kv_cache, 16) || (four && !aligned(scales, 16)))
+        return fail(ATTN_ERR_INVALID_ARG, "kv_cache and scales must be 16-byte aligned");
+    if (!aligned(weights, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
+        return fail(ATTN_ERR_INVALID_ARG, "weights, block_table and seq_lens must be 4-byte aligned");
+    if (static_cast<long long>(B) * Hkv > 0x7fffffffLL || static_cast<long long>(B) * max_pages_per_seq > 0x7fffffffLL)
+        return fail(ATTN_ERR_INVALID_ARG, "B*Hkv and B*max_pages_per_seq must fit in 31 bits");
+    if (static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 1024)
+        return fail(ATTN_ERR_INVALID_ARG, "max_pages_per_seq*page_size must be below 2^31 - 1024");
+    return ATTN_OK;
+}
+
+attn_status run_weights(bool four, const attn_rows* q, const float* lse, long long lse_head, long long lse_token,
+                        const void* kv_cache, const void* scales, const float* factors, const int* block_table,
+                        const int* cu_seqlens, const int* seq_lens, float* weights, int B, int total, int Hkv, int D,
+                        int page_size, int max_pages_per_seq, int num_blocks, float scale, attn_dtype dtype,
+                        cudaStream_t stream) {
+    if (dtype == ATTN_F32)
+        return fail(ATTN_ERR_UNSUPPORTED, "the weights of a paged cache are implemented for 16-bit I/O only");
+    if (dtype != ATTN_BF16 && dtype != ATTN_F16)
+        return fail(ATTN_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
+    attn_status st = validate_pool(kv_cache, scales, four, weights, block_table, seq_lens, B, Hkv, D, page_size,
+                                   max_pages_per_seq, num_blocks);
+    if (st != ATTN_OK) return st;
+    if (total < 0 || total > 0x7fffffff - 1024)
+        return fail(ATTN_ERR_INVALID_ARG, "total must be >= 0 and below 2^31 - 1024");
+    if (!std::isfinite(scale) || !(scale > 0.0f))
+        return fail(ATTN_ERR_INVALID_ARG, "scale must be finite and positive (got %g)", (double)scale);
+    if (!q) return fail(ATTN_ERR_INVALID_ARG, "q must be non-null");
+    if (total == 0) {
+        record_launch(0, 0, 0);
+        return ok();
+    }
+    if ((st = validate_rows("q", q, 1, total, D, 2, -1)) != ATTN_OK) return st;
+    if (q->heads % Hkv != 0) return fail(ATTN_ERR_INVALID_ARG, "Hq=%d is not a multiple of Hkv=%d", q->heads, Hkv);
+    if (static_cast<long long>(total) * q->heads > 0x7fffffffLL - 1024)
+        return fail(ATTN_ERR_INVALID_ARG, "total*Hq must be below 2^31 - 1024");
+    if (!lse || !cu_seqlens) return fail(ATTN_ERR_INVALID_ARG, "lse and cu_seqlens must be non-null");
+    if (!aligned(lse, 4) || !aligned(cu_seqlens, 4) || !aligned(factors, 4))
+        return fail(ATTN_ERR_INVALID_ARG, "lse, cu_seqlens and factors must be 4-byte aligned");
+    if (lse_head < 0 || lse_token < 0 || lse_head > (1ll << 40) || lse_token > (1ll << 40))
+        return fail(ATTN_ERR_INVALID_ARG, "lse's strides must be in 0..2^40");
+    LaunchEnv env;
+    if ((st = device_env(stream, &env)) != ATTN_OK) return st;
+    const attn_rows rows = plain_rows(*q, 1, total);
+    WeightsShape s{};
+    s.q = rows.x;
+    s.q_token = rows.x_token;
+    s.q_head = rows.x_head;
+    s.lse = lse;
+    s.lse_head = lse_head;
+    s.lse_token = lse_token;
+    s.cache = kv_cache;
+    s.scales = static_cast<const uint8_t*>(scales);
+    s.factors = factors;
+    s.block_table = block_table;
+    s.cu_seqlens = cu_seqlens;
+    s.seq_lens = seq_lens;
+    s.weights = weights;
+    s.B = B;
+    s.total = total;
+    s.Hq = q->heads;
+    s.Hkv = Hkv;
+    s.D = D;
+    s.page = page_size;
+    s.max_pages = max_pages_per_seq;
+    s.num_blocks = num_blocks;
+    s.scale = scale;
+    s.f16 = dtype == ATTN_F16 ? 1 : 0;
+    int grid = 0, kernels = 0;
+    const cudaError_t e = launch_weights_paged(s, env, &grid, &kernels);
+    if (e == cudaErrorInvalidConfiguration) return fail(ATTN_ERR_UNSUPPORTED, "too many requests or heads for one launch");
+    if (e != cudaSuccess) return cuda_fail(e, "weights launch");
+    record_launch(grid, 0, kernels);
+    return ok();
+}
+
+// Whether two ranges of bytes meet.
+bool meet(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
+attn_status run_evict(bool four, void* kv_cache, void* scales, float* weights, const int* block_table,
+                      const int* seq_lens, int* new_lens, int* kept, int B, int Hkv, int D, int page_size,
+                      int max_pages_per_seq, int num_blocks, int keep, int recent, cudaStream_t stream) {
+    attn_status st = validate_pool(kv_cache, scales, four, weights, block_table, seq_lens, B, Hkv, D, page_size,
+                                   max_pages_per_seq, num_blocks);
+    if (st != ATTN_OK) return st;
+    if (keep < 1 || recent < 0 || recent > keep)
+        return fail(ATTN_ERR_INVALID_ARG, "keep must be >= 1 and recent in 0..keep (got %d, %d)", keep, recent);
+    if (keep > 0x7fffffff - 65536) return fail(ATTN_ERR_INVALID_ARG, "keep must be below 2^31 - 65536");
+    if (!new_lens || !aligned(new_lens, 4) || !aligned(kept, 4))
+        return fail(ATTN_ERR_INVALID_ARG, "new_lens must be non-null, and new_lens and kept 4-byte aligned");
+    const size_t kept_bytes = 4ull * B * Hkv * keep;
+    if (meet(new_lens, 4ull * B, seq_lens, 4ull * B))
+        return fail(ATTN_ERR_INVALID_ARG, "new_lens may not share memory with seq_lens");
+    LaunchEnv env;
+    if ((st = device_env(stream, &env)) != ATTN_OK) return st;
+    void* ws = nullptr;
+    if (!kept) {
+        const cudaError_t e = workspace_alloc(&ws, kept_bytes, env);
+        if (e != cudaSuccess || ws == nullptr) {
+            cudaGetLastError();
+            return fail(ATTN_ERR_NO_MEMORY, "eviction workspace of %zu bytes: %s", kept_bytes, cudaGetErrorString(e));
+        }
+    }
+    const EvictShape s{kv_cache, static_cast<uint8_t*>(scales), weights, block_table, seq_lens, new_lens,
+                       kept ? kept : static_cast<int*>(ws), B, Hkv, D, page_size, max_pages_per_seq, num_blocks, keep,
+                       recent};
+    int grid = 0, kernels = 0;
+    cudaError_t e = launch_evict_paged(s, env, &grid, &kernels);
+    if (ws) {
+        const cudaError_t f = cudaFreeAsync(ws, env.stream);
+        if (e == cudaSuccess && f != cudaSuccess) e = f;
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "eviction launch");
     record_launch(grid, 0, kernels);
     return ok();
 }
@@ -1235,7 +1375,8 @@ attn_status attn_append_paged(const attn_rows* q, const attn_rows* k, const attn
                               const int* seq_lens, const int* positions, const int* block_table, void* kv_cache,
                               int B, int total, int D, int page_size, int max_pages_per_seq, int num_blocks,
                               const attn_rotation* rotation, attn_dtype dtype, cudaStream_t stream) {
-    return attn::run_append(false, q, k, v, cu_seqlens, seq_lens, positions, block_table, kv_cache, nullptr, B,
+    return attn::run_append(attn::CacheFormat::k16, q, k, v, cu_seqlens, seq_lens, positions, block_table, kv_cache,
+                            nullptr, nullptr, B,
                             total, D, page_size, max_pages_per_seq, num_blocks, rotation, dtype, stream);
 }
 
@@ -1244,7 +1385,8 @@ attn_status attn_append_paged_e4m3(const attn_rows* q, const attn_rows* k, const
                                    const int* block_table, void* kv_cache, float* scales, int B, int total, int D,
                                    int page_size, int max_pages_per_seq, int num_blocks,
                                    const attn_rotation* rotation, attn_dtype dtype, cudaStream_t stream) {
-    return attn::run_append(true, q, k, v, cu_seqlens, seq_lens, positions, block_table, kv_cache, scales, B,
+    return attn::run_append(attn::CacheFormat::kE4m3, q, k, v, cu_seqlens, seq_lens, positions, block_table, kv_cache,
+                            scales, nullptr, B,
                             total, D, page_size, max_pages_per_seq, num_blocks, rotation, dtype, stream);
 }
 
@@ -1285,6 +1427,95 @@ attn_status attn_fwd_decode_paged_e4m3(const void* q, const void* kv_cache, cons
     if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
     record_launch(grid, 0, kernels);
     return ok();
+}
+
+attn_status attn_append_paged_e2m1(const attn_rows* q, const attn_rows* k, const attn_rows* v,
+                                   const int* cu_seqlens, const int* seq_lens, const int* positions,
+                                   const int* block_table, void* kv_cache, void* scales, const float* factors, int B,
+                                   int total, int D, int page_size, int max_pages_per_seq, int num_blocks,
+                                   const attn_rotation* rotation, attn_dtype dtype, cudaStream_t stream) {
+    return attn::run_append(attn::CacheFormat::kE2m1, q, k, v, cu_seqlens, seq_lens, positions, block_table, kv_cache,
+                            scales, factors, B, total, D, page_size, max_pages_per_seq, num_blocks, rotation, dtype,
+                            stream);
+}
+
+attn_status attn_fwd_decode_paged_e2m1(const void* q, const void* kv_cache, const void* scales, const float* factors,
+                                       const int* block_table, const int* seq_lens, void* o, float* lse,
+                                       float* weights, int B, int Hq, int Hkv, int D, int page_size,
+                                       int max_pages_per_seq, int num_blocks, float scale, attn_dtype dtype,
+                                       cudaStream_t stream) {
+    using namespace attn;
+    if (dtype == ATTN_F32)
+        return fail(ATTN_ERR_UNSUPPORTED, "the paged decode is implemented for 16-bit I/O only");
+    if (!scales || !aligned(scales, 16))
+        return fail(ATTN_ERR_INVALID_ARG, "scales must be a non-null, 16-byte aligned device pointer");
+    if (!aligned(factors, 4) || !aligned(weights, 4))
+        return fail(ATTN_ERR_INVALID_ARG, "factors and weights must be 4-byte aligned");
+    attn_status st = validate_paged(q, kv_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, D, page_size,
+                                    max_pages_per_seq, num_blocks, scale, dtype);
+    if (st != ATTN_OK) return st;
+    if (B > 0x7fffffff - 1024) return fail(ATTN_ERR_INVALID_ARG, "B must be below 2^31 - 1024");
+    LaunchEnv env;
+    st = device_env(stream, &env);
+    if (st != ATTN_OK) return st;
+    PagedShape s{B, Hq, Hkv, D, page_size, max_pages_per_seq, num_blocks, scale};
+    s.f16 = dtype == ATTN_F16 ? 1 : 0;
+    const size_t bytes = decode_e2m1_workspace_bytes(s, env.num_sms, weights != nullptr, lse == nullptr);
+    void* ws = nullptr;
+    cudaError_t e = bytes > 0 ? workspace_alloc(&ws, bytes, env) : cudaSuccess;
+    if (e != cudaSuccess || (bytes > 0 && ws == nullptr)) {
+        cudaGetLastError();
+        return fail(ATTN_ERR_NO_MEMORY, "paged decode workspace of %zu bytes: %s", bytes, cudaGetErrorString(e));
+    }
+    int grid = 0, kernels = 0;
+    e = launch_decode_paged_e2m1(static_cast<const uint16_t*>(q), static_cast<const uint8_t*>(kv_cache),
+                                 static_cast<const uint8_t*>(scales), factors, block_table, seq_lens,
+                                 static_cast<uint16_t*>(o), lse, weights, ws, s, env, &grid, &kernels);
+    if (ws) {
+        cudaError_t f = cudaFreeAsync(ws, env.stream);
+        if (e == cudaSuccess && f != cudaSuccess) e = f;
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
+    record_launch(grid, 0, kernels);
+    return ok();
+}
+
+attn_status attn_weights_paged(const attn_rows* q, const float* lse, long long lse_head, long long lse_token,
+                               const void* kv_cache, const int* block_table, const int* cu_seqlens,
+                               const int* seq_lens, float* weights, int B, int total, int Hkv, int D, int page_size,
+                               int max_pages_per_seq, int num_blocks, float scale, attn_dtype dtype,
+                               cudaStream_t stream) {
+    return attn::run_weights(false, q, lse, lse_head, lse_token, kv_cache, nullptr, nullptr, block_table, cu_seqlens,
+                             seq_lens, weights, B, total, Hkv, D, page_size, max_pages_per_seq, num_blocks, scale,
+                             dtype, stream);
+}
+
+attn_status attn_weights_paged_e2m1(const attn_rows* q, const float* lse, long long lse_head, long long lse_token,
+                                    const void* kv_cache, const void* scales, const float* factors,
+                                    const int* block_table, const int* cu_seqlens, const int* seq_lens,
+                                    float* weights, int B, int total, int Hkv, int D, int page_size,
+                                    int max_pages_per_seq, int num_blocks, float scale, attn_dtype dtype,
+                                    cudaStream_t stream) {
+    return attn::run_weights(true, q, lse, lse_head, lse_token, kv_cache, scales, factors, block_table, cu_seqlens,
+                             seq_lens, weights, B, total, Hkv, D, page_size, max_pages_per_seq, num_blocks, scale,
+                             dtype, stream);
+}
+
+attn_status attn_evict_paged(void* kv_cache, float* weights, const int* block_table, const int* seq_lens,
+                             int* new_lens, int* kept, int B, int Hkv, int D, int page_size, int max_pages_per_seq,
+                             int num_blocks, int keep, int recent, attn_dtype dtype, cudaStream_t stream) {
+    if (dtype != ATTN_BF16 && dtype != ATTN_F16)
+        return attn::fail(dtype == ATTN_F32 ? ATTN_ERR_UNSUPPORTED : ATTN_ERR_INVALID_ARG,
+                          "the eviction is implemented for 16-bit caches (and 4-bit ones, by a call of their own)");
+    return attn::run_evict(false, kv_cache, nullptr, weights, block_table, seq_lens, new_lens, kept, B, Hkv, D,
+                           page_size, max_pages_per_seq, num_blocks, keep, recent, stream);
+}
+
+attn_status attn_evict_paged_e2m1(void* kv_cache, void* scales, float* weights, const int* block_table,
+                                  const int* seq_lens, int* new_lens, int* kept, int B, int Hkv, int D, int page_size,
+                                  int max_pages_per_seq, int num_blocks, int keep, int recent, cudaStream_t stream) {
+    return attn::run_evict(true, kv_cache, scales, weights, block_table, seq_lens, new_lens, kept, B, Hkv, D,
+                           page_size, max_pages_per_seq, num_blocks, keep, recent, stream);
 }
 
 }  // extern "C"

@@ -171,6 +171,8 @@ struct AppendShape {
     const int* block_table;
     void* cache;
     float* scales;  // 8-bit cache only
+    uint8_t* row_scales;   // 4-bit cache only, and
+    const float* factors;  // [2, heads] or null
     int B, total, page, max_pages, num_blocks;
 };
 struct AppendParams;
@@ -190,14 +192,58 @@ cudaError_t launch_append_paged_e4m3(const AppendShape& s, const RopeShape& r, c
 // The workspace is 0 bytes where a cluster takes each unit (decode_e4m3_short.cu):
 // decode_e4m3_short_ranks() CTAs, 0 otherwise.
 int decode_e4m3_short_ranks(const PagedShape& s, int num_sms);
-struct E4m3Params;
-cudaError_t launch_decode_e4m3_short(const E4m3Params& p, const PagedShape& s, int ranks, const LaunchEnv& env,
+struct CacheParams;
+cudaError_t launch_decode_e4m3_short(const CacheParams& p, const PagedShape& s, int ranks, const LaunchEnv& env,
                                      int* grid_out);
 size_t decode_e4m3_workspace_bytes(const PagedShape& s, int num_sms);
 cudaError_t launch_decode_paged_e4m3(const uint16_t* q, const uint8_t* kv, const float* scales,
                                      const int32_t* block_table, const int32_t* seq_lens,
                                      uint16_t* o, float* lse, void* ws, const PagedShape& s,
                                      const LaunchEnv& env, int* grid_out, int* kernels_launched);
+
+// The 4-bit cache: codes [num_blocks, 2, Hkv, page, D / 2], scales [num_blocks, 2, Hkv, page,
+// D / 16] (e4m3), factors [2, Hkv] or null.
+cudaError_t launch_append_paged_e2m1(const AppendShape& s, const RopeShape& r, const RopeRows* q,
+                                     const RopeRows& k, const RopeRows& v, const LaunchEnv& env,
+                                     int* grid_out, int* kernels_launched);
+// weights: [num_blocks, Hkv, page] or null; the workspace then also holds the scores, and
+// (own_lse: lse is null) the log-sum-exps.
+int decode_e2m1_short_ranks(const PagedShape& s, int num_sms);
+cudaError_t launch_decode_e2m1_short(const CacheParams& p, const PagedShape& s, int ranks, const LaunchEnv& env,
+                                     int* grid_out);
+size_t decode_e2m1_workspace_bytes(const PagedShape& s, int num_sms, bool weights, bool own_lse);
+cudaError_t launch_decode_paged_e2m1(const uint16_t* q, const uint8_t* kv, const uint8_t* scales, const float* factors,
+                                     const int32_t* block_table, const int32_t* seq_lens, uint16_t* o, float* lse,
+                                     float* weights, void* ws, const PagedShape& s, const LaunchEnv& env,
+                                     int* grid_out, int* kernels_launched);
+
+// Attention weights of packed queries added up over a paged cache's keys.
+struct WeightsShape {
+    const void* q;  // [total, Hq, D], strides in elements
+    long long q_token, q_head;
+    const float* lse;  // [Hq, total], strides in elements
+    long long lse_head, lse_token;
+    const void* cache;
+    const uint8_t* scales;  // 4-bit cache; null: 16-bit
+    const float* factors;
+    const int *block_table, *cu_seqlens, *seq_lens;
+    float* weights;
+    int B, total, Hq, Hkv, D, page, max_pages, num_blocks;
+    float scale;
+    int f16;
+};
+cudaError_t launch_weights_paged(const WeightsShape& s, const LaunchEnv& env, int* grid_out, int* kernels_launched);
+
+// Eviction: the kept rows of each request and KV head moved to its first slots.
+struct EvictShape {
+    void* cache;
+    uint8_t* scales;  // 4-bit cache; null: 16-bit
+    float* weights;
+    const int *block_table, *seq_lens;
+    int *new_lens, *kept;
+    int B, Hkv, D, page, max_pages, num_blocks, keep, recent;
+};
+cudaError_t launch_evict_paged(const EvictShape& s, const LaunchEnv& env, int* grid_out, int* kernels_launched);
 
 // Diagnostics.
 cudaError_t launch_diag_mma_tile(const CUtensorMap& a, const CUtensorMap& b,

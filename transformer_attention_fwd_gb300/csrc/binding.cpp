@@ -1,4 +1,4 @@
-// binding.cpp -- the rotary, append and 8-bit-cache calls on torch tensors.
+// binding.cpp -- the rotary, append, quantised-cache and eviction calls on torch tensors.
 //
 // Argument checks and marshalling only: every tensor's type, shape, placement and
 // strides are checked against what the call reads and writes, outputs are
@@ -285,10 +285,60 @@ PyObject* rope(PyObject* const* a, Py_ssize_t n) {
     return st == ATTN_OK ? two(yq, yk) : failed(st);
 }
 
+// A paged cache's pool: 16-bit rows of `type`, e4m3 codes (scales: float32 for each block, K
+// or V, and head), or e2m1 codes in pairs (scales: e4m3 for each 16 elements of a row; factors:
+// float32 [2, Hkv] or none).
+enum class Held { k16, kE4m3, kE2m1 };
+struct Pool {
+    int64_t blocks, Hkv, page, D;
+    void* cache;
+    void* scales = nullptr;
+    const float* factors = nullptr;
+    // heads: the KV heads there have to be, 0: any.  D: the head dim, 0: the cache's.
+    Pool(Held held, const Tensor& t, const Tensor* s, const Tensor* f, at::ScalarType type, int64_t heads, int64_t dim,
+         int device) {
+        const at::ScalarType kind = held == Held::k16 ? type : held == Held::kE4m3 ? at::kFloat8_e4m3fn : at::kByte;
+        const int64_t per = held == Held::kE2m1 ? 2 : 1;
+        if (t.dim() != 5 || t.scalar_type() != kind || t.size(1) != 2 || (heads && t.size(2) != heads) ||
+            (dim && t.size(4) * per != dim) || !t.is_contiguous()) {
+            std::ostringstream shape;
+            shape << "[num_blocks, 2, ";
+            if (heads) shape << heads; else shape << "Hkv";
+            shape << ", page_size, ";
+            if (dim) shape << dim / per; else shape << (per == 2 ? "D / 2" : "D");
+            refuse("kv_cache must be a contiguous ", kind, " tensor ", shape.str(), "] (got ", t.scalar_type(), " ", t.sizes(), ")");
+        }
+        on_device(t, "kv_cache", device);
+        blocks = t.size(0);
+        Hkv = t.size(2);
+        page = t.size(3);
+        D = t.size(4) * per;
+        cache = t.data_ptr();
+        if (held == Held::kE4m3) {
+            exact(*s, "scales", at::kFloat, {blocks, 2, Hkv}, device);
+            scales = s->data_ptr();
+        }
+        if (held == Held::kE2m1) {
+            exact(*s, "scales", at::kFloat8_e4m3fn, {blocks, 2, Hkv, page, D / 16}, device);
+            scales = s->data_ptr();
+            if (f) {
+                exact(*f, "factors", at::kFloat, {2, Hkv}, device);
+                factors = f->data_ptr<float>();
+            }
+        }
+    }
+};
+
+// The weights of a pool's slots.
+float* weights_of(const Tensor& w, const Pool& pool, int device) {
+    exact(w, "weights", at::kFloat, {pool.blocks, pool.Hkv, pool.page}, device);
+    return w.data_ptr<float>();
+}
+
 // append(k, v, kv_cache, scales, block_table, cu_seqlens, seq_lens, rotation, positions, q, out_q,
-//        out_k, stream) -> (out_q, out_k)
+//        out_k, stream, factors, four) -> (out_q, out_k)
 PyObject* append(PyObject* const* a, Py_ssize_t n) {
-    arguments(n, 13);
+    arguments(n, 15);
     const Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &cache = tensor(a[2], "kv_cache");
     const Tensor* scales = maybe(a[3], "scales");
     const Tensor &table = tensor(a[4], "block_table"), &cu = tensor(a[5], "cu_seqlens"), &lens = tensor(a[6], "seq_lens");
@@ -303,14 +353,9 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
     if (v.size(1) != Hkv) refuse("k and v must have the same heads");
     if (q) rq = rows_in("q", *q, k, device);
     else if (given_q) refuse("out_q without q");
-    const at::ScalarType held = scales ? at::kFloat8_e4m3fn : k.scalar_type();
-    if (cache.dim() != 5 || cache.scalar_type() != held || cache.size(1) != 2 || cache.size(2) != Hkv ||
-        cache.size(4) != D || !cache.is_contiguous())
-        refuse("kv_cache must be a contiguous ", held, " tensor [num_blocks, 2, ", Hkv, ", page_size, ", D, "] (got ",
-               cache.scalar_type(), " ", cache.sizes(), ")");
-    on_device(cache, "kv_cache", device);
-    const int64_t blocks = cache.size(0), page = cache.size(3);
-    if (scales) exact(*scales, "scales", at::kFloat, {blocks, 2, Hkv}, device);
+    const Tensor* factors = maybe(a[13], "factors");
+    const Held held = !scales ? Held::k16 : a[14] == Py_True ? Held::kE2m1 : Held::kE4m3;
+    const Pool pool(held, cache, scales, factors, k.scalar_type(), Hkv, D, device);
     if (table.dim() != 2) refuse("block_table must be [B, max_pages]");
     const int64_t B = table.size(0), pages = table.size(1);
     const int* table_p = ints(table, "block_table", {B, pages}, device);
@@ -323,39 +368,40 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
     std::optional<Tensor> yq, yk;
     if (q) yq = rows_out("q", *q, given_q, rq);
     if (given_k) yk = rows_out("k", k, given_k, rk);
-    const int b = as_int(B, "B"), t = as_int(total, "total"), d = as_int(D, "D"), p = as_int(page, "page_size");
-    const int w = as_int(pages, "max_pages"), nb = as_int(blocks, "num_blocks");
+    const int b = as_int(B, "B"), t = as_int(total, "total"), d = as_int(D, "D"), p = as_int(pool.page, "page_size");
+    const int w = as_int(pages, "max_pages"), nb = as_int(pool.blocks, "num_blocks");
     const attn_dtype type = type_of(k);
-    void* cache_p = cache.data_ptr();
-    float* scales_p = scales ? scales->data_ptr<float>() : nullptr;
     attn_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = scales ? attn_append_paged_e4m3(q ? &rq : nullptr, &rk, &rv, cu_p, lens_p, pos_p, table_p, cache_p, scales_p, b,
-                                         t, d, p, w, nb, rotation.r, type, on.stream)
-                : attn_append_paged(q ? &rq : nullptr, &rk, &rv, cu_p, lens_p, pos_p, table_p, cache_p, b, t, d, p, w, nb,
-                                    rotation.r, type, on.stream);
+    if (held == Held::kE2m1)
+        st = attn_append_paged_e2m1(q ? &rq : nullptr, &rk, &rv, cu_p, lens_p, pos_p, table_p, pool.cache, pool.scales,
+                                    pool.factors, b, t, d, p, w, nb, rotation.r, type, on.stream);
+    else if (held == Held::kE4m3)
+        st = attn_append_paged_e4m3(q ? &rq : nullptr, &rk, &rv, cu_p, lens_p, pos_p, table_p, pool.cache,
+                                    static_cast<float*>(pool.scales), b, t, d, p, w, nb, rotation.r, type, on.stream);
+    else
+        st = attn_append_paged(q ? &rq : nullptr, &rk, &rv, cu_p, lens_p, pos_p, table_p, pool.cache, b, t, d, p, w, nb,
+                               rotation.r, type, on.stream);
     Py_END_ALLOW_THREADS
     return st == ATTN_OK ? two(yq, yk) : failed(st);
 }
 
-// decode_e4m3(q, kv_cache, scales, block_table, seq_lens, scale, out, lse, want_lse, stream)
+// decode(q, kv_cache, scales, block_table, seq_lens, scale, out, lse, want_lse, stream, factors, weights, four)
 //   -> (out, lse); scale None: 1 / sqrt(D)
-PyObject* decode_e4m3(PyObject* const* a, Py_ssize_t n) {
-    arguments(n, 10);
+PyObject* decode(PyObject* const* a, Py_ssize_t n) {
+    arguments(n, 13);
     const Tensor &q = tensor(a[0], "q"), &cache = tensor(a[1], "kv_cache"), &scales = tensor(a[2], "scales");
     const Tensor &table = tensor(a[3], "block_table"), &lens = tensor(a[4], "seq_lens");
     const Tensor *given = maybe(a[6], "out"), *given_lse = maybe(a[7], "lse");
+    const Tensor *factors = maybe(a[10], "factors"), *weights = maybe(a[11], "weights");
+    const bool four = a[12] == Py_True;
     if (!q.is_cuda() || q.dim() != 4 || q.size(2) != 1 || !q.is_contiguous() ||
         (q.scalar_type() != at::kBFloat16 && q.scalar_type() != at::kHalf))
         refuse("q must be a contiguous bf16 or fp16 CUDA tensor [B, Hq, 1, D]");
     const int device = q.get_device();
     const int64_t B = q.size(0), Hq = q.size(1), D = q.size(3);
-    if (cache.dim() != 5 || cache.scalar_type() != at::kFloat8_e4m3fn || cache.size(1) != 2 || cache.size(4) != D ||
-        !cache.is_contiguous())
-        refuse("kv_cache must be a contiguous float8_e4m3fn tensor [num_blocks, 2, Hkv, page_size, ", D, "]");
-    on_device(cache, "kv_cache", device);
-    const int64_t blocks = cache.size(0), Hkv = cache.size(2), page = cache.size(3);
-    exact(scales, "scales", at::kFloat, {blocks, 2, Hkv}, device);
+    const Pool pool(four ? Held::kE2m1 : Held::kE4m3, cache, &scales, factors, q.scalar_type(), 0, D, device);
+    float* weights_p = weights ? weights_of(*weights, pool, device) : nullptr;
     if (table.dim() != 2) refuse("block_table must be [B, max_pages]");
     const int64_t pages = table.size(1);
     const int* table_p = ints(table, "block_table", {B, pages}, device);
@@ -382,19 +428,116 @@ PyObject* decode_e4m3(PyObject* const* a, Py_ssize_t n) {
     std::optional<Tensor> lse;
     if (given_lse) lse = *given_lse;
     else if (a[8] == Py_True) lse = fresh({B, Hq}, at::kFloat, q);
-    const int b = as_int(B, "B"), hq = as_int(Hq, "Hq"), hkv = as_int(Hkv, "Hkv"), d = as_int(D, "D");
-    const int p = as_int(page, "page_size"), w = as_int(pages, "max_pages"), nb = as_int(blocks, "num_blocks");
+    const int b = as_int(B, "B"), hq = as_int(Hq, "Hq"), hkv = as_int(pool.Hkv, "Hkv"), d = as_int(D, "D");
+    const int p = as_int(pool.page, "page_size"), w = as_int(pages, "max_pages"), nb = as_int(pool.blocks, "num_blocks");
     const attn_dtype type = type_of(q);
-    const void *q_p = q.data_ptr(), *cache_p = cache.data_ptr();
-    const float* scales_p = scales.data_ptr<float>();
+    const void* q_p = q.data_ptr();
     void* out_p = out.data_ptr();
     float* lse_p = lse ? lse->data_ptr<float>() : nullptr;
     attn_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = attn_fwd_decode_paged_e4m3(q_p, cache_p, scales_p, table_p, lens_p, out_p, lse_p, b, hq, hkv, d, p, w, nb,
-                                    static_cast<float>(scale), type, on.stream);
+    if (four)
+        st = attn_fwd_decode_paged_e2m1(q_p, pool.cache, pool.scales, pool.factors, table_p, lens_p, out_p, lse_p,
+                                        weights_p, b, hq, hkv, d, p, w, nb, static_cast<float>(scale), type, on.stream);
+    else
+        st = attn_fwd_decode_paged_e4m3(q_p, pool.cache, static_cast<const float*>(pool.scales), table_p, lens_p, out_p,
+                                        lse_p, b, hq, hkv, d, p, w, nb, static_cast<float>(scale), type, on.stream);
     Py_END_ALLOW_THREADS
     return st == ATTN_OK ? two(out, lse) : failed(st);
+}
+
+// add_weights(q, lse, kv_cache, scales, block_table, cu_seqlens, seq_lens, weights, scale, factors, stream) -> weights
+PyObject* add_weights(PyObject* const* a, Py_ssize_t n) {
+    arguments(n, 11);
+    const Tensor &q = tensor(a[0], "q"), &lse = tensor(a[1], "lse"), &cache = tensor(a[2], "kv_cache");
+    const Tensor* scales = maybe(a[3], "scales");
+    const Tensor &table = tensor(a[4], "block_table"), &cu = tensor(a[5], "cu_seqlens"), &lens = tensor(a[6], "seq_lens");
+    const Tensor& weights = tensor(a[7], "weights");
+    const Tensor* factors = maybe(a[9], "factors");
+    if (q.scalar_type() != at::kBFloat16 && q.scalar_type() != at::kHalf)
+        refuse("the weights of a paged cache take bf16 or fp16 queries");
+    const int device = device_of(q, "q");
+    if (q.dim() != 3) refuse("q must be [total, Hq, D] (got ", q.sizes(), ")");
+    const int64_t total = q.size(0), Hq = q.size(1), D = q.size(2);
+    attn_rows rq = rows_in("q", q, q, device);
+    const Pool pool(scales ? Held::kE2m1 : Held::k16, cache, scales, factors, q.scalar_type(), 0, D, device);
+    float* weights_p = weights_of(weights, pool, device);
+    on_device(lse, "lse", device);
+    if (lse.scalar_type() != at::kFloat || lse.dim() != 2 || lse.size(0) != Hq || lse.size(1) != total)
+        refuse("lse must be a float32 tensor [", Hq, ", ", total, "] (got ", lse.scalar_type(), " ", lse.sizes(), ")");
+    if (table.dim() != 2) refuse("block_table must be [B, max_pages]");
+    const int64_t B = table.size(0), pages = table.size(1);
+    const int* table_p = ints(table, "block_table", {B, pages}, device);
+    const int* lens_p = ints(lens, "seq_lens", {B}, device);
+    const int* cu_p = ints(cu, "cu_seqlens", {B + 1}, device);
+    double scale = 1.0 / std::sqrt(static_cast<double>(D));
+    if (a[8] != Py_None) {
+        scale = PyFloat_AsDouble(a[8]);
+        if (PyErr_Occurred()) throw PythonError{};
+    }
+    current(device);
+    const OnStream on(a[10], device);
+    const int b = as_int(B, "B"), t = as_int(total, "total"), hkv = as_int(pool.Hkv, "Hkv"), d = as_int(D, "D");
+    const int p = as_int(pool.page, "page_size"), w = as_int(pages, "max_pages"), nb = as_int(pool.blocks, "num_blocks");
+    const attn_dtype type = type_of(q);
+    const float* lse_p = lse.data_ptr<float>();
+    const long long head = lse.stride(0), token = lse.stride(1);
+    attn_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = scales ? attn_weights_paged_e2m1(&rq, lse_p, head, token, pool.cache, pool.scales, pool.factors, table_p, cu_p,
+                                          lens_p, weights_p, b, t, hkv, d, p, w, nb, static_cast<float>(scale), type,
+                                          on.stream)
+                : attn_weights_paged(&rq, lse_p, head, token, pool.cache, table_p, cu_p, lens_p, weights_p, b, t, hkv, d,
+                                     p, w, nb, static_cast<float>(scale), type, on.stream);
+    Py_END_ALLOW_THREADS
+    if (st != ATTN_OK) return failed(st);
+    Py_INCREF(a[7]);
+    return a[7];
+}
+
+// evict(kv_cache, scales, weights, block_table, seq_lens, keep, recent, new_lens, kept, want_kept, stream)
+//   -> (new_lens, kept)
+PyObject* evict(PyObject* const* a, Py_ssize_t n) {
+    arguments(n, 11);
+    const Tensor& cache = tensor(a[0], "kv_cache");
+    const Tensor* scales = maybe(a[1], "scales");
+    const Tensor &weights = tensor(a[2], "weights"), &table = tensor(a[3], "block_table"), &lens = tensor(a[4], "seq_lens");
+    const Tensor *given_lens = maybe(a[7], "new_lens"), *given_kept = maybe(a[8], "kept");
+    const int device = device_of(cache, "kv_cache");
+    if (!scales && cache.scalar_type() != at::kBFloat16 && cache.scalar_type() != at::kHalf)
+        refuse("the eviction takes bf16 or fp16 caches (got ", cache.scalar_type(), ")");
+    const Pool pool(scales ? Held::kE2m1 : Held::k16, cache, scales, nullptr, cache.scalar_type(), 0, 0, device);
+    float* weights_p = weights_of(weights, pool, device);
+    if (table.dim() != 2) refuse("block_table must be [B, max_pages]");
+    const int64_t B = table.size(0), pages = table.size(1);
+    const int* table_p = ints(table, "block_table", {B, pages}, device);
+    const int* lens_p = ints(lens, "seq_lens", {B}, device);
+    const int64_t keep = PyLong_AsLongLong(a[5]), recent = PyLong_AsLongLong(a[6]);
+    if (PyErr_Occurred()) throw PythonError{};
+    if (keep < 1 || recent < 0 || recent > keep)
+        refuse("keep must be >= 1 and recent in 0..keep (got ", keep, ", ", recent, ")");
+    const int k = as_int(keep, "keep"), r = as_int(recent, "recent");
+    current(device);
+    const OnStream on(a[10], device);
+    if (given_lens) exact(*given_lens, "new_lens", at::kInt, {B}, device);
+    if (given_kept) exact(*given_kept, "kept", at::kInt, {B, pool.Hkv, keep}, device);
+    const Tensor new_lens = given_lens ? *given_lens : fresh({B}, at::kInt, cache);
+    std::optional<Tensor> kept;
+    if (given_kept) kept = *given_kept;
+    else if (a[9] == Py_True) kept = fresh({B, pool.Hkv, keep}, at::kInt, cache);
+    const int b = as_int(B, "B"), hkv = as_int(pool.Hkv, "Hkv"), d = as_int(pool.D, "D");
+    const int p = as_int(pool.page, "page_size"), w = as_int(pages, "max_pages"), nb = as_int(pool.blocks, "num_blocks");
+    int* new_p = new_lens.data_ptr<int>();
+    int* kept_p = kept ? kept->data_ptr<int>() : nullptr;
+    const attn_dtype type = scales ? ATTN_BF16 : type_of(cache);
+    attn_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = scales ? attn_evict_paged_e2m1(pool.cache, pool.scales, weights_p, table_p, lens_p, new_p, kept_p, b, hkv, d, p,
+                                        w, nb, k, r, on.stream)
+                : attn_evict_paged(pool.cache, weights_p, table_p, lens_p, new_p, kept_p, b, hkv, d, p, w, nb, k, r, type,
+                                   on.stream);
+    Py_END_ALLOW_THREADS
+    return st == ATTN_OK ? two(new_lens, kept) : failed(st);
 }
 
 // set_error(cls): the exception class of a status other than ATTN_OK.
@@ -419,7 +562,9 @@ PyMethodDef g_methods[] = {
     {"rotation", fast<rotation>(), METH_FASTCALL, nullptr},
     {"rope", fast<rope>(), METH_FASTCALL, nullptr},
     {"append", fast<append>(), METH_FASTCALL, nullptr},
-    {"decode_e4m3", fast<decode_e4m3>(), METH_FASTCALL, nullptr},
+    {"decode", fast<decode>(), METH_FASTCALL, nullptr},
+    {"add_weights", fast<add_weights>(), METH_FASTCALL, nullptr},
+    {"evict", fast<evict>(), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

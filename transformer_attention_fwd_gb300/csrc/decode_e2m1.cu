@@ -1,0 +1,107 @@
+// decode_e2m1.cu -- decode (one query row per (request, head)) over the paged 4-bit
+// cache with one scale for each 16 elements of a row (attn_fwd_decode_paged_e2m1), and
+// the sums of its attention weights.
+//
+//   O = sum_j p_j v_j / sum_j p_j,  p_j = 2^x_j,  x_j = log2(e) * scale * (q . k_j)
+//
+// with k_j, v_j = code * scale * the head's factor.  HBM bound: 2 * (D/2 + D/16) bytes
+// per key and KV head are read once.  The work, its split and its merge are the 8-bit
+// decode's (decode_e4m3.cu).  A code times its scale is exact in fp16, so the operands
+// of the tensor cores are made from both in registers: two codes of K to one word by a
+// conversion, V's by the same conversion once the nibbles of two keys' rows share a
+// byte, each then times its scale; the heads' factors multiply the query and the result.
+// V's sizes are in the operand, so one reference serves the sum of the weights and the
+// weighted sum (the 8-bit decode has a scale per block in its weights).
+//
+// Weights added up: the tiles leave their scores (fp32, one for each key and head) in a
+// workspace, and once the log-sum-exp is known a second kernel adds 2^(x - lse) over a KV
+// head's query heads to each key's weight: 2 * 4 * group bytes per key and KV head
+// instead of the row of K that a second look at the keys would read.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "decode_cache_long.cuh"
+#include "decode_e2m1.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kAddThreads = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// weights[slot] += sum over a KV head's query heads of 2^(score - lse).  Block (x, y):
+// keys x * kAddThreads and on, gridDim.x blocks apart, of (request, KV head) y, y + gridDim.y, ..
+__global__ void __launch_bounds__(kAddThreads) add_scores_kernel(const CacheParams p, float* weights) {
+    grid_wait();
+    grid_launch_next();
+    const int units = p.B * p.Hkv;
+    for (int u = blockIdx.y; u < units; u += gridDim.y) {
+        const int b = u / p.Hkv, hkv = u - b * p.Hkv;
+        const int len = clamped_len(p, b);
+        const float* lse = p.lse + static_cast<int64_t>(b) * p.Hq + hkv * p.group;
+        const float* scores = p.scores + static_cast<int64_t>(u) * p.max_pages * p.page.size * p.group;
+        for (int key = blockIdx.x * kAddThreads + threadIdx.x; key < len; key += gridDim.x * kAddThreads) {
+            int row;
+            const int id = p.block_table[static_cast<int64_t>(b) * p.max_pages + p.page.split(key, &row)];
+            if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) continue;  // reported by the decode
+            const float* x = scores + static_cast<int64_t>(key) * p.group;
+            float sum = 0.0f;
+            for (int h = 0; h < p.group; ++h) sum += ex2_approx(x[h] - lse[h] * kLog2e);
+            float* w = weights + (static_cast<int64_t>(id) * p.Hkv + hkv) * p.page.size + row;
+            *w += sum;
+        }
+    }
+}
+
+struct AddLayout {
+    size_t scores, lse, bytes;  // behind the decode's own workspace
+    AddLayout(const PagedShape& s, size_t at, bool weights, bool own_lse) {
+        auto up16 = [](size_t x) { return (x + 15) / 16 * 16; };
+        scores = up16(at);
+        lse = up16(scores + (weights ? 4ull * s.B * s.Hq * s.max_pages * s.page : 0));
+        bytes = weights ? lse + (own_lse ? 4ull * s.B * s.Hq : 0) : at;
+    }
+};
+
+size_t decode_bytes(const PagedShape& s, int num_sms) {
+    return decode_e2m1_short_ranks(s, num_sms) > 0 ? 0 : decode_long_workspace<E2m1Cache>(s, num_sms);
+}
+
+}  // namespace
+
+size_t decode_e2m1_workspace_bytes(const PagedShape& s, int num_sms, bool weights, bool own_lse) {
+    return AddLayout(s, decode_bytes(s, num_sms), weights, own_lse).bytes;
+}
+
+cudaError_t launch_decode_paged_e2m1(const uint16_t* q, const uint8_t* kv, const uint8_t* scales, const float* factors,
+                                     const int32_t* block_table, const int32_t* seq_lens, uint16_t* o, float* lse,
+                                     float* weights, void* ws, const PagedShape& s, const LaunchEnv& env,
+                                     int* grid_out, int* kernels_launched) {
+    CacheParams p = cache_params(q, kv, block_table, seq_lens, o, lse, s, env);
+    p.row_scales = scales;
+    p.factors = factors;
+    if (weights) {
+        uint8_t* base = static_cast<uint8_t*>(ws);
+        const AddLayout lay(s, decode_bytes(s, env.num_sms), true, lse == nullptr);
+        p.scores = reinterpret_cast<float*>(base + lay.scores);
+        if (!lse) p.lse = reinterpret_cast<float*>(base + lay.lse);
+    }
+    cudaError_t e;
+    if (const int ranks = decode_e2m1_short_ranks(s, env.num_sms); ranks > 0) {
+        *kernels_launched = 1;
+        e = launch_decode_e2m1_short(p, s, ranks, env, grid_out);
+    } else {
+        e = launch_decode_long<E2m1Cache>(p, s, ws, env, grid_out, kernels_launched);
+    }
+    if (e != cudaSuccess || !weights) return e;
+    ++*kernels_launched;
+    const long long keys = static_cast<long long>(s.max_pages) * s.page, units = static_cast<long long>(s.B) * s.Hkv;
+    // Blocks for eight to an SM, not more than there are keys for by the table's width.
+    const unsigned y = static_cast<unsigned>(std::min(units, 65535ll));
+    const long long want = std::max(1ll, 16ll * env.num_sms / y);
+    const unsigned x = static_cast<unsigned>(std::min(want, (keys + kAddThreads - 1) / kAddThreads));
+    return launch_serial(add_scores_kernel, dim3(x, y), kAddThreads, 0, env.stream, p, weights);
+}
+
+}  // namespace attn

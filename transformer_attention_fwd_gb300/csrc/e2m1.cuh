@@ -1,0 +1,49 @@
+// e2m1.cuh -- the 4-bit element of the quantised cache (sign, 2 exponent bits and 1
+// mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and its scales, one e4m3 value for each 16
+// elements of a row.  Two codes share a byte, the even element in the low half.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "e4m3.cuh"
+
+namespace attn {
+
+constexpr float kE2m1Max = 6.0f;
+constexpr float kRowScaleMin = 0x1p-9f;  // the smallest e4m3 value above 0
+constexpr int kRowScaleSpan = 16;        // elements of a scale
+
+// The four bytes' codes as pairs of fp16 values: exact.
+__device__ __forceinline__ void e2m1_to_f16x8(uint32_t codes, uint32_t (&v)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(codes));
+}
+// Eight fp32 values to codes: to the nearest, halfway to the even code, beyond 6 to 6.
+__device__ __forceinline__ uint32_t e2m1_pack8(const float (&x)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return r;
+}
+// Two e4m3 values (the low 16 bits) as fp16: exact.
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t codes) {
+    uint32_t v;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(v) : "r"(codes));
+    return v;
+}
+// Products of fp16 pairs.  A code times its scale is exact: 2 and 4 significant bits,
+// between 2^-10 and 2688.
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+}  // namespace attn
