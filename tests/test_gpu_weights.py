@@ -77,6 +77,8 @@ CASES = [
     dict(lens=[260, 70], new=[40, 3], tail=9),   # rows behind the last request
     dict(lens=[(37 * i) % 90 + 1 for i in range(150)], new=[min((37 * i) % 90 + 1, i % 5) for i in range(150)], Hq=2),
     dict(lens=[1100], new=[1100], Hq=4, Hkv=2),  # a whole prompt
+    dict(lens=[600, 100], new=[2, 5], Hq=130, Hkv=1, D=64),  # more heads than a tile has rows
+    dict(lens=[2000, 700, 2600], new=[1400, 30, 513], Hq=2, Hkv=1, D=64),  # ranges of queries
     dict(lens=[1029], new=[1029], Hq=3, Hkv=1, D=64, page=5, dtype="f16"),
 ]
 
@@ -120,9 +122,11 @@ def test_strides_of_queries_and_lse(four):
     assert torch.equal(pr.run(a, q=fused[:, 3:11]), w)
     assert torch.equal(pr.run(a, q=pr.q.cuda().transpose(0, 1).contiguous().transpose(0, 1)), w)
     assert torch.equal(pr.run(a, lse=pr.lse.cuda().t().contiguous().t()), w)
-    one = pr.q[:1].cuda().expand(52, 8, 128)
-    same = pr.q[:1].expand(52, 8, 128).contiguous().cuda()
-    assert torch.equal(pr.run(a, q=one), pr.run(a, q=same))
+    pr.q = pr.q[:1].expand(52, 8, 128)  # one query for all tokens, and one for all heads too
+    pr.check(pr.run(a, q=pr.q[:1].cuda().expand(52, 8, 128)), what="a token's stride of 0")
+    pr.q = pr.q[:, :1].expand(52, 8, 128)
+    pr.check(pr.run(a, q=pr.q[:1, :1].cuda().expand(52, 8, 128)), what="strides of 0")
+    pr.check(pr.run(a, q=pr.q[:, :1].contiguous().cuda().expand(52, 8, 128)), what="a head's stride of 0")
     check_status(a)
 
 

@@ -29,7 +29,7 @@ BINDING = os.path.join(BUILD, "_attn_binding.so")
 SOURCES = ["attn_api.cu", "prefill_bf16.cu", "prefill_d64.cu", "decode_bf16.cu", "simt_f32.cu",
            "varlen_sched.cu", "rope.cu", "append.cu", "append_e4m3.cu", "decode_e4m3.cu",
            "decode_e4m3_short.cu", "append_e2m1.cu", "decode_e2m1.cu", "decode_e2m1_short.cu",
-           "weights.cu", "evict.cu"]
+           "weights.cu", "weights_tiles.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
               "--expt-relaxed-constexpr", "-I", INCLUDE]

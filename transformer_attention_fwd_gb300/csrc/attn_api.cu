@@ -1202,6 +1202,27 @@ attn_status validate_pool(const void* kv_cache, const void* scales, bool four, c
     return ATTN_OK;
 }
 
+// Packed queries [total][Hq][D] at their strides, boxes of 64 elements x a KV head's query heads x
+// `tokens` tokens, 128-byte swizzle, zeros past the last token.
+attn_status make_query_map(const WeightsShape& s, int tokens, CUtensorMap* out) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(s.D), static_cast<cuuint64_t>(s.Hq),
+                                static_cast<cuuint64_t>(s.total)};
+    // A dimension of one entry has no stride: any serves.
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.Hq == 1 ? s.D : s.q_head) * 2,
+                                   static_cast<cuuint64_t>(s.total == 1 ? s.D : s.q_token) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(s.Hq / s.Hkv), static_cast<cuuint32_t>(tokens)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(out, s.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                          const_cast<void*>(s.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+    return ATTN_OK;
+}
+
 attn_status run_weights(bool four, const attn_rows* q, const float* lse, long long lse_head, long long lse_token,
                         const void* kv_cache, const void* scales, const float* factors, const int* block_table,
                         const int* cu_seqlens, const int* seq_lens, float* weights, int B, int total, int Hkv, int D,
@@ -1260,7 +1281,27 @@ attn_status run_weights(bool four, const attn_rows* q, const float* lse, long lo
     s.scale = scale;
     s.f16 = dtype == ATTN_F16 ? 1 : 0;
     int grid = 0, kernels = 0;
-    const cudaError_t e = launch_weights_paged(s, env, &grid, &kernels);
+    cudaError_t e = cudaSuccess;
+    // TMA reads the queries where their strides are real (a broadcast has stride 0).
+    const int group = s.Hq / s.Hkv, tokens = weights_tile_tokens(group);
+    if (tokens > 0 && (s.Hq == 1 || s.q_head > 0) && (total == 1 || s.q_token > 0)) {
+        CUtensorMap map;
+        if ((st = make_query_map(s, tokens, &map)) != ATTN_OK) return st;
+        const size_t bytes = weights_workspace_bytes(s);
+        void* ws = nullptr;
+        if (bytes > 0) e = workspace_alloc(&ws, bytes, env);
+        if (e != cudaSuccess || (bytes > 0 && ws == nullptr)) {
+            cudaGetLastError();
+            return fail(ATTN_ERR_NO_MEMORY, "weights workspace of %zu bytes: %s", bytes, cudaGetErrorString(e));
+        }
+        e = launch_weights_tiles(s, map, ws, env, &grid, &kernels);
+        if (ws) {
+            const cudaError_t f = cudaFreeAsync(ws, env.stream);
+            if (e == cudaSuccess && f != cudaSuccess) e = f;
+        }
+    } else {
+        e = launch_weights_paged(s, env, &grid, &kernels);
+    }
     if (e == cudaErrorInvalidConfiguration) return fail(ATTN_ERR_UNSUPPORTED, "too many requests or heads for one launch");
     if (e != cudaSuccess) return cuda_fail(e, "weights launch");
     record_launch(grid, 0, kernels);

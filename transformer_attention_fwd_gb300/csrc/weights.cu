@@ -20,6 +20,7 @@
 #include "e2m1.cuh"
 #include "pdl.cuh"
 #include "sm100.cuh"
+#include "weights.cuh"
 
 namespace attn {
 namespace {
@@ -27,23 +28,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kWarpKeys = 32;
 constexpr int kBlockKeys = kWarps * kWarpKeys;
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct WeightsParams {
-    const uint16_t* q;
-    long long q_token, q_head;
-    const float* lse;
-    long long lse_head, lse_token;
-    const uint8_t* cache;
-    const uint8_t* scales;
-    const float* factors;
-    const int *block_table, *cu, *lens;
-    float* weights;
-    unsigned* status;
-    PageDivider page;
-    int B, total, Hq, Hkv, group, max_pages, num_blocks;
-    float scale_log2;
-};
 
 template <bool kF16>
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -105,14 +89,12 @@ weights_kernel(const WeightsParams p) {
     grid_launch_next();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
     const int hkv = blockIdx.y, b = blockIdx.z;
-    const int asked = p.lens[b], most = p.max_pages * p.page.size;
-    const int begin = p.cu[b], end = p.cu[b + 1];
-    const bool ok = begin >= 0 && begin <= end && end <= p.total && asked >= end - begin && asked <= most;
-    if (!ok) {
+    const WeightsRequest r = weights_request(p, b);
+    if (!r.ok) {
         if (blockIdx.x == 0 && hkv == 0 && threadIdx.x == 0) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
         return;
     }
-    const int len = asked, n = end - begin;
+    const int len = r.len, begin = r.begin, n = r.end - r.begin;
     const int key0 = blockIdx.x * kBlockKeys + warp * kWarpKeys;
     if (n == 0 || key0 >= len) return;
 
@@ -144,15 +126,15 @@ weights_kernel(const WeightsParams p) {
     const int rows = n * p.group;  // checked on the host: fits
     const int first_token = max(0, key0 - (len - n));
     for (int r0 = first_token * p.group / 8 * 8; r0 < rows; r0 += 8) {
-        const int r = r0 + g;
+        const int mine = r0 + g;
         uint32_t qb[D / 8];
         {
-            const int token = r / p.group, head = r - token * p.group;
+            const int token = mine / p.group, head = mine - token * p.group;
             const uint4* src = reinterpret_cast<const uint4*>(p.q + (begin + token) * p.q_token +
                                                               (hkv * p.group + head) * p.q_head + t * (D / 4));
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                const uint4 u = r < rows ? src[i] : make_uint4(0, 0, 0, 0);
+                const uint4 u = mine < rows ? src[i] : make_uint4(0, 0, 0, 0);
                 qb[4 * i] = u.x; qb[4 * i + 1] = u.y; qb[4 * i + 2] = u.z; qb[4 * i + 3] = u.w;
             }
         }
@@ -164,7 +146,7 @@ weights_kernel(const WeightsParams p) {
             lse[i] = 0.0f;
             last[i] = -1;
             if (rr < rows) {
-                lse[i] = p.lse[(hkv * p.group + head) * p.lse_head + (begin + token) * p.lse_token] * kLog2e;
+                lse[i] = p.lse[(hkv * p.group + head) * p.lse_head + (begin + token) * p.lse_token] * kWeightsLog2e;
                 last[i] = lse[i] == -INFINITY ? -1 : len - n + token;
             }
         }
@@ -202,30 +184,7 @@ cudaError_t launch_type(const WeightsParams& p, dim3 grid, bool f16, cudaStream_
 }  // namespace
 
 cudaError_t launch_weights_paged(const WeightsShape& s, const LaunchEnv& env, int* grid_out, int* kernels_launched) {
-    WeightsParams p{};
-    p.q = static_cast<const uint16_t*>(s.q);
-    p.q_token = s.q_token;
-    p.q_head = s.q_head;
-    p.lse = s.lse;
-    p.lse_head = s.lse_head;
-    p.lse_token = s.lse_token;
-    p.cache = static_cast<const uint8_t*>(s.cache);
-    p.scales = s.scales;
-    p.factors = s.factors;
-    p.block_table = s.block_table;
-    p.cu = s.cu_seqlens;
-    p.lens = s.seq_lens;
-    p.weights = s.weights;
-    p.status = env.status;
-    p.page = PageDivider(s.page);
-    p.B = s.B;
-    p.total = s.total;
-    p.Hq = s.Hq;
-    p.Hkv = s.Hkv;
-    p.group = s.Hq / s.Hkv;
-    p.max_pages = s.max_pages;
-    p.num_blocks = s.num_blocks;
-    p.scale_log2 = s.scale * kLog2e;
+    const WeightsParams p = weights_params(s, env);
     const long long keys = static_cast<long long>(s.max_pages) * s.page;
     const dim3 grid(static_cast<unsigned>((keys + kBlockKeys - 1) / kBlockKeys), s.Hkv, s.B);
     if (s.Hkv > 65535 || s.B > 65535) return cudaErrorInvalidConfiguration;

@@ -1,0 +1,732 @@
+// weights_tiles.cu -- attention weights of packed queries added up over the keys of a
+// paged cache (weights.cu has the formula), on the 5th-generation tensor cores.
+//
+// S^T tiles of 128 keys (tensor-memory lanes) by 128 query rows (columns): a thread of
+// the sum warps owns a key and adds 2^(x - lse) over the columns, so nothing crosses
+// lanes, the probabilities never leave registers and each key's sum has a fixed order.
+//
+// A work item is 256 keys of one (request, KV head) with the queries that see them, at
+// most `range` tokens of them; a CTA per SM walks the items of all requests in a fixed
+// order.  A key's sums from several ranges go to a workspace, and a second kernel adds
+// them up in order.  Warps:
+//   0-7    sums: warps 0-3 keys 0-127 of the item, warps 4-7 keys 128-255
+//   8-11   K rows, page by page, into one of two buffers: 16-bit rows by asynchronous
+//          16-byte copies, 4-bit rows converted in registers (a code times its scale has
+//          six significant bits: exact in either 16-bit type)
+//   12     query tiles by TMA: whole tokens, a KV head's query heads within, read straight
+//          out of the caller's tensor (a box of 64 elements x heads x tokens)
+//   13     tensor memory, and all MMAs: for each query tile one 128 x 128 x D product for
+//          each half of the keys, into one of two accumulators each
+//   14     the rows' -lse into shared memory
+// Every wait is bounded (sm100.cuh).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "attn_internal.h"
+#include "e2m1.cuh"
+#include "pdl.cuh"
+#include "prefill_common.cuh"
+#include "sm100.cuh"
+#include "weights.cuh"
+
+namespace attn {
+namespace {
+
+using prefill::align1024;
+using prefill::desc_advance;
+using prefill::issue_qk;
+using prefill::kDrainLimitNs;
+using prefill::wait_quiet;
+using prefill::warp_wait;
+
+constexpr int kKeys = 256;  // of an item
+constexpr int kHalf = 128;  // keys of an MMA
+constexpr int kCols = 128;  // query rows of a tile
+constexpr int kQStages = 3, kKStages = 2, kSBufs = 2;
+constexpr int kSumWarps = 8, kLoadWarps = 4;
+constexpr int kLoadWarp0 = kSumWarps, kQWarp = 12, kMmaWarp = 13;  // and the last: -lse
+constexpr int kThreads = 15 * 32;
+constexpr uint32_t kTmemCols = 512;
+
+enum : unsigned {
+    SITE_W_K_EMPTY = 48, SITE_W_K_FULL, SITE_W_Q_EMPTY, SITE_W_Q_FULL, SITE_W_L_EMPTY, SITE_W_L_FULL,
+    SITE_W_S_EMPTY, SITE_W_S_FULL
+};
+
+struct Control {
+    uint64_t k_full[kKStages], k_empty[kKStages];
+    uint64_t q_full[kQStages], q_empty[kQStages];
+    uint64_t l_full[kQStages], l_empty[kQStages];
+    uint64_t s_full[2][kSBufs], s_empty[2][kSBufs];  // [half of the keys]
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    alignas(16) float nlse[kQStages][kCols];  // -log2(e) lse of a tile's rows
+    alignas(16) uint8_t token[kCols];         // of a tile's rows, from the tile's first
+};
+
+template <int D>
+struct Layout {
+    static constexpr int kTile = kHalf * D * 2;  // 128 rows: D / 64 boxes of 128 rows x 128 bytes
+    static constexpr int kK = 0;
+    static constexpr int kQ = kK + kKStages * 2 * kTile;
+    static constexpr int kControl = kQ + kQStages * kTile;
+    static constexpr int kBytes = kControl + 2048 + 1024;  // and alignment
+    static_assert(sizeof(Control) <= 2048, "control block");
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+struct TilesParams {
+    WeightsParams w;
+    float* partial;       // [slots, Hkv, keys] sums of ranges, or null: no request has several
+    long long keys;       // max_pages * page
+    int range;            // tokens of an item, a multiple of kKeys
+    int tile_tokens;      // tokens of a query tile
+    unsigned long long limit_ns;
+};
+
+// Blocks of keys that all n queries see, all blocks, and the items of one KV head: block kb has
+// range_count() of them.  The last n - ... keys are seen by fewer queries block by block:
+// their counts, from the last block on, are floor(j / m) + 1 with m = range / kKeys.
+struct Counts {
+    int blocks, flat, ranges, m;
+    __device__ __forceinline__ Counts(const TilesParams& p, int len, int n) : m(p.range / kKeys) {
+        blocks = (len + kKeys - 1) / kKeys;
+        flat = min(blocks, (len - n) / kKeys + 1);
+        ranges = (n + p.range - 1) / p.range;
+    }
+    __device__ __forceinline__ long long tail(int j) const {  // items of the last j blocks
+        const int a = j / m, c = j - a * m;
+        return j + static_cast<long long>(m) * a * (a - 1) / 2 + static_cast<long long>(a) * c;
+    }
+    __device__ __forceinline__ long long items() const {
+        return static_cast<long long>(flat) * ranges + tail(blocks - flat);
+    }
+    // Item i: its block and range.
+    __device__ __forceinline__ void find(long long i, int* kb, int* r) const {
+        if (i < static_cast<long long>(flat) * ranges) {
+            *kb = static_cast<int>(i / ranges);
+            *r = static_cast<int>(i - static_cast<long long>(*kb) * ranges);
+            return;
+        }
+        i -= static_cast<long long>(flat) * ranges;
+        int lo = 0, hi = blocks - flat - 1;  // the last j with tail(j) <= i
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (tail(mid) <= i) lo = mid; else hi = mid - 1;
+        }
+        *kb = blocks - 1 - lo;
+        *r = static_cast<int>(i - tail(lo));
+    }
+};
+
+struct Item {
+    int b, hkv, begin, n, len;
+    int key0;      // first key
+    int t0, t1;    // tokens of the item, counted from the request's first query
+    int slot;      // of the partial sums; -1: none
+};
+
+// This CTA's items one after the other; every call by a whole warp.  32 requests are looked at
+// at a time, a lane each.
+struct Items {
+    const TilesParams& p;
+    const int lane;
+    long long next, base = 0, incl = 0, chunk = 0;  // items before the lanes' requests; their prefix; all of them
+    int first = -32, begin = 0, n = 0, len = 0, slots = 0, slot_base = 0;
+    __device__ __forceinline__ Items(const TilesParams& params, int lane_id)
+        : p(params), lane(lane_id), next(blockIdx.x) {}
+
+    __device__ __forceinline__ void look() {
+        base += chunk;
+        slot_base += __shfl_sync(0xffffffffu, slots, 31);
+        first += 32;
+        const int b = first + lane;
+        long long count = 0;
+        int own_slots = 0;
+        if (b < p.w.B) {
+            const WeightsRequest r = weights_request(p.w, b);
+            begin = r.begin;
+            n = r.ok ? r.end - r.begin : 0;
+            len = r.len;
+            if (!r.ok && blockIdx.x == 0) atomicOr(p.w.status, ATTN_DEV_BAD_INPUT);
+            if (n > 0) {
+                const Counts c(p, len, n);
+                count = c.items() * p.w.Hkv;
+                if (c.ranges > 1) own_slots = c.ranges;
+            }
+        }
+        incl = count;
+        slots = own_slots;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            const int y = __shfl_up_sync(0xffffffffu, slots, o);
+            if (lane >= o) {
+                incl += x;
+                slots += y;
+            }
+        }
+        chunk = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    __device__ __forceinline__ bool take(Item& it) {
+        while (next - base >= chunk) {
+            if (first + 32 >= p.w.B) return false;
+            look();
+        }
+        const int at = __popc(__ballot_sync(0xffffffffu, incl <= next - base));  // the request's lane
+        const long long before = __shfl_sync(0xffffffffu, incl, max(at - 1, 0));
+        const int slots_before = __shfl_sync(0xffffffffu, slots, max(at - 1, 0));
+        it.b = first + at;
+        it.begin = __shfl_sync(0xffffffffu, begin, at);
+        it.n = __shfl_sync(0xffffffffu, n, at);
+        it.len = __shfl_sync(0xffffffffu, len, at);
+        const Counts c(p, it.len, it.n);
+        const long long i = next - base - (at > 0 ? before : 0), per = c.items();
+        it.hkv = static_cast<int>(i / per);
+        int kb, r;
+        c.find(i - it.hkv * per, &kb, &r);
+        it.key0 = kb * kKeys;
+        it.t0 = max(0, it.key0 - (it.len - it.n)) + r * p.range;
+        it.t1 = min(it.n, it.t0 + p.range);
+        it.slot = c.ranges > 1 ? slot_base + (at > 0 ? slots_before : 0) + r : -1;
+        next += gridDim.x;
+        return true;
+    }
+};
+
+// 64 keys of an item for one of four warps: two lanes' worth of slots, looked up ahead.
+struct RowIds {
+    int64_t row[2];  // of keys lane and lane + 32 in the pool of rows; negative: none
+    __device__ __forceinline__ void find(const WeightsParams& p, const Item& it, int first, int lane) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int key = first + lane + 32 * i;
+            row[i] = -1;
+            if (key >= it.len) continue;
+            int in_page;
+            const int id = p.block_table[static_cast<int64_t>(it.b) * p.max_pages + p.page.split(key, &in_page)];
+            if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks))
+                row[i] = (static_cast<int64_t>(id) * 2 * p.Hkv + it.hkv) * p.page.size + in_page;
+            else
+                atomicOr(p.status, ATTN_DEV_BAD_INPUT);
+        }
+    }
+    // Of key i of the 64.
+    __device__ __forceinline__ int64_t of(int i) const {
+        const int64_t a = __shfl_sync(0xffffffffu, row[0], i & 31), b = __shfl_sync(0xffffffffu, row[1], i & 31);
+        return i < 32 ? a : b;
+    }
+};
+
+// Byte of 16-byte chunk c of key k in a K buffer: 128-byte rows, swizzled by the row.
+template <int D>
+__device__ __forceinline__ uint32_t key_chunk(int k, int c) {
+    return static_cast<uint32_t>((k / kHalf) * Layout<D>::kTile + (c >> 3) * (kHalf * 128) + (k % kHalf) * 128 +
+                                 (((c & 7) ^ (k & 7)) << 4));
+}
+
+template <int D>
+__device__ void load_rows16(const TilesParams& p, uint8_t* smem, Control* ctl, int warp, int lane, const WaitGuard& g) {
+    constexpr int kPer = D / 8;           // chunks of a row
+    constexpr int kRowsPer = 32 / kPer;   // rows of a warp's copy
+    const uint32_t buffers = smem_u32(smem + Layout<D>::kK);
+    const int c = lane % kPer;
+    Items items(p, lane);
+    Item it;
+    uint32_t k_it = 0;
+    bool waiting = false;  // the copies before have not been handed over
+    auto hand_over = [&](uint32_t n) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->k_full[n % kKStages]);
+    };
+    while (items.take(it)) {
+        RowIds ids;
+        ids.find(p.w, it, it.key0 + warp * 64, lane);
+        const uint32_t s = k_it % kKStages;
+        if (k_it >= kKStages) {
+            const uint32_t parity = ((k_it / kKStages) & 1) ^ 1;
+            if (waiting && !__all_sync(0xffffffffu, mbar_try_wait(&ctl->k_empty[s], parity))) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                hand_over(k_it - 1);
+                waiting = false;
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(&ctl->k_empty[s], parity, g, SITE_W_K_EMPTY))) break;
+        }
+        const uint32_t to = buffers + s * 2 * Layout<D>::kTile;
+#pragma unroll 8
+        for (int i = 0; i < 64 / kRowsPer; ++i) {
+            const int r = i * kRowsPer + lane / kPer;
+            const int64_t row = ids.of(r);
+            const uint8_t* src = p.w.cache + (row < 0 ? 0 : row) * (D * 2) + c * 16;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                         :: "r"(to + key_chunk<D>(warp * 64 + r, c)), "l"(src), "r"(row < 0 ? 0 : 16) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (waiting) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            hand_over(k_it - 1);
+        }
+        waiting = true;
+        ++k_it;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (waiting) hand_over(k_it - 1);
+}
+
+template <int D, bool kF16>
+__device__ void load_rows4(const TilesParams& p, uint8_t* smem, Control* ctl, int warp, int lane, const WaitGuard& g) {
+    constexpr int kPer = D / 32;         // lanes of a row: 32 elements each
+    constexpr int kRowsPer = 32 / kPer;
+    constexpr int kSteps = 64 / kRowsPer;
+    uint8_t* buffers = smem + Layout<D>::kK;
+    const int part = lane % kPer;
+    Items items(p, lane);
+    Item it;
+    uint32_t k_it = 0;
+    while (items.take(it)) {
+        RowIds ids;
+        ids.find(p.w, it, it.key0 + warp * 64, lane);
+        uint4 codes[kSteps];
+        uint32_t scales[kSteps];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int64_t row = ids.of(i * kRowsPer + lane / kPer);
+            codes[i] = make_uint4(0, 0, 0, 0);
+            scales[i] = 0;
+            if (row >= 0) {
+                codes[i] = *reinterpret_cast<const uint4*>(p.w.cache + row * (D / 2) + part * 16);
+                scales[i] = *reinterpret_cast<const uint16_t*>(p.w.scales + row * (D / kRowScaleSpan) + part * 2);
+            }
+        }
+        const uint32_t s = k_it % kKStages;
+        if (k_it >= kKStages &&
+            !__all_sync(0xffffffffu, mbar_wait(&ctl->k_empty[s], ((k_it / kKStages) & 1) ^ 1, g, SITE_W_K_EMPTY)))
+            return;
+        uint8_t* to = buffers + s * 2 * Layout<D>::kTile;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int k = warp * 64 + i * kRowsPer + lane / kPer;
+            const uint32_t f = e4m3_to_f16x2(scales[i]);
+            const uint32_t by[2] = {__byte_perm(f, f, 0x1010), __byte_perm(f, f, 0x3232)};
+            const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t v[4];
+                e2m1_to_f16x8(w[j], v);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    v[x] = f16x2_mul(v[x], by[j / 2]);
+                    if (!kF16) v[x] = pack_bf16x2(f16_lo_to_f32(v[x]), f16_hi_to_f32(v[x]));
+                }
+                *reinterpret_cast<uint4*>(to + key_chunk<D>(k, part * 4 + j)) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->k_full[s]);
+        ++k_it;
+    }
+}
+
+template <int D>
+__device__ void load_queries(const TilesParams& p, const CUtensorMap* tmQ, uint8_t* smem, Control* ctl, int lane,
+                             const WaitGuard& g) {
+    const uint32_t bytes = static_cast<uint32_t>(p.tile_tokens * p.w.group) * D * 2;
+    Items items(p, lane);
+    Item it;
+    uint32_t q_it = 0;
+    bool ok = true;
+    while (ok && items.take(it)) {
+        for (int t = it.t0; t < it.t1; t += p.tile_tokens, ++q_it) {
+            const uint32_t s = q_it % kQStages;
+            if (q_it >= kQStages) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl->q_empty[s], ((q_it / kQStages) & 1) ^ 1, g, SITE_W_Q_EMPTY));
+                if (!ok) break;
+            }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&ctl->q_full[s], bytes);
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                    tma_load_3d(smem + Layout<D>::kQ + s * Layout<D>::kTile + h * (kCols * 128), tmQ, &ctl->q_full[s],
+                                h * 64, it.hkv * p.w.group, it.begin + t);
+            }
+        }
+    }
+    // Copies in flight land before the CTA leaves (they have, but for an abort elsewhere).
+    if (lane == 0)
+        for (uint32_t i = q_it > kQStages ? q_it - kQStages : 0; i < q_it; ++i)
+            wait_quiet(&ctl->q_full[i % kQStages], (i / kQStages) & 1, kDrainLimitNs);
+}
+
+__device__ void load_lse(const TilesParams& p, Control* ctl, int lane, const WaitGuard& g) {
+    const WeightsParams& w = p.w;
+    // This lane's rows of a tile: lane, lane + 32, ..
+    int token[kCols / 32];
+    long long head_at[kCols / 32];
+#pragma unroll
+    for (int i = 0; i < kCols / 32; ++i) {
+        const int row = lane + 32 * i;
+        token[i] = row / w.group;
+        head_at[i] = (row - token[i] * w.group) * w.lse_head;
+    }
+    auto load = [&](const Item& it, int t, float (&v)[kCols / 32]) {
+#pragma unroll
+        for (int i = 0; i < kCols / 32; ++i) {
+            v[i] = INFINITY;
+            if (token[i] < p.tile_tokens && t + token[i] < it.t1)
+                v[i] = w.lse[it.hkv * w.group * w.lse_head + head_at[i] + (it.begin + t + token[i]) * w.lse_token];
+        }
+    };
+    Items items(p, lane);
+    Item it{};
+    uint32_t l_it = 0;
+    bool more = items.take(it);
+    int t = it.t0;
+    float next[kCols / 32];
+    if (more) load(it, t, next);
+    while (more) {
+        float v[kCols / 32];
+#pragma unroll
+        for (int i = 0; i < kCols / 32; ++i) v[i] = next[i];
+        t += p.tile_tokens;
+        if (t >= it.t1) {
+            more = items.take(it);
+            t = it.t0;
+        }
+        if (more) load(it, t, next);
+        const uint32_t s = l_it % kQStages;
+        if (l_it >= kQStages &&
+            !__all_sync(0xffffffffu, mbar_wait(&ctl->l_empty[s], ((l_it / kQStages) & 1) ^ 1, g, SITE_W_L_EMPTY)))
+            return;
+#pragma unroll
+        for (int i = 0; i < kCols / 32; ++i)  // a row that saw nothing (-inf) adds nothing
+            ctl->nlse[s][lane + 32 * i] = v[i] == -INFINITY ? -INFINITY : -v[i] * kWeightsLog2e;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->l_full[s]);
+        ++l_it;
+    }
+}
+
+template <int D, bool kF16>
+__device__ void issue_mmas(const TilesParams& p, uint8_t* smem, Control* ctl, uint32_t tmem, int lane,
+                           const WaitGuard& g) {
+    constexpr uint32_t kTile16 = Layout<D>::kTile >> 4;
+    const uint64_t k0 = smem_desc_sw128(smem_u32(smem + Layout<D>::kK), 16, 1024);
+    const uint64_t q0 = smem_desc_sw128(smem_u32(smem + Layout<D>::kQ), 16, 1024);
+    const uint32_t leader = elect_leader();
+    Items items(p, lane);
+    Item it;
+    uint32_t k_it = 0, q_it = 0, s_it[2] = {0, 0};
+    bool ok = true;
+    while (ok && items.take(it)) {
+        const uint32_t ks = k_it % kKStages;
+        const int halves = it.key0 + kHalf < it.len ? 2 : 1;
+        ok = warp_wait(&ctl->k_full[ks], (k_it / kKStages) & 1, g, SITE_W_K_FULL);
+        for (int t = it.t0; ok && t < it.t1; t += p.tile_tokens, ++q_it) {
+            const uint32_t qs = q_it % kQStages;
+            ok = warp_wait(&ctl->q_full[qs], (q_it / kQStages) & 1, g, SITE_W_Q_FULL);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!ok || h >= halves) continue;
+                const uint32_t buf = s_it[h] % kSBufs;
+                if (s_it[h] >= kSBufs)
+                    ok = warp_wait(&ctl->s_empty[h][buf], ((s_it[h] / kSBufs) & 1) ^ 1, g, SITE_W_S_EMPTY);
+                if (!ok) continue;
+                tc_fence_after_sync();
+                issue_qk<D, kF16>(tmem + (h * kSBufs + buf) * kCols, desc_advance(k0, (ks * 2 + h) * kTile16),
+                                  desc_advance(q0, qs * kTile16), leader);
+                mma_commit(&ctl->s_full[h][buf], leader);
+                ++s_it[h];
+            }
+            mma_commit(&ctl->q_empty[qs], leader);
+        }
+        mma_commit(&ctl->k_empty[ks], leader);
+        ++k_it;
+    }
+    // Every MMA issued so far is done before tensor memory is released.
+    mma_commit(&ctl->drain, leader);
+    wait_quiet(&ctl->drain, 0, kDrainLimitNs);
+}
+
+// 32 columns of a key: adds 2^(x sc + nl) of all of them.
+__device__ __forceinline__ void add_columns(const uint32_t (&s)[32], const float* nl, uint64_t sc2, uint64_t (&acc)[2]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 l = reinterpret_cast<const float4*>(nl)[i];
+        const uint64_t l2[2] = {f2_pack(l.x, l.y), f2_pack(l.z, l.w)};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float x, y;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[4 * i + 2 * k]), __uint_as_float(s[4 * i + 2 * k + 1])), sc2, l2[k]),
+                      x, y);
+            acc[k] = f2_add(acc[k], f2_pack(ex2_approx(x), ex2_approx(y)));
+        }
+    }
+}
+// The same of those whose token is at least `from` and whose place is below `valid`.
+__device__ __forceinline__ void add_some_columns(const uint32_t (&s)[32], const float* nl, const uint8_t* token, float sc,
+                                                 int from, int valid, uint64_t (&acc)[2]) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float e = ex2_approx(fmaf(__uint_as_float(s[i]), sc, nl[i]));
+        sum += i < valid && token[i] >= from ? e : 0.0f;
+    }
+    acc[0] = f2_add(acc[0], f2_pack(sum, 0.0f));
+}
+
+__device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int warp, int lane, const WaitGuard& g) {
+    const WeightsParams& w = p.w;
+    const int half = warp / 4, quarter = warp % 4;
+    const uint32_t lanes = tmem_lane_base(tmem, warp) + half * kSBufs * kCols;
+    Items items(p, lane);
+    Item it;
+    uint32_t s_it = 0, l_it = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, g, site)) != 0;
+    };
+    while (items.take(it)) {
+        const int first = it.key0 + half * kHalf, key = first + quarter * 32 + lane;
+        if (first >= it.len) {  // no keys in this half: the tiles' rows pass by
+            for (int t = it.t0; t < it.t1; t += p.tile_tokens, ++l_it) {
+                const uint32_t s = l_it % kQStages;
+                if (!wait(&ctl->l_full[s], (l_it / kQStages) & 1, SITE_W_L_FULL)) return;
+                if (lane == 0) mbar_arrive(&ctl->l_empty[s]);
+            }
+            continue;
+        }
+        float* to = nullptr;
+        if (key < it.len) {
+            if (it.slot >= 0) {
+                to = p.partial + (static_cast<int64_t>(it.slot) * w.Hkv + it.hkv) * p.keys + key;
+            } else {
+                int in_page;
+                const int id = w.block_table[static_cast<int64_t>(it.b) * w.max_pages + w.page.split(key, &in_page)];
+                if (static_cast<unsigned>(id) < static_cast<unsigned>(w.num_blocks))
+                    to = w.weights + (static_cast<int64_t>(id) * w.Hkv + it.hkv) * w.page.size + in_page;
+            }
+        }
+        const float sc = w.scale_log2 * (w.factors ? w.factors[it.hkv] : 1.0f);
+        const uint64_t sc2 = f2_pack(sc, sc);
+        float sum = 0.0f;
+        for (int t = it.t0; t < it.t1; t += p.tile_tokens, ++l_it, ++s_it) {
+            const uint32_t ls = l_it % kQStages, buf = s_it % kSBufs;
+            const int valid = min(p.tile_tokens, it.t1 - t) * w.group;
+            // Token t sees keys up to len - n + t; this key is seen from token `from` of the tile on.
+            const int from = key - (it.len - it.n) - t;
+            const bool all = quarter * 32 + 31 + first - (it.len - it.n) <= t;  // by all tokens, every key of the warp
+            if (!wait(&ctl->l_full[ls], (l_it / kQStages) & 1, SITE_W_L_FULL)) return;
+            if (!wait(&ctl->s_full[half][buf], (s_it / kSBufs) & 1, SITE_W_S_FULL)) return;
+            tc_fence_after_sync();
+            uint64_t acc[2] = {0, 0};
+            uint32_t a[32], b[32];
+            const uint32_t at = lanes + buf * kCols;
+            auto add = [&](const uint32_t (&s)[32], int c) {
+                if (all && valid >= c + 32) add_columns(s, ctl->nlse[ls] + c, sc2, acc);
+                else add_some_columns(s, ctl->nlse[ls] + c, ctl->token + c, sc, from, valid - c, acc);
+            };
+            tmem_ld32(at, a);
+            tmem_wait_ld(a);
+            if (valid > 32) tmem_ld32(at + 32, b);
+            add(a, 0);
+            if (valid > 32) {
+                tmem_wait_ld(b);
+                if (valid > 64) tmem_ld32(at + 64, a);
+                add(b, 32);
+            }
+            if (valid > 64) {
+                tmem_wait_ld(a);
+                if (valid > 96) tmem_ld32(at + 96, b);
+                add(a, 64);
+            }
+            if (valid > 96) tmem_wait_ld(b);
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->s_empty[half][buf]);
+            if (valid > 96) add(b, 96);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->l_empty[ls]);
+            float x, y, u, v;
+            f2_unpack(acc[0], x, y);
+            f2_unpack(acc[1], u, v);
+            sum += (x + y) + (u + v);
+        }
+        if (to) {
+            if (it.slot >= 0) *to = sum;
+            else atomicAdd(to, sum);  // the only addition to this key in the call
+        }
+    }
+}
+
+template <int D, bool kF16, bool kFour>
+__global__ void __launch_bounds__(kThreads, 1)
+weights_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TilesParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align1024(smem_raw);
+    Control* ctl = reinterpret_cast<Control*>(smem + Layout<D>::kControl);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kKStages; ++i) {
+            mbar_init(&ctl->k_full[i], kLoadWarps);
+            mbar_init(&ctl->k_empty[i], 1);
+        }
+        for (int i = 0; i < kQStages; ++i) {
+            mbar_init(&ctl->q_full[i], 1);
+            mbar_init(&ctl->q_empty[i], 1);
+            mbar_init(&ctl->l_full[i], 1);
+            mbar_init(&ctl->l_empty[i], kSumWarps);
+        }
+        for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < kSBufs; ++i) {
+                mbar_init(&ctl->s_full[h][i], 1);
+                mbar_init(&ctl->s_empty[h][i], 4);
+            }
+        mbar_init(&ctl->drain, 1);
+        ctl->abort = 0;
+        fence_mbar_init();
+    }
+    // Rows of a query tile past its tokens stay zeros.
+    for (int i = threadIdx.x; i < kQStages * Layout<D>::kTile / 16; i += kThreads)
+        reinterpret_cast<uint4*>(smem + Layout<D>::kQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (threadIdx.x < kCols) ctl->token[threadIdx.x] = static_cast<uint8_t>(threadIdx.x / p.w.group);
+    if (warp == kQWarp && lane == 0) tma_prefetch_desc(&tmQ);
+    if (warp == kMmaWarp) {
+        tmem_alloc(&ctl->tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = ctl->tmem_base;
+    const WaitGuard g{p.w.status, &ctl->abort, p.limit_ns};
+    grid_wait();
+    grid_launch_next();
+
+    if (warp < kSumWarps) {
+        add_up(p, ctl, tmem, warp, lane, g);
+    } else if (warp < kLoadWarp0 + kLoadWarps) {
+        if constexpr (kFour) load_rows4<D, kF16>(p, smem, ctl, warp - kLoadWarp0, lane, g);
+        else load_rows16<D>(p, smem, ctl, warp - kLoadWarp0, lane, g);
+    } else if (warp == kQWarp) {
+        load_queries<D>(p, &tmQ, smem, ctl, lane, g);
+    } else if (warp == kMmaWarp) {
+        issue_mmas<D, kF16>(p, smem, ctl, tmem, lane, g);
+    } else {
+        load_lse(p, ctl, lane, g);
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Adds the partial sums of requests with several ranges, in their order.  Block (x, y, z): keys
+// of KV head y of requests z, z + gridDim.z, ..
+constexpr int kAddThreads = 256;
+
+__global__ void __launch_bounds__(kAddThreads) weights_ranges_kernel(const __grid_constant__ TilesParams p) {
+    __shared__ int s_base[kAddThreads / 32];
+    grid_wait();
+    grid_launch_next();
+    const int hkv = blockIdx.y;
+    for (int b = blockIdx.z; b < p.w.B; b += gridDim.z) {
+        const WeightsRequest r = weights_request(p.w, b);
+        const int n = r.ok ? r.end - r.begin : 0;
+        if (n <= p.range) continue;
+        // Slots of the requests before.
+        int base = 0;
+        for (int i = threadIdx.x; i < b; i += kAddThreads) {
+            const WeightsRequest q = weights_request(p.w, i);
+            const int m = q.ok ? q.end - q.begin : 0;
+            if (m > p.range) base += (m + p.range - 1) / p.range;
+        }
+        base = __reduce_add_sync(0xffffffffu, base);
+        __syncthreads();  // the request before has been read
+        if (threadIdx.x % 32 == 0) s_base[threadIdx.x / 32] = base;
+        __syncthreads();
+        base = 0;
+        for (int i = 0; i < kAddThreads / 32; ++i) base += s_base[i];
+        for (int key = blockIdx.x * kAddThreads + threadIdx.x; key < r.len; key += gridDim.x * kAddThreads) {
+            int in_page;
+            const int id = p.w.block_table[static_cast<int64_t>(b) * p.w.max_pages + p.w.page.split(key, &in_page)];
+            if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.w.num_blocks)) continue;  // reported
+            const int t0 = max(0, key / kKeys * kKeys - (r.len - n)), ranges = (n - t0 + p.range - 1) / p.range;
+            float sum = 0.0f;
+            for (int i = 0; i < ranges; ++i) sum += p.partial[(static_cast<int64_t>(base + i) * p.w.Hkv + hkv) * p.keys + key];
+            p.w.weights[(static_cast<int64_t>(id) * p.w.Hkv + hkv) * p.w.page.size + in_page] += sum;
+        }
+    }
+}
+
+// Tokens of an item: enough items for all SMs from two blocks of keys on, more where the
+// partial sums would not stay in the L2 (64 MB).
+constexpr long long kPartialBytes = 64ll << 20;
+int range_of(const WeightsShape& s) {
+    const long long keys = static_cast<long long>(s.max_pages) * s.page;
+    long long range = 2 * kKeys;
+    while (s.total > range && 2 * s.total / range * s.Hkv * keys * 4 > kPartialBytes) range *= 2;
+    return static_cast<int>(std::min(range, 1ll << 30));
+}
+long long partial_bytes(const WeightsShape& s) {
+    const int range = range_of(s);
+    if (s.total <= range) return 0;
+    // A request over `range` tokens has at most 2 n / range ranges.
+    return 2ll * s.total / range * s.Hkv * s.max_pages * s.page * 4;
+}
+
+template <int D, bool kF16, bool kFour>
+cudaError_t launch_tiles(const CUtensorMap& map, const TilesParams& p, int grid, const LaunchEnv& env) {
+    auto* kern = weights_tiles_kernel<D, kF16, kFour>;
+    static bool attr_set[64] = {};  // device < 64 (device_env)
+    if (!attr_set[env.device]) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
+        if (e != cudaSuccess) return e;
+        attr_set[env.device] = true;
+    }
+    return launch_serial(kern, dim3(grid), kThreads, Layout<D>::kBytes, env.stream, map, p);
+}
+
+template <int D>
+cudaError_t launch_types(const CUtensorMap& map, const TilesParams& p, bool f16, bool four, int grid, const LaunchEnv& env) {
+    if (four) return f16 ? launch_tiles<D, true, true>(map, p, grid, env) : launch_tiles<D, false, true>(map, p, grid, env);
+    return f16 ? launch_tiles<D, true, false>(map, p, grid, env) : launch_tiles<D, false, false>(map, p, grid, env);
+}
+
+}  // namespace
+
+int weights_tile_tokens(int group) { return group <= kCols ? kCols / group : 0; }
+
+size_t weights_workspace_bytes(const WeightsShape& s) { return static_cast<size_t>(partial_bytes(s)); }
+
+cudaError_t launch_weights_tiles(const WeightsShape& s, const CUtensorMap& queries, void* ws, const LaunchEnv& env,
+                                 int* grid_out, int* kernels_launched) {
+    TilesParams p{};
+    p.w = weights_params(s, env);
+    p.partial = static_cast<float*>(ws);
+    p.keys = static_cast<long long>(s.max_pages) * s.page;
+    p.range = range_of(s);
+    p.tile_tokens = weights_tile_tokens(p.w.group);
+    p.limit_ns = env.wait_limit_ns;
+    const int grid = env.num_sms;
+    *grid_out = grid;
+    *kernels_launched = ws ? 2 : 1;
+    const bool four = s.scales != nullptr, f16 = s.f16 != 0;
+    cudaError_t e = s.D == 64 ? launch_types<64>(queries, p, f16, four, grid, env)
+                              : launch_types<128>(queries, p, f16, four, grid, env);
+    if (e != cudaSuccess || !ws) return e;
+    const unsigned y = static_cast<unsigned>(s.Hkv), z = static_cast<unsigned>(std::min(s.B, 64));
+    const long long want = std::max(1ll, 8ll * env.num_sms / (static_cast<long long>(y) * z));
+    const unsigned x = static_cast<unsigned>(std::min(want, (p.keys + kAddThreads - 1) / kAddThreads));
+    return launch_serial(weights_ranges_kernel, dim3(x, y, z), kAddThreads, 0, env.stream, p);
+}
+
+}  // namespace attn
