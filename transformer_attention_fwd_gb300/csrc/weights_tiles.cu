@@ -42,7 +42,7 @@ using prefill::kDrainLimitNs;
 using prefill::wait_quiet;
 using prefill::warp_wait;
 
-constexpr int kKeys = 256;  // of an item
+constexpr int kKeyShift = 8, kKeys = 1 << kKeyShift;  // of an item
 constexpr int kHalf = 128;  // keys of an MMA
 constexpr int kCols = 128;  // query rows of a tile
 constexpr int kQStages = 3, kKStages = 2, kSBufs = 2;
@@ -65,7 +65,6 @@ struct Control {
     uint32_t tmem_base;
     int abort;
     alignas(16) float nlse[kQStages][kCols];  // -log2(e) lse of a tile's rows
-    alignas(16) uint8_t token[kCols];         // of a tile's rows, from the tile's first
 };
 
 template <int D>
@@ -83,7 +82,7 @@ struct TilesParams {
     WeightsParams w;
     float* partial;       // [slots, Hkv, keys] sums of ranges, or null: no request has several
     long long keys;       // max_pages * page
-    int range;            // tokens of an item, a multiple of kKeys
+    int range_shift;      // log2 of the tokens of an item
     int tile_tokens;      // tokens of a query tile
     unsigned long long limit_ns;
 };
@@ -92,34 +91,33 @@ struct TilesParams {
 // range_count() of them.  The last n - ... keys are seen by fewer queries block by block:
 // their counts, from the last block on, are floor(j / m) + 1 with m = range / kKeys.
 struct Counts {
-    int blocks, flat, ranges, m;
-    __device__ __forceinline__ Counts(const TilesParams& p, int len, int n) : m(p.range / kKeys) {
-        blocks = (len + kKeys - 1) / kKeys;
-        flat = min(blocks, (len - n) / kKeys + 1);
-        ranges = (n + p.range - 1) / p.range;
+    int blocks, flat, ranges, shift;  // m = 1 << shift
+    __device__ __forceinline__ Counts(const TilesParams& p, int len, int n) : shift(p.range_shift - kKeyShift) {
+        blocks = (len + kKeys - 1) >> kKeyShift;
+        flat = min(blocks, ((len - n) >> kKeyShift) + 1);
+        ranges = (n + (1 << p.range_shift) - 1) >> p.range_shift;
     }
-    __device__ __forceinline__ long long tail(int j) const {  // items of the last j blocks
-        const int a = j / m, c = j - a * m;
-        return j + static_cast<long long>(m) * a * (a - 1) / 2 + static_cast<long long>(a) * c;
+    // Items of the last j blocks.  (Items of a head fit in 31 bits: range_of().)
+    __device__ __forceinline__ int tail(int j) const {
+        const unsigned a = static_cast<unsigned>(j) >> shift, c = j - (a << shift);
+        return j + static_cast<int>(((a * (a - 1) / 2) << shift) + a * c);
     }
-    __device__ __forceinline__ long long items() const {
-        return static_cast<long long>(flat) * ranges + tail(blocks - flat);
-    }
+    __device__ __forceinline__ int items() const { return flat * ranges + tail(blocks - flat); }
     // Item i: its block and range.
-    __device__ __forceinline__ void find(long long i, int* kb, int* r) const {
-        if (i < static_cast<long long>(flat) * ranges) {
-            *kb = static_cast<int>(i / ranges);
-            *r = static_cast<int>(i - static_cast<long long>(*kb) * ranges);
+    __device__ __forceinline__ void find(int i, int* kb, int* r) const {
+        if (i < flat * ranges) {
+            *kb = ranges == 1 ? i : static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(ranges));
+            *r = i - *kb * ranges;
             return;
         }
-        i -= static_cast<long long>(flat) * ranges;
+        i -= flat * ranges;
         int lo = 0, hi = blocks - flat - 1;  // the last j with tail(j) <= i
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (tail(mid) <= i) lo = mid; else hi = mid - 1;
         }
         *kb = blocks - 1 - lo;
-        *r = static_cast<int>(i - tail(lo));
+        *r = i - tail(lo);
     }
 };
 
@@ -155,7 +153,7 @@ struct Items {
             if (!r.ok && blockIdx.x == 0) atomicOr(p.w.status, ATTN_DEV_BAD_INPUT);
             if (n > 0) {
                 const Counts c(p, len, n);
-                count = c.items() * p.w.Hkv;
+                count = static_cast<long long>(c.items()) * p.w.Hkv;
                 if (c.ranges > 1) own_slots = c.ranges;
             }
         }
@@ -185,13 +183,14 @@ struct Items {
         it.n = __shfl_sync(0xffffffffu, n, at);
         it.len = __shfl_sync(0xffffffffu, len, at);
         const Counts c(p, it.len, it.n);
-        const long long i = next - base - (at > 0 ? before : 0), per = c.items();
-        it.hkv = static_cast<int>(i / per);
+        const long long i = next - base - (at > 0 ? before : 0);
+        const int per = c.items();
+        it.hkv = (i >> 31) == 0 ? static_cast<int>(static_cast<unsigned>(i) / static_cast<unsigned>(per)) : static_cast<int>(i / per);
         int kb, r;
-        c.find(i - it.hkv * per, &kb, &r);
-        it.key0 = kb * kKeys;
-        it.t0 = max(0, it.key0 - (it.len - it.n)) + r * p.range;
-        it.t1 = min(it.n, it.t0 + p.range);
+        c.find(static_cast<int>(i - static_cast<long long>(it.hkv) * per), &kb, &r);
+        it.key0 = kb << kKeyShift;
+        it.t0 = max(0, it.key0 - (it.len - it.n)) + (r << p.range_shift);
+        it.t1 = min(it.n, it.t0 + (1 << p.range_shift));
         it.slot = c.ranges > 1 ? slot_base + (at > 0 ? slots_before : 0) + r : -1;
         next += gridDim.x;
         return true;
@@ -364,52 +363,67 @@ __device__ void load_queries(const TilesParams& p, const CUtensorMap* tmQ, uint8
 }
 
 __device__ void load_lse(const TilesParams& p, Control* ctl, int lane, const WaitGuard& g) {
+    constexpr int kOwn = kCols / 32;
     const WeightsParams& w = p.w;
     // This lane's rows of a tile: lane, lane + 32, ..
-    int token[kCols / 32];
-    long long head_at[kCols / 32];
+    int token[kOwn];
+    long long head_at[kOwn];
 #pragma unroll
-    for (int i = 0; i < kCols / 32; ++i) {
+    for (int i = 0; i < kOwn; ++i) {
         const int row = lane + 32 * i;
         token[i] = row / w.group;
         head_at[i] = (row - token[i] * w.group) * w.lse_head;
+        if (token[i] >= p.tile_tokens) token[i] = 1 << 30;  // no row
     }
-    auto load = [&](const Item& it, int t, float (&v)[kCols / 32]) {
-#pragma unroll
-        for (int i = 0; i < kCols / 32; ++i) {
-            v[i] = INFINITY;
-            if (token[i] < p.tile_tokens && t + token[i] < it.t1)
-                v[i] = w.lse[it.hkv * w.group * w.lse_head + head_at[i] + (it.begin + t + token[i]) * w.lse_token];
-        }
-    };
     Items items(p, lane);
     Item it{};
-    uint32_t l_it = 0;
     bool more = items.take(it);
     int t = it.t0;
-    float next[kCols / 32];
-    if (more) load(it, t, next);
-    while (more) {
-        float v[kCols / 32];
+    unsigned there[2] = {0, 0};  // which rows of the last two tiles asked for exist
+    uint32_t asked = 0, made = 0;
+    auto ask = [&]() -> bool {  // the next tile's copies; false: aborted
+        const uint32_t s = asked % kQStages;
+        there[1] = there[0];
+        there[0] = 0;
+        if (more) {
+            if (asked >= kQStages &&
+                !__all_sync(0xffffffffu, mbar_wait(&ctl->l_empty[s], ((asked / kQStages) & 1) ^ 1, g, SITE_W_L_EMPTY)))
+                return false;
+            const float* from = w.lse + it.hkv * w.group * w.lse_head + (it.begin + t) * w.lse_token;
 #pragma unroll
-        for (int i = 0; i < kCols / 32; ++i) v[i] = next[i];
-        t += p.tile_tokens;
-        if (t >= it.t1) {
-            more = items.take(it);
-            t = it.t0;
+            for (int i = 0; i < kOwn; ++i)
+                if (token[i] < it.t1 - t) {
+                    there[0] |= 1u << i;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                                 :: "r"(smem_u32(&ctl->nlse[s][lane + 32 * i])), "l"(from + head_at[i] + token[i] * w.lse_token)
+                                 : "memory");
+                }
+            ++asked;
+            t += p.tile_tokens;
+            if (t >= it.t1) {
+                more = items.take(it);
+                t = it.t0;
+            }
         }
-        if (more) load(it, t, next);
-        const uint32_t s = l_it % kQStages;
-        if (l_it >= kQStages &&
-            !__all_sync(0xffffffffu, mbar_wait(&ctl->l_empty[s], ((l_it / kQStages) & 1) ^ 1, g, SITE_W_L_EMPTY)))
-            return;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return true;
+    };
+    bool ok = ask();
+    while (ok && made < asked) {
+        ok = ask();  // one tile ahead
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const uint32_t s = made % kQStages;
 #pragma unroll
-        for (int i = 0; i < kCols / 32; ++i)  // a row that saw nothing (-inf) adds nothing
-            ctl->nlse[s][lane + 32 * i] = v[i] == -INFINITY ? -INFINITY : -v[i] * kWeightsLog2e;
+        for (int i = 0; i < kOwn; ++i) {  // a row that saw nothing (-inf) adds nothing, as no row does
+            float* at = &ctl->nlse[s][lane + 32 * i];
+            const float v = there[1] >> i & 1u ? *at : INFINITY;
+            *at = v == -INFINITY ? -INFINITY : -v * kWeightsLog2e;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->l_full[s]);
-        ++l_it;
+        ++made;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <int D, bool kF16>
@@ -468,16 +482,15 @@ __device__ __forceinline__ void add_columns(const uint32_t (&s)[32], const float
         }
     }
 }
-// The same of those whose token is at least `from` and whose place is below `valid`.
-__device__ __forceinline__ void add_some_columns(const uint32_t (&s)[32], const float* nl, const uint8_t* token, float sc,
-                                                 int from, int valid, uint64_t (&acc)[2]) {
+// The same of columns lo .. hi - 1 of them.
+__device__ __forceinline__ float add_some_columns(const uint32_t (&s)[32], const float* nl, float sc, int lo, int hi) {
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         const float e = ex2_approx(fmaf(__uint_as_float(s[i]), sc, nl[i]));
-        sum += i < valid && token[i] >= from ? e : 0.0f;
+        sum += i >= lo && i < hi ? e : 0.0f;
     }
-    acc[0] = f2_add(acc[0], f2_pack(sum, 0.0f));
+    return sum;
 }
 
 __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int warp, int lane, const WaitGuard& g) {
@@ -500,65 +513,70 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
             }
             continue;
         }
-        float* to = nullptr;
-        if (key < it.len) {
-            if (it.slot >= 0) {
-                to = p.partial + (static_cast<int64_t>(it.slot) * w.Hkv + it.hkv) * p.keys + key;
-            } else {
-                int in_page;
-                const int id = w.block_table[static_cast<int64_t>(it.b) * w.max_pages + w.page.split(key, &in_page)];
-                if (static_cast<unsigned>(id) < static_cast<unsigned>(w.num_blocks))
-                    to = w.weights + (static_cast<int64_t>(id) * w.Hkv + it.hkv) * w.page.size + in_page;
-            }
-        }
+        int in_page;  // (the id is looked at once the sums are there)
+        const int page = w.page.split(min(key, it.len - 1), &in_page);
+        const int id = w.block_table[static_cast<int64_t>(it.b) * w.max_pages + page];
         const float sc = w.scale_log2 * (w.factors ? w.factors[it.hkv] : 1.0f);
         const uint64_t sc2 = f2_pack(sc, sc);
         float sum = 0.0f;
         for (int t = it.t0; t < it.t1; t += p.tile_tokens, ++l_it, ++s_it) {
             const uint32_t ls = l_it % kQStages, buf = s_it % kSBufs;
             const int valid = min(p.tile_tokens, it.t1 - t) * w.group;
-            // Token t sees keys up to len - n + t; this key is seen from token `from` of the tile on.
-            const int from = key - (it.len - it.n) - t;
-            const bool all = quarter * 32 + 31 + first - (it.len - it.n) <= t;  // by all tokens, every key of the warp
+            // Token t sees keys up to len - n + t: this key is seen from column lo on, the warp's
+            // first key from lo_warp on.
+            const int past = it.len - it.n + t;
+            const int lo = (key - past) * w.group, lo_warp = (first + quarter * 32 - past) * w.group;
+            const bool whole = (first + quarter * 32 + 31 <= past) && (valid & 31) == 0;
             if (!wait(&ctl->l_full[ls], (l_it / kQStages) & 1, SITE_W_L_FULL)) return;
             if (!wait(&ctl->s_full[half][buf], (s_it / kSBufs) & 1, SITE_W_S_FULL)) return;
             tc_fence_after_sync();
-            uint64_t acc[2] = {0, 0};
-            uint32_t a[32], b[32];
             const uint32_t at = lanes + buf * kCols;
-            auto add = [&](const uint32_t (&s)[32], int c) {
-                if (all && valid >= c + 32) add_columns(s, ctl->nlse[ls] + c, sc2, acc);
-                else add_some_columns(s, ctl->nlse[ls] + c, ctl->token + c, sc, from, valid - c, acc);
+            const float* nl = ctl->nlse[ls];
+            auto read = [&]() {  // the accumulator has been read
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->s_empty[half][buf]);
             };
-            tmem_ld32(at, a);
-            tmem_wait_ld(a);
-            if (valid > 32) tmem_ld32(at + 32, b);
-            add(a, 0);
-            if (valid > 32) {
-                tmem_wait_ld(b);
-                if (valid > 64) tmem_ld32(at + 64, a);
-                add(b, 32);
+            if (whole) {
+                uint64_t acc[2] = {0, 0};
+                uint32_t a[32], b[32];
+                tmem_ld32(at, a);
+#pragma unroll 1  // (unrolled, with the other path behind each chunk, the loop outgrew the instruction caches: 58 us of 124)
+                for (int c = 0; c < valid; c += 64) {
+                    tmem_wait_ld(a);
+                    if (c + 32 < valid) tmem_ld32(at + c + 32, b);
+                    else read();
+                    add_columns(a, nl + c, sc2, acc);
+                    if (c + 32 >= valid) break;
+                    tmem_wait_ld(b);
+                    if (c + 64 < valid) tmem_ld32(at + c + 64, a);
+                    else read();
+                    add_columns(b, nl + c + 32, sc2, acc);
+                }
+                float x, y, u, v;
+                f2_unpack(acc[0], x, y);
+                f2_unpack(acc[1], u, v);
+                sum += (x + y) + (u + v);
+            } else {
+                float part = 0.0f;
+#pragma unroll 1
+                for (int c = max(0, lo_warp) & ~31; c < valid; c += 32) {
+                    uint32_t a[32];
+                    tmem_ld32(at + c, a);
+                    tmem_wait_ld(a);
+                    part += add_some_columns(a, nl + c, sc, lo - c, valid - c);
+                }
+                read();
+                sum += part;
             }
-            if (valid > 64) {
-                tmem_wait_ld(a);
-                if (valid > 96) tmem_ld32(at + 96, b);
-                add(a, 64);
-            }
-            if (valid > 96) tmem_wait_ld(b);
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->s_empty[half][buf]);
-            if (valid > 96) add(b, 96);
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->l_empty[ls]);
-            float x, y, u, v;
-            f2_unpack(acc[0], x, y);
-            f2_unpack(acc[1], u, v);
-            sum += (x + y) + (u + v);
         }
-        if (to) {
-            if (it.slot >= 0) *to = sum;
-            else atomicAdd(to, sum);  // the only addition to this key in the call
+        if (key < it.len) {
+            if (it.slot >= 0)
+                p.partial[(static_cast<int64_t>(it.slot) * w.Hkv + it.hkv) * p.keys + key] = sum;
+            else if (static_cast<unsigned>(id) < static_cast<unsigned>(w.num_blocks))  // the call's only addition to this key
+                atomicAdd(w.weights + (static_cast<int64_t>(id) * w.Hkv + it.hkv) * w.page.size + in_page, sum);
         }
     }
 }
@@ -594,7 +612,6 @@ weights_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     for (int i = threadIdx.x; i < kQStages * Layout<D>::kTile / 16; i += kThreads)
         reinterpret_cast<uint4*>(smem + Layout<D>::kQ)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
-    if (threadIdx.x < kCols) ctl->token[threadIdx.x] = static_cast<uint8_t>(threadIdx.x / p.w.group);
     if (warp == kQWarp && lane == 0) tma_prefetch_desc(&tmQ);
     if (warp == kMmaWarp) {
         tmem_alloc(&ctl->tmem_base, kTmemCols);
@@ -641,13 +658,13 @@ __global__ void __launch_bounds__(kAddThreads) weights_ranges_kernel(const __gri
     for (int b = blockIdx.z; b < p.w.B; b += gridDim.z) {
         const WeightsRequest r = weights_request(p.w, b);
         const int n = r.ok ? r.end - r.begin : 0;
-        if (n <= p.range) continue;
+        if (n <= 1 << p.range_shift) continue;
         // Slots of the requests before.
         int base = 0;
         for (int i = threadIdx.x; i < b; i += kAddThreads) {
             const WeightsRequest q = weights_request(p.w, i);
             const int m = q.ok ? q.end - q.begin : 0;
-            if (m > p.range) base += (m + p.range - 1) / p.range;
+            if (m > 1 << p.range_shift) base += (m + (1 << p.range_shift) - 1) >> p.range_shift;
         }
         base = __reduce_add_sync(0xffffffffu, base);
         __syncthreads();  // the request before has been read
@@ -659,7 +676,7 @@ __global__ void __launch_bounds__(kAddThreads) weights_ranges_kernel(const __gri
             int in_page;
             const int id = p.w.block_table[static_cast<int64_t>(b) * p.w.max_pages + p.w.page.split(key, &in_page)];
             if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.w.num_blocks)) continue;  // reported
-            const int t0 = max(0, key / kKeys * kKeys - (r.len - n)), ranges = (n - t0 + p.range - 1) / p.range;
+            const int t0 = max(0, (key & -kKeys) - (r.len - n)), ranges = (n - t0 + (1 << p.range_shift) - 1) >> p.range_shift;
             float sum = 0.0f;
             for (int i = 0; i < ranges; ++i) sum += p.partial[(static_cast<int64_t>(base + i) * p.w.Hkv + hkv) * p.keys + key];
             p.w.weights[(static_cast<int64_t>(id) * p.w.Hkv + hkv) * p.w.page.size + in_page] += sum;
@@ -667,20 +684,21 @@ __global__ void __launch_bounds__(kAddThreads) weights_ranges_kernel(const __gri
     }
 }
 
-// Tokens of an item: enough items for all SMs from two blocks of keys on, more where the
-// partial sums would not stay in the L2 (64 MB).
+// log2 of an item's tokens: two blocks of keys, so that there are items for all SMs; more where
+// the partial sums would not stay in the L2 (64 MB), or a head's items not fit in 31 bits.
 constexpr long long kPartialBytes = 64ll << 20;
-int range_of(const WeightsShape& s) {
+int range_shift_of(const WeightsShape& s) {
     const long long keys = static_cast<long long>(s.max_pages) * s.page;
-    long long range = 2 * kKeys;
-    while (s.total > range && 2 * s.total / range * s.Hkv * keys * 4 > kPartialBytes) range *= 2;
-    return static_cast<int>(std::min(range, 1ll << 30));
+    int shift = kKeyShift + 1;
+    while (s.total >> shift > 0 && ((2ll * s.total >> shift) * s.Hkv * keys * 4 > kPartialBytes ||
+                                    ((keys >> kKeyShift) + 1) * ((s.total >> shift) + 1) > 0x3fffffffll))
+        ++shift;
+    return shift;
 }
 long long partial_bytes(const WeightsShape& s) {
-    const int range = range_of(s);
-    if (s.total <= range) return 0;
-    // A request over `range` tokens has at most 2 n / range ranges.
-    return 2ll * s.total / range * s.Hkv * s.max_pages * s.page * 4;
+    const int shift = range_shift_of(s);
+    // A request with more tokens than a range has at most 2 n / range of them.
+    return s.total <= 1ll << shift ? 0 : (2ll * s.total >> shift) * s.Hkv * s.max_pages * s.page * 4;
 }
 
 template <int D, bool kF16, bool kFour>
@@ -713,7 +731,7 @@ cudaError_t launch_weights_tiles(const WeightsShape& s, const CUtensorMap& queri
     p.w = weights_params(s, env);
     p.partial = static_cast<float*>(ws);
     p.keys = static_cast<long long>(s.max_pages) * s.page;
-    p.range = range_of(s);
+    p.range_shift = range_shift_of(s);
     p.tile_tokens = weights_tile_tokens(p.w.group);
     p.limit_ns = env.wait_limit_ns;
     const int grid = env.num_sms;
