@@ -1285,8 +1285,12 @@ attn_status run_weights(bool four, const attn_rows* q, const float* lse, long lo
     // TMA reads the queries where their strides are real (a broadcast has stride 0).
     const int group = s.Hq / s.Hkv, tokens = weights_tile_tokens(group);
     if (tokens > 0 && (s.Hq == 1 || s.q_head > 0) && (total == 1 || s.q_token > 0)) {
-        CUtensorMap map;
-        if ((st = make_query_map(s, tokens, &map)) != ATTN_OK) return st;
+        WeightsMaps maps{};
+        if ((st = make_query_map(s, tokens, &maps.q)) != ATTN_OK) return st;
+        if (const int rows = weights_page_rows(s); rows > 0) {
+            st = make_map(kv_cache, page_size, 2ll * num_blocks * Hkv, D, rows, 3, &maps.k, false, s.f16 != 0);
+            if (st != ATTN_OK) return st;
+        }
         const size_t bytes = weights_workspace_bytes(s);
         void* ws = nullptr;
         if (bytes > 0) e = workspace_alloc(&ws, bytes, env);
@@ -1294,7 +1298,7 @@ attn_status run_weights(bool four, const attn_rows* q, const float* lse, long lo
             cudaGetLastError();
             return fail(ATTN_ERR_NO_MEMORY, "weights workspace of %zu bytes: %s", bytes, cudaGetErrorString(e));
         }
-        e = launch_weights_tiles(s, map, ws, env, &grid, &kernels);
+        e = launch_weights_tiles(s, maps, ws, env, &grid, &kernels);
         if (ws) {
             const cudaError_t f = cudaFreeAsync(ws, env.stream);
             if (e == cudaSuccess && f != cudaSuccess) e = f;

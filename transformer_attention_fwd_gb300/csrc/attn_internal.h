@@ -233,11 +233,16 @@ struct WeightsShape {
     int f16;
 };
 cudaError_t launch_weights_paged(const WeightsShape& s, const LaunchEnv& env, int* grid_out, int* kernels_launched);
-// The same on the 5th-generation tensor cores, for groups of up to 128 heads.  queries: the
-// packed queries as [total][Hq][D], box 64 x group x weights_tile_tokens(group), 128-byte swizzle.
-int weights_tile_tokens(int group);  // 0: the group is too large
+// The same on the 5th-generation tensor cores, for groups of up to 128 heads.  128-byte swizzle;
+// q: the packed queries as [total][Hq][D], box 64 x group x weights_tile_tokens(group); k: the
+// cache as [num_blocks * 2 * Hkv][page][D], box 64 x weights_page_rows(s) x 1.
+struct WeightsMaps {
+    CUtensorMap q, k;
+};
+int weights_tile_tokens(int group);            // 0: the group is too large
+int weights_page_rows(const WeightsShape& s);  // 0: not by TMA, k is not used
 size_t weights_workspace_bytes(const WeightsShape& s);
-cudaError_t launch_weights_tiles(const WeightsShape& s, const CUtensorMap& queries, void* ws, const LaunchEnv& env,
+cudaError_t launch_weights_tiles(const WeightsShape& s, const WeightsMaps& maps, void* ws, const LaunchEnv& env,
                                  int* grid_out, int* kernels_launched);
 
 // Eviction: the kept rows of each request and KV head moved to its first slots.

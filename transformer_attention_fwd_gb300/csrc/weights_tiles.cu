@@ -9,15 +9,18 @@
 // most `range` tokens of them; a CTA per SM walks the items of all requests in a fixed
 // order.  A key's sums from several ranges go to a workspace, and a second kernel adds
 // them up in order.  Warps:
-//   0-7    sums: warps 0-3 keys 0-127 of the item, warps 4-7 keys 128-255
-//   8-11   K rows, page by page, into one of two buffers: 16-bit rows by asynchronous
-//          16-byte copies, 4-bit rows converted in registers (a code times its scale has
-//          six significant bits: exact in either 16-bit type)
-//   12     query tiles by TMA: whole tokens, a KV head's query heads within, read straight
+//   0-15   sums: eight warps take the even query tiles, eight the odd ones; of each eight,
+//          four have keys 0-127 of the item and four keys 128-255.  (Eight in all left the
+//          tensor cores waiting.)  At an item's end the second eight hand their sums over.
+//   16     query tiles by TMA: whole tokens, a KV head's query heads within, read straight
 //          out of the caller's tensor (a box of 64 elements x heads x tokens)
-//   13     tensor memory, and all MMAs: for each query tile one 128 x 128 x D product for
+//   17     tensor memory, and all MMAs: for each query tile one 128 x 128 x D product for
 //          each half of the keys, into one of two accumulators each
-//   14     the rows' -lse into shared memory
+//   18     the rows' -lse into shared memory
+//   19 on  K rows into one of two buffers.  16-bit pages of 8 .. 256 rows (a power of two)
+//          by TMA, other 16-bit rows by asynchronous 16-byte copies, 4-bit rows converted in
+//          registers (a code times its scale has six significant bits: exact in either
+//          16-bit type)
 // Every wait is bounded (sm100.cuh).
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -35,7 +38,6 @@
 namespace attn {
 namespace {
 
-using prefill::align1024;
 using prefill::desc_advance;
 using prefill::issue_qk;
 using prefill::kDrainLimitNs;
@@ -46,14 +48,19 @@ constexpr int kKeyShift = 8, kKeys = 1 << kKeyShift;  // of an item
 constexpr int kHalf = 128;  // keys of an MMA
 constexpr int kCols = 128;  // query rows of a tile
 constexpr int kQStages = 3, kKStages = 2, kSBufs = 2;
-constexpr int kSumWarps = 8, kLoadWarps = 4;
-constexpr int kLoadWarp0 = kSumWarps, kQWarp = 12, kMmaWarp = 13;  // and the last: -lse
-constexpr int kThreads = 15 * 32;
+constexpr int kSumWarps = 16, kRowWarps = 4;
+constexpr int kQWarp = kSumWarps, kMmaWarp = kQWarp + 1, kLseWarp = kMmaWarp + 1, kLoadWarp0 = kLseWarp + 1;
+// How an item's keys arrive, and the warps for it.
+enum KeyLoads { kPages, kRows16, kRows4 };
+template <int kLoads>
+constexpr int kLoadWarps = kLoads == kPages ? 1 : kRowWarps;
+template <int kLoads>
+constexpr int kThreads = (kLoadWarp0 + kLoadWarps<kLoads>) * 32;
 constexpr uint32_t kTmemCols = 512;
 
 enum : unsigned {
     SITE_W_K_EMPTY = 48, SITE_W_K_FULL, SITE_W_Q_EMPTY, SITE_W_Q_FULL, SITE_W_L_EMPTY, SITE_W_L_FULL,
-    SITE_W_S_EMPTY, SITE_W_S_FULL
+    SITE_W_S_EMPTY, SITE_W_S_FULL, SITE_W_X_EMPTY, SITE_W_X_FULL
 };
 
 struct Control {
@@ -61,10 +68,12 @@ struct Control {
     uint64_t q_full[kQStages], q_empty[kQStages];
     uint64_t l_full[kQStages], l_empty[kQStages];
     uint64_t s_full[2][kSBufs], s_empty[2][kSBufs];  // [half of the keys]
+    uint64_t x_full[2], x_empty[2];                  // sums handed over
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
     alignas(16) float nlse[kQStages][kCols];  // -log2(e) lse of a tile's rows
+    float handed[kKeys];
 };
 
 template <int D>
@@ -73,8 +82,7 @@ struct Layout {
     static constexpr int kK = 0;
     static constexpr int kQ = kK + kKStages * 2 * kTile;
     static constexpr int kControl = kQ + kQStages * kTile;
-    static constexpr int kBytes = kControl + 2048 + 1024;  // and alignment
-    static_assert(sizeof(Control) <= 2048, "control block");
+    static constexpr int kBytes = kControl + static_cast<int>(sizeof(Control));
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -226,6 +234,55 @@ template <int D>
 __device__ __forceinline__ uint32_t key_chunk(int k, int c) {
     return static_cast<uint32_t>((k / kHalf) * Layout<D>::kTile + (c >> 3) * (kHalf * 128) + (k % kHalf) * 128 +
                                  (((c & 7) ^ (k & 7)) << 4));
+}
+
+// Pages by TMA: a box of up to 128 rows x 64 elements.  Rows past the request's last key are
+// other slots' or stale: they are lanes that nobody adds up.
+template <int D>
+__device__ void load_pages(const TilesParams& p, const CUtensorMap* tmK, uint8_t* smem, Control* ctl, int lane,
+                           const WaitGuard& g) {
+    const int page = p.w.page.size, rows = min(page, kHalf), boxes = kKeys / rows;  // boxes of an item, up to 32
+    Items items(p, lane);
+    Item it;
+    bool more = items.take(it);
+    auto look_up = [&]() {  // this lane's box; -1: none
+        const int key = it.key0 + lane * rows;
+        return more && lane < boxes && key < it.len
+                   ? p.w.block_table[static_cast<int64_t>(it.b) * p.w.max_pages + p.w.page.quotient(key)] : -1;
+    };
+    int id = look_up();
+    uint32_t k_it = 0;
+    bool ok = true;
+    while (more) {
+        const uint32_t s = k_it % kKStages;
+        if (k_it >= kKStages) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&ctl->k_empty[s], ((k_it / kKStages) & 1) ^ 1, g, SITE_W_K_EMPTY));
+            if (!ok) break;
+        }
+        const bool have = lane < boxes && it.key0 + lane * rows < it.len;
+        const bool good = have && static_cast<unsigned>(id) < static_cast<unsigned>(p.w.num_blocks);
+        if (have && !good) atomicOr(p.w.status, ATTN_DEV_BAD_INPUT);
+        const unsigned there = __ballot_sync(0xffffffffu, good);
+        if (lane == 0)
+            mbar_arrive_expect_tx(&ctl->k_full[s], static_cast<uint32_t>(__popc(there)) * rows * D * 2);
+        __syncwarp();
+        if (good) {
+            uint8_t* to = smem + Layout<D>::kK + s * 2 * Layout<D>::kTile + (lane * rows / kHalf) * Layout<D>::kTile +
+                          (lane * rows % kHalf) * 128;
+            const int slab = id * 2 * p.w.Hkv + it.hkv;  // fits (the host checks)
+            const int row = lane * rows % page;          // pages of 256 rows are two boxes
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(to + h * (kHalf * 128), tmK, &ctl->k_full[s], h * 64, row, slab);
+        }
+        ++k_it;
+        more = items.take(it);
+        id = look_up();
+    }
+    // Copies in flight land before the CTA leaves.
+    if (lane == 0)
+        for (uint32_t i = k_it > kKStages ? k_it - kKStages : 0; i < k_it; ++i)
+            wait_quiet(&ctl->k_full[i % kKStages], (i / kKStages) & 1, kDrainLimitNs);
 }
 
 template <int D>
@@ -435,7 +492,7 @@ __device__ void issue_mmas(const TilesParams& p, uint8_t* smem, Control* ctl, ui
     const uint32_t leader = elect_leader();
     Items items(p, lane);
     Item it;
-    uint32_t k_it = 0, q_it = 0, s_it[2] = {0, 0};
+    uint32_t k_it = 0, q_it = 0, uses[2][kSBufs] = {};
     bool ok = true;
     while (ok && items.take(it)) {
         const uint32_t ks = k_it % kKStages;
@@ -444,18 +501,19 @@ __device__ void issue_mmas(const TilesParams& p, uint8_t* smem, Control* ctl, ui
         for (int t = it.t0; ok && t < it.t1; t += p.tile_tokens, ++q_it) {
             const uint32_t qs = q_it % kQStages;
             ok = warp_wait(&ctl->q_full[qs], (q_it / kQStages) & 1, g, SITE_W_Q_FULL);
+            const uint32_t buf = q_it & 1;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (!ok || h >= halves) continue;
-                const uint32_t buf = s_it[h] % kSBufs;
-                if (s_it[h] >= kSBufs)
-                    ok = warp_wait(&ctl->s_empty[h][buf], ((s_it[h] / kSBufs) & 1) ^ 1, g, SITE_W_S_EMPTY);
+                const uint32_t used = buf ? uses[h][1] : uses[h][0];
+                if (used > 0) ok = warp_wait(&ctl->s_empty[h][buf], (used - 1) & 1, g, SITE_W_S_EMPTY);
                 if (!ok) continue;
                 tc_fence_after_sync();
                 issue_qk<D, kF16>(tmem + (h * kSBufs + buf) * kCols, desc_advance(k0, (ks * 2 + h) * kTile16),
                                   desc_advance(q0, qs * kTile16), leader);
                 mma_commit(&ctl->s_full[h][buf], leader);
-                ++s_it[h];
+                uses[h][0] += buf ^ 1;
+                uses[h][1] += buf;
             }
             mma_commit(&ctl->q_empty[qs], leader);
         }
@@ -495,11 +553,11 @@ __device__ __forceinline__ float add_some_columns(const uint32_t (&s)[32], const
 
 __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int warp, int lane, const WaitGuard& g) {
     const WeightsParams& w = p.w;
-    const int half = warp / 4, quarter = warp % 4;
-    const uint32_t lanes = tmem_lane_base(tmem, warp) + half * kSBufs * kCols;
+    const int set = warp / 8, half = warp / 4 % 2, quarter = warp % 4;
+    const uint32_t at = tmem_lane_base(tmem, warp) + (half * kSBufs + set) * kCols;  // the accumulator
     Items items(p, lane);
     Item it;
-    uint32_t s_it = 0, l_it = 0;
+    uint32_t l_it = 0, uses = 0, handed = 0;
     auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, g, site)) != 0;
     };
@@ -507,6 +565,7 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
         const int first = it.key0 + half * kHalf, key = first + quarter * 32 + lane;
         if (first >= it.len) {  // no keys in this half: the tiles' rows pass by
             for (int t = it.t0; t < it.t1; t += p.tile_tokens, ++l_it) {
+                if ((l_it & 1) != set) continue;
                 const uint32_t s = l_it % kQStages;
                 if (!wait(&ctl->l_full[s], (l_it / kQStages) & 1, SITE_W_L_FULL)) return;
                 if (lane == 0) mbar_arrive(&ctl->l_empty[s]);
@@ -519,8 +578,9 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
         const float sc = w.scale_log2 * (w.factors ? w.factors[it.hkv] : 1.0f);
         const uint64_t sc2 = f2_pack(sc, sc);
         float sum = 0.0f;
-        for (int t = it.t0; t < it.t1; t += p.tile_tokens, ++l_it, ++s_it) {
-            const uint32_t ls = l_it % kQStages, buf = s_it % kSBufs;
+        for (int t = it.t0; t < it.t1; t += p.tile_tokens, ++l_it) {
+            if ((l_it & 1) != set) continue;
+            const uint32_t ls = l_it % kQStages;
             const int valid = min(p.tile_tokens, it.t1 - t) * w.group;
             // Token t sees keys up to len - n + t: this key is seen from column lo on, the warp's
             // first key from lo_warp on.
@@ -528,30 +588,24 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
             const int lo = (key - past) * w.group, lo_warp = (first + quarter * 32 - past) * w.group;
             const bool whole = (first + quarter * 32 + 31 <= past) && (valid & 31) == 0;
             if (!wait(&ctl->l_full[ls], (l_it / kQStages) & 1, SITE_W_L_FULL)) return;
-            if (!wait(&ctl->s_full[half][buf], (s_it / kSBufs) & 1, SITE_W_S_FULL)) return;
+            if (!wait(&ctl->s_full[half][set], uses & 1, SITE_W_S_FULL)) return;
+            ++uses;
             tc_fence_after_sync();
-            const uint32_t at = lanes + buf * kCols;
             const float* nl = ctl->nlse[ls];
             auto read = [&]() {  // the accumulator has been read
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->s_empty[half][buf]);
+                if (lane == 0) mbar_arrive(&ctl->s_empty[half][set]);
             };
             if (whole) {
                 uint64_t acc[2] = {0, 0};
-                uint32_t a[32], b[32];
-                tmem_ld32(at, a);
-#pragma unroll 1  // (unrolled, with the other path behind each chunk, the loop outgrew the instruction caches: 58 us of 124)
-                for (int c = 0; c < valid; c += 64) {
+#pragma unroll 1  // (unrolled the loops outgrow the instruction caches: 58 us of a prompt's 124)
+                for (int c = 0; c < valid; c += 32) {
+                    uint32_t a[32];
+                    tmem_ld32(at + c, a);
                     tmem_wait_ld(a);
-                    if (c + 32 < valid) tmem_ld32(at + c + 32, b);
-                    else read();
+                    if (c + 32 >= valid) read();
                     add_columns(a, nl + c, sc2, acc);
-                    if (c + 32 >= valid) break;
-                    tmem_wait_ld(b);
-                    if (c + 64 < valid) tmem_ld32(at + c + 64, a);
-                    else read();
-                    add_columns(b, nl + c + 32, sc2, acc);
                 }
                 float x, y, u, v;
                 f2_unpack(acc[0], x, y);
@@ -572,7 +626,21 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->l_empty[ls]);
         }
-        if (key < it.len) {
+        // The odd tiles' sums to the warps of the even ones.
+        const int place = half * kHalf + quarter * 32 + lane;
+        if (set == 1) {
+            if (handed > 0 && !wait(&ctl->x_empty[half], (handed - 1) & 1, SITE_W_X_EMPTY)) return;
+            ctl->handed[place] = sum;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->x_full[half]);
+        } else {
+            if (!wait(&ctl->x_full[half], handed & 1, SITE_W_X_FULL)) return;
+            sum += ctl->handed[place];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->x_empty[half]);
+        }
+        ++handed;
+        if (set == 0 && key < it.len) {
             if (it.slot >= 0)
                 p.partial[(static_cast<int64_t>(it.slot) * w.Hkv + it.hkv) * p.keys + key] = sum;
             else if (static_cast<unsigned>(id) < static_cast<unsigned>(w.num_blocks))  // the call's only addition to this key
@@ -581,35 +649,42 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
     }
 }
 
-template <int D, bool kF16, bool kFour>
-__global__ void __launch_bounds__(kThreads, 1)
-weights_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TilesParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = align1024(smem_raw);
+template <int D, bool kF16, int kLoads>
+__global__ void __launch_bounds__(kThreads<kLoads>, 1)
+weights_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ TilesParams p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle needs it; there is no room for slack
+        if (threadIdx.x == 0) atomicOr(p.w.status, ATTN_DEV_BAD_INPUT);
+        return;
+    }
     Control* ctl = reinterpret_cast<Control*>(smem + Layout<D>::kControl);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kKStages; ++i) {
-            mbar_init(&ctl->k_full[i], kLoadWarps);
+            mbar_init(&ctl->k_full[i], kLoadWarps<kLoads>);
             mbar_init(&ctl->k_empty[i], 1);
         }
         for (int i = 0; i < kQStages; ++i) {
             mbar_init(&ctl->q_full[i], 1);
             mbar_init(&ctl->q_empty[i], 1);
             mbar_init(&ctl->l_full[i], 1);
-            mbar_init(&ctl->l_empty[i], kSumWarps);
+            mbar_init(&ctl->l_empty[i], kSumWarps / 2);
         }
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&ctl->x_full[h], 4);
+            mbar_init(&ctl->x_empty[h], 4);
             for (int i = 0; i < kSBufs; ++i) {
                 mbar_init(&ctl->s_full[h][i], 1);
                 mbar_init(&ctl->s_empty[h][i], 4);
             }
+        }
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
         fence_mbar_init();
     }
     // Rows of a query tile past its tokens stay zeros.
-    for (int i = threadIdx.x; i < kQStages * Layout<D>::kTile / 16; i += kThreads)
+    for (int i = threadIdx.x; i < kQStages * Layout<D>::kTile / 16; i += kThreads<kLoads>)
         reinterpret_cast<uint4*>(smem + Layout<D>::kQ)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     if (warp == kQWarp && lane == 0) tma_prefetch_desc(&tmQ);
@@ -627,15 +702,16 @@ weights_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 
     if (warp < kSumWarps) {
         add_up(p, ctl, tmem, warp, lane, g);
-    } else if (warp < kLoadWarp0 + kLoadWarps) {
-        if constexpr (kFour) load_rows4<D, kF16>(p, smem, ctl, warp - kLoadWarp0, lane, g);
-        else load_rows16<D>(p, smem, ctl, warp - kLoadWarp0, lane, g);
     } else if (warp == kQWarp) {
         load_queries<D>(p, &tmQ, smem, ctl, lane, g);
     } else if (warp == kMmaWarp) {
         issue_mmas<D, kF16>(p, smem, ctl, tmem, lane, g);
-    } else {
+    } else if (warp == kLseWarp) {
         load_lse(p, ctl, lane, g);
+    } else {
+        if constexpr (kLoads == kRows4) load_rows4<D, kF16>(p, smem, ctl, warp - kLoadWarp0, lane, g);
+        else if constexpr (kLoads == kRows16) load_rows16<D>(p, smem, ctl, warp - kLoadWarp0, lane, g);
+        else load_pages<D>(p, &tmK, smem, ctl, lane, g);
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -701,31 +777,42 @@ long long partial_bytes(const WeightsShape& s) {
     return s.total <= 1ll << shift ? 0 : (2ll * s.total >> shift) * s.Hkv * s.max_pages * s.page * 4;
 }
 
-template <int D, bool kF16, bool kFour>
-cudaError_t launch_tiles(const CUtensorMap& map, const TilesParams& p, int grid, const LaunchEnv& env) {
-    auto* kern = weights_tiles_kernel<D, kF16, kFour>;
+template <int D, bool kF16, int kLoads>
+cudaError_t launch_tiles(const WeightsMaps& maps, const TilesParams& p, int grid, const LaunchEnv& env) {
+    auto* kern = weights_tiles_kernel<D, kF16, kLoads>;
     static bool attr_set[64] = {};  // device < 64 (device_env)
     if (!attr_set[env.device]) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
         if (e != cudaSuccess) return e;
         attr_set[env.device] = true;
     }
-    return launch_serial(kern, dim3(grid), kThreads, Layout<D>::kBytes, env.stream, map, p);
+    return launch_serial(kern, dim3(grid), kThreads<kLoads>, Layout<D>::kBytes, env.stream, maps.q, maps.k, p);
 }
 
+template <int D, int kLoads>
+cudaError_t launch_types(const WeightsMaps& maps, const TilesParams& p, bool f16, int grid, const LaunchEnv& env) {
+    return f16 ? launch_tiles<D, true, kLoads>(maps, p, grid, env) : launch_tiles<D, false, kLoads>(maps, p, grid, env);
+}
 template <int D>
-cudaError_t launch_types(const CUtensorMap& map, const TilesParams& p, bool f16, bool four, int grid, const LaunchEnv& env) {
-    if (four) return f16 ? launch_tiles<D, true, true>(map, p, grid, env) : launch_tiles<D, false, true>(map, p, grid, env);
-    return f16 ? launch_tiles<D, true, false>(map, p, grid, env) : launch_tiles<D, false, false>(map, p, grid, env);
+cudaError_t launch_loads(const WeightsMaps& maps, const TilesParams& p, bool f16, int loads, int grid, const LaunchEnv& env) {
+    if (loads == kRows4) return launch_types<D, kRows4>(maps, p, f16, grid, env);
+    if (loads == kRows16) return launch_types<D, kRows16>(maps, p, f16, grid, env);
+    return launch_types<D, kPages>(maps, p, f16, grid, env);
 }
 
 }  // namespace
 
 int weights_tile_tokens(int group) { return group <= kCols ? kCols / group : 0; }
 
+int weights_page_rows(const WeightsShape& s) {
+    const bool box = s.page >= 8 && s.page <= kKeys && (s.page & (s.page - 1)) == 0;
+    const long long slabs = 2ll * s.num_blocks * s.Hkv;
+    return !s.scales && box && slabs <= 0x7fffffffll ? std::min(s.page, kHalf) : 0;
+}
+
 size_t weights_workspace_bytes(const WeightsShape& s) { return static_cast<size_t>(partial_bytes(s)); }
 
-cudaError_t launch_weights_tiles(const WeightsShape& s, const CUtensorMap& queries, void* ws, const LaunchEnv& env,
+cudaError_t launch_weights_tiles(const WeightsShape& s, const WeightsMaps& maps, void* ws, const LaunchEnv& env,
                                  int* grid_out, int* kernels_launched) {
     TilesParams p{};
     p.w = weights_params(s, env);
@@ -737,9 +824,9 @@ cudaError_t launch_weights_tiles(const WeightsShape& s, const CUtensorMap& queri
     const int grid = env.num_sms;
     *grid_out = grid;
     *kernels_launched = ws ? 2 : 1;
-    const bool four = s.scales != nullptr, f16 = s.f16 != 0;
-    cudaError_t e = s.D == 64 ? launch_types<64>(queries, p, f16, four, grid, env)
-                              : launch_types<128>(queries, p, f16, four, grid, env);
+    const int loads = s.scales ? kRows4 : weights_page_rows(s) > 0 ? kPages : kRows16;
+    cudaError_t e = s.D == 64 ? launch_loads<64>(maps, p, s.f16 != 0, loads, grid, env)
+                              : launch_loads<128>(maps, p, s.f16 != 0, loads, grid, env);
     if (e != cudaSuccess || !ws) return e;
     const unsigned y = static_cast<unsigned>(s.Hkv), z = static_cast<unsigned>(std::min(s.B, 64));
     const long long want = std::max(1ll, 8ll * env.num_sms / (static_cast<long long>(y) * z));
