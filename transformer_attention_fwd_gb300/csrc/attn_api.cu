@@ -1283,7 +1283,7 @@ attn_status run_weights(bool four, const attn_rows* q, const float* lse, long lo
     int grid = 0, kernels = 0;
     cudaError_t e = cudaSuccess;
     // TMA reads the queries where their strides are real (a broadcast has stride 0).
-    const int group = s.Hq / s.Hkv, tokens = weights_tile_tokens(group);
+    const int tokens = weights_tile_tokens(s);
     if (tokens > 0 && (s.Hq == 1 || s.q_head > 0) && (total == 1 || s.q_token > 0)) {
         WeightsMaps maps{};
         if ((st = make_query_map(s, tokens, &maps.q)) != ATTN_OK) return st;

@@ -234,12 +234,14 @@ struct WeightsShape {
 };
 cudaError_t launch_weights_paged(const WeightsShape& s, const LaunchEnv& env, int* grid_out, int* kernels_launched);
 // The same on the 5th-generation tensor cores, for groups of up to 128 heads.  128-byte swizzle;
-// q: the packed queries as [total][Hq][D], box 64 x group x weights_tile_tokens(group); k: the
+// q: the packed queries as [total][Hq][D], box 64 x group x weights_tile_tokens(s); k: the
 // cache as [num_blocks * 2 * Hkv][page][D], box 64 x weights_page_rows(s) x 1.
 struct WeightsMaps {
     CUtensorMap q, k;
 };
-int weights_tile_tokens(int group);            // 0: the group is too large
+// Tokens of a query tile: as many as it has rows for, or one where the requests have one each
+// (a decode step); 0: the group is too large.
+int weights_tile_tokens(const WeightsShape& s);
 int weights_page_rows(const WeightsShape& s);  // 0: not by TMA, k is not used
 size_t weights_workspace_bytes(const WeightsShape& s);
 cudaError_t launch_weights_tiles(const WeightsShape& s, const WeightsMaps& maps, void* ws, const LaunchEnv& env,

@@ -17,7 +17,9 @@
 //   17     tensor memory, and all MMAs: for each query tile one 128 x 128 x D product for
 //          each half of the keys, into one of two accumulators each
 //   18     the rows' -lse into shared memory
-//   19 on  K rows into one of two buffers.  16-bit pages of 8 .. 256 rows (a power of two)
+//   19     the items: their place in the requests takes some 1400 cycles to find, which
+//          every warp by itself spent at every item (a window's period was 5800 cycles)
+//   20 on  K rows into one of two buffers.  16-bit pages of 8 .. 256 rows (a power of two)
 //          by TMA, other 16-bit rows by asynchronous 16-byte copies, 4-bit rows converted in
 //          registers (a code times its scale has six significant bits: exact in either
 //          16-bit type)
@@ -39,7 +41,6 @@ namespace attn {
 namespace {
 
 using prefill::desc_advance;
-using prefill::issue_qk;
 using prefill::kDrainLimitNs;
 using prefill::wait_quiet;
 using prefill::warp_wait;
@@ -47,9 +48,10 @@ using prefill::warp_wait;
 constexpr int kKeyShift = 8, kKeys = 1 << kKeyShift;  // of an item
 constexpr int kHalf = 128;  // keys of an MMA
 constexpr int kCols = 128;  // query rows of a tile
-constexpr int kQStages = 3, kKStages = 2, kSBufs = 2;
+constexpr int kQStages = 3, kKStages = 2, kSBufs = 2, kItems = 4;
 constexpr int kSumWarps = 16, kRowWarps = 4;
-constexpr int kQWarp = kSumWarps, kMmaWarp = kQWarp + 1, kLseWarp = kMmaWarp + 1, kLoadWarp0 = kLseWarp + 1;
+constexpr int kQWarp = kSumWarps, kMmaWarp = kQWarp + 1, kLseWarp = kMmaWarp + 1, kItemWarp = kLseWarp + 1;
+constexpr int kLoadWarp0 = kItemWarp + 1;
 // How an item's keys arrive, and the warps for it.
 enum KeyLoads { kPages, kRows16, kRows4 };
 template <int kLoads>
@@ -60,7 +62,16 @@ constexpr uint32_t kTmemCols = 512;
 
 enum : unsigned {
     SITE_W_K_EMPTY = 48, SITE_W_K_FULL, SITE_W_Q_EMPTY, SITE_W_Q_FULL, SITE_W_L_EMPTY, SITE_W_L_FULL,
-    SITE_W_S_EMPTY, SITE_W_S_FULL, SITE_W_X_EMPTY, SITE_W_X_FULL
+    SITE_W_S_EMPTY, SITE_W_S_FULL, SITE_W_X_EMPTY, SITE_W_X_FULL, SITE_W_I_EMPTY,
+    SITE_W_I_FULL
+};
+
+struct alignas(16) Item {  // b < 0: the end
+    int b, hkv, begin, n;
+    int len, key0;  // keys of the request; the item's first
+    int t0, t1;     // tokens of the item, counted from the request's first query
+    int slot;       // of the partial sums; -1: none
+    int pad[3];
 };
 
 struct Control {
@@ -69,11 +80,13 @@ struct Control {
     uint64_t l_full[kQStages], l_empty[kQStages];
     uint64_t s_full[2][kSBufs], s_empty[2][kSBufs];  // [half of the keys]
     uint64_t x_full[2], x_empty[2];                  // sums handed over
+    uint64_t i_full[kItems], i_empty[kItems];
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
     alignas(16) float nlse[kQStages][kCols];  // -log2(e) lse of a tile's rows
     float handed[kKeys];
+    Item items[kItems];
 };
 
 template <int D>
@@ -129,21 +142,14 @@ struct Counts {
     }
 };
 
-struct Item {
-    int b, hkv, begin, n, len;
-    int key0;      // first key
-    int t0, t1;    // tokens of the item, counted from the request's first query
-    int slot;      // of the partial sums; -1: none
-};
-
-// This CTA's items one after the other; every call by a whole warp.  32 requests are looked at
-// at a time, a lane each.
-struct Items {
+// This CTA's items one after the other, by a whole warp.  32 requests are looked at at a time,
+// a lane each.
+struct Finder {
     const TilesParams& p;
     const int lane;
     long long next, base = 0, incl = 0, chunk = 0;  // items before the lanes' requests; their prefix; all of them
     int first = -32, begin = 0, n = 0, len = 0, slots = 0, slot_base = 0;
-    __device__ __forceinline__ Items(const TilesParams& params, int lane_id)
+    __device__ __forceinline__ Finder(const TilesParams& params, int lane_id)
         : p(params), lane(lane_id), next(blockIdx.x) {}
 
     __device__ __forceinline__ void look() {
@@ -205,6 +211,52 @@ struct Items {
     }
 };
 
+// The items as the other warps take them from the item warp; every call by a whole warp.
+struct Items {
+    Control* ctl;
+    const int lane;
+    const WaitGuard& g;
+    uint32_t i_it = 0;
+    __device__ __forceinline__ Items(Control* control, int lane_id, const WaitGuard& guard)
+        : ctl(control), lane(lane_id), g(guard) {}
+    // kVote: not in the MMA warp (warp_wait says why).
+    template <bool kVote = true>
+    __device__ __forceinline__ bool take(Item& it) {
+        const uint32_t s = i_it % kItems;
+        bool ok = warp_wait(&ctl->i_full[s], (i_it / kItems) & 1, g, SITE_W_I_FULL);
+        if (kVote) ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        const int4* at = reinterpret_cast<const int4*>(&ctl->items[s]);
+        const int4 x = at[0], y = at[1];
+        it.slot = ctl->items[s].slot;
+        it.b = x.x; it.hkv = x.y; it.begin = x.z; it.n = x.w;
+        it.len = y.x; it.key0 = y.y; it.t0 = y.z; it.t1 = y.w;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->i_empty[s]);
+        ++i_it;
+        return it.b >= 0;
+    }
+};
+
+__device__ void find_items(const TilesParams& p, Control* ctl, int lane, const WaitGuard& g) {
+    Finder finder(p, lane);
+    bool more = true;
+    for (uint32_t i_it = 0; more; ++i_it) {
+        Item it{};
+        more = finder.take(it);
+        if (!more) it.b = -1;
+        const uint32_t s = i_it % kItems;
+        if (i_it >= kItems &&
+            !__all_sync(0xffffffffu, mbar_wait(&ctl->i_empty[s], ((i_it / kItems) & 1) ^ 1, g, SITE_W_I_EMPTY)))
+            return;
+        if (lane == 0) {
+            ctl->items[s] = it;
+            mbar_arrive(&ctl->i_full[s]);
+        }
+        __syncwarp();
+    }
+}
+
 // 64 keys of an item for one of four warps: two lanes' worth of slots, looked up ahead.
 struct RowIds {
     int64_t row[2];  // of keys lane and lane + 32 in the pool of rows; negative: none
@@ -242,7 +294,7 @@ template <int D>
 __device__ void load_pages(const TilesParams& p, const CUtensorMap* tmK, uint8_t* smem, Control* ctl, int lane,
                            const WaitGuard& g) {
     const int page = p.w.page.size, rows = min(page, kHalf), boxes = kKeys / rows;  // boxes of an item, up to 32
-    Items items(p, lane);
+    Items items(ctl, lane, g);
     Item it;
     bool more = items.take(it);
     auto look_up = [&]() {  // this lane's box; -1: none
@@ -291,7 +343,7 @@ __device__ void load_rows16(const TilesParams& p, uint8_t* smem, Control* ctl, i
     constexpr int kRowsPer = 32 / kPer;   // rows of a warp's copy
     const uint32_t buffers = smem_u32(smem + Layout<D>::kK);
     const int c = lane % kPer;
-    Items items(p, lane);
+    Items items(ctl, lane, g);
     Item it;
     uint32_t k_it = 0;
     bool waiting = false;  // the copies before have not been handed over
@@ -341,7 +393,7 @@ __device__ void load_rows4(const TilesParams& p, uint8_t* smem, Control* ctl, in
     constexpr int kSteps = 64 / kRowsPer;
     uint8_t* buffers = smem + Layout<D>::kK;
     const int part = lane % kPer;
-    Items items(p, lane);
+    Items items(ctl, lane, g);
     Item it;
     uint32_t k_it = 0;
     while (items.take(it)) {
@@ -393,7 +445,7 @@ template <int D>
 __device__ void load_queries(const TilesParams& p, const CUtensorMap* tmQ, uint8_t* smem, Control* ctl, int lane,
                              const WaitGuard& g) {
     const uint32_t bytes = static_cast<uint32_t>(p.tile_tokens * p.w.group) * D * 2;
-    Items items(p, lane);
+    Items items(ctl, lane, g);
     Item it;
     uint32_t q_it = 0;
     bool ok = true;
@@ -432,7 +484,7 @@ __device__ void load_lse(const TilesParams& p, Control* ctl, int lane, const Wai
         head_at[i] = (row - token[i] * w.group) * w.lse_head;
         if (token[i] >= p.tile_tokens) token[i] = 1 << 30;  // no row
     }
-    Items items(p, lane);
+    Items items(ctl, lane, g);
     Item it{};
     bool more = items.take(it);
     int t = it.t0;
@@ -483,6 +535,21 @@ __device__ void load_lse(const TilesParams& p, Control* ctl, int lane, const Wai
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// S[tmem cols] = keys . queries^T: M = 128, N as idesc has it, K = D in steps of 16.
+template <int D>
+__device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint64_t kd, uint64_t qd, uint32_t idesc, uint32_t leader) {
+    constexpr int kSteps = D / 16;
+    uint64_t a[kSteps], b[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const uint32_t off16 = static_cast<uint32_t>(((i / 4) * (kHalf * 128) + (i % 4) * 32) >> 4);
+        a[i] = desc_advance(kd, off16);
+        b[i] = desc_advance(qd, off16);
+    }
+    if constexpr (kSteps == 8) mma_bf16_ss_x8(d_tmem, a, b, idesc, 0u, leader);
+    else mma_bf16_ss_x4(d_tmem, a, b, idesc, 0u, leader);
+}
+
 template <int D, bool kF16>
 __device__ void issue_mmas(const TilesParams& p, uint8_t* smem, Control* ctl, uint32_t tmem, int lane,
                            const WaitGuard& g) {
@@ -490,11 +557,14 @@ __device__ void issue_mmas(const TilesParams& p, uint8_t* smem, Control* ctl, ui
     const uint64_t k0 = smem_desc_sw128(smem_u32(smem + Layout<D>::kK), 16, 1024);
     const uint64_t q0 = smem_desc_sw128(smem_u32(smem + Layout<D>::kQ), 16, 1024);
     const uint32_t leader = elect_leader();
-    Items items(p, lane);
+    // Columns for a tile's rows, a multiple of 16.
+    const int cols = (p.tile_tokens * p.w.group + 15) & ~15;
+    const uint32_t idesc = mma_idesc_bf16_f32(kHalf, 16, false, false, kF16) + ((static_cast<uint32_t>(cols) >> 3) - 2u << 17);
+    Items items(ctl, lane, g);
     Item it;
     uint32_t k_it = 0, q_it = 0, uses[2][kSBufs] = {};
     bool ok = true;
-    while (ok && items.take(it)) {
+    while (ok && items.take<false>(it)) {
         const uint32_t ks = k_it % kKStages;
         const int halves = it.key0 + kHalf < it.len ? 2 : 1;
         ok = warp_wait(&ctl->k_full[ks], (k_it / kKStages) & 1, g, SITE_W_K_FULL);
@@ -509,8 +579,8 @@ __device__ void issue_mmas(const TilesParams& p, uint8_t* smem, Control* ctl, ui
                 if (used > 0) ok = warp_wait(&ctl->s_empty[h][buf], (used - 1) & 1, g, SITE_W_S_EMPTY);
                 if (!ok) continue;
                 tc_fence_after_sync();
-                issue_qk<D, kF16>(tmem + (h * kSBufs + buf) * kCols, desc_advance(k0, (ks * 2 + h) * kTile16),
-                                  desc_advance(q0, qs * kTile16), leader);
+                issue_scores<D>(tmem + (h * kSBufs + buf) * kCols, desc_advance(k0, (ks * 2 + h) * kTile16),
+                                desc_advance(q0, qs * kTile16), idesc, leader);
                 mma_commit(&ctl->s_full[h][buf], leader);
                 uses[h][0] += buf ^ 1;
                 uses[h][1] += buf;
@@ -555,7 +625,7 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
     const WeightsParams& w = p.w;
     const int set = warp / 8, half = warp / 4 % 2, quarter = warp % 4;
     const uint32_t at = tmem_lane_base(tmem, warp) + (half * kSBufs + set) * kCols;  // the accumulator
-    Items items(p, lane);
+    Items items(ctl, lane, g);
     Item it;
     uint32_t l_it = 0, uses = 0, handed = 0;
     auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
@@ -679,6 +749,10 @@ weights_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                 mbar_init(&ctl->s_empty[h][i], 4);
             }
         }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&ctl->i_full[i], 1);
+            mbar_init(&ctl->i_empty[i], kLoadWarp0 - 1 + kLoadWarps<kLoads>);  // all warps but the item warp
+        }
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
         fence_mbar_init();
@@ -708,6 +782,8 @@ weights_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         issue_mmas<D, kF16>(p, smem, ctl, tmem, lane, g);
     } else if (warp == kLseWarp) {
         load_lse(p, ctl, lane, g);
+    } else if (warp == kItemWarp) {
+        find_items(p, ctl, lane, g);
     } else {
         if constexpr (kLoads == kRows4) load_rows4<D, kF16>(p, smem, ctl, warp - kLoadWarp0, lane, g);
         else if constexpr (kLoads == kRows16) load_rows16<D>(p, smem, ctl, warp - kLoadWarp0, lane, g);
@@ -802,7 +878,11 @@ cudaError_t launch_loads(const WeightsMaps& maps, const TilesParams& p, bool f16
 
 }  // namespace
 
-int weights_tile_tokens(int group) { return group <= kCols ? kCols / group : 0; }
+int weights_tile_tokens(const WeightsShape& s) {
+    const int group = s.Hq / s.Hkv;
+    if (group > kCols) return 0;
+    return s.total <= s.B ? 1 : kCols / group;
+}
 
 int weights_page_rows(const WeightsShape& s) {
     const bool box = s.page >= 8 && s.page <= kKeys && (s.page & (s.page - 1)) == 0;
@@ -819,7 +899,7 @@ cudaError_t launch_weights_tiles(const WeightsShape& s, const WeightsMaps& maps,
     p.partial = static_cast<float*>(ws);
     p.keys = static_cast<long long>(s.max_pages) * s.page;
     p.range_shift = range_shift_of(s);
-    p.tile_tokens = weights_tile_tokens(p.w.group);
+    p.tile_tokens = weights_tile_tokens(s);
     p.limit_ns = env.wait_limit_ns;
     const int grid = env.num_sms;
     *grid_out = grid;
