@@ -1,7 +1,8 @@
 // decode_cache.cuh -- shared by the decodes over the 8-bit and the 4-bit cache: the
-// sequence of 16-key tiles, the copies that feed a warp's ring, the weighted sum of a
+// sequence of key tiles, the copies that feed a warp's ring, the weighted sum of a
 // tile's V rows and the merge of partial results.  decode_e4m3.cu says what is computed
 // and how.  What depends on the cache's format is in a class C (E4m3Cache, E2m1Cache):
+//   kKeys             keys of a tile, 16 or 32
 //   kStageBytes<D>    a tile in shared memory
 //   kTwoReferences    the weights' sum and the weighted sum have references of their own
 //   kFactors          K and V have a factor for each head
@@ -19,7 +20,7 @@
 
 namespace attn {
 
-constexpr int kTile = 16;          // keys of a tile
+constexpr int kTile = 16;          // keys of a product
 constexpr int kMaxPrefixB = 1024;  // requests whose tile counts a CTA sums itself
 constexpr float kSlack = 6.0f;
 // A weight is held as two fp16 terms, what the first leaves out in the second, relative
@@ -433,8 +434,9 @@ struct Feed {
         look_up();
     }
     __device__ __forceinline__ void look_up() {
-        const int key = lc.tile * kTile + (kWholePages ? 0 : lane & 15);
-        const int page = p.page.split(kWholePages || key < lc.len ? key : lc.len - 1, &row);
+        // The keys of a product in one page: its first; else each.
+        const int key = lc.tile * C::kKeys + (kWholePages ? (lane & (C::kKeys - 1)) & -kTile : lane & (C::kKeys - 1));
+        const int page = p.page.split(key < lc.len ? key : lc.len - 1, &row);
         id = p.block_table[static_cast<int64_t>(lc.b) * p.max_pages + page];
     }
     __device__ __forceinline__ void issue() {
@@ -444,14 +446,15 @@ struct Feed {
                 id = 0;
             }
             const int hkv = p.chunks == 1 ? lc.unit : lc.unit / p.chunks;
-            const int valid = lc.len - lc.tile * kTile;  // 16 and more: the whole tile
+            const int valid = lc.len - lc.tile * C::kKeys;  // kKeys and more: the whole tile
             copies.issue(p, fill, id, row, hkv, valid);
             fill += C::template kStageBytes<D>;
             if (fill == ring + kStages * C::template kStageBytes<D>) fill = ring;
             if (++loaded < count) {
                 const int tile = lc.tile;
                 cursor_next(p, cum, lc);
-                if (kWholePages && lc.tile == tile + 1 && row + kTile < p.page.size) row += kTile;  // the same page
+                if (kWholePages && C::kKeys == kTile && lc.tile == tile + 1 && row + kTile < p.page.size)
+                    row += kTile;  // the same page
                 else look_up();
             }
         }
@@ -510,7 +513,7 @@ __device__ __forceinline__ TileScores tile_scores(const CacheParams& p, const Cu
     const int hkv = p.chunks == 1 ? c.unit : c.unit / p.chunks, chunk = c.unit - hkv * p.chunks;
     t.heads = min(HC, p.group - chunk * HC);
     t.at = p.scores + ((static_cast<int64_t>(c.b) * p.Hkv + hkv) * p.max_pages * p.page.size +
-                       static_cast<int64_t>(c.tile) * kTile) * p.group + chunk * HC;
+                       static_cast<int64_t>(c.tile) * C::kKeys) * p.group + chunk * HC;
     return t;
 }
 

@@ -51,7 +51,8 @@ __device__ __forceinline__ Cursor cursor_at(const CacheParams& p, const long lon
 }
 
 // cum[b] = tiles of requests 0 .. b - 1, by the whole block.
-static __device__ void tile_prefix(const CacheParams& p, long long* cum, long long* scan, bool report) {
+template <class C>
+__device__ void tile_prefix(const CacheParams& p, long long* cum, long long* scan, bool report) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + nt - 1) / nt;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
@@ -59,7 +60,7 @@ static __device__ void tile_prefix(const CacheParams& p, long long* cum, long lo
     for (int b = b0; b < b1; ++b) {
         const int n = p.seq_lens[b], L = clamped(p, n);
         if (report && L != n) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
-        mine += (L + kTile - 1) / kTile;
+        mine += (L + C::kKeys - 1) / C::kKeys;
     }
     long long incl = mine;
 #pragma unroll
@@ -73,7 +74,7 @@ static __device__ void tile_prefix(const CacheParams& p, long long* cum, long lo
     for (int i = 0; i < warp; ++i) run += scan[i];
     const long long end = run + mine;
     for (int b = b0; b < b1; ++b) {  // one request: nothing to read again
-        run = b + 1 == b1 ? end : run + (clamped_len(p, b) + kTile - 1) / kTile;
+        run = b + 1 == b1 ? end : run + (clamped_len(p, b) + C::kKeys - 1) / C::kKeys;
         cum[b + 1] = run;
     }
     if (tid == 0) cum[0] = 0;
@@ -83,7 +84,7 @@ static __device__ void tile_prefix(const CacheParams& p, long long* cum, long lo
 template <class C>
 __global__ void __launch_bounds__(1024) decode_prefix_kernel(const CacheParams p) {
     __shared__ long long scan[32];
-    tile_prefix(p, p.cum, scan, true);
+    tile_prefix<C>(p, p.cum, scan, true);
 }
 
 // Tiles of a CTA's slice: at least one a warp.
@@ -113,7 +114,7 @@ decode_long_kernel(const CacheParams p, int prefix_in_kernel) {
     grid_wait();
     grid_launch_next();
     if (prefix_in_kernel) {
-        tile_prefix(p, s_cum, s_cum + kMaxPrefixB + 1, blockIdx.x == 0);
+        tile_prefix<C>(p, s_cum, s_cum + kMaxPrefixB + 1, blockIdx.x == 0);
         cum = s_cum;
     }
     const int grid = static_cast<int>(gridDim.x);
@@ -157,7 +158,7 @@ decode_long_kernel(const CacheParams p, int prefix_in_kernel) {
             asm volatile("cp.async.wait_group %0;" :: "n"(L::kStages - 2) : "memory");
             __syncwarp();  // the tile is there, and the stage filled next has been read
             feed.issue();
-            C::template tile<D, HC, kWholePages>(stage, min(kTile, cc.len - cc.tile * kTile), lane, s,
+            C::template tile<D, HC, kWholePages>(stage, min(C::kKeys, cc.len - cc.tile * C::kKeys), lane, s,
                                                  tile_scores<C, HC>(p, cc));
             stage += L::kStage;
             if (stage == ring + L::kStages * L::kStage) stage = ring;

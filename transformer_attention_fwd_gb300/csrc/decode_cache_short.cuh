@@ -15,29 +15,28 @@
 namespace attn {
 
 constexpr int kShortWarps = 4;
-constexpr int kShortStages = 4;
 constexpr int kMaxRanks = 8;  // CTAs of a cluster
 // When a cluster takes each unit, with both kernels' times at head dim 128, Hkv 8,
 // Hq 32, page 16:
-//  - a warp has at most 16 tiles by the table's width (one request of 1024, 4096
+//  - a warp has at most 16 tiles of 16 by the table's width (one request of 1024, 4096
 //    and 8192 keys: 6.4, 8.9 and 13.5 us against 9.1, 11.9 and 13.8; of 32768, 64
 //    tiles a warp: 41.1 against 19.8);
 //  - the units fill the GPU at most twice (64 and 96 requests of 200 keys: 10.1 and
 //    12.6 us against 14.6 and 16.6; 256 requests of one key, 4.5 times: 15.3
 //    against 9.8, and 1024 of 200 keys, 18 times: 109 against 77).
-constexpr int kMaxTiles = 16, kMaxFills = 2;
-// A rank more only for over 16 tiles of the unit (8 requests of 200 keys: 4.8, 5.2
+constexpr int kMaxKeys = 256, kMaxFills = 2;  // of a warp
+// A rank more only for over 16 such tiles of the unit (8 requests of 200 keys: 4.8, 5.2
 // and 6.0 us with 1, 2 and 8 CTAs; of 1024: 12.0, 8.9 and 8.5 with 1, 2 and 4).
-constexpr int kRankTiles = 16;
+constexpr int kRankKeys = 256;
 
 template <class C, int D, int HC>
 struct ShortLayout {
     static constexpr int kPerSm = D == 128 ? (HC == 8 ? 3 : 2) : (HC == 8 ? 4 : 3);  // CTAs, as registers allow
-    static constexpr int kPartOff = kShortWarps * kShortStages * C::template kStageBytes<D>;  // the CTA's part [HC][D]
+    static constexpr int kPartOff = kShortWarps * C::kShortStages * C::template kStageBytes<D>;  // the CTA's part [HC][D]
     static constexpr int kMlOff = kPartOff + HC * D * 4;                // the warps' {m, l, mv} [kShortWarps][HC]
     static constexpr int kPartMlOff = kMlOff + kShortWarps * HC * 16;        // the CTA's [HC]
     static constexpr int kBytes = kPartMlOff + HC * 16;
-    static_assert(kShortStages * C::template kStageBytes<D> >= HC * D * 4, "a warp's ring holds its part");
+    static_assert(C::kShortStages * C::template kStageBytes<D> >= HC * D * 4, "a warp's ring holds its part");
     static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "CTAs to an SM");
 };
 
@@ -81,7 +80,7 @@ decode_short_kernel(const CacheParams p, int ranks) {
     using L = ShortLayout<C, D, HC>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint8_t* ring = smem + warp * kShortStages * C::template kStageBytes<D>;
+    uint8_t* ring = smem + warp * C::kShortStages * C::template kStageBytes<D>;
     float* part = reinterpret_cast<float*>(smem + L::kPartOff);
     float4* ml = reinterpret_cast<float4*>(smem + L::kMlOff);
     float4* part_ml = reinterpret_cast<float4*>(smem + L::kPartMlOff);
@@ -95,7 +94,7 @@ decode_short_kernel(const CacheParams p, int ranks) {
     cc.unit = cluster - cc.b * U;
     const int asked = p.seq_lens[cc.b];
     cc.len = clamped(p, asked);
-    cc.tiles = (cc.len + kTile - 1) / kTile;
+    cc.tiles = (cc.len + C::kKeys - 1) / C::kKeys;
     const int hkv = p.chunks == 1 ? cc.unit : cc.unit / p.chunks, chunk = cc.unit - hkv * p.chunks;
     const int heads = min(HC, p.group - chunk * HC);
     const int64_t row0 = static_cast<int64_t>(cc.b) * p.Hq + hkv * p.group + chunk * HC;
@@ -116,20 +115,20 @@ decode_short_kernel(const CacheParams p, int ranks) {
     const int active = min(kShortWarps, max(0, (cc.tiles - rank * kShortWarps * per + per - 1) / per));
     if (count > 0) {
         cc.tile = first;
-        Feed<C, D, kShortStages, kWholePages> feed(p, nullptr, cc, count, ring, lane);
+        Feed<C, D, C::kShortStages, kWholePages> feed(p, nullptr, cc, count, ring, lane);
 #pragma unroll
-        for (int i = 0; i < kShortStages - 1; ++i) feed.issue();
+        for (int i = 0; i < C::kShortStages - 1; ++i) feed.issue();
         UnitState<D, HC> s;
         const uint8_t* stage = ring;
         unit_begin<C, D, HC, kF16>(p, cc, lane, s);
         for (int n = 0; n < count; ++n) {
-            asm volatile("cp.async.wait_group %0;" :: "n"(kShortStages - 2) : "memory");
+            asm volatile("cp.async.wait_group %0;" :: "n"(C::kShortStages - 2) : "memory");
             __syncwarp();  // the tile is there, and the stage filled next has been read
             feed.issue();
-            C::template tile<D, HC, kWholePages>(stage, min(kTile, cc.len - cc.tile * kTile), lane, s,
+            C::template tile<D, HC, kWholePages>(stage, min(C::kKeys, cc.len - cc.tile * C::kKeys), lane, s,
                                                  tile_scores<C, HC>(p, cc));
             stage += C::template kStageBytes<D>;
-            if (stage == ring + kShortStages * C::template kStageBytes<D>) stage = ring;
+            if (stage == ring + C::kShortStages * C::template kStageBytes<D>) stage = ring;
             ++cc.tile;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -145,7 +144,7 @@ decode_short_kernel(const CacheParams p, int ranks) {
             const int h = warp + i * kShortWarps;
             float4 all;
             const Columns<D> acc = m.head(h, active, lane, [&](int k, Columns<D>& x) {
-                x.load(reinterpret_cast<const float*>(smem + k * kShortStages * C::template kStageBytes<D>) + h * D, lane);
+                x.load(reinterpret_cast<const float*>(smem + k * C::kShortStages * C::template kStageBytes<D>) + h * D, lane);
             }, &all);
             if (parts == 1) {  // this CTA had all of the unit
                 if (h >= heads) continue;
@@ -216,13 +215,13 @@ template <class C>
 int decode_short_ranks(const PagedShape& s, int num_sms) {
     const int group = s.Hq / s.Hkv, hc = heads_at_once(group);
     const long long units = static_cast<long long>(s.B) * s.Hkv * ((group + hc - 1) / hc);
-    const long long tiles = (static_cast<long long>(s.max_pages) * s.page + kTile - 1) / kTile;  // at most
+    const long long keys = static_cast<long long>(s.max_pages) * s.page;  // at most
     const int per_sm = s.D == 128 ? (hc == 8 ? ShortLayout<C, 128, 8>::kPerSm : ShortLayout<C, 128, 16>::kPerSm)
                                   : (hc == 8 ? ShortLayout<C, 64, 8>::kPerSm : ShortLayout<C, 64, 16>::kPerSm);
     const long long room = static_cast<long long>(per_sm) * num_sms;
     int ranks = 1;
-    while (ranks < kMaxRanks && 2 * ranks * units <= room && tiles > kRankTiles * ranks) ranks *= 2;
-    return units <= kMaxFills * room && tiles <= kMaxTiles * kShortWarps * ranks ? ranks : 0;
+    while (ranks < kMaxRanks && 2 * ranks * units <= room && keys > kRankKeys * ranks) ranks *= 2;
+    return units <= kMaxFills * room && keys <= kMaxKeys * kShortWarps * ranks ? ranks : 0;
 }
 
 template <class C>

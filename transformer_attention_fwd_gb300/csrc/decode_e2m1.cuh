@@ -18,17 +18,23 @@ __device__ __forceinline__ int chunk4_at(int row, int chunk) {
 }
 
 struct E2m1Cache {
-    // K rows, V rows, their scales.
+    // Two products' keys to a tile: their chains of dependent instructions run side by side,
+    // and one check of the reference serves both.
+    static constexpr int kKeys = 32, kParts = kKeys / kTile;
+    // Of each part: K rows, V rows, their scales.
     template <int D>
-    static constexpr int kStageBytes = 2 * kTile * (D / 2 + D / 16);
+    static constexpr int kPartBytes = 2 * kTile * (D / 2 + D / 16);
+    template <int D>
+    static constexpr int kStageBytes = kParts * kPartBytes<D>;
     static constexpr bool kTwoReferences = false, kFactors = true;
     // The long kernel: CTAs to an SM, as registers allow, and the stages of a warp's ring.
     template <int D, int HC>
     static constexpr int kLongPerSm = D == 128 ? (HC == 8 ? 3 : 2) : (HC == 8 ? 4 : 3);
     template <int D, int HC>
-    static constexpr int kLongStages = D == 128 && HC == 8 ? 5 : 6;
+    static constexpr int kLongStages = D == 128 && HC == 8 ? 2 : 3;
+    static constexpr int kShortStages = 3;
 
-    // Where things are in a stage.
+    // Where things are in a part.
     template <int D>
     struct Stage {
         static constexpr int kV = kTile * D / 2, kScales = 2 * kV, kVScales = kScales + kTile * (D / 16);
@@ -49,10 +55,22 @@ struct E2m1Cache {
                 put[i] = chunk4_at<D>((lane + 32 * i) / kPerRow, (lane + 32 * i) % kPerRow);
         }
 
-        // valid: keys of the tile (kTile and more: all); id, row: of key 0, or (pages that end
-        // inside a tile) of key lane % 16.
+        // valid: keys of the tile (kKeys and more: all); id, row: of key lane, or (pages that hold a
+        // part's keys) of key 0 of part lane / 16.
         __device__ __forceinline__ void issue(const CacheParams& p, uint32_t fill, int id, int row, int hkv,
                                               int valid) const {
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                const int from = i * kTile + (kWholePages ? 0 : lane % kTile);
+                part(p, fill + i * kPartBytes<D>, __shfl_sync(0xffffffffu, id, from), __shfl_sync(0xffffffffu, row, from),
+                     hkv, valid - i * kTile);
+            }
+        }
+
+      private:
+        // id, row: of key 0, or of key lane % 16.
+        __device__ __forceinline__ void part(const CacheParams& p, uint32_t fill, int id, int row, int hkv,
+                                             int valid) const {
             using S = Stage<D>;
             if (kWholePages) {  // one run of rows
                 const int64_t first = (static_cast<int64_t>(id) * 2 * p.Hkv + hkv) * p.page.size + row;
@@ -95,7 +113,6 @@ struct E2m1Cache {
             }
         }
 
-      private:
         // `bytes` of 16, zeros behind them.
         static __device__ __forceinline__ void copy16_part(uint32_t dst, const void* src, int bytes) {
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -114,144 +131,177 @@ struct E2m1Cache {
         using S = Stage<D>;
         constexpr int kR = HC / 8, kS = D / 16, kScaleRow = D / kRowScaleSpan;
         const int g = lane >> 2, t = lane & 3;
-        // Key g's and key g + 8's columns of this lane, D/4 from t * D/4 on, and their scales,
-        // each in both halves of a word.
-        uint32_t kw[2][D / 32], kscale[2][D / 64];
+        float sc[kParts][kR][4], sd[kParts][kR][4];  // two chains of products each
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int row = n * 8 + g;
-            const uint8_t* at = stage + S::kScales + row * kScaleRow;
-            if constexpr (D == 128) {
-                const uint4 u = *reinterpret_cast<const uint4*>(stage + chunk4_at<D>(row, t));
-                kw[n][0] = u.x; kw[n][1] = u.y; kw[n][2] = u.z; kw[n][3] = u.w;
-                const uint32_t f = e4m3_to_f16x2(*reinterpret_cast<const uint16_t*>(at + 2 * t));
-                kscale[n][0] = __byte_perm(f, f, 0x1010);
-                kscale[n][1] = __byte_perm(f, f, 0x3232);
-            } else {
-                const uint2 u = *reinterpret_cast<const uint2*>(stage + chunk4_at<D>(row, t >> 1) + (t & 1) * 8);
-                kw[n][0] = u.x; kw[n][1] = u.y;
-                const uint32_t f = e4m3_to_f16x2(at[t]);
-                kscale[n][0] = __byte_perm(f, f, 0x1010);
-            }
-        }
-        // Keys 2t, 2t + 1, 2t + 8 and 2t + 9: this lane's D/8 columns of V from g * D/8 on, and
-        // the scales, two keys' in a word.
-        uint32_t vw[4][D / 64], vscale[2];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int row = 2 * t + (j & 1) + 8 * (j >> 1);
-            if constexpr (D == 128) {
-                const uint2 u = *reinterpret_cast<const uint2*>(stage + S::kV + chunk4_at<D>(row, g >> 1) + (g & 1) * 8);
-                vw[j][0] = u.x; vw[j][1] = u.y;
-            } else {
-                vw[j][0] = *reinterpret_cast<const uint32_t*>(stage + S::kV + chunk4_at<D>(row, g >> 2) + (g & 3) * 4);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint8_t* at = stage + S::kVScales + (2 * t + 8 * j) * kScaleRow + (D == 128 ? g : g >> 1);
-            vscale[j] = e4m3_to_f16x2(at[0] | (static_cast<uint32_t>(at[kScaleRow]) << 8));
-        }
-        float sc[kR][4], sd[kR][4];  // two chains of products
-#pragma unroll
-        for (int r = 0; r < kR; ++r)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sc[r][i] = sd[r][i] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kS; j += 2) {  // two product steps out of a word of eight columns
-            uint32_t a[2][4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                e2m1_to_f16x8(kw[n][j / 2], a[n]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a[n][i] = f16x2_mul(a[n][i], kscale[n][j / 4]);
-            }
-#pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                mma_f16(sc[r], a[0][0], a[1][0], a[0][1], a[1][1], s.qb[j][r][0], s.qb[j][r][1]);
-                mma_f16(sd[r], a[0][2], a[1][2], a[0][3], a[1][3], s.qb[j + 1][r][0], s.qb[j + 1][r][1]);
-            }
-        }
-        // V^T's operand (with eight heads all of it now, while the products run): the low halves of two
-        // keys' bytes are one column's codes, the high halves the next column's.
-        uint32_t va[kS][4];
-        auto columns = [&](int word, int key, int i0) {  // steps i0 .. i0 + 3, keys `key` of 0 or 2
-            const uint32_t x = vw[key][word], y = vw[key + 1][word];
-            uint32_t even[4], odd[4];
-            e2m1_to_f16x8((x & 0x0f0f0f0fu) | ((y & 0x0f0f0f0fu) << 4), even);
-            e2m1_to_f16x8(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), odd);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                va[i0 + i][key] = f16x2_mul(even[i], vscale[key / 2]);
-                va[i0 + i][key + 1] = f16x2_mul(odd[i], vscale[key / 2]);
-            }
-        };
-        auto convert = [&](int i) {
-            if (i % 4 != 0) return;
-            columns(i / 4, 0, i);
-            columns(i / 4, 2, i);
-        };
-        if (HC == 8)
-#pragma unroll
-            for (int i = 0; i < kS; ++i) convert(i);
-        float x[kR][4], e[kR][4], w[kR][4];  // exponents, the same under the reference, weights
-#pragma unroll
-        for (int r = 0; r < kR; ++r)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[r][i] = (sc[r][i] + sd[r][i]) * s.qs[r][i & 1];
-        if (scores.at != nullptr) {
+        for (int i = 0; i < kParts; ++i)
 #pragma unroll
             for (int r = 0; r < kR; ++r)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = (i >> 1) * 8 + g, h = r * 8 + 2 * t + (i & 1);
-                    if (key < valid && h < scores.heads) scores.at[key * scores.group + h] = x[r][i];
+                for (int n = 0; n < 4; ++n) sc[i][r][n] = sd[i][r][n] = 0.0f;
+        {
+            // Key g's and key g + 8's columns of this lane, D/4 from t * D/4 on, and their scales,
+            // each in both halves of a word.
+            uint32_t kw[kParts][2][D / 32], kscale[kParts][2][D / 64];
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                const uint8_t* part = stage + i * kPartBytes<D>;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int row = n * 8 + g;
+                    const uint8_t* at = part + S::kScales + row * kScaleRow;
+                    if constexpr (D == 128) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(part + chunk4_at<D>(row, t));
+                        kw[i][n][0] = u.x; kw[i][n][1] = u.y; kw[i][n][2] = u.z; kw[i][n][3] = u.w;
+                        const uint32_t f = e4m3_to_f16x2(*reinterpret_cast<const uint16_t*>(at + 2 * t));
+                        kscale[i][n][0] = __byte_perm(f, f, 0x1010);
+                        kscale[i][n][1] = __byte_perm(f, f, 0x3232);
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2*>(part + chunk4_at<D>(row, t >> 1) + (t & 1) * 8);
+                        kw[i][n][0] = u.x; kw[i][n][1] = u.y;
+                        const uint32_t f = e4m3_to_f16x2(at[t]);
+                        kscale[i][n][0] = __byte_perm(f, f, 0x1010);
+                    }
                 }
-        }
-        if (valid < kTile) {  // the unit's last tile
-#pragma unroll
-            for (int r = 0; r < kR; ++r)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if ((i >> 1) * 8 + g >= valid) x[r][i] = -INFINITY;
-        }
-        bool need = false;
-#pragma unroll
-        for (int r = 0; r < kR; ++r)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                e[r][i] = x[r][i] - s.mv[r][i & 1];
-                need |= e[r][i] > kLift + kSlack;
             }
-        if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
-            for (int r = 0; r < kR; ++r) {
+            for (int j = 0; j < kS; j += 2) {  // two product steps out of a word of eight columns
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float mv = fmaxf(s.mv[r][i], heads_max(fmaxf(x[r][i], x[r][i + 2])) - kLift);
-                    const float alpha = ex2_approx(s.mv[r][i] - mv);
-                    s.l[r][i] *= alpha;
-                    s.mv[r][i] = mv;
-                    e[r][i] = x[r][i] - mv;
-                    e[r][i + 2] = x[r][i + 2] - mv;
+                for (int i = 0; i < kParts; ++i) {
+                    uint32_t a[2][4];
 #pragma unroll
-                    for (int j = 0; j < kS; ++j) {
-                        s.o[r][j][i] *= alpha;
-                        s.o[r][j][i + 2] *= alpha;
+                    for (int n = 0; n < 2; ++n) {
+                        e2m1_to_f16x8(kw[i][n][j / 2], a[n]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) a[n][k] = f16x2_mul(a[n][k], kscale[i][n][j / 4]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < kR; ++r) {
+                        mma_f16(sc[i][r], a[0][0], a[1][0], a[0][1], a[1][1], s.qb[j][r][0], s.qb[j][r][1]);
+                        mma_f16(sd[i][r], a[0][2], a[1][2], a[0][3], a[1][3], s.qb[j + 1][r][0], s.qb[j + 1][r][1]);
                     }
                 }
             }
         }
-        float least = INFINITY;
+        float x[kParts][kR][4], e[kParts][kR][4], w[kParts][kR][4];  // exponents, under the reference, weights
 #pragma unroll
-        for (int r = 0; r < kR; ++r)
+        for (int i = 0; i < kParts; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[r][i] = ex2_approx(e[r][i]);
-                s.l[r][i & 1] += w[r][i];
-                least = fminf(least, e[r][i]);
+            for (int r = 0; r < kR; ++r)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) x[i][r][n] = (sc[i][r][n] + sd[i][r][n]) * s.qs[r][n & 1];
+        if (scores.at != nullptr) {
+#pragma unroll
+            for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                for (int r = 0; r < kR; ++r)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int key = i * kTile + (n >> 1) * 8 + g, h = r * 8 + 2 * t + (n & 1);
+                        if (key < valid && h < scores.heads) scores.at[key * scores.group + h] = x[i][r][n];
+                    }
+        }
+        if (valid < kKeys) {  // the unit's last tile
+#pragma unroll
+            for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                for (int r = 0; r < kR; ++r)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        if (i * kTile + (n >> 1) * 8 + g >= valid) x[i][r][n] = -INFINITY;
+        }
+        bool need = false;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    e[i][r][n] = x[i][r][n] - s.mv[r][n & 1];
+                    need |= e[i][r][n] > kLift + kSlack;
+                }
+        if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    float most = fmaxf(x[0][r][n], x[0][r][n + 2]);
+#pragma unroll
+                    for (int i = 1; i < kParts; ++i) most = fmaxf(most, fmaxf(x[i][r][n], x[i][r][n + 2]));
+                    const float mv = fmaxf(s.mv[r][n], heads_max(most) - kLift);
+                    const float alpha = ex2_approx(s.mv[r][n] - mv);
+                    s.l[r][n] *= alpha;
+                    s.mv[r][n] = mv;
+#pragma unroll
+                    for (int i = 0; i < kParts; ++i) {
+                        e[i][r][n] = x[i][r][n] - mv;
+                        e[i][r][n + 2] = x[i][r][n + 2] - mv;
+                    }
+#pragma unroll
+                    for (int j = 0; j < kS; ++j) {
+                        s.o[r][j][n] *= alpha;
+                        s.o[r][j][n + 2] *= alpha;
+                    }
+                }
             }
-        weighted_rows<D, HC>(e, w, least, va, convert, s);
+        }
+        float least[kParts];
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            least[i] = INFINITY;
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    w[i][r][n] = ex2_approx(e[i][r][n]);
+                    s.l[r][n & 1] += w[i][r][n];
+                    least[i] = fminf(least[i], e[i][r][n]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            // Keys 2t, 2t + 1, 2t + 8 and 2t + 9: this lane's D/8 columns of V from g * D/8 on, and
+            // the scales, two keys' in a word.
+            const uint8_t* part = stage + i * kPartBytes<D>;
+            uint32_t vw[4][D / 64], vscale[2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = 2 * t + (j & 1) + 8 * (j >> 1);
+                if constexpr (D == 128) {
+                    const uint2 u = *reinterpret_cast<const uint2*>(part + S::kV + chunk4_at<D>(row, g >> 1) + (g & 1) * 8);
+                    vw[j][0] = u.x; vw[j][1] = u.y;
+                } else {
+                    vw[j][0] = *reinterpret_cast<const uint32_t*>(part + S::kV + chunk4_at<D>(row, g >> 2) + (g & 3) * 4);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint8_t* at = part + S::kVScales + (2 * t + 8 * j) * kScaleRow + (D == 128 ? g : g >> 1);
+                vscale[j] = e4m3_to_f16x2(at[0] | (static_cast<uint32_t>(at[kScaleRow]) << 8));
+            }
+            // V^T's operand, eight columns of a lane at a time: the low halves of two keys' bytes are
+            // one column's codes, the high halves the next column's.
+            uint32_t va[kS][4];
+            auto columns = [&](int word, int key, int i0) {  // steps i0 .. i0 + 3, keys `key` of 0 or 2
+                const uint32_t u = vw[key][word], v = vw[key + 1][word];
+                uint32_t even[4], odd[4];
+                e2m1_to_f16x8((u & 0x0f0f0f0fu) | ((v & 0x0f0f0f0fu) << 4), even);
+                e2m1_to_f16x8(((u >> 4) & 0x0f0f0f0fu) | (v & 0xf0f0f0f0u), odd);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    va[i0 + k][key] = f16x2_mul(even[k], vscale[key / 2]);
+                    va[i0 + k][key + 1] = f16x2_mul(odd[k], vscale[key / 2]);
+                }
+            };
+            auto convert = [&](int k) {
+                if (k % 4 != 0) return;
+                columns(k / 4, 0, k);
+                columns(k / 4, 2, k);
+            };
+            if (HC == 8)
+#pragma unroll
+                for (int k = 0; k < kS; ++k) convert(k);
+            weighted_rows<D, HC>(e[i], w[i], least[i], va, convert, s);
+        }
     }
 };
 

@@ -27,6 +27,7 @@ __device__ __forceinline__ void load_v(const uint8_t* rows, int row, int g, uint
 }
 
 struct E4m3Cache {
+    static constexpr int kKeys = kTile;
     // K rows, V rows, their scales.
     template <int D>
     static constexpr int kStageBytes = 2 * kTile * D + 2 * kTile * 4;
@@ -36,6 +37,7 @@ struct E4m3Cache {
     static constexpr int kLongPerSm = D == 128 ? (HC == 8 ? 3 : 2) : (HC == 8 ? 4 : 3);
     template <int D, int HC>
     static constexpr int kLongStages = HC == 8 ? 3 : 4;
+    static constexpr int kShortStages = 4;
 
     // Where a lane's copies go in a stage: row r0 + i * kRowsPer, chunk col.  The
     // chunks' order repeats every eight rows.
