@@ -257,45 +257,44 @@ struct E2m1Cache {
                     least[i] = fminf(least[i], e[i][r][n]);
                 }
         }
+        if (__all_sync(0xffffffffu, fminf(least[0], least[kParts - 1]) >= -kLow)) {
+            // In one stretch, so that a part's operand is made under the other's products.
+            Weights pb[kParts][kR][2];
+#pragma unroll
+            for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    pb[i][r][0].set(w[i][r][0], w[i][r][1]);
+                    pb[i][r][1].set(w[i][r][2], w[i][r][3]);
+                }
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                const Values<D> v(stage + i * kPartBytes<D>, g, t);
+#pragma unroll
+                for (int j = 0; j < kS; j += 4) {
+                    uint32_t va[4][4];
+                    v.columns(j / 4, va);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) {
+                            mma_f16(s.o[r][j + k], va[k][0], va[k][1], va[k][2], va[k][3], pb[i][r][0].hi, pb[i][r][1].hi);
+                            mma_f16(s.o[r][j + k], va[k][0], va[k][1], va[k][2], va[k][3], pb[i][r][0].lo, pb[i][r][1].lo);
+                        }
+                }
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-            // Keys 2t, 2t + 1, 2t + 8 and 2t + 9: this lane's D/8 columns of V from g * D/8 on, and
-            // the scales, two keys' in a word.
-            const uint8_t* part = stage + i * kPartBytes<D>;
-            uint32_t vw[4][D / 64], vscale[2];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = 2 * t + (j & 1) + 8 * (j >> 1);
-                if constexpr (D == 128) {
-                    const uint2 u = *reinterpret_cast<const uint2*>(part + S::kV + chunk4_at<D>(row, g >> 1) + (g & 1) * 8);
-                    vw[j][0] = u.x; vw[j][1] = u.y;
-                } else {
-                    vw[j][0] = *reinterpret_cast<const uint32_t*>(part + S::kV + chunk4_at<D>(row, g >> 2) + (g & 3) * 4);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint8_t* at = part + S::kVScales + (2 * t + 8 * j) * kScaleRow + (D == 128 ? g : g >> 1);
-                vscale[j] = e4m3_to_f16x2(at[0] | (static_cast<uint32_t>(at[kScaleRow]) << 8));
-            }
-            // V^T's operand, eight columns of a lane at a time: the low halves of two keys' bytes are
-            // one column's codes, the high halves the next column's.
+            const Values<D> v(stage + i * kPartBytes<D>, g, t);
             uint32_t va[kS][4];
-            auto columns = [&](int word, int key, int i0) {  // steps i0 .. i0 + 3, keys `key` of 0 or 2
-                const uint32_t u = vw[key][word], v = vw[key + 1][word];
-                uint32_t even[4], odd[4];
-                e2m1_to_f16x8((u & 0x0f0f0f0fu) | ((v & 0x0f0f0f0fu) << 4), even);
-                e2m1_to_f16x8(((u >> 4) & 0x0f0f0f0fu) | (v & 0xf0f0f0f0u), odd);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    va[i0 + k][key] = f16x2_mul(even[k], vscale[key / 2]);
-                    va[i0 + k][key + 1] = f16x2_mul(odd[k], vscale[key / 2]);
-                }
-            };
             auto convert = [&](int k) {
                 if (k % 4 != 0) return;
-                columns(k / 4, 0, k);
-                columns(k / 4, 2, k);
+                uint32_t c[4][4];
+                v.columns(k / 4, c);
+#pragma unroll
+                for (int n = 0; n < 16; ++n) va[k + n / 4][n % 4] = c[n / 4][n % 4];
             };
             if (HC == 8)
 #pragma unroll
@@ -303,6 +302,49 @@ struct E2m1Cache {
             weighted_rows<D, HC>(e[i], w[i], least[i], va, convert, s);
         }
     }
+
+  private:
+    // A part's V as this lane needs it: keys 2t, 2t + 1, 2t + 8 and 2t + 9, D/8 columns from
+    // g * D/8 on, and the scales, two keys' in a word.
+    template <int D>
+    struct Values {
+        uint32_t w[4][D / 64], scale[2];
+        __device__ __forceinline__ Values(const uint8_t* part, int g, int t) {
+            using S = Stage<D>;
+            constexpr int kScaleRow = D / kRowScaleSpan;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = 2 * t + (j & 1) + 8 * (j >> 1);
+                if constexpr (D == 128) {
+                    const uint2 u = *reinterpret_cast<const uint2*>(part + S::kV + chunk4_at<D>(row, g >> 1) + (g & 1) * 8);
+                    w[j][0] = u.x; w[j][1] = u.y;
+                } else {
+                    w[j][0] = *reinterpret_cast<const uint32_t*>(part + S::kV + chunk4_at<D>(row, g >> 2) + (g & 3) * 4);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint8_t* at = part + S::kVScales + (2 * t + 8 * j) * kScaleRow + (D == 128 ? g : g >> 1);
+                scale[j] = e4m3_to_f16x2(at[0] | (static_cast<uint32_t>(at[kScaleRow]) << 8));
+            }
+        }
+        // V^T's operand of eight columns, two to a product step: the low halves of two keys' bytes are
+        // one column's codes, the high halves the next column's.
+        __device__ __forceinline__ void columns(int word, uint32_t (&va)[4][4]) const {
+#pragma unroll
+            for (int key = 0; key < 4; key += 2) {
+                const uint32_t u = w[key][word], v = w[key + 1][word];
+                uint32_t even[4], odd[4];
+                e2m1_to_f16x8((u & 0x0f0f0f0fu) | ((v & 0x0f0f0f0fu) << 4), even);
+                e2m1_to_f16x8(((u >> 4) & 0x0f0f0f0fu) | (v & 0xf0f0f0f0u), odd);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    va[k][key] = f16x2_mul(even[k], scale[key / 2]);
+                    va[k][key + 1] = f16x2_mul(odd[k], scale[key / 2]);
+                }
+            }
+        }
+    };
 };
 
 }  // namespace attn
