@@ -4,6 +4,7 @@
 // and how.  What depends on the cache's format is in a class C (E4m3Cache, E2m1Cache):
 //   kKeys             keys of a tile, 16 or 32
 //   kStageBytes<D>    a tile in shared memory
+//   kFourHeads        up to four heads have a kernel of their own
 //   kTwoReferences    the weights' sum and the weighted sum have references of their own
 //   kFactors          K and V have a factor for each head
 //   Copies<D, kWhole> a lane's copies of a tile
@@ -115,11 +116,17 @@ __device__ __forceinline__ float elem_f32(uint16_t x) {
     return kF16 ? f16_lo_to_f32(x) : bf16_lo_to_f32(x);
 }
 
+// Columns of the products: eight to a half.  Four heads fill one half twice: the second four
+// columns hold the same queries, and of the weights the second terms, whose products then
+// cost nothing; a head's weighted sum is that of its two columns.
+template <int HC>
+constexpr int kHalves = HC < 8 ? 1 : HC / 8;
+
 // The state of the unit a warp is in.  Lane (g, t) = (lane / 4, lane % 4) works
 // on heads 2t and 2t + 1 (of each half of eight).
 template <int D, int HC>
 struct UnitState {
-    static constexpr int kR = HC / 8;       // halves of eight heads
+    static constexpr int kR = kHalves<HC>;
     uint32_t qb[D / 16][kR][2];             // Q^T operand: head g, two runs of inner indices
     float qs[kR][2];                        // what a product with it is multiplied by
     float m[kR][2], l[kR][2], mv[kR][2];    // reference and this lane's sum of the p; O's reference
@@ -143,8 +150,8 @@ __device__ __forceinline__ void unit_begin(const CacheParams& p, const Cursor& c
     const int heads = min(HC, p.group - chunk * HC);
     const int hq0 = hkv * p.group + chunk * HC;
 #pragma unroll
-    for (int r = 0; r < HC / 8; ++r) {
-        const int h = r * 8 + g;
+    for (int r = 0; r < kHalves<HC>; ++r) {
+        const int h = HC < 8 ? g % HC : r * 8 + g;
         uint32_t w[D / 8];  // the lane's D/4 columns, t * D/4 on
         float most = 0.0f;
         if (h < heads) {
@@ -321,13 +328,19 @@ struct MergedHeads {
     }
 };
 
-// Two weights as two terms each, P^T's operand.
+// Two weights as two terms each, P^T's operand; with four heads in one word, the second terms
+// in the second four columns.
+template <int HC>
 struct Weights {
     uint32_t hi, lo;
-    __device__ __forceinline__ void set(float a, float b) {
-        const uint32_t h = pack_f16x2(a, b);
-        hi = transpose8x8(h);
-        lo = transpose8x8(pack_f16x2(a - f16_lo_to_f32(h), b - f16_hi_to_f32(h)));
+    __device__ __forceinline__ void set(float a, float b, int t) {
+        const uint32_t h = pack_f16x2(a, b), l = pack_f16x2(a - f16_lo_to_f32(h), b - f16_hi_to_f32(h));
+        if (HC < 8) {
+            hi = transpose8x8(t < HC / 2 ? h : l);
+        } else {
+            hi = transpose8x8(h);
+            lo = transpose8x8(l);
+        }
     }
 };
 
@@ -349,23 +362,24 @@ __device__ __forceinline__ float heaviest(float& e0, float& e1, float& w0, float
 // exponent; va, V^T's operand (with more than eight heads made by convert(i), column
 // pair by column pair).
 template <int D, int HC, typename Convert>
-__device__ __forceinline__ void weighted_rows(float (&e)[HC / 8][4], float (&w)[HC / 8][4], float least,
-                                              uint32_t (&va)[D / 16][4], Convert convert, UnitState<D, HC>& s) {
-    constexpr int kR = HC / 8, kS = D / 16;
+__device__ __forceinline__ void weighted_rows(float (&e)[kHalves<HC>][4], float (&w)[kHalves<HC>][4], float least,
+                                              uint32_t (&va)[D / 16][4], Convert convert, int lane, UnitState<D, HC>& s) {
+    constexpr int kR = kHalves<HC>, kS = D / 16;
+    const int t = lane & 3;
     if (__all_sync(0xffffffffu, least >= -kLow)) {
-        Weights pb[kR][2];
+        Weights<HC> pb[kR][2];
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
-            pb[r][0].set(w[r][0], w[r][1]);
-            pb[r][1].set(w[r][2], w[r][3]);
+            pb[r][0].set(w[r][0], w[r][1], t);
+            pb[r][1].set(w[r][2], w[r][3], t);
         }
 #pragma unroll
         for (int i = 0; i < kS; ++i) {
-            if (HC != 8) convert(i);
+            if (HC > 8) convert(i);
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
                 mma_f16(s.o[r][i], va[i][0], va[i][1], va[i][2], va[i][3], pb[r][0].hi, pb[r][1].hi);
-                mma_f16(s.o[r][i], va[i][0], va[i][1], va[i][2], va[i][3], pb[r][0].lo, pb[r][1].lo);
+                if (HC >= 8) mma_f16(s.o[r][i], va[i][0], va[i][1], va[i][2], va[i][3], pb[r][0].lo, pb[r][1].lo);
             }
         }
         return;
@@ -376,27 +390,27 @@ __device__ __forceinline__ void weighted_rows(float (&e)[HC / 8][4], float (&w)[
     // heavy key with an empty value still has the others'.
     bool more = true;
     while (more) {
-        Weights pb[kR][2];
+        Weights<HC> pb[kR][2];
         float back[kR][2];
         float most = -INFINITY;
         auto half = [&](int r) {
             back[r][0] = heaviest(e[r][0], e[r][2], w[r][0], w[r][2]);
             back[r][1] = heaviest(e[r][1], e[r][3], w[r][1], w[r][3]);
             most = fmaxf(most, fmaxf(fmaxf(e[r][0], e[r][1]), fmaxf(e[r][2], e[r][3])));
-            pb[r][0].set(w[r][0], w[r][1]);
-            pb[r][1].set(w[r][2], w[r][3]);
+            pb[r][0].set(w[r][0], w[r][1], t);
+            pb[r][1].set(w[r][2], w[r][3], t);
         };
         half(0);  // (a loop here is not unrolled, and puts the arrays in memory)
         if (kR == 2) half(kR - 1);
         more = __any_sync(0xffffffffu, most > -kGone);
 #pragma unroll
         for (int i = 0; i < kS; ++i) {
-            if (HC != 8) convert(i);
+            if (HC > 8) convert(i);
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
                 float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 mma_f16(part, va[i][0], va[i][1], va[i][2], va[i][3], pb[r][0].hi, pb[r][1].hi);
-                mma_f16(part, va[i][0], va[i][1], va[i][2], va[i][3], pb[r][0].lo, pb[r][1].lo);
+                if (HC >= 8) mma_f16(part, va[i][0], va[i][1], va[i][2], va[i][3], pb[r][0].lo, pb[r][1].lo);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) s.o[r][i][n] = fmaf(part[n], back[r][n & 1], s.o[r][i][n]);
             }
@@ -462,13 +476,19 @@ struct Feed {
     }
 };
 
+// A head's sum out of this column and, with four heads, of its second one.
+template <int HC>
+__device__ __forceinline__ float head_sum(float o) {
+    return HC < 8 ? o + __shfl_xor_sync(0xffffffffu, o, 2) : o;
+}
+
 // The unit's result: a warp had all its keys.
 template <class C, int D, int HC, bool kF16>
 __device__ __forceinline__ void unit_out(const UnitState<D, HC>& s, const CacheParams& p, int hkv, int64_t row0,
                                          int heads, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int r = 0; r < HC / 8; ++r) {
+    for (int r = 0; r < kHalves<HC>; ++r) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int h = r * 8 + 2 * t + i;
@@ -477,8 +497,8 @@ __device__ __forceinline__ void unit_out(const UnitState<D, HC>& s, const CacheP
             float c[D / 8];
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
-                c[2 * j] = out_of(s.o[r][j][i], f);
-                c[2 * j + 1] = out_of(s.o[r][j][i + 2], f);
+                c[2 * j] = out_of(head_sum<HC>(s.o[r][j][i]), f);
+                c[2 * j + 1] = out_of(head_sum<HC>(s.o[r][j][i + 2]), f);
             }
             if (h < heads) store_row<kF16>(p.o + (row0 + h) * D + g * (D / 8), c);
             if (p.lse && g == 0 && h < heads) p.lse[row0 + h] = (m + __log2f(l)) * kLn2;
@@ -491,16 +511,18 @@ template <class C, int D, int HC>
 __device__ __forceinline__ void unit_piece(const UnitState<D, HC>& s, float* piece, float4* ml, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int r = 0; r < HC / 8; ++r) {
+    for (int r = 0; r < kHalves<HC>; ++r) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int h = r * 8 + 2 * t + i;
             const float l = heads_sum(s.l[r][i]);
 #pragma unroll
-            for (int j = 0; j < D / 16; j += 2)
-                *reinterpret_cast<float4*>(piece + h * D + g * (D / 8) + 2 * j) =
-                    make_float4(s.o[r][j][i], s.o[r][j][i + 2], s.o[r][j + 1][i], s.o[r][j + 1][i + 2]);
-            if (g == 0) ml[h] = make_float4(C::kTwoReferences ? s.m[r][i] : s.mv[r][i], l, s.mv[r][i], 0.0f);
+            for (int j = 0; j < D / 16; j += 2) {
+                const float4 c = make_float4(head_sum<HC>(s.o[r][j][i]), head_sum<HC>(s.o[r][j][i + 2]),
+                                             head_sum<HC>(s.o[r][j + 1][i]), head_sum<HC>(s.o[r][j + 1][i + 2]));
+                if (h < HC) *reinterpret_cast<float4*>(piece + h * D + g * (D / 8) + 2 * j) = c;
+            }
+            if (g == 0 && h < HC) ml[h] = make_float4(C::kTwoReferences ? s.m[r][i] : s.mv[r][i], l, s.mv[r][i], 0.0f);
         }
     }
 }
@@ -517,11 +539,29 @@ __device__ __forceinline__ TileScores tile_scores(const CacheParams& p, const Cu
     return t;
 }
 
-// Query heads a CTA serves at a time: one or two 8-row halves of the product.
-inline int heads_at_once(int group) { return group <= 8 ? 8 : 16; }
+// Query heads a CTA serves at a time: one or two 8-row halves of the product, or half a one.
+template <class C>
+int heads_at_once(int group) {
+    return C::kFourHeads && group <= 4 ? 4 : group <= 8 ? 8 : 16;
+}
+
+template <int N>
+struct IntArg {
+    static constexpr int value = N;
+};
+// f(head dim, heads at once), as IntArg, for a call.
+template <class C, typename F>
+auto by_shape(int D, int group, F f) {
+    const int hc = heads_at_once<C>(group);
+    if constexpr (C::kFourHeads)
+        if (hc == 4) return D == 64 ? f(IntArg<64>{}, IntArg<4>{}) : f(IntArg<128>{}, IntArg<4>{});
+    if (hc == 8) return D == 64 ? f(IntArg<64>{}, IntArg<8>{}) : f(IntArg<128>{}, IntArg<8>{});
+    return D == 64 ? f(IntArg<64>{}, IntArg<16>{}) : f(IntArg<128>{}, IntArg<16>{});
+}
 
 // What every format's launch sets.
-inline CacheParams cache_params(const uint16_t* q, const uint8_t* kv, const int32_t* block_table,
+template <class C>
+CacheParams cache_params(const uint16_t* q, const uint8_t* kv, const int32_t* block_table,
                                 const int32_t* seq_lens, uint16_t* o, float* lse, const PagedShape& s,
                                 const LaunchEnv& env) {
     CacheParams p{};
@@ -537,7 +577,7 @@ inline CacheParams cache_params(const uint16_t* q, const uint8_t* kv, const int3
     p.Hq = s.Hq;
     p.Hkv = s.Hkv;
     p.group = s.Hq / s.Hkv;
-    const int hc = heads_at_once(p.group);
+    const int hc = heads_at_once<C>(p.group);
     p.chunks = (p.group + hc - 1) / hc;
     p.max_pages = s.max_pages;
     p.num_blocks = s.num_blocks;

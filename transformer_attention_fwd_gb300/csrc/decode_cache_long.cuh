@@ -304,16 +304,17 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode_combine_pieces_kern
 
 template <class C>
 int long_per_sm(const PagedShape& s) {
-    if (heads_at_once(s.Hq / s.Hkv) == 8) return s.D == 64 ? LongLayout<C, 64, 8>::kPerSm : LongLayout<C, 128, 8>::kPerSm;
-    return s.D == 64 ? LongLayout<C, 64, 16>::kPerSm : LongLayout<C, 128, 16>::kPerSm;
+    return by_shape<C>(s.D, s.Hq / s.Hkv, [](auto d, auto h) {
+        return LongLayout<C, decltype(d)::value, decltype(h)::value>::kPerSm;
+    });
 }
 
 // Workspace: cum (long long [B + 1]), geom (longlong2), first (int4 [grid]), the
 // pieces of the cut units and their references and sums.
 struct WsLayout {
     size_t geom, first, ws_o, ws_ml, bytes;
-    WsLayout(const PagedShape& s, int grid) {
-        const size_t rows = 2ull * grid * heads_at_once(s.Hq / s.Hkv);
+    WsLayout(const PagedShape& s, int grid, int heads) {
+        const size_t rows = 2ull * grid * heads;
         auto up16 = [](size_t x) { return (x + 15) / 16 * 16; };
         geom = up16(8ull * (s.B + 1));
         first = geom + sizeof(longlong2);
@@ -359,7 +360,7 @@ template <class C>
 cudaError_t launch_decode_long(CacheParams p, const PagedShape& s, void* ws, const LaunchEnv& env, int* grid_out,
                                int* kernels_launched) {
     const int grid = long_per_sm<C>(s) * env.num_sms;
-    const WsLayout lay(s, grid);
+    const WsLayout lay(s, grid, heads_at_once<C>(p.group));
     uint8_t* base = static_cast<uint8_t*>(ws);
     const bool prefix = s.B <= kMaxPrefixB;
     p.cum = prefix ? nullptr : reinterpret_cast<long long*>(base);
@@ -374,14 +375,10 @@ cudaError_t launch_decode_long(CacheParams p, const PagedShape& s, void* ws, con
         e = cudaGetLastError();
     }
     const bool f16 = s.f16 != 0, whole = s.page % kTile == 0;
-    if (e == cudaSuccess) {
-        if (s.D == 64)
-            e = heads_at_once(p.group) == 8 ? launch_types<C, 64, 8>(p, f16, whole, grid, prefix, env)
-                        : launch_types<C, 64, 16>(p, f16, whole, grid, prefix, env);
-        else
-            e = heads_at_once(p.group) == 8 ? launch_types<C, 128, 8>(p, f16, whole, grid, prefix, env)
-                        : launch_types<C, 128, 16>(p, f16, whole, grid, prefix, env);
-    }
+    if (e == cudaSuccess)
+        e = by_shape<C>(s.D, p.group, [&](auto d, auto h) {
+            return launch_types<C, decltype(d)::value, decltype(h)::value>(p, f16, whole, grid, prefix, env);
+        });
     *grid_out = grid;
     *kernels_launched = (prefix ? 1 : 2) + (grid > 1 ? 1 : 0);
     return e;
@@ -389,7 +386,7 @@ cudaError_t launch_decode_long(CacheParams p, const PagedShape& s, void* ws, con
 
 template <class C>
 size_t decode_long_workspace(const PagedShape& s, int num_sms) {
-    return WsLayout(s, long_per_sm<C>(s) * num_sms).bytes;
+    return WsLayout(s, long_per_sm<C>(s) * num_sms, heads_at_once<C>(s.Hq / s.Hkv)).bytes;
 }
 
 }  // namespace attn

@@ -31,7 +31,7 @@ constexpr int kRankKeys = 256;
 
 template <class C, int D, int HC>
 struct ShortLayout {
-    static constexpr int kPerSm = D == 128 ? (HC == 8 ? 3 : 2) : (HC == 8 ? 4 : 3);  // CTAs, as registers allow
+    static constexpr int kPerSm = D == 128 ? (HC <= 8 ? 3 : 2) : (HC <= 8 ? 4 : 3);  // CTAs, as registers allow
     static constexpr int kPartOff = kShortWarps * C::kShortStages * C::template kStageBytes<D>;  // the CTA's part [HC][D]
     static constexpr int kMlOff = kPartOff + HC * D * 4;                // the warps' {m, l, mv} [kShortWarps][HC]
     static constexpr int kPartMlOff = kMlOff + kShortWarps * HC * 16;        // the CTA's [HC]
@@ -213,11 +213,12 @@ cudaError_t launch_short_types(const CacheParams& p, bool f16, bool whole, int r
 // CTAs of a cluster that takes each unit; 0: the long kernel takes the call.
 template <class C>
 int decode_short_ranks(const PagedShape& s, int num_sms) {
-    const int group = s.Hq / s.Hkv, hc = heads_at_once(group);
+    const int group = s.Hq / s.Hkv, hc = heads_at_once<C>(group);
     const long long units = static_cast<long long>(s.B) * s.Hkv * ((group + hc - 1) / hc);
     const long long keys = static_cast<long long>(s.max_pages) * s.page;  // at most
-    const int per_sm = s.D == 128 ? (hc == 8 ? ShortLayout<C, 128, 8>::kPerSm : ShortLayout<C, 128, 16>::kPerSm)
-                                  : (hc == 8 ? ShortLayout<C, 64, 8>::kPerSm : ShortLayout<C, 64, 16>::kPerSm);
+    const int per_sm = by_shape<C>(s.D, group, [](auto d, auto h) {
+        return ShortLayout<C, decltype(d)::value, decltype(h)::value>::kPerSm;
+    });
     const long long room = static_cast<long long>(per_sm) * num_sms;
     int ranks = 1;
     while (ranks < kMaxRanks && 2 * ranks * units <= room && keys > kRankKeys * ranks) ranks *= 2;
@@ -230,11 +231,9 @@ cudaError_t launch_decode_short(const CacheParams& p, const PagedShape& s, int r
     const unsigned grid = static_cast<unsigned>(s.B) * static_cast<unsigned>(p.Hkv * p.chunks) * ranks;
     const bool f16 = s.f16 != 0, whole = s.page % kTile == 0;
     *grid_out = static_cast<int>(grid);
-    if (heads_at_once(p.group) == 8)
-        return s.D == 64 ? launch_short_types<C, 64, 8>(p, f16, whole, ranks, grid, env)
-                         : launch_short_types<C, 128, 8>(p, f16, whole, ranks, grid, env);
-    return s.D == 64 ? launch_short_types<C, 64, 16>(p, f16, whole, ranks, grid, env)
-                     : launch_short_types<C, 128, 16>(p, f16, whole, ranks, grid, env);
+    return by_shape<C>(s.D, p.group, [&](auto d, auto h) {
+        return launch_short_types<C, decltype(d)::value, decltype(h)::value>(p, f16, whole, ranks, grid, env);
+    });
 }
 
 }  // namespace attn

@@ -78,7 +78,7 @@ cudaError_t launch_decode_paged_e2m1(const uint16_t* q, const uint8_t* kv, const
                                      const int32_t* block_table, const int32_t* seq_lens, uint16_t* o, float* lse,
                                      float* weights, void* ws, const PagedShape& s, const LaunchEnv& env,
                                      int* grid_out, int* kernels_launched) {
-    CacheParams p = cache_params(q, kv, block_table, seq_lens, o, lse, s, env);
+    CacheParams p = cache_params<E2m1Cache>(q, kv, block_table, seq_lens, o, lse, s, env);
     p.row_scales = scales;
     p.factors = factors;
     if (weights) {

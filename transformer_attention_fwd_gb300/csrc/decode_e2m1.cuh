@@ -26,12 +26,12 @@ struct E2m1Cache {
     static constexpr int kPartBytes = 2 * kTile * (D / 2 + D / 16);
     template <int D>
     static constexpr int kStageBytes = kParts * kPartBytes<D>;
-    static constexpr bool kTwoReferences = false, kFactors = true;
+    static constexpr bool kFourHeads = true, kTwoReferences = false, kFactors = true;
     // The long kernel: CTAs to an SM, as registers allow, and the stages of a warp's ring.
     template <int D, int HC>
-    static constexpr int kLongPerSm = D == 128 ? (HC == 8 ? 3 : 2) : (HC == 8 ? 4 : 3);
+    static constexpr int kLongPerSm = D == 128 ? (HC <= 8 ? 3 : 2) : (HC <= 8 ? 4 : 3);
     template <int D, int HC>
-    static constexpr int kLongStages = D == 128 && HC == 8 ? 2 : 3;
+    static constexpr int kLongStages = D == 128 && HC <= 8 ? 2 : 3;
     static constexpr int kShortStages = 3;
 
     // Where things are in a part.
@@ -129,7 +129,7 @@ struct E2m1Cache {
     static __device__ __forceinline__ void tile(const uint8_t* stage, int valid, int lane, UnitState<D, HC>& s,
                                                 const TileScores& scores) {
         using S = Stage<D>;
-        constexpr int kR = HC / 8, kS = D / 16, kScaleRow = D / kRowScaleSpan;
+        constexpr int kR = kHalves<HC>, kS = D / 16, kScaleRow = D / kRowScaleSpan;
         const int g = lane >> 2, t = lane & 3;
         float sc[kParts][kR][4], sd[kParts][kR][4];  // two chains of products each
 #pragma unroll
@@ -259,13 +259,13 @@ struct E2m1Cache {
         }
         if (__all_sync(0xffffffffu, fminf(least[0], least[kParts - 1]) >= -kLow)) {
             // In one stretch, so that a part's operand is made under the other's products.
-            Weights pb[kParts][kR][2];
+            Weights<HC> pb[kParts][kR][2];
 #pragma unroll
             for (int i = 0; i < kParts; ++i)
 #pragma unroll
                 for (int r = 0; r < kR; ++r) {
-                    pb[i][r][0].set(w[i][r][0], w[i][r][1]);
-                    pb[i][r][1].set(w[i][r][2], w[i][r][3]);
+                    pb[i][r][0].set(w[i][r][0], w[i][r][1], t);
+                    pb[i][r][1].set(w[i][r][2], w[i][r][3], t);
                 }
 #pragma unroll
             for (int i = 0; i < kParts; ++i) {
@@ -279,7 +279,9 @@ struct E2m1Cache {
 #pragma unroll
                         for (int r = 0; r < kR; ++r) {
                             mma_f16(s.o[r][j + k], va[k][0], va[k][1], va[k][2], va[k][3], pb[i][r][0].hi, pb[i][r][1].hi);
-                            mma_f16(s.o[r][j + k], va[k][0], va[k][1], va[k][2], va[k][3], pb[i][r][0].lo, pb[i][r][1].lo);
+                            if (HC >= 8)
+                                mma_f16(s.o[r][j + k], va[k][0], va[k][1], va[k][2], va[k][3], pb[i][r][0].lo,
+                                        pb[i][r][1].lo);
                         }
                 }
             }
@@ -296,10 +298,10 @@ struct E2m1Cache {
 #pragma unroll
                 for (int n = 0; n < 16; ++n) va[k + n / 4][n % 4] = c[n / 4][n % 4];
             };
-            if (HC == 8)
+            if (HC <= 8)
 #pragma unroll
                 for (int k = 0; k < kS; ++k) convert(k);
-            weighted_rows<D, HC>(e[i], w[i], least[i], va, convert, s);
+            weighted_rows<D, HC>(e[i], w[i], least[i], va, convert, lane, s);
         }
     }
 

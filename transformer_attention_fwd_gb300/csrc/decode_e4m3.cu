@@ -64,7 +64,7 @@ cudaError_t launch_decode_paged_e4m3(const uint16_t* q, const uint8_t* kv, const
                                      const int32_t* block_table, const int32_t* seq_lens,
                                      uint16_t* o, float* lse, void* ws, const PagedShape& s,
                                      const LaunchEnv& env, int* grid_out, int* kernels_launched) {
-    CacheParams p = cache_params(q, kv, block_table, seq_lens, o, lse, s, env);
+    CacheParams p = cache_params<E4m3Cache>(q, kv, block_table, seq_lens, o, lse, s, env);
     p.scales = scales;
     if (const int ranks = decode_e4m3_short_ranks(s, env.num_sms); ranks > 0) {
         *kernels_launched = 1;

@@ -31,7 +31,7 @@ struct E4m3Cache {
     // K rows, V rows, their scales.
     template <int D>
     static constexpr int kStageBytes = 2 * kTile * D + 2 * kTile * 4;
-    static constexpr bool kTwoReferences = true, kFactors = false;
+    static constexpr bool kFourHeads = false, kTwoReferences = true, kFactors = false;
     // The long kernel: CTAs to an SM, as registers allow, and the stages of a warp's ring.
     template <int D, int HC>
     static constexpr int kLongPerSm = D == 128 ? (HC == 8 ? 3 : 2) : (HC == 8 ? 4 : 3);
@@ -199,7 +199,7 @@ struct E4m3Cache {
                 w[r][i] = ex2_approx(e[r][i]);
                 least = fminf(least, e[r][i]);
             }
-        weighted_rows<D, HC>(e, w, least, va, convert, s);
+        weighted_rows<D, HC>(e, w, least, va, convert, lane, s);
     }
 };
 
