@@ -47,7 +47,15 @@ __global__ void __launch_bounds__(kAddThreads) add_scores_kernel(const CachePara
             if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) continue;  // reported by the decode
             const float* x = scores + static_cast<int64_t>(key) * p.group;
             float sum = 0.0f;
-            for (int h = 0; h < p.group; ++h) sum += ex2_approx(x[h] - lse[h] * kLog2e);
+            if (p.group % 4 == 0) {  // 16 bytes at a time: the workspace is aligned to them
+                for (int h = 0; h < p.group; h += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(x + h);
+                    sum += (ex2_approx(v.x - lse[h] * kLog2e) + ex2_approx(v.y - lse[h + 1] * kLog2e)) +
+                           (ex2_approx(v.z - lse[h + 2] * kLog2e) + ex2_approx(v.w - lse[h + 3] * kLog2e));
+                }
+            } else {
+                for (int h = 0; h < p.group; ++h) sum += ex2_approx(x[h] - lse[h] * kLog2e);
+            }
             float* w = weights + (static_cast<int64_t>(id) * p.Hkv + hkv) * p.page.size + row;
             *w += sum;
         }
@@ -97,9 +105,10 @@ cudaError_t launch_decode_paged_e2m1(const uint16_t* q, const uint8_t* kv, const
     if (e != cudaSuccess || !weights) return e;
     ++*kernels_launched;
     const long long keys = static_cast<long long>(s.max_pages) * s.page, units = static_cast<long long>(s.B) * s.Hkv;
-    // Blocks for eight to an SM, not more than there are keys for by the table's width.
+    // A thread has a chain of dependent reads for each of its keys, so most have one or two; not more
+    // blocks than there are keys for by the table's width.
     const unsigned y = static_cast<unsigned>(std::min(units, 65535ll));
-    const long long want = std::max(1ll, 16ll * env.num_sms / y);
+    const long long want = std::max(1ll, 96ll * env.num_sms / y);
     const unsigned x = static_cast<unsigned>(std::min(want, (keys + kAddThreads - 1) / kAddThreads));
     return launch_serial(add_scores_kernel, dim3(x, y), kAddThreads, 0, env.stream, p, weights);
 }

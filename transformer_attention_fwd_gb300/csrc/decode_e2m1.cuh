@@ -21,6 +21,7 @@ struct E2m1Cache {
     // Two products' keys to a tile: their chains of dependent instructions run side by side,
     // and one check of the reference serves both.
     static constexpr int kKeys = 32, kParts = kKeys / kTile;
+    static_assert(kParts == 2, "sixteen lanes to a part");
     // Of each part: K rows, V rows, their scales.
     template <int D>
     static constexpr int kPartBytes = 2 * kTile * (D / 2 + D / 16);
@@ -40,79 +41,70 @@ struct E2m1Cache {
         static constexpr int kV = kTile * D / 2, kScales = 2 * kV, kVScales = kScales + kTile * (D / 16);
     };
 
+    // A lane's copies.  Pages that hold a part's keys: sixteen lanes to a part, each copying
+    // chunks l, l + 16, .. of its run of rows, whose places repeat every 256 bytes but for
+    // a swap of chunk pairs.  Else a row at a time.
     template <int D, bool kWholePages>
     struct Copies {
-        static constexpr int kPerRow = D / 32, kCopies = kTile * kPerRow / 32;
+        static constexpr int kPerRow = D / 32, kCopies = kTile * kPerRow / 16;
         static constexpr int kScaleRow = D / kRowScaleSpan, kScaleChunks = kTile * kScaleRow / 16;
+        static constexpr uint32_t kSwap = D == 128 ? 32 : 0;
         const int lane;
-        int put[kCopies];
-        const int64_t row_bytes, to_v;  // of codes; scales have an eighth
+        const uint32_t put0;     // of the lane's first chunk, in the tile
+        const int64_t to_v;      // of codes; scales have an eighth
 
         __device__ __forceinline__ Copies(const CacheParams& p, int lane_id)
-            : lane(lane_id), row_bytes(D / 2), to_v(static_cast<int64_t>(p.Hkv) * p.page.size * (D / 2)) {
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i)
-                put[i] = chunk4_at<D>((lane + 32 * i) / kPerRow, (lane + 32 * i) % kPerRow);
-        }
+            : lane(lane_id), put0((lane_id >> 4) * kPartBytes<D> + chunk4_at<D>((lane_id & 15) / kPerRow, lane_id % kPerRow)),
+              to_v(static_cast<int64_t>(p.Hkv) * p.page.size * (D / 2)) {}
+        __device__ __forceinline__ uint32_t put(int i) const { return ((i & 1) ? put0 ^ kSwap : put0) + i * 256; }
 
         // valid: keys of the tile (kKeys and more: all); id, row: of key lane, or (pages that hold a
-        // part's keys) of key 0 of part lane / 16.
+        // part's keys) of key 0 of the lane's part.
         __device__ __forceinline__ void issue(const CacheParams& p, uint32_t fill, int id, int row, int hkv,
                                               int valid) const {
+            using S = Stage<D>;
+            const int64_t first = (static_cast<int64_t>(id) * 2 * p.Hkv + hkv) * p.page.size + row;
+            if (kWholePages) {
+                const int l = lane & 15, c = l % kScaleChunks;
+                const uint8_t* src = p.kv + first * (D / 2) + l * 16;
+                const uint8_t* scales = p.row_scales + first * kScaleRow + (l < kScaleChunks ? 0 : to_v / 8) + c * 16;
+                const uint32_t scales_to = fill + (lane >> 4) * kPartBytes<D> + S::kScales + l * 16;  // K's, then V's
+                if (valid >= kKeys) {
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) {
-                const int from = i * kTile + (kWholePages ? 0 : lane % kTile);
-                part(p, fill + i * kPartBytes<D>, __shfl_sync(0xffffffffu, id, from), __shfl_sync(0xffffffffu, row, from),
-                     hkv, valid - i * kTile);
+                    for (int i = 0; i < kCopies; ++i) {
+                        copy16(fill + put(i), src + i * 256);
+                        copy16(fill + S::kV + put(i), src + to_v + i * 256);
+                    }
+                    if (l < 2 * kScaleChunks) copy16(scales_to, scales);
+                } else {
+                    valid -= lane & 16;  // of the part
+#pragma unroll
+                    for (int i = 0; i < kCopies; ++i) {
+                        const bool in = (l + 16 * i) / kPerRow < valid;
+                        const uint8_t* at = in ? src + i * 256 : p.kv;
+                        copy16_or_zero(fill + put(i), at, in);
+                        copy16_or_zero(fill + S::kV + put(i), in ? at + to_v : p.kv, in);
+                    }
+                    const int bytes = min(16, max(0, valid * kScaleRow - c * 16));
+                    if (l < 2 * kScaleChunks) copy16_part(scales_to, bytes > 0 ? scales : p.row_scales, bytes);
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < kKeys * kPerRow / 32; ++n) {
+                    const int r = (lane + 32 * n) / kPerRow, chunk = lane % kPerRow;
+                    const int64_t at = __shfl_sync(0xffffffffu, first, r);
+                    const uint8_t* src = p.kv + at * (D / 2) + chunk * 16;
+                    const uint32_t to = fill + (r / kTile) * kPartBytes<D> + chunk4_at<D>(r % kTile, chunk);
+                    copy16_or_zero(to, src, r < valid);
+                    copy16_or_zero(to + S::kV, src + to_v, r < valid);
+                }
+                const uint32_t to = fill + (lane >> 4) * kPartBytes<D> + S::kScales + (lane & 15) * kScaleRow;
+                copy_scales<kScaleRow>(to, p.row_scales + first * kScaleRow, lane < valid);
+                copy_scales<kScaleRow>(to + kTile * kScaleRow, p.row_scales + first * kScaleRow + to_v / 8, lane < valid);
             }
         }
 
       private:
-        // id, row: of key 0, or of key lane % 16.
-        __device__ __forceinline__ void part(const CacheParams& p, uint32_t fill, int id, int row, int hkv,
-                                             int valid) const {
-            using S = Stage<D>;
-            if (kWholePages) {  // one run of rows
-                const int64_t first = (static_cast<int64_t>(id) * 2 * p.Hkv + hkv) * p.page.size + row;
-                const uint8_t* src = p.kv + first * row_bytes + lane * 16;
-                if (valid >= kTile) {
-#pragma unroll
-                    for (int i = 0; i < kCopies; ++i) {
-                        copy16(fill + put[i], src + i * 512);
-                        copy16(fill + S::kV + put[i], src + to_v + i * 512);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kCopies; ++i) {
-                        const bool in = (lane + 32 * i) / kPerRow < valid;
-                        const uint8_t* at = in ? src + i * 512 : p.kv;
-                        copy16_or_zero(fill + put[i], at, in);
-                        copy16_or_zero(fill + S::kV + put[i], in ? at + to_v : p.kv, in);
-                    }
-                }
-                if (lane < 2 * kScaleChunks) {  // K's scales, then V's
-                    const int c = lane % kScaleChunks;
-                    const int bytes = min(16, max(0, valid * kScaleRow - c * 16));
-                    const uint8_t* at = p.row_scales + first * kScaleRow + (lane < kScaleChunks ? 0 : to_v / 8) + c * 16;
-                    copy16_part(fill + S::kScales + lane * 16, bytes > 0 ? at : p.row_scales, bytes);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const int r = (lane + 32 * i) / kPerRow;
-                    const int rid = __shfl_sync(0xffffffffu, id, r), rrow = __shfl_sync(0xffffffffu, row, r);
-                    const uint8_t* src = p.kv + ((static_cast<int64_t>(rid) * 2 * p.Hkv + hkv) * p.page.size + rrow) * row_bytes +
-                                         (lane + 32 * i) % kPerRow * 16;
-                    copy16_or_zero(fill + put[i], src, r < valid);
-                    copy16_or_zero(fill + S::kV + put[i], src + to_v, r < valid);
-                }
-                // Lanes 0 .. 15: K's scales, 16 .. 31: V's.
-                const uint8_t* at = p.row_scales + ((static_cast<int64_t>(id) * 2 * p.Hkv + hkv) * p.page.size + row) * kScaleRow +
-                                    (lane < kTile ? 0 : to_v / 8);
-                copy_scales<kScaleRow>(fill + S::kScales + lane * kScaleRow, at, lane % kTile < valid);
-            }
-        }
-
         // `bytes` of 16, zeros behind them.
         static __device__ __forceinline__ void copy16_part(uint32_t dst, const void* src, int bytes) {
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -142,24 +134,23 @@ struct E2m1Cache {
             // Key g's and key g + 8's columns of this lane, D/4 from t * D/4 on, and their scales,
             // each in both halves of a word.
             uint32_t kw[kParts][2][D / 32], kscale[kParts][2][D / 64];
+            const uint8_t* codes = stage + (D == 128 ? chunk4_at<D>(g, t) : chunk4_at<D>(g, t >> 1) + (t & 1) * 8);
+            const uint8_t* scale = stage + S::kScales + g * kScaleRow + t * (D / 64);
 #pragma unroll
             for (int i = 0; i < kParts; ++i) {
-                const uint8_t* part = stage + i * kPartBytes<D>;
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const int row = n * 8 + g;
-                    const uint8_t* at = part + S::kScales + row * kScaleRow;
+                    const uint8_t* c = codes + i * kPartBytes<D> + n * (8 * D / 2);  // eight rows on: the same place
+                    const uint8_t* at = scale + i * kPartBytes<D> + n * 8 * kScaleRow;
                     if constexpr (D == 128) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(part + chunk4_at<D>(row, t));
+                        const uint4 u = *reinterpret_cast<const uint4*>(c);
                         kw[i][n][0] = u.x; kw[i][n][1] = u.y; kw[i][n][2] = u.z; kw[i][n][3] = u.w;
-                        const uint32_t f = e4m3_to_f16x2(*reinterpret_cast<const uint16_t*>(at + 2 * t));
-                        kscale[i][n][0] = __byte_perm(f, f, 0x1010);
-                        kscale[i][n][1] = __byte_perm(f, f, 0x3232);
+                        both_halves(e4m3_to_f16x2(*reinterpret_cast<const uint16_t*>(at)), kscale[i][n][0], kscale[i][n][1]);
                     } else {
-                        const uint2 u = *reinterpret_cast<const uint2*>(part + chunk4_at<D>(row, t >> 1) + (t & 1) * 8);
+                        const uint2 u = *reinterpret_cast<const uint2*>(c);
                         kw[i][n][0] = u.x; kw[i][n][1] = u.y;
-                        const uint32_t f = e4m3_to_f16x2(at[t]);
-                        kscale[i][n][0] = __byte_perm(f, f, 0x1010);
+                        uint32_t none;
+                        both_halves(e4m3_to_f16x2(*at), kscale[i][n][0], none);
                     }
                 }
             }
@@ -190,14 +181,22 @@ struct E2m1Cache {
 #pragma unroll
                 for (int n = 0; n < 4; ++n) x[i][r][n] = (sc[i][r][n] + sd[i][r][n]) * s.qs[r][n & 1];
         if (scores.at != nullptr) {
+            const bool pairs = scores.group % 2 == 0;  // a lane's two heads are 8-byte aligned
 #pragma unroll
             for (int i = 0; i < kParts; ++i)
 #pragma unroll
                 for (int r = 0; r < kR; ++r)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const int key = i * kTile + (n >> 1) * 8 + g, h = r * 8 + 2 * t + (n & 1);
-                        if (key < valid && h < scores.heads) scores.at[key * scores.group + h] = x[i][r][n];
+                    for (int n = 0; n < 4; n += 2) {
+                        const int key = i * kTile + (n >> 1) * 8 + g, h = r * 8 + 2 * t;
+                        float* to = scores.at + key * scores.group + h;
+                        if (key >= valid || h >= scores.heads) continue;
+                        if (pairs) {
+                            *reinterpret_cast<float2*>(to) = make_float2(x[i][r][n], x[i][r][n + 1]);
+                        } else {
+                            to[0] = x[i][r][n];
+                            if (h + 1 < scores.heads) to[1] = x[i][r][n + 1];
+                        }
                     }
         }
         if (valid < kKeys) {  // the unit's last tile
@@ -314,14 +313,17 @@ struct E2m1Cache {
         __device__ __forceinline__ Values(const uint8_t* part, int g, int t) {
             using S = Stage<D>;
             constexpr int kScaleRow = D / kRowScaleSpan;
+            // Row 2t + 1 is in the next half (quarter) of row 2t's line, or the one before.
+            const uint32_t even = D == 128 ? chunk4_at<D>(2 * t, g >> 1) + (g & 1) * 8 : chunk4_at<D>(2 * t, g >> 2) + (g & 3) * 4;
+            const uint32_t odd = even ^ (D / 2);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int row = 2 * t + (j & 1) + 8 * (j >> 1);
+                const uint8_t* c = part + S::kV + ((j & 1) ? odd : even) + (j >> 1) * (8 * D / 2);
                 if constexpr (D == 128) {
-                    const uint2 u = *reinterpret_cast<const uint2*>(part + S::kV + chunk4_at<D>(row, g >> 1) + (g & 1) * 8);
+                    const uint2 u = *reinterpret_cast<const uint2*>(c);
                     w[j][0] = u.x; w[j][1] = u.y;
                 } else {
-                    w[j][0] = *reinterpret_cast<const uint32_t*>(part + S::kV + chunk4_at<D>(row, g >> 2) + (g & 3) * 4);
+                    w[j][0] = *reinterpret_cast<const uint32_t*>(c);
                 }
             }
 #pragma unroll

@@ -38,6 +38,11 @@ __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t codes) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(v) : "r"(codes));
     return v;
 }
+// Each half of a word in both halves of one.
+__device__ __forceinline__ void both_halves(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 %0, {l, l};\n\tmov.b32 %1, {h, h};\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(x));
+}
 // Products of fp16 pairs.  A code times its scale is exact: 2 and 4 significant bits,
 // between 2^-10 and 2688.
 __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
