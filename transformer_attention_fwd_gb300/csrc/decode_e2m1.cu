@@ -28,10 +28,14 @@ namespace attn {
 namespace {
 
 constexpr int kAddThreads = 128;
+constexpr int kAddKeys = 4;  // of a thread, their reads in flight together
 constexpr float kLog2e = 1.4426950408889634f;
 
-// weights[slot] += sum over a KV head's query heads of 2^(score - lse).  Block (x, y):
-// keys x * kAddThreads and on, gridDim.x blocks apart, of (request, KV head) y, y + gridDim.y, ..
+// weights[slot] += sum over a KV head's query heads of 2^(score - lse).  Block (x, y): runs of
+// kAddKeys * kAddThreads keys, gridDim.x runs apart, of (request, KV head) y, y + gridDim.y, ..
+// A thread's chain is the length, the block ids, the weights; with one key at a time the blocks
+// took 20 us at 64 x 4096 keys, most of them waiting.
+template <bool kFours>
 __global__ void __launch_bounds__(kAddThreads) add_scores_kernel(const CacheParams p, float* weights) {
     grid_wait();
     grid_launch_next();
@@ -40,24 +44,43 @@ __global__ void __launch_bounds__(kAddThreads) add_scores_kernel(const CachePara
         const int b = u / p.Hkv, hkv = u - b * p.Hkv;
         const int len = clamped_len(p, b);
         const float* lse = p.lse + static_cast<int64_t>(b) * p.Hq + hkv * p.group;
+        const int* table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
         const float* scores = p.scores + static_cast<int64_t>(u) * p.max_pages * p.page.size * p.group;
-        for (int key = blockIdx.x * kAddThreads + threadIdx.x; key < len; key += gridDim.x * kAddThreads) {
-            int row;
-            const int id = p.block_table[static_cast<int64_t>(b) * p.max_pages + p.page.split(key, &row)];
-            if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) continue;  // reported by the decode
-            const float* x = scores + static_cast<int64_t>(key) * p.group;
-            float sum = 0.0f;
-            if (p.group % 4 == 0) {  // 16 bytes at a time: the workspace is aligned to them
-                for (int h = 0; h < p.group; h += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(x + h);
-                    sum += (ex2_approx(v.x - lse[h] * kLog2e) + ex2_approx(v.y - lse[h + 1] * kLog2e)) +
-                           (ex2_approx(v.z - lse[h + 2] * kLog2e) + ex2_approx(v.w - lse[h + 3] * kLog2e));
-                }
-            } else {
-                for (int h = 0; h < p.group; ++h) sum += ex2_approx(x[h] - lse[h] * kLog2e);
+        for (int key0 = blockIdx.x * (kAddKeys * kAddThreads) + threadIdx.x; key0 < len;
+             key0 += gridDim.x * (kAddKeys * kAddThreads)) {
+            int id[kAddKeys], row[kAddKeys];
+#pragma unroll
+            for (int i = 0; i < kAddKeys; ++i) {
+                const int key = key0 + i * kAddThreads;
+                id[i] = key < len ? table[p.page.split(key, &row[i])] : -1;
             }
-            float* w = weights + (static_cast<int64_t>(id) * p.Hkv + hkv) * p.page.size + row;
-            *w += sum;
+            float sum[kAddKeys] = {};
+            for (int h = 0; h < p.group; h += kFours ? 4 : 1) {
+                if constexpr (kFours) {  // 16 bytes at a time: the workspace is aligned to them
+                    float4 v[kAddKeys];
+#pragma unroll
+                    for (int i = 0; i < kAddKeys; ++i) {
+                        const int key = min(key0 + i * kAddThreads, len - 1);
+                        v[i] = *reinterpret_cast<const float4*>(scores + static_cast<int64_t>(key) * p.group + h);
+                    }
+                    const float z[4] = {lse[h] * kLog2e, lse[h + 1] * kLog2e, lse[h + 2] * kLog2e, lse[h + 3] * kLog2e};
+#pragma unroll
+                    for (int i = 0; i < kAddKeys; ++i)
+                        sum[i] += (ex2_approx(v[i].x - z[0]) + ex2_approx(v[i].y - z[1])) +
+                                  (ex2_approx(v[i].z - z[2]) + ex2_approx(v[i].w - z[3]));
+                } else {
+                    const float z = lse[h] * kLog2e;
+#pragma unroll
+                    for (int i = 0; i < kAddKeys; ++i) {
+                        const int key = min(key0 + i * kAddThreads, len - 1);
+                        sum[i] += ex2_approx(scores[static_cast<int64_t>(key) * p.group + h] - z);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAddKeys; ++i)
+                if (static_cast<unsigned>(id[i]) < static_cast<unsigned>(p.num_blocks))  // others: reported by the decode
+                    atomicAdd(weights + (static_cast<int64_t>(id[i]) * p.Hkv + hkv) * p.page.size + row[i], sum[i]);
         }
     }
 }
@@ -105,12 +128,12 @@ cudaError_t launch_decode_paged_e2m1(const uint16_t* q, const uint8_t* kv, const
     if (e != cudaSuccess || !weights) return e;
     ++*kernels_launched;
     const long long keys = static_cast<long long>(s.max_pages) * s.page, units = static_cast<long long>(s.B) * s.Hkv;
-    // A thread has a chain of dependent reads for each of its keys, so most have one or two; not more
-    // blocks than there are keys for by the table's width.
+    // Not more blocks than there are keys for by the table's width.
     const unsigned y = static_cast<unsigned>(std::min(units, 65535ll));
-    const long long want = std::max(1ll, 96ll * env.num_sms / y);
-    const unsigned x = static_cast<unsigned>(std::min(want, (keys + kAddThreads - 1) / kAddThreads));
-    return launch_serial(add_scores_kernel, dim3(x, y), kAddThreads, 0, env.stream, p, weights);
+    const long long want = std::max(1ll, 32ll * env.num_sms / y), run = kAddKeys * kAddThreads;
+    const unsigned x = static_cast<unsigned>(std::min(want, (keys + run - 1) / run));
+    return launch_serial(p.group % 4 == 0 ? add_scores_kernel<true> : add_scores_kernel<false>, dim3(x, y), kAddThreads, 0,
+                         env.stream, p, weights);
 }
 
 }  // namespace attn

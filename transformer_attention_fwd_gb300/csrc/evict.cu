@@ -4,12 +4,13 @@
 // Of a request with more than `keep` keys, each KV head keeps its last `recent` slots and
 // the keep - recent heaviest of the others, and the kept rows move to slots 0 .. keep - 1 in
 // their order.  Two kernels.  evict_select_kernel, a CTA for each (request, KV head): the
-// weights as ordered integers, the smallest kept one found digit by digit from histograms
-// (radix selection: 11, 11 and 10 bits), then the kept slots written in order and the
-// weights moved.  evict_move_kernel: the rows.  A kept row never moves up, so in place is
-// safe if a row is read before its slot is written: slots are taken in order, a chunk is
-// read whole before any of it is written.  Columns of a row have nothing to do with one
-// another: where (request, KV head) pairs are few their columns go to CTAs of their own,
+// weights in shared memory as they were read, the smallest kept one found digit by digit of
+// their order from histograms (radix selection: 11, 11 and 10 bits), then the kept slots and
+// their weights written in order.  evict_move_kernel: the rows.  A kept row never moves up,
+// so in place is safe if a row is read before its slot is written: slots are taken in order,
+// a chunk is read whole before any of it is written, and the next chunk is read before that
+// too (its rows lie above every slot of this one).  Columns of a row have nothing to do with
+// one another: where (request, KV head) pairs are few their columns go to CTAs of their own,
 // instead of CTAs that would have to wait for one another.
 #include <cuda_runtime.h>
 
@@ -33,16 +34,18 @@ struct EvictParams {
     unsigned* status;
     PageDivider page;
     int B, Hkv, max_pages, num_blocks, keep, recent;
+    int held;  // weights a CTA of the first kernel has room for
 };
 
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kHeldKeys = 8192;  // in shared memory; those behind are read again
+constexpr int kMaxHeld = 40960;  // weights in shared memory; of longer requests those behind are read again
+constexpr int kBatch = 8;        // weights of a thread read at a time
 
 // Integers in the order of the weights: -0 as 0, NaN under everything.
-__device__ __forceinline__ uint32_t ordered(float w) {
-    const uint32_t u = __float_as_uint(w + 0.0f);
+__device__ __forceinline__ uint32_t ordered(uint32_t raw) {
+    const uint32_t u = __float_as_uint(__uint_as_float(raw) + 0.0f);
     if ((u & 0x7fffffffu) > 0x7f800000u) return 0;
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
@@ -73,8 +76,8 @@ struct Slots {
 };
 
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams p) {
-    __shared__ uint32_t s_key[kHeldKeys];
-    __shared__ int s_bin[kBins];
+    extern __shared__ uint32_t s_raw[];  // [held]
+    __shared__ __align__(16) int s_bin[kBins];
     __shared__ int s_warp[kSelectWarps][2];
     __shared__ int s_digit, s_above;
     grid_wait();
@@ -90,13 +93,34 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             continue;
         }
         const int n = slots.len - p.recent, want = p.keep - p.recent;  // candidates, those of them kept
-        auto load = [&](int i) {
+        const int held = min(slots.len, p.held);
+        auto load = [&](int i) {  // a weight's bits; of a bad block NaN's
             const float* w = slots.weight(i, hkv);
-            return w ? ordered(*w) : 0u;
+            return w ? __float_as_uint(*w) : 0x7fffffffu;
         };
         __syncthreads();  // the unit before has been read
-        for (int i = tid; i < min(n, kHeldKeys); i += kSelectThreads) s_key[i] = load(i);
-        auto key = [&](int i) { return i < kHeldKeys ? s_key[i] : load(i); };
+        for (int i = tid; i < kBins; i += kSelectThreads) s_bin[i] = 0;
+        __syncthreads();
+        // The weights, and the first digit's histogram.
+        for (int i0 = tid; i0 < held; i0 += kBatch * kSelectThreads) {
+            int id[kBatch], row[kBatch];
+            uint32_t raw[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                id[u] = i0 + u * kSelectThreads < held ? slots.find(i0 + u * kSelectThreads, &row[u]) : -1;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                raw[u] = id[u] < 0 ? 0x7fffffffu
+                                   : __float_as_uint(p.weights[(static_cast<int64_t>(id[u]) * p.Hkv + hkv) * p.page.size + row[u]]);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int i = i0 + u * kSelectThreads;
+                if (i < held) s_raw[i] = raw[u];
+                if (i < min(n, held)) atomicAdd(&s_bin[ordered(raw[u]) >> 21], 1);
+            }
+        }
+        for (int i = held + tid; i < n; i += kSelectThreads) atomicAdd(&s_bin[ordered(load(i)) >> 21], 1);
+        auto key = [&](int i) { return ordered(i < held ? s_raw[i] : load(i)); };
 
         // The key of the last kept one, from the highest digit on: `left` of those that share
         // the digits so far are kept.
@@ -104,18 +128,21 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
         int left = want, shift = 32;
         for (int bits = 11; shift > 0 && want > 0; shift -= bits, bits = shift < 11 ? shift : 11) {
             const int low = shift - bits;
-            for (int i = tid; i < kBins; i += kSelectThreads) s_bin[i] = 0;
-            __syncthreads();
-            for (int i = tid; i < n; i += kSelectThreads) {
-                const uint32_t k = key(i);
-                if (shift == 32 || (k >> shift) == prefix) atomicAdd(&s_bin[(k >> low) & ((1u << bits) - 1)], 1);
+            if (shift < 32) {
+                for (int i = tid; i < kBins; i += kSelectThreads) s_bin[i] = 0;
+                __syncthreads();
+                for (int i = tid; i < n; i += kSelectThreads) {
+                    const uint32_t k = key(i);
+                    if ((k >> shift) == prefix) atomicAdd(&s_bin[(k >> low) & ((1u << bits) - 1)], 1);
+                }
             }
             __syncthreads();
             // Thread i has bins 4 i .. 4 i + 3; counts from the top bin down.
             constexpr int kPer = kBins / kSelectThreads;
-            int mine[kPer], own = 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) own += mine[i] = s_bin[tid * kPer + i];
+            static_assert(kPer == 4, "a thread's bins are one int4");
+            const int4 bins = reinterpret_cast<const int4*>(s_bin)[tid];
+            const int mine[kPer] = {bins.x, bins.y, bins.z, bins.w};
+            const int own = (bins.x + bins.y) + (bins.z + bins.w);
             int above = own;  // in this and all higher lanes, then warps
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -158,6 +185,12 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             over += s_warp[i][0];
             equal += s_warp[i][1];
         }
+        // With all weights in shared memory they are written as their slots are found.
+        const bool whole = slots.len <= p.held;
+        auto place = [&](int slot, uint32_t raw) {
+            float* at = slots.weight(slot, hkv);
+            if (at) *at = __uint_as_float(raw);
+        };
         if (want > 0)
             for (int i = from; i < to; i += 32) {
                 const uint32_t k = i + lane < to ? key(i + lane) : 0u;
@@ -165,76 +198,97 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
                 const unsigned e = __ballot_sync(0xffffffffu, i + lane < to && k == prefix);
                 const unsigned below = (1u << lane) - 1;
                 const int before = equal + __popc(e & below);  // equal ones in front: the lowest stay
-                if ((o >> lane & 1) || ((e >> lane & 1) && before < left))
-                    kept[over + __popc(o & below) + min(before, left)] = i + lane;
+                if ((o >> lane & 1) || ((e >> lane & 1) && before < left)) {
+                    const int at = over + __popc(o & below) + min(before, left);
+                    kept[at] = i + lane;
+                    if (whole) place(at, s_raw[i + lane]);
+                }
                 over += __popc(o);
                 equal += __popc(e);
             }
-        for (int i = tid; i < p.recent; i += kSelectThreads) kept[want + i] = n + i;
-        __syncthreads();
-
-        // The weights follow, then zeros.
-        for (int i0 = 0; i0 < p.keep; i0 += kSelectThreads) {
-            const int i = i0 + tid;
-            float w = 0.0f;
-            if (i < p.keep) {
-                const float* at = slots.weight(kept[i], hkv);
-                if (at) w = *at;
+        for (int i = tid; i < p.recent; i += kSelectThreads) {
+            kept[want + i] = n + i;
+            if (whole) place(want + i, s_raw[n + i]);
+        }
+        if (!whole) {  // the weights follow as the rows do
+            __syncthreads();
+            for (int i0 = 0; i0 < p.keep; i0 += kSelectThreads) {
+                const int i = i0 + tid;
+                uint32_t raw = 0;
+                if (i < p.keep) raw = load(kept[i]);
+                __syncthreads();
+                if (i < p.keep) place(i, raw);
             }
             __syncthreads();
-            if (i < p.keep) {
-                float* at = slots.weight(i, hkv);
-                if (at) *at = w;
-            }
         }
-        __syncthreads();
-        for (int i = p.keep + tid; i < slots.len; i += kSelectThreads) {
-            float* at = slots.weight(i, hkv);
-            if (at) *at = 0.0f;
-        }
+        for (int i = p.keep + tid; i < slots.len; i += kSelectThreads) place(i, 0u);  // none of these is read again
     }
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveDepth = 4;  // pieces of a thread in flight
+constexpr int kMoveDepth = 4;  // pieces of a thread in a chunk; two chunks are in flight
 
-// Moves one column range of the kept rows of (request, KV head, K or V): pieces of T, `pieces`
-// (a power of two) to a row, at byte `first` of rows of row_bytes.
-template <typename T>
-__device__ __forceinline__ void move_rows(const EvictParams& p, uint8_t* base, int row_bytes, int first, int pieces,
+// Moves one column range of the kept rows of (request, KV head, K or V): pieces of T, kPieces to a
+// row, at byte `first` of rows of row_bytes.  A warp's lanes find the places of its rows of a
+// chunk, a row each, and hand them round.
+template <typename T, int kPieces>
+__device__ __forceinline__ void move_rows(const EvictParams& p, uint8_t* base, int row_bytes, int first,
                                           const Slots& slots, const int* kept, int side, int hkv) {
-    const int tid = threadIdx.x, piece = tid & (pieces - 1), r0 = tid / pieces, rows = kMoveThreads / pieces;
-    auto at = [&](int slot) -> T* {
+    constexpr int kStep = 32 / kPieces, kRows = kMoveThreads / kPieces;  // rows of a warp, of the CTA, at a time
+    constexpr int kChunk = kRows * kMoveDepth, kOwn = kStep * kMoveDepth;  // rows of the CTA's and the warp's chunk
+    constexpr int kFinds = kOwn <= 32 ? 1 : kOwn / 32;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, piece = lane % kPieces;
+    // Row `slot` in the pool of rows; negative: none.
+    auto row_of = [&](int slot) -> int64_t {
         int row;
         const int id = slots.find(slot, &row);
-        if (id < 0) return nullptr;
-        const int64_t n = (static_cast<int64_t>(id) * 2 + side) * p.Hkv + hkv;
-        return reinterpret_cast<T*>(base + (n * p.page.size + row) * row_bytes + first) + piece;
+        return id < 0 ? -1 : ((static_cast<int64_t>(id) * 2 + side) * p.Hkv + hkv) * p.page.size + row;
     };
-    for (int i0 = 0; i0 < p.keep; i0 += rows * kMoveDepth) {
-        T v[kMoveDepth];
-        bool moves[kMoveDepth];
+    auto at = [&](int64_t row) { return reinterpret_cast<T*>(base + row * row_bytes + first) + piece; };
+    T v[2][kMoveDepth];
+    int64_t to[2][kMoveDepth];  // negative: the row stays, or has no place
+    auto load = [&](int i0, T (&x)[kMoveDepth], int64_t (&dst)[kMoveDepth]) {
+        int64_t src_row[kFinds], dst_row[kFinds];
+#pragma unroll
+        for (int f = 0; f < kFinds; ++f) {
+            const int r = lane + 32 * f, i = i0 + r / kStep * kRows + warp * kStep + r % kStep;
+            const int slot = r < kOwn && i < p.keep ? kept[i] : i;
+            src_row[f] = dst_row[f] = -1;
+            if (slot != i) {
+                src_row[f] = row_of(slot);
+                dst_row[f] = row_of(i);
+                if (src_row[f] < 0) dst_row[f] = -1;
+            }
+        }
 #pragma unroll
         for (int u = 0; u < kMoveDepth; ++u) {
-            const int i = i0 + u * rows + r0, from = i < p.keep ? kept[i] : i;
-            const T* src = from != i ? at(from) : nullptr;
-            moves[u] = src != nullptr;
-            if (moves[u]) v[u] = *src;
+            const int r = u * kStep + lane / kPieces;
+            const int64_t src = __shfl_sync(0xffffffffu, src_row[u * kStep / 32], r % 32);
+            dst[u] = __shfl_sync(0xffffffffu, dst_row[u * kStep / 32], r % 32);
+            if (dst[u] >= 0) x[u] = *at(src);
         }
+    };
+    auto store = [&](const T (&x)[kMoveDepth], const int64_t (&dst)[kMoveDepth]) {
+#pragma unroll
+        for (int u = 0; u < kMoveDepth; ++u)
+            if (dst[u] >= 0) *at(dst[u]) = x[u];
+    };
+    load(0, v[0], to[0]);
+    for (int i0 = 0; i0 < p.keep; i0 += 2 * kChunk) {
+        if (i0 + kChunk < p.keep) load(i0 + kChunk, v[1], to[1]);
         __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kMoveDepth; ++u) {
-            T* dst = moves[u] ? at(i0 + u * rows + r0) : nullptr;
-            if (dst) *dst = v[u];
-        }
-        // (The next chunk's rows lie above every slot written here.)
+        store(v[0], to[0]);
+        if (i0 + kChunk >= p.keep) break;
+        if (i0 + 2 * kChunk < p.keep) load(i0 + 2 * kChunk, v[0], to[0]);
+        __syncthreads();
+        store(v[1], to[1]);
     }
 }
 
 // Block (x, y): unit y of (request, KV head), part x: sides times column ranges, then sides of
 // the scales.
-template <int kRowBytes, int kScaleBytes>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, int ranges) {
+template <int kRowBytes, int kScaleBytes, int kRanges>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
     grid_wait();
     grid_launch_next();
     for (long long unit = blockIdx.y; unit < static_cast<long long>(p.B) * p.Hkv; unit += gridDim.y) {
@@ -242,27 +296,26 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
         const Slots slots(p, b, false);
         if (slots.len <= p.keep) continue;
         const int* kept = p.kept + unit * p.keep;
-        const int part = blockIdx.x;
-        if (part < 2 * ranges) {
-            const int bytes = kRowBytes / ranges;
-            move_rows<uint4>(p, p.cache, kRowBytes, part / 2 * bytes, bytes / 16, slots, kept, part % 2, hkv);
-        } else if constexpr (kScaleBytes == 8) {
-            move_rows<uint2>(p, p.scales, 8, 0, 1, slots, kept, part % 2, hkv);
-        } else if constexpr (kScaleBytes == 4) {
-            move_rows<uint32_t>(p, p.scales, 4, 0, 1, slots, kept, part % 2, hkv);
-        }
-        __syncthreads();
+        const int part = blockIdx.x, side = part % 2;
+        constexpr int kBytes = kRowBytes / kRanges;
+        if (part < 2 * kRanges)
+            move_rows<uint4, kBytes / 16>(p, p.cache, kRowBytes, part / 2 * kBytes, slots, kept, side, hkv);
+        else if constexpr (kScaleBytes == 8)
+            move_rows<uint2, 1>(p, p.scales, 8, 0, slots, kept, side, hkv);
+        else if constexpr (kScaleBytes == 4)
+            move_rows<uint32_t, 1>(p, p.scales, 4, 0, slots, kept, side, hkv);
     }
 }
 
-template <int kRowBytes, int kScaleBytes>
+// Column ranges of 32 bytes and more, a power of two of them, until there are four CTAs for an SM.
+template <int kRowBytes, int kScaleBytes, int kRanges = 1>
 cudaError_t launch_move(const EvictParams& p, const LaunchEnv& env, int* grid_out) {
     const long long units = static_cast<long long>(p.B) * p.Hkv;
-    int ranges = 1;
-    while (ranges * 32 < kRowBytes && 2 * ranges * units < 4ll * env.num_sms) ranges *= 2;
-    const dim3 grid(2 * ranges + (kScaleBytes ? 2 : 0), static_cast<unsigned>(std::min(units, 65535ll)));
+    if constexpr (kRanges * 32 < kRowBytes)
+        if (2 * kRanges * units < 4ll * env.num_sms) return launch_move<kRowBytes, kScaleBytes, 2 * kRanges>(p, env, grid_out);
+    const dim3 grid(2 * kRanges + (kScaleBytes ? 2 : 0), static_cast<unsigned>(std::min(units, 65535ll)));
     *grid_out = static_cast<int>(grid.x * grid.y);
-    return launch_serial(evict_move_kernel<kRowBytes, kScaleBytes>, grid, kMoveThreads, 0, env.stream, p, ranges);
+    return launch_serial(evict_move_kernel<kRowBytes, kScaleBytes, kRanges>, grid, kMoveThreads, 0, env.stream, p);
 }
 
 }  // namespace
@@ -284,9 +337,17 @@ cudaError_t launch_evict_paged(const EvictShape& s, const LaunchEnv& env, int* g
     p.num_blocks = s.num_blocks;
     p.keep = s.keep;
     p.recent = s.recent;
+    p.held = static_cast<int>(std::min<long long>(static_cast<long long>(s.max_pages) * s.page, kMaxHeld));
+    static bool attr_set[64] = {};  // device < 64 (device_env)
+    cudaError_t e = cudaSuccess;
+    if (!attr_set[env.device]) {
+        e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxHeld * 4);
+        if (e != cudaSuccess) return e;
+        attr_set[env.device] = true;
+    }
     const long long units = static_cast<long long>(s.B) * s.Hkv;
-    cudaError_t e = launch_serial(evict_select_kernel, dim3(static_cast<unsigned>(std::min(units, 0x7fffffffll))),
-                                  kSelectThreads, 0, env.stream, p);
+    e = launch_serial(evict_select_kernel, dim3(static_cast<unsigned>(std::min(units, 0x7fffffffll))), kSelectThreads,
+                      static_cast<size_t>(p.held) * 4, env.stream, p);
     if (e != cudaSuccess) return e;
     *kernels_launched = 2;
     if (s.scales) return s.D == 64 ? launch_move<32, 4>(p, env, grid_out) : launch_move<64, 8>(p, env, grid_out);
