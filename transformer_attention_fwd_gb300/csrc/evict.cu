@@ -4,9 +4,9 @@
 // Of a request with more than `keep` keys, each KV head keeps its last `recent` slots and
 // the keep - recent heaviest of the others, and the kept rows move to slots 0 .. keep - 1 in
 // their order.  Two kernels.  evict_select_kernel, a CTA for each (request, KV head): the
-// weights in shared memory as they were read, the smallest kept one found digit by digit of
-// their order from histograms (radix selection: 11, 11 and 10 bits), then the kept slots and
-// their weights written in order.  evict_move_kernel: the rows.  A kept row never moves up,
+// weights as integers in their order in shared memory, the smallest kept one found digit by
+// digit from histograms (radix selection: 11, 11 and 10 bits; once few share the first digit,
+// among those alone), then the kept slots and their weights written in order.  evict_move_kernel: the rows.  A kept row never moves up,
 // so in place is safe if a row is read before its slot is written: slots are taken in order,
 // a chunk is read whole before any of it is written, and the next chunk is read before that
 // too (its rows lie above every slot of this one).  Columns of a row have nothing to do with
@@ -41,7 +41,10 @@ constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxHeld = 40960;  // weights in shared memory; of longer requests those behind are read again
-constexpr int kBatch = 8;        // weights of a thread read at a time
+constexpr int kPages = 1024;     // pages whose places are
+constexpr int kList = 1024;      // keys that share the first digit, if they are so few
+constexpr int kFew = 64;         // so few are compared with one another
+constexpr int kBatch = 4;        // weights of a thread read at a time
 
 // Integers in the order of the weights: -0 as 0, NaN under everything.
 __device__ __forceinline__ uint32_t ordered(uint32_t raw) {
@@ -49,6 +52,9 @@ __device__ __forceinline__ uint32_t ordered(uint32_t raw) {
     if ((u & 0x7fffffffu) > 0x7f800000u) return 0;
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
+
+// The weight of a key (not of -0 and NaN, which are not told apart).
+__device__ __forceinline__ uint32_t weight_of(uint32_t key) { return (key & 0x80000000u) ? key ^ 0x80000000u : ~key; }
 
 // A request's slots; len: 0 if out of range (reported by the first kernel).
 struct Slots {
@@ -61,25 +67,23 @@ struct Slots {
         len = n < 0 ? 0 : (n > most ? most : n);
         if (report && len != n) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
     }
-    // Block and row of a slot; the block is -1 (reported) if its id is outside the pool.
-    __device__ __forceinline__ int find(int slot, int* row) const {
-        const int id = table[p.page.split(slot, row)];
+    // Block of a page; -1 (reported) if its id is outside the pool.
+    __device__ __forceinline__ int block(int page) const {
+        const int id = table[page];
         if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks)) return id;
         atomicOr(p.status, ATTN_DEV_BAD_INPUT);
         return -1;
     }
-    __device__ __forceinline__ float* weight(int slot, int hkv) const {
-        int row;
-        const int id = find(slot, &row);
-        return id < 0 ? nullptr : p.weights + (static_cast<int64_t>(id) * p.Hkv + hkv) * p.page.size + row;
-    }
 };
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams p) {
-    extern __shared__ uint32_t s_raw[];  // [held]
+__global__ void __launch_bounds__(kSelectThreads, 3) evict_select_kernel(const EvictParams p) {
+    extern __shared__ __align__(16) uint32_t s_key[];  // [held]
     __shared__ __align__(16) int s_bin[kBins];
+    __shared__ int64_t s_page[kPages];  // first weight of a page; negative: none
+    __shared__ uint32_t s_list[kList];
     __shared__ int s_warp[kSelectWarps][2];
-    __shared__ int s_digit, s_above;
+    __shared__ int s_digit, s_above, s_count, s_odd;
+    __shared__ uint32_t s_found;
     grid_wait();
     grid_launch_next();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -94,46 +98,108 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
         }
         const int n = slots.len - p.recent, want = p.keep - p.recent;  // candidates, those of them kept
         const int held = min(slots.len, p.held);
-        auto load = [&](int i) {  // a weight's bits; of a bad block NaN's
-            const float* w = slots.weight(i, hkv);
-            return w ? __float_as_uint(*w) : 0x7fffffffu;
+        const int pages = p.page.quotient(slots.len - 1) + 1;
+        auto page_at = [&](int page) -> int64_t {
+            const int id = slots.block(page);
+            return id < 0 ? -1 : (static_cast<int64_t>(id) * p.Hkv + hkv) * p.page.size;
         };
         __syncthreads();  // the unit before has been read
+        for (int i = tid; i < min(pages, kPages); i += kSelectThreads) s_page[i] = page_at(i);
         for (int i = tid; i < kBins; i += kSelectThreads) s_bin[i] = 0;
+        if (tid == 0) s_count = s_odd = 0;
         __syncthreads();
+        auto at = [&](int slot) -> float* {
+            int row;
+            const int page = p.page.split(slot, &row);
+            const int64_t first = page < kPages ? s_page[page] : page_at(page);
+            return first < 0 ? nullptr : p.weights + first + row;
+        };
+        auto load = [&](int slot) {  // a weight's bits; of a bad block NaN's
+            const float* w = at(slot);
+            return w ? __float_as_uint(*w) : 0x7fffffffu;
+        };
         // The weights, and the first digit's histogram.
+        bool odd = false;
         for (int i0 = tid; i0 < held; i0 += kBatch * kSelectThreads) {
-            int id[kBatch], row[kBatch];
+            const float* from[kBatch];
             uint32_t raw[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u)
-                id[u] = i0 + u * kSelectThreads < held ? slots.find(i0 + u * kSelectThreads, &row[u]) : -1;
+                from[u] = i0 + u * kSelectThreads < held ? at(i0 + u * kSelectThreads) : nullptr;
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                raw[u] = id[u] < 0 ? 0x7fffffffu
-                                   : __float_as_uint(p.weights[(static_cast<int64_t>(id[u]) * p.Hkv + hkv) * p.page.size + row[u]]);
+            for (int u = 0; u < kBatch; ++u) raw[u] = from[u] ? __float_as_uint(*from[u]) : 0x7fffffffu;
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const int i = i0 + u * kSelectThreads;
-                if (i < held) s_raw[i] = raw[u];
-                if (i < min(n, held)) atomicAdd(&s_bin[ordered(raw[u]) >> 21], 1);
+                if (i >= held) break;
+                odd |= raw[u] == 0x80000000u || (raw[u] & 0x7fffffffu) > 0x7f800000u;
+                const uint32_t k = ordered(raw[u]);
+                s_key[i] = k;
+                if (i < n) atomicAdd(&s_bin[k >> 21], 1);
             }
         }
+        if (odd) s_odd = 1;
         for (int i = held + tid; i < n; i += kSelectThreads) atomicAdd(&s_bin[ordered(load(i)) >> 21], 1);
-        auto key = [&](int i) { return ordered(i < held ? s_raw[i] : load(i)); };
+        // Keys i .. i + 3 (i a multiple of 4; those from n on are not to be looked at).
+        auto keys = [&](int i) {
+            if (i + 3 < held) return *reinterpret_cast<const uint4*>(s_key + i);
+            uint32_t k[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) k[u] = i + u < held ? s_key[i + u] : i + u < n ? ordered(load(i + u)) : 0u;
+            return make_uint4(k[0], k[1], k[2], k[3]);
+        };
 
         // The key of the last kept one, from the highest digit on: `left` of those that share
         // the digits so far are kept.
         uint32_t prefix = 0;
-        int left = want, shift = 32;
-        for (int bits = 11; shift > 0 && want > 0; shift -= bits, bits = shift < 11 ? shift : 11) {
+        int left = want;
+        for (int shift = 32, bits = 11; shift > 0 && want > 0; shift -= bits, bits = shift < 11 ? shift : 11) {
             const int low = shift - bits;
+            const uint32_t mask = (1u << bits) - 1;
+            if (shift == 21) {  // those with the first digit, if they are few
+                for (int i = 4 * tid; i < n; i += 4 * kSelectThreads) {
+                    const uint4 k = keys(i);
+                    const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (i + u < n && (v[u] >> 21) == prefix) {
+                            const int place = atomicAdd(&s_count, 1);
+                            if (place < kList) s_list[place] = v[u];
+                        }
+                }
+            }
             if (shift < 32) {
                 for (int i = tid; i < kBins; i += kSelectThreads) s_bin[i] = 0;
                 __syncthreads();
-                for (int i = tid; i < n; i += kSelectThreads) {
-                    const uint32_t k = key(i);
-                    if ((k >> shift) == prefix) atomicAdd(&s_bin[(k >> low) & ((1u << bits) - 1)], 1);
+                const int some = s_count;
+                if (some <= kFew) {  // each counts those over it
+                    const uint32_t own = tid < some ? s_list[tid] : 0u;
+                    int greater = 0, same = 0;
+                    if (tid < kFew)
+                        for (int i = 0; i < some; ++i) {
+                            greater += s_list[i] > own;
+                            same += s_list[i] == own;
+                        }
+                    if (tid < some && greater < left && left <= greater + same) {  // the same key and count in each that is it
+                        s_found = own;
+                        s_above = greater;
+                    }
+                    __syncthreads();
+                    prefix = s_found;
+                    left -= s_above;
+                    break;
+                }
+                if (some <= kList) {
+                    for (int i = tid; i < some; i += kSelectThreads)
+                        if ((s_list[i] >> shift) == prefix) atomicAdd(&s_bin[s_list[i] >> low & mask], 1);
+                } else {
+                    for (int i = 4 * tid; i < n; i += 4 * kSelectThreads) {
+                        const uint4 k = keys(i);
+                        const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (i + u < n && (v[u] >> shift) == prefix) atomicAdd(&s_bin[v[u] >> low & mask], 1);
+                    }
                 }
             }
             __syncthreads();
@@ -166,14 +232,22 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             left -= s_above;
         }
 
-        // Kept slots in order: a warp has a run of them, and counts first.
-        const int run = (n + kSelectWarps - 1) / kSelectWarps, from = min(n, warp * run), to = min(n, from + run);
+        // Kept slots in order: a warp has a run of them, four to a lane at a time, and counts first.
+        constexpr int kStep = 128;
+        const int run = (n + kSelectWarps * kStep - 1) / (kSelectWarps * kStep) * kStep;
+        const int from = static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(warp) * run)), to = min(n, from + run);
         int over = 0, equal = 0;
-        for (int i = from; i < to; i += 32) {
-            const uint32_t k = i + lane < to ? key(i + lane) : 0u;
-            over += __popc(__ballot_sync(0xffffffffu, i + lane < to && k > prefix));
-            equal += __popc(__ballot_sync(0xffffffffu, i + lane < to && k == prefix));
+        for (int i = from + 4 * lane; i < to; i += kStep) {
+            const uint4 k = keys(i);
+            const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                over += i + u < to && v[u] > prefix;
+                equal += i + u < to && v[u] == prefix;
+            }
         }
+        over = __reduce_add_sync(0xffffffffu, over);
+        equal = __reduce_add_sync(0xffffffffu, equal);
         __syncthreads();  // s_warp has been read
         if (lane == 0) {
             s_warp[warp][0] = over;
@@ -185,30 +259,47 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             over += s_warp[i][0];
             equal += s_warp[i][1];
         }
-        // With all weights in shared memory they are written as their slots are found.
-        const bool whole = slots.len <= p.held;
+        // With all weights at hand they are written as their slots are found.
+        const bool whole = slots.len <= p.held && s_odd == 0;
         auto place = [&](int slot, uint32_t raw) {
-            float* at = slots.weight(slot, hkv);
-            if (at) *at = __uint_as_float(raw);
+            float* w = at(slot);
+            if (w) *w = __uint_as_float(raw);
         };
         if (want > 0)
-            for (int i = from; i < to; i += 32) {
-                const uint32_t k = i + lane < to ? key(i + lane) : 0u;
-                const unsigned o = __ballot_sync(0xffffffffu, i + lane < to && k > prefix);
-                const unsigned e = __ballot_sync(0xffffffffu, i + lane < to && k == prefix);
-                const unsigned below = (1u << lane) - 1;
-                const int before = equal + __popc(e & below);  // equal ones in front: the lowest stay
-                if ((o >> lane & 1) || ((e >> lane & 1) && before < left)) {
-                    const int at = over + __popc(o & below) + min(before, left);
-                    kept[at] = i + lane;
-                    if (whole) place(at, s_raw[i + lane]);
+            for (int i0 = from; i0 < to; i0 += kStep) {
+                const int i = i0 + 4 * lane;
+                const uint4 k = i < to ? keys(i) : make_uint4(0, 0, 0, 0);
+                const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+                int mine = 0;  // over in the low half, equal in the high one
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (i + u < to) mine += v[u] > prefix ? 1 : v[u] == prefix ? 1 << 16 : 0;
+                int incl = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += x;
                 }
-                over += __popc(o);
-                equal += __popc(e);
+                const int all = __shfl_sync(0xffffffffu, incl, 31), before = incl - mine;
+                int o = over + (before & 0xffff), e = equal + (before >> 16);  // in front of this lane's
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (i + u >= to) break;
+                    const bool is_over = v[u] > prefix, is_equal = v[u] == prefix;
+                    if (is_over || (is_equal && e < left)) {  // of equal ones the lowest stay
+                        const int place_at = o + min(e, left);
+                        kept[place_at] = i + u;
+                        if (whole) place(place_at, weight_of(v[u]));
+                    }
+                    o += is_over;
+                    e += is_equal;
+                }
+                over += all & 0xffff;
+                equal += all >> 16;
             }
         for (int i = tid; i < p.recent; i += kSelectThreads) {
             kept[want + i] = n + i;
-            if (whole) place(want + i, s_raw[n + i]);
+            if (whole) place(want + i, weight_of(s_key[n + i]));
         }
         if (!whole) {  // the weights follow as the rows do
             __syncthreads();
@@ -221,12 +312,16 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             }
             __syncthreads();
         }
+#pragma unroll 4
         for (int i = p.keep + tid; i < slots.len; i += kSelectThreads) place(i, 0u);  // none of these is read again
     }
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveDepth = 4;  // pieces of a thread in a chunk; two chunks are in flight
+// Pieces of a thread in a chunk; two chunks are in flight.  A warp's lanes find the places of a row
+// each, so of small rows a chunk has no more.
+template <int kPieces>
+constexpr int kDepthOf = kPieces < 4 ? kPieces : 4;
 
 // Moves one column range of the kept rows of (request, KV head, K or V): pieces of T, kPieces to a
 // row, at byte `first` of rows of row_bytes.  A warp's lanes find the places of its rows of a
@@ -234,37 +329,34 @@ constexpr int kMoveDepth = 4;  // pieces of a thread in a chunk; two chunks are 
 template <typename T, int kPieces>
 __device__ __forceinline__ void move_rows(const EvictParams& p, uint8_t* base, int row_bytes, int first,
                                           const Slots& slots, const int* kept, int side, int hkv) {
+    constexpr int kMoveDepth = kDepthOf<kPieces>;
     constexpr int kStep = 32 / kPieces, kRows = kMoveThreads / kPieces;  // rows of a warp, of the CTA, at a time
     constexpr int kChunk = kRows * kMoveDepth, kOwn = kStep * kMoveDepth;  // rows of the CTA's and the warp's chunk
-    constexpr int kFinds = kOwn <= 32 ? 1 : kOwn / 32;
+    static_assert(kOwn <= 32, "a lane a row");
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, piece = lane % kPieces;
     // Row `slot` in the pool of rows; negative: none.
     auto row_of = [&](int slot) -> int64_t {
         int row;
-        const int id = slots.find(slot, &row);
+        const int id = slots.block(p.page.split(slot, &row));
         return id < 0 ? -1 : ((static_cast<int64_t>(id) * 2 + side) * p.Hkv + hkv) * p.page.size + row;
     };
     auto at = [&](int64_t row) { return reinterpret_cast<T*>(base + row * row_bytes + first) + piece; };
     T v[2][kMoveDepth];
     int64_t to[2][kMoveDepth];  // negative: the row stays, or has no place
     auto load = [&](int i0, T (&x)[kMoveDepth], int64_t (&dst)[kMoveDepth]) {
-        int64_t src_row[kFinds], dst_row[kFinds];
-#pragma unroll
-        for (int f = 0; f < kFinds; ++f) {
-            const int r = lane + 32 * f, i = i0 + r / kStep * kRows + warp * kStep + r % kStep;
-            const int slot = r < kOwn && i < p.keep ? kept[i] : i;
-            src_row[f] = dst_row[f] = -1;
-            if (slot != i) {
-                src_row[f] = row_of(slot);
-                dst_row[f] = row_of(i);
-                if (src_row[f] < 0) dst_row[f] = -1;
-            }
+        const int i = i0 + lane / kStep * kRows + warp * kStep + lane % kStep;
+        const int slot = lane < kOwn && i < p.keep ? kept[i] : i;
+        int64_t src_row = -1, dst_row = -1;
+        if (slot != i) {
+            src_row = row_of(slot);
+            dst_row = row_of(i);
+            if (src_row < 0) dst_row = -1;
         }
 #pragma unroll
         for (int u = 0; u < kMoveDepth; ++u) {
             const int r = u * kStep + lane / kPieces;
-            const int64_t src = __shfl_sync(0xffffffffu, src_row[u * kStep / 32], r % 32);
-            dst[u] = __shfl_sync(0xffffffffu, dst_row[u * kStep / 32], r % 32);
+            const int64_t src = __shfl_sync(0xffffffffu, src_row, r);
+            dst[u] = __shfl_sync(0xffffffffu, dst_row, r);
             if (dst[u] >= 0) x[u] = *at(src);
         }
     };
@@ -288,7 +380,7 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, uint8_t* base, i
 // Block (x, y): unit y of (request, KV head), part x: sides times column ranges, then sides of
 // the scales.
 template <int kRowBytes, int kScaleBytes, int kRanges>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictParams p) {
     grid_wait();
     grid_launch_next();
     for (long long unit = blockIdx.y; unit < static_cast<long long>(p.B) * p.Hkv; unit += gridDim.y) {
@@ -307,12 +399,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     }
 }
 
-// Column ranges of 32 bytes and more, a power of two of them, until there are four CTAs for an SM.
+// Column ranges of 32 bytes and more, a power of two of them, until there are two CTAs for an SM.
 template <int kRowBytes, int kScaleBytes, int kRanges = 1>
 cudaError_t launch_move(const EvictParams& p, const LaunchEnv& env, int* grid_out) {
     const long long units = static_cast<long long>(p.B) * p.Hkv;
     if constexpr (kRanges * 32 < kRowBytes)
-        if (2 * kRanges * units < 4ll * env.num_sms) return launch_move<kRowBytes, kScaleBytes, 2 * kRanges>(p, env, grid_out);
+        if (2 * kRanges * units < 2ll * env.num_sms) return launch_move<kRowBytes, kScaleBytes, 2 * kRanges>(p, env, grid_out);
     const dim3 grid(2 * kRanges + (kScaleBytes ? 2 : 0), static_cast<unsigned>(std::min(units, 65535ll)));
     *grid_out = static_cast<int>(grid.x * grid.y);
     return launch_serial(evict_move_kernel<kRowBytes, kScaleBytes, kRanges>, grid, kMoveThreads, 0, env.stream, p);
@@ -337,7 +429,7 @@ cudaError_t launch_evict_paged(const EvictShape& s, const LaunchEnv& env, int* g
     p.num_blocks = s.num_blocks;
     p.keep = s.keep;
     p.recent = s.recent;
-    p.held = static_cast<int>(std::min<long long>(static_cast<long long>(s.max_pages) * s.page, kMaxHeld));
+    p.held = static_cast<int>(std::min<long long>((static_cast<long long>(s.max_pages) * s.page + 3) / 4 * 4, kMaxHeld));
     static bool attr_set[64] = {};  // device < 64 (device_env)
     cudaError_t e = cudaSuccess;
     if (!attr_set[env.device]) {
