@@ -171,7 +171,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int token, in
                 if (kKind == 2 || half == 0) {  // copied as they are
                     if (kKind != 2 && in && r.y) R::store(y, y + to1, raw[u]);
                     if constexpr (!Sink::kPlain) {
-                        if (kKind != 0) sink.store(p, h + u * R::kRows + (kKind == 2 ? p.k.heads : 0), in, R::unpack(raw[u]));
+                        if (kKind != 0) sink.store(p, h + u * R::kRows + (kKind == 2 ? p.k.heads : 0), in, raw[u]);
                     } else {
                         if (kKind != 0 && in && cache) R::store(cache + c, cache + c + to1, raw[u]);
                     }
