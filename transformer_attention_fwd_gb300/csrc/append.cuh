@@ -134,7 +134,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int token, in
         int b, slot;
         mine = append_slot(p, token, lane, &b, &slot);
         if (!mine) return;
-        if (s0 < k_end) {
+        if (s0 < k_end && half > 0) {
             rope_fill<D>(p.table, p.positions ? p.positions[token] : slot, lane, table);
             R::coefficients(table, j, coef);
         }
