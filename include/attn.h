@@ -546,7 +546,10 @@ attn_status attn_fwd_decode_paged_e2m1(const void* q, const void* kv_cache, cons
  * dtype (ATTN_BF16 or ATTN_F16) is q's and the cache's type.  The sums are fp32 in a
  * fixed order.  Device-side checks, reported as ATTN_ERR_BAD_INPUT: a request whose
  * offsets or length are out of range is left out, and so is a slot whose block id is.
- * No workspace.  B and Hkv up to 65535 (ATTN_ERR_UNSUPPORTED beyond).
+ * Queries whose strides are not 0, with up to 128 query heads to a KV head, run on the
+ * 5th-generation tensor cores, others on a slower kernel.  Requests with over 512 queries
+ * (more where the sums would be over 64 MB) have these cut into ranges, whose sums pass
+ * through a workspace and are added in order.
  */
 attn_status attn_weights_paged(const attn_rows* q, const float* lse, long long lse_head,
                                long long lse_token, const void* kv_cache, const int* block_table,

@@ -68,6 +68,12 @@ def test_decode_refuses(a, kw, code, msg):
     assert msg in a.last_error()
 
 
+def test_decode_refuses_scores_beyond_any_memory(a):
+    """Sizes whose product would pass 64 bits."""
+    big = dict(B=1 << 12, Hq=1 << 18, Hkv=1 << 18, pages=1 << 17, page=(1 << 14) - 1)
+    assert _decode(a, weights=FAKE, **big) == a.ATTN_ERR_NO_MEMORY and "2^44" in a.last_error()
+
+
 def _weights(a, four, **kw):
     c = dict(q=rows(a), lse=FAKE, lse_head=5, lse_token=1, kv=FAKE, scales=FAKE, factors=None, table=FAKE, cu=FAKE,
              lens=FAKE, weights=FAKE, B=2, total=5, Hkv=2, D=64, page=16, pages=4, blocks=8, scale=0.1, dtype=1)
@@ -123,6 +129,10 @@ def _evict(a, four, **kw):
 def test_evict_refuses(a, four, kw, code, msg):
     assert _evict(a, four, **kw) == code
     assert msg in a.last_error()
+
+
+def test_evict_refuses_lists_beyond_any_memory(a):
+    assert _evict(a, False, B=1 << 12, Hkv=1 << 18, keep=1 << 30) == 1 and "2^42" in a.last_error()
 
 
 def test_evict_refuses_types(a):

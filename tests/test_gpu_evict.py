@@ -67,7 +67,7 @@ fours = pytest.mark.parametrize("four", [False, True], ids=["16bit", "4bit"])
     ([60, 61], 400, 20, {}),                                  # nobody is that long
     ([30, 20], 10 ** 5, 20, {}),
     ([9000, 8193], 4100, 512, dict(Hkv=1)),
-    ([45000, 40961, 40960], 2000, 300, dict(Hkv=1, D=64, page=64)),  # more than are held in shared memory, and as many
+    ([30000, 24577, 24576], 2000, 300, dict(Hkv=1, D=64, page=64)),  # more than are held in shared memory, and as many
     ([70] * 40, 20, 5, dict(Hkv=8)),
 ])
 def test_matches_slot_by_slot(lens, keep, recent, kw, four):

@@ -234,3 +234,73 @@ def test_graph_on_a_side_stream(four):
         side.synchronize()
         assert torch.equal(w, want)
     check_status(a)
+
+
+@fours
+def test_two_streams_at_once_with_ranges(four):
+    """Prompts whose queries are cut into ranges, captured and eager, on two streams: each call's
+    sums pass through a workspace of its own."""
+    a = attn()
+    problems = [Problem([1500, 40], [1500, 3], Hq=4, D=64, four=four, seed=s) for s in (191, 192)]
+    want = [pr.run(a) for pr in problems]
+    torch.cuda.synchronize()
+    streams, graphs, held = [torch.cuda.Stream(), torch.cuda.Stream()], [], []
+
+    def call(pr, dev, w):
+        q, lse, cache, table, cu, lens, scales, factors = dev
+        if four:
+            a.attn_weights_paged_e2m1(q, lse, cache, scales, table, cu, lens, w, factors=factors)
+        else:
+            a.attn_weights_paged(q, lse, cache, table, cu, lens, w)
+
+    for s, pr in zip(streams, problems):
+        dev = [None if t is None else t.cuda() for t in (pr.q, pr.lse, pr.cache, pr.table, pr.cu, pr.lens, pr.scales, pr.factors)]
+        before, w = pr.weights.cuda(), pr.weights.cuda()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            w.copy_(before)
+            call(pr, dev, w)
+        graphs.append(g)
+        held.append((dev, before, w))
+    for _ in range(5):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    eager = []
+    for s, pr, (dev, before, w) in zip(streams, problems, held):
+        with torch.cuda.stream(s):
+            e = before.clone()
+            call(pr, dev, e)
+            eager.append(e)
+    torch.cuda.synchronize()
+    for w, e, (_, _, g) in zip(want, eager, held):
+        assert torch.equal(e, w) and torch.equal(g, w)
+    check_status(a)
+
+
+@fours
+def test_many_requests(four):
+    """5000 requests of which few have queries, found 32 at a time."""
+    a = attn()
+    B = 5000
+    lens = [1 + (i * 7) % 40 for i in range(B)]
+    new = [0] * B
+    for i in (0, 31, 32, 2999, 4999):
+        new[i] = min(3, lens[i])
+    pr = Problem(lens, new, Hq=2, Hkv=1, D=64, four=four, seed=193)
+    pr.check(pr.run(a))
+    check_status(a)
+    pr.lens[4998] = -1
+    pr.run(a)
+    assert a.device_status() == a.ATTN_ERR_BAD_INPUT
+
+
+@fours
+def test_a_request_that_is_not_valid_between_long_ones(four):
+    a = attn()
+    pr = Problem([800, 700, 900], [600, 600, 600], Hq=2, Hkv=1, D=64, four=four, seed=194)
+    lens = pr.lens.clone()
+    lens[1] = 599
+    pr.check(pr.run(a, lens=lens), skip=(1,))
+    assert a.device_status() == a.ATTN_ERR_BAD_INPUT

@@ -996,6 +996,9 @@ cudaError_t workspace_alloc(void** out, size_t bytes, const LaunchEnv& env) {
     return cudaMallocFromPoolAsync(out, bytes, pool, env.stream);
 }
 
+// Workspaces beyond this are refused before their size can wrap.
+constexpr double kMaxWorkspace = 1ull << 44;
+
 int dtype_bytes(attn_dtype t) { return t == ATTN_F32 ? 4 : 2; }
 
 attn_status validate_rotation(const attn_rotation* r, int D) {
@@ -1306,7 +1309,6 @@ attn_status run_weights(bool four, const attn_rows* q, const float* lse, long lo
     } else {
         e = launch_weights_paged(s, env, &grid, &kernels);
     }
-    if (e == cudaErrorInvalidConfiguration) return fail(ATTN_ERR_UNSUPPORTED, "too many requests or heads for one launch");
     if (e != cudaSuccess) return cuda_fail(e, "weights launch");
     record_launch(grid, 0, kernels);
     return ok();
@@ -1329,6 +1331,7 @@ attn_status run_evict(bool four, void* kv_cache, void* scales, float* weights, c
     if (keep > 0x7fffffff - 65536) return fail(ATTN_ERR_INVALID_ARG, "keep must be below 2^31 - 65536");
     if (!new_lens || !aligned(new_lens, 4) || !aligned(kept, 4))
         return fail(ATTN_ERR_INVALID_ARG, "new_lens must be non-null, and new_lens and kept 4-byte aligned");
+    if (4.0 * B * Hkv * keep > kMaxWorkspace) return fail(ATTN_ERR_INVALID_ARG, "B*Hkv*keep must be below 2^42");
     const size_t kept_bytes = 4ull * B * Hkv * keep;
     if (meet(new_lens, 4ull * B, seq_lens, 4ull * B))
         return fail(ATTN_ERR_INVALID_ARG, "new_lens may not share memory with seq_lens");
@@ -1500,6 +1503,8 @@ attn_status attn_fwd_decode_paged_e2m1(const void* q, const void* kv_cache, cons
                                     max_pages_per_seq, num_blocks, scale, dtype);
     if (st != ATTN_OK) return st;
     if (B > 0x7fffffff - 1024) return fail(ATTN_ERR_INVALID_ARG, "B must be below 2^31 - 1024");
+    if (weights && 4.0 * B * Hq * max_pages_per_seq * page_size > kMaxWorkspace)
+        return fail(ATTN_ERR_NO_MEMORY, "the scores of B*Hq*max_pages_per_seq*page_size keys are over 2^44 bytes");
     LaunchEnv env;
     st = device_env(stream, &env);
     if (st != ATTN_OK) return st;

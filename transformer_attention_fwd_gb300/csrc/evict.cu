@@ -40,7 +40,9 @@ struct EvictParams {
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxHeld = 40960;  // weights in shared memory; of longer requests those behind are read again
+// Weights in shared memory; of longer requests those behind are read again.  (As many as leave room for two
+// CTAs on an SM: the table's width sizes them, whatever the requests' lengths.)
+constexpr int kMaxHeld = 24576;
 constexpr int kPages = 1024;     // pages whose places are
 constexpr int kList = 1024;      // keys that share the first digit, if they are so few
 constexpr int kFew = 64;         // so few are compared with one another

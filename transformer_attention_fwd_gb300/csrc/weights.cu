@@ -81,23 +81,11 @@ __device__ __forceinline__ void load_key(const WeightsParams& p, int64_t row, in
     }
 }
 
-// Block (x, y, z): keys x * kBlockKeys .. of KV head y of request z.
+// Adds up the 32 keys from key0 on of one (request, KV head), by a warp.
 template <int D, bool kF16, bool kFour>
-__global__ void __launch_bounds__(kWarps * 32)
-weights_kernel(const WeightsParams p) {
-    grid_wait();
-    grid_launch_next();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
-    const int hkv = blockIdx.y, b = blockIdx.z;
-    const WeightsRequest r = weights_request(p, b);
-    if (!r.ok) {
-        if (blockIdx.x == 0 && hkv == 0 && threadIdx.x == 0) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
-        return;
-    }
-    const int len = r.len, begin = r.begin, n = r.end - r.begin;
-    const int key0 = blockIdx.x * kBlockKeys + warp * kWarpKeys;
-    if (n == 0 || key0 >= len) return;
-
+__device__ __forceinline__ void weights_keys(const WeightsParams& p, const WeightsRequest& req, int b, int hkv, int key0,
+                                             int g, int t) {
+    const int len = req.len, begin = req.begin, n = req.end - req.begin;
     // Rows g, g + 8, g + 16, g + 24 of the warp's keys.
     uint32_t kw[4][D / 8];
     int64_t slot[4];  // of the weights; negative: none
@@ -175,6 +163,23 @@ weights_kernel(const WeightsParams p) {
     }
 }
 
+// Block (x, y, z): keys x * kBlockKeys .. of KV heads y, y + gridDim.y, .. of requests z, z + gridDim.z, ..
+template <int D, bool kF16, bool kFour>
+__global__ void __launch_bounds__(kWarps * 32)
+weights_kernel(const WeightsParams p) {
+    grid_wait();
+    grid_launch_next();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
+    for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
+        const WeightsRequest r = weights_request(p, b);
+        if (!r.ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
+        const int key0 = blockIdx.x * kBlockKeys + warp * kWarpKeys;
+        if (!r.ok || r.end == r.begin || key0 >= r.len) continue;
+        for (int hkv = blockIdx.y; hkv < p.Hkv; hkv += gridDim.y)
+            weights_keys<D, kF16, kFour>(p, r, b, hkv, key0, g, t);
+    }
+}
+
 template <int D, bool kFour>
 cudaError_t launch_type(const WeightsParams& p, dim3 grid, bool f16, cudaStream_t st) {
     return f16 ? launch_serial(weights_kernel<D, true, kFour>, grid, kWarps * 32, 0, st, p)
@@ -186,8 +191,7 @@ cudaError_t launch_type(const WeightsParams& p, dim3 grid, bool f16, cudaStream_
 cudaError_t launch_weights_paged(const WeightsShape& s, const LaunchEnv& env, int* grid_out, int* kernels_launched) {
     const WeightsParams p = weights_params(s, env);
     const long long keys = static_cast<long long>(s.max_pages) * s.page;
-    const dim3 grid(static_cast<unsigned>((keys + kBlockKeys - 1) / kBlockKeys), s.Hkv, s.B);
-    if (s.Hkv > 65535 || s.B > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>((keys + kBlockKeys - 1) / kBlockKeys), std::min(s.Hkv, 65535), std::min(s.B, 65535));
     *grid_out = static_cast<int>(grid.x);
     *kernels_launched = 1;
     if (s.scales)

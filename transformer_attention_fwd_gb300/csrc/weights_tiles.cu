@@ -799,14 +799,13 @@ weights_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 }
 
 // Adds the partial sums of requests with several ranges, in their order.  Block (x, y, z): keys
-// of KV head y of requests z, z + gridDim.z, ..
+// of KV heads y, y + gridDim.y, .. of requests z, z + gridDim.z, ..
 constexpr int kAddThreads = 256;
 
 __global__ void __launch_bounds__(kAddThreads) weights_ranges_kernel(const __grid_constant__ TilesParams p) {
     __shared__ int s_base[kAddThreads / 32];
     grid_wait();
     grid_launch_next();
-    const int hkv = blockIdx.y;
     for (int b = blockIdx.z; b < p.w.B; b += gridDim.z) {
         const WeightsRequest r = weights_request(p.w, b);
         const int n = r.ok ? r.end - r.begin : 0;
@@ -829,9 +828,12 @@ __global__ void __launch_bounds__(kAddThreads) weights_ranges_kernel(const __gri
             const int id = p.w.block_table[static_cast<int64_t>(b) * p.w.max_pages + p.w.page.split(key, &in_page)];
             if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.w.num_blocks)) continue;  // reported
             const int t0 = max(0, (key & -kKeys) - (r.len - n)), ranges = (n - t0 + (1 << p.range_shift) - 1) >> p.range_shift;
-            float sum = 0.0f;
-            for (int i = 0; i < ranges; ++i) sum += p.partial[(static_cast<int64_t>(base + i) * p.w.Hkv + hkv) * p.keys + key];
-            p.w.weights[(static_cast<int64_t>(id) * p.w.Hkv + hkv) * p.w.page.size + in_page] += sum;
+            for (int hkv = blockIdx.y; hkv < p.w.Hkv; hkv += gridDim.y) {
+                float sum = 0.0f;
+                for (int i = 0; i < ranges; ++i)
+                    sum += p.partial[(static_cast<int64_t>(base + i) * p.w.Hkv + hkv) * p.keys + key];
+                p.w.weights[(static_cast<int64_t>(id) * p.w.Hkv + hkv) * p.w.page.size + in_page] += sum;
+            }
         }
     }
 }
@@ -842,8 +844,9 @@ constexpr long long kPartialBytes = 64ll << 20;
 int range_shift_of(const WeightsShape& s) {
     const long long keys = static_cast<long long>(s.max_pages) * s.page;
     int shift = kKeyShift + 1;
-    while (s.total >> shift > 0 && ((2ll * s.total >> shift) * s.Hkv * keys * 4 > kPartialBytes ||
-                                    ((keys >> kKeyShift) + 1) * ((s.total >> shift) + 1) > 0x3fffffffll))
+    while (s.total >> shift > 0 &&
+           (static_cast<double>(2ll * s.total >> shift) * s.Hkv * keys * 4 > kPartialBytes ||  // (may pass 64 bits)
+            ((keys >> kKeyShift) + 1) * ((s.total >> shift) + 1) > 0x3fffffffll))
         ++shift;
     return shift;
 }
@@ -908,7 +911,7 @@ cudaError_t launch_weights_tiles(const WeightsShape& s, const WeightsMaps& maps,
     cudaError_t e = s.D == 64 ? launch_loads<64>(maps, p, s.f16 != 0, loads, grid, env)
                               : launch_loads<128>(maps, p, s.f16 != 0, loads, grid, env);
     if (e != cudaSuccess || !ws) return e;
-    const unsigned y = static_cast<unsigned>(s.Hkv), z = static_cast<unsigned>(std::min(s.B, 64));
+    const unsigned y = static_cast<unsigned>(std::min(s.Hkv, 65535)), z = static_cast<unsigned>(std::min(s.B, 64));
     const long long want = std::max(1ll, 8ll * env.num_sms / (static_cast<long long>(y) * z));
     const unsigned x = static_cast<unsigned>(std::min(want, (p.keys + kAddThreads - 1) / kAddThreads));
     return launch_serial(weights_ranges_kernel, dim3(x, y, z), kAddThreads, 0, env.stream, p);
