@@ -205,12 +205,11 @@ __global__ void __launch_bounds__(kSelectThreads, 3) evict_select_kernel(const E
                 }
             }
             __syncthreads();
-            // Thread i has bins 4 i .. 4 i + 3; counts from the top bin down.
+            // Thread i has bins kPer i and on; counts from the top bin down.
             constexpr int kPer = kBins / kSelectThreads;
-            static_assert(kPer == 4, "a thread's bins are one int4");
-            const int4 bins = reinterpret_cast<const int4*>(s_bin)[tid];
-            const int mine[kPer] = {bins.x, bins.y, bins.z, bins.w};
-            const int own = (bins.x + bins.y) + (bins.z + bins.w);
+            int mine[kPer], own = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) own += mine[i] = s_bin[tid * kPer + i];
             int above = own;  // in this and all higher lanes, then warps
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
