@@ -484,55 +484,47 @@ __device__ void load_lse(const TilesParams& p, Control* ctl, int lane, const Wai
         head_at[i] = (row - token[i] * w.group) * w.lse_head;
         if (token[i] >= p.tile_tokens) token[i] = 1 << 30;  // no row
     }
+    // The next kAhead tiles' values are on their way in registers (one tile ahead, a tile took the
+    // reads' latency: 30 us of a prompt's 77).  A tile's are handed over before the next are asked
+    // for, so that a wait for another item holds up nothing that the item before needs.
+    constexpr int kAhead = 4;
     Items items(ctl, lane, g);
     Item it{};
     bool more = items.take(it);
     int t = it.t0;
-    unsigned there[2] = {0, 0};  // which rows of the last two tiles asked for exist
-    uint32_t asked = 0, made = 0;
-    auto ask = [&]() -> bool {  // the next tile's copies; false: aborted
-        const uint32_t s = asked % kQStages;
-        there[1] = there[0];
-        there[0] = 0;
-        if (more) {
-            if (asked >= kQStages &&
-                !__all_sync(0xffffffffu, mbar_wait(&ctl->l_empty[s], ((asked / kQStages) & 1) ^ 1, g, SITE_W_L_EMPTY)))
-                return false;
-            const float* from = w.lse + it.hkv * w.group * w.lse_head + (it.begin + t) * w.lse_token;
+    float v[kAhead][kOwn];
+    bool there[kAhead];
+    auto ask = [&](float (&x)[kOwn]) -> bool {  // the next tile's values; false: there is none
+        if (!more) return false;
+        const float* from = w.lse + it.hkv * w.group * w.lse_head + (it.begin + t) * w.lse_token;
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i)
-                if (token[i] < it.t1 - t) {
-                    there[0] |= 1u << i;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
-                                 :: "r"(smem_u32(&ctl->nlse[s][lane + 32 * i])), "l"(from + head_at[i] + token[i] * w.lse_token)
-                                 : "memory");
-                }
-            ++asked;
-            t += p.tile_tokens;
-            if (t >= it.t1) {
-                more = items.take(it);
-                t = it.t0;
-            }
+        for (int i = 0; i < kOwn; ++i) x[i] = token[i] < it.t1 - t ? from[head_at[i] + token[i] * w.lse_token] : INFINITY;
+        t += p.tile_tokens;
+        if (t >= it.t1) {
+            more = items.take(it);
+            t = it.t0;
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
         return true;
     };
-    bool ok = ask();
-    while (ok && made < asked) {
-        ok = ask();  // one tile ahead
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        const uint32_t s = made % kQStages;
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) {  // a row that saw nothing (-inf) adds nothing, as no row does
-            float* at = &ctl->nlse[s][lane + 32 * i];
-            const float v = there[1] >> i & 1u ? *at : INFINITY;
-            *at = v == -INFINITY ? -INFINITY : -v * kWeightsLog2e;
+    for (int a = 0; a < kAhead; ++a) there[a] = ask(v[a]);
+    uint32_t l_it = 0;
+    while (there[0]) {
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a, ++l_it) {
+            if (!there[a]) return;
+            const uint32_t s = l_it % kQStages;
+            if (l_it >= kQStages &&
+                !__all_sync(0xffffffffu, mbar_wait(&ctl->l_empty[s], ((l_it / kQStages) & 1) ^ 1, g, SITE_W_L_EMPTY)))
+                return;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i)  // a row that saw nothing (-inf) adds nothing, as no row does
+                ctl->nlse[s][lane + 32 * i] = v[a][i] == -INFINITY ? -INFINITY : -v[a][i] * kWeightsLog2e;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->l_full[s]);
+            there[a] = ask(v[a]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->l_full[s]);
-        ++made;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // S[tmem cols] = keys . queries^T: M = 128, N as idesc has it, K = D in steps of 16.
