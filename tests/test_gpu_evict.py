@@ -103,6 +103,69 @@ def test_weights_of_all_kinds(kind, four):
 
 
 @fours
+@pytest.mark.parametrize("lens,keep,recent,kw", [
+    ([2049], 1000, 100, dict(Hkv=1)),
+    ([2175, 2177], 2048, 2048, dict(Hkv=1, D=64, page=1)),
+    ([5000, 0, 1300], 1290, 0, dict(Hkv=1, page=5, D=64)),
+    ([16385], 16384, 5, dict(Hkv=1, page=64)),
+    ([17000], 8200, 8199, dict(Hkv=1, page=1, dtype=torch.float16)),
+    ([20000, 300, 9001], 5000, 1, dict(Hkv=2, page=24)),
+    ([16000], 15000, 3, dict(Hkv=3, D=64)),
+    ([200001], 3000, 700, dict(Hkv=1, D=64, page=256)),
+])
+def test_few_long_ones(lens, keep, recent, kw, four):
+    a = attn()
+    Problem(lens, **kw, four=four, seed=178).check(a, keep, recent)
+
+
+@fours
+@pytest.mark.parametrize("kind", ["equal", "nan in one place", "a thousand of a digit", "last few", "one digit"])
+def test_few_long_ones_of_all_kinds(kind, four):
+    a = attn()
+    pr = Problem([20000], Hkv=1, four=four, page=16, seed=179)
+    g = torch.Generator().manual_seed(180)
+    w = pr.weights
+    at = lambda slot: (int(pr.table[0, slot // 16]), 0, slot % 16)
+    if kind == "equal":
+        w[:] = 0.25
+    elif kind == "nan in one place":
+        w[at(13001)] = math.nan
+    elif kind == "a thousand of a digit":  # and those close by, so that the second digit decides
+        w[:] = 4 * torch.rand(w.shape, generator=g)
+        for i in range(1100):
+            w[at(18 * i)] = 1.0 + i * 2.0 ** -14
+    elif kind == "last few":
+        w[:] = 0
+        for slot in range(15000, 15050):
+            w[at(slot)] = slot % 7
+    else:
+        w.view(torch.int32)[:] = torch.randint(0, 4, w.shape, generator=g, dtype=torch.int32) << 21
+    for keep, recent in ((10000, 10), (15000, 0), (6000, 5990), (19999, 1)):
+        pr.check(a, keep, recent)
+
+
+@fours
+def test_bad_blocks_of_a_long_one(four):
+    a = attn()
+    pr = Problem([9000], Hkv=1, four=four, seed=181)
+    for bad in (-1, pr.weights.shape[0]):
+        table = pr.table.clone()
+        table[0, 100] = table[0, 400] = bad
+        got = pr.run(a, 4000, 50, table=table)
+        assert a.device_status() == a.ATTN_ERR_BAD_INPUT
+        kept = got[3].cpu()[0, 0].long()
+        assert int(got[2][0]) == 4000 and torch.equal(kept[-50:], torch.arange(8950, 9000))
+        assert bool((kept[1:] > kept[:-1]).all())
+        slots = torch.arange(9000)
+        w = pr.weights[table[0].clamp(0, pr.weights.shape[0] - 1).long()[slots // 16], 0, slots % 16].clone()
+        w[(slots // 16 == 100) | (slots // 16 == 400)] = math.nan
+        w = w.tolist()
+        heaviest = sorted(range(8950), key=lambda i: (math.isnan(w[i]), 0.0 if math.isnan(w[i]) else -w[i], i))[:3950]
+        assert kept[:-50].tolist() == sorted(heaviest)
+    check_status(a)
+
+
+@fours
 def test_evicted_again_and_again(four):
     """Each eviction's result is the next one's input; pages past the kept keys are free."""
     a = attn()

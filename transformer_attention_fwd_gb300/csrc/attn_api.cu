@@ -1328,7 +1328,8 @@ attn_status run_evict(bool four, void* kv_cache, void* scales, float* weights, c
     if (st != ATTN_OK) return st;
     if (keep < 1 || recent < 0 || recent > keep)
         return fail(ATTN_ERR_INVALID_ARG, "keep must be >= 1 and recent in 0..keep (got %d, %d)", keep, recent);
-    if (keep > 0x7fffffff - 65536) return fail(ATTN_ERR_INVALID_ARG, "keep must be below 2^31 - 65536");
+    if (keep > 0x7fffffff - 65536 || static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffff - 65536)
+        return fail(ATTN_ERR_INVALID_ARG, "keep and max_pages_per_seq*page_size must be below 2^31 - 65536");
     if (!new_lens || !aligned(new_lens, 4) || !aligned(kept, 4))
         return fail(ATTN_ERR_INVALID_ARG, "new_lens must be non-null, and new_lens and kept 4-byte aligned");
     if (4.0 * B * Hkv * keep > kMaxWorkspace) return fail(ATTN_ERR_INVALID_ARG, "B*Hkv*keep must be below 2^42");

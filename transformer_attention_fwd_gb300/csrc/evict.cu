@@ -10,8 +10,10 @@
 // so in place is safe if a row is read before its slot is written: slots are taken in order,
 // a chunk is read whole before any of it is written, and the next chunk is read before that
 // too (its rows lie above every slot of this one).  Columns of a row have nothing to do with
-// one another: where (request, KV head) pairs are few their columns go to CTAs of their own,
-// instead of CTAs that would have to wait for one another.
+// one another: where (request, KV head) pairs are few their columns go to CTAs of their own.
+// Where that leaves SMs idle, a cluster of CTAs takes a run of slots, or of rows, each: the
+// histograms meet in the first one's shared memory, and a chunk is read by all before any of
+// it is written.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -37,6 +39,7 @@ struct EvictParams {
     int held;  // weights a CTA of the first kernel has room for
 };
 
+constexpr int kMaxRanks = 8;  // CTAs of a cluster
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
@@ -58,6 +61,47 @@ __device__ __forceinline__ uint32_t ordered(uint32_t raw) {
 // The weight of a key (not of -0 and NaN, which are not told apart).
 __device__ __forceinline__ uint32_t weight_of(uint32_t key) { return (key & 0x80000000u) ? key ^ 0x80000000u : ~key; }
 
+// The CTAs that share a unit: a cluster.
+template <bool kCluster>
+struct Team {
+    const int ranks, rank;
+    __device__ __forceinline__ void sync() const {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    // Shared memory of another CTA of the cluster, at this CTA's address.
+    static __device__ __forceinline__ uint32_t of(const void* p, int rank) {
+        uint32_t r;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+        return r;
+    }
+    static __device__ __forceinline__ int read(const int* p, int rank) {
+        int v;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(of(p, rank)) : "memory");
+        return v;
+    }
+    static __device__ __forceinline__ void write(uint32_t* p, int rank, uint32_t v) {
+        asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(of(p, rank)), "r"(v) : "memory");
+    }
+    static __device__ __forceinline__ int add(int* p, int rank, int v) {
+        int old;
+        asm volatile("atom.shared::cluster.add.s32 %0, [%1], %2;" : "=r"(old) : "r"(of(p, rank)), "r"(v) : "memory");
+        return old;
+    }
+};
+
+// One CTA (which the runtime form costs 4% of a long eviction of many).
+template <>
+struct Team<false> {
+    static constexpr int ranks = 1, rank = 0;
+    __device__ __forceinline__ Team(int, int) {}
+    __device__ __forceinline__ void sync() const { __syncthreads(); }
+    static __device__ __forceinline__ int read(const int* p, int) { return *p; }
+    static __device__ __forceinline__ void write(uint32_t* p, int, uint32_t v) { *p = v; }
+    static __device__ __forceinline__ int add(int* p, int, int v) { return atomicAdd(p, v); }
+};
+
 // A request's slots; len: 0 if out of range (reported by the first kernel).
 struct Slots {
     const EvictParams& p;
@@ -78,28 +122,43 @@ struct Slots {
     }
 };
 
-__global__ void __launch_bounds__(kSelectThreads, 3) evict_select_kernel(const EvictParams p) {
-    extern __shared__ __align__(16) uint32_t s_key[];  // [held]
+// What the ranks of a unit agree on, in the first one's shared memory.
+struct Agreed {
+    int digit, above, found, count, odd;
+};
+
+template <bool kCluster>
+__global__ void __launch_bounds__(kSelectThreads, 3) evict_select_kernel(const EvictParams p, int all_ranks) {
+    extern __shared__ __align__(16) uint32_t s_key[];  // [held], of this rank's slots
     __shared__ __align__(16) int s_bin[kBins];
     __shared__ int64_t s_page[kPages];  // first weight of a page; negative: none
     __shared__ uint32_t s_list[kList];
     __shared__ int s_warp[kSelectWarps][2];
-    __shared__ int s_digit, s_above, s_count, s_odd;
-    __shared__ uint32_t s_found;
+    __shared__ int s_total[2];
+    __shared__ Agreed s_agreed;
     grid_wait();
     grid_launch_next();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    for (long long unit = blockIdx.x; unit < static_cast<long long>(p.B) * p.Hkv; unit += gridDim.x) {
+    const Team<kCluster> team{all_ranks, static_cast<int>(blockIdx.x) % all_ranks};
+    const int ranks = team.ranks;
+    const bool lead = team.rank == 0;
+    const long long units = static_cast<long long>(p.B) * p.Hkv;
+    for (long long unit = blockIdx.x / ranks; unit < units; unit += gridDim.x / ranks) {
         const int b = static_cast<int>(unit / p.Hkv), hkv = static_cast<int>(unit % p.Hkv);
-        const Slots slots(p, b, hkv == 0 && tid == 0);
+        const Slots slots(p, b, hkv == 0 && lead && tid == 0);
         int* kept = p.kept + unit * p.keep;
-        if (hkv == 0 && tid == 0) p.new_lens[b] = min(slots.len, p.keep);
+        if (hkv == 0 && lead && tid == 0) p.new_lens[b] = min(slots.len, p.keep);
         if (slots.len <= p.keep) {
-            for (int i = tid; i < p.keep; i += kSelectThreads) kept[i] = i < slots.len ? i : -1;
+            if (lead)
+                for (int i = tid; i < p.keep; i += kSelectThreads) kept[i] = i < slots.len ? i : -1;
             continue;
         }
         const int n = slots.len - p.recent, want = p.keep - p.recent;  // candidates, those of them kept
-        const int held = min(slots.len, p.held);
+        // This rank's slots, and the candidates and held weights among them.
+        constexpr int kStep = 128;
+        const int per = ((slots.len + ranks - 1) / ranks + kStep - 1) / kStep * kStep;
+        const int lo = static_cast<int>(min(static_cast<long long>(slots.len), static_cast<long long>(team.rank) * per));
+        const int hi = lo + min(slots.len - lo, per), last = max(lo, min(hi, n)), held = lo + min(hi - lo, p.held);
         const int pages = p.page.quotient(slots.len - 1) + 1;
         auto page_at = [&](int page) -> int64_t {
             const int id = slots.block(page);
@@ -108,8 +167,8 @@ __global__ void __launch_bounds__(kSelectThreads, 3) evict_select_kernel(const E
         __syncthreads();  // the unit before has been read
         for (int i = tid; i < min(pages, kPages); i += kSelectThreads) s_page[i] = page_at(i);
         for (int i = tid; i < kBins; i += kSelectThreads) s_bin[i] = 0;
-        if (tid == 0) s_count = s_odd = 0;
-        __syncthreads();
+        if (tid == 0) s_agreed.count = s_agreed.odd = 0;
+        team.sync();
         auto at = [&](int slot) -> float* {
             int row;
             const int page = p.page.split(slot, &row);
@@ -122,7 +181,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) evict_select_kernel(const E
         };
         // The weights, and the first digit's histogram.
         bool odd = false;
-        for (int i0 = tid; i0 < held; i0 += kBatch * kSelectThreads) {
+        for (int i0 = lo + tid; i0 < held; i0 += kBatch * kSelectThreads) {
             const float* from[kBatch];
             uint32_t raw[kBatch];
 #pragma unroll
@@ -136,18 +195,18 @@ __global__ void __launch_bounds__(kSelectThreads, 3) evict_select_kernel(const E
                 if (i >= held) break;
                 odd |= raw[u] == 0x80000000u || (raw[u] & 0x7fffffffu) > 0x7f800000u;
                 const uint32_t k = ordered(raw[u]);
-                s_key[i] = k;
+                s_key[i - lo] = k;
                 if (i < n) atomicAdd(&s_bin[k >> 21], 1);
             }
         }
-        if (odd) s_odd = 1;
-        for (int i = held + tid; i < n; i += kSelectThreads) atomicAdd(&s_bin[ordered(load(i)) >> 21], 1);
-        // Keys i .. i + 3 (i a multiple of 4; those from n on are not to be looked at).
+        for (int i = held + tid; i < last; i += kSelectThreads) atomicAdd(&s_bin[ordered(load(i)) >> 21], 1);
+        if (odd || hi > held) team.add(&s_agreed.odd, 0, 1);  // not all at hand, or not as they are
+        // Keys i .. i + 3 (i - lo a multiple of 4; those from `last` on are not to be looked at).
         auto keys = [&](int i) {
-            if (i + 3 < held) return *reinterpret_cast<const uint4*>(s_key + i);
+            if (i + 3 < held) return *reinterpret_cast<const uint4*>(s_key + (i - lo));
             uint32_t k[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) k[u] = i + u < held ? s_key[i + u] : i + u < n ? ordered(load(i + u)) : 0u;
+            for (int u = 0; u < 4; ++u) k[u] = i + u < held ? s_key[i + u - lo] : i + u < last ? ordered(load(i + u)) : 0u;
             return make_uint4(k[0], k[1], k[2], k[3]);
         };
 
@@ -158,85 +217,95 @@ __global__ void __launch_bounds__(kSelectThreads, 3) evict_select_kernel(const E
         for (int shift = 32, bits = 11; shift > 0 && want > 0; shift -= bits, bits = shift < 11 ? shift : 11) {
             const int low = shift - bits;
             const uint32_t mask = (1u << bits) - 1;
-            if (shift == 21) {  // those with the first digit, if they are few
-                for (int i = 4 * tid; i < n; i += 4 * kSelectThreads) {
-                    const uint4 k = keys(i);
-                    const uint32_t v[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (i + u < n && (v[u] >> 21) == prefix) {
-                            const int place = atomicAdd(&s_count, 1);
-                            if (place < kList) s_list[place] = v[u];
-                        }
-                }
-            }
+            bool few = false;  // the first rank goes on alone
             if (shift < 32) {
                 for (int i = tid; i < kBins; i += kSelectThreads) s_bin[i] = 0;
-                __syncthreads();
-                const int some = s_count;
-                if (some <= kFew) {  // each counts those over it
-                    const uint32_t own = tid < some ? s_list[tid] : 0u;
-                    int greater = 0, same = 0;
-                    if (tid < kFew)
-                        for (int i = 0; i < some; ++i) {
-                            greater += s_list[i] > own;
-                            same += s_list[i] == own;
-                        }
-                    if (tid < some && greater < left && left <= greater + same) {  // the same key and count in each that is it
-                        s_found = own;
-                        s_above = greater;
-                    }
-                    __syncthreads();
-                    prefix = s_found;
-                    left -= s_above;
-                    break;
-                }
-                if (some <= kList) {
-                    for (int i = tid; i < some; i += kSelectThreads)
-                        if ((s_list[i] >> shift) == prefix) atomicAdd(&s_bin[s_list[i] >> low & mask], 1);
-                } else {
-                    for (int i = 4 * tid; i < n; i += 4 * kSelectThreads) {
+                if (shift == 21)  // those with the first digit, if they are few, to the first rank
+                    for (int i = lo + 4 * tid; i < last; i += 4 * kSelectThreads) {
                         const uint4 k = keys(i);
                         const uint32_t v[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            if (i + u < n && (v[u] >> shift) == prefix) atomicAdd(&s_bin[v[u] >> low & mask], 1);
+                            if (i + u < last && (v[u] >> 21) == prefix) {
+                                const int place = team.add(&s_agreed.count, 0, 1);
+                                if (place < kList) team.write(&s_list[place], 0, v[u]);
+                            }
+                    }
+                team.sync();
+                const int some = team.read(&s_agreed.count, 0);
+                few = some <= kList;
+                if (some <= kFew) {  // each counts those over it
+                    if (lead && tid < some) {
+                        const uint32_t own = s_list[tid];
+                        int greater = 0, same = 0;
+                        for (int i = 0; i < some; ++i) {
+                            greater += s_list[i] > own;
+                            same += s_list[i] == own;
+                        }
+                        if (greater < left && left <= greater + same) {  // the same key and count in each that is it
+                            s_agreed.found = static_cast<int>(own);
+                            s_agreed.above = greater;
+                        }
+                    }
+                    team.sync();
+                    prefix = static_cast<uint32_t>(team.read(&s_agreed.found, 0));
+                    left -= team.read(&s_agreed.above, 0);
+                    break;
+                }
+                if (few) {
+                    if (lead)
+                        for (int i = tid; i < some; i += kSelectThreads)
+                            if ((s_list[i] >> shift) == prefix) atomicAdd(&s_bin[s_list[i] >> low & mask], 1);
+                } else {
+                    for (int i = lo + 4 * tid; i < last; i += 4 * kSelectThreads) {
+                        const uint4 k = keys(i);
+                        const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (i + u < last && (v[u] >> shift) == prefix) atomicAdd(&s_bin[v[u] >> low & mask], 1);
                     }
                 }
             }
-            __syncthreads();
-            // Thread i has bins kPer i and on; counts from the top bin down.
-            constexpr int kPer = kBins / kSelectThreads;
-            int mine[kPer], own = 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) own += mine[i] = s_bin[tid * kPer + i];
-            int above = own;  // in this and all higher lanes, then warps
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_down_sync(0xffffffffu, above, o);
-                if (lane + o < 32) above += x;
+            if (ranks > 1 && !few) {  // all histograms into the first rank's
+                team.sync();
+                if (!lead)
+                    for (int i = tid; i < kBins; i += kSelectThreads)
+                        if (s_bin[i] > 0) team.add(&s_bin[i], 0, s_bin[i]);
             }
-            if (lane == 0) s_warp[warp][0] = above;
-            __syncthreads();
-            for (int i = warp + 1; i < kSelectWarps; ++i) above += s_warp[i][0];
-            above -= own;
+            team.sync();
+            if (lead) {
+                // Thread i has bins kPer i and on; counts from the top bin down.
+                constexpr int kPer = kBins / kSelectThreads;
+                int mine[kPer], own = 0;
 #pragma unroll
-            for (int i = kPer - 1; i >= 0; --i) {
-                if (above < left && left <= above + mine[i]) {
-                    s_digit = tid * kPer + i;
-                    s_above = above;
+                for (int i = 0; i < kPer; ++i) own += mine[i] = s_bin[tid * kPer + i];
+                int above = own;  // in this and all higher lanes, then warps
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_down_sync(0xffffffffu, above, o);
+                    if (lane + o < 32) above += x;
                 }
-                above += mine[i];
+                if (lane == 0) s_warp[warp][0] = above;
+                __syncthreads();
+                for (int i = warp + 1; i < kSelectWarps; ++i) above += s_warp[i][0];
+                above -= own;
+#pragma unroll
+                for (int i = kPer - 1; i >= 0; --i) {
+                    if (above < left && left <= above + mine[i]) {
+                        s_agreed.digit = tid * kPer + i;
+                        s_agreed.above = above;
+                    }
+                    above += mine[i];
+                }
             }
-            __syncthreads();
-            prefix = prefix << bits | static_cast<uint32_t>(s_digit);
-            left -= s_above;
+            team.sync();
+            prefix = prefix << bits | static_cast<uint32_t>(team.read(&s_agreed.digit, 0));
+            left -= team.read(&s_agreed.above, 0);
         }
 
         // Kept slots in order: a warp has a run of them, four to a lane at a time, and counts first.
-        constexpr int kStep = 128;
-        const int run = (n + kSelectWarps * kStep - 1) / (kSelectWarps * kStep) * kStep;
-        const int from = static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(warp) * run)), to = min(n, from + run);
+        const int run = (last - lo + kSelectWarps * kStep - 1) / (kSelectWarps * kStep) * kStep;
+        const int from = min(last, lo + warp * run), to = min(last, from + run);
         int over = 0, equal = 0;
         for (int i = from + 4 * lane; i < to; i += kStep) {
             const uint4 k = keys(i);
@@ -256,12 +325,22 @@ __global__ void __launch_bounds__(kSelectThreads, 3) evict_select_kernel(const E
         }
         __syncthreads();
         over = equal = 0;
-        for (int i = 0; i < warp; ++i) {
+        for (int i = 0; i < kSelectWarps; ++i) {
+            if (i == warp && lane == 0 && warp == kSelectWarps - 1) {
+                s_total[0] = over + s_warp[i][0];
+                s_total[1] = equal + s_warp[i][1];
+            }
+            if (i >= warp) continue;
             over += s_warp[i][0];
             equal += s_warp[i][1];
         }
+        team.sync();  // and every rank's weights have been read
+        for (int i = 0; i < team.rank; ++i) {
+            over += team.read(&s_total[0], i);
+            equal += team.read(&s_total[1], i);
+        }
         // With all weights at hand they are written as their slots are found.
-        const bool whole = slots.len <= p.held && s_odd == 0;
+        const bool whole = team.read(&s_agreed.odd, 0) == 0;
         auto place = [&](int slot, uint32_t raw) {
             float* w = at(slot);
             if (w) *w = __uint_as_float(raw);
@@ -298,38 +377,42 @@ __global__ void __launch_bounds__(kSelectThreads, 3) evict_select_kernel(const E
                 over += all & 0xffff;
                 equal += all >> 16;
             }
-        for (int i = tid; i < p.recent; i += kSelectThreads) {
-            kept[want + i] = n + i;
-            if (whole) place(want + i, weight_of(s_key[n + i]));
+        for (int i = max(n, lo) + tid; i < hi; i += kSelectThreads) {  // the recent ones
+            kept[want + i - n] = i;
+            if (whole) place(want + i - n, weight_of(s_key[i - lo]));
         }
-        if (!whole) {  // the weights follow as the rows do
-            __syncthreads();
-            for (int i0 = 0; i0 < p.keep; i0 += kSelectThreads) {
-                const int i = i0 + tid;
-                uint32_t raw = 0;
-                if (i < p.keep) raw = load(kept[i]);
-                __syncthreads();
-                if (i < p.keep) place(i, raw);
+        if (!whole) {  // the weights follow as the rows do, by the first rank
+            team.sync();
+            if (lead) {
+                for (int i0 = 0; i0 < p.keep; i0 += kSelectThreads) {
+                    const int i = i0 + tid;
+                    uint32_t raw = 0;
+                    if (i < p.keep) raw = load(kept[i]);
+                    __syncthreads();
+                    if (i < p.keep) place(i, raw);
+                }
             }
-            __syncthreads();
+            team.sync();
         }
 #pragma unroll 4
-        for (int i = p.keep + tid; i < slots.len; i += kSelectThreads) place(i, 0u);  // none of these is read again
+        for (int i = max(p.keep, lo) + tid; i < hi; i += kSelectThreads) place(i, 0u);  // none of these is read again
+        if (ranks > 1) team.sync();  // the first rank's memory has been read
     }
 }
 
 constexpr int kMoveThreads = 256;
 // Pieces of a thread in a chunk; two chunks are in flight.  A warp's lanes find the places of a row
-// each, so of small rows a chunk has no more.
+// each, so of small rows a chunk has no more.  (Four of those too, two rows to a lane: 3 us less
+// for one head of 4000 keys of 16 bits, but 4-bit rows take 10 to 20% longer.)
 template <int kPieces>
 constexpr int kDepthOf = kPieces < 4 ? kPieces : 4;
 
 // Moves one column range of the kept rows of (request, KV head, K or V): pieces of T, kPieces to a
 // row, at byte `first` of rows of row_bytes.  A warp's lanes find the places of its rows of a
 // chunk, a row each, and hand them round.
-template <typename T, int kPieces>
+template <typename T, int kPieces, typename Team>
 __device__ __forceinline__ void move_rows(const EvictParams& p, uint8_t* base, int row_bytes, int first,
-                                          const Slots& slots, const int* kept, int side, int hkv) {
+                                          const Slots& slots, const int* kept, int side, int hkv, const Team& team) {
     constexpr int kMoveDepth = kDepthOf<kPieces>;
     constexpr int kStep = 32 / kPieces, kRows = kMoveThreads / kPieces;  // rows of a warp, of the CTA, at a time
     constexpr int kChunk = kRows * kMoveDepth, kOwn = kStep * kMoveDepth;  // rows of the CTA's and the warp's chunk
@@ -366,22 +449,24 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, uint8_t* base, i
         for (int u = 0; u < kMoveDepth; ++u)
             if (dst[u] >= 0) *at(dst[u]) = x[u];
     };
-    load(0, v[0], to[0]);
-    for (int i0 = 0; i0 < p.keep; i0 += 2 * kChunk) {
-        if (i0 + kChunk < p.keep) load(i0 + kChunk, v[1], to[1]);
-        __syncthreads();
+    // Each rank has a chunk of its own of the cluster's.
+    const int step = team.ranks * kChunk, own = team.rank * kChunk;
+    load(own, v[0], to[0]);
+    for (int i0 = 0; i0 < p.keep; i0 += 2 * step) {
+        if (i0 + step < p.keep) load(i0 + step + own, v[1], to[1]);
+        team.sync();
         store(v[0], to[0]);
-        if (i0 + kChunk >= p.keep) break;
-        if (i0 + 2 * kChunk < p.keep) load(i0 + 2 * kChunk, v[0], to[0]);
-        __syncthreads();
+        if (i0 + step >= p.keep) break;
+        if (i0 + 2 * step < p.keep) load(i0 + 2 * step + own, v[0], to[0]);
+        team.sync();
         store(v[1], to[1]);
     }
 }
 
-// Block (x, y): unit y of (request, KV head), part x: sides times column ranges, then sides of
-// the scales.
-template <int kRowBytes, int kScaleBytes, int kRanges>
-__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictParams p) {
+// Block (x, y): unit y of (request, KV head), rank x % ranks of part x / ranks: sides times column
+// ranges, then sides of the scales.
+template <int kRowBytes, int kScaleBytes, int kRanges, bool kCluster>
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictParams p, int ranks) {
     grid_wait();
     grid_launch_next();
     for (long long unit = blockIdx.y; unit < static_cast<long long>(p.B) * p.Hkv; unit += gridDim.y) {
@@ -389,14 +474,15 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
         const Slots slots(p, b, false);
         if (slots.len <= p.keep) continue;
         const int* kept = p.kept + unit * p.keep;
-        const int part = blockIdx.x, side = part % 2;
+        const Team<kCluster> team{ranks, static_cast<int>(blockIdx.x) % ranks};
+        const int part = static_cast<int>(blockIdx.x) / team.ranks, side = part % 2;
         constexpr int kBytes = kRowBytes / kRanges;
         if (part < 2 * kRanges)
-            move_rows<uint4, kBytes / 16>(p, p.cache, kRowBytes, part / 2 * kBytes, slots, kept, side, hkv);
+            move_rows<uint4, kBytes / 16>(p, p.cache, kRowBytes, part / 2 * kBytes, slots, kept, side, hkv, team);
         else if constexpr (kScaleBytes == 8)
-            move_rows<uint2, 1>(p, p.scales, 8, 0, slots, kept, side, hkv);
+            move_rows<uint2, 1>(p, p.scales, 8, 0, slots, kept, side, hkv, team);
         else if constexpr (kScaleBytes == 4)
-            move_rows<uint32_t, 1>(p, p.scales, 4, 0, slots, kept, side, hkv);
+            move_rows<uint32_t, 1>(p, p.scales, 4, 0, slots, kept, side, hkv, team);
     }
 }
 
@@ -406,9 +492,18 @@ cudaError_t launch_move(const EvictParams& p, const LaunchEnv& env, int* grid_ou
     const long long units = static_cast<long long>(p.B) * p.Hkv;
     if constexpr (kRanges * 32 < kRowBytes)
         if (2 * kRanges * units < 2ll * env.num_sms) return launch_move<kRowBytes, kScaleBytes, 2 * kRanges>(p, env, grid_out);
-    const dim3 grid(2 * kRanges + (kScaleBytes ? 2 : 0), static_cast<unsigned>(std::min(units, 65535ll)));
+    const int parts = 2 * kRanges + (kScaleBytes ? 2 : 0);
+    int ranks = 1;
+    if constexpr (kRanges * 32 >= kRowBytes)  // until the SMs have two CTAs each, or a rank 512 rows
+        while (ranks < kMaxRanks && 2 * ranks * parts * units <= 2ll * env.num_sms && p.keep > 512 * ranks) ranks *= 2;
+    const dim3 grid(parts * ranks, static_cast<unsigned>(std::min(units, 65535ll)));
     *grid_out = static_cast<int>(grid.x * grid.y);
-    return launch_serial(evict_move_kernel<kRowBytes, kScaleBytes, kRanges>, grid, kMoveThreads, 0, env.stream, p);
+    if constexpr (kRanges * 32 >= kRowBytes)
+        if (ranks > 1)
+            return launch_serial_clusters(evict_move_kernel<kRowBytes, kScaleBytes, kRanges, true>, grid, kMoveThreads,
+                                          0, ranks, env.stream, p, ranks);
+    return launch_serial(evict_move_kernel<kRowBytes, kScaleBytes, kRanges, false>, grid, kMoveThreads, 0, env.stream,
+                         p, 1);
 }
 
 }  // namespace
@@ -430,17 +525,24 @@ cudaError_t launch_evict_paged(const EvictShape& s, const LaunchEnv& env, int* g
     p.num_blocks = s.num_blocks;
     p.keep = s.keep;
     p.recent = s.recent;
-    p.held = static_cast<int>(std::min<long long>((static_cast<long long>(s.max_pages) * s.page + 3) / 4 * 4, kMaxHeld));
     static bool attr_set[64] = {};  // device < 64 (device_env)
     cudaError_t e = cudaSuccess;
     if (!attr_set[env.device]) {
-        e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxHeld * 4);
-        if (e != cudaSuccess) return e;
+        for (auto* kernel : {evict_select_kernel<false>, evict_select_kernel<true>}) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxHeld * 4);
+            if (e != cudaSuccess) return e;
+        }
         attr_set[env.device] = true;
     }
-    const long long units = static_cast<long long>(s.B) * s.Hkv;
-    e = launch_serial(evict_select_kernel, dim3(static_cast<unsigned>(std::min(units, 0x7fffffffll))), kSelectThreads,
-                      static_cast<size_t>(p.held) * 4, env.stream, p);
+    const long long units = static_cast<long long>(s.B) * s.Hkv, keys = static_cast<long long>(s.max_pages) * s.page;
+    int ranks = 1;  // of tables wider than 4096: until the SMs have a CTA each, or a rank 2048 slots
+    while (keys > 4096 && ranks < kMaxRanks && 2 * ranks * units <= env.num_sms && keys > 2048 * ranks) ranks *= 2;
+    const long long per = ((keys + ranks - 1) / ranks + 127) / 128 * 128;
+    p.held = static_cast<int>(std::min<long long>(per, kMaxHeld));
+    const long long clusters = std::min(units, 0x7fffffffll / ranks);
+    auto* select = ranks > 1 ? evict_select_kernel<true> : evict_select_kernel<false>;
+    e = launch_serial_clusters(select, dim3(static_cast<unsigned>(clusters * ranks)), kSelectThreads,
+                               static_cast<size_t>(p.held) * 4, ranks, env.stream, p, ranks);
     if (e != cudaSuccess) return e;
     *kernels_launched = 2;
     if (s.scales) return s.D == 64 ? launch_move<32, 4>(p, env, grid_out) : launch_move<64, 8>(p, env, grid_out);
