@@ -511,8 +511,8 @@ attn_status attn_append_paged_e2m1(const attn_rows* q, const attn_rows* k, const
  *            attention weight is added to its place, summed over the query heads of the
  *            KV head:  weights[block, hkv, row] += sum_h exp(x_h - lse_h), x_h the scaled
  *            score and lse_h the result's log-sum-exp.  Places of other slots stay as
- *            they are.  A block that two requests of the call share gets undefined
- *            weights.  The scores pass through a workspace of
+ *            they are.  A block that requests share gets the weights of all, added up
+ *            in no fixed order.  The scores pass through a workspace of
  *            4 * B * Hq * max_pages_per_seq * page_size bytes.
  * The other arguments, checks, errors and the workspace are those of
  * attn_fwd_decode_paged_e4m3.
@@ -541,10 +541,10 @@ attn_status attn_fwd_decode_paged_e2m1(const void* q, const void* kv_cache, cons
  *               -inf adds nothing.
  *   seq_lens:   [B] int32, the keys of each request, its queries' own among them.
  *   weights:    [num_blocks, Hkv, page_size] float32; places of other slots stay as
- *               they are.  The blocks of the requests that have queries are theirs alone.
+ *               they are.  A block that requests share gets the weights of all.
  *   scale:      finite, > 0.
- * dtype (ATTN_BF16 or ATTN_F16) is q's and the cache's type.  The sums are fp32 in a
- * fixed order.  Device-side checks, reported as ATTN_ERR_BAD_INPUT: a request whose
+ * dtype (ATTN_BF16 or ATTN_F16) is q's and the cache's type.  A request's sums are fp32
+ * in a fixed order; those of requests that share a block are added up in no fixed one.  Device-side checks, reported as ATTN_ERR_BAD_INPUT: a request whose
  * offsets or length are out of range is left out, and so is a slot whose block id is.
  * Queries whose strides are not 0, with up to 128 query heads to a KV head, run on the
  * 5th-generation tensor cores, others on a slower kernel.  Requests with over 512 queries
@@ -581,7 +581,8 @@ attn_status attn_weights_paged_e2m1(const attn_rows* q, const float* lse, long l
  *             past the request's new length.
  * A block belongs to one request of the call.  dtype: ATTN_BF16 or ATTN_F16.  Device-side
  * checks as for attn_weights_paged; a row whose old or new block id is out of range does
- * not move.  Without `kept` it is a workspace.  (No such call over the 8-bit cache:
+ * not move.  Without `kept` it is a workspace.  keep and max_pages_per_seq * page_size
+ * are below 2^31 - 65536.  (No such call over the 8-bit cache:
  * rows of its blocks share a scale, and moving one would round it again.)
  */
 attn_status attn_evict_paged(void* kv_cache, float* weights, const int* block_table,

@@ -205,6 +205,20 @@ def test_unused_rows_and_blocks_are_never_read(way):
 
 
 @ways
+def test_requests_that_share_blocks_add_up(way):
+    a = attn()
+    pr = _problem([300, 290, 700, 4], 8, 2, 128, 16, seed=156)
+    for b in (1, 2):
+        pr[3][b, :15] = pr[3][0, :15]
+    q, cache, scales, table, lens, f, weights = pr
+    o, lse, w = _run(a, way(pr))
+    check_status(a)
+    ref = kv4_ref.decode(q, kv4_ref.held(cache, scales, f), table, lens)
+    kv4_ref.check_decode(o, lse, ref, 700)
+    kv4_ref.check_weights(w, weights, table, lens, ref[4], ref[5], 700)
+
+
+@ways
 def test_nan_in_a_used_row_reaches_its_head_only(way):
     a = attn()
     pr = way(_problem([40, 40], 4, 2, 64, 16, seed=155))

@@ -203,6 +203,18 @@ def test_bad_requests_and_blocks(four):
     check_status(a)
 
 
+@fours
+@pytest.mark.parametrize("Hq,new", [(8, 20), (8, 1), (2, 600), (130, 3)], ids=["prompts", "step", "ranges", "fallback"])
+def test_requests_that_share_blocks_add_up(Hq, new, four):
+    a = attn()
+    pr = Problem([700, 650, 900], [new, new, new], Hq=Hq, Hkv=1, D=64, four=four, seed=183)
+    for b in (1, 2):
+        pr.table[b, :30] = pr.table[0, :30]  # the same first 480 keys
+    w = pr.run(a)
+    check_status(a)
+    pr.check(w)
+
+
 def test_no_tokens_launch_nothing():
     a = attn()
     pr = Problem([5, 3], [0, 0], seed=169)

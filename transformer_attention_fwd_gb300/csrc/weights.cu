@@ -159,7 +159,7 @@ __device__ __forceinline__ void weights_keys(const WeightsParams& p, const Weigh
     for (int i = 0; i < 4; ++i) {
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-        if (t == 0 && slot[i] >= 0) p.weights[slot[i]] += sum[i];
+        if (t == 0 && slot[i] >= 0) atomicAdd(p.weights + slot[i], sum[i]);  // another request may share the block
     }
 }
 

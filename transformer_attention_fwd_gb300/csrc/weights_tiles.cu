@@ -705,7 +705,7 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
         if (set == 0 && key < it.len) {
             if (it.slot >= 0)
                 p.partial[(static_cast<int64_t>(it.slot) * w.Hkv + it.hkv) * p.keys + key] = sum;
-            else if (static_cast<unsigned>(id) < static_cast<unsigned>(w.num_blocks))  // the call's only addition to this key
+            else if (static_cast<unsigned>(id) < static_cast<unsigned>(w.num_blocks))  // the request's only addition to this key
                 atomicAdd(w.weights + (static_cast<int64_t>(id) * w.Hkv + it.hkv) * w.page.size + in_page, sum);
         }
     }
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(kAddThreads) weights_ranges_kernel(const __gri
                 float sum = 0.0f;
                 for (int i = 0; i < ranges; ++i)
                     sum += p.partial[(static_cast<int64_t>(base + i) * p.w.Hkv + hkv) * p.keys + key];
-                p.w.weights[(static_cast<int64_t>(id) * p.w.Hkv + hkv) * p.w.page.size + in_page] += sum;
+                atomicAdd(p.w.weights + (static_cast<int64_t>(id) * p.w.Hkv + hkv) * p.w.page.size + in_page, sum);
             }
         }
     }
