@@ -80,6 +80,10 @@ CASES = [
     dict(lens=[600, 100], new=[2, 5], Hq=130, Hkv=1, D=64),  # more heads than a tile has rows
     dict(lens=[2000, 700, 2600], new=[1400, 30, 513], Hq=2, Hkv=1, D=64),  # ranges of queries
     dict(lens=[1029], new=[1029], Hq=3, Hkv=1, D=64, page=5, dtype="f16"),
+    dict(lens=[33, 500, 0, 700, 257, 64], new=[1, 1, 0, 1, 1, 1], Hq=32, Hkv=2, D=64),  # a step of 16 heads to a KV head
+    dict(lens=[900] + [40] * 30, new=[31] + [0] * 30, Hq=4, Hkv=4),   # eight rows to a request, and all in one
+    dict(lens=[5000, 4100, 1, 3], new=[2, 2, 1, 3], Hq=8, Hkv=2, page=1),
+    dict(lens=[(53 * i) % 700 for i in range(60)], new=[min(1, (53 * i) % 700) for i in range(60)], Hq=7, Hkv=7, page=24),
 ]
 
 

@@ -51,4 +51,26 @@ __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
     return d;
 }
 
+// Codes times scales in fp16 or bf16, exact in either.  Two groups' scales as factors:
+template <bool kF16>
+__device__ __forceinline__ void e2m1_scales(uint32_t codes, uint32_t (&by)[2]) {
+    const uint32_t f = e4m3_to_f16x2(codes);
+    if (kF16) {
+        both_halves(f, by[0], by[1]);
+    } else {
+        const float lo = f16_lo_to_f32(f) * 0x1p112f, hi = f16_hi_to_f32(f) * 0x1p112f;
+        by[0] = pack_bf16x2(lo, lo);
+        by[1] = pack_bf16x2(hi, hi);
+    }
+}
+// fp16 values of two codes times such a factor.  In bf16 their bits, three places down, are the
+// values times 2^-112 (the low bits are 0): no conversion, and the factor has 2^112.
+template <bool kF16>
+__device__ __forceinline__ uint32_t e2m1_times(uint32_t v, uint32_t by) {
+    if (kF16) return f16x2_mul(v, by);
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(((v >> 3) & 0x0fff0fffu) | (v & 0x80008000u)), "r"(by));
+    return d;
+}
+
 }  // namespace attn

@@ -25,9 +25,11 @@
 namespace attn {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kWarpKeys = 32;
-constexpr int kBlockKeys = kWarps * kWarpKeys;
+// A block is a warp: with four, that leave together, a step over 64 x 4096 4-bit keys took 66 us
+// instead of 47, over 16-bit ones 103 instead of 88.
+constexpr int kPerSm = 16;  // blocks an SM has room for (128 registers)
+constexpr int kMostRun = 8;  // chunks of a block
+constexpr int kKeys = 32;  // of a chunk, which a warp reads at a time
 
 template <bool kF16>
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -41,164 +43,246 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A lane's D/4 elements of a K row as words of the queries' type; zeros without a row.
-template <int D, bool kF16, bool kFour>
-__device__ __forceinline__ void load_key(const WeightsParams& p, int64_t row, int t, uint32_t (&w)[D / 8]) {
-    if (kFour) {
-        const uint8_t* codes = p.cache + row * (D / 2) + t * (D / 8);
-        const uint8_t* scales = p.scales + row * (D / kRowScaleSpan) + t * (D / 64);
-        uint32_t c[D / 32] = {}, s = 0;
-        if (row >= 0) {
-            if (D == 128) {
-                const uint4 u = *reinterpret_cast<const uint4*>(codes);
-                c[0] = u.x; c[1] = u.y; c[D / 32 - 2] = u.z; c[D / 32 - 1] = u.w;
-                s = *reinterpret_cast<const uint16_t*>(scales);
-            } else {
-                const uint2 u = *reinterpret_cast<const uint2*>(codes);
-                c[0] = u.x; c[1] = u.y;
-                s = *scales;
-            }
-        }
-        s = e4m3_to_f16x2(s);
-        const uint32_t by[2] = {__byte_perm(s, s, 0x1010), __byte_perm(s, s, 0x3232)};
+// A lane's D/4 elements of a K row as they are in the cache: a run of 4-bit ones, every fourth eight
+// of 16-bit ones, so that four lanes' reads are whole sectors.  Zeros without a row.
+template <int D, bool kFour>
+struct RawKey {
+    static constexpr int kWords = kFour ? D / 32 : D / 8;
+    uint32_t w[kWords], scale;
+    __device__ __forceinline__ void load(const WeightsParams& p, int64_t row, int t) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            uint32_t v[4];
-            e2m1_to_f16x8(c[i], v);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t x = f16x2_mul(v[k], by[i / 2]);  // exact, in bf16 too: six significant bits
-                w[4 * i + k] = kF16 ? x : pack_bf16x2(f16_lo_to_f32(x), f16_hi_to_f32(x));
-            }
-        }
-    } else {
-        const uint4* src = reinterpret_cast<const uint4*>(p.cache + (row * D + t * (D / 4)) * 2);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const uint4 u = row >= 0 ? src[i] : make_uint4(0, 0, 0, 0);
-            w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
-        }
-    }
-}
-
-// Adds up the 32 keys from key0 on of one (request, KV head), by a warp.
-template <int D, bool kF16, bool kFour>
-__device__ __forceinline__ void weights_keys(const WeightsParams& p, const WeightsRequest& req, int b, int hkv, int key0,
-                                             int g, int t) {
-    const int len = req.len, begin = req.begin, n = req.end - req.begin;
-    // Rows g, g + 8, g + 16, g + 24 of the warp's keys.
-    uint32_t kw[4][D / 8];
-    int64_t slot[4];  // of the weights; negative: none
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int key = key0 + i * 8 + g;
-        slot[i] = -1;
-        int64_t row = -1;
-        if (key < len) {
-            int in_page;
-            const int id = p.block_table[static_cast<int64_t>(b) * p.max_pages + p.page.split(key, &in_page)];
-            if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks)) {
-                row = (static_cast<int64_t>(id) * 2 * p.Hkv + hkv) * p.page.size + in_page;
-                slot[i] = (static_cast<int64_t>(id) * p.Hkv + hkv) * p.page.size + in_page;
-            } else {
-                atomicOr(p.status, ATTN_DEV_BAD_INPUT);
-            }
-        }
-        load_key<D, kF16, kFour>(p, row, t, kw[i]);
-    }
-    const float by = p.scale_log2 * (p.factors ? p.factors[hkv] : 1.0f);
-    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-
-    // Query rows: token by token, a KV head's query heads within.  Token i sees keys up to
-    // len - n + i.
-    const int rows = n * p.group;  // checked on the host: fits
-    const int first_token = max(0, key0 - (len - n));
-    for (int r0 = first_token * p.group / 8 * 8; r0 < rows; r0 += 8) {
-        const int mine = r0 + g;
-        uint32_t qb[D / 8];
-        {
-            const int token = mine / p.group, head = mine - token * p.group;
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (begin + token) * p.q_token +
-                                                              (hkv * p.group + head) * p.q_head + t * (D / 4));
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+        scale = 0;
+        if (row < 0) return;
+        if constexpr (!kFour) {
+            const uint4* src = reinterpret_cast<const uint4*>(p.cache + row * (D * 2)) + t;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                const uint4 u = mine < rows ? src[i] : make_uint4(0, 0, 0, 0);
+                const uint4 u = src[4 * i];
+                w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+            }
+        } else {
+            const uint8_t* codes = p.cache + row * (D / 2) + t * (D / 8);
+            const uint8_t* scales = p.scales + row * (D / kRowScaleSpan) + t * (D / 64);
+            if constexpr (D == 128) {
+                const uint4 u = *reinterpret_cast<const uint4*>(codes);
+                w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+                scale = *reinterpret_cast<const uint16_t*>(scales);
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2*>(codes);
+                w[0] = u.x; w[1] = u.y;
+                scale = *scales;
+            }
+        }
+    }
+    // As words of the products' type: a code times its scale is exact in fp16.
+    __device__ __forceinline__ void words(uint32_t (&out)[D / 8]) const {
+        if constexpr (!kFour) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) out[i] = w[i];
+        } else {
+            uint32_t by[2];
+            both_halves(e4m3_to_f16x2(scale), by[0], by[1]);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                uint32_t v[4];
+                e2m1_to_f16x8(w[i], v);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) out[4 * i + k] = f16x2_mul(v[k], by[i / 2]);
+            }
+        }
+    }
+};
+
+// Eight query rows of a KV head, from r0 on: token by token, the head's query heads within.
+// Token i sees keys up to len - n + i.  Over a 4-bit cache they are fp16, bf16 ones times a power
+// of two that takes a row's largest element to [512, 1024): what is exact is the decode's.
+template <int D, bool kF16, bool kFour>
+struct QueryRows {
+    uint32_t qb[D / 8];  // row g's elements, those that the lane has of a K row
+    float by[2], lse[2];  // of rows 2t and 2t + 1: what a product is multiplied by, log2(e) times the lse
+    int last[2];          // the last key they see; -1: no row
+    __device__ __forceinline__ void load(const WeightsParams& p, const WeightsRequest& req, int hkv, float scale, int r0,
+                                         int g, int t) {
+        const int n = req.end - req.begin, rows = n * p.group;  // checked on the host: fits
+        const int mine = r0 + g;
+        {
+            const int token = mine / p.group, head = mine - token * p.group;
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (req.begin + token) * p.q_token +
+                                                              (hkv * p.group + head) * p.q_head);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 u = mine < rows ? src[kFour ? t * (D / 32) + i : 4 * i + t] : make_uint4(0, 0, 0, 0);
                 qb[4 * i] = u.x; qb[4 * i + 1] = u.y; qb[4 * i + 2] = u.z; qb[4 * i + 3] = u.w;
             }
         }
-        float lse[2];
-        int last[2];  // the last key that rows r0 + 2t, r0 + 2t + 1 see; -1: no row
+        by[0] = by[1] = scale;
+        if constexpr (kFour && !kF16) {
+            float most = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                most = fmaxf(most, fmaxf(fabsf(bf16_lo_to_f32(qb[i])), fabsf(bf16_hi_to_f32(qb[i]))));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            // 2^k; 1 for zero, subnormal or non-finite rows.
+            const int e = static_cast<int>(__float_as_uint(most) >> 23);
+            const int k = (e == 0 || e == 255) ? 0 : max(-126, min(126, 9 - (e - 127)));
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+            const float back = scale * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+            by[0] = __shfl_sync(0xffffffffu, back, 8 * t);
+            by[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) qb[i] = pack_f16x2(bf16_lo_to_f32(qb[i]) * up, bf16_hi_to_f32(qb[i]) * up);
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int rr = r0 + 2 * t + i, token = rr / p.group, head = rr - token * p.group;
             lse[i] = 0.0f;
             last[i] = -1;
             if (rr < rows) {
-                lse[i] = p.lse[(hkv * p.group + head) * p.lse_head + (begin + token) * p.lse_token] * kWeightsLog2e;
-                last[i] = lse[i] == -INFINITY ? -1 : len - n + token;
+                lse[i] = p.lse[(hkv * p.group + head) * p.lse_head + (req.begin + token) * p.lse_token] * kWeightsLog2e;
+                last[i] = lse[i] == -INFINITY ? -1 : req.len - n + token;
             }
         }
-        float s[2][4] = {};
+    }
+    // Adds the weights of keys key0 + g and key0 + g + 8 (kw) to sum.
+    __device__ __forceinline__ void add(const uint32_t (&kw0)[D / 8], const uint32_t (&kw1)[D / 8], int key0, int g,
+                                        float (&sum)[2]) const {
+        float s[2][4] = {};  // two chains
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t a[4] = {kw[2 * h][2 * j], kw[2 * h + 1][2 * j], kw[2 * h][2 * j + 1], kw[2 * h + 1][2 * j + 1]};
-                mma16<kF16>(s[h], a, qb[2 * j], qb[2 * j + 1]);
-            }
+            const uint32_t a[4] = {kw0[2 * j], kw1[2 * j], kw0[2 * j + 1], kw1[2 * j + 1]};
+            mma16<kF16 || kFour>(s[j % 2], a, qb[2 * j], qb[2 * j + 1]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float w = ex2_approx(fmaf(s[i / 2][(i % 2) * 2 + k], by, -lse[k]));
+                const float w = ex2_approx(fmaf(s[0][2 * i + k] + s[1][2 * i + k], by[k], -lse[k]));
                 sum[i] += key0 + i * 8 + g <= last[k] ? w : 0.0f;
             }
     }
+};
+
+// The keys of [key0, end) of one (request, KV head), by a warp.  Of 4-bit rows the next chunk is
+// read while one is worked on, and the blocks of the one after are looked up; of 16-bit rows a warp
+// has one chunk.
+template <int D, bool kF16, bool kFour>
+__device__ __forceinline__ void weights_keys(const WeightsParams& p, const WeightsRequest& req, int b, int hkv, int key0,
+                                             int end, int g, int t) {
+    const int* table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
+    // This lane's own key of a chunk is 8 t + g: {block id, row in it}; id < 0: none.
+    auto find = [&](int from) {
+        const int key = from + t * 8 + g;
+        int2 at = make_int2(-1, 0);
+        if (key < end) {
+            at.x = table[p.page.split(key, &at.y)];
+            if (static_cast<unsigned>(at.x) >= static_cast<unsigned>(p.num_blocks)) {
+                atomicOr(p.status, ATTN_DEV_BAD_INPUT);
+                at.x = -1;
+            }
+        }
+        return at;
+    };
+    auto read = [&](int2 at, RawKey<D, kFour> (&raw)[4]) {
+        const int64_t own = at.x < 0 ? -1 : (static_cast<int64_t>(at.x) * 2 * p.Hkv + hkv) * p.page.size + at.y;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
-        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-        if (t == 0 && slot[i] >= 0) atomicAdd(p.weights + slot[i], sum[i]);  // another request may share the block
+        for (int i = 0; i < 4; ++i) raw[i].load(p, __shfl_sync(0xffffffffu, own, 4 * g + i), t);
+    };
+    const int n = req.end - req.begin, rows = n * p.group;
+    const float scale = p.scale_log2 * (p.factors ? p.factors[hkv] : 1.0f);
+    int2 at = find(key0), next = make_int2(-1, 0);
+    RawKey<D, kFour> raw[4];
+    read(at, raw);
+    if (kFour && key0 + kKeys < end) next = find(key0 + kKeys);
+    QueryRows<D, kF16, kFour> q;
+    if (rows <= 8) q.load(p, req, hkv, scale, 0, g, t);
+    while (true) {
+        RawKey<D, kFour> now[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) now[i] = raw[i];
+        const int2 here = at;
+        if constexpr (kFour) {
+            at = next;
+            if (key0 + kKeys < end) read(at, raw);
+            next = key0 + 2 * kKeys < end ? find(key0 + 2 * kKeys) : make_int2(-1, 0);
+        }
+        float sum[2][2] = {};
+        // The query rows pass by: 16-bit rows of K all at once; 4-bit ones as they are converted, sixteen
+        // at a time (all of them spilled registers).
+        constexpr int kAtOnce = kFour ? 1 : 2;
+#pragma unroll
+        for (int h0 = 0; h0 < 2; h0 += kAtOnce) {
+            uint32_t kw[2 * kAtOnce][D / 8];
+#pragma unroll
+            for (int i = 0; i < 2 * kAtOnce; ++i) now[2 * h0 + i].words(kw[i]);
+            const int first_token = max(0, key0 + 16 * h0 - (req.len - n));
+            for (int r0 = first_token * p.group / 8 * 8; r0 < rows; r0 += 8) {
+                if (rows > 8) q.load(p, req, hkv, scale, r0, g, t);
+#pragma unroll
+                for (int h = 0; h < kAtOnce; ++h) q.add(kw[2 * h], kw[2 * h + 1], key0 + (h0 + h) * 16, g, sum[h0 + h]);
+            }
+        }
+        float own = 0.0f;  // this lane's key's sum
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x = sum[i / 2][i % 2];
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            if (t == i) own = x;
+        }
+        if (here.x >= 0)  // (another request may share the block)
+            atomicAdd(p.weights + (static_cast<int64_t>(here.x) * p.Hkv + hkv) * p.page.size + here.y, own);
+        key0 += kKeys;
+        if (!kFour || key0 >= end) break;
     }
 }
 
-// Block (x, y, z): keys x * kBlockKeys .. of KV heads y, y + gridDim.y, .. of requests z, z + gridDim.z, ..
+// Block (x, y, z): the x-th run of `run` chunks of KV heads y, y + gridDim.y, .. of requests z, z + gridDim.z, ..
 template <int D, bool kF16, bool kFour>
-__global__ void __launch_bounds__(kWarps * 32)
-weights_kernel(const WeightsParams p) {
+__global__ void __launch_bounds__(32, kPerSm)
+weights_kernel(const WeightsParams p, int run) {
     grid_wait();
     grid_launch_next();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
+    const int g = threadIdx.x / 4, t = threadIdx.x % 4;
+    const int keys = run * kKeys;
     for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
         const WeightsRequest r = weights_request(p, b);
         if (!r.ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
-        const int key0 = blockIdx.x * kBlockKeys + warp * kWarpKeys;
+        const long long key0 = static_cast<long long>(blockIdx.x) * keys;
         if (!r.ok || r.end == r.begin || key0 >= r.len) continue;
+        const int first = static_cast<int>(key0), end = first + min(r.len - first, keys);
         for (int hkv = blockIdx.y; hkv < p.Hkv; hkv += gridDim.y)
-            weights_keys<D, kF16, kFour>(p, r, b, hkv, key0, g, t);
+            weights_keys<D, kF16, kFour>(p, r, b, hkv, first, end, g, t);
     }
 }
 
 template <int D, bool kFour>
-cudaError_t launch_type(const WeightsParams& p, dim3 grid, bool f16, cudaStream_t st) {
-    return f16 ? launch_serial(weights_kernel<D, true, kFour>, grid, kWarps * 32, 0, st, p)
-               : launch_serial(weights_kernel<D, false, kFour>, grid, kWarps * 32, 0, st, p);
+cudaError_t launch_type(const WeightsParams& p, const LaunchEnv& env, bool f16, int* grid_out) {
+    const long long chunks = (static_cast<long long>(p.max_pages) * p.page.size + kKeys - 1) / kKeys;
+    // Of 4-bit rows even runs, long enough to read ahead in where that leaves three blocks for every two
+    // places.
+    long long run = 1;
+    if (kFour) {
+        const double per = static_cast<double>(chunks) * p.B * p.Hkv / (1.5 * kPerSm * env.num_sms);
+        run = per >= kMostRun ? kMostRun : per < 1 ? 1 : static_cast<long long>(per);
+        const long long runs = (chunks + run - 1) / run;
+        run = (chunks + runs - 1) / runs;
+    }
+    const dim3 grid(static_cast<unsigned>((chunks + run - 1) / run), std::min(p.Hkv, 65535), std::min(p.B, 65535));
+    *grid_out = static_cast<int>(grid.x);
+    return f16 ? launch_serial(weights_kernel<D, true, kFour>, grid, 32, 0, env.stream, p, static_cast<int>(run))
+               : launch_serial(weights_kernel<D, false, kFour>, grid, 32, 0, env.stream, p, static_cast<int>(run));
 }
 
 }  // namespace
 
 cudaError_t launch_weights_paged(const WeightsShape& s, const LaunchEnv& env, int* grid_out, int* kernels_launched) {
     const WeightsParams p = weights_params(s, env);
-    const long long keys = static_cast<long long>(s.max_pages) * s.page;
-    const dim3 grid(static_cast<unsigned>((keys + kBlockKeys - 1) / kBlockKeys), std::min(s.Hkv, 65535), std::min(s.B, 65535));
-    *grid_out = static_cast<int>(grid.x);
     *kernels_launched = 1;
     if (s.scales)
-        return s.D == 64 ? launch_type<64, true>(p, grid, s.f16, env.stream)
-                         : launch_type<128, true>(p, grid, s.f16, env.stream);
-    return s.D == 64 ? launch_type<64, false>(p, grid, s.f16, env.stream)
-                     : launch_type<128, false>(p, grid, s.f16, env.stream);
+        return s.D == 64 ? launch_type<64, true>(p, env, s.f16, grid_out) : launch_type<128, true>(p, env, s.f16, grid_out);
+    return s.D == 64 ? launch_type<64, false>(p, env, s.f16, grid_out) : launch_type<128, false>(p, env, s.f16, grid_out);
 }
 
 }  // namespace attn

@@ -48,7 +48,7 @@ using prefill::warp_wait;
 constexpr int kKeyShift = 8, kKeys = 1 << kKeyShift;  // of an item
 constexpr int kHalf = 128;  // keys of an MMA
 constexpr int kCols = 128;  // query rows of a tile
-constexpr int kQStages = 3, kKStages = 2, kSBufs = 2, kItems = 4;
+constexpr int kQStages = 3, kKStages = 2, kSBufs = 2, kItems = 5;
 constexpr int kSumWarps = 16, kRowWarps = 4;
 constexpr int kQWarp = kSumWarps, kMmaWarp = kQWarp + 1, kLseWarp = kMmaWarp + 1, kItemWarp = kLseWarp + 1;
 constexpr int kLoadWarp0 = kItemWarp + 1;
@@ -66,12 +66,14 @@ enum : unsigned {
     SITE_W_I_FULL
 };
 
-struct alignas(16) Item {  // b < 0: the end
+struct Item {  // b < 0: the end
     int b, hkv, begin, n;
     int len, key0;  // keys of the request; the item's first
     int t0, t1;     // tokens of the item, counted from the request's first query
     int slot;       // of the partial sums; -1: none
-    int pad[3];
+};
+struct alignas(16) ItemPlace {  // all but the slot
+    int4 request, keys;
 };
 
 struct Control {
@@ -86,7 +88,8 @@ struct Control {
     int abort;
     alignas(16) float nlse[kQStages][kCols];  // -log2(e) lse of a tile's rows
     float handed[kKeys];
-    Item items[kItems];
+    ItemPlace items[kItems];
+    int item_slots[kItems];
 };
 
 template <int D>
@@ -226,9 +229,8 @@ struct Items {
         bool ok = warp_wait(&ctl->i_full[s], (i_it / kItems) & 1, g, SITE_W_I_FULL);
         if (kVote) ok = __all_sync(0xffffffffu, ok);
         if (!ok) return false;
-        const int4* at = reinterpret_cast<const int4*>(&ctl->items[s]);
-        const int4 x = at[0], y = at[1];
-        it.slot = ctl->items[s].slot;
+        const int4 x = ctl->items[s].request, y = ctl->items[s].keys;
+        it.slot = ctl->item_slots[s];
         it.b = x.x; it.hkv = x.y; it.begin = x.z; it.n = x.w;
         it.len = y.x; it.key0 = y.y; it.t0 = y.z; it.t1 = y.w;
         __syncwarp();
@@ -250,7 +252,9 @@ __device__ void find_items(const TilesParams& p, Control* ctl, int lane, const W
             !__all_sync(0xffffffffu, mbar_wait(&ctl->i_empty[s], ((i_it / kItems) & 1) ^ 1, g, SITE_W_I_EMPTY)))
             return;
         if (lane == 0) {
-            ctl->items[s] = it;
+            ctl->items[s].request = make_int4(it.b, it.hkv, it.begin, it.n);
+            ctl->items[s].keys = make_int4(it.len, it.key0, it.t0, it.t1);
+            ctl->item_slots[s] = it.slot;
             mbar_arrive(&ctl->i_full[s]);
         }
         __syncwarp();
@@ -386,58 +390,89 @@ __device__ void load_rows16(const TilesParams& p, uint8_t* smem, Control* ctl, i
     if (waiting) hand_over(k_it - 1);
 }
 
+// The next 32 keys' codes are read as a warp's are converted, and the places of those after are
+// looked up.
 template <int D, bool kF16>
 __device__ void load_rows4(const TilesParams& p, uint8_t* smem, Control* ctl, int warp, int lane, const WaitGuard& g) {
     constexpr int kPer = D / 32;         // lanes of a row: 32 elements each
     constexpr int kRowsPer = 32 / kPer;
-    constexpr int kSteps = 64 / kRowsPer;
+    constexpr int kSteps = 32 / kRowsPer, kTurns = kKeys / (32 * kRowWarps);  // of 32 keys a warp, for an item
     uint8_t* buffers = smem + Layout<D>::kK;
     const int part = lane % kPer;
+    // Rows of 128 elements: the second half's chunks go out in another order, so that eight
+    // lanes' meet no bank twice (key_chunk puts both halves' on the same ones).
+    const int swap = part & 2;
     Items items(ctl, lane, g);
-    Item it;
-    uint32_t k_it = 0;
-    while (items.take(it)) {
-        RowIds ids;
-        ids.find(p.w, it, it.key0 + warp * 64, lane);
-        uint4 codes[kSteps];
-        uint32_t scales[kSteps];
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int64_t row = ids.of(i * kRowsPer + lane / kPer);
-            codes[i] = make_uint4(0, 0, 0, 0);
-            scales[i] = 0;
-            if (row >= 0) {
-                codes[i] = *reinterpret_cast<const uint4*>(p.w.cache + row * (D / 2) + part * 16);
-                scales[i] = *reinterpret_cast<const uint16_t*>(p.w.scales + row * (D / kRowScaleSpan) + part * 2);
-            }
+    Item it{};
+    int turn = 0;  // that is looked up
+    auto first = [&](int n) { return (n * kRowWarps + warp) * 32; };
+    auto advance = [&]() {
+        if (++turn < kTurns) return true;
+        turn = 0;
+        return items.take(it);
+    };
+    auto find = [&]() -> int64_t {  // row of this lane's key in the pool of rows; negative: none
+        const int key = it.key0 + first(turn) + lane;
+        if (key >= it.len) return -1;
+        int in_page;
+        const int id = p.w.block_table[static_cast<int64_t>(it.b) * p.w.max_pages + p.w.page.split(key, &in_page)];
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(p.w.num_blocks))
+            return (static_cast<int64_t>(id) * 2 * p.w.Hkv + it.hkv) * p.w.page.size + in_page;
+        atomicOr(p.w.status, ATTN_DEV_BAD_INPUT);
+        return -1;
+    };
+    uint4 codes[kSteps];
+    uint32_t scales[kSteps];
+    auto read = [&](int i, int64_t rows) {
+        const int64_t row = __shfl_sync(0xffffffffu, rows, i * kRowsPer + lane / kPer);
+        codes[i] = make_uint4(0, 0, 0, 0);
+        scales[i] = 0;
+        if (row >= 0) {
+            codes[i] = *reinterpret_cast<const uint4*>(p.w.cache + row * (D / 2) + part * 16);
+            scales[i] = *reinterpret_cast<const uint16_t*>(p.w.scales + row * (D / kRowScaleSpan) + part * 2);
         }
-        const uint32_t s = k_it % kKStages;
-        if (k_it >= kKStages &&
+    };
+    bool more = items.take(it);
+    int64_t rows = more ? find() : -1;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) read(i, rows);
+    bool next = more && advance();
+    rows = next ? find() : -1;
+    for (uint32_t n = 0; more; ++n) {
+        const uint32_t k_it = n / kTurns, s = k_it % kKStages;
+        if (n % kTurns == 0 && k_it >= kKStages &&
             !__all_sync(0xffffffffu, mbar_wait(&ctl->k_empty[s], ((k_it / kKStages) & 1) ^ 1, g, SITE_W_K_EMPTY)))
             return;
         uint8_t* to = buffers + s * 2 * Layout<D>::kTile;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const int k = warp * 64 + i * kRowsPer + lane / kPer;
-            const uint32_t f = e4m3_to_f16x2(scales[i]);
-            const uint32_t by[2] = {__byte_perm(f, f, 0x1010), __byte_perm(f, f, 0x3232)};
-            const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+            const int k = first(n % kTurns) + i * kRowsPer + lane / kPer;
+            uint32_t by[2];
+            e2m1_scales<kF16>(scales[i], by);
+            uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+            if (swap) {
+                const uint32_t w0 = w[0], w1 = w[1], by0 = by[0];
+                w[0] = w[2]; w[1] = w[3]; by[0] = by[1];
+                w[2] = w0; w[3] = w1; by[1] = by0;
+            }
+            read(i, rows);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t v[4];
                 e2m1_to_f16x8(w[j], v);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    v[x] = f16x2_mul(v[x], by[j / 2]);
-                    if (!kF16) v[x] = pack_bf16x2(f16_lo_to_f32(v[x]), f16_hi_to_f32(v[x]));
-                }
-                *reinterpret_cast<uint4*>(to + key_chunk<D>(k, part * 4 + j)) = make_uint4(v[0], v[1], v[2], v[3]);
+                for (int x = 0; x < 4; ++x) v[x] = e2m1_times<kF16>(v[x], by[j / 2]);
+                *reinterpret_cast<uint4*>(to + key_chunk<D>(k, part * 4 + (j ^ swap))) = make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->k_full[s]);
-        ++k_it;
+        if (n % kTurns == kTurns - 1) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->k_full[s]);
+        }
+        more = next;
+        next = more && advance();
+        rows = next ? find() : -1;
     }
 }
 
@@ -634,6 +669,12 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
             }
             continue;
         }
+        // An item of one tile (of a decode step, all are) is one set's alone.
+        const bool single = it.t1 - it.t0 <= p.tile_tokens;
+        if (single && static_cast<int>(l_it & 1) != set) {
+            ++l_it;
+            continue;
+        }
         int in_page;  // (the id is looked at once the sums are there)
         const int page = w.page.split(min(key, it.len - 1), &in_page);
         const int id = w.block_table[static_cast<int64_t>(it.b) * w.max_pages + page];
@@ -690,7 +731,8 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
         }
         // The odd tiles' sums to the warps of the even ones.
         const int place = half * kHalf + quarter * 32 + lane;
-        if (set == 1) {
+        if (single) {
+        } else if (set == 1) {
             if (handed > 0 && !wait(&ctl->x_empty[half], (handed - 1) & 1, SITE_W_X_EMPTY)) return;
             ctl->handed[place] = sum;
             __syncwarp();
@@ -701,8 +743,8 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->x_empty[half]);
         }
-        ++handed;
-        if (set == 0 && key < it.len) {
+        handed += !single;
+        if ((set == 0 || single) && key < it.len) {
             if (it.slot >= 0)
                 p.partial[(static_cast<int64_t>(it.slot) * w.Hkv + it.hkv) * p.keys + key] = sum;
             else if (static_cast<unsigned>(id) < static_cast<unsigned>(w.num_blocks))  // the request's only addition to this key
@@ -875,7 +917,10 @@ cudaError_t launch_loads(const WeightsMaps& maps, const TilesParams& p, bool f16
 
 int weights_tile_tokens(const WeightsShape& s) {
     const int group = s.Hq / s.Hkv;
-    if (group > kCols) return 0;
+    // Up to eight query rows to a KV head, as far as the host can tell, are the other kernel's: with a
+    // step's one token over 64 x 4096 keys this one took 98 us (16 bits) and 152 (4 bits), that one 88
+    // and 47; with 16 rows over 32 x 4096, 53 and 77 here, 63 and 77 there.
+    if (group > kCols || static_cast<long long>(s.total) * group <= 8ll * s.B) return 0;
     return s.total <= s.B ? 1 : kCols / group;
 }
 
