@@ -7,7 +7,9 @@
 // to settle and no older rows to follow, so the work is the 16-bit append's (append.cu):
 // a warp takes one token and a run of its heads.  A lane holds two chunks of eight
 // elements of a row, and a group's two chunks meet by shuffles; each of its two lanes settles one of the
-// two groups they share.
+// two groups they share.  Bound by its instructions: 17100 tokens of 8 KV heads (D 128) take 25 to
+// 28 us, 57% of the issue slots at 18 warps an SM (floor by bytes 13); a step of 64 tokens takes
+// 3.1, a chain of reads.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -6,14 +6,20 @@
 // their order.  Two kernels.  evict_select_kernel, a CTA for each (request, KV head): the
 // weights as integers in their order in shared memory, the smallest kept one found digit by
 // digit from histograms (radix selection: 11, 11 and 10 bits; once few share the first digit,
-// among those alone), then the kept slots and their weights written in order.  evict_move_kernel: the rows.  A kept row never moves up,
-// so in place is safe if a row is read before its slot is written: slots are taken in order,
-// a chunk is read whole before any of it is written, and the next chunk is read before that
-// too (its rows lie above every slot of this one).  Columns of a row have nothing to do with
+// among those alone), then the kept slots and their weights written in order.
+// evict_move_kernel: the rows.  A kept row never moves up, so in place is safe if a row is
+// read before its slot is written: slots are taken in order, a chunk is read whole before any
+// of it is written, and the next chunk is read before that too (its rows lie above every slot
+// of this one).  Columns of a row have nothing to do with
 // one another: where (request, KV head) pairs are few their columns go to CTAs of their own.
 // Where that leaves SMs idle, a cluster of CTAs takes a run of slots, or of rows, each: the
 // histograms meet in the first one's shared memory, and a chunk is read by all before any of
 // it is written.
+//
+// Measured: 64 requests of 4096 16-bit keys, 8 KV heads, to 2048: selection 31 us (bound by its
+// instructions), move 163 (HBM, 6.2 TB/s).  32 of 8192 4-bit keys to 4096: 31 and 68; the scales'
+// rows of 8 bytes leave most of their sectors unused.  One pair of 32000 keys: 51, one CTA
+// for each part 205.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -40,7 +46,7 @@ struct EvictParams {
 };
 
 constexpr int kMaxRanks = 8;  // CTAs of a cluster
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 512;  // (256 with five CTAs an SM: 122 us instead of 114 for 32 x 8192 4-bit keys)
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 // Weights in shared memory; of longer requests those behind are read again.  (As many as leave room for two
@@ -486,12 +492,14 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
     }
 }
 
-// Column ranges of 32 bytes and more, a power of two of them, until there are two CTAs for an SM.
+// Column ranges of 32 bytes and more, a power of two of them, until there are two CTAs for an SM (64
+// pairs of 16000 16-bit keys: 165 us instead of 262 with whole rows, one pair of 32000 46 instead of 97).
 template <int kRowBytes, int kScaleBytes, int kRanges = 1>
 cudaError_t launch_move(const EvictParams& p, const LaunchEnv& env, int* grid_out) {
     const long long units = static_cast<long long>(p.B) * p.Hkv;
     if constexpr (kRanges * 32 < kRowBytes)
-        if (2 * kRanges * units < 2ll * env.num_sms) return launch_move<kRowBytes, kScaleBytes, 2 * kRanges>(p, env, grid_out);
+        if (2 * kRanges * units < 2ll * env.num_sms)
+            return launch_move<kRowBytes, kScaleBytes, 2 * kRanges>(p, env, grid_out);
     const int parts = 2 * kRanges + (kScaleBytes ? 2 : 0);
     int ranks = 1;
     if constexpr (kRanges * 32 >= kRowBytes)  // until the SMs have two CTAs each, or a rank 512 rows
@@ -535,6 +543,8 @@ cudaError_t launch_evict_paged(const EvictShape& s, const LaunchEnv& env, int* g
         attr_set[env.device] = true;
     }
     const long long units = static_cast<long long>(s.B) * s.Hkv, keys = static_cast<long long>(s.max_pages) * s.page;
+    // With one CTA for each pair 8 pairs of 8000 4-bit keys took 41 us, with clusters 31; 16-bit ones
+    // 43 both; at up to 4096 keys clusters lose 2 us, and so they do where SMs have work already.
     int ranks = 1;  // of tables wider than 4096: until the SMs have a CTA each, or a rank 2048 slots
     while (keys > 4096 && ranks < kMaxRanks && 2 * ranks * units <= env.num_sms && keys > 2048 * ranks) ranks *= 2;
     const long long per = ((keys + ranks - 1) / ranks + 127) / 128 * 128;

@@ -9,8 +9,10 @@
 // tensor cores (mma.sync m16n8k16, fp32 sums) with 16 keys as rows: a key's sum then stays in
 // the four lanes that hold its row.  A warp keeps 32 rows of K in registers and passes all
 // query rows that see them by; each key belongs to one warp, so nothing is added twice or in
-// a changing order.  The order of a product's inner index is free, so each lane reads runs of
-// D/4 contiguous elements of its rows.
+// a changing order.  The order of a product's inner index is free, so each lane reads what suits
+// the reads.  For decode steps: up to eight query rows are one column block, held in registers
+// while the keys stream by.  HBM bound in 16 bits (64 requests of 4096 keys, 8 KV heads, D 128:
+// 88 us, 554 MB at 6.3 TB/s); in 4 bits by the conversions' instructions (47 us, 168 MB).
 #include <cuda_runtime.h>
 
 #include <algorithm>
