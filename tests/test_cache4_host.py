@@ -123,7 +123,8 @@ def _evict(a, four, **kw):
     (dict(B=0), 1, ">= 1"), (dict(D=96), 2, "D=96"), (dict(keep=0), 1, "keep"), (dict(recent=6), 1, "recent"),
     (dict(recent=-1), 1, "recent"), (dict(keep=2 ** 31 - 1), 1, "keep"), (dict(new=None), 1, "new_lens"),
     (dict(pages=(2 ** 31 - 2048) // 16), 1, "max_pages_per_seq"),
-    (dict(new=FAKE), 1, "seq_lens"), (dict(new=FAKE + 4), 1, "seq_lens"), (dict(kept=FAKE + 2), 1, "4-byte"),
+    (dict(new=FAKE), 1, "seq_lens"), (dict(new=FAKE + 4), 1, "seq_lens"), (dict(kept=FAKE), 1, "share memory"),
+    (dict(kept=FAKE + 4096 - 76), 1, "share memory"), (dict(table=FAKE + 4096, lens=FAKE + 8), 1, "share memory"), (dict(kept=FAKE + 2), 1, "4-byte"),
     (dict(weights=None), 1, "non-null"), (dict(kv=FAKE + 8), 1, "16-byte"), (dict(table=None), 1, "non-null"),
     (dict(pages=1 << 28), 1, "max_pages_per_seq*page_size"), (dict(B=1 << 20, Hkv=1 << 12), 1, "31 bits"),
 ])

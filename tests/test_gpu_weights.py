@@ -296,6 +296,20 @@ def test_two_streams_at_once_with_ranges(four):
 
 
 @fours
+def test_a_step_of_many_requests_some_long(four):
+    """More runs of keys to a request than blocks for it; and a table far wider than any request."""
+    a = attn()
+    lens = [(13 * i) % 40 for i in range(400)]
+    lens[7], lens[399] = 2500, 2049
+    pr = Problem(lens, [min(1, n) for n in lens], Hq=8, Hkv=8, D=64, page=64, four=four, seed=184)
+    w = pr.run(a)
+    check_status(a)
+    pr.check(w)
+    assert torch.equal(pr.run(a, table=torch.nn.functional.pad(pr.table, (0, 3000), value=-3)), w)
+    check_status(a)
+
+
+@fours
 def test_many_requests(four):
     """5000 requests of which few have queries, found 32 at a time."""
     a = attn()

@@ -1334,8 +1334,11 @@ attn_status run_evict(bool four, void* kv_cache, void* scales, float* weights, c
         return fail(ATTN_ERR_INVALID_ARG, "new_lens must be non-null, and new_lens and kept 4-byte aligned");
     if (4.0 * B * Hkv * keep > kMaxWorkspace) return fail(ATTN_ERR_INVALID_ARG, "B*Hkv*keep must be below 2^42");
     const size_t kept_bytes = 4ull * B * Hkv * keep;
-    if (meet(new_lens, 4ull * B, seq_lens, 4ull * B))
-        return fail(ATTN_ERR_INVALID_ARG, "new_lens may not share memory with seq_lens");
+    const size_t lens_bytes = 4ull * B, table_bytes = 4ull * B * max_pages_per_seq;
+    if (meet(new_lens, lens_bytes, seq_lens, lens_bytes) || meet(new_lens, lens_bytes, block_table, table_bytes) ||
+        meet(kept, kept_bytes, seq_lens, lens_bytes) || meet(kept, kept_bytes, block_table, table_bytes) ||
+        meet(kept, kept_bytes, new_lens, lens_bytes))
+        return fail(ATTN_ERR_INVALID_ARG, "new_lens and kept may not share memory with seq_lens, block_table or one another");
     LaunchEnv env;
     if ((st = device_env(stream, &env)) != ATTN_OK) return st;
     void* ws = nullptr;

@@ -240,7 +240,8 @@ __device__ __forceinline__ void weights_keys(const WeightsParams& p, const Weigh
     }
 }
 
-// Block (x, y, z): the x-th run of `run` chunks of KV heads y, y + gridDim.y, .. of requests z, z + gridDim.z, ..
+// Block (x, y, z): runs x, x + gridDim.x, .. of `run` chunks of KV heads y, y + gridDim.y, .. of requests z,
+// z + gridDim.z, ..
 template <int D, bool kF16, bool kFour>
 __global__ void __launch_bounds__(32, kPerSm)
 weights_kernel(const WeightsParams p, int run) {
@@ -251,11 +252,13 @@ weights_kernel(const WeightsParams p, int run) {
     for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
         const WeightsRequest r = weights_request(p, b);
         if (!r.ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
-        const long long key0 = static_cast<long long>(blockIdx.x) * keys;
-        if (!r.ok || r.end == r.begin || key0 >= r.len) continue;
-        const int first = static_cast<int>(key0), end = first + min(r.len - first, keys);
-        for (int hkv = blockIdx.y; hkv < p.Hkv; hkv += gridDim.y)
-            weights_keys<D, kF16, kFour>(p, r, b, hkv, first, end, g, t);
+        if (!r.ok || r.end == r.begin) continue;
+        for (long long key0 = static_cast<long long>(blockIdx.x) * keys; key0 < r.len;
+             key0 += static_cast<long long>(gridDim.x) * keys) {
+            const int first = static_cast<int>(key0), end = first + min(r.len - first, keys);
+            for (int hkv = blockIdx.y; hkv < p.Hkv; hkv += gridDim.y)
+                weights_keys<D, kF16, kFour>(p, r, b, hkv, first, end, g, t);
+        }
     }
 }
 
@@ -271,7 +274,12 @@ cudaError_t launch_type(const WeightsParams& p, const LaunchEnv& env, bool f16, 
         const long long runs = (chunks + run - 1) / run;
         run = (chunks + runs - 1) / runs;
     }
-    const dim3 grid(static_cast<unsigned>((chunks + run - 1) / run), std::min(p.Hkv, 65535), std::min(p.B, 65535));
+    // Not many more blocks than it takes, however wide the table is: one that has nothing to do costs too.
+    const unsigned y = std::min(p.Hkv, 65535), z = std::min(p.B, 65535);
+    // (64 requests of 4096 4-bit keys in tables eight times as wide: 78 us with 32 blocks to a place, 47 with
+    // tables as wide as the requests.)
+    const long long most = std::max(1ll, (kFour ? 6ll : 32ll) * kPerSm * env.num_sms / (static_cast<long long>(y) * z));
+    const dim3 grid(static_cast<unsigned>(std::min((chunks + run - 1) / run, most)), y, z);
     *grid_out = static_cast<int>(grid.x);
     return f16 ? launch_serial(weights_kernel<D, true, kFour>, grid, 32, 0, env.stream, p, static_cast<int>(run))
                : launch_serial(weights_kernel<D, false, kFour>, grid, 32, 0, env.stream, p, static_cast<int>(run));

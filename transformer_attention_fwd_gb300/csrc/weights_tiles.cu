@@ -22,7 +22,7 @@
 //   20 on  K rows into one of two buffers.  16-bit pages of 8 .. 256 rows (a power of two)
 //          by TMA, other 16-bit rows by asynchronous 16-byte copies, 4-bit rows converted in
 //          registers (a code times its scale has six significant bits: exact in either
-//          16-bit type)
+//          16-bit type), by four warps or eight
 // Every wait is bounded (sm100.cuh).
 //
 // What bounds it: a 128 x 128 x 16 product takes 67 cycles and reads 8 KB, all that shared memory
@@ -60,9 +60,9 @@ constexpr int kSumWarps = 16, kRowWarps = 4;
 constexpr int kQWarp = kSumWarps, kMmaWarp = kQWarp + 1, kLseWarp = kMmaWarp + 1, kItemWarp = kLseWarp + 1;
 constexpr int kLoadWarp0 = kItemWarp + 1;
 // How an item's keys arrive, and the warps for it.
-enum KeyLoads { kPages, kRows16, kRows4 };
+enum KeyLoads { kPages, kRows16, kRows4, kRows4More };
 template <int kLoads>
-constexpr int kLoadWarps = kLoads == kPages ? 1 : kRowWarps;
+constexpr int kLoadWarps = kLoads == kPages ? 1 : kLoads == kRows4More ? 2 * kRowWarps : kRowWarps;
 template <int kLoads>
 constexpr int kThreads = (kLoadWarp0 + kLoadWarps<kLoads>) * 32;
 constexpr uint32_t kTmemCols = 512;
@@ -399,11 +399,11 @@ __device__ void load_rows16(const TilesParams& p, uint8_t* smem, Control* ctl, i
 
 // The next 32 keys' codes are read as a warp's are converted, and the places of those after are
 // looked up.
-template <int D, bool kF16>
+template <int D, bool kF16, int kWarps>
 __device__ void load_rows4(const TilesParams& p, uint8_t* smem, Control* ctl, int warp, int lane, const WaitGuard& g) {
     constexpr int kPer = D / 32;         // lanes of a row: 32 elements each
     constexpr int kRowsPer = 32 / kPer;
-    constexpr int kSteps = 32 / kRowsPer, kTurns = kKeys / (32 * kRowWarps);  // of 32 keys a warp, for an item
+    constexpr int kSteps = 32 / kRowsPer, kTurns = kKeys / (32 * kWarps);  // of 32 keys a warp, for an item
     uint8_t* buffers = smem + Layout<D>::kK;
     const int part = lane % kPer;
     // Rows of 128 elements: the second half's chunks go out in another order, so that eight
@@ -412,7 +412,7 @@ __device__ void load_rows4(const TilesParams& p, uint8_t* smem, Control* ctl, in
     Items items(ctl, lane, g);
     Item it{};
     int turn = 0;  // that is looked up
-    auto first = [&](int n) { return (n * kRowWarps + warp) * 32; };
+    auto first = [&](int n) { return (n * kWarps + warp) * 32; };
     auto advance = [&]() {
         if (++turn < kTurns) return true;
         turn = 0;
@@ -826,7 +826,8 @@ weights_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     } else if (warp == kItemWarp) {
         find_items(p, ctl, lane, g);
     } else {
-        if constexpr (kLoads == kRows4) load_rows4<D, kF16>(p, smem, ctl, warp - kLoadWarp0, lane, g);
+        if constexpr (kLoads == kRows4 || kLoads == kRows4More)
+            load_rows4<D, kF16, kLoadWarps<kLoads>>(p, smem, ctl, warp - kLoadWarp0, lane, g);
         else if constexpr (kLoads == kRows16) load_rows16<D>(p, smem, ctl, warp - kLoadWarp0, lane, g);
         else load_pages<D>(p, &tmK, smem, ctl, lane, g);
     }
@@ -917,6 +918,7 @@ cudaError_t launch_types(const WeightsMaps& maps, const TilesParams& p, bool f16
 template <int D>
 cudaError_t launch_loads(const WeightsMaps& maps, const TilesParams& p, bool f16, int loads, int grid, const LaunchEnv& env) {
     if (loads == kRows4) return launch_types<D, kRows4>(maps, p, f16, grid, env);
+    if (loads == kRows4More) return launch_types<D, kRows4More>(maps, p, f16, grid, env);
     if (loads == kRows16) return launch_types<D, kRows16>(maps, p, f16, grid, env);
     return launch_types<D, kPages>(maps, p, f16, grid, env);
 }
@@ -953,7 +955,12 @@ cudaError_t launch_weights_tiles(const WeightsShape& s, const WeightsMaps& maps,
     const int grid = env.num_sms;
     *grid_out = grid;
     *kernels_launched = ws ? 2 : 1;
-    const int loads = s.scales ? kRows4 : weights_page_rows(s) > 0 ? kPages : kRows16;
+    // Four warps convert 4-bit rows under the products of many query tiles; where an item has few,
+    // eight: 16 rows over 32 x 4096 keys (D 128) 108 us with four, 77 with eight, 512 rows over 16 x 4096
+    // 91 and 88, a 4096-token prompt 76 and 79 (eight leave the sums too few registers); D 64, 160
+    // rows over 32 x 4096, 82 and 89.
+    const bool few = static_cast<long long>(s.total) * p.w.group <= (s.D == 128 ? 4ll : 1ll) * kCols * s.B;
+    const int loads = s.scales ? (few ? kRows4More : kRows4) : weights_page_rows(s) > 0 ? kPages : kRows16;
     cudaError_t e = s.D == 64 ? launch_loads<64>(maps, p, s.f16 != 0, loads, grid, env)
                               : launch_loads<128>(maps, p, s.f16 != 0, loads, grid, env);
     if (e != cudaSuccess || !ws) return e;
