@@ -145,6 +145,24 @@ def test_few_long_ones_of_all_kinds(kind, four):
 
 
 @fours
+@pytest.mark.parametrize("lens,keep,recent", [([300, 77, 129], 65, 3), ([5000], 2001, 100)])
+def test_weights_at_any_place(lens, keep, recent, four):
+    """Weights that four floats at a time could not be read from."""
+    a = attn()
+    pr = Problem(lens, Hkv=1, D=64, four=four, seed=185)
+    pools, t, n = [p.cuda() for p in pr.pools], pr.table.cuda(), pr.lens.cuda()
+    w = torch.empty(pr.weights.numel() + 1, device="cuda")[1:].view(pr.weights.shape)
+    w.copy_(pr.weights)
+    call = a.attn_evict_paged_e2m1 if four else a.attn_evict_paged
+    new, kept = call(*pools, w, t, n, keep, recent)
+    check_status(a)
+    want = pr.run(a, keep, recent)
+    assert torch.equal(w.view(torch.int32), want[1].view(torch.int32))
+    assert torch.equal(new, want[2]) and torch.equal(kept, want[3])
+    assert all(torch.equal(_bits(x), _bits(y)) for x, y in zip(pools, want[0]))
+
+
+@fours
 def test_bad_blocks_of_a_long_one(four):
     a = attn()
     pr = Problem([9000], Hkv=1, four=four, seed=181)
