@@ -184,6 +184,38 @@ def test_bad_blocks_of_a_long_one(four):
 
 
 @fours
+def test_two_graphs_at_once_of_long_ones(four):
+    """Captured on two streams without a list of what is kept (a workspace each), replayed side by side."""
+    a = attn()
+    runs = []
+    for seed, lens, Hkv in ((186, [9000], 2), (187, [6000, 30, 4500], 1)):
+        pr = Problem(lens, Hkv=Hkv, D=64, four=four, seed=seed)
+        want = pr.run(a, 2500, 70)
+        pools, w, t, n = [p.cuda() for p in pr.pools], pr.weights.cuda(), pr.table.cuda(), pr.lens.cuda()
+        start = [p.clone() for p in pools], w.clone()
+        new = torch.empty(len(lens), dtype=torch.int32, device="cuda")
+        call = a.attn_evict_paged_e2m1 if four else a.attn_evict_paged
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            for p, s in zip(pools, start[0]):
+                p.copy_(s)
+            w.copy_(start[1])
+            call(*pools, w, t, n, 2500, 70, new_lens=new, want_kept=False)
+        runs.append((graph, side, pools, w, new, want, start, t, n))
+    for _ in range(5):
+        for graph, side, *_ in runs:
+            with torch.cuda.stream(side):
+                graph.replay()
+    torch.cuda.synchronize()
+    check_status(a)
+    for _, _, pools, w, new, want, *_ in runs:
+        assert torch.equal(new, want[2]) and torch.equal(w.view(torch.int32), want[1].view(torch.int32))
+        assert all(torch.equal(_bits(x), _bits(y)) for x, y in zip(pools, want[0]))
+
+
+@fours
 def test_evicted_again_and_again(four):
     """Each eviction's result is the next one's input; pages past the kept keys are free."""
     a = attn()
