@@ -7,8 +7,8 @@
 // to settle and no older rows to follow, so the work is the 16-bit append's (append.cu):
 // a warp takes one token and a run of its heads.  A lane holds two chunks of eight
 // elements of a row, and a group's two chunks meet by shuffles; each of its two lanes settles one of the
-// two groups they share.  Bound by its instructions: 17100 tokens of 8 KV heads (D 128) take 25 to
-// 28 us, 57% of the issue slots at 18 warps an SM (floor by bytes 13); a step of 64 tokens takes
+// two groups they share.  Bound by its instructions: 17100 tokens of 8 KV heads (D 128) take 24 to
+// 27 us, some 60% of the issue slots (floor by bytes 13); a step of 64 tokens takes
 // 3.1, a chain of reads.
 #include <cuda_runtime.h>
 
@@ -121,7 +121,8 @@ struct E2m1Rows {
     __device__ __forceinline__ void store(const AppendParams& p, int head, bool in, typename R::Pairs v, uint32_t m0,
                                           uint32_t m1) const {
         const float factor = p.factors && in ? p.factors[head] : 1.0f;
-        const float over = 1.0f / (kE2m1Max * factor);
+        float over;  // off by up to 2^-23
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(over) : "f"(kE2m1Max * factor));
         uint32_t code[2];
         float by[2];
         if (next) {  // both groups are shared with the next lane: a lane settles one of them
@@ -164,8 +165,10 @@ struct E2m1Rows {
     }
 };
 
+// Blocks to an SM by registers: six (17100 tokens of 8 KV heads as they are 23.6 us, with five 24.0; adjacent
+// pairs 28.2 and 28.7), but for halves, which spill at six (30.7 and 30.1).
 template <typename E, int D, int kLayout>
-__global__ void __launch_bounds__(kAppendWarps * 32, 5)
+__global__ void __launch_bounds__(kAppendWarps * 32, kLayout == kRopeHalves ? 5 : 6)
 append_e2m1_kernel(const AppendParams p) {
     using R = Rope<E, D, kLayout>;
     __shared__ __align__(16) float s_table[kAppendWarps][D];
