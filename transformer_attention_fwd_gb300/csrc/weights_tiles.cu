@@ -54,7 +54,7 @@ constexpr int kKeyShift = 8, kKeys = 1 << kKeyShift;  // of an item
 constexpr int kHalf = 128;  // keys of an MMA
 constexpr int kCols = 128;  // query rows of a tile
 // Items: the lse warp is four tiles ahead, so four items where they have one tile each (with four
-// places and one-tile items through both sets of sum warps, a step took 158 us instead of 152).
+// places windows of 64 tokens over 16 x 4096 4-bit keys took 61.7 us instead of 60.3).
 constexpr int kQStages = 3, kKStages = 2, kSBufs = 2, kItems = 5;
 constexpr int kSumWarps = 16, kRowWarps = 4;
 constexpr int kQWarp = kSumWarps, kMmaWarp = kQWarp + 1, kLseWarp = kMmaWarp + 1, kItemWarp = kLseWarp + 1;
