@@ -544,8 +544,11 @@ attn_status attn_fwd_decode_paged_e2m1(const void* q, const void* kv_cache, cons
  *               they are.  A block that requests share gets the weights of all.
  *   scale:      finite, > 0.
  * dtype (ATTN_BF16 or ATTN_F16) is q's and the cache's type.  A request's sums are fp32
- * in a fixed order; those of requests that share a block are added up in no fixed one.  Device-side checks, reported as ATTN_ERR_BAD_INPUT: a request whose
- * offsets or length are out of range is left out, and so is a slot whose block id is.
+ * in a fixed order; those of requests that share a block are added up in no fixed one.
+ * Device-side checks, reported as ATTN_ERR_BAD_INPUT: a request whose offsets or length are
+ * out of range is left out, and so is a slot whose block id is.  Where offsets out of order
+ * give several requests the same queries, one whose queries are cut into ranges (below) is
+ * left out and reported too once those before it have used the workspace up.
  * Queries whose strides are not 0, with up to 128 query heads to a KV head and on average
  * over 8 query rows to a request's KV head, run on the 5th-generation tensor cores, others
  * (decode steps) on a kernel that streams the keys.  Of the former, requests with over 512 queries

@@ -41,6 +41,7 @@
 #include "prefill_common.cuh"
 #include "sm100.cuh"
 #include "weights.cuh"
+#include "weights_counts.h"
 
 namespace attn {
 namespace {
@@ -50,7 +51,7 @@ using prefill::kDrainLimitNs;
 using prefill::wait_quiet;
 using prefill::warp_wait;
 
-constexpr int kKeyShift = 8, kKeys = 1 << kKeyShift;  // of an item
+constexpr int kKeyShift = kWeightsKeyShift, kKeys = 1 << kKeyShift;  // of an item
 constexpr int kHalf = 128;  // keys of an MMA
 constexpr int kCols = 128;  // query rows of a tile
 // Items: the lse warp is four tiles ahead, so four items where they have one tile each (with four
@@ -111,9 +112,9 @@ struct Layout {
 
 struct TilesParams {
     WeightsParams w;
-    float* partial;       // [slots, Hkv, keys] sums of ranges, or null: no request has several
+    float* partial;       // [ranges.places, Hkv, keys] sums of ranges, or null: no request has several
     long long keys;       // max_pages * page
-    int range_shift;      // log2 of the tokens of an item
+    WeightsRanges ranges;
     int tile_tokens;      // tokens of a query tile
     unsigned long long limit_ns;
 };
@@ -123,10 +124,10 @@ struct TilesParams {
 // their counts, from the last block on, are floor(j / m) + 1 with m = range / kKeys.
 struct Counts {
     int blocks, flat, ranges, shift;  // m = 1 << shift
-    __device__ __forceinline__ Counts(const TilesParams& p, int len, int n) : shift(p.range_shift - kKeyShift) {
+    __device__ __forceinline__ Counts(const TilesParams& p, int len, int n) : shift(p.ranges.shift - kKeyShift) {
         blocks = (len + kKeys - 1) >> kKeyShift;
         flat = min(blocks, ((len - n) >> kKeyShift) + 1);
-        ranges = (n + (1 << p.range_shift) - 1) >> p.range_shift;
+        ranges = (n + (1 << p.ranges.shift) - 1) >> p.ranges.shift;
     }
     // Items of the last j blocks.  (Items of a head fit in 31 bits: range_of().)
     __device__ __forceinline__ int tail(int j) const {
@@ -164,33 +165,35 @@ struct Finder {
 
     __device__ __forceinline__ void look() {
         base += chunk;
-        slot_base += __shfl_sync(0xffffffffu, slots, 31);
+        slot_base = WeightsRanges::add(slot_base, __shfl_sync(0xffffffffu, slots, 31));
         first += 32;
         const int b = first + lane;
-        long long count = 0;
-        int own_slots = 0;
+        bool ok = true;
+        n = 0;
         if (b < p.w.B) {
             const WeightsRequest r = weights_request(p.w, b);
             begin = r.begin;
             n = r.ok ? r.end - r.begin : 0;
             len = r.len;
-            if (!r.ok && blockIdx.x == 0) atomicOr(p.w.status, ATTN_DEV_BAD_INPUT);
-            if (n > 0) {
-                const Counts c(p, len, n);
-                count = static_cast<long long>(c.items()) * p.w.Hkv;
-                if (c.ranges > 1) own_slots = c.ranges;
-            }
+            ok = r.ok;
         }
-        incl = count;
+        const int own_slots = p.ranges.of(n);
         slots = own_slots;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, slots, o);
+            if (lane >= o) slots += x;
+        }
+        if (own_slots > 0 && !p.ranges.fits(slot_base + slots)) {  // (weights_ranges_kernel leaves it out too)
+            n = 0;
+            ok = false;
+        }
+        if (!ok && blockIdx.x == 0) atomicOr(p.w.status, ATTN_DEV_BAD_INPUT);
+        incl = n > 0 ? static_cast<long long>(Counts(p, len, n).items()) * p.w.Hkv : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
             const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-            const int y = __shfl_up_sync(0xffffffffu, slots, o);
-            if (lane >= o) {
-                incl += x;
-                slots += y;
-            }
+            if (lane >= o) incl += x;
         }
         chunk = __shfl_sync(0xffffffffu, incl, 31);
     }
@@ -213,8 +216,8 @@ struct Finder {
         int kb, r;
         c.find(static_cast<int>(i - static_cast<long long>(it.hkv) * per), &kb, &r);
         it.key0 = kb << kKeyShift;
-        it.t0 = max(0, it.key0 - (it.len - it.n)) + (r << p.range_shift);
-        it.t1 = min(it.n, it.t0 + (1 << p.range_shift));
+        it.t0 = max(0, it.key0 - (it.len - it.n)) + (r << p.ranges.shift);
+        it.t1 = min(it.n, it.t0 + (1 << p.ranges.shift));
         it.slot = c.ranges > 1 ? slot_base + (at > 0 ? slots_before : 0) + r : -1;
         next += gridDim.x;
         return true;
@@ -851,25 +854,26 @@ __global__ void __launch_bounds__(kAddThreads) weights_ranges_kernel(const __gri
     for (int b = blockIdx.z; b < p.w.B; b += gridDim.z) {
         const WeightsRequest r = weights_request(p.w, b);
         const int n = r.ok ? r.end - r.begin : 0;
-        if (n <= 1 << p.range_shift) continue;
+        const int own = p.ranges.of(n);
+        if (own == 0) continue;
         // Slots of the requests before.
         int base = 0;
         for (int i = threadIdx.x; i < b; i += kAddThreads) {
             const WeightsRequest q = weights_request(p.w, i);
-            const int m = q.ok ? q.end - q.begin : 0;
-            if (m > 1 << p.range_shift) base += (m + (1 << p.range_shift) - 1) >> p.range_shift;
+            base = WeightsRanges::add(base, p.ranges.of(q.ok ? q.end - q.begin : 0));
         }
-        base = __reduce_add_sync(0xffffffffu, base);
+        base = WeightsRanges::add(0, __reduce_add_sync(0xffffffffu, base));
         __syncthreads();  // the request before has been read
         if (threadIdx.x % 32 == 0) s_base[threadIdx.x / 32] = base;
         __syncthreads();
         base = 0;
         for (int i = 0; i < kAddThreads / 32; ++i) base += s_base[i];
+        if (!p.ranges.fits(base + own)) continue;  // left out and reported
         for (int key = blockIdx.x * kAddThreads + threadIdx.x; key < r.len; key += gridDim.x * kAddThreads) {
             int in_page;
             const int id = p.w.block_table[static_cast<int64_t>(b) * p.w.max_pages + p.w.page.split(key, &in_page)];
             if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.w.num_blocks)) continue;  // reported
-            const int t0 = max(0, (key & -kKeys) - (r.len - n)), ranges = (n - t0 + (1 << p.range_shift) - 1) >> p.range_shift;
+            const int t0 = max(0, (key & -kKeys) - (r.len - n)), ranges = (n - t0 + (1 << p.ranges.shift) - 1) >> p.ranges.shift;
             for (int hkv = blockIdx.y; hkv < p.w.Hkv; hkv += gridDim.y) {
                 float sum = 0.0f;
                 for (int i = 0; i < ranges; ++i)
@@ -880,23 +884,8 @@ __global__ void __launch_bounds__(kAddThreads) weights_ranges_kernel(const __gri
     }
 }
 
-// log2 of an item's tokens: two blocks of keys, so that there are items for all SMs (a 4096-token
-// prompt took 82 us with one block, 77 with two, 99 with four, 122 with sixteen); more where
-// the partial sums would not stay in the L2 (64 MB), or a head's items not fit in 31 bits.
-constexpr long long kPartialBytes = 64ll << 20;
-int range_shift_of(const WeightsShape& s) {
-    const long long keys = static_cast<long long>(s.max_pages) * s.page;
-    int shift = kKeyShift + 1;
-    while (s.total >> shift > 0 &&
-           (static_cast<double>(2ll * s.total >> shift) * s.Hkv * keys * 4 > kPartialBytes ||  // (may pass 64 bits)
-            ((keys >> kKeyShift) + 1) * ((s.total >> shift) + 1) > 0x3fffffffll))
-        ++shift;
-    return shift;
-}
-long long partial_bytes(const WeightsShape& s) {
-    const int shift = range_shift_of(s);
-    // A request with more tokens than a range has at most 2 n / range of them.
-    return s.total <= 1ll << shift ? 0 : (2ll * s.total >> shift) * s.Hkv * s.max_pages * s.page * 4;
+WeightsRanges ranges_of(const WeightsShape& s) {
+    return weights_ranges(s.total, s.Hkv, static_cast<long long>(s.max_pages) * s.page);
 }
 
 template <int D, bool kF16, int kLoads>
@@ -941,7 +930,9 @@ int weights_page_rows(const WeightsShape& s) {
     return !s.scales && box && slabs <= 0x7fffffffll ? std::min(s.page, kHalf) : 0;
 }
 
-size_t weights_workspace_bytes(const WeightsShape& s) { return static_cast<size_t>(partial_bytes(s)); }
+size_t weights_workspace_bytes(const WeightsShape& s) {
+    return 4ull * ranges_of(s).places * s.Hkv * s.max_pages * s.page;
+}
 
 cudaError_t launch_weights_tiles(const WeightsShape& s, const WeightsMaps& maps, void* ws, const LaunchEnv& env,
                                  int* grid_out, int* kernels_launched) {
@@ -949,7 +940,7 @@ cudaError_t launch_weights_tiles(const WeightsShape& s, const WeightsMaps& maps,
     p.w = weights_params(s, env);
     p.partial = static_cast<float*>(ws);
     p.keys = static_cast<long long>(s.max_pages) * s.page;
-    p.range_shift = range_shift_of(s);
+    p.ranges = ranges_of(s);
     p.tile_tokens = weights_tile_tokens(s);
     p.limit_ns = env.wait_limit_ns;
     const int grid = env.num_sms;
