@@ -75,6 +75,22 @@ int main() {
 }
 """
 
+COLUMNS = PROLOGUE + r"""
+int main() {
+    const ll top = 0x7fffffffll - 1024;
+    for (int i = 0; i < 2000000; ++i) {
+        const int group = static_cast<int>(uniform(1, 128));
+        const ll past = i % 2 ? uniform(0, top) : spread(top);
+        // Any earlier key, and those of an item from `past` on.
+        const ll key = i % 3 ? uniform(0, past) : std::min(top + 511, past + uniform(0, 511));
+        const ll want = std::max<ll>(0, (key - past) * group);
+        const int got = weights_first_column(static_cast<int>(key), static_cast<int>(past), group);
+        if (got != want) return std::printf("key %lld, past %lld, group %d: %d\n", key, past, group, got), 1;
+    }
+    return 0;
+}
+"""
+
 
 def run(tmp_path, program):
     from transformer_attention_fwd_gb300 import build
@@ -93,3 +109,8 @@ def test_no_place_is_past_those_allocated(tmp_path):
     """Offsets in order or not: a request has places within the workspace or is left out, by
     both kernels alike."""
     run(tmp_path, PLACES)
+
+
+def test_first_columns_of_long_contexts(tmp_path):
+    """Up to 2^31 keys and 128 heads, against 64 bits."""
+    run(tmp_path, COLUMNS)

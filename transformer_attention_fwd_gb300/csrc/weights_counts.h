@@ -41,4 +41,10 @@ inline WeightsRanges weights_ranges(int total, int Hkv, long long keys) {
     return WeightsRanges{shift, total <= 1ll << shift ? 0 : static_cast<int>(2ll * total >> shift)};
 }
 
+// A tile's first column that sees a key: token i of the tile, `group` columns, sees the keys up to
+// past + i.  At most an item's keys lie behind past; those far before it, times the group, would wrap.
+__host__ __device__ inline int weights_first_column(int key, int past, int group) {
+    return key > past ? (key - past) * group : 0;
+}
+
 }  // namespace attn

@@ -698,7 +698,8 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
             // Token t sees keys up to len - n + t: this key is seen from column lo on, the warp's
             // first key from lo_warp on.
             const int past = it.len - it.n + t;
-            const int lo = (key - past) * w.group, lo_warp = (first + quarter * 32 - past) * w.group;
+            const int lo = weights_first_column(key, past, w.group);
+            const int lo_warp = weights_first_column(first + quarter * 32, past, w.group);
             const bool whole = (first + quarter * 32 + 31 <= past) && (valid & 31) == 0;
             if (!wait(&ctl->l_full[ls], (l_it / kQStages) & 1, SITE_W_L_FULL)) return;
             if (!wait(&ctl->s_full[half][set], uses & 1, SITE_W_S_FULL)) return;
@@ -727,7 +728,7 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
             } else {
                 float part = 0.0f;
 #pragma unroll 1
-                for (int c = max(0, lo_warp) & ~31; c < valid; c += 32) {
+                for (int c = lo_warp & ~31; c < valid; c += 32) {
                     uint32_t a[32];
                     tmem_ld32(at + c, a);
                     tmem_wait_ld(a);
