@@ -94,10 +94,11 @@ struct Control {
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
-    alignas(16) float nlse[kQStages][kCols];  // -log2(e) lse of a tile's rows
+    alignas(16) float nlse[kQStages][kCols];  // -log2(e) lse of a tile's rows; +inf: adds nothing
     float handed[kKeys];
     ItemPlace items[kItems];
     int item_slots[kItems];
+    int rows[kQStages];  // of a tile that add something
 };
 
 template <int D>
@@ -543,7 +544,7 @@ __device__ void load_lse(const TilesParams& p, Control* ctl, int lane, const Wai
         if (!more) return false;
         const float* from = w.lse + it.hkv * w.group * w.lse_head + (it.begin + t) * w.lse_token;
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) x[i] = token[i] < it.t1 - t ? from[head_at[i] + token[i] * w.lse_token] : INFINITY;
+        for (int i = 0; i < kOwn; ++i) x[i] = token[i] < it.t1 - t ? from[head_at[i] + token[i] * w.lse_token] : -INFINITY;
         t += p.tile_tokens;
         if (t >= it.t1) {
             more = items.take(it);
@@ -562,9 +563,15 @@ __device__ void load_lse(const TilesParams& p, Control* ctl, int lane, const Wai
             if (l_it >= kQStages &&
                 !__all_sync(0xffffffffu, mbar_wait(&ctl->l_empty[s], ((l_it / kQStages) & 1) ^ 1, g, SITE_W_L_EMPTY)))
                 return;
+            int rows = 0;
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i)  // a row that saw nothing (-inf) adds nothing, as no row does
-                ctl->nlse[s][lane + 32 * i] = v[a][i] == -INFINITY ? -INFINITY : -v[a][i] * kWeightsLog2e;
+            for (int i = 0; i < kOwn; ++i) {
+                const float nl = -v[a][i] * kWeightsLog2e;
+                ctl->nlse[s][lane + 32 * i] = nl;
+                // A row that saw nothing (-inf) is as no row, whatever its scores are.
+                rows += __popc(__ballot_sync(0xffffffffu, nl != INFINITY));
+            }
+            if (lane == 0) ctl->rows[s] = rows;
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->l_full[s]);
             there[a] = ask(v[a]);
@@ -647,13 +654,13 @@ __device__ __forceinline__ void add_columns(const uint32_t (&s)[32], const float
         }
     }
 }
-// The same of columns lo .. hi - 1 of them.
-__device__ __forceinline__ float add_some_columns(const uint32_t (&s)[32], const float* nl, float sc, int lo, int hi) {
+// The same of those columns whose bits are set; others may hold anything.
+__device__ __forceinline__ float add_some_columns(const uint32_t (&s)[32], const float* nl, float sc, uint32_t bits) {
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         const float e = ex2_approx(fmaf(__uint_as_float(s[i]), sc, nl[i]));
-        sum += i >= lo && i < hi ? e : 0.0f;
+        sum += bits >> i & 1 ? e : 0.0f;
     }
     return sum;
 }
@@ -700,8 +707,8 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
             const int past = it.len - it.n + t;
             const int lo = weights_first_column(key, past, w.group);
             const int lo_warp = weights_first_column(first + quarter * 32, past, w.group);
-            const bool whole = (first + quarter * 32 + 31 <= past) && (valid & 31) == 0;
             if (!wait(&ctl->l_full[ls], (l_it / kQStages) & 1, SITE_W_L_FULL)) return;
+            const bool whole = (first + quarter * 32 + 31 <= past) && (valid & 31) == 0 && ctl->rows[ls] == valid;
             if (!wait(&ctl->s_full[half][set], uses & 1, SITE_W_S_FULL)) return;
             ++uses;
             tc_fence_after_sync();
@@ -732,7 +739,8 @@ __device__ void add_up(const TilesParams& p, Control* ctl, uint32_t tmem, int wa
                     uint32_t a[32];
                     tmem_ld32(at + c, a);
                     tmem_wait_ld(a);
-                    part += add_some_columns(a, nl + c, sc, lo - c, valid - c);
+                    const uint32_t bits = __ballot_sync(0xffffffffu, nl[c + lane] != INFINITY);
+                    part += add_some_columns(a, nl + c, sc, lo <= c ? bits : lo - c < 32 ? bits & ~0u << (lo - c) : 0u);
                 }
                 read();
                 sum += part;
