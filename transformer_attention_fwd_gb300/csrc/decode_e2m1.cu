@@ -54,8 +54,10 @@ __global__ void __launch_bounds__(kAddThreads) add_scores_kernel(const CachePara
         const float* lse = p.lse + static_cast<int64_t>(b) * p.Hq + hkv * p.group;
         const int* table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
         const float* scores = p.scores + static_cast<int64_t>(u) * p.max_pages * p.page.size * p.group;
-        for (int key0 = blockIdx.x * (kAddKeys * kAddThreads) + threadIdx.x; key0 < len;
-             key0 += gridDim.x * (kAddKeys * kAddThreads)) {
+        // (Unsigned: a step behind the last keys of the longest tables passes 2^31.)
+        for (unsigned from = blockIdx.x * (kAddKeys * kAddThreads) + threadIdx.x; from < static_cast<unsigned>(len);
+             from += gridDim.x * (kAddKeys * kAddThreads)) {
+            const int key0 = static_cast<int>(from);
             int id[kAddKeys], row[kAddKeys];
 #pragma unroll
             for (int i = 0; i < kAddKeys; ++i) {
