@@ -91,6 +91,30 @@ int main() {
 }
 """
 
+SHIFTS = PROLOGUE + r"""
+int main() {
+    const ll top = 0x7fffffffll - 1024;
+    bool far = false;
+    for (int i = 0; i < 300000; ++i) {
+        const ll total = i % 2 ? spread(top) : uniform(1, top), Hkv = i % 3 ? 1 : spread(64), group = spread(128);
+        if (weights_tile_tokens(static_cast<int>(total), static_cast<int>(group), 1) == 0) continue;
+        const ll keys = std::max(total, spread(top));
+        const WeightsRanges r = weights_ranges(static_cast<int>(total), static_cast<int>(Hkv), keys);
+        far |= r.shift == 30;
+        if (r.shift > 30 || 1 << r.shift != 1ll << r.shift || r.places >= WeightsRanges::kMany) return 1;
+        // A request of n tokens has its last range's end, and its count of ranges, in 31 bits.
+        for (ll n : {1ll, total / 2 + 1, total - 1, total}) {
+            if (n < 1) continue;
+            const ll ranges = (n + (1ll << r.shift) - 1) >> r.shift;
+            if (r.of(static_cast<int>(n)) != (ranges > 1 ? ranges : 0) || ((n - 1) >> r.shift << r.shift) + (1ll << r.shift) > 0x7fffffffll ||
+                r.of(static_cast<int>(n)) > r.places)
+                return std::printf("%lld of %lld tokens, %lld keys: shift %d\n", n, total, keys, r.shift), 1;
+        }
+    }
+    return far ? 0 : 2;
+}
+"""
+
 
 def run(tmp_path, program):
     from transformer_attention_fwd_gb300 import build
@@ -114,3 +138,8 @@ def test_no_place_is_past_those_allocated(tmp_path):
 def test_first_columns_of_long_contexts(tmp_path):
     """Up to 2^31 keys and 128 heads, against 64 bits."""
     run(tmp_path, COLUMNS)
+
+
+def test_ranges_stay_in_31_bits(tmp_path):
+    """Of as many tokens as the tiles take."""
+    run(tmp_path, SHIFTS)

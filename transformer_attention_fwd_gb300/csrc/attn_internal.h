@@ -239,8 +239,7 @@ cudaError_t launch_weights_paged(const WeightsShape& s, const LaunchEnv& env, in
 struct WeightsMaps {
     CUtensorMap q, k;
 };
-// Tokens of a query tile: as many as it has rows for, or one where the requests have one each
-// (a decode step); 0: the group is too large.
+// Tokens of a query tile; 0: launch_weights_paged() takes the call (weights_counts.h has the rule).
 int weights_tile_tokens(const WeightsShape& s);
 int weights_page_rows(const WeightsShape& s);  // 0: not by TMA, k is not used
 size_t weights_workspace_bytes(const WeightsShape& s);

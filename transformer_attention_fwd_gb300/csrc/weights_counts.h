@@ -7,6 +7,17 @@
 namespace attn {
 
 constexpr int kWeightsKeyShift = 8;  // log2 of an item's keys
+constexpr int kWeightsCols = 128;    // query rows of a tile
+
+// Tokens of a query tile: as many as it has rows for.  0: the kernel that streams the keys
+// (weights.cu) takes the call: a group that a tile has no room for; up to eight query rows to a KV
+// head, as far as the host can tell (with a step's one token over 64 x 4096 keys tiles took 98 us
+// in 16 bits and 152 in 4, that kernel 88 and 47; with 16 rows over 32 x 4096, 53 and 77, that one 63
+// and 77); so many tokens that a range, or what follows it, would pass 31 bits.
+inline int weights_tile_tokens(int total, int group, int B) {
+    if (group > kWeightsCols || static_cast<long long>(total) * group <= 8ll * B || total >= 1 << 30) return 0;
+    return kWeightsCols / group;
+}
 
 // A request's queries are worked on in ranges of 1 << shift tokens.  One with several has a
 // place in the workspace for each range's sums; places are handed out request by request.
@@ -29,6 +40,7 @@ struct WeightsRanges {
 // Two blocks of keys to a range, so that there are items for all SMs (a 4096-token prompt took
 // 82 us with one block, 77 with two, 99 with four, 122 with sixteen); more where the partial sums
 // would not stay in the L2 (64 MB), or a head's items not fit in 31 bits.
+// total: under 2^30 (weights_tile_tokens), so that shift is at most 30.
 inline WeightsRanges weights_ranges(int total, int Hkv, long long keys) {
     constexpr double kPartialBytes = 64ll << 20;
     int shift = kWeightsKeyShift + 1;

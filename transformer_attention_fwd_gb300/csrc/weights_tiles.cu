@@ -53,7 +53,7 @@ using prefill::warp_wait;
 
 constexpr int kKeyShift = kWeightsKeyShift, kKeys = 1 << kKeyShift;  // of an item
 constexpr int kHalf = 128;  // keys of an MMA
-constexpr int kCols = 128;  // query rows of a tile
+constexpr int kCols = kWeightsCols;  // query rows of a tile
 // Items: the lse warp is four tiles ahead, so four items where they have one tile each (with four
 // places windows of 64 tokens over 16 x 4096 4-bit keys took 61.7 us instead of 60.3).
 constexpr int kQStages = 3, kKStages = 2, kSBufs = 2, kItems = 5;
@@ -923,14 +923,7 @@ cudaError_t launch_loads(const WeightsMaps& maps, const TilesParams& p, bool f16
 
 }  // namespace
 
-int weights_tile_tokens(const WeightsShape& s) {
-    const int group = s.Hq / s.Hkv;
-    // Up to eight query rows to a KV head, as far as the host can tell, are the other kernel's: with a
-    // step's one token over 64 x 4096 keys this one took 98 us (16 bits) and 152 (4 bits), that one 88
-    // and 47; with 16 rows over 32 x 4096, 53 and 77 here, 63 and 77 there.
-    if (group > kCols || static_cast<long long>(s.total) * group <= 8ll * s.B) return 0;
-    return kCols / group;
-}
+int weights_tile_tokens(const WeightsShape& s) { return weights_tile_tokens(s.total, s.Hq / s.Hkv, s.B); }
 
 // Pages that boxes cover come by TMA: windows of 64 tokens took 60 us by the warps' copies, 45 so.
 int weights_page_rows(const WeightsShape& s) {
