@@ -115,6 +115,22 @@ int main() {
 }
 """
 
+ROWS = PROLOGUE + r"""
+int main() {
+    const ll top = 0x7fffffffll - 1024;
+    for (int i = 0; i < 2000000; ++i) {
+        const ll group = spread(1 << 20), most = top / group, n = i % 2 ? most : uniform(1, most);
+        const ll len = std::min(top, n + (i % 3 ? uniform(0, top - n) : uniform(0, 40)));
+        const ll key = i % 5 ? uniform(0, len - 1) : len - 1 + uniform(0, 31);
+        const ll token = std::max<ll>(0, key - (len - n));
+        const int got = weights_first_row(static_cast<int>(key), static_cast<int>(len), static_cast<int>(n), static_cast<int>(group));
+        if (got != std::min(token, n) * group)
+            return std::printf("key %lld of %lld, %lld tokens, group %lld: %d\n", key, len, n, group, got), 1;
+    }
+    return 0;
+}
+"""
+
 
 def run(tmp_path, program):
     from transformer_attention_fwd_gb300 import build
@@ -143,3 +159,8 @@ def test_first_columns_of_long_contexts(tmp_path):
 def test_ranges_stay_in_31_bits(tmp_path):
     """Of as many tokens as the tiles take."""
     run(tmp_path, SHIFTS)
+
+
+def test_first_rows_of_many_heads(tmp_path):
+    """As many rows as a call may have, and the places of a chunk behind the last key."""
+    run(tmp_path, ROWS)

@@ -23,6 +23,7 @@
 #include "pdl.cuh"
 #include "sm100.cuh"
 #include "weights.cuh"
+#include "weights_counts.h"
 
 namespace attn {
 namespace {
@@ -218,8 +219,7 @@ __device__ __forceinline__ void weights_keys(const WeightsParams& p, const Weigh
             uint32_t kw[2 * kAtOnce][D / 8];
 #pragma unroll
             for (int i = 0; i < 2 * kAtOnce; ++i) now[2 * h0 + i].words(kw[i]);
-            const int first_token = max(0, key0 + 16 * h0 - (req.len - n));
-            for (int r0 = first_token * p.group / 8 * 8; r0 < rows; r0 += 8) {
+            for (int r0 = weights_first_row(key0 + 16 * h0, req.len, n, p.group) / 8 * 8; r0 < rows; r0 += 8) {
                 if (rows > 8) q.load(p, req, hkv, scale, r0, g, t);
 #pragma unroll
                 for (int h = 0; h < kAtOnce; ++h) q.add(kw[2 * h], kw[2 * h + 1], key0 + (h0 + h) * 16, g, sum[h0 + h]);

@@ -53,6 +53,13 @@ inline WeightsRanges weights_ranges(int total, int Hkv, long long keys) {
     return WeightsRanges{shift, total <= 1ll << shift ? 0 : static_cast<int>(2ll * total >> shift)};
 }
 
+// A request's first query row, of n tokens with `group` rows each, that sees a key of its len ones;
+// of a key behind them (a chunk's places end later) n * group, which the host has checked.
+__host__ __device__ inline int weights_first_row(int key, int len, int n, int group) {
+    const int token = key - (len - n);
+    return token <= 0 ? 0 : (token < n ? token : n) * group;
+}
+
 // A tile's first column that sees a key: token i of the tile, `group` columns, sees the keys up to
 // past + i.  At most an item's keys lie behind past; those far before it, times the group, would wrap.
 __host__ __device__ inline int weights_first_column(int key, int past, int group) {
