@@ -1238,6 +1238,7 @@ attn_status run_weights(bool four, const attn_rows* q, const float* lse, long lo
     attn_status st = validate_pool(kv_cache, scales, four, weights, block_table, seq_lens, B, Hkv, D, page_size,
                                    max_pages_per_seq, num_blocks);
     if (st != ATTN_OK) return st;
+    if (B > 0x7fffffff - 65536) return fail(ATTN_ERR_INVALID_ARG, "B must be below 2^31 - 65536");
     if (total < 0 || total > 0x7fffffff - 1024)
         return fail(ATTN_ERR_INVALID_ARG, "total must be >= 0 and below 2^31 - 1024");
     if (!std::isfinite(scale) || !(scale > 0.0f))
