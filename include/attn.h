@@ -580,7 +580,8 @@ attn_status attn_weights_paged_e2m1(const attn_rows* q, const float* lse, long l
  * rows stay as they are (a shorter table may follow: the pages past slot keep-1 are
  * free).  Keys keep the rotation they have, so tokens appended later need positions.
  *   weights:  [num_blocks, Hkv, page_size] float32 (attn_weights_paged).
- *   new_lens: [B] int32: min(seq_lens[b], keep).  May not be seq_lens (nor may kept).
+ *   new_lens: [B] int32: min(seq_lens[b], keep), 0 for a request that is left out.  May not
+ *             be seq_lens (nor may kept).
  *   kept:     [B, Hkv, keep] int32 or NULL: the slot each kept row had before, -1
  *             past the request's new length.
  * A block belongs to one request of the call.  dtype: ATTN_BF16 or ATTN_F16.  Device-side

@@ -109,7 +109,7 @@ struct Team<false> {
     static __device__ __forceinline__ int add(int* p, int, int v) { return atomicAdd(p, v); }
 };
 
-// A request's slots; len: 0 if out of range (reported by the first kernel).
+// A request's slots; len: 0 if out of range (reported by the first kernel), so that it is left out.
 struct Slots {
     const EvictParams& p;
     const int* table;
@@ -117,7 +117,7 @@ struct Slots {
     __device__ __forceinline__ Slots(const EvictParams& params, int b, bool report)
         : p(params), table(params.block_table + static_cast<int64_t>(b) * params.max_pages) {
         const int n = p.lens[b], most = p.max_pages * p.page.size;
-        len = n < 0 ? 0 : (n > most ? most : n);
+        len = n < 0 || n > most ? 0 : n;
         if (report && len != n) atomicOr(p.status, ATTN_DEV_BAD_INPUT);
     }
     // Block of a page; -1 (reported) if its id is outside the pool.
