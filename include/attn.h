@@ -585,8 +585,9 @@ attn_status attn_weights_paged_e2m1(const attn_rows* q, const float* lse, long l
  *   kept:     [B, Hkv, keep] int32 or NULL: the slot each kept row had before, -1
  *             past the request's new length.
  * A block belongs to one request of the call.  dtype: ATTN_BF16 or ATTN_F16.  Device-side
- * checks as for attn_weights_paged; a row whose old or new block id is out of range does
- * not move.  Without `kept` it is a workspace.  keep and max_pages_per_seq * page_size
+ * checks as for attn_weights_paged; a slot whose block id is out of range counts as one of
+ * weight NaN, and a row whose old or new one is does not move, nor does its weight.  Without
+ * `kept` it is a workspace.  keep and max_pages_per_seq * page_size
  * are below 2^31 - 65536.  (No such call over the 8-bit cache:
  * rows of its blocks share a scale, and moving one would round it again.)
  */

@@ -416,10 +416,10 @@ __global__ void __launch_bounds__(kSelectThreads, 3) evict_select_kernel(const E
             if (lead) {
                 for (int i0 = 0; i0 < p.keep; i0 += kSelectThreads) {
                     const int i = i0 + tid;
-                    uint32_t raw = 0;
-                    if (i < p.keep) raw = load(kept[i]);
+                    const float* old = i < p.keep ? at(kept[i]) : nullptr;  // null: the row stays too
+                    const uint32_t raw = old ? __float_as_uint(*old) : 0u;
                     __syncthreads();
-                    if (i < p.keep) place(i, raw);
+                    if (old) place(i, raw);
                 }
             }
             team.sync();
