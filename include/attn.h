@@ -513,7 +513,9 @@ attn_status attn_append_paged_e2m1(const attn_rows* q, const attn_rows* k, const
  *            score and lse_h the result's log-sum-exp.  Places of other slots stay as
  *            they are.  A block that requests share gets the weights of all, added up
  *            in no fixed order.  The scores pass through a workspace of
- *            4 * B * Hq * max_pages_per_seq * page_size bytes.
+ *            4 * B * Hq * max_pages_per_seq * page_size bytes, whatever the requests'
+ *            lengths: pass a table no wider than they need.  (Outside a capture the library
+ *            keeps the memory of its largest workspaces for later calls.)
  * The other arguments, checks, errors and the workspace are those of
  * attn_fwd_decode_paged_e4m3.
  */
@@ -538,10 +540,12 @@ attn_status attn_fwd_decode_paged_e2m1(const void* q, const void* kv_cache, cons
  *   lse:        float32, the log-sum-exp of every query row, at lse + h * lse_head +
  *               token * lse_token (strides in elements, >= 0): what the attention over
  *               these keys returned (attn_fwd_varlen: [Hq, total]).  A row whose lse is
- *               -inf adds nothing.
+ *               -inf, or so low that it is in base 2, adds nothing, whatever it holds.
  *   seq_lens:   [B] int32, the keys of each request, its queries' own among them.
  *   weights:    [num_blocks, Hkv, page_size] float32; places of other slots stay as
- *               they are.  A block that requests share gets the weights of all.
+ *               they are.  A block that requests share gets the weights of all.  Of a block
+ *               that is handed to a new request the caller clears them: the appends do not.
+ *   B:          below 2^31 - 65536.
  *   scale:      finite, > 0.
  * dtype (ATTN_BF16 or ATTN_F16) is q's and the cache's type.  A request's sums are fp32
  * in a fixed order; those of requests that share a block are added up in no fixed one.
@@ -549,11 +553,12 @@ attn_status attn_fwd_decode_paged_e2m1(const void* q, const void* kv_cache, cons
  * out of range is left out, and so is a slot whose block id is.  Where offsets out of order
  * give several requests the same queries, one whose queries are cut into ranges (below) is
  * left out and reported too once those before it have used the workspace up.
- * Queries whose strides are not 0, with up to 128 query heads to a KV head and on average
- * over 8 query rows to a request's KV head, run on the 5th-generation tensor cores, others
- * (decode steps) on a kernel that streams the keys.  Of the former, requests with over 512 queries
- * (more where the sums would be over 64 MB) have these cut into ranges, whose sums pass
- * through a workspace and are added in order.
+ * Fewer than 2^30 queries whose strides are not 0, with up to 128 query heads to a KV head and
+ * on average over 8 query rows to a request's KV head, run on the 5th-generation tensor cores,
+ * others (decode steps) on a kernel that streams the keys, which is slow for a prompt among
+ * many steps: give prompts and steps calls of their own.  Of the former, requests with over
+ * 512 queries (more where the sums would be over 64 MB) have these cut into ranges, whose
+ * sums pass through a workspace and are added in order.
  */
 attn_status attn_weights_paged(const attn_rows* q, const float* lse, long long lse_head,
                                long long lse_token, const void* kv_cache, const int* block_table,
@@ -579,7 +584,8 @@ attn_status attn_weights_paged_e2m1(const attn_rows* q, const float* lse, long l
  * order and their weights with them; the weights of slots keep and up become 0, their
  * rows stay as they are (a shorter table may follow: the pages past slot keep-1 are
  * free).  Keys keep the rotation they have, so tokens appended later need positions.
- *   weights:  [num_blocks, Hkv, page_size] float32 (attn_weights_paged).
+ *   weights:  [num_blocks, Hkv, page_size] float32 (attn_weights_paged).  Those of the free
+ *             pages are 0 up to the old length.
  *   new_lens: [B] int32: min(seq_lens[b], keep), 0 for a request that is left out.  May not
  *             be seq_lens (nor may kept).
  *   kept:     [B, Hkv, keep] int32 or NULL: the slot each kept row had before, -1
@@ -587,9 +593,9 @@ attn_status attn_weights_paged_e2m1(const attn_rows* q, const float* lse, long l
  * A block belongs to one request of the call.  dtype: ATTN_BF16 or ATTN_F16.  Device-side
  * checks as for attn_weights_paged; a slot whose block id is out of range counts as one of
  * weight NaN, and a row whose old or new one is does not move, nor does its weight.  Without
- * `kept` it is a workspace.  keep and max_pages_per_seq * page_size
- * are below 2^31 - 65536.  (No such call over the 8-bit cache:
- * rows of its blocks share a scale, and moving one would round it again.)
+ * `kept` it is a workspace.  keep and max_pages_per_seq * page_size are below 2^31 - 65536.
+ * (No such call over the 8-bit cache: rows of its blocks share a scale, and moving one would
+ * round it again.)
  */
 attn_status attn_evict_paged(void* kv_cache, float* weights, const int* block_table,
                              const int* seq_lens, int* new_lens, int* kept, int B, int Hkv,

@@ -563,6 +563,7 @@ def attn_weights_paged(q, lse, kv_cache, block_table, cu_seqlens, seq_lens, weig
     cu_seqlens[b+1]-1: the last tokens of its seq_lens[b], each of which sees the keys
     up to its own; lse: [Hq, total] float32 of any strides, as ``attn_fwd_varlen``
     returns it (after a decode step: q[:, :, 0], lse.t() and one query a request).
+    Clear the weights of a block that goes to a new request: the appends do not.
     Returns ``weights``.
     """
     return _native.add_weights(q, lse, kv_cache, None, block_table, cu_seqlens, seq_lens, weights, scale, None,
@@ -585,8 +586,8 @@ def attn_evict_paged(kv_cache, weights, block_table, seq_lens, keep: int, recent
     last ``recent`` and the heaviest of the others by ``weights`` (float32 [num_blocks,
     Hkv, page_size]); rows and weights move to the first slots in place
     (``attn_evict_paged``).  Returns ``(new_lens [B], kept [B, Hkv, keep] or None)``:
-    the new lengths, and the slot each kept key had before (-1 past the length), both
-    int32.  Keys keep their rotation: appending later tokens takes ``positions``.
+    the new lengths (0 for a request left out for its length), and the slot each kept
+    key had before (-1 past the length), both int32.  Keys keep their rotation: appending later tokens takes ``positions``.
     """
     return _native.evict(kv_cache, None, weights, block_table, seq_lens, keep, recent, new_lens, kept, want_kept,
                          None if stream is None else stream.cuda_stream)

@@ -7,9 +7,10 @@
 // to settle and no older rows to follow, so the work is the 16-bit append's (append.cu):
 // a warp takes one token and a run of its heads.  A lane holds two chunks of eight
 // elements of a row, and a group's two chunks meet by shuffles; each of its two lanes settles one of the
-// two groups they share.  Bound by its instructions: 17100 tokens of 8 KV heads (D 128) take 24 to
-// 27 us, some 60% of the issue slots (floor by bytes 13); a step of 64 tokens takes
-// 3.1, a chain of reads.
+// two groups they share.  17100 tokens of 8 KV heads (D 128) take 24 to 27 us (floor by bytes
+// 13): 18 M instructions, the groups' exchanges between lanes among them, in 60% of the issue slots,
+// which is no limit; the rest waits, mostly for memory, at a third of the warps an SM can hold.
+// A step of 64 tokens takes 3.1, a chain of reads.
 #include <cuda_runtime.h>
 
 #include <algorithm>

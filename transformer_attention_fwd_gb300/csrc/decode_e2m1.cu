@@ -14,8 +14,8 @@
 // weighted sum (the 8-bit decode has a scale per block in its weights).
 //
 // Measured (64 requests of 4096 keys, 32 + 8 heads, D 128): 67.6 us, 302 MB; the copies alone
-// take 58, 12 of them start, tail and combine.  Conversions and products take 59% of the issue
-// slots.  Tiles of 32 keys instead of 16: 91 -> 81 us; V's products of both halves in one stretch:
+// take 58, 12 of them start, tail and combine.  Conversions and products fill 59% of the issue
+// slots: no limit, but three warps to a scheduler wait out their own instructions in the rest.  Tiles of 32 keys instead of 16: 91 -> 81 us; V's products of both halves in one stretch:
 // 79; for up to four heads the weights' second terms in the free columns: 77; half a warp copying
 // each half: 68.
 //

@@ -26,9 +26,11 @@
 // Every wait is bounded (sm100.cuh).
 //
 // What bounds it: a 128 x 128 x 16 product takes 67 cycles and reads 8 KB, all that shared memory
-// gives, so the products of a 4096-token prompt (32 + 8 heads, D 128, 4-bit keys) take 65 us, the
-// sums' exponentials alone 68, both together 77 (floor by operations 36); windows of 64 tokens
-// over 16 requests of 4096 16-bit keys 45 (floor by bytes 21).
+// gives, so the products of a 4096-token prompt (32 + 8 heads, D 128, 4-bit keys) take 65 us (a pair
+// of CTAs with half of the queries each would read half), the sums alone 68: their 268 M
+// exponentials would take 28 at 32 a clock and SM, but a sum warp reads 32 columns of tensor memory,
+// waits, and only then adds.  Both together 77 to 80 (floor by operations 36); windows of 64 tokens
+// over 16 requests of 4096 16-bit keys 42 to 46 (floor by bytes 21).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
