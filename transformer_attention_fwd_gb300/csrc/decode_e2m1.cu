@@ -15,9 +15,9 @@
 //
 // Measured (64 requests of 4096 keys, 32 + 8 heads, D 128): 67.6 us, 302 MB; the copies alone
 // take 58, 12 of them start, tail and combine.  Conversions and products fill 59% of the issue
-// slots: no limit, but three warps to a scheduler wait out their own instructions in the rest.  Tiles of 32 keys instead of 16: 91 -> 81 us; V's products of both halves in one stretch:
-// 79; for up to four heads the weights' second terms in the free columns: 77; half a warp copying
-// each half: 68.
+// slots: no limit, but three warps to a scheduler wait out their own instructions in the rest.
+// Tiles of 32 keys instead of 16: 91 -> 81 us; V's products of both halves in one stretch: 79; for up
+// to four heads the weights' second terms in the free columns: 77; half a warp copying each half: 68.
 //
 // Weights added up: the tiles leave their scores (fp32, one for each key and head) in a
 // workspace, and once the log-sum-exp is known a second kernel adds 2^(x - lse) over a KV

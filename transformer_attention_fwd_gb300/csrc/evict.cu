@@ -51,10 +51,10 @@ constexpr int kSelectThreads = 512;  // (256 with five CTAs an SM: 122 us instea
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 // Weights in shared memory; of longer requests those behind are read again.  The table's width
-// sizes them, whatever the requests' lengths; from some 23,700 on one CTA has an SM to itself.  (With at
-// most 23,680 there is always room for two: 64 requests of 30,000 4-bit keys, 8 KV heads, D 64, took 499 us instead of
-// 516 and 64 of 4096 in tables as wide 89.7 instead of 91.5, but 64 of 16,000 304 instead of 294, and 32
-// of 24,000, which are then read twice, 221 instead of 183.)
+// sizes them, whatever the requests' lengths; from some 23,700 on one CTA has an SM to itself.
+// (With at most 23,680 there is always room for two: 64 requests of 30,000 4-bit keys, 8 KV heads,
+// D 64, took 499 us instead of 516 and 64 of 4096 in tables as wide 89.7 instead of 91.5, but 64 of
+// 16,000 304 instead of 294, and 32 of 24,000, which are then read twice, 221 instead of 183.)
 constexpr int kMaxHeld = 24576;
 constexpr int kPages = 1024;     // pages whose places are
 constexpr int kList = 1024;      // keys that share the first digit, if they are so few
