@@ -586,14 +586,14 @@ attn_status attn_weights_paged_e2m1(const attn_rows* q, const float* lse, long l
  * free).  Keys keep the rotation they have, so tokens appended later need positions.
  *   weights:  [num_blocks, Hkv, page_size] float32 (attn_weights_paged).  Those of the free
  *             pages are 0 up to the old length.
- *   new_lens: [B] int32: min(seq_lens[b], keep), 0 for a request that is left out.  May not
- *             be seq_lens (nor may kept).
+ *   new_lens: [B] int32: min(seq_lens[b], keep), 0 for a request that is left out.
  *   kept:     [B, Hkv, keep] int32 or NULL: the slot each kept row had before, -1
  *             past the request's new length.
- * A block belongs to one request of the call.  dtype: ATTN_BF16 or ATTN_F16.  Device-side
- * checks as for attn_weights_paged; a slot whose block id is out of range counts as one of
- * weight NaN, and a row whose old or new one is does not move, nor does its weight.  Without
- * `kept` it is a workspace.  keep and max_pages_per_seq * page_size are below 2^31 - 65536.
+ * No two tensors of the call may share memory, seq_lens and block_table aside (refused).  A
+ * block belongs to one request of the call.  dtype: ATTN_BF16 or ATTN_F16.  Device-side checks
+ * as for attn_weights_paged; a slot whose block id is out of range counts as one of weight
+ * NaN, and a row whose old or new one is does not move, nor does its weight.  Without `kept`
+ * it is a workspace.  keep and max_pages_per_seq * page_size are below 2^31 - 65536.
  * (No such call over the 8-bit cache: rows of its blocks share a scale, and moving one would
  * round it again.)
  */

@@ -1315,11 +1315,16 @@ attn_status run_weights(bool four, const attn_rows* q, const float* lse, long lo
     return ok();
 }
 
-// Whether two ranges of bytes meet.
-bool meet(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + nb && y < x + na;
-}
+// A range of bytes; of more than any memory has, that many.
+struct Range {
+    const void* at;
+    uintptr_t bytes;
+    Range(const void* p, double n) : at(p), bytes(n < 0x1p60 ? static_cast<uintptr_t>(n) : 1ull << 60) {}
+    bool meets(const Range& o) const {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(at), y = reinterpret_cast<uintptr_t>(o.at);
+        return at && o.at && x < y + o.bytes && y < x + bytes;
+    }
+};
 
 attn_status run_evict(bool four, void* kv_cache, void* scales, float* weights, const int* block_table,
                       const int* seq_lens, int* new_lens, int* kept, int B, int Hkv, int D, int page_size,
@@ -1335,11 +1340,21 @@ attn_status run_evict(bool four, void* kv_cache, void* scales, float* weights, c
         return fail(ATTN_ERR_INVALID_ARG, "new_lens must be non-null, and new_lens and kept 4-byte aligned");
     if (4.0 * B * Hkv * keep > kMaxWorkspace) return fail(ATTN_ERR_INVALID_ARG, "B*Hkv*keep must be below 2^42");
     const size_t kept_bytes = 4ull * B * Hkv * keep;
-    const size_t lens_bytes = 4ull * B, table_bytes = 4ull * B * max_pages_per_seq;
-    if (meet(new_lens, lens_bytes, seq_lens, lens_bytes) || meet(new_lens, lens_bytes, block_table, table_bytes) ||
-        meet(kept, kept_bytes, seq_lens, lens_bytes) || meet(kept, kept_bytes, block_table, table_bytes) ||
-        meet(kept, kept_bytes, new_lens, lens_bytes))
-        return fail(ATTN_ERR_INVALID_ARG, "new_lens and kept may not share memory with seq_lens, block_table or one another");
+    // What is written is read again, slots and block ids among it: nothing of it may be something else.
+    const double rows = 2.0 * num_blocks * Hkv * page_size;
+    const Range written[] = {{kept, 4.0 * B * Hkv * keep},          {new_lens, 4.0 * B},
+                             {weights, 2.0 * rows},                 {kv_cache, rows * (four ? D / 2 : 2 * D)},
+                             {four ? scales : nullptr, rows * D / 16}};
+    const Range read[] = {{seq_lens, 4.0 * B}, {block_table, 4.0 * B * max_pages_per_seq}};
+    for (const Range* w = written; w != std::end(written); ++w) {
+        bool met = false;
+        for (const Range* o = w + 1; o != std::end(written); ++o) met |= w->meets(*o);
+        for (const Range& r : read) met |= w->meets(r);
+        if (met)
+            return fail(ATTN_ERR_INVALID_ARG,
+                        "new_lens, kept, weights, kv_cache and scales may not share memory with seq_lens, block_table "
+                        "or one another");
+    }
     LaunchEnv env;
     if ((st = device_env(stream, &env)) != ATTN_OK) return st;
     void* ws = nullptr;
